@@ -63,8 +63,10 @@ extern "C" {
  * modulation-table add also accepts binary32 inputs and writes binary32, and
  * the FP8 producers write an extra FP8 E4M3 (one byte per element) output and
  * the NVFP4 producers packed FP4 E2M1 pairs (MBX_E2M1X2, one byte per two
- * elements) with E4M3 block scales. */
-enum { MBX_BF16 = 1, MBX_F32 = 2, MBX_E4M3 = 3, MBX_E2M1X2 = 4 };
+ * elements) with E4M3 block scales.  The training entry points (the section at
+ * the end) also take binary32 activations, and mbx_rope_axes reads int32 or
+ * binary32 positions and binary64 frequencies. */
+enum { MBX_BF16 = 1, MBX_F32 = 2, MBX_E4M3 = 3, MBX_E2M1X2 = 4, MBX_I32 = 5, MBX_F64 = 6 };
 
 /* variant codes */
 enum { MBX_LOSSLESS = 0, MBX_HIGH = 1 };
@@ -333,6 +335,169 @@ MBX_API int mbx_check_qk_norm_rope_qkv_epilogue(
     int64_t heads, const mbx_cview* wq_txt, const mbx_cview* wk_txt, const mbx_cview* wq_img,
     const mbx_cview* wk_img, const float* cos_txt, const float* sin_txt, const float* cos_img,
     const float* sin_img, float eps, int variant);
+
+/* ------------------------------------------------------------------------
+ * The training path: affine LayerNorm, the gradients of LayerNorm and of
+ * AdaLN modulation, dropout in the gated residual with its gradients, and
+ * rotary positions on several axes (their gradient is the inverse rotation).
+ *
+ * These have one numeric variant: every operation is binary32 and each output
+ * is rounded once to its type.  Activations (x, y, out and their gradients)
+ * are all MBX_BF16 or all MBX_F32; parameters (weight, bias, scale, gate) and
+ * their gradients have the activations' dtype, or MBX_F32 with MBX_BF16
+ * activations.  The modulation broadcast, the checks, their order and the
+ * statuses are those above.  rows must be below 2^32.
+ *
+ * A gradient that sums rows (of a weight, a bias, or a modulation row shared
+ * by several rows) may need a workspace: mbx_param_grad_workspace() gives its
+ * size in bytes for the current device (0: pass NULL).  It is scratch of one
+ * call: 16-byte aligned, overlapping no operand, its content undefined before
+ * and after, free again when the call's work on `stream` is done.  The sums
+ * are formed in a fixed order: the same call on the same device model gives
+ * the same bits.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Affine LayerNorm: out = (x - mean) / sqrt(var + eps) * weight + bias, var
+ * the biased variance of the row.  weight, bias [1, D], either NULL (1, 0); of
+ * one dtype.  out overlaps nothing.
+ */
+MBX_API int mbx_layer_norm(const mbx_view* out, const mbx_cview* x, const mbx_cview* weight,
+                           const mbx_cview* bias, float eps, void* stream);
+
+/* Workspace bytes of the three calls below that sum `rows` rows of `cols`
+ * activations of `dtype` into mod_rows parameter rows (LayerNorm: 1). */
+MBX_API int mbx_param_grad_workspace(int64_t rows, int64_t cols, int64_t mod_rows, int dtype,
+                                     int64_t* bytes);
+
+/*
+ * Gradients of mbx_layer_norm.  With xh = (x - mean) * rstd (statistics taken
+ * from x again: the forward pass saves nothing) and gy = dout * weight:
+ *   dx      = rstd * (gy - mean(gy) - xh * mean(gy * xh)) + dresidual
+ *   dweight = sum over the rows of dout * xh,   dbias = sum of dout
+ * dresidual [rows, D] or NULL is added to dx (the gradient that the residual
+ * stream carries past the norm); dx may be exactly dresidual.  dweight and
+ * dbias [1, D] of weight's dtype, either NULL (not computed); both NULL when
+ * weight is NULL.
+ */
+MBX_API int mbx_layer_norm_backward(const mbx_view* dx, const mbx_view* dweight,
+                                    const mbx_view* dbias, const mbx_cview* dout,
+                                    const mbx_cview* x, const mbx_cview* weight,
+                                    const mbx_cview* dresidual, float eps, float* workspace,
+                                    int64_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of mbx_ln_modulate (of the formula LN(x) * (1 + scale) + shift;
+ * the roundings of the lossless variant are treated as exact): dx as above
+ * with 1 + scale in weight's place, and for each modulation row
+ *   dscale = sum over its rows of dout * xh,   dshift = sum of dout
+ * scale, dscale, dshift [mod_rows, D] of one dtype; dscale and dshift may be
+ * NULL.  With per-token modulation (mod_rows = rows) nothing is summed.
+ */
+MBX_API int mbx_ln_modulate_backward(const mbx_view* dx, const mbx_view* dscale,
+                                     const mbx_view* dshift, const mbx_cview* dout,
+                                     const mbx_cview* x, const mbx_cview* scale,
+                                     const mbx_cview* dresidual, float eps, float* workspace,
+                                     int64_t workspace_bytes, void* stream);
+
+/*
+ * Dropout with a mask that is computed, not stored: element (r, c) is kept
+ * where word c mod 4 of Philox4x32-10 (Salmon, Moraes, Dror & Shaw, "Parallel
+ * random numbers: as easy as 1, 2, 3", SC 2011) with the key rng[0] and the
+ * counter words (c / 4, r, low and high half of rng[1] + offset, modulo 2^64)
+ * is at least floor(p * 2^32).
+ *   mbx_dropout:           out = kept ? x / (1 - p) : 0
+ *   mbx_dropout_gate_add:  out = kept ? x + gate * y / (1 - p) : x
+ * A dropped element contributes nothing, whatever gate and y hold there.
+ * rng: device pointer to 2 int64 (seed, counter), 8-byte aligned, read on the
+ * stream, so that a captured graph draws another mask when they change;
+ * `offset` tells the layers of one step apart.  0 <= p < 1; p = 0 keeps all.
+ * The gradient of mbx_dropout is mbx_dropout of the incoming gradient with the
+ * same p, rng and offset.  out may be exactly x.  gate [mod_rows, D].
+ */
+MBX_API int mbx_dropout(const mbx_view* out, const mbx_cview* x, double p, const int64_t* rng,
+                        int64_t offset, void* stream);
+MBX_API int mbx_dropout_gate_add(const mbx_view* out, const mbx_cview* x, const mbx_cview* gate,
+                                 const mbx_cview* y, double p, const int64_t* rng, int64_t offset,
+                                 void* stream);
+
+/*
+ * Gradients of mbx_dropout_gate_add (that of x is dout itself):
+ *   dy    = kept ? dout * gate / (1 - p) : 0
+ *   dgate = sum over the gate row's rows of kept ? dout * y / (1 - p) : 0
+ * dgate [mod_rows, D] of gate's dtype, or NULL.  No output overlaps anything.
+ */
+MBX_API int mbx_dropout_gate_add_backward(const mbx_view* dy, const mbx_view* dgate,
+                                          const mbx_cview* dout, const mbx_cview* gate,
+                                          const mbx_cview* y, double p, const int64_t* rng,
+                                          int64_t offset, float* workspace,
+                                          int64_t workspace_bytes, void* stream);
+
+/* [batch, tokens, heads, head_dim] array, the last dimension contiguous, any
+ * other strides (in elements, not negative): token-major [B, S, H, hd],
+ * head-major [B, H, S, hd] and slices of a merged QKV buffer alike. */
+typedef struct {
+    const void* data;
+    int64_t batch, tokens, heads, head_dim;
+    int64_t batch_stride, token_stride, head_stride;
+    int32_t dtype;
+} mbx_heads_cview;
+
+typedef struct {
+    void* data;
+    int64_t batch, tokens, heads, head_dim;
+    int64_t batch_stride, token_stride, head_stride;
+    int32_t dtype;
+} mbx_heads_view;
+
+/*
+ * Rotary positions on 1 to 4 axes, Q and K in one launch.  axes[a] (even, at
+ * least 2) elements of a head belong to axis a, in order; their sum 2n may be
+ * less than head_dim, and the rest passes through.  The 2n elements form n
+ * pairs, (2j, 2j+1) when interleaved is 1, (j, j+n) when it is 0; pair j of
+ * the n lies on the axis a whose range of pairs holds j, and turns by
+ *   angle = positions[token][a] * freqs[j]     (binary64)
+ *   o0 = x0*cos - x1*sin,   o1 = x0*sin + x1*cos
+ * or by -angle when inverse is 1, which is also the gradient of the rotation.
+ * positions [tokens, axes] (shared by the batch) or [batch*tokens, axes],
+ * MBX_I32 or MBX_F32; freqs [1, n] MBX_F64, radians per position.  q and k
+ * (NULL with k_out: none) have the same batch, tokens, head_dim and dtype, and
+ * any numbers of heads.  Each output may be exactly its input, also inside one
+ * merged buffer; no other overlap is allowed, nor an output that overlaps
+ * itself (MBX_E_STRIDE).  head_dim <= 256; batch * tokens below 2^31.
+ */
+MBX_API int mbx_rope_axes(const mbx_heads_view* q_out, const mbx_heads_view* k_out,
+                          const mbx_heads_cview* q, const mbx_heads_cview* k,
+                          const mbx_cview* positions, const mbx_cview* freqs, const int32_t* axes,
+                          int n_axes, int interleaved, int inverse, void* stream);
+
+/* Validation only, as above. */
+MBX_API int mbx_check_layer_norm(const mbx_view* out, const mbx_cview* x, const mbx_cview* weight,
+                                 const mbx_cview* bias, float eps);
+MBX_API int mbx_check_layer_norm_backward(const mbx_view* dx, const mbx_view* dweight,
+                                          const mbx_view* dbias, const mbx_cview* dout,
+                                          const mbx_cview* x, const mbx_cview* weight,
+                                          const mbx_cview* dresidual, float eps,
+                                          const float* workspace, int64_t workspace_bytes);
+MBX_API int mbx_check_ln_modulate_backward(const mbx_view* dx, const mbx_view* dscale,
+                                           const mbx_view* dshift, const mbx_cview* dout,
+                                           const mbx_cview* x, const mbx_cview* scale,
+                                           const mbx_cview* dresidual, float eps,
+                                           const float* workspace, int64_t workspace_bytes);
+MBX_API int mbx_check_dropout(const mbx_view* out, const mbx_cview* x, double p,
+                              const int64_t* rng, int64_t offset);
+MBX_API int mbx_check_dropout_gate_add(const mbx_view* out, const mbx_cview* x,
+                                       const mbx_cview* gate, const mbx_cview* y, double p,
+                                       const int64_t* rng, int64_t offset);
+MBX_API int mbx_check_dropout_gate_add_backward(const mbx_view* dy, const mbx_view* dgate,
+                                                const mbx_cview* dout, const mbx_cview* gate,
+                                                const mbx_cview* y, double p, const int64_t* rng,
+                                                int64_t offset, const float* workspace,
+                                                int64_t workspace_bytes);
+MBX_API int mbx_check_rope_axes(const mbx_heads_view* q_out, const mbx_heads_view* k_out,
+                                const mbx_heads_cview* q, const mbx_heads_cview* k,
+                                const mbx_cview* positions, const mbx_cview* freqs,
+                                const int32_t* axes, int n_axes, int interleaved, int inverse);
 
 /*
  * Exhaustive self-test of the kernels' arithmetic building blocks against the

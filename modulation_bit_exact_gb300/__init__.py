@@ -32,11 +32,15 @@ __all__ = [
     "check_ln_modulate", "check_rmsnorm_scale",
     "check_rmsnorm_tanh_residual", "check_residual_gate_add",
     "check_qk_norm_rope_qkv_epilogue", "selftest", "status_string", "MbxError",
+    "layer_norm", "layer_norm_backward", "ln_modulate_backward", "param_grad_workspace",
+    "dropout", "dropout_gate_add", "dropout_gate_add_backward", "rope_axes", "rope_axis_freqs",
+    "check_layer_norm", "check_layer_norm_backward", "check_ln_modulate_backward", "check_dropout",
+    "check_dropout_gate_add", "check_dropout_gate_add_backward", "check_rope_axes",
     "LOSSLESS", "HIGH", "library_path",
 ]
 
 LOSSLESS, HIGH = 0, 1
-MBX_BF16, MBX_F32, MBX_E4M3, MBX_E2M1X2 = 1, 2, 3, 4
+MBX_BF16, MBX_F32, MBX_E4M3, MBX_E2M1X2, MBX_I32, MBX_F64 = 1, 2, 3, 4, 5, 6
 _VARIANTS = {"lossless": LOSSLESS, "high": HIGH, LOSSLESS: LOSSLESS, HIGH: HIGH}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -63,8 +67,16 @@ class _View(ctypes.Structure):
                 ("row_stride", ctypes.c_int64), ("dtype", ctypes.c_int32)]
 
 
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("tokens", ctypes.c_int64),
+                ("heads", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("batch_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
 _P = ctypes.POINTER(_View)
+_H = ctypes.POINTER(_Heads)
 _i64, _f32, _int, _vp = ctypes.c_int64, ctypes.c_float, ctypes.c_int, ctypes.c_void_p
+_f64 = ctypes.c_double
 
 _lock = threading.Lock()
 _lib = None
@@ -108,6 +120,21 @@ def _load() -> ctypes.CDLL:
             "mbx_check_residual_gate_add": [_P, _P, _P, _P, _int],
             "mbx_check_qk_norm_rope_qkv_epilogue": [_P, _P, _P, _i64, _i64, _P, _P, _P, _P,
                                                     _vp, _vp, _vp, _vp, _f32, _int],
+            "mbx_layer_norm": [_P, _P, _P, _P, _f32, _vp],
+            "mbx_check_layer_norm": [_P, _P, _P, _P, _f32],
+            "mbx_param_grad_workspace": [_i64, _i64, _i64, _int, ctypes.POINTER(_i64)],
+            "mbx_layer_norm_backward": [_P, _P, _P, _P, _P, _P, _P, _f32, _vp, _i64, _vp],
+            "mbx_check_layer_norm_backward": [_P, _P, _P, _P, _P, _P, _P, _f32, _vp, _i64],
+            "mbx_ln_modulate_backward": [_P, _P, _P, _P, _P, _P, _P, _f32, _vp, _i64, _vp],
+            "mbx_check_ln_modulate_backward": [_P, _P, _P, _P, _P, _P, _P, _f32, _vp, _i64],
+            "mbx_dropout": [_P, _P, _f64, _vp, _i64, _vp],
+            "mbx_check_dropout": [_P, _P, _f64, _vp, _i64],
+            "mbx_dropout_gate_add": [_P, _P, _P, _P, _f64, _vp, _i64, _vp],
+            "mbx_check_dropout_gate_add": [_P, _P, _P, _P, _f64, _vp, _i64],
+            "mbx_dropout_gate_add_backward": [_P, _P, _P, _P, _P, _f64, _vp, _i64, _vp, _i64, _vp],
+            "mbx_check_dropout_gate_add_backward": [_P, _P, _P, _P, _P, _f64, _vp, _i64, _vp, _i64],
+            "mbx_rope_axes": [_H, _H, _H, _H, _P, _P, ctypes.POINTER(ctypes.c_int32), _int, _int, _int, _vp],
+            "mbx_check_rope_axes": [_H, _H, _H, _H, _P, _P, ctypes.POINTER(ctypes.c_int32), _int, _int, _int],
             "mbx_selftest": [_int, _vp, _vp],
             "mbx_abi_version": [],
         }
@@ -170,7 +197,8 @@ def _view(t: torch.Tensor) -> _View:
     return _View(t.data_ptr() if t.numel() else None, rows, cols, stride, dtype)
 
 
-_DTYPES = {torch.bfloat16: MBX_BF16, torch.float32: MBX_F32, torch.uint8: MBX_E4M3}
+_DTYPES = {torch.bfloat16: MBX_BF16, torch.float32: MBX_F32, torch.uint8: MBX_E4M3,
+           torch.int32: MBX_I32, torch.float64: MBX_F64}
 if hasattr(torch, "float8_e4m3fn"):
     _DTYPES[torch.float8_e4m3fn] = MBX_E4M3
 
@@ -463,6 +491,199 @@ def qk_norm_rope_qkv_epilogue(txt_qkv, img_qkv, batch: int, heads: int, head_dim
         _ptr(cos_txt), _ptr(sin_txt), _ptr(cos_img), _ptr(sin_img), eps, _variant(variant),
         _stream(ref)))
     return out
+
+
+# ---------------------------------------------------------------- training path
+
+
+def _opt(t):
+    return None if t is None else ctypes.byref(_view(t))
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None):
+    """Affine LayerNorm over the last dimension (see mbx_layer_norm): x
+    bfloat16 or float32, weight and bias [D] of x's dtype or float32, or None."""
+    L = _load()
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    _raise(L.mbx_layer_norm(_ref(_view(out)), _ref(_view(x)), _opt(weight), _opt(bias), eps, _stream(x)))
+    return out
+
+
+def check_layer_norm(out, x, weight=None, bias=None, eps=1e-6) -> int:
+    return _load().mbx_check_layer_norm(_ref(_view(out)), _ref(_view(x)), _opt(weight), _opt(bias), eps)
+
+
+def param_grad_workspace(rows: int, cols: int, mod_rows: int, dtype: torch.dtype) -> int:
+    """Workspace bytes of the backward calls that sum `rows` rows of `cols`
+    elements of `dtype` into `mod_rows` parameter rows, on the current device
+    (see mbx_param_grad_workspace)."""
+    n = ctypes.c_int64()
+    _raise(_load().mbx_param_grad_workspace(rows, cols, mod_rows, _DTYPES.get(dtype, 0), ctypes.byref(n)))
+    return n.value
+
+
+def _workspace(x, params):
+    """A workspace for the gradient of `params` summed over x's rows, or None."""
+    if not x.is_cuda or x.numel() == 0 or params.numel() == 0:
+        return None  # the call itself is refused
+    cols = x.shape[-1]
+    rows, mod_rows = x.numel() // cols, params.numel() // cols
+    if mod_rows == 0 or rows == mod_rows:
+        return None
+    n = ctypes.c_int64()
+    if _load().mbx_param_grad_workspace(rows, cols, mod_rows, _DTYPES.get(x.dtype, 0), ctypes.byref(n)) != 0:
+        return None
+    return torch.empty(n.value // 4, dtype=torch.float32, device=x.device) if n.value else None
+
+
+def _ws_args(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def layer_norm_backward(dout, x, weight=None, eps: float = 1e-6, dresidual=None, dx=None, dweight=None,
+                        dbias=None):
+    """Gradients of ``layer_norm`` (see mbx_layer_norm_backward): (dx, dweight,
+    dbias), the last two None without a weight.  ``dresidual`` is added to dx,
+    and ``dx=dresidual`` updates it in place."""
+    L = _load()
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx is None else dx
+    ws = None
+    if weight is not None:
+        dweight = torch.empty(weight.shape, dtype=weight.dtype, device=weight.device) if dweight is None else dweight
+        dbias = torch.empty(weight.shape, dtype=weight.dtype, device=weight.device) if dbias is None else dbias
+        ws = _workspace(x, weight)
+    _raise(L.mbx_layer_norm_backward(_ref(_view(dx)), _opt(dweight), _opt(dbias), _ref(_view(dout)), _ref(_view(x)),
+                                     _opt(weight), _opt(dresidual), eps, *_ws_args(ws), _stream(x)))
+    return dx, dweight, dbias
+
+
+def check_layer_norm_backward(dx, dweight, dbias, dout, x, weight=None, eps=1e-6, dresidual=None,
+                              workspace=None) -> int:
+    return _load().mbx_check_layer_norm_backward(
+        _ref(_view(dx)), _opt(dweight), _opt(dbias), _ref(_view(dout)), _ref(_view(x)), _opt(weight),
+        _opt(dresidual), eps, *_ws_args(workspace))
+
+
+def ln_modulate_backward(dout, x, scale, eps: float = 1e-6, dresidual=None, dx=None, dscale=None, dshift=None):
+    """Gradients of ``ln_modulate`` (see mbx_ln_modulate_backward): (dx,
+    dscale, dshift), the last two of scale's shape and dtype, summed over the
+    rows that share a modulation row.  ``dresidual`` is added to dx."""
+    L = _load()
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx is None else dx
+    dscale = torch.empty(scale.shape, dtype=scale.dtype, device=scale.device) if dscale is None else dscale
+    dshift = torch.empty(scale.shape, dtype=scale.dtype, device=scale.device) if dshift is None else dshift
+    ws = _workspace(x, scale)
+    _raise(L.mbx_ln_modulate_backward(_ref(_view(dx)), _ref(_view(dscale)), _ref(_view(dshift)), _ref(_view(dout)),
+                                      _ref(_view(x)), _ref(_view(scale)), _opt(dresidual), eps, *_ws_args(ws),
+                                      _stream(x)))
+    return dx, dscale, dshift
+
+
+def check_ln_modulate_backward(dx, dscale, dshift, dout, x, scale, eps=1e-6, dresidual=None, workspace=None) -> int:
+    return _load().mbx_check_ln_modulate_backward(
+        _ref(_view(dx)), _opt(dscale), _opt(dshift), _ref(_view(dout)), _ref(_view(x)), _ref(_view(scale)),
+        _opt(dresidual), eps, *_ws_args(workspace))
+
+
+def _rng(rng):
+    """Pointer of the generator's state: an int64 tensor (seed, counter)."""
+    if rng is None or rng.dtype != torch.int64 or rng.numel() != 2 or not rng.is_contiguous():
+        raise MbxError(-12, "MBX_E_ARG: rng must be a contiguous int64 tensor (seed, counter)")
+    return rng.data_ptr()
+
+
+def dropout(x, p: float, rng, offset: int = 0, out=None):
+    """Dropout whose mask is computed from rng, an int64 CUDA tensor (seed,
+    counter), and never stored (see mbx_dropout); ``out=x`` is in place.  The
+    gradient is ``dropout(dout, p, rng, offset)``."""
+    L = _load()
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    _raise(L.mbx_dropout(_ref(_view(out)), _ref(_view(x)), p, _rng(rng), offset, _stream(x)))
+    return out
+
+
+def check_dropout(out, x, p, rng, offset=0) -> int:
+    return _load().mbx_check_dropout(_ref(_view(out)), _ref(_view(x)), p, _rng(rng), offset)
+
+
+def dropout_gate_add(x, gate, y, p: float, rng, offset: int = 0, out=None):
+    """out = x + gate * dropout(y) (see mbx_dropout_gate_add); ``out=x`` is in place."""
+    L = _load()
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    _raise(L.mbx_dropout_gate_add(_ref(_view(out)), _ref(_view(x)), _ref(_view(gate)), _ref(_view(y)), p, _rng(rng),
+                                  offset, _stream(x)))
+    return out
+
+
+def check_dropout_gate_add(out, x, gate, y, p, rng, offset=0) -> int:
+    return _load().mbx_check_dropout_gate_add(_ref(_view(out)), _ref(_view(x)), _ref(_view(gate)), _ref(_view(y)), p,
+                                              _rng(rng), offset)
+
+
+def dropout_gate_add_backward(dout, gate, y, p: float, rng, offset: int = 0, dy=None, dgate=None):
+    """Gradients of ``dropout_gate_add`` (see mbx_dropout_gate_add_backward):
+    (dy, dgate); the gradient of x is dout itself."""
+    L = _load()
+    dy = torch.empty(y.shape, dtype=y.dtype, device=y.device) if dy is None else dy
+    dgate = torch.empty(gate.shape, dtype=gate.dtype, device=gate.device) if dgate is None else dgate
+    ws = _workspace(y, gate)
+    _raise(L.mbx_dropout_gate_add_backward(_ref(_view(dy)), _ref(_view(dgate)), _ref(_view(dout)), _ref(_view(gate)),
+                                           _ref(_view(y)), p, _rng(rng), offset, *_ws_args(ws), _stream(y)))
+    return dy, dgate
+
+
+def check_dropout_gate_add_backward(dy, dgate, dout, gate, y, p, rng, offset=0, workspace=None) -> int:
+    return _load().mbx_check_dropout_gate_add_backward(
+        _ref(_view(dy)), _opt(dgate), _ref(_view(dout)), _ref(_view(gate)), _ref(_view(y)), p, _rng(rng), offset,
+        *_ws_args(workspace))
+
+
+def rope_axis_freqs(axes, theta: float = 10000.0, device="cuda") -> torch.Tensor:
+    """The frequency ladder of ``rope_axes``: for each axis of d elements the
+    angles per position theta^(-2j/d), j < d/2, as one float64 tensor."""
+    return torch.cat([
+        torch.pow(torch.tensor(float(theta), dtype=torch.float64),
+                  torch.arange(0, d, 2, dtype=torch.float64) / -d) for d in axes]).to(device)
+
+
+def _heads(t):
+    """View of a [batch, tokens, heads, head_dim] (or [tokens, heads, head_dim])
+    tensor; strides of any order, the last dimension contiguous."""
+    if t.dim() == 3:
+        t = t.unsqueeze(0)
+    if t.dim() != 4:
+        raise MbxError(-5, "MBX_E_SHAPE: expected [batch, tokens, heads, head_dim]")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise MbxError(-6, "MBX_E_STRIDE: the last dimension must be contiguous")
+    return _Heads(t.data_ptr() if t.numel() else None, *t.shape, *t.stride()[:3], _DTYPES.get(t.dtype, 0))
+
+
+def _rope_args(q, k, positions, freqs, axes, interleaved, inverse, q_out, k_out):
+    hv = [None if t is None else ctypes.byref(_heads(t)) for t in (q_out, k_out, q, k)]
+    dims = (ctypes.c_int32 * max(1, len(axes)))(*axes)
+    return (*hv, _ref(_view(positions)), _ref(_view(freqs)), dims, len(axes), int(interleaved), int(inverse))
+
+
+def rope_axes(q, k, positions, freqs, axes, interleaved: bool = True, inverse: bool = False, q_out=None,
+              k_out=None):
+    """Rotary positions on several axes for Q and K in one launch (see
+    mbx_rope_axes).
+
+    q [B, S, Hq, hd] and k [B, S, Hk, hd] (or None) may be strided: slices of a
+    merged QKV buffer, or a head-major buffer transposed to this order.
+    positions [S, A] or [B, S, A] int32 or float32; axes: the A axis widths;
+    freqs: ``rope_axis_freqs(axes)`` or other angles per position, float64.
+    ``inverse=True`` turns back, which is the gradient.  Returns (q_out, k_out);
+    ``q_out=q, k_out=k`` rotates in place."""
+    L = _load()
+    q_out = torch.empty_like(q) if q_out is None else q_out
+    k_out = torch.empty_like(k) if k_out is None and k is not None else k_out
+    _raise(L.mbx_rope_axes(*_rope_args(q, k, positions, freqs, axes, interleaved, inverse, q_out, k_out), _stream(q)))
+    return q_out, k_out
+
+
+def check_rope_axes(q_out, k_out, q, k, positions, freqs, axes, interleaved=True, inverse=False) -> int:
+    return _load().mbx_check_rope_axes(*_rope_args(q, k, positions, freqs, axes, interleaved, inverse, q_out, k_out))
 
 
 # ---------------------------------------------------------------- validation only

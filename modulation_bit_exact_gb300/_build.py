@@ -16,16 +16,21 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = [
     os.path.join(CSRC, "mbx_api.cu"),
+    os.path.join(CSRC, "train_api.cu"),
     os.path.join(KERN, "ln_modulate.cu"),
     os.path.join(KERN, "ln_nvfp4.cu"),
     os.path.join(KERN, "rmsnorm.cu"),
     os.path.join(KERN, "residual.cu"),
     os.path.join(KERN, "qkv.cu"),
     os.path.join(KERN, "modtable.cu"),
+    os.path.join(KERN, "layernorm.cu"),
+    os.path.join(KERN, "dropout.cu"),
+    os.path.join(KERN, "colsum.cu"),
+    os.path.join(KERN, "rope.cu"),
     os.path.join(KERN, "selftest.cu"),
 ]
 HEADERS = [os.path.join(KERN, f) for f in os.listdir(KERN) if f.endswith((".cuh", ".h", ".inc"))]
-HEADERS.append(os.path.join(INCLUDE, "mbx.h"))
+HEADERS += [os.path.join(CSRC, "views.h"), os.path.join(INCLUDE, "mbx.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
