@@ -24,6 +24,7 @@ SOURCES = [
     os.path.join(KERN, "qkv.cu"),
     os.path.join(KERN, "modtable.cu"),
     os.path.join(KERN, "layernorm.cu"),
+    os.path.join(KERN, "layernorm_bwd.cu"),
     os.path.join(KERN, "dropout.cu"),
     os.path.join(KERN, "colsum.cu"),
     os.path.join(KERN, "rope.cu"),

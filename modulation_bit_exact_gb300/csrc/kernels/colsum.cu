@@ -5,34 +5,62 @@
 
 namespace mbx {
 
-RowShape row_shape(int D, int esize) {
-    const int ce = 16 / esize;
-    RowShape s;
-    s.epl = D <= 256 ? 8 : 16;
-    const int lanes = (D + s.epl - 1) / s.epl;  // threads that own a full share
-    s.tpr = (lanes + 31) / 32 * 32;
-    (void)ce;
-    s.groups = s.tpr >= 256 ? 1 : 256 / s.tpr;
+RingShape ring_shape(int tpr, int row_bytes, int rows, int extra_bytes) {
+    RingShape s;
+    s.tpr = tpr;
+    s.row_bytes = row_bytes;
+    s.extra_bytes = extra_bytes;
+    s.groups = tpr >= 320 ? 1 : 320 / tpr;
+    while (s.groups * tpr % 32) --s.groups;  // whole warps
+    s.sums_bytes = tpr > 32 ? s.groups * 2 * 8 * 16 * (int)sizeof(float) : 0;
+    const int stage = (rows * row_bytes + extra_bytes) * s.groups;
+    // as many blocks as the threads allow, if two stages fit for each
+    for (s.ctas_per_sm = kRingThreads / (s.groups * tpr);; --s.ctas_per_sm) {
+        const int room = 228 * 1024 / s.ctas_per_sm - 1024 - s.sums_bytes;  // 1 KB of each block's is the system's
+        s.stages = room / stage;
+        if (s.stages >= 2 || s.ctas_per_sm == 1) break;
+    }
+    if (s.stages > 4) s.stages = 4;
+    s.group_bytes = s.stages * (rows * row_bytes + extra_bytes);
+    s.smem = s.sums_bytes + s.groups * s.group_bytes;
     return s;
 }
 
-GradPlan grad_plan(int64_t rows, int64_t mod_rows, const RowShape& sh) {
+cudaError_t SmemOptIn::allow(const void* kernel, const RingShape& sh) {
+    if (sh.stages < 1) return cudaErrorInvalidConfiguration;
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (allowed[dev].load(std::memory_order_acquire) >= sh.smem) return cudaSuccess;
+    int most = 0;
+    if (cudaError_t e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) return e;
+    if (sh.smem > most) return cudaErrorInvalidConfiguration;
+    // the limit itself: another thread may ask for more at the same time
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) return e;
+    allowed[dev].store(most, std::memory_order_release);
+    return cudaSuccess;
+}
+
+RingShape grad_shape(int D, int esize, int rows) {
+    const int tpr = row_threads(D);
+    return ring_shape(tpr, 16 * esize * tpr, rows, 0);
+}
+
+GradPlan grad_plan(int64_t rows, int64_t mod_rows, int D, int esize) {
     const int64_t seq = rows / mod_rows;
+    const RingShape sh = grad_shape(D, esize, 2);
+    const int64_t round = (int64_t)sh.groups * 2;  // whole rounds of a block, which takes one or two rows a group
+    int64_t parts = ((int64_t)sm_count() * sh.ctas_per_sm + mod_rows - 1) / mod_rows;
+    if (parts > (seq + round - 1) / round) parts = (seq + round - 1) / round;
     GradPlan g;
-    g.groups = seq >= 2 * sh.groups ? sh.groups : 1;
-    const int64_t target = (int64_t)sm_count() * (sh.block() <= 320 ? 2 : 1);
-    int64_t parts = (target + mod_rows - 1) / mod_rows;
-    const int64_t most = (seq + 2 * g.groups - 1) / (2 * g.groups);  // two rows a group at least
-    if (parts > most) parts = most;
-    if (parts < 1) parts = 1;
-    g.rows_per_part = (seq + parts - 1) / parts;
+    g.rows_per_part = ((seq + parts - 1) / parts + round - 1) / round * round;
     g.parts = (seq + g.rows_per_part - 1) / g.rows_per_part;
     return g;
 }
 
 int64_t grad_workspace_bytes(int64_t rows, int64_t mod_rows, int D, int esize) {
     if (rows == mod_rows) return 0;
-    const GradPlan g = grad_plan(rows, mod_rows, row_shape(D, esize));
+    const GradPlan g = grad_plan(rows, mod_rows, D, esize);
     return g.parts == 1 ? 0 : mod_rows * g.parts * 2 * D * (int64_t)sizeof(float);
 }
 

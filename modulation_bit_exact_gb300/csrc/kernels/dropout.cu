@@ -185,35 +185,38 @@ __global__ void __launch_bounds__(512) dropout_backward_kernel(DropParams p) {
 // ---------------------------------------------------------------- launch
 
 template <class T, int NCH>
-static cudaError_t drop_fwd(const DropParams& p0, const RowShape& sh, bool vec, cudaStream_t s) {
+static cudaError_t drop_fwd(const DropParams& p0, bool vec, cudaStream_t s) {
     DropParams p = p0;
-    p.tpr = sh.tpr;
+    p.tpr = row_threads(p.D);
+    if (p.tpr < 32) p.tpr = 32;
+    p.groups = p.tpr >= 256 ? 1 : 256 / p.tpr;
+    const int block = p.tpr * p.groups;
     auto k = p.gate ? (vec ? dropout_kernel<T, NCH, kVec, true> : dropout_kernel<T, NCH, kQuad, true>)
                     : (vec ? dropout_kernel<T, NCH, kVec, false> : dropout_kernel<T, NCH, kQuad, false>);
-    const int grid = grid_for_rows(reinterpret_cast<const void*>(k), p.rows, sh.groups, sh.block());
+    const int grid = grid_for_rows(reinterpret_cast<const void*>(k), p.rows, p.groups, block);
     if (grid < 0) return cudaErrorUnknown;
-    return launch_pdl(k, grid, sh.block(), 0, s, p);
+    return launch_pdl(k, grid, block, 0, s, p);
 }
 
 cudaError_t launch_dropout(const DropParams& p, bool f32, bool vec, cudaStream_t s) {
-    const RowShape sh = row_shape(p.D, f32 ? 4 : 2);
-    if (f32) return sh.epl == 16 ? drop_fwd<float, 4>(p, sh, vec, s) : drop_fwd<float, 2>(p, sh, vec, s);
-    return sh.epl == 16 ? drop_fwd<uint16_t, 2>(p, sh, vec, s) : drop_fwd<uint16_t, 1>(p, sh, vec, s);
+    return f32 ? drop_fwd<float, 4>(p, vec, s) : drop_fwd<uint16_t, 2>(p, vec, s);
 }
 
 template <class T, int NCH>
-static cudaError_t drop_bwd(const DropParams& p0, const RowShape& sh, bool vec, cudaStream_t s) {
+static cudaError_t drop_bwd(const DropParams& p0, bool vec, cudaStream_t s) {
     DropParams p = p0;
-    p.tpr = sh.tpr;
+    p.tpr = row_threads(p.D);
+    if (p.tpr < 32) p.tpr = 32;
+    p.groups = p.tpr >= 256 ? 1 : 256 / p.tpr;
+    const int block = p.tpr * p.groups;
     if (p.seq == 1) {
         auto k = vec ? dropout_backward_token_kernel<T, NCH, kVec> : dropout_backward_token_kernel<T, NCH, kQuad>;
-        const int grid = grid_for_rows(reinterpret_cast<const void*>(k), p.rows, sh.groups, sh.block());
+        const int grid = grid_for_rows(reinterpret_cast<const void*>(k), p.rows, p.groups, block);
         if (grid < 0) return cudaErrorUnknown;
-        return launch_pdl(k, grid, sh.block(), 0, s, p);
+        return launch_pdl(k, grid, block, 0, s, p);
     }
-    p.plan = grad_plan(p.rows, p.mod_rows, sh);
-    const int block = p.plan.groups * sh.tpr;
-    const size_t smem = p.plan.groups > 1 ? (size_t)block * sh.epl * sizeof(float) : 0;
+    p.plan = grad_plan(p.rows, p.mod_rows, p.D, (int)sizeof(T));
+    const size_t smem = p.groups > 1 ? (size_t)block * 16 * sizeof(float) : 0;
     const int64_t units = p.mod_rows * p.plan.parts;
     auto k = vec ? dropout_backward_kernel<T, NCH, kVec> : dropout_backward_kernel<T, NCH, kQuad>;
     cudaError_t e = launch_pdl(k, (unsigned)(units < (1 << 30) ? units : (1 << 30)), block, smem, s, p);
@@ -223,10 +226,8 @@ static cudaError_t drop_bwd(const DropParams& p0, const RowShape& sh, bool vec, 
 }
 
 cudaError_t launch_dropout_backward(const DropParams& p, bool f32, bool vec, cudaStream_t s) {
-    const RowShape sh = row_shape(p.D, f32 ? 4 : 2);
     return launch_all_or_none([&] {
-        if (f32) return sh.epl == 16 ? drop_bwd<float, 4>(p, sh, vec, s) : drop_bwd<float, 2>(p, sh, vec, s);
-        return sh.epl == 16 ? drop_bwd<uint16_t, 2>(p, sh, vec, s) : drop_bwd<uint16_t, 1>(p, sh, vec, s);
+        return f32 ? drop_bwd<float, 4>(p, vec, s) : drop_bwd<uint16_t, 2>(p, vec, s);
     });
 }
 

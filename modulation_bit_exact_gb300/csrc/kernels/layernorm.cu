@@ -16,274 +16,138 @@
 // ones: x is in registers for xh anyway, sum(x) travels with sum(gy) and
 // sum((x-mean)^2) with sum(gy*(x-mean)), so it costs one more row sum of two
 // and no memory, and a forward pass need not save anything.
-#include "rowgroup.cuh"
+#include "lnorm.cuh"
 
 namespace mbx {
 
-template <class T, int NCH, Access A>
-__global__ void __launch_bounds__(512) layer_norm_kernel(LnFwdParams p, int tpr) {
+// R rows of a group at a time: their sums share the shuffles and the barrier.
+template <class T, int NCH, Access A, int R>
+__global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p, RingShape sh) {
     constexpr int CE = ChunkOf<T>::CE, E = NCH * CE;
-    __shared__ float2 sums[512 / 32][2][kMaxWarpsPerRow];
-    const int g = threadIdx.x / tpr, t = threadIdx.x % tpr, groups = blockDim.x / tpr;
-    GroupSum gsum{&sums[g][0][0], t, tpr, g + 1, 0};
+    extern __shared__ __align__(16) char smem[];
+    const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr;
+    const Lane L = make_lane<CE, A>(t, tpr, p.D);
+    GroupSums sums = group_sums(smem, sh, g, t);
+    char* ring = smem + sh.sums_bytes + g * sh.group_bytes;
     const float inv_d = 1.0f / (float)p.D;
     grid_dep_wait();  // launched programmatically: the previous kernel has finished
     grid_dep_launch();
 
-    float w[E], b[E];
-    if (p.weight) load_params<T, NCH, A>(w, p.weight, 0, p.p_f32, p.D, t, tpr, 0.0f);
-    else
+    u64 w[E / 2], b[E / 2];
 #pragma unroll
-        for (int e = 0; e < E; ++e) w[e] = 1.0f;
-    if (p.bias) load_params<T, NCH, A>(b, p.bias, 0, p.p_f32, p.D, t, tpr, 0.0f);
-    else
+    for (int j = 0; j < NCH; ++j) {
+        u64 c[CE / 2];
 #pragma unroll
-        for (int e = 0; e < E; ++e) b[e] = 0.0f;
+        for (int i = 0; i < CE / 2; ++i) c[i] = f2(1.0f, 1.0f);
+        if (p.weight) get_param_chunk<T, CE, A>(c, p.weight, 0, p.p_f32, j, L);
+#pragma unroll
+        for (int i = 0; i < CE / 2; ++i) w[j * (CE / 2) + i] = c[i], c[i] = 0;
+        if (p.bias) get_param_chunk<T, CE, A>(c, p.bias, 0, p.p_f32, j, L);
+#pragma unroll
+        for (int i = 0; i < CE / 2; ++i) b[j * (CE / 2) + i] = c[i];
+    }
 
     const T* x = static_cast<const T*>(p.x);
     T* out = static_cast<T*>(p.out);
-    const int64_t step = (int64_t)gridDim.x * groups;
-    RawRow<T, NCH, A> next;
-    int64_t row = (int64_t)blockIdx.x * groups + g;
-    if (row < p.rows) next.load(x + row * p.x_stride, p.D, t, tpr);
-    for (; row < p.rows; row += step) {
-        float v[E];
-        next.widen(v);
-        if (row + step < p.rows) next.load(x + (row + step) * p.x_stride, p.D, t, tpr);
-        float s = 0.0f;
+    const int row_bytes = sh.row_bytes, stage_bytes = R * row_bytes;
+    // batches of R consecutive rows, dealt to the groups of the whole grid
+    const int64_t per_round = (int64_t)gridDim.x * sh.groups;
+    const int64_t first = (int64_t)blockIdx.x * sh.groups + g;
+    const int64_t rounds = ((p.rows + R - 1) / R + per_round - 1) / per_round;  // the same for every group
+    int fill_stage = 0;
+    auto fill = [&](int64_t round) {
+        const int64_t r0 = (first + round * per_round) * R;
+        char* dst = ring + fill_stage * stage_bytes;
+        if (++fill_stage == sh.stages) fill_stage = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) s += v[e];
-        const float mean = gsum(s, 0.0f).x * inv_d;
-        float q = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            v[e] = col_of<T, A>(e, t, tpr) < p.D ? v[e] - mean : 0.0f;
-            q = fmaf(v[e], v[e], q);
-        }
-        const float var = gsum(q, 0.0f).x * inv_d;
-        const float rstd = 1.0f / sqrtf(var + p.eps);
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = fmaf(v[e] * rstd, w[e], b[e]);
-        store_row<T, NCH, A>(out + row * p.out_stride, v, p.D, t, tpr);
-    }
-}
+        for (int k = 0; k < R; ++k)
+            if (r0 + k < p.rows) ring_fill<T, NCH, CE, A>(dst + k * row_bytes, x + (r0 + k) * p.x_stride, L);
+        ring_commit();
+    };
+    for (int i = 0; i < sh.stages - 1; ++i) fill(i);
+    int stage = 0;
+    for (int64_t round = 0; round < rounds; ++round) {
+        ring_turn(sh.stages, round, fill);
+        const char* src = ring + stage * stage_bytes;
+        if (++stage == sh.stages) stage = 0;
+        const int64_t r0 = (first + round * per_round) * R;
 
-// One row's gradient: v holds x and becomes xh, dy holds dy, dx is returned.
-template <class T, int NCH, Access A>
-__device__ __forceinline__ void ln_row_backward(float (&v)[NCH * ChunkOf<T>::CE], const float (&dy)[NCH * ChunkOf<T>::CE],
-                                                const float (&f)[NCH * ChunkOf<T>::CE],
-                                                float (&dx)[NCH * ChunkOf<T>::CE], const LnBwdParams& p, float inv_d,
-                                                GroupSum& gsum) {
-    constexpr int CE = ChunkOf<T>::CE, E = NCH * CE;
-    float s = 0.0f, sg = 0.0f;
+        float mean[R], rstd[R];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        s += v[e];
-        dx[e] = dy[e] * f[e];  // gy
-        sg += dx[e];
-    }
-    const float2 m = gsum(s, sg);
-    const float mean = m.x * inv_d, c1 = m.y * inv_d;
-    float q = 0.0f, qg = 0.0f;
+        for (int k = 0; k < R; ++k) {
+            u64 s = 0;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        v[e] = col_of<T, A>(e, gsum.t, gsum.tpr) < p.D ? v[e] - mean : 0.0f;
-        q = fmaf(v[e], v[e], q);
-        qg = fmaf(dx[e], v[e], qg);
-    }
-    const float2 m2 = gsum(q, qg);
-    const float rstd = 1.0f / sqrtf(m2.x * inv_d + p.eps);
-    const float c2 = m2.y * inv_d * rstd;
+            for (int j = 0; j < NCH; ++j) {
+                if (!has_chunk<A>(j, L)) continue;
+                u64 v[CE / 2];
+                ring_read<T, CE, A>(v, src + k * row_bytes, j, L);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        v[e] *= rstd;
-        dx[e] = rstd * (fmaf(-v[e], c2, dx[e] - c1));
-    }
-}
-
-template <class T, int NCH, Access A>
-__device__ __forceinline__ void load_factor(float (&f)[NCH * ChunkOf<T>::CE], const LnBwdParams& p, int64_t mrow, int t,
-                                            int tpr) {
-    constexpr int E = NCH * ChunkOf<T>::CE;
-    if (p.factor) {
-        load_params<T, NCH, A>(f, p.factor, mrow * p.factor_stride, p.p_f32, p.D, t, tpr, 0.0f);
-#pragma unroll
-        for (int e = 0; e < E; ++e) f[e] += p.factor_add;
-    } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) f[e] = 1.0f + p.factor_add;
-    }
-}
-
-// One modulation row for every row: nothing is summed, every output is a row.
-template <class T, int NCH, Access A>
-__global__ void __launch_bounds__(512) ln_backward_token_kernel(LnBwdParams p) {
-    constexpr int CE = ChunkOf<T>::CE, E = NCH * CE;
-    __shared__ float2 sums[512 / 32][2][kMaxWarpsPerRow];
-    const int tpr = p.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr, groups = blockDim.x / tpr;
-    GroupSum gsum{&sums[g][0][0], t, tpr, g + 1, 0};
-    const float inv_d = 1.0f / (float)p.D;
-    grid_dep_wait();
-    grid_dep_launch();
-    const int64_t step = (int64_t)gridDim.x * groups;
-    for (int64_t row = (int64_t)blockIdx.x * groups + g; row < p.rows; row += step) {
-        RawRow<T, NCH, A> rx, rd, rr;
-        rx.load(static_cast<const T*>(p.x) + row * p.x_stride, p.D, t, tpr);
-        rd.load(static_cast<const T*>(p.dout) + row * p.dout_stride, p.D, t, tpr);
-        float v[E], dy[E], f[E], dx[E];
-        load_factor<T, NCH, A>(f, p, row, t, tpr);
-        if (p.dres) rr.load(static_cast<const T*>(p.dres) + row * p.dres_stride, p.D, t, tpr);
-        rx.widen(v);
-        rd.widen(dy);
-        ln_row_backward<T, NCH, A>(v, dy, f, dx, p, inv_d, gsum);
-        if (p.dres) {
-            float r[E];
-            rr.widen(r);
-#pragma unroll
-            for (int e = 0; e < E; ++e) dx[e] += r[e];
-        }
-        store_row<T, NCH, A>(static_cast<T*>(p.dx) + row * p.dx_stride, dx, p.D, t, tpr);
-        if (p.dshift) store_params<T, NCH, A>(p.dshift, row * p.dshift_stride, p.p_f32, dy, p.D, t, tpr);
-        if (p.dfactor) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[e] *= dy[e];
-            store_params<T, NCH, A>(p.dfactor, row * p.dfactor_stride, p.p_f32, v, p.D, t, tpr);
-        }
-    }
-}
-
-// Modulation rows shared by seq rows: a block takes one part of a segment, its
-// row groups the rows of the part in turn; every thread sums its own columns
-// in binary32 registers, the groups are added in shared memory, and the part's
-// sums go to the workspace (or out, when the segment is one part).
-template <class T, int NCH, Access A>
-__global__ void __launch_bounds__(512) ln_backward_kernel(LnBwdParams p) {
-    constexpr int CE = ChunkOf<T>::CE, E = NCH * CE;
-    __shared__ float2 sums[512 / 32][2][kMaxWarpsPerRow];
-    extern __shared__ float acc_smem[];  // [2][E][block]
-    const int tpr = p.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr, groups = blockDim.x / tpr;
-    GroupSum gsum{&sums[g][0][0], t, tpr, g + 1, 0};
-    const float inv_d = 1.0f / (float)p.D;
-    grid_dep_wait();
-    grid_dep_launch();
-    const T* px = static_cast<const T*>(p.x);
-    const T* pd = static_cast<const T*>(p.dout);
-    const T* pr = static_cast<const T*>(p.dres);
-    const int64_t units = p.mod_rows * p.plan.parts;
-    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const int64_t seg = unit / p.plan.parts, part = unit - seg * p.plan.parts;
-        const int64_t r0 = seg * p.seq + part * p.plan.rows_per_part;
-        int64_t r1 = r0 + p.plan.rows_per_part;
-        if (r1 > (seg + 1) * p.seq) r1 = (seg + 1) * p.seq;
-        float f[E], adf[E], ads[E];
-        load_factor<T, NCH, A>(f, p, seg, t, tpr);
-#pragma unroll
-        for (int e = 0; e < E; ++e) adf[e] = ads[e] = 0.0f;
-        RawRow<T, NCH, A> rx, rd;
-        int64_t row = r0 + g;
-        if (row < r1) {
-            rx.load(px + row * p.x_stride, p.D, t, tpr);
-            rd.load(pd + row * p.dout_stride, p.D, t, tpr);
-        }
-        for (; row < r1; row += groups) {
-            float v[E], dy[E], dx[E];
-            rx.widen(v);
-            rd.widen(dy);
-            RawRow<T, NCH, A> rr;
-            if (pr) rr.load(pr + row * p.dres_stride, p.D, t, tpr);
-            if (row + groups < r1) {
-                rx.load(px + (row + groups) * p.x_stride, p.D, t, tpr);
-                rd.load(pd + (row + groups) * p.dout_stride, p.D, t, tpr);
+                for (int i = 0; i < CE / 2; ++i) s = add2(s, v[i]);
             }
-            ln_row_backward<T, NCH, A>(v, dy, f, dx, p, inv_d, gsum);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                adf[e] = fmaf(dy[e], v[e], adf[e]);
-                ads[e] += dy[e];
-            }
-            if (pr) {
-                float r[E];
-                rr.widen(r);
-#pragma unroll
-                for (int e = 0; e < E; ++e) dx[e] += r[e];
-            }
-            store_row<T, NCH, A>(static_cast<T*>(p.dx) + row * p.dx_stride, dx, p.D, t, tpr);
+            mean[k] = f2lo(s) + f2hi(s);
         }
-        if (p.dfactor == nullptr && p.dshift == nullptr) continue;
-        if (groups > 1) {
-            const int n = blockDim.x;
+        sums(mean);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                acc_smem[e * n + threadIdx.x] = adf[e];
-                acc_smem[(E + e) * n + threadIdx.x] = ads[e];
-            }
-            __syncthreads();
-            if (g == 0) {
+        for (int k = 0; k < R; ++k) {
+            mean[k] *= inv_d;
+            const u64 m = f2(mean[k], mean[k]);
+            u64 q = 0;
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    for (int k = 1; k < groups; ++k) {
-                        adf[e] += acc_smem[e * n + k * tpr + t];
-                        ads[e] += acc_smem[(E + e) * n + k * tpr + t];
-                    }
+            for (int j = 0; j < NCH; ++j) {
+                if (!has_chunk<A>(j, L)) continue;
+                u64 v[CE / 2];
+                ring_read<T, CE, A>(v, src + k * row_bytes, j, L);
+#pragma unroll
+                for (int i = 0; i < CE / 2; ++i) {
+                    const u64 c = mask_pair<CE, A>(sub2(v[i], m), j, i, L);
+                    q = fma2(c, c, q);
+                }
             }
-            __syncthreads();
+            rstd[k] = f2lo(q) + f2hi(q);
         }
-        if (g == 0) {
-            if (p.plan.parts == 1) {
-                if (p.dfactor)
-                    store_params<T, NCH, A>(p.dfactor, seg * p.dfactor_stride, p.p_f32, adf, p.D, t, tpr);
-                if (p.dshift) store_params<T, NCH, A>(p.dshift, seg * p.dshift_stride, p.p_f32, ads, p.D, t, tpr);
-            } else {
-                store_params<T, NCH, A>(p.ws, unit * 2 * p.D, true, adf, p.D, t, tpr);
-                store_params<T, NCH, A>(p.ws, (unit * 2 + 1) * p.D, true, ads, p.D, t, tpr);
+        sums(rstd);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            rstd[k] = 1.0f / sqrtf(rstd[k] * inv_d + p.eps);
+            const u64 m = f2(mean[k], mean[k]), rs = f2(rstd[k], rstd[k]);
+            if (r0 + k >= p.rows) continue;
+            T* dst = out + (r0 + k) * p.out_stride;
+#pragma unroll
+            for (int j = 0; j < NCH; ++j) {
+                if (!has_chunk<A>(j, L)) continue;
+                u64 v[CE / 2];
+                ring_read<T, CE, A>(v, src + k * row_bytes, j, L);
+#pragma unroll
+                for (int i = 0; i < CE / 2; ++i)
+                    v[i] = fma2(mul2(sub2(v[i], m), rs), w[j * (CE / 2) + i], b[j * (CE / 2) + i]);
+                put_chunk<T, CE, A>(dst, v, j, L);
             }
         }
     }
 }
 
-// ---------------------------------------------------------------- launch
+template <class T, int NCH, Access A, int R>
+static cudaError_t ln_fwd(const LnFwdParams& p, int tpr, cudaStream_t s) {
+    auto k = layer_norm_kernel<T, NCH, A, R>;
+    const RingShape sh = ring_shape(tpr, kRowBytesPerThread<T, NCH, ChunkOf<T>::CE> * tpr, R, 0);
+    static SmemOptIn opt_in;
+    if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
+    const int64_t batches = (p.rows + R - 1) / R, need = (batches + sh.groups - 1) / sh.groups;
+    const int64_t most = (int64_t)sm_count() * sh.ctas_per_sm;
+    return launch_pdl(k, (unsigned)(need < most ? need : most), sh.groups * tpr, sh.smem, s, p, sh);
+}
 
 template <class T, int NCH>
-static cudaError_t ln_fwd(const LnFwdParams& p, const RowShape& sh, bool vec, cudaStream_t s) {
-    auto k = vec ? layer_norm_kernel<T, NCH, kVec> : layer_norm_kernel<T, NCH, kScalar>;
-    const int grid = grid_for_rows(reinterpret_cast<const void*>(k), p.rows, sh.groups, sh.block());
-    if (grid < 0) return cudaErrorUnknown;
-    return launch_pdl(k, grid, sh.block(), 0, s, p, sh.tpr);
+static cudaError_t ln_fwd_r(const LnFwdParams& p, bool vec, cudaStream_t s) {
+    const int tpr = row_threads(p.D);
+    // two rows a round while every SM has several
+    const bool two = p.rows >= 8 * (int64_t)sm_count();
+    if (!vec) return ln_fwd<T, NCH, kScalar, 1>(p, tpr, s);
+    return two ? ln_fwd<T, NCH, kVec, 2>(p, tpr, s) : ln_fwd<T, NCH, kVec, 1>(p, tpr, s);
 }
 
 cudaError_t launch_layer_norm(const LnFwdParams& p, bool f32, bool vec, cudaStream_t s) {
-    const RowShape sh = row_shape(p.D, f32 ? 4 : 2);
-    if (f32) return sh.epl == 16 ? ln_fwd<float, 4>(p, sh, vec, s) : ln_fwd<float, 2>(p, sh, vec, s);
-    return sh.epl == 16 ? ln_fwd<uint16_t, 2>(p, sh, vec, s) : ln_fwd<uint16_t, 1>(p, sh, vec, s);
-}
-
-template <class T, int NCH>
-static cudaError_t ln_bwd(const LnBwdParams& p0, const RowShape& sh, bool vec, cudaStream_t s) {
-    LnBwdParams p = p0;
-    p.tpr = sh.tpr;
-    if (p.seq == 1) {
-        auto k = vec ? ln_backward_token_kernel<T, NCH, kVec> : ln_backward_token_kernel<T, NCH, kScalar>;
-        const int grid = grid_for_rows(reinterpret_cast<const void*>(k), p.rows, sh.groups, sh.block());
-        if (grid < 0) return cudaErrorUnknown;
-        return launch_pdl(k, grid, sh.block(), 0, s, p);
-    }
-    p.plan = grad_plan(p.rows, p.mod_rows, sh);
-    const int block = p.plan.groups * sh.tpr;
-    const size_t smem = p.plan.groups > 1 ? (size_t)block * sh.epl * 2 * sizeof(float) : 0;
-    const int64_t units = p.mod_rows * p.plan.parts;
-    auto k = vec ? ln_backward_kernel<T, NCH, kVec> : ln_backward_kernel<T, NCH, kScalar>;
-    cudaError_t e = launch_pdl(k, (unsigned)(units < (1 << 30) ? units : (1 << 30)), block, smem, s, p);
-    if (e != cudaSuccess || p.plan.parts == 1 || (!p.dfactor && !p.dshift)) return e;
-    ColSumParams c{p.ws, p.plan.parts, p.mod_rows, p.D, 2, {p.dfactor, p.dshift}, {p.dfactor_stride, p.dshift_stride}, p.p_f32};
-    return launch_column_sums(c, s);
-}
-
-cudaError_t launch_ln_backward(const LnBwdParams& p, bool f32, bool vec, cudaStream_t s) {
-    const RowShape sh = row_shape(p.D, f32 ? 4 : 2);
-    return launch_all_or_none([&] {
-        if (f32) return sh.epl == 16 ? ln_bwd<float, 4>(p, sh, vec, s) : ln_bwd<float, 2>(p, sh, vec, s);
-        return sh.epl == 16 ? ln_bwd<uint16_t, 2>(p, sh, vec, s) : ln_bwd<uint16_t, 1>(p, sh, vec, s);
-    });
+    return f32 ? ln_fwd_r<float, 4>(p, vec, s) : ln_fwd_r<uint16_t, 2>(p, vec, s);
 }
 
 }  // namespace mbx

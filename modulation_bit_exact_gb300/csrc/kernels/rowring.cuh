@@ -1,0 +1,254 @@
+// rowring.cuh -- rows streamed through shared memory for the LayerNorm kernels.
+//
+// A row group of `tpr` threads (8, 16 or 32 lanes of a warp, or whole warps)
+// works on R rows at a time; thread t owns E = NCH*CE columns of every row.
+// Rows arrive by cp.async in a ring of stages: each thread copies exactly the
+// pieces that it reads, so its own cp.async.wait_group is the only
+// synchronisation, and later rows are in flight while a row is reduced.
+//
+// kVec: chunk j of thread t is columns (j*tpr + t)*CE ..., moved in 16-byte
+// pieces.  kScalar (a width that is no multiple of CE, or a row that starts at
+// no 16-byte boundary): element e is column e*tpr + t, moved one at a time
+// (binary32 by 4-byte cp.async; bfloat16, which cp.async does not move alone,
+// by a load and a shared store).
+#pragma once
+
+#include "rowgroup.cuh"
+
+namespace mbx {
+
+__device__ __forceinline__ void ring_cp16(void* dst, const void* src) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+}
+__device__ __forceinline__ void ring_cp4(void* dst, const void* src) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
+}
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest stages-2 groups have landed (stages <= 4).
+__device__ __forceinline__ void ring_wait(int stages) {
+    if (stages <= 2) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (stages == 3) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 2;" ::: "memory");
+}
+
+// Round `round`'s stage is ready and the next free stage is on its way; one
+// stage (the largest rows) is filled and awaited in turn.
+template <class Fill>
+__device__ __forceinline__ void ring_turn(int stages, int64_t round, Fill& fill) {
+    if (stages == 1) fill(round);
+    ring_wait(stages);
+    if (stages > 1) fill(round + stages - 1);
+}
+
+// This thread's place in its row group and the columns that it owns.
+struct Lane {
+    int t, tpr;
+    int nv;  // kVec: chunks that exist; kScalar: elements that exist
+};
+template <int CE, Access A>
+__device__ __forceinline__ Lane make_lane(int t, int tpr, int D) {
+    const int units = A == kVec ? D / CE : D;
+    return Lane{t, tpr, units > t ? (units - t + tpr - 1) / tpr : 0};
+}
+
+template <class Q, int NCH, int CE>
+constexpr int kRowBytesPerThread = NCH * CE * (int)sizeof(Q);
+
+// Start the copy of this thread's part of `row` to its place in a stage.
+template <class Q, int NCH, int CE, Access A>
+__device__ __forceinline__ void ring_fill(char* dst, const Q* row, const Lane& L) {
+    if constexpr (A == kVec) {
+        constexpr int P = CE * (int)sizeof(Q) / 16;  // 16-byte pieces of a chunk
+#pragma unroll
+        for (int j = 0; j < NCH; ++j)
+            if (j < L.nv) {
+#pragma unroll
+                for (int h = 0; h < P; ++h)
+                    ring_cp16(dst + ((j * P + h) * L.tpr + L.t) * 16, row + (int64_t)(j * L.tpr + L.t) * CE + h * (16 / sizeof(Q)));
+            }
+    } else {
+#pragma unroll
+        for (int e = 0; e < NCH * CE; ++e) {
+            const int c = e * L.tpr + L.t;
+            if (e < L.nv) {
+                if constexpr (sizeof(Q) == 4) ring_cp4(dst + c * 4, row + c);
+                else reinterpret_cast<Q*>(dst)[c] = ld_u16_rw(row + c);
+            }
+        }
+    }
+}
+
+// Chunk j of a staged row as CE/2 pairs; 0 where no column exists.
+template <class Q, int CE, Access A>
+__device__ __forceinline__ void ring_read(u64 (&p)[CE / 2], const char* src, int j, const Lane& L) {
+    if constexpr (A == kVec) {
+        if constexpr (sizeof(Q) == 2) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src + (j * L.tpr + L.t) * 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = widen2(w_of(v, i));
+        } else {
+#pragma unroll
+            for (int h = 0; h < CE / 4; ++h) {
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(src + ((j * (CE / 4) + h) * L.tpr + L.t) * 16);
+                p[2 * h] = v.x;
+                p[2 * h + 1] = v.y;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < CE; i += 2) {
+            float v[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int e = j * CE + i + h, c = e * L.tpr + L.t;
+                v[h] = 0.0f;
+                if (e < L.nv) {
+                    if constexpr (sizeof(Q) == 4) v[h] = reinterpret_cast<const float*>(src)[c];
+                    else v[h] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(src)[c] << 16);
+                }
+            }
+            p[i / 2] = f2(v[0], v[1]);
+        }
+    }
+}
+
+// Whether chunk j has anything to do (kScalar masks its elements instead).
+template <Access A>
+__device__ __forceinline__ bool has_chunk(int j, const Lane& L) {
+    return A == kVec ? j < L.nv : true;
+}
+// 0 in place of a pair's elements that are no columns.
+template <int CE, Access A>
+__device__ __forceinline__ u64 mask_pair(u64 v, int j, int i, const Lane& L) {
+    if constexpr (A == kVec) return v;
+    const int e = j * CE + 2 * i;
+    return f2(e < L.nv ? f2lo(v) : 0.0f, e + 1 < L.nv ? f2hi(v) : 0.0f);
+}
+
+// Chunk j to a row in memory, each element rounded once to Q.
+template <class Q, int CE, Access A>
+__device__ __forceinline__ void put_chunk(Q* row, const u64 (&p)[CE / 2], int j, const Lane& L) {
+    if constexpr (A == kVec) {
+        Q* d = row + (int64_t)(j * L.tpr + L.t) * CE;
+        if constexpr (sizeof(Q) == 2) {
+            st_v4(d, make_uint4(pack2_rn(p[0]), pack2_rn(p[1]), pack2_rn(p[2]), pack2_rn(p[3])));
+        } else {
+#pragma unroll
+            for (int h = 0; h < CE / 4; ++h)
+                st_v4(d + 4 * h, make_uint4((uint32_t)p[2 * h], (uint32_t)(p[2 * h] >> 32), (uint32_t)p[2 * h + 1],
+                                            (uint32_t)(p[2 * h + 1] >> 32)));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < CE; ++i) {
+            const int e = j * CE + i;
+            if (e < L.nv) store_elem(row + e * L.tpr + L.t, i % 2 ? f2hi(p[i / 2]) : f2lo(p[i / 2]));
+        }
+    }
+}
+// The same for a parameter's row, bfloat16 or binary32 whatever the rows are.
+template <class T, int CE, Access A>
+__device__ __forceinline__ void put_param_chunk(void* p, int64_t off, bool p_f32, const u64 (&v)[CE / 2], int j,
+                                                const Lane& L) {
+    if constexpr (sizeof(T) == 4) put_chunk<float, CE, A>(static_cast<float*>(p) + off, v, j, L);
+    else if (p_f32) put_chunk<float, CE, A>(static_cast<float*>(p) + off, v, j, L);
+    else put_chunk<uint16_t, CE, A>(static_cast<uint16_t*>(p) + off, v, j, L);
+}
+
+// Chunk j of a row in memory, 0 where no column exists.  RW: the kernel may
+// write that row (an exact in-place update), so it is read with coherent loads.
+template <class Q, int CE, Access A, bool RW = false>
+__device__ __forceinline__ void get_chunk(u64 (&p)[CE / 2], const Q* row, int j, const Lane& L) {
+    if constexpr (A == kVec) {
+#pragma unroll
+        for (int i = 0; i < CE / 2; ++i) p[i] = 0;
+        if (j < L.nv) {
+            const Q* s = row + (int64_t)(j * L.tpr + L.t) * CE;
+            if constexpr (sizeof(Q) == 2) {
+                const uint4 v = RW ? ld_stream_rw(s) : ld_shared_row(s);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p[i] = widen2(w_of(v, i));
+            } else {
+#pragma unroll
+                for (int h = 0; h < CE / 4; ++h) {
+                    const uint4 v = RW ? ld_stream_rw(s + 4 * h) : ld_shared_row(s + 4 * h);
+                    p[2 * h] = f2(__uint_as_float(v.x), __uint_as_float(v.y));
+                    p[2 * h + 1] = f2(__uint_as_float(v.z), __uint_as_float(v.w));
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < CE; i += 2) {
+            const int e = j * CE + i;
+            p[i / 2] = f2(e < L.nv ? load_elem(row + e * L.tpr + L.t) : 0.0f,
+                          e + 1 < L.nv ? load_elem(row + (e + 1) * L.tpr + L.t) : 0.0f);
+        }
+    }
+}
+template <class T, int CE, Access A>
+__device__ __forceinline__ void get_param_chunk(u64 (&v)[CE / 2], const void* p, int64_t off, bool p_f32, int j,
+                                                const Lane& L) {
+    if constexpr (sizeof(T) == 4) get_chunk<float, CE, A>(v, static_cast<const float*>(p) + off, j, L);
+    else if (p_f32) get_chunk<float, CE, A>(v, static_cast<const float*>(p) + off, j, L);
+    else get_chunk<uint16_t, CE, A>(v, static_cast<const uint16_t*>(p) + off, j, L);
+}
+
+// Sums of V values (a power of two, at most 8) over a row group, in every
+// thread.  Inside a warp the first log2(V) shuffle steps halve the number of
+// values that a lane carries, so that V sums take about V + log2(lanes)
+// shuffles instead of V*log2(lanes); then the warps' sums meet in shared
+// memory, one barrier, and every warp adds them in the same order.  The
+// published sums alternate between two buffers: a buffer is written again two
+// calls later, after the barrier of the call in between, which every reader
+// has passed.
+struct GroupSums {
+    float* buf;  // [2][8][kMaxWarpsPerRow] of this group, zeroed
+    int t, tpr, bar_id, par;
+    template <int V>
+    __device__ __forceinline__ void operator()(float (&v)[V]) {
+        const int lanes = tpr < 32 ? tpr : 32;
+        const int lane = t & (lanes - 1);
+        int s = lanes / 2;
+        float c[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) c[k] = v[k];
+#pragma unroll
+        for (int n = V / 2; n >= 1; n /= 2) {
+            const bool hi = lane & s;
+#pragma unroll
+            for (int k = 0; k < n; ++k) {
+                const float give = hi ? c[k] : c[k + n], keep = hi ? c[k + n] : c[k];
+                c[k] = keep + __shfl_xor_sync(0xffffffffu, give, s);
+            }
+            s /= 2;
+        }
+        float a = c[0];  // the sum of value `mine` over the lanes that share the bits not yet summed
+        for (; s >= 1; s /= 2) a += __shfl_xor_sync(0xffffffffu, a, s);
+        const int per = lanes / V, mine = lane / per;
+        if (tpr > 32) {
+            float* slot = buf + par * 8 * kMaxWarpsPerRow;
+            par ^= 1;
+            if (lane % per == 0) slot[mine * kMaxWarpsPerRow + t / 32] = a;
+            named_bar(bar_id, tpr);
+            constexpr int W = kMaxWarpsPerRow * V / 32;  // warps' sums that a lane adds
+            a = 0.0f;
+            const float* q = slot + mine * kMaxWarpsPerRow + (lane % (32 / V)) * W;
+            if constexpr (W == 0) {
+                if (lane % (32 / V) < kMaxWarpsPerRow) a = slot[mine * kMaxWarpsPerRow + lane % (32 / V)];
+            } else {
+#pragma unroll
+                for (int w = 0; w < W; ++w) a += q[w];
+            }
+#pragma unroll
+            for (int x = 16 / V; x >= 1; x /= 2) a += __shfl_xor_sync(0xffffffffu, a, x);
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[k] = __shfl_sync(0xffffffffu, a, k * per, lanes);
+    }
+};
+constexpr int kSumFloats = 2 * 8 * kMaxWarpsPerRow;  // of one group
+
+}  // namespace mbx

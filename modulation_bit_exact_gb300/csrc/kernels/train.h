@@ -4,28 +4,45 @@
 // rotary positions on several axes.  Not installed; not part of the ABI.
 #pragma once
 
+#include <atomic>
+
 #include "launch.h"
 
 namespace mbx {
 
 int sm_count();  // SMs of the current device; 0 if the runtime cannot tell
 
-// How a row is spread over threads: `tpr` threads (whole warps) own one row
-// and each holds `epl` of its elements; a block is `groups` such row groups.
-struct RowShape {
-    int tpr, epl, groups;
-    int block() const { return tpr * groups; }
+// Threads that own one row of D elements, 16 elements each: 8 or 16 lanes of a
+// warp for the short rows, else whole warps.
+inline int row_threads(int D) { return D <= 128 ? 8 : D <= 256 ? 16 : (D + 511) / 512 * 32; }
+
+// The row kernels hold two to five rows in registers and accumulators at up to
+// 96 registers a thread, so 640 threads fit on an SM.
+constexpr int kRingThreads = 640;
+
+// How a kernel that streams rows through shared memory fills an SM: blocks of
+// `groups` row groups, `ctas_per_sm` blocks, and for every group a ring of
+// `stages` stages of `rows` rows of row_bytes (and extra_bytes).
+struct RingShape {
+    int tpr, groups, stages, ctas_per_sm;
+    int row_bytes, extra_bytes, sums_bytes, group_bytes, smem;
 };
-RowShape row_shape(int D, int esize);
+RingShape ring_shape(int tpr, int row_bytes, int rows, int extra_bytes);  // stages < 1: does not fit
+
+// Raises a kernel's shared-memory limit once for each device.
+struct SmemOptIn {
+    std::atomic<int> allowed[64] = {};
+    cudaError_t allow(const void* kernel, const RingShape& sh);
+};
 
 // How the rows of each modulation row (a segment of `seq` rows) are split for
 // the parameter gradients: `parts` parts of `rows_per_part` rows, one block a
 // part, whose partial sums a second kernel joins; one part needs neither.
 struct GradPlan {
     int64_t parts, rows_per_part;
-    int groups;
 };
-GradPlan grad_plan(int64_t rows, int64_t mod_rows, const RowShape& sh);
+RingShape grad_shape(int D, int esize, int rows);
+GradPlan grad_plan(int64_t rows, int64_t mod_rows, int D, int esize);
 int64_t grad_workspace_bytes(int64_t rows, int64_t mod_rows, int D, int esize);
 
 struct LnFwdParams {
@@ -64,9 +81,7 @@ struct LnBwdParams {
     int D;
     float eps;
     float* ws;
-    // filled by the launcher
-    GradPlan plan;
-    int tpr;
+    GradPlan plan;  // filled by the launcher
 };
 
 struct DropParams {
@@ -90,7 +105,7 @@ struct DropParams {
     float* ws;
     // filled by the launcher
     GradPlan plan;
-    int tpr;
+    int tpr, groups;
 };
 
 // out[k][s][c] = sum over the parts of ws[s][part][k][c], k < nacc.
