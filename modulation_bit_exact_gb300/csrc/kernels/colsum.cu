@@ -5,7 +5,7 @@
 
 namespace mbx {
 
-RingShape ring_shape(int tpr, int row_bytes, int rows, int extra_bytes) {
+RingShape ring_shape(int tpr, int row_bytes, int rows, int extra_bytes, int fixed_per_thread) {
     RingShape s;
     s.tpr = tpr;
     s.row_bytes = row_bytes;
@@ -13,16 +13,17 @@ RingShape ring_shape(int tpr, int row_bytes, int rows, int extra_bytes) {
     s.groups = tpr >= 320 ? 1 : 320 / tpr;
     while (s.groups * tpr % 32) --s.groups;  // whole warps
     s.sums_bytes = tpr > 32 ? s.groups * 2 * 8 * 16 * (int)sizeof(float) : 0;
+    s.fixed_bytes = fixed_per_thread * s.groups * tpr;
     const int stage = (rows * row_bytes + extra_bytes) * s.groups;
     // as many blocks as the threads allow, if two stages fit for each
     for (s.ctas_per_sm = kRingThreads / (s.groups * tpr);; --s.ctas_per_sm) {
-        const int room = 228 * 1024 / s.ctas_per_sm - 1024 - s.sums_bytes;  // 1 KB of each block's is the system's
+        const int room = 228 * 1024 / s.ctas_per_sm - 1024 - s.sums_bytes - s.fixed_bytes;  // 1 KB of each block's is the system's
         s.stages = room / stage;
         if (s.stages >= 2 || s.ctas_per_sm == 1) break;
     }
     if (s.stages > 4) s.stages = 4;
     s.group_bytes = s.stages * (rows * row_bytes + extra_bytes);
-    s.smem = s.sums_bytes + s.groups * s.group_bytes;
+    s.smem = s.sums_bytes + s.fixed_bytes + s.groups * s.group_bytes;
     return s;
 }
 
@@ -43,7 +44,7 @@ cudaError_t SmemOptIn::allow(const void* kernel, const RingShape& sh) {
 
 RingShape grad_shape(int D, int esize, int rows) {
     const int tpr = row_threads(D);
-    return ring_shape(tpr, 16 * esize * tpr, rows, 0);
+    return ring_shape(tpr, 16 * esize * tpr, rows, 0, 64);
 }
 
 GradPlan grad_plan(int64_t rows, int64_t mod_rows, int D, int esize) {

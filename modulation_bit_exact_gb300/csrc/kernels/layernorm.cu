@@ -23,67 +23,60 @@ namespace mbx {
 // R rows of a group at a time: their sums share the shuffles and the barrier.
 template <class T, int NCH, Access A, int R>
 __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p, RingShape sh) {
-    constexpr int CE = ChunkOf<T>::CE, E = NCH * CE;
+    constexpr int CE = ChunkOf<T>::CE, P = NCH * CE / 2;
     extern __shared__ __align__(16) char smem[];
     const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr;
     const Lane L = make_lane<CE, A>(t, tpr, p.D);
     GroupSums sums = group_sums(smem, sh, g, t);
-    char* ring = smem + sh.sums_bytes + g * sh.group_bytes;
+    char* ring = smem + sh.sums_bytes + sh.fixed_bytes + g * sh.group_bytes;
     const float inv_d = 1.0f / (float)p.D;
     grid_dep_wait();  // launched programmatically: the previous kernel has finished
     grid_dep_launch();
 
-    u64 w[E / 2], b[E / 2];
+    u64 w[P], b[P];
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
         u64 c[CE / 2];
 #pragma unroll
         for (int i = 0; i < CE / 2; ++i) c[i] = f2(1.0f, 1.0f);
-        if (p.weight) get_param_chunk<T, CE, A>(c, p.weight, 0, p.p_f32, j, L);
+        if (p.weight) get_param_chunk<T, CE, A>(c, p.weight, first_col<CE, A>(L), p.p_f32, j, L);
 #pragma unroll
         for (int i = 0; i < CE / 2; ++i) w[j * (CE / 2) + i] = c[i], c[i] = 0;
-        if (p.bias) get_param_chunk<T, CE, A>(c, p.bias, 0, p.p_f32, j, L);
+        if (p.bias) get_param_chunk<T, CE, A>(c, p.bias, first_col<CE, A>(L), p.p_f32, j, L);
 #pragma unroll
         for (int i = 0; i < CE / 2; ++i) b[j * (CE / 2) + i] = c[i];
     }
 
-    const T* x = static_cast<const T*>(p.x);
-    T* out = static_cast<T*>(p.out);
-    const int row_bytes = sh.row_bytes, stage_bytes = R * row_bytes;
+    const int row_bytes = sh.row_bytes, stage_bytes = R * row_bytes, c0 = first_col<CE, A>(L);
     // batches of R consecutive rows, dealt to the groups of the whole grid
-    const int64_t per_round = (int64_t)gridDim.x * sh.groups;
-    const int64_t first = (int64_t)blockIdx.x * sh.groups + g;
-    const int64_t rounds = ((p.rows + R - 1) / R + per_round - 1) / per_round;  // the same for every group
+    const int64_t step = (int64_t)gridDim.x * sh.groups * R;
+    const int64_t rounds = (p.rows + step - 1) / step;  // the same for every group
+    int64_t r = ((int64_t)blockIdx.x * sh.groups + g) * R, fill_row = r;
     int fill_stage = 0;
-    auto fill = [&](int64_t round) {
-        const int64_t r0 = (first + round * per_round) * R;
+    auto fill = [&](int64_t) {
         char* dst = ring + fill_stage * stage_bytes;
         if (++fill_stage == sh.stages) fill_stage = 0;
 #pragma unroll
         for (int k = 0; k < R; ++k)
-            if (r0 + k < p.rows) ring_fill<T, NCH, CE, A>(dst + k * row_bytes, x + (r0 + k) * p.x_stride, L);
+            if (fill_row + k < p.rows)
+                ring_fill<T, NCH, CE, A>(dst + k * row_bytes, static_cast<const T*>(p.x) + (fill_row + k) * p.x_stride + c0, L);
+        fill_row += step;
         ring_commit();
     };
     for (int i = 0; i < sh.stages - 1; ++i) fill(i);
     int stage = 0;
-    for (int64_t round = 0; round < rounds; ++round) {
+    for (int64_t round = 0; round < rounds; ++round, r += step) {
         ring_turn(sh.stages, round, fill);
         const char* src = ring + stage * stage_bytes;
         if (++stage == sh.stages) stage = 0;
-        const int64_t r0 = (first + round * per_round) * R;
-
+        u64 v[R][P];
         float mean[R], rstd[R];
 #pragma unroll
         for (int k = 0; k < R; ++k) {
+            read_row<T, NCH, CE, A>(v[k], src + k * row_bytes, L);
             u64 s = 0;
 #pragma unroll
-            for (int j = 0; j < NCH; ++j) {
-                if (!has_chunk<A>(j, L)) continue;
-                u64 v[CE / 2];
-                ring_read<T, CE, A>(v, src + k * row_bytes, j, L);
-#pragma unroll
-                for (int i = 0; i < CE / 2; ++i) s = add2(s, v[i]);
-            }
+            for (int e = 0; e < P; ++e) s = add2(s, v[k][e]);
             mean[k] = f2lo(s) + f2hi(s);
         }
         sums(mean);
@@ -94,12 +87,11 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
             u64 q = 0;
 #pragma unroll
             for (int j = 0; j < NCH; ++j) {
-                if (!has_chunk<A>(j, L)) continue;
-                u64 v[CE / 2];
-                ring_read<T, CE, A>(v, src + k * row_bytes, j, L);
+                if (!has_chunk<A>(j, L)) continue;  // its elements are 0 and count for nothing
 #pragma unroll
                 for (int i = 0; i < CE / 2; ++i) {
-                    const u64 c = mask_pair<CE, A>(sub2(v[i], m), j, i, L);
+                    u64& c = v[k][j * (CE / 2) + i];
+                    c = mask_pair<CE, A>(sub2(c, m), j, i, L);
                     q = fma2(c, c, q);
                 }
             }
@@ -108,19 +100,20 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
         sums(rstd);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            rstd[k] = 1.0f / sqrtf(rstd[k] * inv_d + p.eps);
-            const u64 m = f2(mean[k], mean[k]), rs = f2(rstd[k], rstd[k]);
-            if (r0 + k >= p.rows) continue;
-            T* dst = out + (r0 + k) * p.out_stride;
+            if (r + k >= p.rows) continue;
+            const float rs1 = rsqrtf(rstd[k] * inv_d + p.eps);
+            const u64 rs = f2(rs1, rs1);
+            T* dst = static_cast<T*>(p.out) + (r + k) * p.out_stride + c0;
 #pragma unroll
             for (int j = 0; j < NCH; ++j) {
                 if (!has_chunk<A>(j, L)) continue;
-                u64 v[CE / 2];
-                ring_read<T, CE, A>(v, src + k * row_bytes, j, L);
+                u64 c[CE / 2];
 #pragma unroll
-                for (int i = 0; i < CE / 2; ++i)
-                    v[i] = fma2(mul2(sub2(v[i], m), rs), w[j * (CE / 2) + i], b[j * (CE / 2) + i]);
-                put_chunk<T, CE, A>(dst, v, j, L);
+                for (int i = 0; i < CE / 2; ++i) {
+                    const int e = j * (CE / 2) + i;
+                    c[i] = fma2(mul2(v[k][e], rs), w[e], b[e]);
+                }
+                put_chunk<T, CE, A>(dst, c, j, L);
             }
         }
     }
@@ -129,7 +122,7 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
 template <class T, int NCH, Access A, int R>
 static cudaError_t ln_fwd(const LnFwdParams& p, int tpr, cudaStream_t s) {
     auto k = layer_norm_kernel<T, NCH, A, R>;
-    const RingShape sh = ring_shape(tpr, kRowBytesPerThread<T, NCH, ChunkOf<T>::CE> * tpr, R, 0);
+    const RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, R, 0, 0);
     static SmemOptIn opt_in;
     if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
     const int64_t batches = (p.rows + R - 1) / R, need = (batches + sh.groups - 1) / sh.groups;

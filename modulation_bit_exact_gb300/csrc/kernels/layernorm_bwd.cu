@@ -15,254 +15,238 @@
 
 namespace mbx {
 
-// The two row sums of R staged rows: mean, rstd, and the two coefficients of
+// One row in registers: x and dy as pairs.  gy(e) gives pair e of dy * f.  On
+// return x holds xh and the result the coefficients of
 //   dx = rstd*gy + k1 + xh*k2,   k1 = -rstd*c1, k2 = -rstd*c2.
-// factor(k, j, f) gives chunk j of row k's factor.
-template <class T, int NCH, Access A, int R, class Factor>
-__device__ __forceinline__ void ln_row_sums(float (&mean)[R], float (&rstd)[R], float (&k1)[R], float (&k2)[R],
-                                            const char* sx, const char* sdy, int row_bytes, const Lane& L,
-                                            const LnBwdParams& p, float inv_d, GroupSums& sums, Factor factor) {
-    constexpr int CE = ChunkOf<T>::CE;
-    float v[2 * R];
+struct RowCoef {
+    float rstd, k1, k2;
+};
+template <int NCH, int CE, Access A, class Gy>
+__device__ __forceinline__ RowCoef ln_row_stats(u64 (&x)[NCH * CE / 2], const Lane& L, float inv_d, float eps,
+                                                GroupSums& sums, Gy gy) {
+    constexpr int H = CE / 2;
+    u64 s = 0, sg = 0;
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-        u64 s = 0, sg = 0;
-#pragma unroll
-        for (int j = 0; j < NCH; ++j) {
-            if (!has_chunk<A>(j, L)) continue;
-            u64 x[CE / 2], dy[CE / 2], f[CE / 2];
-            ring_read<T, CE, A>(x, sx + k * row_bytes, j, L);
-            ring_read<T, CE, A>(dy, sdy + k * row_bytes, j, L);
-            factor(k, j, f);
-#pragma unroll
-            for (int i = 0; i < CE / 2; ++i) {
-                s = add2(s, x[i]);
-                sg = fma2(dy[i], f[i], sg);
-            }
-        }
-        v[2 * k] = f2lo(s) + f2hi(s);
-        v[2 * k + 1] = f2lo(sg) + f2hi(sg);
+    for (int e = 0; e < NCH * H; ++e) {
+        s = add2(s, x[e]);
+        sg = add2(sg, gy(e));
     }
+    float v[2] = {f2lo(s) + f2hi(s), f2lo(sg) + f2hi(sg)};
     sums(v);
+    const float mean = v[0] * inv_d, c1 = v[1] * inv_d;
+    const u64 m = f2(mean, mean);
+    u64 q = 0, qg = 0;
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-        mean[k] = v[2 * k] * inv_d;
-        k1[k] = v[2 * k + 1] * inv_d;
-        const u64 m = f2(mean[k], mean[k]);
-        u64 q = 0, qg = 0;
+    for (int j = 0; j < NCH; ++j) {
+        if (!has_chunk<A>(j, L)) continue;  // its x and dy are 0 and count for nothing
 #pragma unroll
-        for (int j = 0; j < NCH; ++j) {
-            if (!has_chunk<A>(j, L)) continue;
-            u64 x[CE / 2], dy[CE / 2], f[CE / 2];
-            ring_read<T, CE, A>(x, sx + k * row_bytes, j, L);
-            ring_read<T, CE, A>(dy, sdy + k * row_bytes, j, L);
-            factor(k, j, f);
-#pragma unroll
-            for (int i = 0; i < CE / 2; ++i) {
-                const u64 c = mask_pair<CE, A>(sub2(x[i], m), j, i, L);
-                q = fma2(c, c, q);
-                qg = fma2(mul2(dy[i], f[i]), c, qg);
-            }
+        for (int i = 0; i < H; ++i) {
+            const int e = j * H + i;
+            x[e] = mask_pair<CE, A>(sub2(x[e], m), j, i, L);
+            q = fma2(x[e], x[e], q);
+            qg = fma2(gy(e), x[e], qg);
         }
-        v[2 * k] = f2lo(q) + f2hi(q);
-        v[2 * k + 1] = f2lo(qg) + f2hi(qg);
     }
+    v[0] = f2lo(q) + f2hi(q);
+    v[1] = f2lo(qg) + f2hi(qg);
     sums(v);
+    const float rstd = rsqrtf(v[0] * inv_d + eps);
+    const u64 rs = f2(rstd, rstd);
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-        rstd[k] = 1.0f / sqrtf(v[2 * k] * inv_d + p.eps);
-        k1[k] *= -rstd[k];
-        k2[k] = -rstd[k] * (v[2 * k + 1] * inv_d * rstd[k]);
-    }
+    for (int e = 0; e < NCH * H; ++e) x[e] = mul2(x[e], rs);
+    return RowCoef{rstd, -rstd * c1, -rstd * (v[1] * inv_d * rstd)};
 }
 
 // One modulation row for every row: nothing is summed, every output is a row,
 // and the factor's row streams with x and dy.
 template <class T, int NCH, Access A, bool RES>
 __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdParams p, RingShape sh) {
-    constexpr int CE = ChunkOf<T>::CE;
+    constexpr int CE = ChunkOf<T>::CE, H = CE / 2;
+    constexpr int kF = RES ? 3 : 2;  // a stage: x, dy, the residual's gradient, the factor
     extern __shared__ __align__(16) char smem[];
     const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr;
     const Lane L = make_lane<CE, A>(t, tpr, p.D);
     GroupSums sums = group_sums(smem, sh, g, t);
-    char* ring = smem + sh.sums_bytes + g * sh.group_bytes;
+    char* ring = smem + sh.sums_bytes + sh.fixed_bytes + g * sh.group_bytes;
     const float inv_d = 1.0f / (float)p.D;
     grid_dep_wait();
     grid_dep_launch();
-    const T* px = static_cast<const T*>(p.x);
-    const T* pd = static_cast<const T*>(p.dout);
-    const int row_bytes = sh.row_bytes, stage_bytes = (RES ? 3 : 2) * row_bytes + sh.extra_bytes;
-    constexpr int kF = RES ? 3 : 2;  // the factor's row comes last
-    const int64_t per_round = (int64_t)gridDim.x * sh.groups, first = (int64_t)blockIdx.x * sh.groups + g;
-    const int64_t rounds = (p.rows + per_round - 1) / per_round;
+    const int row_bytes = sh.row_bytes, stage_bytes = kF * row_bytes + sh.extra_bytes;
+    const int64_t step = (int64_t)gridDim.x * sh.groups, first = (int64_t)blockIdx.x * sh.groups + g;
+    const int64_t rounds = (p.rows + step - 1) / step;  // the same for every group
+    const int c0 = first_col<CE, A>(L);
     const u64 one = f2(p.factor_add, p.factor_add);
+    int64_t fill_row = first;
     int fill_stage = 0;
-    auto fill = [&](int64_t round) {
-        const int64_t r = first + round * per_round;
+    auto fill = [&](int64_t) {
         char* dst = ring + fill_stage * stage_bytes;
         if (++fill_stage == sh.stages) fill_stage = 0;
-        if (r < p.rows) {
-            ring_fill<T, NCH, CE, A>(dst, px + r * p.x_stride, L);
-            ring_fill<T, NCH, CE, A>(dst + row_bytes, pd + r * p.dout_stride, L);
+        if (fill_row < p.rows) {
+            ring_fill<T, NCH, CE, A>(dst, static_cast<const T*>(p.x) + fill_row * p.x_stride + c0, L);
+            ring_fill<T, NCH, CE, A>(dst + row_bytes, static_cast<const T*>(p.dout) + fill_row * p.dout_stride + c0, L);
             if constexpr (RES)
-                ring_fill<T, NCH, CE, A>(dst + 2 * row_bytes, static_cast<const T*>(p.dres) + r * p.dres_stride, L);
+                ring_fill<T, NCH, CE, A>(dst + 2 * row_bytes, static_cast<const T*>(p.dres) + fill_row * p.dres_stride + c0, L);
+            const int64_t f0 = fill_row * p.factor_stride + c0;
             if (sizeof(T) == 4 || p.p_f32)
-                ring_fill<float, NCH, CE, A>(dst + kF * row_bytes, static_cast<const float*>(p.factor) + r * p.factor_stride, L);
-            else
-                ring_fill<uint16_t, NCH, CE, A>(dst + kF * row_bytes, static_cast<const uint16_t*>(p.factor) + r * p.factor_stride, L);
+                ring_fill<float, NCH, CE, A>(dst + kF * row_bytes, static_cast<const float*>(p.factor) + f0, L);
+            else ring_fill<uint16_t, NCH, CE, A>(dst + kF * row_bytes, static_cast<const uint16_t*>(p.factor) + f0, L);
         }
+        fill_row += step;
         ring_commit();
     };
     for (int i = 0; i < sh.stages - 1; ++i) fill(i);
     int stage = 0;
-    for (int64_t round = 0; round < rounds; ++round) {
+    int64_t r = first;
+    for (int64_t round = 0; round < rounds; ++round, r += step) {
         ring_turn(sh.stages, round, fill);
         const char* src = ring + stage * stage_bytes;
         if (++stage == sh.stages) stage = 0;
-        const int64_t r = first + round * per_round;
-        auto factor = [&](int, int j, u64 (&f)[CE / 2]) {
-            if (sizeof(T) == 4 || p.p_f32) ring_read<float, CE, A>(f, src + kF * row_bytes, j, L);
-            else ring_read<uint16_t, CE, A>(f, src + kF * row_bytes, j, L);
+        u64 x[NCH * H], dy[NCH * H], gy[NCH * H];
+        read_row<T, NCH, CE, A>(x, src, L);
+        read_row<T, NCH, CE, A>(dy, src + row_bytes, L);
+        if (sizeof(T) == 4 || p.p_f32) read_row<float, NCH, CE, A>(gy, src + kF * row_bytes, L);
+        else read_row<uint16_t, NCH, CE, A>(gy, src + kF * row_bytes, L);
 #pragma unroll
-            for (int i = 0; i < CE / 2; ++i) f[i] = add2(f[i], one);
-        };
-        float mean[1], rstd[1], k1[1], k2[1];
-        ln_row_sums<T, NCH, A, 1>(mean, rstd, k1, k2, src, src + row_bytes, row_bytes, L, p, inv_d, sums, factor);
+        for (int e = 0; e < NCH * H; ++e) gy[e] = mul2(dy[e], add2(gy[e], one));
+        const RowCoef k = ln_row_stats<NCH, CE, A>(x, L, inv_d, p.eps, sums, [&](int e) { return gy[e]; });
         if (r >= p.rows) continue;
-        const u64 m = f2(mean[0], mean[0]), rs = f2(rstd[0], rstd[0]), a = f2(k1[0], k1[0]), b = f2(k2[0], k2[0]);
+        const u64 rs = f2(k.rstd, k.rstd), a = f2(k.k1, k.k1), b = f2(k.k2, k.k2);
+        T* dx_row = static_cast<T*>(p.dx) + r * p.dx_stride + c0;
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
             if (!has_chunk<A>(j, L)) continue;
-            u64 x[CE / 2], dy[CE / 2], f[CE / 2], res[CE / 2];
+            u64 dx[H], xd[H], d[H], res[H];
             if constexpr (RES) ring_read<T, CE, A>(res, src + 2 * row_bytes, j, L);
-            ring_read<T, CE, A>(x, src, j, L);
-            ring_read<T, CE, A>(dy, src + row_bytes, j, L);
-            factor(0, j, f);
 #pragma unroll
-            for (int i = 0; i < CE / 2; ++i) {
-                x[i] = mul2(sub2(x[i], m), rs);
-                f[i] = fma2(x[i], b, fma2(mul2(dy[i], f[i]), rs, a));
-                if constexpr (RES) f[i] = add2(f[i], res[i]);
-                x[i] = mul2(x[i], dy[i]);
+            for (int i = 0; i < H; ++i) {
+                const int e = j * H + i;
+                dx[i] = fma2(x[e], b, fma2(gy[e], rs, a));
+                if constexpr (RES) dx[i] = add2(dx[i], res[i]);
+                xd[i] = mul2(x[e], dy[e]);
+                d[i] = dy[e];
             }
-            put_chunk<T, CE, A>(static_cast<T*>(p.dx) + r * p.dx_stride, f, j, L);
-            if (p.dfactor) put_param_chunk<T, CE, A>(p.dfactor, r * p.dfactor_stride, p.p_f32, x, j, L);
-            if (p.dshift) put_param_chunk<T, CE, A>(p.dshift, r * p.dshift_stride, p.p_f32, dy, j, L);
+            put_chunk<T, CE, A>(dx_row, dx, j, L);
+            if (p.dfactor) put_param_chunk<T, CE, A>(p.dfactor, r * p.dfactor_stride + c0, p.p_f32, xd, j, L);
+            if (p.dshift) put_param_chunk<T, CE, A>(p.dshift, r * p.dshift_stride + c0, p.p_f32, d, j, L);
         }
     }
 }
 
 // Modulation rows shared by seq rows: a block takes one part of a segment, its
-// row groups batches of R rows of the part in turn; every thread sums its own
-// columns in binary32 registers, the groups are added in shared memory, and
-// the part's sums go to the workspace (or out, when the segment is one part).
-template <class T, int NCH, Access A, int R, bool RES>
+// row groups the rows of the part in turn; every thread sums its own columns
+// in binary32 registers, the groups are added in shared memory, and the part's
+// sums go to the workspace (or out, when the segment is one part).
+template <class T, int NCH, Access A, bool RES>
 __global__ void __launch_bounds__(kRingThreads) ln_backward_kernel(LnBwdParams p, RingShape sh) {
-    constexpr int CE = ChunkOf<T>::CE, E = NCH * CE;
+    constexpr int CE = ChunkOf<T>::CE, H = CE / 2, P = NCH * H;
     extern __shared__ __align__(16) char smem[];
     const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr, groups = sh.groups;
     const Lane L = make_lane<CE, A>(t, tpr, p.D);
     GroupSums sums = group_sums(smem, sh, g, t);
-    char* ring = smem + sh.sums_bytes + g * sh.group_bytes;
+    // the factor lives in shared memory, each thread's own copy, so that x, dy
+    // and the two sums of every column fit in registers
+    ulonglong2* fs = reinterpret_cast<ulonglong2*>(smem + sh.sums_bytes) + threadIdx.x;  // [P/2][block]
+    char* ring = smem + sh.sums_bytes + sh.fixed_bytes + g * sh.group_bytes;
+    const int block = groups * tpr;
     const float inv_d = 1.0f / (float)p.D;
     grid_dep_wait();
     grid_dep_launch();
-    const T* px = static_cast<const T*>(p.x);
-    const T* pd = static_cast<const T*>(p.dout);
-    const int row_bytes = sh.row_bytes, stage_bytes = (RES ? 3 : 2) * R * row_bytes;
+    const int row_bytes = sh.row_bytes, stage_bytes = (RES ? 3 : 2) * row_bytes;
+    const int c0 = first_col<CE, A>(L);
     const int64_t units = p.mod_rows * p.plan.parts;
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
         const int64_t seg = unit / p.plan.parts, part = unit - seg * p.plan.parts;
         const int64_t r0 = seg * p.seq + part * p.plan.rows_per_part;
-        int64_t r1 = r0 + p.plan.rows_per_part;
-        if (r1 > (seg + 1) * p.seq) r1 = (seg + 1) * p.seq;
-        const int64_t per_round = (int64_t)groups * R, rounds = (r1 - r0 + per_round - 1) / per_round;
-        u64 f[E / 2], adf[E / 2], ads[E / 2];
+        const int64_t left = (seg + 1) * p.seq - r0;
+        const int n_rows = (int)(left < p.plan.rows_per_part ? left : p.plan.rows_per_part);
+        const int rounds = (n_rows + groups - 1) / groups;
+        u64 adf[P], ads[P];
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
-            u64 c[CE / 2];
+            u64 c[H];
 #pragma unroll
-            for (int i = 0; i < CE / 2; ++i) c[i] = f2(1.0f, 1.0f);
-            if (p.factor) get_param_chunk<T, CE, A>(c, p.factor, seg * p.factor_stride, p.p_f32, j, L);
+            for (int i = 0; i < H; ++i) c[i] = f2(1.0f, 1.0f);
+            if (p.factor) get_param_chunk<T, CE, A>(c, p.factor, seg * p.factor_stride + c0, p.p_f32, j, L);
 #pragma unroll
-            for (int i = 0; i < CE / 2; ++i) {
-                f[j * (CE / 2) + i] = add2(c[i], f2(p.factor_add, p.factor_add));
-                adf[j * (CE / 2) + i] = ads[j * (CE / 2) + i] = 0;
+            for (int i = 0; i < H; i += 2) {
+                const u64 one = f2(p.factor_add, p.factor_add);
+                fs[(j * H + i) / 2 * block] = make_ulonglong2(add2(c[i], one), add2(c[i + 1], one));
+                adf[j * H + i] = adf[j * H + i + 1] = ads[j * H + i] = ads[j * H + i + 1] = 0;
             }
         }
-        int fill_stage = 0;
-        auto fill = [&](int64_t round) {
-            const int64_t r = r0 + round * per_round + g * R;
+        auto factor = [&](int e) {
+            const ulonglong2 v = fs[e / 2 * block];
+            return e % 2 ? v.y : v.x;
+        };
+        const T* nx = static_cast<const T*>(p.x) + (r0 + g) * p.x_stride + c0;
+        const T* nd = static_cast<const T*>(p.dout) + (r0 + g) * p.dout_stride + c0;
+        const T* nr = RES ? static_cast<const T*>(p.dres) + (r0 + g) * p.dres_stride + c0 : nullptr;
+        T* dx_row = static_cast<T*>(p.dx) + (r0 + g) * p.dx_stride + c0;
+        int fill_row = g, fill_stage = 0;
+        auto fill = [&](int64_t) {
             char* dst = ring + fill_stage * stage_bytes;
             if (++fill_stage == sh.stages) fill_stage = 0;
-#pragma unroll
-            for (int k = 0; k < R; ++k)
-                if (r + k < r1) {
-                    ring_fill<T, NCH, CE, A>(dst + k * row_bytes, px + (r + k) * p.x_stride, L);
-                    ring_fill<T, NCH, CE, A>(dst + (R + k) * row_bytes, pd + (r + k) * p.dout_stride, L);
-                    if constexpr (RES)
-                        ring_fill<T, NCH, CE, A>(dst + (2 * R + k) * row_bytes,
-                                                 static_cast<const T*>(p.dres) + (r + k) * p.dres_stride, L);
-                }
+            if (fill_row < n_rows) {
+                ring_fill<T, NCH, CE, A>(dst, nx, L);
+                ring_fill<T, NCH, CE, A>(dst + row_bytes, nd, L);
+                if constexpr (RES) ring_fill<T, NCH, CE, A>(dst + 2 * row_bytes, nr, L);
+            }
+            fill_row += groups;
+            nx += groups * p.x_stride;
+            nd += groups * p.dout_stride;
+            if constexpr (RES) nr += groups * p.dres_stride;
             ring_commit();
-        };
-        auto factor = [&](int, int j, u64 (&c)[CE / 2]) {
-#pragma unroll
-            for (int i = 0; i < CE / 2; ++i) c[i] = f[j * (CE / 2) + i];
         };
         for (int i = 0; i < sh.stages - 1; ++i) fill(i);
         int stage = 0;
-        for (int64_t round = 0; round < rounds; ++round) {
+        for (int round = 0; round < rounds; ++round, dx_row += groups * p.dx_stride) {
             ring_turn(sh.stages, round, fill);
             const char* src = ring + stage * stage_bytes;
             if (++stage == sh.stages) stage = 0;
-            const int64_t r = r0 + round * per_round + g * R;
-            float mean[R], rstd[R], k1[R], k2[R];
-            ln_row_sums<T, NCH, A, R>(mean, rstd, k1, k2, src, src + R * row_bytes, row_bytes, L, p, inv_d, sums, factor);
+            u64 x[P], dy[P];
+            read_row<T, NCH, CE, A>(x, src, L);
+            read_row<T, NCH, CE, A>(dy, src + row_bytes, L);
+            const RowCoef k =
+                ln_row_stats<NCH, CE, A>(x, L, inv_d, p.eps, sums, [&](int e) { return mul2(dy[e], factor(e)); });
+            if (round * groups + g >= n_rows) continue;
+            const u64 rs = f2(k.rstd, k.rstd), a = f2(k.k1, k.k1), b = f2(k.k2, k.k2);
 #pragma unroll
-            for (int k = 0; k < R; ++k) {
-                if (r + k >= r1) continue;
-                const u64 m = f2(mean[k], mean[k]), rs = f2(rstd[k], rstd[k]), a = f2(k1[k], k1[k]), b = f2(k2[k], k2[k]);
+            for (int j = 0; j < NCH; ++j) {
+                if (!has_chunk<A>(j, L)) continue;
+                u64 dx[H], res[H];
+                if constexpr (RES) ring_read<T, CE, A>(res, src + 2 * row_bytes, j, L);
 #pragma unroll
-                for (int j = 0; j < NCH; ++j) {
-                    if (!has_chunk<A>(j, L)) continue;
-                    u64 x[CE / 2], dy[CE / 2], dx[CE / 2], res[CE / 2];
-                    if constexpr (RES) ring_read<T, CE, A>(res, src + (2 * R + k) * row_bytes, j, L);
-                    ring_read<T, CE, A>(x, src + k * row_bytes, j, L);
-                    ring_read<T, CE, A>(dy, src + (R + k) * row_bytes, j, L);
-#pragma unroll
-                    for (int i = 0; i < CE / 2; ++i) {
-                        const int e = j * (CE / 2) + i;
-                        const u64 xh = mask_pair<CE, A>(mul2(sub2(x[i], m), rs), j, i, L);
-                        dx[i] = fma2(xh, b, fma2(mul2(dy[i], f[e]), rs, a));
-                        if constexpr (RES) dx[i] = add2(dx[i], res[i]);
-                        adf[e] = fma2(xh, dy[i], adf[e]);
-                        ads[e] = add2(ads[e], dy[i]);
-                    }
-                    put_chunk<T, CE, A>(static_cast<T*>(p.dx) + (r + k) * p.dx_stride, dx, j, L);
+                for (int i = 0; i < H; ++i) {
+                    const int e = j * H + i;
+                    dx[i] = fma2(x[e], b, fma2(mul2(dy[e], factor(e)), rs, a));
+                    if constexpr (RES) dx[i] = add2(dx[i], res[i]);
+                    adf[e] = fma2(x[e], dy[e], adf[e]);
+                    ads[e] = add2(ads[e], dy[e]);
                 }
+                put_chunk<T, CE, A>(dx_row, dx, j, L);
             }
         }
         if (p.dfactor == nullptr && p.dshift == nullptr) continue;
         if (groups > 1) {
-            // every group's sums in shared memory (the ring is drained: every
-            // thread waited for its last rows), added in group order
-            u64* acc = reinterpret_cast<u64*>(smem + sh.sums_bytes);  // [E][block]
-            const int n = groups * tpr;
+            // every group's sums in shared memory, in the place of the ring
+            // (two stages of two rows at least, so it holds them; drained:
+            // every thread waited for its last rows), added in group order
+            u64* acc = reinterpret_cast<u64*>(smem + sh.sums_bytes + sh.fixed_bytes);  // [2P][block]
+            const int n = block;
             asm volatile("cp.async.wait_group 0;" ::: "memory");
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < E / 2; ++e) {
+            for (int e = 0; e < P; ++e) {
                 acc[e * n + threadIdx.x] = adf[e];
-                acc[(E / 2 + e) * n + threadIdx.x] = ads[e];
+                acc[(P + e) * n + threadIdx.x] = ads[e];
             }
             __syncthreads();
             if (g == 0) {
 #pragma unroll
-                for (int e = 0; e < E / 2; ++e)
+                for (int e = 0; e < P; ++e)
                     for (int k = 1; k < groups; ++k) {
                         adf[e] = add2(adf[e], acc[e * n + k * tpr + t]);
-                        ads[e] = add2(ads[e], acc[(E / 2 + e) * n + k * tpr + t]);
+                        ads[e] = add2(ads[e], acc[(P + e) * n + k * tpr + t]);
                     }
             }
             __syncthreads();
@@ -271,18 +255,18 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_kernel(LnBwdParams p
 #pragma unroll
             for (int j = 0; j < NCH; ++j) {
                 if (!has_chunk<A>(j, L)) continue;
-                u64 c[2][CE / 2];
+                u64 c[2][H];
 #pragma unroll
-                for (int i = 0; i < CE / 2; ++i) {
-                    c[0][i] = adf[j * (CE / 2) + i];
-                    c[1][i] = ads[j * (CE / 2) + i];
+                for (int i = 0; i < H; ++i) {
+                    c[0][i] = adf[j * H + i];
+                    c[1][i] = ads[j * H + i];
                 }
                 if (p.plan.parts == 1) {
-                    if (p.dfactor) put_param_chunk<T, CE, A>(p.dfactor, seg * p.dfactor_stride, p.p_f32, c[0], j, L);
-                    if (p.dshift) put_param_chunk<T, CE, A>(p.dshift, seg * p.dshift_stride, p.p_f32, c[1], j, L);
+                    if (p.dfactor) put_param_chunk<T, CE, A>(p.dfactor, seg * p.dfactor_stride + c0, p.p_f32, c[0], j, L);
+                    if (p.dshift) put_param_chunk<T, CE, A>(p.dshift, seg * p.dshift_stride + c0, p.p_f32, c[1], j, L);
                 } else {
-                    put_chunk<float, CE, A>(p.ws + unit * 2 * p.D, c[0], j, L);
-                    put_chunk<float, CE, A>(p.ws + (unit * 2 + 1) * p.D, c[1], j, L);
+                    put_chunk<float, CE, A>(p.ws + unit * 2 * p.D + c0, c[0], j, L);
+                    put_chunk<float, CE, A>(p.ws + (unit * 2 + 1) * p.D + c0, c[1], j, L);
                 }
             }
         }
@@ -295,36 +279,24 @@ template <class T, int NCH, Access A, bool RES>
 static cudaError_t ln_bwd_token(const LnBwdParams& p, cudaStream_t s) {
     auto k = ln_backward_token_kernel<T, NCH, A, RES>;
     const int tpr = row_threads(p.D), elem = p.p_f32 ? 4 : 2;
-    const RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, RES ? 3 : 2, 16 * elem * tpr);
+    const RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, RES ? 3 : 2, 16 * elem * tpr, 0);
     static SmemOptIn opt_in;
     if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
     const int64_t need = (p.rows + sh.groups - 1) / sh.groups, most = (int64_t)sm_count() * sh.ctas_per_sm;
     return launch_pdl(k, (unsigned)(need < most ? need : most), sh.groups * tpr, sh.smem, s, p, sh);
 }
 
-template <class T, int NCH, Access A, int R, bool RES>
-static cudaError_t ln_bwd_sum(const LnBwdParams& p, const RingShape& sh, cudaStream_t s) {
-    auto k = ln_backward_kernel<T, NCH, A, R, RES>;
-    static SmemOptIn opt_in;
-    if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
-    const int64_t units = p.mod_rows * p.plan.parts, most = 1 << 30;
-    return launch_pdl(k, (unsigned)(units < most ? units : most), sh.groups * sh.tpr, sh.smem, s, p, sh);
-}
-
 template <class T, int NCH, Access A, bool RES>
 static cudaError_t ln_bwd(const LnBwdParams& p0, cudaStream_t s) {
     LnBwdParams p = p0;
     if (p.seq == 1 && p.factor) return ln_bwd_token<T, NCH, A, RES>(p, s);
+    auto k = ln_backward_kernel<T, NCH, A, RES>;
     p.plan = grad_plan(p.rows, p.mod_rows, p.D, (int)sizeof(T));
-    const RingShape one = grad_shape(p.D, (int)sizeof(T), RES ? 3 : 2), two = grad_shape(p.D, (int)sizeof(T), RES ? 6 : 4);
-    cudaError_t e;
-    // two rows a round where two stages of them fit in as many blocks
-    if constexpr (A == kVec) {
-        if (two.stages >= 2 && two.ctas_per_sm == one.ctas_per_sm) e = ln_bwd_sum<T, NCH, A, 2, RES>(p, two, s);
-        else e = ln_bwd_sum<T, NCH, A, 1, RES>(p, one, s);
-    } else {
-        e = ln_bwd_sum<T, NCH, A, 1, RES>(p, one, s);
-    }
+    const RingShape sh = grad_shape(p.D, (int)sizeof(T), RES ? 3 : 2);
+    static SmemOptIn opt_in;
+    if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
+    const int64_t units = p.mod_rows * p.plan.parts, most = 1 << 30;
+    const cudaError_t e = launch_pdl(k, (unsigned)(units < most ? units : most), sh.groups * sh.tpr, sh.smem, s, p, sh);
     if (e != cudaSuccess || p.plan.parts == 1 || (!p.dfactor && !p.dshift)) return e;
     ColSumParams c{p.ws, p.plan.parts, p.mod_rows, p.D, 2, {p.dfactor, p.dshift}, {p.dfactor_stride, p.dshift_stride}, p.p_f32};
     return launch_column_sums(c, s);

@@ -52,11 +52,14 @@ __device__ __forceinline__ Lane make_lane(int t, int tpr, int D) {
     const int units = A == kVec ? D / CE : D;
     return Lane{t, tpr, units > t ? (units - t + tpr - 1) / tpr : 0};
 }
+// This thread's first column.
+template <int CE, Access A>
+__device__ __forceinline__ int first_col(const Lane& L) {
+    return A == kVec ? L.t * CE : L.t;
+}
 
-template <class Q, int NCH, int CE>
-constexpr int kRowBytesPerThread = NCH * CE * (int)sizeof(Q);
-
-// Start the copy of this thread's part of `row` to its place in a stage.
+// Start the copy of this thread's part of a row to its place in a stage; `row`
+// points at its first column.
 template <class Q, int NCH, int CE, Access A>
 __device__ __forceinline__ void ring_fill(char* dst, const Q* row, const Lane& L) {
     if constexpr (A == kVec) {
@@ -66,15 +69,15 @@ __device__ __forceinline__ void ring_fill(char* dst, const Q* row, const Lane& L
             if (j < L.nv) {
 #pragma unroll
                 for (int h = 0; h < P; ++h)
-                    ring_cp16(dst + ((j * P + h) * L.tpr + L.t) * 16, row + (int64_t)(j * L.tpr + L.t) * CE + h * (16 / sizeof(Q)));
+                    ring_cp16(dst + ((j * P + h) * L.tpr + L.t) * 16, row + j * L.tpr * CE + h * (16 / (int)sizeof(Q)));
             }
     } else {
 #pragma unroll
         for (int e = 0; e < NCH * CE; ++e) {
             const int c = e * L.tpr + L.t;
             if (e < L.nv) {
-                if constexpr (sizeof(Q) == 4) ring_cp4(dst + c * 4, row + c);
-                else reinterpret_cast<Q*>(dst)[c] = ld_u16_rw(row + c);
+                if constexpr (sizeof(Q) == 4) ring_cp4(dst + c * 4, row + e * L.tpr);
+                else reinterpret_cast<Q*>(dst)[c] = ld_u16_rw(row + e * L.tpr);
             }
         }
     }
@@ -119,6 +122,21 @@ template <Access A>
 __device__ __forceinline__ bool has_chunk(int j, const Lane& L) {
     return A == kVec ? j < L.nv : true;
 }
+
+// A staged row as pairs; 0 where no column exists.
+template <class Q, int NCH, int CE, Access A>
+__device__ __forceinline__ void read_row(u64 (&v)[NCH * CE / 2], const char* src, const Lane& L) {
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+        u64 c[CE / 2];
+#pragma unroll
+        for (int i = 0; i < CE / 2; ++i) c[i] = 0;
+        if (has_chunk<A>(j, L)) ring_read<Q, CE, A>(c, src, j, L);
+#pragma unroll
+        for (int i = 0; i < CE / 2; ++i) v[j * (CE / 2) + i] = c[i];
+    }
+}
+
 // 0 in place of a pair's elements that are no columns.
 template <int CE, Access A>
 __device__ __forceinline__ u64 mask_pair(u64 v, int j, int i, const Lane& L) {
@@ -127,11 +145,12 @@ __device__ __forceinline__ u64 mask_pair(u64 v, int j, int i, const Lane& L) {
     return f2(e < L.nv ? f2lo(v) : 0.0f, e + 1 < L.nv ? f2hi(v) : 0.0f);
 }
 
-// Chunk j to a row in memory, each element rounded once to Q.
+// Chunk j to a row in memory, each element rounded once to Q; `row` points at
+// the thread's first column.
 template <class Q, int CE, Access A>
 __device__ __forceinline__ void put_chunk(Q* row, const u64 (&p)[CE / 2], int j, const Lane& L) {
     if constexpr (A == kVec) {
-        Q* d = row + (int64_t)(j * L.tpr + L.t) * CE;
+        Q* d = row + j * L.tpr * CE;
         if constexpr (sizeof(Q) == 2) {
             st_v4(d, make_uint4(pack2_rn(p[0]), pack2_rn(p[1]), pack2_rn(p[2]), pack2_rn(p[3])));
         } else {
@@ -144,7 +163,7 @@ __device__ __forceinline__ void put_chunk(Q* row, const u64 (&p)[CE / 2], int j,
 #pragma unroll
         for (int i = 0; i < CE; ++i) {
             const int e = j * CE + i;
-            if (e < L.nv) store_elem(row + e * L.tpr + L.t, i % 2 ? f2hi(p[i / 2]) : f2lo(p[i / 2]));
+            if (e < L.nv) store_elem(row + e * L.tpr, i % 2 ? f2hi(p[i / 2]) : f2lo(p[i / 2]));
         }
     }
 }
@@ -157,23 +176,23 @@ __device__ __forceinline__ void put_param_chunk(void* p, int64_t off, bool p_f32
     else put_chunk<uint16_t, CE, A>(static_cast<uint16_t*>(p) + off, v, j, L);
 }
 
-// Chunk j of a row in memory, 0 where no column exists.  RW: the kernel may
-// write that row (an exact in-place update), so it is read with coherent loads.
-template <class Q, int CE, Access A, bool RW = false>
+// Chunk j of a row in memory, 0 where no column exists.  For
+// parameters, which no output overlaps.
+template <class Q, int CE, Access A>
 __device__ __forceinline__ void get_chunk(u64 (&p)[CE / 2], const Q* row, int j, const Lane& L) {
     if constexpr (A == kVec) {
 #pragma unroll
         for (int i = 0; i < CE / 2; ++i) p[i] = 0;
         if (j < L.nv) {
-            const Q* s = row + (int64_t)(j * L.tpr + L.t) * CE;
+            const Q* s = row + j * L.tpr * CE;
             if constexpr (sizeof(Q) == 2) {
-                const uint4 v = RW ? ld_stream_rw(s) : ld_shared_row(s);
+                const uint4 v = ld_shared_row(s);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) p[i] = widen2(w_of(v, i));
             } else {
 #pragma unroll
                 for (int h = 0; h < CE / 4; ++h) {
-                    const uint4 v = RW ? ld_stream_rw(s + 4 * h) : ld_shared_row(s + 4 * h);
+                    const uint4 v = ld_shared_row(s + 4 * h);
                     p[2 * h] = f2(__uint_as_float(v.x), __uint_as_float(v.y));
                     p[2 * h + 1] = f2(__uint_as_float(v.z), __uint_as_float(v.w));
                 }
@@ -183,8 +202,8 @@ __device__ __forceinline__ void get_chunk(u64 (&p)[CE / 2], const Q* row, int j,
 #pragma unroll
         for (int i = 0; i < CE; i += 2) {
             const int e = j * CE + i;
-            p[i / 2] = f2(e < L.nv ? load_elem(row + e * L.tpr + L.t) : 0.0f,
-                          e + 1 < L.nv ? load_elem(row + (e + 1) * L.tpr + L.t) : 0.0f);
+            p[i / 2] = f2(e < L.nv ? load_elem(row + e * L.tpr) : 0.0f,
+                          e + 1 < L.nv ? load_elem(row + (e + 1) * L.tpr) : 0.0f);
         }
     }
 }
@@ -209,44 +228,50 @@ struct GroupSums {
     int t, tpr, bar_id, par;
     template <int V>
     __device__ __forceinline__ void operator()(float (&v)[V]) {
-        const int lanes = tpr < 32 ? tpr : 32;
-        const int lane = t & (lanes - 1);
-        int s = lanes / 2;
+        if (tpr >= 32) run<V, 32>(v);
+        else if (tpr == 16) run<V, 16>(v);
+        else run<V, 8>(v);
+    }
+
+    template <int V, int LANES>
+    __device__ __forceinline__ void run(float (&v)[V]) {
+        const int lane = t % LANES;
         float c[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) c[k] = v[k];
+        constexpr int kPer = LANES / V;  // lanes that end up with the same value
 #pragma unroll
-        for (int n = V / 2; n >= 1; n /= 2) {
+        for (int n = V / 2, s = LANES / 2; n >= 1; n /= 2, s /= 2) {
             const bool hi = lane & s;
 #pragma unroll
             for (int k = 0; k < n; ++k) {
                 const float give = hi ? c[k] : c[k + n], keep = hi ? c[k + n] : c[k];
                 c[k] = keep + __shfl_xor_sync(0xffffffffu, give, s);
             }
-            s /= 2;
         }
-        float a = c[0];  // the sum of value `mine` over the lanes that share the bits not yet summed
-        for (; s >= 1; s /= 2) a += __shfl_xor_sync(0xffffffffu, a, s);
-        const int per = lanes / V, mine = lane / per;
-        if (tpr > 32) {
-            float* slot = buf + par * 8 * kMaxWarpsPerRow;
-            par ^= 1;
-            if (lane % per == 0) slot[mine * kMaxWarpsPerRow + t / 32] = a;
-            named_bar(bar_id, tpr);
-            constexpr int W = kMaxWarpsPerRow * V / 32;  // warps' sums that a lane adds
-            a = 0.0f;
-            const float* q = slot + mine * kMaxWarpsPerRow + (lane % (32 / V)) * W;
-            if constexpr (W == 0) {
-                if (lane % (32 / V) < kMaxWarpsPerRow) a = slot[mine * kMaxWarpsPerRow + lane % (32 / V)];
-            } else {
+        float a = c[0];  // of value lane / kPer, over the lanes that differ in the bits above
 #pragma unroll
-                for (int w = 0; w < W; ++w) a += q[w];
+        for (int s = kPer / 2; s >= 1; s /= 2) a += __shfl_xor_sync(0xffffffffu, a, s);
+        if constexpr (LANES == 32) {
+            if (tpr > 32) {
+                float* slot = buf + par * 8 * kMaxWarpsPerRow + lane / kPer * kMaxWarpsPerRow;
+                par ^= 1;
+                if (lane % kPer == 0) slot[t / 32] = a;
+                named_bar(bar_id, tpr);
+                constexpr int W = kMaxWarpsPerRow / kPer;  // warps' sums that a lane adds
+                a = 0.0f;
+                if constexpr (W == 0) {
+                    if (lane % kPer < kMaxWarpsPerRow) a = slot[lane % kPer];
+                } else {
+#pragma unroll
+                    for (int w = 0; w < W; ++w) a += slot[lane % kPer * W + w];
+                }
+#pragma unroll
+                for (int s = kPer / 2; s >= 1; s /= 2) a += __shfl_xor_sync(0xffffffffu, a, s);
             }
-#pragma unroll
-            for (int x = 16 / V; x >= 1; x /= 2) a += __shfl_xor_sync(0xffffffffu, a, x);
         }
 #pragma unroll
-        for (int k = 0; k < V; ++k) v[k] = __shfl_sync(0xffffffffu, a, k * per, lanes);
+        for (int k = 0; k < V; ++k) v[k] = __shfl_sync(0xffffffffu, a, k * kPer, LANES);
     }
 };
 constexpr int kSumFloats = 2 * 8 * kMaxWarpsPerRow;  // of one group

@@ -22,12 +22,13 @@ constexpr int kRingThreads = 640;
 
 // How a kernel that streams rows through shared memory fills an SM: blocks of
 // `groups` row groups, `ctas_per_sm` blocks, and for every group a ring of
-// `stages` stages of `rows` rows of row_bytes (and extra_bytes).
+// `stages` stages of `rows` rows of row_bytes (and extra_bytes); fixed_bytes are
+// the block's own.
 struct RingShape {
     int tpr, groups, stages, ctas_per_sm;
-    int row_bytes, extra_bytes, sums_bytes, group_bytes, smem;
+    int row_bytes, extra_bytes, sums_bytes, fixed_bytes, group_bytes, smem;
 };
-RingShape ring_shape(int tpr, int row_bytes, int rows, int extra_bytes);  // stages < 1: does not fit
+RingShape ring_shape(int tpr, int row_bytes, int rows, int extra_bytes, int fixed_per_thread);  // stages < 1: does not fit
 
 // Raises a kernel's shared-memory limit once for each device.
 struct SmemOptIn {
