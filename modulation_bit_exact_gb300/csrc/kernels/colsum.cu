@@ -5,18 +5,18 @@
 
 namespace mbx {
 
-RingShape ring_shape(int tpr, int row_bytes, int rows, int extra_bytes, int fixed_per_thread) {
+RingShape ring_shape(int tpr, int row_bytes, int rows, int extra_bytes, int fixed_per_thread, int threads_per_sm) {
     RingShape s;
     s.tpr = tpr;
     s.row_bytes = row_bytes;
     s.extra_bytes = extra_bytes;
-    s.groups = tpr >= 320 ? 1 : 320 / tpr;
+    s.groups = 2 * tpr > threads_per_sm ? 1 : threads_per_sm / 2 / tpr;  // two blocks an SM
     while (s.groups * tpr % 32) --s.groups;  // whole warps
     s.sums_bytes = tpr > 32 ? s.groups * 2 * 8 * 16 * (int)sizeof(float) : 0;
     s.fixed_bytes = fixed_per_thread * s.groups * tpr;
     const int stage = (rows * row_bytes + extra_bytes) * s.groups;
     // as many blocks as the threads allow, if two stages fit for each
-    for (s.ctas_per_sm = kRingThreads / (s.groups * tpr);; --s.ctas_per_sm) {
+    for (s.ctas_per_sm = threads_per_sm / (s.groups * tpr);; --s.ctas_per_sm) {
         const int room = 228 * 1024 / s.ctas_per_sm - 1024 - s.sums_bytes - s.fixed_bytes;  // 1 KB of each block's is the system's
         s.stages = room / stage;
         if (s.stages >= 2 || s.ctas_per_sm == 1) break;
@@ -44,7 +44,7 @@ cudaError_t SmemOptIn::allow(const void* kernel, const RingShape& sh) {
 
 RingShape grad_shape(int D, int esize, int rows) {
     const int tpr = row_threads(D);
-    return ring_shape(tpr, 16 * esize * tpr, rows, 0, 64);
+    return ring_shape(tpr, 16 * esize * tpr, rows, 0, 64, kGradThreads);
 }
 
 GradPlan grad_plan(int64_t rows, int64_t mod_rows, int D, int esize) {
@@ -65,7 +65,7 @@ int64_t grad_workspace_bytes(int64_t rows, int64_t mod_rows, int D, int esize) {
     return g.parts == 1 ? 0 : mod_rows * g.parts * 2 * D * (int64_t)sizeof(float);
 }
 
-constexpr int kColTile = 32, kColLanes = 8;
+constexpr int kColTile = 32, kColLanes = 16;
 
 __global__ void __launch_bounds__(kColTile* kColLanes) column_sums_kernel(ColSumParams p) {
     __shared__ float part[kColLanes][kColTile];
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kColTile* kColLanes) column_sums_kernel(ColSum
         const float* w = p.ws + seg * p.parts * cols;
         float s = 0.0f;
         if (c < cols) {
-#pragma unroll 4
+#pragma unroll 8
             for (int64_t i = threadIdx.y; i < p.parts; i += kColLanes) s += w[i * cols + c];
         }
         part[threadIdx.y][threadIdx.x] = s;

@@ -52,10 +52,8 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
     const int64_t step = (int64_t)gridDim.x * sh.groups * R;
     const int64_t rounds = (p.rows + step - 1) / step;  // the same for every group
     int64_t r = ((int64_t)blockIdx.x * sh.groups + g) * R, fill_row = r;
-    int fill_stage = 0;
-    auto fill = [&](int64_t) {
-        char* dst = ring + fill_stage * stage_bytes;
-        if (++fill_stage == sh.stages) fill_stage = 0;
+    auto fill = [&](int st) {
+        char* dst = ring + st * stage_bytes;
 #pragma unroll
         for (int k = 0; k < R; ++k)
             if (fill_row + k < p.rows)
@@ -63,17 +61,18 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
         fill_row += step;
         ring_commit();
     };
-    for (int i = 0; i < sh.stages - 1; ++i) fill(i);
+    for (int i = 0; i < sh.stages; ++i) fill(i);
     int stage = 0;
     for (int64_t round = 0; round < rounds; ++round, r += step) {
-        ring_turn(sh.stages, round, fill);
-        const char* src = ring + stage * stage_bytes;
-        if (++stage == sh.stages) stage = 0;
+        ring_wait(sh.stages);
         u64 v[R][P];
         float mean[R], rstd[R];
 #pragma unroll
+        for (int k = 0; k < R; ++k) read_row<T, NCH, CE, A>(v[k], ring + stage * stage_bytes + k * row_bytes, L);
+        fill(stage);
+        if (++stage == sh.stages) stage = 0;
+#pragma unroll
         for (int k = 0; k < R; ++k) {
-            read_row<T, NCH, CE, A>(v[k], src + k * row_bytes, L);
             u64 s = 0;
 #pragma unroll
             for (int e = 0; e < P; ++e) s = add2(s, v[k][e]);
@@ -122,7 +121,7 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
 template <class T, int NCH, Access A, int R>
 static cudaError_t ln_fwd(const LnFwdParams& p, int tpr, cudaStream_t s) {
     auto k = layer_norm_kernel<T, NCH, A, R>;
-    const RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, R, 0, 0);
+    const RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, R, 0, 0, kRingThreads);
     static SmemOptIn opt_in;
     if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
     const int64_t batches = (p.rows + R - 1) / R, need = (batches + sh.groups - 1) / sh.groups;

@@ -15,46 +15,62 @@
 
 namespace mbx {
 
-// One row in registers: x and dy as pairs.  gy(e) gives pair e of dy * f.  On
-// return x holds xh and the result the coefficients of
+// R rows in registers, x as pairs; gy(k, e) gives pair e of row k's dy * f.  On
+// return x holds xh, and c the coefficients of
 //   dx = rstd*gy + k1 + xh*k2,   k1 = -rstd*c1, k2 = -rstd*c2.
 struct RowCoef {
     float rstd, k1, k2;
 };
-template <int NCH, int CE, Access A, class Gy>
-__device__ __forceinline__ RowCoef ln_row_stats(u64 (&x)[NCH * CE / 2], const Lane& L, float inv_d, float eps,
-                                                GroupSums& sums, Gy gy) {
+template <int R, int NCH, int CE, Access A, class Gy>
+__device__ __forceinline__ void ln_row_stats(RowCoef (&c)[R], u64 (&x)[R][NCH * CE / 2], const Lane& L, float inv_d,
+                                             float eps, GroupSums& sums, Gy gy) {
     constexpr int H = CE / 2;
-    u64 s = 0, sg = 0;
+    float v[2 * R];
 #pragma unroll
-    for (int e = 0; e < NCH * H; ++e) {
-        s = add2(s, x[e]);
-        sg = add2(sg, gy(e));
-    }
-    float v[2] = {f2lo(s) + f2hi(s), f2lo(sg) + f2hi(sg)};
-    sums(v);
-    const float mean = v[0] * inv_d, c1 = v[1] * inv_d;
-    const u64 m = f2(mean, mean);
-    u64 q = 0, qg = 0;
+    for (int k = 0; k < R; ++k) {
+        u64 s[2] = {0, 0}, sg[2] = {0, 0};
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-        if (!has_chunk<A>(j, L)) continue;  // its x and dy are 0 and count for nothing
-#pragma unroll
-        for (int i = 0; i < H; ++i) {
-            const int e = j * H + i;
-            x[e] = mask_pair<CE, A>(sub2(x[e], m), j, i, L);
-            q = fma2(x[e], x[e], q);
-            qg = fma2(gy(e), x[e], qg);
+        for (int e = 0; e < NCH * H; ++e) {
+            s[e % 2] = add2(s[e % 2], x[k][e]);
+            sg[e % 2] = add2(sg[e % 2], gy(k, e));
         }
+        s[0] = add2(s[0], s[1]);
+        sg[0] = add2(sg[0], sg[1]);
+        v[2 * k] = f2lo(s[0]) + f2hi(s[0]);
+        v[2 * k + 1] = f2lo(sg[0]) + f2hi(sg[0]);
     }
-    v[0] = f2lo(q) + f2hi(q);
-    v[1] = f2lo(qg) + f2hi(qg);
     sums(v);
-    const float rstd = rsqrtf(v[0] * inv_d + eps);
-    const u64 rs = f2(rstd, rstd);
 #pragma unroll
-    for (int e = 0; e < NCH * H; ++e) x[e] = mul2(x[e], rs);
-    return RowCoef{rstd, -rstd * c1, -rstd * (v[1] * inv_d * rstd)};
+    for (int k = 0; k < R; ++k) {
+        const float mean = v[2 * k] * inv_d;
+        c[k].k1 = v[2 * k + 1] * inv_d;
+        const u64 m = f2(mean, mean);
+        u64 q[2] = {0, 0}, qg[2] = {0, 0};
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+            if (!has_chunk<A>(j, L)) continue;  // its x and dy are 0 and count for nothing
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const int e = j * H + i;
+                x[k][e] = mask_pair<CE, A>(sub2(x[k][e], m), j, i, L);
+                q[e % 2] = fma2(x[k][e], x[k][e], q[e % 2]);
+                qg[e % 2] = fma2(gy(k, e), x[k][e], qg[e % 2]);
+            }
+        }
+        q[0] = add2(q[0], q[1]);
+        qg[0] = add2(qg[0], qg[1]);
+        v[2 * k] = f2lo(q[0]) + f2hi(q[0]);
+        v[2 * k + 1] = f2lo(qg[0]) + f2hi(qg[0]);
+    }
+    sums(v);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        const float rstd = rsqrtf(v[2 * k] * inv_d + eps);
+        const u64 rs = f2(rstd, rstd);
+#pragma unroll
+        for (int e = 0; e < NCH * H; ++e) x[k][e] = mul2(x[k][e], rs);
+        c[k] = RowCoef{rstd, -rstd * c[k].k1, -rstd * (v[2 * k + 1] * inv_d * rstd)};
+    }
 }
 
 // One modulation row for every row: nothing is summed, every output is a row,
@@ -77,10 +93,8 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
     const int c0 = first_col<CE, A>(L);
     const u64 one = f2(p.factor_add, p.factor_add);
     int64_t fill_row = first;
-    int fill_stage = 0;
-    auto fill = [&](int64_t) {
-        char* dst = ring + fill_stage * stage_bytes;
-        if (++fill_stage == sh.stages) fill_stage = 0;
+    auto fill = [&](int st) {
+        char* dst = ring + st * stage_bytes;
         if (fill_row < p.rows) {
             ring_fill<T, NCH, CE, A>(dst, static_cast<const T*>(p.x) + fill_row * p.x_stride + c0, L);
             ring_fill<T, NCH, CE, A>(dst + row_bytes, static_cast<const T*>(p.dout) + fill_row * p.dout_stride + c0, L);
@@ -94,34 +108,39 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
         fill_row += step;
         ring_commit();
     };
-    for (int i = 0; i < sh.stages - 1; ++i) fill(i);
+    for (int i = 0; i < sh.stages; ++i) fill(i);
     int stage = 0;
     int64_t r = first;
     for (int64_t round = 0; round < rounds; ++round, r += step) {
-        ring_turn(sh.stages, round, fill);
+        ring_wait(sh.stages);
         const char* src = ring + stage * stage_bytes;
-        if (++stage == sh.stages) stage = 0;
-        u64 x[NCH * H], dy[NCH * H], gy[NCH * H];
+        u64 xs[1][NCH * H], dy[NCH * H], gy[NCH * H];
+        u64(&x)[NCH * H] = xs[0];
         read_row<T, NCH, CE, A>(x, src, L);
         read_row<T, NCH, CE, A>(dy, src + row_bytes, L);
         if (sizeof(T) == 4 || p.p_f32) read_row<float, NCH, CE, A>(gy, src + kF * row_bytes, L);
         else read_row<uint16_t, NCH, CE, A>(gy, src + kF * row_bytes, L);
+        uint4 res[RES ? NCH : 1];
+        if constexpr (RES) read_pieces<T, NCH, A>(res, src + 2 * row_bytes, L);
+        fill(stage);
+        if (++stage == sh.stages) stage = 0;
 #pragma unroll
         for (int e = 0; e < NCH * H; ++e) gy[e] = mul2(dy[e], add2(gy[e], one));
-        const RowCoef k = ln_row_stats<NCH, CE, A>(x, L, inv_d, p.eps, sums, [&](int e) { return gy[e]; });
+        RowCoef ks[1];
+        const RowCoef& k = ks[0];
+        ln_row_stats<1, NCH, CE, A>(ks, xs, L, inv_d, p.eps, sums, [&](int, int e) { return gy[e]; });
         if (r >= p.rows) continue;
         const u64 rs = f2(k.rstd, k.rstd), a = f2(k.k1, k.k1), b = f2(k.k2, k.k2);
         T* dx_row = static_cast<T*>(p.dx) + r * p.dx_stride + c0;
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
             if (!has_chunk<A>(j, L)) continue;
-            u64 dx[H], xd[H], d[H], res[H];
-            if constexpr (RES) ring_read<T, CE, A>(res, src + 2 * row_bytes, j, L);
+            u64 dx[H], xd[H], d[H];
 #pragma unroll
             for (int i = 0; i < H; ++i) {
                 const int e = j * H + i;
                 dx[i] = fma2(x[e], b, fma2(gy[e], rs, a));
-                if constexpr (RES) dx[i] = add2(dx[i], res[i]);
+                if constexpr (RES) dx[i] = add2(dx[i], piece_pair<T>(res, e));
                 xd[i] = mul2(x[e], dy[e]);
                 d[i] = dy[e];
             }
@@ -137,7 +156,7 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
 // in binary32 registers, the groups are added in shared memory, and the part's
 // sums go to the workspace (or out, when the segment is one part).
 template <class T, int NCH, Access A, bool RES>
-__global__ void __launch_bounds__(kRingThreads) ln_backward_kernel(LnBwdParams p, RingShape sh) {
+__global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p, RingShape sh) {
     constexpr int CE = ChunkOf<T>::CE, H = CE / 2, P = NCH * H;
     extern __shared__ __align__(16) char smem[];
     const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr, groups = sh.groups;
@@ -174,18 +193,13 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_kernel(LnBwdParams p
                 adf[j * H + i] = adf[j * H + i + 1] = ads[j * H + i] = ads[j * H + i + 1] = 0;
             }
         }
-        auto factor = [&](int e) {
-            const ulonglong2 v = fs[e / 2 * block];
-            return e % 2 ? v.y : v.x;
-        };
         const T* nx = static_cast<const T*>(p.x) + (r0 + g) * p.x_stride + c0;
         const T* nd = static_cast<const T*>(p.dout) + (r0 + g) * p.dout_stride + c0;
         const T* nr = RES ? static_cast<const T*>(p.dres) + (r0 + g) * p.dres_stride + c0 : nullptr;
         T* dx_row = static_cast<T*>(p.dx) + (r0 + g) * p.dx_stride + c0;
-        int fill_row = g, fill_stage = 0;
-        auto fill = [&](int64_t) {
-            char* dst = ring + fill_stage * stage_bytes;
-            if (++fill_stage == sh.stages) fill_stage = 0;
+        int fill_row = g;
+        auto fill = [&](int st) {
+            char* dst = ring + st * stage_bytes;
             if (fill_row < n_rows) {
                 ring_fill<T, NCH, CE, A>(dst, nx, L);
                 ring_fill<T, NCH, CE, A>(dst + row_bytes, nd, L);
@@ -197,29 +211,38 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_kernel(LnBwdParams p
             if constexpr (RES) nr += groups * p.dres_stride;
             ring_commit();
         };
-        for (int i = 0; i < sh.stages - 1; ++i) fill(i);
+        for (int i = 0; i < sh.stages; ++i) fill(i);
         int stage = 0;
         for (int round = 0; round < rounds; ++round, dx_row += groups * p.dx_stride) {
-            ring_turn(sh.stages, round, fill);
+            ring_wait(sh.stages);
             const char* src = ring + stage * stage_bytes;
-            if (++stage == sh.stages) stage = 0;
-            u64 x[P], dy[P];
+            u64 xs[1][P], dy[P], gy[P];
+            u64(&x)[P] = xs[0];
             read_row<T, NCH, CE, A>(x, src, L);
             read_row<T, NCH, CE, A>(dy, src + row_bytes, L);
-            const RowCoef k =
-                ln_row_stats<NCH, CE, A>(x, L, inv_d, p.eps, sums, [&](int e) { return mul2(dy[e], factor(e)); });
+            uint4 res[RES ? NCH : 1];
+            if constexpr (RES) read_pieces<T, NCH, A>(res, src + 2 * row_bytes, L);
+            fill(stage);
+            if (++stage == sh.stages) stage = 0;
+#pragma unroll
+            for (int e = 0; e < P; e += 2) {
+                const ulonglong2 f = fs[e / 2 * block];
+                gy[e] = mul2(dy[e], f.x);
+                gy[e + 1] = mul2(dy[e + 1], f.y);
+            }
+            RowCoef c[1];
+            ln_row_stats<1, NCH, CE, A>(c, xs, L, inv_d, p.eps, sums, [&](int, int e) { return gy[e]; });
             if (round * groups + g >= n_rows) continue;
-            const u64 rs = f2(k.rstd, k.rstd), a = f2(k.k1, k.k1), b = f2(k.k2, k.k2);
+            const u64 rs = f2(c[0].rstd, c[0].rstd), a = f2(c[0].k1, c[0].k1), b = f2(c[0].k2, c[0].k2);
 #pragma unroll
             for (int j = 0; j < NCH; ++j) {
                 if (!has_chunk<A>(j, L)) continue;
-                u64 dx[H], res[H];
-                if constexpr (RES) ring_read<T, CE, A>(res, src + 2 * row_bytes, j, L);
+                u64 dx[H];
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     const int e = j * H + i;
-                    dx[i] = fma2(x[e], b, fma2(mul2(dy[e], factor(e)), rs, a));
-                    if constexpr (RES) dx[i] = add2(dx[i], res[i]);
+                    dx[i] = fma2(x[e], b, fma2(gy[e], rs, a));
+                    if constexpr (RES) dx[i] = add2(dx[i], piece_pair<T>(res, e));
                     adf[e] = fma2(x[e], dy[e], adf[e]);
                     ads[e] = add2(ads[e], dy[e]);
                 }
@@ -279,7 +302,7 @@ template <class T, int NCH, Access A, bool RES>
 static cudaError_t ln_bwd_token(const LnBwdParams& p, cudaStream_t s) {
     auto k = ln_backward_token_kernel<T, NCH, A, RES>;
     const int tpr = row_threads(p.D), elem = p.p_f32 ? 4 : 2;
-    const RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, RES ? 3 : 2, 16 * elem * tpr, 0);
+    const RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, RES ? 3 : 2, 16 * elem * tpr, 0, kRingThreads);
     static SmemOptIn opt_in;
     if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
     const int64_t need = (p.rows + sh.groups - 1) / sh.groups, most = (int64_t)sm_count() * sh.ctas_per_sm;

@@ -26,20 +26,14 @@ __device__ __forceinline__ void ring_cp4(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
 }
 __device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All but the newest stages-2 groups have landed (stages <= 4).
+// All but the newest stages-1 groups have landed (stages <= 4): the oldest
+// stage is ready.  Its rows go to registers at once and the stage is filled
+// again, so that every stage but that one is always on its way.
 __device__ __forceinline__ void ring_wait(int stages) {
-    if (stages <= 2) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    else if (stages == 3) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else asm volatile("cp.async.wait_group 2;" ::: "memory");
-}
-
-// Round `round`'s stage is ready and the next free stage is on its way; one
-// stage (the largest rows) is filled and awaited in turn.
-template <class Fill>
-__device__ __forceinline__ void ring_turn(int stages, int64_t round, Fill& fill) {
-    if (stages == 1) fill(round);
-    ring_wait(stages);
-    if (stages > 1) fill(round + stages - 1);
+    if (stages == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (stages == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
 
 // This thread's place in its row group and the columns that it owns.
@@ -135,6 +129,33 @@ __device__ __forceinline__ void read_row(u64 (&v)[NCH * CE / 2], const char* src
 #pragma unroll
         for (int i = 0; i < CE / 2; ++i) v[j * (CE / 2) + i] = c[i];
     }
+}
+
+// A staged row as it came, widened where it is used: 16-byte pieces of T, or
+// (kScalar) single elements packed the same way.
+template <class T, int NCH, Access A>
+__device__ __forceinline__ void read_pieces(uint4 (&v)[NCH], const char* src, const Lane& L) {
+    constexpr int CE = ChunkOf<T>::CE;
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+        if constexpr (A == kVec) {
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (j < L.nv) v[j] = *reinterpret_cast<const uint4*>(src + (j * L.tpr + L.t) * 16);
+        } else {
+            u64 c[CE / 2];
+            ring_read<T, CE, A>(c, src, j, L);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (sizeof(T) == 2) w_set(v[j], i, pack2_rn(c[i]));
+                else w_set(v[j], i, (uint32_t)(c[i / 2] >> (i % 2 * 32)));
+            }
+        }
+    }
+}
+template <class T, int NCH>
+__device__ __forceinline__ u64 piece_pair(const uint4 (&v)[NCH], int e) {
+    if constexpr (sizeof(T) == 2) return widen2(w_of(v[e / 4], e % 4));
+    else return f2(__uint_as_float(w_of(v[e / 2], e % 2 * 2)), __uint_as_float(w_of(v[e / 2], e % 2 * 2 + 1)));
 }
 
 // 0 in place of a pair's elements that are no columns.

@@ -16,9 +16,9 @@ int sm_count();  // SMs of the current device; 0 if the runtime cannot tell
 // warp for the short rows, else whole warps.
 inline int row_threads(int D) { return D <= 128 ? 8 : D <= 256 ? 16 : (D + 511) / 512 * 32; }
 
-// The row kernels hold two to five rows in registers and accumulators at up to
-// 96 registers a thread, so 640 threads fit on an SM.
-constexpr int kRingThreads = 640;
+// Threads of an SM: the row kernels take up to 96 registers a thread, those
+// that also hold the sums of their columns up to 128.
+constexpr int kRingThreads = 640, kGradThreads = 512;
 
 // How a kernel that streams rows through shared memory fills an SM: blocks of
 // `groups` row groups, `ctas_per_sm` blocks, and for every group a ring of
@@ -28,7 +28,8 @@ struct RingShape {
     int tpr, groups, stages, ctas_per_sm;
     int row_bytes, extra_bytes, sums_bytes, fixed_bytes, group_bytes, smem;
 };
-RingShape ring_shape(int tpr, int row_bytes, int rows, int extra_bytes, int fixed_per_thread);  // stages < 1: does not fit
+RingShape ring_shape(int tpr, int row_bytes, int rows, int extra_bytes, int fixed_per_thread,
+                     int threads_per_sm);  // stages < 1: does not fit
 
 // Raises a kernel's shared-memory limit once for each device.
 struct SmemOptIn {
