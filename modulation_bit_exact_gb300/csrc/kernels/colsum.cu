@@ -12,7 +12,7 @@ RingShape ring_shape(int tpr, int row_bytes, int rows, int extra_bytes, int fixe
     s.extra_bytes = extra_bytes;
     s.groups = 2 * tpr > threads_per_sm ? 1 : threads_per_sm / 2 / tpr;  // two blocks an SM
     while (s.groups * tpr % 32) --s.groups;  // whole warps
-    s.sums_bytes = tpr > 32 ? s.groups * 2 * 8 * 16 * (int)sizeof(float) : 0;
+    s.sums_bytes = tpr > 32 ? s.groups * 2 * 4 * 16 * (int)sizeof(float) : 0;
     s.fixed_bytes = fixed_per_thread * s.groups * tpr;
     const int stage = (rows * row_bytes + extra_bytes) * s.groups;
     // as many blocks as the threads allow, if two stages fit for each

@@ -61,6 +61,7 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
         fill_row += step;
         ring_commit();
     };
+    for (int i = 0; i < sh.stages * R; ++i) ring_clear<T, NCH, CE, A>(ring + i * row_bytes, L);
     for (int i = 0; i < sh.stages; ++i) fill(i);
     int stage = 0;
     for (int64_t round = 0; round < rounds; ++round, r += step) {
@@ -82,15 +83,13 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             mean[k] *= inv_d;
-            const u64 m = f2(mean[k], mean[k]);
             u64 q = 0;
 #pragma unroll
             for (int j = 0; j < NCH; ++j) {
-                if (!has_chunk<A>(j, L)) continue;  // its elements are 0 and count for nothing
 #pragma unroll
                 for (int i = 0; i < CE / 2; ++i) {
                     u64& c = v[k][j * (CE / 2) + i];
-                    c = mask_pair<CE, A>(sub2(c, m), j, i, L);
+                    c = sub2(c, where_column<CE, A>(mean[k], j, i, L));
                     q = fma2(c, c, q);
                 }
             }

@@ -44,15 +44,13 @@ __device__ __forceinline__ void ln_row_stats(RowCoef (&c)[R], u64 (&x)[R][NCH * 
     for (int k = 0; k < R; ++k) {
         const float mean = v[2 * k] * inv_d;
         c[k].k1 = v[2 * k + 1] * inv_d;
-        const u64 m = f2(mean, mean);
         u64 q[2] = {0, 0}, qg[2] = {0, 0};
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
-            if (!has_chunk<A>(j, L)) continue;  // its x and dy are 0 and count for nothing
 #pragma unroll
             for (int i = 0; i < H; ++i) {
                 const int e = j * H + i;
-                x[k][e] = mask_pair<CE, A>(sub2(x[k][e], m), j, i, L);
+                x[k][e] = sub2(x[k][e], where_column<CE, A>(mean, j, i, L));
                 q[e % 2] = fma2(x[k][e], x[k][e], q[e % 2]);
                 qg[e % 2] = fma2(gy(k, e), x[k][e], qg[e % 2]);
             }
@@ -93,6 +91,12 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
     const int c0 = first_col<CE, A>(L);
     const u64 one = f2(p.factor_add, p.factor_add);
     int64_t fill_row = first;
+    for (int i = 0; i < sh.stages; ++i) {
+        char* dst = ring + i * stage_bytes;
+        for (int o = 0; o < kF; ++o) ring_clear<T, NCH, CE, A>(dst + o * row_bytes, L);
+        if (sizeof(T) == 4 || p.p_f32) ring_clear<float, NCH, CE, A>(dst + kF * row_bytes, L);
+        else ring_clear<uint16_t, NCH, CE, A>(dst + kF * row_bytes, L);
+    }
     auto fill = [&](int st) {
         char* dst = ring + st * stage_bytes;
         if (fill_row < p.rows) {
@@ -197,7 +201,10 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
         const T* nd = static_cast<const T*>(p.dout) + (r0 + g) * p.dout_stride + c0;
         const T* nr = RES ? static_cast<const T*>(p.dres) + (r0 + g) * p.dres_stride + c0 : nullptr;
         T* dx_row = static_cast<T*>(p.dx) + (r0 + g) * p.dx_stride + c0;
+        for (int i = 0; i < sh.stages * (RES ? 3 : 2); ++i) ring_clear<T, NCH, CE, A>(ring + i * row_bytes, L);
         int fill_row = g;
+        const int64_t x_step = groups * p.x_stride, d_step = groups * p.dout_stride, r_step = groups * p.dres_stride,
+                      dx_step = groups * p.dx_stride;
         auto fill = [&](int st) {
             char* dst = ring + st * stage_bytes;
             if (fill_row < n_rows) {
@@ -206,14 +213,14 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
                 if constexpr (RES) ring_fill<T, NCH, CE, A>(dst + 2 * row_bytes, nr, L);
             }
             fill_row += groups;
-            nx += groups * p.x_stride;
-            nd += groups * p.dout_stride;
-            if constexpr (RES) nr += groups * p.dres_stride;
+            nx += x_step;
+            nd += d_step;
+            if constexpr (RES) nr += r_step;
             ring_commit();
         };
         for (int i = 0; i < sh.stages; ++i) fill(i);
         int stage = 0;
-        for (int round = 0; round < rounds; ++round, dx_row += groups * p.dx_stride) {
+        for (int round = 0; round < rounds; ++round, dx_row += dx_step) {
             ring_wait(sh.stages);
             const char* src = ring + stage * stage_bytes;
             u64 xs[1][P], dy[P], gy[P];

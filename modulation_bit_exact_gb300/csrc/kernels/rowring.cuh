@@ -77,7 +77,8 @@ __device__ __forceinline__ void ring_fill(char* dst, const Q* row, const Lane& L
     }
 }
 
-// Chunk j of a staged row as CE/2 pairs; 0 where no column exists.
+// Chunk j of a staged row as CE/2 pairs (0 where no column exists: see
+// ring_clear).
 template <class Q, int CE, Access A>
 __device__ __forceinline__ void ring_read(u64 (&p)[CE / 2], const char* src, int j, const Lane& L) {
     if constexpr (A == kVec) {
@@ -99,36 +100,57 @@ __device__ __forceinline__ void ring_read(u64 (&p)[CE / 2], const char* src, int
             float v[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int e = j * CE + i + h, c = e * L.tpr + L.t;
-                v[h] = 0.0f;
-                if (e < L.nv) {
-                    if constexpr (sizeof(Q) == 4) v[h] = reinterpret_cast<const float*>(src)[c];
-                    else v[h] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(src)[c] << 16);
-                }
+                const int c = (j * CE + i + h) * L.tpr + L.t;
+                if constexpr (sizeof(Q) == 4) v[h] = reinterpret_cast<const float*>(src)[c];
+                else v[h] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(src)[c] << 16);
             }
             p[i / 2] = f2(v[0], v[1]);
         }
     }
 }
 
-// Whether chunk j has anything to do (kScalar masks its elements instead).
-template <Access A>
-__device__ __forceinline__ bool has_chunk(int j, const Lane& L) {
-    return A == kVec ? j < L.nv : true;
+// Zero this thread's places of a staged row that hold no column and that no
+// copy ever writes, so that reading needs no mask.
+template <class Q, int NCH, int CE, Access A>
+__device__ __forceinline__ void ring_clear(char* dst, const Lane& L) {
+    if constexpr (A == kVec) {
+        constexpr int P = CE * (int)sizeof(Q) / 16;
+        for (int j = L.nv; j < NCH; ++j)
+            for (int h = 0; h < P; ++h)
+                *reinterpret_cast<uint4*>(dst + ((j * P + h) * L.tpr + L.t) * 16) = make_uint4(0, 0, 0, 0);
+    } else {
+        for (int e = L.nv; e < NCH * CE; ++e) reinterpret_cast<Q*>(dst)[e * L.tpr + L.t] = 0;
+    }
 }
 
-// A staged row as pairs; 0 where no column exists.
+// A staged row as pairs.
 template <class Q, int NCH, int CE, Access A>
 __device__ __forceinline__ void read_row(u64 (&v)[NCH * CE / 2], const char* src, const Lane& L) {
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
         u64 c[CE / 2];
-#pragma unroll
-        for (int i = 0; i < CE / 2; ++i) c[i] = 0;
-        if (has_chunk<A>(j, L)) ring_read<Q, CE, A>(c, src, j, L);
+        ring_read<Q, CE, A>(c, src, j, L);
 #pragma unroll
         for (int i = 0; i < CE / 2; ++i) v[j * (CE / 2) + i] = c[i];
     }
+}
+
+// v for the columns of pair i of chunk j, 0 for the rest: subtracted from a
+// row's 0 there, the mean must leave 0.
+template <int CE, Access A>
+__device__ __forceinline__ u64 where_column(float v, int j, int i, const Lane& L) {
+    if constexpr (A == kVec) {
+        const float w = j < L.nv ? v : 0.0f;
+        return f2(w, w);
+    }
+    const int e = j * CE + 2 * i;
+    return f2(e < L.nv ? v : 0.0f, e + 1 < L.nv ? v : 0.0f);
+}
+
+// Whether chunk j is stored (kScalar masks its elements instead).
+template <Access A>
+__device__ __forceinline__ bool has_chunk(int j, const Lane& L) {
+    return A == kVec ? j < L.nv : true;
 }
 
 // A staged row as it came, widened where it is used: 16-byte pieces of T, or
@@ -139,8 +161,7 @@ __device__ __forceinline__ void read_pieces(uint4 (&v)[NCH], const char* src, co
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
         if constexpr (A == kVec) {
-            v[j] = make_uint4(0, 0, 0, 0);
-            if (j < L.nv) v[j] = *reinterpret_cast<const uint4*>(src + (j * L.tpr + L.t) * 16);
+            v[j] = *reinterpret_cast<const uint4*>(src + (j * L.tpr + L.t) * 16);
         } else {
             u64 c[CE / 2];
             ring_read<T, CE, A>(c, src, j, L);
@@ -156,14 +177,6 @@ template <class T, int NCH>
 __device__ __forceinline__ u64 piece_pair(const uint4 (&v)[NCH], int e) {
     if constexpr (sizeof(T) == 2) return widen2(w_of(v[e / 4], e % 4));
     else return f2(__uint_as_float(w_of(v[e / 2], e % 2 * 2)), __uint_as_float(w_of(v[e / 2], e % 2 * 2 + 1)));
-}
-
-// 0 in place of a pair's elements that are no columns.
-template <int CE, Access A>
-__device__ __forceinline__ u64 mask_pair(u64 v, int j, int i, const Lane& L) {
-    if constexpr (A == kVec) return v;
-    const int e = j * CE + 2 * i;
-    return f2(e < L.nv ? f2lo(v) : 0.0f, e + 1 < L.nv ? f2hi(v) : 0.0f);
 }
 
 // Chunk j to a row in memory, each element rounded once to Q; `row` points at
@@ -236,22 +249,40 @@ __device__ __forceinline__ void get_param_chunk(u64 (&v)[CE / 2], const void* p,
     else get_chunk<uint16_t, CE, A>(v, static_cast<const uint16_t*>(p) + off, j, L);
 }
 
-// Sums of V values (a power of two, at most 8) over a row group, in every
+// Sums of V values (a power of two, at most 4) over a row group, in every
 // thread.  Inside a warp the first log2(V) shuffle steps halve the number of
 // values that a lane carries, so that V sums take about V + log2(lanes)
 // shuffles instead of V*log2(lanes); then the warps' sums meet in shared
-// memory, one barrier, and every warp adds them in the same order.  The
-// published sums alternate between two buffers: a buffer is written again two
-// calls later, after the barrier of the call in between, which every reader
-// has passed.
+// memory, one barrier, and every thread adds them in warp order (reading them
+// all costs less time than five more dependent shuffles).  The published sums
+// alternate between two buffers: a buffer is written again two calls later,
+// after the barrier of the call in between, which every reader has passed.
 struct GroupSums {
-    float* buf;  // [2][8][kMaxWarpsPerRow] of this group, zeroed
+    float* buf;  // [2][kMaxWarpsPerRow][4] of this group, zeroed
     int t, tpr, bar_id, par;
     template <int V>
     __device__ __forceinline__ void operator()(float (&v)[V]) {
         if (tpr >= 32) run<V, 32>(v);
         else if (tpr == 16) run<V, 16>(v);
         else run<V, 8>(v);
+    }
+
+    // The sums of W published warps (those that are not there hold 0).
+    template <int V, int W>
+    __device__ __forceinline__ void add_warps(float (&v)[V], const float* slot) {
+        float r[W * V];
+#pragma unroll
+        for (int i = 0; i < W * V; i += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(slot + i);
+            r[i] = q.x;
+            r[i + 1] = q.y;
+            r[i + 2] = q.z;
+            r[i + 3] = q.w;
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[k] = r[k];
+#pragma unroll
+        for (int i = V; i < W * V; ++i) v[i % V] += r[i];
     }
 
     template <int V, int LANES>
@@ -275,26 +306,20 @@ struct GroupSums {
         for (int s = kPer / 2; s >= 1; s /= 2) a += __shfl_xor_sync(0xffffffffu, a, s);
         if constexpr (LANES == 32) {
             if (tpr > 32) {
-                float* slot = buf + par * 8 * kMaxWarpsPerRow + lane / kPer * kMaxWarpsPerRow;
+                float* slot = buf + par * 4 * kMaxWarpsPerRow;
                 par ^= 1;
-                if (lane % kPer == 0) slot[t / 32] = a;
+                if (lane % kPer == 0) slot[t / 32 * V + lane / kPer] = a;
                 named_bar(bar_id, tpr);
-                constexpr int W = kMaxWarpsPerRow / kPer;  // warps' sums that a lane adds
-                a = 0.0f;
-                if constexpr (W == 0) {
-                    if (lane % kPer < kMaxWarpsPerRow) a = slot[lane % kPer];
-                } else {
-#pragma unroll
-                    for (int w = 0; w < W; ++w) a += slot[lane % kPer * W + w];
-                }
-#pragma unroll
-                for (int s = kPer / 2; s >= 1; s /= 2) a += __shfl_xor_sync(0xffffffffu, a, s);
+                if (tpr <= 128) add_warps<V, 4>(v, slot);
+                else if (tpr <= 256) add_warps<V, 8>(v, slot);
+                else add_warps<V, 16>(v, slot);
+                return;
             }
         }
 #pragma unroll
         for (int k = 0; k < V; ++k) v[k] = __shfl_sync(0xffffffffu, a, k * kPer, LANES);
     }
 };
-constexpr int kSumFloats = 2 * 8 * kMaxWarpsPerRow;  // of one group
+constexpr int kSumFloats = 2 * 4 * kMaxWarpsPerRow;  // of one group
 
 }  // namespace mbx
