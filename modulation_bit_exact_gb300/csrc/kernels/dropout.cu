@@ -15,219 +15,301 @@
 // A dropped element contributes nothing: it is selected away, so an infinity
 // or a NaN in its y or gate does not reach an output.  binary32 throughout,
 // one rounding at each output.
-#include "rowgroup.cuh"
+#include "rowring.cuh"
 
 namespace mbx {
 
-struct PhiloxKey {
-    uint32_t k0, k1, c2, c3;
+// The generator's key schedule and the upper counter words, the same for a
+// whole call.
+struct Philox {
+    uint32_t k0[10], k1[10], c2, c3;
+    __device__ __forceinline__ explicit Philox(const DropParams& p) {
+        const uint64_t seed = (uint64_t)p.rng[0], ctr = (uint64_t)p.rng[1] + (uint64_t)p.offset;
+        c2 = (uint32_t)ctr;
+        c3 = (uint32_t)(ctr >> 32);
+#pragma unroll
+        for (int r = 0; r < 10; ++r) {
+            k0[r] = (uint32_t)seed + r * 0x9E3779B9u;
+            k1[r] = (uint32_t)(seed >> 32) + r * 0xBB67AE85u;
+            // kept in registers: formed again at every use they would be a
+            // third of the generator's instructions
+            asm volatile("" : "+r"(k0[r]), "+r"(k1[r]));
+        }
+    }
+    __device__ __forceinline__ uint4 operator()(uint32_t quad, uint32_t row) const {
+        uint32_t w0 = quad, w1 = row, w2 = c2, w3 = c3;
+#pragma unroll
+        for (int r = 0; r < 10; ++r) {
+            const uint64_t a = (uint64_t)0xD2511F53u * w0, b = (uint64_t)0xCD9E8D57u * w2;
+            w0 = (uint32_t)(b >> 32) ^ w1 ^ k0[r];
+            w1 = (uint32_t)b;
+            w2 = (uint32_t)(a >> 32) ^ w3 ^ k1[r];
+            w3 = (uint32_t)a;
+        }
+        return make_uint4(w0, w1, w2, w3);
+    }
 };
 
-__device__ __forceinline__ PhiloxKey philox_key(const DropParams& p) {
-    const uint64_t seed = (uint64_t)p.rng[0], ctr = (uint64_t)p.rng[1] + (uint64_t)p.offset;
-    return PhiloxKey{(uint32_t)seed, (uint32_t)(seed >> 32), (uint32_t)ctr, (uint32_t)(ctr >> 32)};
-}
-
-__device__ __forceinline__ uint4 philox(uint32_t quad, uint32_t row, const PhiloxKey& key) {
-    uint32_t c0 = quad, c1 = row, c2 = key.c2, c3 = key.c3, k0 = key.k0, k1 = key.k1;
-#pragma unroll
-    for (int r = 0; r < 10; ++r) {
-        const uint64_t a = (uint64_t)0xD2511F53u * c0, b = (uint64_t)0xCD9E8D57u * c2;
-        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
-        c1 = (uint32_t)b;
-        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
-        c3 = (uint32_t)a;
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
-    }
-    return make_uint4(c0, c1, c2, c3);
-}
-
-// Bit e of the result: whether this thread's element e of the row is kept.
-// Elements come in fours that share a counter.
-template <class T, int NCH, Access A>
-__device__ __forceinline__ uint32_t keep_bits(const PhiloxKey& key, uint32_t row, uint32_t threshold, int t, int tpr) {
-    constexpr int E = NCH * ChunkOf<T>::CE;
+// The quad (column / 4) of this thread's elements e .. e+3.
+template <int CE, Access A>
+__device__ __forceinline__ uint32_t quad_of(int e, const Lane& L) {
     static_assert(A != kScalar, "four columns of a thread are consecutive");
-    uint32_t bits = 0;
-#pragma unroll
-    for (int e = 0; e < E; e += 4) {
-        const uint4 w = philox((uint32_t)col_of<T, A>(e, t, tpr) / 4u, row, key);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) bits |= (w_of(w, i) >= threshold ? 1u : 0u) << (e + i);
-    }
-    return bits;
+    return A == kVec && CE == 8 ? (uint32_t)(e / 8 * L.tpr + L.t) * 2 + e % 8 / 4 : (uint32_t)(e / 4 * L.tpr + L.t);
 }
 
-// GATED: out = x + gate * drop(y); otherwise out = drop(x).
+// v where the element is kept, else `dropped`.
+__device__ __forceinline__ u64 keep_pair(u64 v, uint32_t a, uint32_t b, uint32_t threshold, float dropped) {
+    return f2(a >= threshold ? f2lo(v) : dropped, b >= threshold ? f2hi(v) : dropped);
+}
+
+// GATED: out = x + gate * drop(y); otherwise out = drop(x).  Rows stream
+// through a ring (rowring.cuh); no thread waits for another.
 template <class T, int NCH, Access A, bool GATED>
-__global__ void __launch_bounds__(512) dropout_kernel(DropParams p) {
-    constexpr int E = NCH * ChunkOf<T>::CE;
-    const int tpr = p.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr, groups = blockDim.x / tpr;
+__global__ void __launch_bounds__(kRingThreads) dropout_kernel(DropParams p, RingShape sh) {
+    constexpr int CE = ChunkOf<T>::CE, H = CE / 2, P = NCH * H;
+    extern __shared__ __align__(16) char smem[];
+    const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr;
+    const Lane L = make_lane<16, CE, A>(t, tpr, p.D);
+    char* ring = smem + g * sh.group_bytes;
     grid_dep_wait();  // launched programmatically: the previous kernel has finished
     grid_dep_launch();
-    const PhiloxKey key = philox_key(p);
-    const int64_t step = (int64_t)gridDim.x * groups;
-    float gate[E];
-    int64_t seg = -1;
-    for (int64_t row = (int64_t)blockIdx.x * groups + g; row < p.rows; row += step) {
-        RawRow<T, NCH, A> rx, ry;
-        rx.load(static_cast<const T*>(p.x) + row * p.x_stride, p.D, t, tpr);
+    const Philox philox(p);
+    const int row_bytes = sh.row_bytes, stage_bytes = (GATED ? 2 : 1) * row_bytes, c0 = first_col<CE, A>(L);
+    const int64_t step = (int64_t)gridDim.x * sh.groups;
+    int64_t row = (int64_t)blockIdx.x * sh.groups + g, fill_row = row;
+    auto fill = [&](int st) {
+        char* dst = ring + st * stage_bytes;
+        if (fill_row < p.rows) {
+            ring_fill<T, NCH, CE, A>(dst, static_cast<const T*>(p.x) + fill_row * p.x_stride + c0, L);
+            if constexpr (GATED)
+                ring_fill<T, NCH, CE, A>(dst + row_bytes, static_cast<const T*>(p.y) + fill_row * p.y_stride + c0, L);
+        }
+        fill_row += step;
+        ring_commit();
+    };
+    for (int i = 0; i < sh.stages; ++i) fill(i);
+    u64 gate[GATED ? P : 1];  // gate / (1-p)
+    int64_t seg_end = 0;  // the rows below it share the gate that is loaded
+    int stage = 0;
+    const u64 inv = f2(p.inv_keep, p.inv_keep);
+    for (; row < p.rows; row += step) {
         if constexpr (GATED) {
-            ry.load(static_cast<const T*>(p.y) + row * p.y_stride, p.D, t, tpr);
-            const int64_t m = p.seq == 1 ? row : row / p.seq;
-            if (m != seg) load_params<T, NCH, A>(gate, p.gate, m * p.gate_stride, p.p_f32, p.D, t, tpr, 0.0f);
-            seg = m;
-        }
-        const uint32_t keep = keep_bits<T, NCH, A>(key, (uint32_t)row, p.threshold, t, tpr);
-        float v[E];
-        rx.widen(v);
-        if constexpr (GATED) {
-            float y[E];
-            ry.widen(y);
+            if (row >= seg_end) {
+                const int64_t m = p.mod_rows == p.rows ? row : row / p.seq;
+                seg_end = (m + 1) * p.seq;
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (keep >> e & 1) v[e] = fmaf(gate[e], y[e] * p.inv_keep, v[e]);
-        } else {
+                for (int j = 0; j < NCH; ++j) {
+                    u64 c[H];
+                    get_param_chunk<T, CE, A>(c, p.gate, m * p.gate_stride + c0, p.p_f32, j, L);
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = (keep >> e & 1) ? v[e] * p.inv_keep : 0.0f;
-        }
-        store_row<T, NCH, A>(static_cast<T*>(p.out) + row * p.out_stride, v, p.D, t, tpr);
-    }
-}
-
-// One gate row for every row: dgate is a row too.
-template <class T, int NCH, Access A>
-__global__ void __launch_bounds__(512) dropout_backward_token_kernel(DropParams p) {
-    constexpr int E = NCH * ChunkOf<T>::CE;
-    const int tpr = p.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr, groups = blockDim.x / tpr;
-    grid_dep_wait();
-    grid_dep_launch();
-    const PhiloxKey key = philox_key(p);
-    const int64_t step = (int64_t)gridDim.x * groups;
-    for (int64_t row = (int64_t)blockIdx.x * groups + g; row < p.rows; row += step) {
-        RawRow<T, NCH, A> rd, ry;
-        rd.load(static_cast<const T*>(p.x) + row * p.x_stride, p.D, t, tpr);
-        ry.load(static_cast<const T*>(p.y) + row * p.y_stride, p.D, t, tpr);
-        float gate[E], d[E], y[E];
-        load_params<T, NCH, A>(gate, p.gate, row * p.gate_stride, p.p_f32, p.D, t, tpr, 0.0f);
-        const uint32_t keep = keep_bits<T, NCH, A>(key, (uint32_t)row, p.threshold, t, tpr);
-        rd.widen(d);
-        ry.widen(y);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float k = d[e] * p.inv_keep;
-            d[e] = (keep >> e & 1) ? k * gate[e] : 0.0f;
-            y[e] = (keep >> e & 1) ? k * y[e] : 0.0f;
-        }
-        store_row<T, NCH, A>(static_cast<T*>(p.out) + row * p.out_stride, d, p.D, t, tpr);
-        if (p.dgate) store_params<T, NCH, A>(p.dgate, row * p.dgate_stride, p.p_f32, y, p.D, t, tpr);
-    }
-}
-
-// Gate rows shared by seq rows: the parts of a segment as in the gradients of
-// LayerNorm's parameters (layernorm.cu).
-template <class T, int NCH, Access A>
-__global__ void __launch_bounds__(512) dropout_backward_kernel(DropParams p) {
-    constexpr int E = NCH * ChunkOf<T>::CE;
-    extern __shared__ float acc_smem[];  // [E][block]
-    const int tpr = p.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr, groups = blockDim.x / tpr;
-    grid_dep_wait();
-    grid_dep_launch();
-    const PhiloxKey key = philox_key(p);
-    const int64_t units = p.mod_rows * p.plan.parts;
-    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const int64_t seg = unit / p.plan.parts, part = unit - seg * p.plan.parts;
-        const int64_t r0 = seg * p.seq + part * p.plan.rows_per_part;
-        int64_t r1 = r0 + p.plan.rows_per_part;
-        if (r1 > (seg + 1) * p.seq) r1 = (seg + 1) * p.seq;
-        float gate[E], acc[E];
-        load_params<T, NCH, A>(gate, p.gate, seg * p.gate_stride, p.p_f32, p.D, t, tpr, 0.0f);
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-        for (int64_t row = r0 + g; row < r1; row += groups) {
-            RawRow<T, NCH, A> rd, ry;
-            rd.load(static_cast<const T*>(p.x) + row * p.x_stride, p.D, t, tpr);
-            ry.load(static_cast<const T*>(p.y) + row * p.y_stride, p.D, t, tpr);
-            const uint32_t keep = keep_bits<T, NCH, A>(key, (uint32_t)row, p.threshold, t, tpr);
-            float d[E], y[E];
-            rd.widen(d);
-            ry.widen(y);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float k = d[e] * p.inv_keep;
-                d[e] = (keep >> e & 1) ? k * gate[e] : 0.0f;
-                if (keep >> e & 1) acc[e] = fmaf(k, y[e], acc[e]);
+                    for (int i = 0; i < H; ++i) gate[j * H + i] = mul2(c[i], inv);
+                }
             }
-            store_row<T, NCH, A>(static_cast<T*>(p.out) + row * p.out_stride, d, p.D, t, tpr);
         }
-        if (p.dgate == nullptr) continue;
-        if (groups > 1) {
-            const int n = blockDim.x;
+        ring_wait(sh.stages);
+        uint4 xr[NCH], yr[GATED ? NCH : 1];
+        read_pieces<T, NCH, A>(xr, ring + stage * stage_bytes, L);
+        if constexpr (GATED) read_pieces<T, NCH, A>(yr, ring + stage * stage_bytes + row_bytes, L);
+        fill(stage);
+        if (++stage == sh.stages) stage = 0;
+        T* dst = static_cast<T*>(p.out) + row * p.out_stride + c0;
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc_smem[e * n + threadIdx.x] = acc[e];
-            __syncthreads();
+        for (int j = 0; j < NCH; ++j) {
+            u64 o[H];
+#pragma unroll
+            for (int i = 0; i < H; i += 2) {
+                const int e = j * H + i;
+                const uint4 w = philox(quad_of<CE, A>(2 * e, L), (uint32_t)row);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t w0 = h ? w.z : w.x, w1 = h ? w.w : w.y;
+                    const u64 x = piece_pair<T>(xr, e + h);
+                    if constexpr (GATED)  // -0 leaves every x as it is
+                        o[i + h] = add2(x, keep_pair(mul2(piece_pair<T>(yr, e + h), gate[e + h]), w0, w1, p.threshold, -0.0f));
+                    else o[i + h] = keep_pair(mul2(x, inv), w0, w1, p.threshold, 0.0f);
+                }
+            }
+            if (has_chunk<A>(j, L)) put_chunk<T, CE, A>(dst, o, j, L);
+        }
+    }
+}
+
+// The gradients.  TOKEN: one gate row for every row, and dgate is a row too.
+// Otherwise the parts of a segment as in the gradients of LayerNorm's
+// parameters (layernorm_bwd.cu): every thread sums its own columns.
+template <class T, int NCH, Access A, bool TOKEN>
+__global__ void __launch_bounds__(kGradThreads) dropout_backward_kernel(DropParams p, RingShape sh) {
+    constexpr int CE = ChunkOf<T>::CE, H = CE / 2, P = NCH * H;
+    extern __shared__ __align__(16) char smem[];
+    const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr, groups = sh.groups;
+    const Lane L = make_lane<16, CE, A>(t, tpr, p.D);
+    char* ring = smem + g * sh.group_bytes;
+    grid_dep_wait();
+    grid_dep_launch();
+    const Philox philox(p);
+    const int row_bytes = sh.row_bytes, stage_bytes = 2 * row_bytes, c0 = first_col<CE, A>(L);
+    const u64 inv = f2(p.inv_keep, p.inv_keep);
+    const int64_t units = TOKEN ? 1 : p.mod_rows * p.plan.parts;
+    for (int64_t unit = TOKEN ? 0 : blockIdx.x; unit < units; unit += gridDim.x) {
+        int64_t seg = 0, row, end, step;
+        if constexpr (TOKEN) {
+            row = (int64_t)blockIdx.x * groups + g;
+            end = p.rows;
+            step = (int64_t)gridDim.x * groups;
+        } else {
+            seg = unit / p.plan.parts;
+            const int64_t r0 = seg * p.seq + (unit - seg * p.plan.parts) * p.plan.rows_per_part;
+            end = min(r0 + p.plan.rows_per_part, (seg + 1) * p.seq);
+            row = r0 + g;
+            step = groups;
+        }
+        int64_t fill_row = row;
+        auto fill = [&](int st) {
+            char* dst = ring + st * stage_bytes;
+            if (fill_row < end) {
+                ring_fill<T, NCH, CE, A>(dst, static_cast<const T*>(p.x) + fill_row * p.x_stride + c0, L);
+                ring_fill<T, NCH, CE, A>(dst + row_bytes, static_cast<const T*>(p.y) + fill_row * p.y_stride + c0, L);
+            }
+            fill_row += step;
+            ring_commit();
+        };
+        for (int i = 0; i < sh.stages; ++i) fill(i);
+        u64 gate[P], acc[P];
+        auto load_gate = [&](int64_t m) {
+#pragma unroll
+            for (int j = 0; j < NCH; ++j) {
+                u64 c[H];
+                get_param_chunk<T, CE, A>(c, p.gate, m * p.gate_stride + c0, p.p_f32, j, L);
+#pragma unroll
+                for (int i = 0; i < H; ++i) gate[j * H + i] = mul2(c[i], inv);
+            }
+        };
+        if constexpr (!TOKEN) {
+            load_gate(seg);
+#pragma unroll
+            for (int e = 0; e < P; ++e) acc[e] = 0;
+        }
+        int stage = 0;
+        for (; row < end; row += step) {
+            if constexpr (TOKEN) load_gate(row);
+            ring_wait(sh.stages);
+            uint4 dr[NCH], yr[NCH];
+            read_pieces<T, NCH, A>(dr, ring + stage * stage_bytes, L);
+            read_pieces<T, NCH, A>(yr, ring + stage * stage_bytes + row_bytes, L);
+            fill(stage);
+            if (++stage == sh.stages) stage = 0;
+            T* dst = static_cast<T*>(p.out) + row * p.out_stride + c0;
+#pragma unroll
+            for (int j = 0; j < NCH; ++j) {
+                u64 o[H], og[H];
+#pragma unroll
+                for (int i = 0; i < H; i += 2) {
+                    const int e = j * H + i;
+                    const uint4 w = philox(quad_of<CE, A>(2 * e, L), (uint32_t)row);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t w0 = h ? w.z : w.x, w1 = h ? w.w : w.y;
+                        const u64 d = piece_pair<T>(dr, e + h);
+                        o[i + h] = keep_pair(mul2(d, gate[e + h]), w0, w1, p.threshold, 0.0f);
+                        og[i + h] = keep_pair(mul2(d, piece_pair<T>(yr, e + h)), w0, w1, p.threshold, 0.0f);
+                        if constexpr (!TOKEN) acc[e + h] = add2(acc[e + h], og[i + h]);
+                        else og[i + h] = mul2(og[i + h], inv);
+                    }
+                }
+                if (!has_chunk<A>(j, L)) continue;
+                put_chunk<T, CE, A>(dst, o, j, L);
+                if constexpr (TOKEN)
+                    if (p.dgate) put_param_chunk<T, CE, A>(p.dgate, row * p.dgate_stride + c0, p.p_f32, og, j, L);
+            }
+        }
+        if constexpr (!TOKEN) {
+            if (p.dgate == nullptr) continue;
+            if (groups > 1) {
+                u64* sums = reinterpret_cast<u64*>(smem);  // [P][block], in the place of the drained ring
+                const int n = groups * tpr;
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < P; ++e) sums[e * n + threadIdx.x] = acc[e];
+                __syncthreads();
+                if (g == 0) {
+#pragma unroll
+                    for (int e = 0; e < P; ++e)
+                        for (int k = 1; k < groups; ++k) acc[e] = add2(acc[e], sums[e * n + k * tpr + t]);
+                }
+                __syncthreads();
+            }
             if (g == 0) {
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    for (int k = 1; k < groups; ++k) acc[e] += acc_smem[e * n + k * tpr + t];
+                for (int j = 0; j < NCH; ++j) {
+                    if (!has_chunk<A>(j, L)) continue;
+                    u64 c[H];
+#pragma unroll
+                    for (int i = 0; i < H; ++i) c[i] = mul2(acc[j * H + i], inv);
+                    if (p.plan.parts == 1)
+                        put_param_chunk<T, CE, A>(p.dgate, seg * p.dgate_stride + c0, p.p_f32, c, j, L);
+                    else put_chunk<float, CE, A>(p.ws + unit * p.D + c0, c, j, L);
+                }
             }
-            __syncthreads();
-        }
-        if (g == 0) {
-            if (p.plan.parts == 1)
-                store_params<T, NCH, A>(p.dgate, seg * p.dgate_stride, p.p_f32, acc, p.D, t, tpr);
-            else store_params<T, NCH, A>(p.ws, unit * p.D, true, acc, p.D, t, tpr);
         }
     }
 }
 
 // ---------------------------------------------------------------- launch
 
+template <class T, int NCH, Access A, bool GATED>
+static cudaError_t drop_fwd(const DropParams& p, cudaStream_t s) {
+    auto k = dropout_kernel<T, NCH, A, GATED>;
+    const int tpr = row_threads(p.D);
+    RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, GATED ? 2 : 1, 0, 0, kRingThreads);
+    sh.smem -= sh.sums_bytes;  // no row sums
+    static SmemOptIn opt_in;
+    if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
+    const int64_t need = (p.rows + sh.groups - 1) / sh.groups, most = (int64_t)sm_count() * sh.ctas_per_sm;
+    return launch_pdl(k, (unsigned)(need < most ? need : most), sh.groups * tpr, sh.smem, s, p, sh);
+}
+
 template <class T, int NCH>
-static cudaError_t drop_fwd(const DropParams& p0, bool vec, cudaStream_t s) {
-    DropParams p = p0;
-    p.tpr = row_threads(p.D);
-    if (p.tpr < 32) p.tpr = 32;
-    p.groups = p.tpr >= 256 ? 1 : 256 / p.tpr;
-    const int block = p.tpr * p.groups;
-    auto k = p.gate ? (vec ? dropout_kernel<T, NCH, kVec, true> : dropout_kernel<T, NCH, kQuad, true>)
-                    : (vec ? dropout_kernel<T, NCH, kVec, false> : dropout_kernel<T, NCH, kQuad, false>);
-    const int grid = grid_for_rows(reinterpret_cast<const void*>(k), p.rows, p.groups, block);
-    if (grid < 0) return cudaErrorUnknown;
-    return launch_pdl(k, grid, block, 0, s, p);
+static cudaError_t drop_fwd_any(const DropParams& p, bool vec, cudaStream_t s) {
+    if (vec) return p.gate ? drop_fwd<T, NCH, kVec, true>(p, s) : drop_fwd<T, NCH, kVec, false>(p, s);
+    return p.gate ? drop_fwd<T, NCH, kQuad, true>(p, s) : drop_fwd<T, NCH, kQuad, false>(p, s);
 }
 
 cudaError_t launch_dropout(const DropParams& p, bool f32, bool vec, cudaStream_t s) {
-    return f32 ? drop_fwd<float, 4>(p, vec, s) : drop_fwd<uint16_t, 2>(p, vec, s);
+    return f32 ? drop_fwd_any<float, 4>(p, vec, s) : drop_fwd_any<uint16_t, 2>(p, vec, s);
+}
+
+template <class T, int NCH, Access A, bool TOKEN>
+static cudaError_t drop_bwd(const DropParams& p0, cudaStream_t s) {
+    DropParams p = p0;
+    auto k = dropout_backward_kernel<T, NCH, A, TOKEN>;
+    const int tpr = row_threads(p.D);
+    RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, 2, 0, 0, kGradThreads);
+    sh.smem -= sh.sums_bytes;
+    static SmemOptIn opt_in;
+    if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
+    if constexpr (TOKEN) {
+        const int64_t need = (p.rows + sh.groups - 1) / sh.groups, most = (int64_t)sm_count() * sh.ctas_per_sm;
+        return launch_pdl(k, (unsigned)(need < most ? need : most), sh.groups * tpr, sh.smem, s, p, sh);
+    } else {
+        p.plan = grad_plan(p.rows, p.mod_rows, p.D, (int)sizeof(T));
+        const int64_t units = p.mod_rows * p.plan.parts, most = 1 << 30;
+        const cudaError_t e = launch_pdl(k, (unsigned)(units < most ? units : most), sh.groups * tpr, sh.smem, s, p, sh);
+        if (e != cudaSuccess || p.plan.parts == 1 || !p.dgate) return e;
+        ColSumParams c{p.ws, p.plan.parts, p.mod_rows, p.D, 1, {p.dgate, nullptr}, {p.dgate_stride, 0}, p.p_f32};
+        return launch_column_sums(c, s);
+    }
 }
 
 template <class T, int NCH>
-static cudaError_t drop_bwd(const DropParams& p0, bool vec, cudaStream_t s) {
-    DropParams p = p0;
-    p.tpr = row_threads(p.D);
-    if (p.tpr < 32) p.tpr = 32;
-    p.groups = p.tpr >= 256 ? 1 : 256 / p.tpr;
-    const int block = p.tpr * p.groups;
-    if (p.seq == 1) {
-        auto k = vec ? dropout_backward_token_kernel<T, NCH, kVec> : dropout_backward_token_kernel<T, NCH, kQuad>;
-        const int grid = grid_for_rows(reinterpret_cast<const void*>(k), p.rows, p.groups, block);
-        if (grid < 0) return cudaErrorUnknown;
-        return launch_pdl(k, grid, block, 0, s, p);
-    }
-    p.plan = grad_plan(p.rows, p.mod_rows, p.D, (int)sizeof(T));
-    const size_t smem = p.groups > 1 ? (size_t)block * 16 * sizeof(float) : 0;
-    const int64_t units = p.mod_rows * p.plan.parts;
-    auto k = vec ? dropout_backward_kernel<T, NCH, kVec> : dropout_backward_kernel<T, NCH, kQuad>;
-    cudaError_t e = launch_pdl(k, (unsigned)(units < (1 << 30) ? units : (1 << 30)), block, smem, s, p);
-    if (e != cudaSuccess || p.plan.parts == 1 || !p.dgate) return e;
-    ColSumParams c{p.ws, p.plan.parts, p.mod_rows, p.D, 1, {p.dgate, nullptr}, {p.dgate_stride, 0}, p.p_f32};
-    return launch_column_sums(c, s);
+static cudaError_t drop_bwd_any(const DropParams& p, bool vec, cudaStream_t s) {
+    if (p.seq == 1) return vec ? drop_bwd<T, NCH, kVec, true>(p, s) : drop_bwd<T, NCH, kQuad, true>(p, s);
+    return vec ? drop_bwd<T, NCH, kVec, false>(p, s) : drop_bwd<T, NCH, kQuad, false>(p, s);
 }
 
 cudaError_t launch_dropout_backward(const DropParams& p, bool f32, bool vec, cudaStream_t s) {
     return launch_all_or_none([&] {
-        return f32 ? drop_bwd<float, 4>(p, vec, s) : drop_bwd<uint16_t, 2>(p, vec, s);
+        return f32 ? drop_bwd_any<float, 4>(p, vec, s) : drop_bwd_any<uint16_t, 2>(p, vec, s);
     });
 }
 

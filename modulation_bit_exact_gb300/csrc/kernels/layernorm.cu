@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
     constexpr int CE = ChunkOf<T>::CE, P = NCH * CE / 2;
     extern __shared__ __align__(16) char smem[];
     const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr;
-    const Lane L = make_lane<CE, A>(t, tpr, p.D);
+    const Lane L = make_lane<16, CE, A>(t, tpr, p.D);
     GroupSums sums = group_sums(smem, sh, g, t);
     char* ring = smem + sh.sums_bytes + sh.fixed_bytes + g * sh.group_bytes;
     const float inv_d = 1.0f / (float)p.D;

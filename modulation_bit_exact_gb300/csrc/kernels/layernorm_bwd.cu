@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
     constexpr int kF = RES ? 3 : 2;  // a stage: x, dy, the residual's gradient, the factor
     extern __shared__ __align__(16) char smem[];
     const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr;
-    const Lane L = make_lane<CE, A>(t, tpr, p.D);
+    const Lane L = make_lane<16, CE, A>(t, tpr, p.D);
     GroupSums sums = group_sums(smem, sh, g, t);
     char* ring = smem + sh.sums_bytes + sh.fixed_bytes + g * sh.group_bytes;
     const float inv_d = 1.0f / (float)p.D;
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
     constexpr int CE = ChunkOf<T>::CE, H = CE / 2, P = NCH * H;
     extern __shared__ __align__(16) char smem[];
     const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr, groups = sh.groups;
-    const Lane L = make_lane<CE, A>(t, tpr, p.D);
+    const Lane L = make_lane<16, CE, A>(t, tpr, p.D);
     GroupSums sums = group_sums(smem, sh, g, t);
     // the factor lives in shared memory, each thread's own copy, so that x, dy
     // and the two sums of every column fit in registers

@@ -10,7 +10,8 @@
 // pieces.  kScalar (a width that is no multiple of CE, or a row that starts at
 // no 16-byte boundary): element e is column e*tpr + t, moved one at a time
 // (binary32 by 4-byte cp.async; bfloat16, which cp.async does not move alone,
-// by a load and a shared store).
+// by a load and a shared store).  kQuad is kScalar with four consecutive
+// columns of a thread at a time, which share one call of the dropout generator.
 #pragma once
 
 #include "rowgroup.cuh"
@@ -39,17 +40,28 @@ __device__ __forceinline__ void ring_wait(int stages) {
 // This thread's place in its row group and the columns that it owns.
 struct Lane {
     int t, tpr;
-    int nv;  // kVec: chunks that exist; kScalar: elements that exist
+    int nv;  // kVec: chunks that exist; else elements that exist
 };
-template <int CE, Access A>
+template <int E, int CE, Access A>
 __device__ __forceinline__ Lane make_lane(int t, int tpr, int D) {
-    const int units = A == kVec ? D / CE : D;
-    return Lane{t, tpr, units > t ? (units - t + tpr - 1) / tpr : 0};
+    int nv = 0;
+    if constexpr (A == kQuad) {
+#pragma unroll
+        for (int q = 0; q < E / 4; ++q) nv += min(max(D - (q * tpr + t) * 4, 0), 4);
+    } else {
+        const int units = A == kVec ? D / CE : D;
+        nv = units > t ? (units - t + tpr - 1) / tpr : 0;
+    }
+    return Lane{t, tpr, nv};
 }
-// This thread's first column.
+// This thread's first column, and how far element e lies beyond it.
 template <int CE, Access A>
 __device__ __forceinline__ int first_col(const Lane& L) {
-    return A == kVec ? L.t * CE : L.t;
+    return A == kVec ? L.t * CE : A == kQuad ? L.t * 4 : L.t;
+}
+template <Access A>
+__device__ __forceinline__ int elem_off(int e, const Lane& L) {
+    return A == kQuad ? e / 4 * L.tpr * 4 + e % 4 : e * L.tpr;
 }
 
 // Start the copy of this thread's part of a row to its place in a stage; `row`
@@ -70,8 +82,8 @@ __device__ __forceinline__ void ring_fill(char* dst, const Q* row, const Lane& L
         for (int e = 0; e < NCH * CE; ++e) {
             const int c = e * L.tpr + L.t;
             if (e < L.nv) {
-                if constexpr (sizeof(Q) == 4) ring_cp4(dst + c * 4, row + e * L.tpr);
-                else reinterpret_cast<Q*>(dst)[c] = ld_u16_rw(row + e * L.tpr);
+                if constexpr (sizeof(Q) == 4) ring_cp4(dst + c * 4, row + elem_off<A>(e, L));
+                else reinterpret_cast<Q*>(dst)[c] = ld_u16_rw(row + elem_off<A>(e, L));
             }
         }
     }
@@ -197,7 +209,7 @@ __device__ __forceinline__ void put_chunk(Q* row, const u64 (&p)[CE / 2], int j,
 #pragma unroll
         for (int i = 0; i < CE; ++i) {
             const int e = j * CE + i;
-            if (e < L.nv) store_elem(row + e * L.tpr, i % 2 ? f2hi(p[i / 2]) : f2lo(p[i / 2]));
+            if (e < L.nv) store_elem(row + elem_off<A>(e, L), i % 2 ? f2hi(p[i / 2]) : f2lo(p[i / 2]));
         }
     }
 }
@@ -236,8 +248,8 @@ __device__ __forceinline__ void get_chunk(u64 (&p)[CE / 2], const Q* row, int j,
 #pragma unroll
         for (int i = 0; i < CE; i += 2) {
             const int e = j * CE + i;
-            p[i / 2] = f2(e < L.nv ? load_elem(row + e * L.tpr) : 0.0f,
-                          e + 1 < L.nv ? load_elem(row + (e + 1) * L.tpr) : 0.0f);
+            p[i / 2] = f2(e < L.nv ? load_elem(row + elem_off<A>(e, L)) : 0.0f,
+                          e + 1 < L.nv ? load_elem(row + elem_off<A>(e + 1, L)) : 0.0f);
         }
     }
 }

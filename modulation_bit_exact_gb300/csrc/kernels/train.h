@@ -105,9 +105,7 @@ struct DropParams {
     int64_t rows, mod_rows, seq;
     int D;
     float* ws;
-    // filled by the launcher
-    GradPlan plan;
-    int tpr, groups;
+    GradPlan plan;  // filled by the launcher
 };
 
 // out[k][s][c] = sum over the parts of ws[s][part][k][c], k < nacc.
