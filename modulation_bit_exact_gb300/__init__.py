@@ -17,6 +17,7 @@ library rejects (MBX_E_STRIDE).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -496,21 +497,29 @@ def qk_norm_rope_qkv_epilogue(txt_qkv, img_qkv, batch: int, heads: int, head_dim
 # ---------------------------------------------------------------- training path
 
 
+# A ctypes structure passes for a pointer to it.
+
+
 def _opt(t):
-    return None if t is None else ctypes.byref(_view(t))
+    return None if t is None else _view(t)
+
+
+def _like(t):
+    """An uninitialised tensor of t's shape and dtype with flat rows."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None):
     """Affine LayerNorm over the last dimension (see mbx_layer_norm): x
     bfloat16 or float32, weight and bias [D] of x's dtype or float32, or None."""
     L = _load()
-    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-    _raise(L.mbx_layer_norm(_ref(_view(out)), _ref(_view(x)), _opt(weight), _opt(bias), eps, _stream(x)))
+    out = _like(x) if out is None else out
+    _raise(L.mbx_layer_norm(_view(out), _view(x), _opt(weight), _opt(bias), eps, _stream(x)))
     return out
 
 
 def check_layer_norm(out, x, weight=None, bias=None, eps=1e-6) -> int:
-    return _load().mbx_check_layer_norm(_ref(_view(out)), _ref(_view(x)), _opt(weight), _opt(bias), eps)
+    return _load().mbx_check_layer_norm(_view(out), _view(x), _opt(weight), _opt(bias), eps)
 
 
 def param_grad_workspace(rows: int, cols: int, mod_rows: int, dtype: torch.dtype) -> int:
@@ -522,18 +531,26 @@ def param_grad_workspace(rows: int, cols: int, mod_rows: int, dtype: torch.dtype
     return n.value
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace_floats(rows: int, cols: int, mod_rows: int, dtype: torch.dtype, device: int) -> int:
+    try:
+        with torch.cuda.device(device):
+            return param_grad_workspace(rows, cols, mod_rows, dtype) // 4
+    except MbxError:
+        return 0  # the call itself is refused
+
+
 def _workspace(x, params):
     """A workspace for the gradient of `params` summed over x's rows, or None."""
-    if not x.is_cuda or x.numel() == 0 or params.numel() == 0:
-        return None  # the call itself is refused
+    n = x.numel()
+    if not n or not x.is_cuda:
+        return None
     cols = x.shape[-1]
-    rows, mod_rows = x.numel() // cols, params.numel() // cols
-    if mod_rows == 0 or rows == mod_rows:
+    rows, mod_rows = n // cols, params.numel() // cols
+    if rows == mod_rows:
         return None
-    n = ctypes.c_int64()
-    if _load().mbx_param_grad_workspace(rows, cols, mod_rows, _DTYPES.get(x.dtype, 0), ctypes.byref(n)) != 0:
-        return None
-    return torch.empty(n.value // 4, dtype=torch.float32, device=x.device) if n.value else None
+    floats = _workspace_floats(rows, cols, mod_rows, x.dtype, x.get_device())
+    return torch.empty(floats, dtype=torch.float32, device=x.device) if floats else None
 
 
 def _ws_args(ws):
@@ -546,13 +563,13 @@ def layer_norm_backward(dout, x, weight=None, eps: float = 1e-6, dresidual=None,
     dbias), the last two None without a weight.  ``dresidual`` is added to dx,
     and ``dx=dresidual`` updates it in place."""
     L = _load()
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx is None else dx
+    dx = _like(x) if dx is None else dx
     ws = None
     if weight is not None:
-        dweight = torch.empty(weight.shape, dtype=weight.dtype, device=weight.device) if dweight is None else dweight
-        dbias = torch.empty(weight.shape, dtype=weight.dtype, device=weight.device) if dbias is None else dbias
+        dweight = _like(weight) if dweight is None else dweight
+        dbias = _like(weight) if dbias is None else dbias
         ws = _workspace(x, weight)
-    _raise(L.mbx_layer_norm_backward(_ref(_view(dx)), _opt(dweight), _opt(dbias), _ref(_view(dout)), _ref(_view(x)),
+    _raise(L.mbx_layer_norm_backward(_view(dx), _opt(dweight), _opt(dbias), _view(dout), _view(x),
                                      _opt(weight), _opt(dresidual), eps, *_ws_args(ws), _stream(x)))
     return dx, dweight, dbias
 
@@ -560,7 +577,7 @@ def layer_norm_backward(dout, x, weight=None, eps: float = 1e-6, dresidual=None,
 def check_layer_norm_backward(dx, dweight, dbias, dout, x, weight=None, eps=1e-6, dresidual=None,
                               workspace=None) -> int:
     return _load().mbx_check_layer_norm_backward(
-        _ref(_view(dx)), _opt(dweight), _opt(dbias), _ref(_view(dout)), _ref(_view(x)), _opt(weight),
+        _view(dx), _opt(dweight), _opt(dbias), _view(dout), _view(x), _opt(weight),
         _opt(dresidual), eps, *_ws_args(workspace))
 
 
@@ -569,25 +586,25 @@ def ln_modulate_backward(dout, x, scale, eps: float = 1e-6, dresidual=None, dx=N
     dscale, dshift), the last two of scale's shape and dtype, summed over the
     rows that share a modulation row.  ``dresidual`` is added to dx."""
     L = _load()
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx is None else dx
-    dscale = torch.empty(scale.shape, dtype=scale.dtype, device=scale.device) if dscale is None else dscale
-    dshift = torch.empty(scale.shape, dtype=scale.dtype, device=scale.device) if dshift is None else dshift
+    dx = _like(x) if dx is None else dx
+    dscale = _like(scale) if dscale is None else dscale
+    dshift = _like(scale) if dshift is None else dshift
     ws = _workspace(x, scale)
-    _raise(L.mbx_ln_modulate_backward(_ref(_view(dx)), _ref(_view(dscale)), _ref(_view(dshift)), _ref(_view(dout)),
-                                      _ref(_view(x)), _ref(_view(scale)), _opt(dresidual), eps, *_ws_args(ws),
+    _raise(L.mbx_ln_modulate_backward(_view(dx), _view(dscale), _view(dshift), _view(dout),
+                                      _view(x), _view(scale), _opt(dresidual), eps, *_ws_args(ws),
                                       _stream(x)))
     return dx, dscale, dshift
 
 
 def check_ln_modulate_backward(dx, dscale, dshift, dout, x, scale, eps=1e-6, dresidual=None, workspace=None) -> int:
     return _load().mbx_check_ln_modulate_backward(
-        _ref(_view(dx)), _opt(dscale), _opt(dshift), _ref(_view(dout)), _ref(_view(x)), _ref(_view(scale)),
+        _view(dx), _opt(dscale), _opt(dshift), _view(dout), _view(x), _view(scale),
         _opt(dresidual), eps, *_ws_args(workspace))
 
 
 def _rng(rng):
     """Pointer of the generator's state: an int64 tensor (seed, counter)."""
-    if rng is None or rng.dtype != torch.int64 or rng.numel() != 2 or not rng.is_contiguous():
+    if rng is None or rng.dtype is not torch.int64 or rng.numel() != 2 or not rng.is_contiguous():
         raise MbxError(-12, "MBX_E_ARG: rng must be a contiguous int64 tensor (seed, counter)")
     return rng.data_ptr()
 
@@ -597,26 +614,26 @@ def dropout(x, p: float, rng, offset: int = 0, out=None):
     counter), and never stored (see mbx_dropout); ``out=x`` is in place.  The
     gradient is ``dropout(dout, p, rng, offset)``."""
     L = _load()
-    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-    _raise(L.mbx_dropout(_ref(_view(out)), _ref(_view(x)), p, _rng(rng), offset, _stream(x)))
+    out = _like(x) if out is None else out
+    _raise(L.mbx_dropout(_view(out), _view(x), p, _rng(rng), offset, _stream(x)))
     return out
 
 
 def check_dropout(out, x, p, rng, offset=0) -> int:
-    return _load().mbx_check_dropout(_ref(_view(out)), _ref(_view(x)), p, _rng(rng), offset)
+    return _load().mbx_check_dropout(_view(out), _view(x), p, _rng(rng), offset)
 
 
 def dropout_gate_add(x, gate, y, p: float, rng, offset: int = 0, out=None):
     """out = x + gate * dropout(y) (see mbx_dropout_gate_add); ``out=x`` is in place."""
     L = _load()
-    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-    _raise(L.mbx_dropout_gate_add(_ref(_view(out)), _ref(_view(x)), _ref(_view(gate)), _ref(_view(y)), p, _rng(rng),
+    out = _like(x) if out is None else out
+    _raise(L.mbx_dropout_gate_add(_view(out), _view(x), _view(gate), _view(y), p, _rng(rng),
                                   offset, _stream(x)))
     return out
 
 
 def check_dropout_gate_add(out, x, gate, y, p, rng, offset=0) -> int:
-    return _load().mbx_check_dropout_gate_add(_ref(_view(out)), _ref(_view(x)), _ref(_view(gate)), _ref(_view(y)), p,
+    return _load().mbx_check_dropout_gate_add(_view(out), _view(x), _view(gate), _view(y), p,
                                               _rng(rng), offset)
 
 
@@ -624,17 +641,17 @@ def dropout_gate_add_backward(dout, gate, y, p: float, rng, offset: int = 0, dy=
     """Gradients of ``dropout_gate_add`` (see mbx_dropout_gate_add_backward):
     (dy, dgate); the gradient of x is dout itself."""
     L = _load()
-    dy = torch.empty(y.shape, dtype=y.dtype, device=y.device) if dy is None else dy
-    dgate = torch.empty(gate.shape, dtype=gate.dtype, device=gate.device) if dgate is None else dgate
+    dy = _like(y) if dy is None else dy
+    dgate = _like(gate) if dgate is None else dgate
     ws = _workspace(y, gate)
-    _raise(L.mbx_dropout_gate_add_backward(_ref(_view(dy)), _ref(_view(dgate)), _ref(_view(dout)), _ref(_view(gate)),
-                                           _ref(_view(y)), p, _rng(rng), offset, *_ws_args(ws), _stream(y)))
+    _raise(L.mbx_dropout_gate_add_backward(_view(dy), _view(dgate), _view(dout), _view(gate),
+                                           _view(y), p, _rng(rng), offset, *_ws_args(ws), _stream(y)))
     return dy, dgate
 
 
 def check_dropout_gate_add_backward(dy, dgate, dout, gate, y, p, rng, offset=0, workspace=None) -> int:
     return _load().mbx_check_dropout_gate_add_backward(
-        _ref(_view(dy)), _opt(dgate), _ref(_view(dout)), _ref(_view(gate)), _ref(_view(y)), p, _rng(rng), offset,
+        _view(dy), _opt(dgate), _view(dout), _view(gate), _view(y), p, _rng(rng), offset,
         *_ws_args(workspace))
 
 
@@ -655,13 +672,19 @@ def _heads(t):
         raise MbxError(-5, "MBX_E_SHAPE: expected [batch, tokens, heads, head_dim]")
     if t.shape[3] > 1 and t.stride(3) != 1:
         raise MbxError(-6, "MBX_E_STRIDE: the last dimension must be contiguous")
-    return _Heads(t.data_ptr() if t.numel() else None, *t.shape, *t.stride()[:3], _DTYPES.get(t.dtype, 0))
+    b, s, h, _ = t.stride()
+    return _Heads(t.data_ptr() if t.numel() else None, *t.shape, b, s, h, _DTYPES.get(t.dtype, 0))
+
+
+@functools.lru_cache(maxsize=64)
+def _axes_array(axes):
+    return (ctypes.c_int32 * max(1, len(axes)))(*axes)
 
 
 def _rope_args(q, k, positions, freqs, axes, interleaved, inverse, q_out, k_out):
-    hv = [None if t is None else ctypes.byref(_heads(t)) for t in (q_out, k_out, q, k)]
-    dims = (ctypes.c_int32 * max(1, len(axes)))(*axes)
-    return (*hv, _ref(_view(positions)), _ref(_view(freqs)), dims, len(axes), int(interleaved), int(inverse))
+    return (None if q_out is None else _heads(q_out), None if k_out is None else _heads(k_out), _heads(q),
+            None if k is None else _heads(k), _view(positions), _view(freqs), _axes_array(tuple(axes)), len(axes),
+            int(interleaved), int(inverse))
 
 
 def rope_axes(q, k, positions, freqs, axes, interleaved: bool = True, inverse: bool = False, q_out=None,

@@ -44,11 +44,9 @@ int check_eps(float eps) { return eps >= 0.0f && std::isfinite(eps) ? MBX_OK : M
 
 bool vec_row(const V& v) { return aligned16(v); }
 
-// The workspace of a call that needs `need` bytes of it (none: may be null),
-// overlapping none of the n views.
-int check_workspace(const float* ws, int64_t bytes, int64_t need, const V* views, int n, bool dev) {
-    if (need < 0) return MBX_E_CUDA;
-    if (need == 0) return MBX_OK;
+// The workspace of a call that needs `need` bytes of it, overlapping none of
+// the n views.
+int check_workspace(const float* ws, int64_t bytes, int64_t need, const V* views, int n) {
     if (!ws) return MBX_E_NULL;
     if (bytes < need) return MBX_E_BOUNDS;
     if (reinterpret_cast<uintptr_t>(ws) % 16) return MBX_E_ALIGN;
@@ -56,7 +54,7 @@ int check_workspace(const float* ws, int64_t bytes, int64_t need, const V* views
     MBX_TRY(extent_ok(w));
     for (int i = 0; i < n; ++i)
         if (overlaps(w, views[i])) return MBX_E_ALIAS;
-    return dev ? raw_on_device(ws, need) : MBX_OK;
+    return MBX_OK;
 }
 
 // Rows, columns and counts that the kernels' index arithmetic takes.
@@ -133,12 +131,11 @@ int check_ln_backward(const mbx_view* dx, const mbx_view* dfactor, const mbx_vie
             if (i != k && overlaps(o.v[k], o.v[i])) return MBX_E_ALIAS;
     if (dfactor || dshift) {
         const int64_t m = o.v[i_f].rows;
-        // without a device the size is unknown: the device check below refuses the call
+        // without a device the size is unknown: the device check refuses the call
         const int64_t need = workspace_need(xv.rows, m, xv.cols, xv.dtype);
-        if (need >= 0) MBX_TRY(check_workspace(ws, ws_bytes, need, o.v, o.n, false));
-        if (dev) {
-            MBX_TRY(views_on_device(o.v, o.n));
-            return check_workspace(ws, ws_bytes, need, o.v, o.n, true);
+        if (need > 0) {
+            MBX_TRY(check_workspace(ws, ws_bytes, need, o.v, o.n));
+            o.add(V{ws, 1, need / 4, need / 4, MBX_F32});
         }
     }
     return dev ? views_on_device(o.v, o.n) : MBX_OK;
@@ -190,16 +187,13 @@ int ln_backward(const mbx_view* dx, const mbx_view* dfactor, const mbx_view* dsh
 
 // ---------------------------------------------------------------- dropout
 
-int check_dropout_args(double p, const int64_t* rng, const V* views, int n, const V& out, bool dev) {
+// p, and the generator's state as a view (16 bytes).
+int check_dropout_args(double p, const int64_t* rng, V* state) {
     if (!(p >= 0.0 && p < 1.0)) return MBX_E_ARG;
     if (!rng) return MBX_E_NULL;
     if (reinterpret_cast<uintptr_t>(rng) % 8) return MBX_E_ALIGN;
-    const V r{rng, 1, 4, 4, MBX_F32};  // 16 bytes
-    MBX_TRY(extent_ok(r));
-    if (overlaps(out, r)) return MBX_E_ALIAS;
-    if (!dev) return MBX_OK;
-    MBX_TRY(views_on_device(views, n));
-    return raw_on_device(rng, 16);
+    *state = V{rng, 1, 4, 4, MBX_F32};
+    return extent_ok(*state);
 }
 
 // x null: plain dropout of y.
@@ -226,7 +220,11 @@ int check_dropout(const mbx_view* out, const mbx_cview* x, const mbx_cview* gate
     const int in_place = gated ? 2 : 1;
     for (int i = 1; i < o.n; ++i)
         if (overlaps(ov, o.v[i]) && !(i == in_place && same_view(ov, o.v[i]))) return MBX_E_ALIAS;
-    return check_dropout_args(prob, rng, o.v, o.n, ov, dev);
+    V state;
+    MBX_TRY(check_dropout_args(prob, rng, &state));
+    if (overlaps(ov, state)) return MBX_E_ALIAS;
+    o.add(state);
+    return dev ? views_on_device(o.v, o.n) : MBX_OK;
 }
 
 int check_dropout_backward(const mbx_view* dy, const mbx_view* dgate, const mbx_cview* dout, const mbx_cview* gate,
@@ -245,21 +243,21 @@ int check_dropout_backward(const mbx_view* dy, const mbx_view* dgate, const mbx_
     MBX_TRY(check_same_shape(dov, yv));
     MBX_TRY(check_mod(g, yv));
     if (dgate) MBX_TRY(check_same_shape(o.v[4], g));
-    for (int i = 1; i < o.n; ++i)
+    V state;
+    MBX_TRY(check_dropout_args(prob, rng, &state));
+    o.add(state);
+    for (int i = 1; i < o.n; ++i) {
         if (overlaps(dyv, o.v[i])) return MBX_E_ALIAS;
-    for (int i = 1; dgate && i < 4; ++i)
-        if (overlaps(o.v[4], o.v[i])) return MBX_E_ALIAS;
-    if (dgate) {
-        const V r{rng, 1, 4, 4, MBX_F32};
-        if (rng) MBX_TRY(extent_ok(r));
-        if (rng && overlaps(o.v[4], r)) return MBX_E_ALIAS;
-        if (rng) o.add(r);  // the workspace may not hold the generator's state either
-        const int64_t need = workspace_need(yv.rows, g.rows, yv.cols, yv.dtype);
-        if (need >= 0) MBX_TRY(check_workspace(ws, ws_bytes, need, o.v, o.n, false));
-        MBX_TRY(check_dropout_args(prob, rng, o.v, o.n, dyv, dev));
-        return dev ? check_workspace(ws, ws_bytes, need, o.v, o.n, true) : MBX_OK;
+        if (dgate && i != 4 && overlaps(o.v[4], o.v[i])) return MBX_E_ALIAS;
     }
-    return check_dropout_args(prob, rng, o.v, o.n, dyv, dev);
+    if (dgate) {
+        const int64_t need = workspace_need(yv.rows, g.rows, yv.cols, yv.dtype);
+        if (need > 0) {
+            MBX_TRY(check_workspace(ws, ws_bytes, need, o.v, o.n));
+            o.add(V{ws, 1, need / 4, need / 4, MBX_F32});
+        }
+    }
+    return dev ? views_on_device(o.v, o.n) : MBX_OK;
 }
 
 mbx::DropParams drop_params(const mbx_view* out, const mbx_cview* x, const mbx_cview* gate, const mbx_cview* y,
@@ -382,8 +380,6 @@ bool disjoint4(const H4& a, const H4& b) {
     return a.t > 1 && b.t > 1 && a.st == b.st && batches && apart(a.st, lo.head_span(), hi.head_span());
 }
 
-int check4_device(const H4& v) { return raw_on_device(v.data, v.span() * v.es()); }
-
 bool vec4(const H4& v) {
     return reinterpret_cast<uintptr_t>(v.data) % 16 == 0 && v.sb * v.es() % 16 == 0 && v.st * v.es() % 16 == 0 &&
            v.sh * v.es() % 16 == 0;
@@ -439,12 +435,8 @@ int check_rope(const mbx_heads_view* q_out, const mbx_heads_view* k_out, const m
         if (overlaps(flat4(out[i]), pv) || overlaps(flat4(out[i]), fv)) return MBX_E_ALIAS;
     }
     if (dev) {
-        for (int i = 0; i < nt; ++i) {
-            MBX_TRY(check4_device(out[i]));
-            MBX_TRY(check4_device(in[i]));
-        }
-        const V both[2] = {pv, fv};
-        MBX_TRY(views_on_device(both, 2));
+        const V all[6] = {pv, fv, flat4(out[0]), flat4(in[0]), flat4(out[nt - 1]), flat4(in[nt - 1])};
+        MBX_TRY(views_on_device(all, k ? 6 : 4));
     }
     return MBX_OK;
 }

@@ -117,47 +117,54 @@ inline AddrRangeFn addr_range_fn() {
     return fn;
 }
 
-inline int device_ok(const void* ptr, int64_t bytes, int dev) {
-    cudaPointerAttributes a;
-    if (cudaPointerGetAttributes(&a, ptr) != cudaSuccess) {
-        cudaGetLastError();
-        return MBX_E_DEVICE;
-    }
-    if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) return MBX_E_DEVICE;
-    if (a.type == cudaMemoryTypeDevice && a.device != dev) return MBX_E_DEVICE;
-    AddrRangeFn fn = addr_range_fn();
-    if (fn == nullptr) return MBX_E_DEVICE;
-    CUdeviceptr base = 0;
-    size_t size = 0;
-    if (fn(&base, &size, reinterpret_cast<CUdeviceptr>(ptr)) != CUDA_SUCCESS) {
-        return a.type == cudaMemoryTypeManaged ? MBX_OK : MBX_E_BOUNDS;
-    }
-    // base <= ptr < base + size; compare the remaining room, never a sum
-    uintptr_t p0 = reinterpret_cast<uintptr_t>(ptr), b0 = (uintptr_t)base;
-    if (p0 < b0 || bytes < 0 || (uintptr_t)bytes > b0 + size - p0) return MBX_E_BOUNDS;
-    return MBX_OK;
-}
+// The device checks of one call.  The allocation found last is kept for the
+// call's other views: tensors of a framework's allocator often share one, and
+// a query costs more than the rest of a view's checks.
+struct DeviceCheck {
+    int dev = -1;
+    uintptr_t lo = 0, hi = 0;  // an allocation of this device
 
-inline int current_device(int* dev) {
-    if (cudaGetDevice(dev) != cudaSuccess) {
-        cudaGetLastError();
-        return MBX_E_DEVICE;
+    int ok(const void* ptr, int64_t bytes) {
+        const uintptr_t p0 = reinterpret_cast<uintptr_t>(ptr);
+        if (bytes >= 0 && p0 >= lo && p0 < hi && (uintptr_t)bytes <= hi - p0) return MBX_OK;
+        if (dev < 0 && cudaGetDevice(&dev) != cudaSuccess) {
+            cudaGetLastError();
+            dev = -1;
+            return MBX_E_DEVICE;
+        }
+        cudaPointerAttributes a;
+        if (cudaPointerGetAttributes(&a, ptr) != cudaSuccess) {
+            cudaGetLastError();
+            return MBX_E_DEVICE;
+        }
+        if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) return MBX_E_DEVICE;
+        if (a.type == cudaMemoryTypeDevice && a.device != dev) return MBX_E_DEVICE;
+        AddrRangeFn fn = addr_range_fn();
+        if (fn == nullptr) return MBX_E_DEVICE;
+        CUdeviceptr base = 0;
+        size_t size = 0;
+        if (fn(&base, &size, reinterpret_cast<CUdeviceptr>(ptr)) != CUDA_SUCCESS) {
+            return a.type == cudaMemoryTypeManaged ? MBX_OK : MBX_E_BOUNDS;
+        }
+        // base <= ptr < base + size; compare the remaining room, never a sum
+        const uintptr_t b0 = (uintptr_t)base;
+        if (p0 < b0 || bytes < 0 || (uintptr_t)bytes > b0 + size - p0) return MBX_E_BOUNDS;
+        lo = b0;
+        hi = b0 + size;
+        return MBX_OK;
     }
-    return MBX_OK;
-}
+};
 
 inline int views_on_device(const V* vs, int n) {
-    int dev = 0;
-    if (int st = current_device(&dev)) return st;
+    DeviceCheck c;
     for (int i = 0; i < n; ++i)
-        if (int st = device_ok(vs[i].data, extent_bytes(vs[i]), dev)) return st;
+        if (int st = c.ok(vs[i].data, extent_bytes(vs[i]))) return st;
     return MBX_OK;
 }
 
 inline int raw_on_device(const void* p, int64_t bytes) {
-    int dev = 0;
-    if (int st = current_device(&dev)) return st;
-    return device_ok(p, bytes, dev);
+    DeviceCheck c;
+    return c.ok(p, bytes);
 }
 
 #define MBX_TRY(expr)                   \
