@@ -51,9 +51,14 @@ GradPlan grad_plan(int64_t rows, int64_t mod_rows, int D, int esize) {
     const int64_t seq = rows / mod_rows;
     const RingShape sh = grad_shape(D, esize, 2);
     const int64_t round = (int64_t)sh.groups * 2;  // whole rounds of a block, which takes one or two rows a group
+    GradPlan g;
+    if (seq <= 4 * sh.groups) {  // few rounds: one block, and no second kernel
+        g.parts = 1;
+        g.rows_per_part = seq;
+        return g;
+    }
     int64_t parts = ((int64_t)sm_count() * sh.ctas_per_sm + mod_rows - 1) / mod_rows;
     if (parts > (seq + round - 1) / round) parts = (seq + round - 1) / round;
-    GradPlan g;
     g.rows_per_part = ((seq + parts - 1) / parts + round - 1) / round * round;
     g.parts = (seq + g.rows_per_part - 1) / g.rows_per_part;
     return g;
@@ -65,7 +70,7 @@ int64_t grad_workspace_bytes(int64_t rows, int64_t mod_rows, int D, int esize) {
     return g.parts == 1 ? 0 : mod_rows * g.parts * 2 * D * (int64_t)sizeof(float);
 }
 
-constexpr int kColTile = 32, kColLanes = 16;
+constexpr int kColTile = 32, kColLanes = 32;
 
 __global__ void __launch_bounds__(kColTile* kColLanes) column_sums_kernel(ColSumParams p) {
     __shared__ float part[kColLanes][kColTile];

@@ -77,41 +77,81 @@ struct HeadPart {
         }
         return r;
     }
-    __device__ __forceinline__ void store(T* head, const Raw& r, const float2 (&cs)[kPairs]) const {
+    // cs: the pairs' cosines and sines, two neighbours a register pair.
+    __device__ __forceinline__ void store(T* head, const Raw& r, const u64 (&c)[kPairs / 2 + 1],
+                                          const u64 (&s)[kPairs / 2 + 1]) const {
         if constexpr (VEC && INTERLEAVED) {
-            float v[CE];
-            widen_chunk(r.a, v);
+            uint4 o;
 #pragma unroll
-            for (int i = 0; i < kPairs; ++i) {
-                const float a0 = v[2 * i], a1 = v[2 * i + 1];
-                if (i < pairs) {
-                    v[2 * i] = fmaf(a0, cs[i].x, -(a1 * cs[i].y));
-                    v[2 * i + 1] = fmaf(a0, cs[i].y, a1 * cs[i].x);
+            for (int i = 0; i < kPairs; i += 2) {  // pairs i and i+1 side by side
+                u64 x0, x1;
+                if constexpr (sizeof(T) == 2) {
+                    x0 = f2(lo_f(w_of(r.a, i)), lo_f(w_of(r.a, i + 1)));
+                    x1 = f2(hi_f(w_of(r.a, i)), hi_f(w_of(r.a, i + 1)));
+                } else {
+                    x0 = f2(__uint_as_float(r.a.x), __uint_as_float(r.a.z));
+                    x1 = f2(__uint_as_float(r.a.y), __uint_as_float(r.a.w));
+                }
+                const u64 o0 = turn0(x0, x1, c[i / 2], s[i / 2]), o1 = turn1(x0, x1, c[i / 2], s[i / 2]);
+                if constexpr (sizeof(T) == 2) {
+                    w_set(o, i, pack_rn(f2lo(o0), f2lo(o1)));
+                    w_set(o, i + 1, pack_rn(f2hi(o0), f2hi(o1)));
+                } else {
+                    o = make_uint4(__float_as_uint(f2lo(o0)), __float_as_uint(f2lo(o1)), __float_as_uint(f2hi(o0)),
+                                   __float_as_uint(f2hi(o1)));
                 }
             }
-            st_v4(head + first, narrow_chunk(v));
+            if (pairs < kPairs) {  // the rest of the chunk passes through
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int pair = sizeof(T) == 2 ? i : i / 2;
+                    if (pair >= pairs) w_set(o, i, w_of(r.a, i));
+                }
+            }
+            st_v4(head + first, o);
         } else if constexpr (VEC) {
             if (second < 0) {
                 st_v4(head + first, r.a);
                 return;
             }
-            float va[CE], vb[CE];
-            widen_chunk(r.a, va);
-            widen_chunk(r.b, vb);
+            uint4 oa, ob;
 #pragma unroll
-            for (int i = 0; i < CE; ++i) {
-                const float a0 = va[i], a1 = vb[i];
-                va[i] = fmaf(a0, cs[i].x, -(a1 * cs[i].y));
-                vb[i] = fmaf(a0, cs[i].y, a1 * cs[i].x);
+            for (int i = 0; i < kPairs; i += 2) {
+                u64 x0, x1;
+                if constexpr (sizeof(T) == 2) {
+                    x0 = widen2(w_of(r.a, i / 2));
+                    x1 = widen2(w_of(r.b, i / 2));
+                } else {
+                    x0 = f2(__uint_as_float(w_of(r.a, i)), __uint_as_float(w_of(r.a, i + 1)));
+                    x1 = f2(__uint_as_float(w_of(r.b, i)), __uint_as_float(w_of(r.b, i + 1)));
+                }
+                const u64 o0 = turn0(x0, x1, c[i / 2], s[i / 2]), o1 = turn1(x0, x1, c[i / 2], s[i / 2]);
+                if constexpr (sizeof(T) == 2) {
+                    w_set(oa, i / 2, pack2_rn(o0));
+                    w_set(ob, i / 2, pack2_rn(o1));
+                } else {
+                    w_set(oa, i, (uint32_t)o0);
+                    w_set(oa, i + 1, (uint32_t)(o0 >> 32));
+                    w_set(ob, i, (uint32_t)o1);
+                    w_set(ob, i + 1, (uint32_t)(o1 >> 32));
+                }
             }
-            st_v4(head + first, narrow_chunk(va));
-            st_v4(head + second, narrow_chunk(vb));
+            st_v4(head + first, oa);
+            st_v4(head + second, ob);
         } else if (second < 0) {
             store_elem(head + first, r.a);
         } else {
-            store_elem(head + first, fmaf(r.a, cs[0].x, -(r.b * cs[0].y)));
-            store_elem(head + second, fmaf(r.a, cs[0].y, r.b * cs[0].x));
+            const float c0 = f2lo(c[0]), s0 = f2lo(s[0]);
+            store_elem(head + first, fmaf(r.a, c0, -(r.b * s0)));
+            store_elem(head + second, fmaf(r.a, s0, r.b * c0));
         }
+    }
+    // x0*cos - x1*sin and x0*sin + x1*cos
+    static __device__ __forceinline__ u64 turn0(u64 x0, u64 x1, u64 c, u64 s) {
+        return sub2(mul2(x0, c), mul2(x1, s));
+    }
+    static __device__ __forceinline__ u64 turn1(u64 x0, u64 x1, u64 c, u64 s) {
+        return fma2(x0, s, mul2(x1, c));
     }
 };
 
@@ -136,17 +176,13 @@ __global__ void __launch_bounds__(256) rope_axes_kernel(RopeParams p, int lanes,
     grid_dep_launch();
 
     // the first heads are on their way while the sines and cosines are computed
-    auto head_in = [&](const RopeTensor& w, int h) {
-        return static_cast<const T*>(w.in) + b * w.ib + s * w.it + h * w.ih;
-    };
-    auto head_out = [&](const RopeTensor& w, int h) {
-        return static_cast<T*>(w.out) + b * w.ob + s * w.ot + h * w.oh;
-    };
+    const T* in = static_cast<const T*>(p.q.in) + b * p.q.ib + s * p.q.it + split * p.q.ih;
+    int64_t in_step = splits * p.q.ih;
     typename Part::Raw raw[kHeadsAtOnce];
     if (active) {
 #pragma unroll
         for (int u = 0; u < kHeadsAtOnce; ++u)
-            if (split + u * splits < p.q.heads) raw[u] = part.load(head_in(p.q, split + u * splits));
+            if (split + u * splits < p.q.heads) raw[u] = part.load(in + u * in_step);
     }
     for (int i = threadIdx.x; i < tok_per_block * n; i += blockDim.x) {
         const int kk = i / n, j = i - kk * n;
@@ -163,25 +199,37 @@ __global__ void __launch_bounds__(256) rope_axes_kernel(RopeParams p, int lanes,
     }
     __syncthreads();
     if (!active) return;
-    float2 cs[Part::kPairs];
+    u64 c[Part::kPairs / 2 + 1], sn[Part::kPairs / 2 + 1];
 #pragma unroll
-    for (int i = 0; i < Part::kPairs; ++i)
-        cs[i] = i < part.pairs ? cs_smem[k * n + part.pair0 + i] : make_float2(1.0f, 0.0f);
+    for (int i = 0; i < Part::kPairs; i += 2) {
+        const float2* q = cs_smem + k * n + part.pair0 + i;
+        const float2 a = i < part.pairs ? q[0] : make_float2(1.0f, 0.0f);
+        const float2 d = i + 1 < part.pairs ? q[1] : make_float2(1.0f, 0.0f);
+        c[i / 2] = f2(a.x, d.x);
+        sn[i / 2] = f2(a.y, d.y);
+    }
 
-    const int batch = kHeadsAtOnce * splits;
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
         const RopeTensor& w = which ? p.k : p.q;
+        T* out = static_cast<T*>(w.out) + b * w.ob + s * w.ot + split * w.oh;
+        const int64_t out_step = splits * w.oh;
+        if (which) {
+            in = static_cast<const T*>(w.in) + b * w.ib + s * w.it + split * w.ih;
+            in_step = splits * w.ih;
+        }
 #pragma unroll 1
-        for (int h0 = split; h0 < w.heads; h0 += batch) {
+        for (int h0 = split; h0 < w.heads; h0 += kHeadsAtOnce * splits) {
             if (which || h0 != split) {
 #pragma unroll
                 for (int u = 0; u < kHeadsAtOnce; ++u)
-                    if (h0 + u * splits < w.heads) raw[u] = part.load(head_in(w, h0 + u * splits));
+                    if (h0 + u * splits < w.heads) raw[u] = part.load(in + u * in_step);
             }
 #pragma unroll
             for (int u = 0; u < kHeadsAtOnce; ++u)
-                if (h0 + u * splits < w.heads) part.store(head_out(w, h0 + u * splits), raw[u], cs);
+                if (h0 + u * splits < w.heads) part.store(out + u * out_step, raw[u], c, sn);
+            in += kHeadsAtOnce * in_step;
+            out += kHeadsAtOnce * out_step;
         }
     }
 }
