@@ -70,31 +70,50 @@ int64_t grad_workspace_bytes(int64_t rows, int64_t mod_rows, int D, int esize) {
     return g.parts == 1 ? 0 : mod_rows * g.parts * 2 * D * (int64_t)sizeof(float);
 }
 
-constexpr int kColTile = 32, kColLanes = 32;
+// A block adds 8*W columns: 8 threads side by side hold W columns each, 32
+// rows of such threads take every 32nd part, with up to eight loads of each in
+// flight, and the 32 sums are added in shared memory in a fixed order.  The
+// parts' sums are 2 to 10 MB that the first kernel has just written, so they
+// come from L2; latency bounds this kernel, not bandwidth.
+constexpr int kColThreads = 8, kColLanes = 32;
 
-__global__ void __launch_bounds__(kColTile* kColLanes) column_sums_kernel(ColSumParams p) {
-    __shared__ float part[kColLanes][kColTile];
+template <int W>
+__global__ void __launch_bounds__(kColThreads* kColLanes) column_sums_kernel(ColSumParams p) {
+    __shared__ float part[kColLanes][kColThreads * W];
     grid_dep_wait();
     grid_dep_launch();
     const int cols = p.nacc * p.D;
-    const int c = blockIdx.x * kColTile + threadIdx.x;
+    const int c0 = (blockIdx.x * kColThreads + threadIdx.x) * W;
     for (int64_t seg = blockIdx.y; seg < p.segments; seg += gridDim.y) {
-        const float* w = p.ws + seg * p.parts * cols;
-        float s = 0.0f;
-        if (c < cols) {
+        const float* w = p.ws + seg * p.parts * cols + c0;
+        float s[W] = {};
+        if (c0 < cols) {
 #pragma unroll 8
-            for (int64_t i = threadIdx.y; i < p.parts; i += kColLanes) s += w[i * cols + c];
+            for (int64_t i = threadIdx.y; i < p.parts; i += kColLanes) {
+                if constexpr (W == 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(w + i * cols);
+                    s[0] += v.x;
+                    s[1] += v.y;
+                    s[2] += v.z;
+                    s[3] += v.w;
+                } else {
+                    s[0] += w[i * cols];
+                }
+            }
         }
-        part[threadIdx.y][threadIdx.x] = s;
-        __syncthreads();
-        if (threadIdx.y == 0 && c < cols) {
 #pragma unroll
-            for (int i = 1; i < kColLanes; ++i) s += part[i][threadIdx.x];
+        for (int i = 0; i < W; ++i) part[threadIdx.y][threadIdx.x * W + i] = s[i];
+        __syncthreads();
+        const int t = threadIdx.y * kColThreads + threadIdx.x, c = blockIdx.x * kColThreads * W + t;
+        if (t < kColThreads * W && c < cols) {
+            float a = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kColLanes; ++i) a += part[i][t];
             const int k = c / p.D, d = c - k * p.D;
             if (p.out[k]) {
                 const int64_t o = seg * p.out_stride[k] + d;
-                if (p.p_f32) store_elem(static_cast<float*>(p.out[k]) + o, s);
-                else store_elem(static_cast<uint16_t*>(p.out[k]) + o, s);
+                if (p.p_f32) store_elem(static_cast<float*>(p.out[k]) + o, a);
+                else store_elem(static_cast<uint16_t*>(p.out[k]) + o, a);
             }
         }
         __syncthreads();
@@ -103,16 +122,19 @@ __global__ void __launch_bounds__(kColTile* kColLanes) column_sums_kernel(ColSum
 
 cudaError_t launch_column_sums(const ColSumParams& p, cudaStream_t s) {
     if (t_dry_run) return cudaSuccess;
+    const int cols = p.nacc * p.D;
+    const bool wide = cols % 4 == 0;  // 16-byte loads (the workspace is 16-byte aligned)
+    const int tile = kColThreads * (wide ? 4 : 1);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((p.nacc * p.D + kColTile - 1) / kColTile, (unsigned)(p.segments < 65535 ? p.segments : 65535));
-    cfg.blockDim = dim3(kColTile, kColLanes);
+    cfg.gridDim = dim3((cols + tile - 1) / tile, (unsigned)(p.segments < 65535 ? p.segments : 65535));
+    cfg.blockDim = dim3(kColThreads, kColLanes);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, column_sums_kernel, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, wide ? column_sums_kernel<4> : column_sums_kernel<1>, p);
     const cudaError_t last = cudaGetLastError();
     return e != cudaSuccess ? e : last;
 }
