@@ -50,7 +50,7 @@ RingShape grad_shape(int D, int esize, int rows) {
 GradPlan grad_plan(int64_t rows, int64_t mod_rows, int D, int esize) {
     const int64_t seq = rows / mod_rows;
     const RingShape sh = grad_shape(D, esize, 2);
-    const int64_t round = (int64_t)sh.groups * 2;  // whole rounds of a block, which takes one or two rows a group
+    const int64_t round = sh.groups;  // rows of a block's round
     GradPlan g;
     if (seq <= 4 * sh.groups) {  // few rounds: one block, and no second kernel
         g.parts = 1;

@@ -71,12 +71,16 @@ __global__ void __launch_bounds__(kRingThreads) dropout_kernel(DropParams p, Rin
     const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr;
     const Lane L = make_lane<16, CE, A>(t, tpr, p.D);
     char* ring = smem + g * sh.group_bytes;
+    const int64_t step = (int64_t)gridDim.x * sh.groups;
+    int64_t row = (int64_t)blockIdx.x * sh.groups + g, fill_row = row;
+    if (row < p.rows) {
+        prefetch_row<T, A>(static_cast<const T*>(p.x) + row * p.x_stride, p.D, t);
+        if constexpr (GATED) prefetch_row<T, A>(static_cast<const T*>(p.y) + row * p.y_stride, p.D, t);
+    }
     grid_dep_wait();  // launched programmatically: the previous kernel has finished
     grid_dep_launch();
     const Philox philox(p);
     const int row_bytes = sh.row_bytes, stage_bytes = (GATED ? 2 : 1) * row_bytes, c0 = first_col<CE, A>(L);
-    const int64_t step = (int64_t)gridDim.x * sh.groups;
-    int64_t row = (int64_t)blockIdx.x * sh.groups + g, fill_row = row;
     auto fill = [&](int st) {
         char* dst = ring + st * stage_bytes;
         if (fill_row < p.rows) {
@@ -144,6 +148,17 @@ __global__ void __launch_bounds__(kGradThreads) dropout_backward_kernel(DropPara
     const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr, groups = sh.groups;
     const Lane L = make_lane<16, CE, A>(t, tpr, p.D);
     char* ring = smem + g * sh.group_bytes;
+    {
+        int64_t r = (int64_t)blockIdx.x * groups + g;
+        if constexpr (!TOKEN) {
+            const int64_t seg = blockIdx.x / p.plan.parts;
+            r = seg * p.seq + (blockIdx.x - seg * p.plan.parts) * p.plan.rows_per_part + g;
+        }
+        if (r < p.rows) {
+            prefetch_row<T, A>(static_cast<const T*>(p.x) + r * p.x_stride, p.D, t);
+            prefetch_row<T, A>(static_cast<const T*>(p.y) + r * p.y_stride, p.D, t);
+        }
+    }
     grid_dep_wait();
     grid_dep_launch();
     const Philox philox(p);

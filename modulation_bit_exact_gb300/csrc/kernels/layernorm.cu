@@ -30,6 +30,13 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
     GroupSums sums = group_sums(smem, sh, g, t);
     char* ring = smem + sh.sums_bytes + sh.fixed_bytes + g * sh.group_bytes;
     const float inv_d = 1.0f / (float)p.D;
+    // batches of R consecutive rows, dealt to the groups of the whole grid
+    const int64_t step = (int64_t)gridDim.x * sh.groups * R;
+    const int64_t rounds = (p.rows + step - 1) / step;  // the same for every group
+    int64_t r = ((int64_t)blockIdx.x * sh.groups + g) * R, fill_row = r;
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+        if (r + k < p.rows) prefetch_row<T, A>(static_cast<const T*>(p.x) + (r + k) * p.x_stride, p.D, t);
     grid_dep_wait();  // launched programmatically: the previous kernel has finished
     grid_dep_launch();
 
@@ -48,10 +55,6 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
     }
 
     const int row_bytes = sh.row_bytes, stage_bytes = R * row_bytes, c0 = first_col<CE, A>(L);
-    // batches of R consecutive rows, dealt to the groups of the whole grid
-    const int64_t step = (int64_t)gridDim.x * sh.groups * R;
-    const int64_t rounds = (p.rows + step - 1) / step;  // the same for every group
-    int64_t r = ((int64_t)blockIdx.x * sh.groups + g) * R, fill_row = r;
     auto fill = [&](int st) {
         char* dst = ring + st * stage_bytes;
 #pragma unroll

@@ -83,10 +83,14 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
     GroupSums sums = group_sums(smem, sh, g, t);
     char* ring = smem + sh.sums_bytes + sh.fixed_bytes + g * sh.group_bytes;
     const float inv_d = 1.0f / (float)p.D;
+    const int64_t step = (int64_t)gridDim.x * sh.groups, first = (int64_t)blockIdx.x * sh.groups + g;
+    if (first < p.rows) {
+        prefetch_row<T, A>(static_cast<const T*>(p.x) + first * p.x_stride, p.D, t);
+        prefetch_row<T, A>(static_cast<const T*>(p.dout) + first * p.dout_stride, p.D, t);
+    }
     grid_dep_wait();
     grid_dep_launch();
     const int row_bytes = sh.row_bytes, stage_bytes = kF * row_bytes + sh.extra_bytes;
-    const int64_t step = (int64_t)gridDim.x * sh.groups, first = (int64_t)blockIdx.x * sh.groups + g;
     const int64_t rounds = (p.rows + step - 1) / step;  // the same for every group
     const int c0 = first_col<CE, A>(L);
     const u64 one = f2(p.factor_add, p.factor_add);
@@ -172,11 +176,18 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
     char* ring = smem + sh.sums_bytes + sh.fixed_bytes + g * sh.group_bytes;
     const int block = groups * tpr;
     const float inv_d = 1.0f / (float)p.D;
+    const int64_t units = p.mod_rows * p.plan.parts;
+    {
+        const int64_t seg = blockIdx.x / p.plan.parts, r = seg * p.seq + (blockIdx.x - seg * p.plan.parts) * p.plan.rows_per_part + g;
+        if (r < p.rows) {
+            prefetch_row<T, A>(static_cast<const T*>(p.x) + r * p.x_stride, p.D, t);
+            prefetch_row<T, A>(static_cast<const T*>(p.dout) + r * p.dout_stride, p.D, t);
+        }
+    }
     grid_dep_wait();
     grid_dep_launch();
     const int row_bytes = sh.row_bytes, stage_bytes = (RES ? 3 : 2) * row_bytes;
     const int c0 = first_col<CE, A>(L);
-    const int64_t units = p.mod_rows * p.plan.parts;
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
         const int64_t seg = unit / p.plan.parts, part = unit - seg * p.plan.parts;
         const int64_t r0 = seg * p.seq + part * p.plan.rows_per_part;

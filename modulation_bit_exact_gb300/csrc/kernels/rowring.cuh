@@ -64,6 +64,15 @@ __device__ __forceinline__ int elem_off(int e, const Lane& L) {
     return A == kQuad ? e / 4 * L.tpr * 4 + e % 4 : e * L.tpr;
 }
 
+// While the previous kernel of the stream drains: bring a row that the ring will
+// be filled with first into L2 (L2 is the point of coherence, so a row that the
+// previous kernel still writes is the written one there).
+template <class Q, Access A>
+__device__ __forceinline__ void prefetch_row(const Q* row, int D, int t) {
+    if constexpr (A == kVec)
+        if (t == 0) prefetch_l2_bulk(row, (uint32_t)(D * (int)sizeof(Q)));
+}
+
 // Start the copy of this thread's part of a row to its place in a stage; `row`
 // points at its first column.
 template <class Q, int NCH, int CE, Access A>
