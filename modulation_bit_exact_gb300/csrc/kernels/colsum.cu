@@ -5,12 +5,14 @@
 
 namespace mbx {
 
-RingShape ring_shape(int tpr, int row_bytes, int rows, int extra_bytes, int fixed_per_thread, int threads_per_sm) {
+RingShape ring_shape(int tpr, int row_bytes, int rows, int extra_bytes, int fixed_per_thread, int threads_per_sm,
+                     int blocks_per_sm) {
     RingShape s;
     s.tpr = tpr;
     s.row_bytes = row_bytes;
     s.extra_bytes = extra_bytes;
-    s.groups = 2 * tpr > threads_per_sm ? 1 : threads_per_sm / 2 / tpr;  // two blocks an SM
+    s.groups = threads_per_sm / blocks_per_sm / tpr;
+    if (s.groups < 1) s.groups = 1;
     while (s.groups * tpr % 32) --s.groups;  // whole warps
     s.sums_bytes = tpr > 32 ? s.groups * 2 * 4 * 16 * (int)sizeof(float) : 0;
     s.fixed_bytes = fixed_per_thread * s.groups * tpr;
@@ -44,7 +46,7 @@ cudaError_t SmemOptIn::allow(const void* kernel, const RingShape& sh) {
 
 RingShape grad_shape(int D, int esize, int rows) {
     const int tpr = row_threads(D);
-    return ring_shape(tpr, 16 * esize * tpr, rows, 0, 64, kGradThreads);
+    return ring_shape(tpr, 16 * esize * tpr, rows, 0, 64, kGradThreads, 1);
 }
 
 GradPlan grad_plan(int64_t rows, int64_t mod_rows, int D, int esize) {

@@ -276,7 +276,7 @@ template <class T, int NCH, Access A, bool GATED>
 static cudaError_t drop_fwd(const DropParams& p, cudaStream_t s) {
     auto k = dropout_kernel<T, NCH, A, GATED>;
     const int tpr = row_threads(p.D);
-    RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, GATED ? 2 : 1, 0, 0, kRingThreads);
+    RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, GATED ? 2 : 1, 0, 0, kRingThreads, 2);
     sh.smem -= sh.sums_bytes;  // no row sums
     static SmemOptIn opt_in;
     if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
@@ -299,7 +299,7 @@ static cudaError_t drop_bwd(const DropParams& p0, cudaStream_t s) {
     DropParams p = p0;
     auto k = dropout_backward_kernel<T, NCH, A, TOKEN>;
     const int tpr = row_threads(p.D);
-    RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, 2, 0, 0, kGradThreads);
+    RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, 2, 0, 0, kGradThreads, TOKEN ? 2 : 1);
     sh.smem -= sh.sums_bytes;
     static SmemOptIn opt_in;
     if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
 template <class T, int NCH, Access A, int R>
 static cudaError_t ln_fwd(const LnFwdParams& p, int tpr, cudaStream_t s) {
     auto k = layer_norm_kernel<T, NCH, A, R>;
-    const RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, R, 0, 0, kRingThreads);
+    const RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, R, 0, 0, kRingThreads, 2);
     static SmemOptIn opt_in;
     if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
     const int64_t batches = (p.rows + R - 1) / R, need = (batches + sh.groups - 1) / sh.groups;

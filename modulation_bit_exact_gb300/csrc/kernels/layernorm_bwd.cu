@@ -194,20 +194,6 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
         const int64_t left = (seg + 1) * p.seq - r0;
         const int n_rows = (int)(left < p.plan.rows_per_part ? left : p.plan.rows_per_part);
         const int rounds = (n_rows + groups - 1) / groups;
-        u64 adf[P], ads[P];
-#pragma unroll
-        for (int j = 0; j < NCH; ++j) {
-            u64 c[H];
-#pragma unroll
-            for (int i = 0; i < H; ++i) c[i] = f2(1.0f, 1.0f);
-            if (p.factor) get_param_chunk<T, CE, A>(c, p.factor, seg * p.factor_stride + c0, p.p_f32, j, L);
-#pragma unroll
-            for (int i = 0; i < H; i += 2) {
-                const u64 one = f2(p.factor_add, p.factor_add);
-                fs[(j * H + i) / 2 * block] = make_ulonglong2(add2(c[i], one), add2(c[i + 1], one));
-                adf[j * H + i] = adf[j * H + i + 1] = ads[j * H + i] = ads[j * H + i + 1] = 0;
-            }
-        }
         const T* nx = static_cast<const T*>(p.x) + (r0 + g) * p.x_stride + c0;
         const T* nd = static_cast<const T*>(p.dout) + (r0 + g) * p.dout_stride + c0;
         const T* nr = RES ? static_cast<const T*>(p.dres) + (r0 + g) * p.dres_stride + c0 : nullptr;
@@ -230,6 +216,20 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
             ring_commit();
         };
         for (int i = 0; i < sh.stages; ++i) fill(i);
+        u64 adf[P], ads[P];
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+            u64 c[H];
+#pragma unroll
+            for (int i = 0; i < H; ++i) c[i] = f2(1.0f, 1.0f);
+            if (p.factor) get_param_chunk<T, CE, A>(c, p.factor, seg * p.factor_stride + c0, p.p_f32, j, L);
+#pragma unroll
+            for (int i = 0; i < H; i += 2) {
+                const u64 one = f2(p.factor_add, p.factor_add);
+                fs[(j * H + i) / 2 * block] = make_ulonglong2(add2(c[i], one), add2(c[i + 1], one));
+                adf[j * H + i] = adf[j * H + i + 1] = ads[j * H + i] = ads[j * H + i + 1] = 0;
+            }
+        }
         int stage = 0;
         for (int round = 0; round < rounds; ++round, dx_row += dx_step) {
             ring_wait(sh.stages);
@@ -320,7 +320,7 @@ template <class T, int NCH, Access A, bool RES>
 static cudaError_t ln_bwd_token(const LnBwdParams& p, cudaStream_t s) {
     auto k = ln_backward_token_kernel<T, NCH, A, RES>;
     const int tpr = row_threads(p.D), elem = p.p_f32 ? 4 : 2;
-    const RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, RES ? 3 : 2, 16 * elem * tpr, 0, kRingThreads);
+    const RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, RES ? 3 : 2, 16 * elem * tpr, 0, kRingThreads, 2);
     static SmemOptIn opt_in;
     if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
     const int64_t need = (p.rows + sh.groups - 1) / sh.groups, most = (int64_t)sm_count() * sh.ctas_per_sm;

@@ -29,7 +29,7 @@ struct RingShape {
     int row_bytes, extra_bytes, sums_bytes, fixed_bytes, group_bytes, smem;
 };
 RingShape ring_shape(int tpr, int row_bytes, int rows, int extra_bytes, int fixed_per_thread,
-                     int threads_per_sm);  // stages < 1: does not fit
+                     int threads_per_sm, int blocks_per_sm);  // stages < 1: does not fit
 
 // Raises a kernel's shared-memory limit once for each device.
 struct SmemOptIn {
