@@ -19,42 +19,73 @@
 
 namespace mbx {
 
-// The generator's key schedule and the upper counter words, the same for a
-// whole call.
+// Philox4x32-10 for the quads (four columns) that a thread keeps for many rows.
+// A round maps (w0, w1, w2, w3) to (hi(b)^w1^k0, lo(b), hi(a)^w3^k1, lo(a)) with
+// a = M0*w0, b = M1*w2.  The counter's words are (quad, row, c2, c3), so after
+// the first round w0 depends on the row alone and w2, w3 on the quad alone;
+// followed through, what depends on one of them alone can be formed once for
+// it, and a call is left with 15 of the 20 products, which bound this kernel.
+constexpr uint32_t kM0 = 0xD2511F53u, kM1 = 0xCD9E8D57u, kW0 = 0x9E3779B9u, kW1 = 0xBB67AE85u;
+
+__device__ __forceinline__ uint32_t hi32(uint64_t v) { return (uint32_t)(v >> 32); }
+
+template <int NQ>
 struct Philox {
-    uint32_t k0[10], k1[10], c2, c3;
-    __device__ __forceinline__ explicit Philox(const DropParams& p) {
+    uint32_t k0[7], k1[7];               // keys of rounds 3 to 9 (counted from 0)
+    uint32_t base;                       // round 0: w0 = base ^ row
+    uint32_t c[NQ], d[NQ], e[NQ], f[NQ];  // of each quad
+    uint64_t a;                          // M0 * (base ^ row)
+
+    __device__ __forceinline__ Philox(const DropParams& p, const uint32_t (&quad)[NQ]) {
         const uint64_t seed = (uint64_t)p.rng[0], ctr = (uint64_t)p.rng[1] + (uint64_t)p.offset;
-        c2 = (uint32_t)ctr;
-        c3 = (uint32_t)(ctr >> 32);
+        const uint32_t s0 = (uint32_t)seed, s1 = hi32(seed), c2 = (uint32_t)ctr, c3 = hi32(ctr);
 #pragma unroll
-        for (int r = 0; r < 10; ++r) {
-            k0[r] = (uint32_t)seed + r * 0x9E3779B9u;
-            k1[r] = (uint32_t)(seed >> 32) + r * 0xBB67AE85u;
+        for (int r = 0; r < 7; ++r) {
+            k0[r] = s0 + (r + 3) * kW0;
+            k1[r] = s1 + (r + 3) * kW1;
             // kept in registers: formed again at every use they would be a
             // third of the generator's instructions
             asm volatile("" : "+r"(k0[r]), "+r"(k1[r]));
         }
-    }
-    __device__ __forceinline__ uint4 operator()(uint32_t quad, uint32_t row) const {
-        uint32_t w0 = quad, w1 = row, w2 = c2, w3 = c3;
+        const uint64_t b0 = (uint64_t)kM1 * c2;
+        base = hi32(b0) ^ s0;
 #pragma unroll
-        for (int r = 0; r < 10; ++r) {
-            const uint64_t a = (uint64_t)0xD2511F53u * w0, b = (uint64_t)0xCD9E8D57u * w2;
-            w0 = (uint32_t)(b >> 32) ^ w1 ^ k0[r];
-            w1 = (uint32_t)b;
-            w2 = (uint32_t)(a >> 32) ^ w3 ^ k1[r];
-            w3 = (uint32_t)a;
+        for (int q = 0; q < NQ; ++q) {
+            const uint64_t a0 = (uint64_t)kM0 * quad[q], b1 = (uint64_t)kM1 * (hi32(a0) ^ c3 ^ s1);
+            const uint64_t a2 = (uint64_t)kM0 * (hi32(b1) ^ (uint32_t)b0 ^ (s0 + kW0));
+            c[q] = (uint32_t)a0 ^ (s1 + kW1);
+            d[q] = hi32(a2) ^ (s1 + 2 * kW1);
+            e[q] = (uint32_t)a2;
+            f[q] = (uint32_t)b1 ^ (s0 + 2 * kW0);
+            asm volatile("" : "+r"(c[q]), "+r"(d[q]), "+r"(e[q]), "+r"(f[q]));
+        }
+    }
+    __device__ __forceinline__ void row(uint32_t r) { a = (uint64_t)kM0 * (base ^ r); }
+    // The four words of quad q of the row.
+    __device__ __forceinline__ uint4 operator()(int q) const {
+        const uint64_t b2 = (uint64_t)kM1 * (hi32(a) ^ c[q]);  // rounds 1 and 2
+        uint32_t w0 = hi32(b2) ^ f[q], w1 = (uint32_t)b2, w2 = d[q] ^ (uint32_t)a, w3 = e[q];
+#pragma unroll
+        for (int r = 0; r < 7; ++r) {
+            const uint64_t x = (uint64_t)kM0 * w0, y = (uint64_t)kM1 * w2;
+            w0 = hi32(y) ^ w1 ^ k0[r];
+            w1 = (uint32_t)y;
+            w2 = hi32(x) ^ w3 ^ k1[r];
+            w3 = (uint32_t)x;
         }
         return make_uint4(w0, w1, w2, w3);
     }
 };
 
-// The quad (column / 4) of this thread's elements e .. e+3.
-template <int CE, Access A>
-__device__ __forceinline__ uint32_t quad_of(int e, const Lane& L) {
+// A thread's quads: column / 4 of its elements 4i .. 4i+3.
+template <int NQ, int CE, Access A>
+__device__ __forceinline__ Philox<NQ> make_philox(const DropParams& p, const Lane& L) {
     static_assert(A != kScalar, "four columns of a thread are consecutive");
-    return A == kVec && CE == 8 ? (uint32_t)(e / 8 * L.tpr + L.t) * 2 + e % 8 / 4 : (uint32_t)(e / 4 * L.tpr + L.t);
+    uint32_t quad[NQ];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+        quad[i] = A == kVec && CE == 8 ? (uint32_t)(i / 2 * L.tpr + L.t) * 2 + i % 2 : (uint32_t)(i * L.tpr + L.t);
+    return Philox<NQ>(p, quad);
 }
 
 // v where the element is kept, else `dropped`.
@@ -79,7 +110,7 @@ __global__ void __launch_bounds__(kRingThreads) dropout_kernel(DropParams p, Rin
     }
     grid_dep_wait();  // launched programmatically: the previous kernel has finished
     grid_dep_launch();
-    const Philox philox(p);
+    Philox<P / 2> philox = make_philox<P / 2, CE, A>(p, L);
     const int row_bytes = sh.row_bytes, stage_bytes = (GATED ? 2 : 1) * row_bytes, c0 = first_col<CE, A>(L);
     auto fill = [&](int st) {
         char* dst = ring + st * stage_bytes;
@@ -116,6 +147,7 @@ __global__ void __launch_bounds__(kRingThreads) dropout_kernel(DropParams p, Rin
         if constexpr (GATED) read_pieces<T, NCH, A>(yr, ring + stage * stage_bytes + row_bytes, L);
         fill(stage);
         if (++stage == sh.stages) stage = 0;
+        philox.row((uint32_t)row);
         T* dst = static_cast<T*>(p.out) + row * p.out_stride + c0;
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
@@ -123,7 +155,7 @@ __global__ void __launch_bounds__(kRingThreads) dropout_kernel(DropParams p, Rin
 #pragma unroll
             for (int i = 0; i < H; i += 2) {
                 const int e = j * H + i;
-                const uint4 w = philox(quad_of<CE, A>(2 * e, L), (uint32_t)row);
+                const uint4 w = philox(e / 2);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t w0 = h ? w.z : w.x, w1 = h ? w.w : w.y;
@@ -161,7 +193,7 @@ __global__ void __launch_bounds__(kGradThreads) dropout_backward_kernel(DropPara
     }
     grid_dep_wait();
     grid_dep_launch();
-    const Philox philox(p);
+    Philox<P / 2> philox = make_philox<P / 2, CE, A>(p, L);
     const int row_bytes = sh.row_bytes, stage_bytes = 2 * row_bytes, c0 = first_col<CE, A>(L);
     const u64 inv = f2(p.inv_keep, p.inv_keep);
     const int64_t units = TOKEN ? 1 : p.mod_rows * p.plan.parts;
@@ -213,6 +245,7 @@ __global__ void __launch_bounds__(kGradThreads) dropout_backward_kernel(DropPara
             read_pieces<T, NCH, A>(yr, ring + stage * stage_bytes + row_bytes, L);
             fill(stage);
             if (++stage == sh.stages) stage = 0;
+            philox.row((uint32_t)row);
             T* dst = static_cast<T*>(p.out) + row * p.out_stride + c0;
 #pragma unroll
             for (int j = 0; j < NCH; ++j) {
@@ -220,7 +253,7 @@ __global__ void __launch_bounds__(kGradThreads) dropout_backward_kernel(DropPara
 #pragma unroll
                 for (int i = 0; i < H; i += 2) {
                     const int e = j * H + i;
-                    const uint4 w = philox(quad_of<CE, A>(2 * e, L), (uint32_t)row);
+                    const uint4 w = philox(e / 2);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t w0 = h ? w.z : w.x, w1 = h ? w.w : w.y;
