@@ -17,7 +17,6 @@ library rejects (MBX_E_STRIDE).
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import threading
 
@@ -497,25 +496,36 @@ def qk_norm_rope_qkv_epilogue(txt_qkv, img_qkv, batch: int, heads: int, head_dim
 # ---------------------------------------------------------------- training path
 
 
-# A ctypes structure passes for a pointer to it.
+# These go through _binding.so (csrc/binding.cpp), which does in native code what
+# the functions above do through ctypes: views, outputs, the current stream, the
+# call, MbxError.  The check_ functions use ctypes; a structure passes for a
+# pointer to it.
+
+_ext = None
+
+
+def _native():
+    global _ext
+    if _ext is None:
+        _load()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError(f"{_HERE}/_binding.so cannot be loaded ({e}): build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        _binding.set_error(MbxError)
+        _ext = _binding
+    return _ext
 
 
 def _opt(t):
     return None if t is None else _view(t)
 
 
-def _like(t):
-    """An uninitialised tensor of t's shape and dtype with flat rows."""
-    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
-
-
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None):
     """Affine LayerNorm over the last dimension (see mbx_layer_norm): x
     bfloat16 or float32, weight and bias [D] of x's dtype or float32, or None."""
-    L = _load()
-    out = _like(x) if out is None else out
-    _raise(L.mbx_layer_norm(_view(out), _view(x), _opt(weight), _opt(bias), eps, _stream(x)))
-    return out
+    return _native().layer_norm(x, weight, bias, eps, out)
 
 
 def check_layer_norm(out, x, weight=None, bias=None, eps=1e-6) -> int:
@@ -531,28 +541,6 @@ def param_grad_workspace(rows: int, cols: int, mod_rows: int, dtype: torch.dtype
     return n.value
 
 
-@functools.lru_cache(maxsize=1024)
-def _workspace_floats(rows: int, cols: int, mod_rows: int, dtype: torch.dtype, device: int) -> int:
-    try:
-        with torch.cuda.device(device):
-            return param_grad_workspace(rows, cols, mod_rows, dtype) // 4
-    except MbxError:
-        return 0  # the call itself is refused
-
-
-def _workspace(x, params):
-    """A workspace for the gradient of `params` summed over x's rows, or None."""
-    n = x.numel()
-    if not n or not x.is_cuda:
-        return None
-    cols = x.shape[-1]
-    rows, mod_rows = n // cols, params.numel() // cols
-    if rows == mod_rows:
-        return None
-    floats = _workspace_floats(rows, cols, mod_rows, x.dtype, x.get_device())
-    return torch.empty(floats, dtype=torch.float32, device=x.device) if floats else None
-
-
 def _ws_args(ws):
     return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
 
@@ -562,16 +550,7 @@ def layer_norm_backward(dout, x, weight=None, eps: float = 1e-6, dresidual=None,
     """Gradients of ``layer_norm`` (see mbx_layer_norm_backward): (dx, dweight,
     dbias), the last two None without a weight.  ``dresidual`` is added to dx,
     and ``dx=dresidual`` updates it in place."""
-    L = _load()
-    dx = _like(x) if dx is None else dx
-    ws = None
-    if weight is not None:
-        dweight = _like(weight) if dweight is None else dweight
-        dbias = _like(weight) if dbias is None else dbias
-        ws = _workspace(x, weight)
-    _raise(L.mbx_layer_norm_backward(_view(dx), _opt(dweight), _opt(dbias), _view(dout), _view(x),
-                                     _opt(weight), _opt(dresidual), eps, *_ws_args(ws), _stream(x)))
-    return dx, dweight, dbias
+    return _native().layer_norm_backward(dout, x, weight, eps, dresidual, dx, dweight, dbias)
 
 
 def check_layer_norm_backward(dx, dweight, dbias, dout, x, weight=None, eps=1e-6, dresidual=None,
@@ -585,15 +564,7 @@ def ln_modulate_backward(dout, x, scale, eps: float = 1e-6, dresidual=None, dx=N
     """Gradients of ``ln_modulate`` (see mbx_ln_modulate_backward): (dx,
     dscale, dshift), the last two of scale's shape and dtype, summed over the
     rows that share a modulation row.  ``dresidual`` is added to dx."""
-    L = _load()
-    dx = _like(x) if dx is None else dx
-    dscale = _like(scale) if dscale is None else dscale
-    dshift = _like(scale) if dshift is None else dshift
-    ws = _workspace(x, scale)
-    _raise(L.mbx_ln_modulate_backward(_view(dx), _view(dscale), _view(dshift), _view(dout),
-                                      _view(x), _view(scale), _opt(dresidual), eps, *_ws_args(ws),
-                                      _stream(x)))
-    return dx, dscale, dshift
+    return _native().ln_modulate_backward(dout, x, scale, eps, dresidual, dx, dscale, dshift)
 
 
 def check_ln_modulate_backward(dx, dscale, dshift, dout, x, scale, eps=1e-6, dresidual=None, workspace=None) -> int:
@@ -613,10 +584,7 @@ def dropout(x, p: float, rng, offset: int = 0, out=None):
     """Dropout whose mask is computed from rng, an int64 CUDA tensor (seed,
     counter), and never stored (see mbx_dropout); ``out=x`` is in place.  The
     gradient is ``dropout(dout, p, rng, offset)``."""
-    L = _load()
-    out = _like(x) if out is None else out
-    _raise(L.mbx_dropout(_view(out), _view(x), p, _rng(rng), offset, _stream(x)))
-    return out
+    return _native().dropout(x, p, rng, offset, out)
 
 
 def check_dropout(out, x, p, rng, offset=0) -> int:
@@ -625,11 +593,7 @@ def check_dropout(out, x, p, rng, offset=0) -> int:
 
 def dropout_gate_add(x, gate, y, p: float, rng, offset: int = 0, out=None):
     """out = x + gate * dropout(y) (see mbx_dropout_gate_add); ``out=x`` is in place."""
-    L = _load()
-    out = _like(x) if out is None else out
-    _raise(L.mbx_dropout_gate_add(_view(out), _view(x), _view(gate), _view(y), p, _rng(rng),
-                                  offset, _stream(x)))
-    return out
+    return _native().dropout_gate_add(x, gate, y, p, rng, offset, out)
 
 
 def check_dropout_gate_add(out, x, gate, y, p, rng, offset=0) -> int:
@@ -640,13 +604,7 @@ def check_dropout_gate_add(out, x, gate, y, p, rng, offset=0) -> int:
 def dropout_gate_add_backward(dout, gate, y, p: float, rng, offset: int = 0, dy=None, dgate=None):
     """Gradients of ``dropout_gate_add`` (see mbx_dropout_gate_add_backward):
     (dy, dgate); the gradient of x is dout itself."""
-    L = _load()
-    dy = _like(y) if dy is None else dy
-    dgate = _like(gate) if dgate is None else dgate
-    ws = _workspace(y, gate)
-    _raise(L.mbx_dropout_gate_add_backward(_view(dy), _view(dgate), _view(dout), _view(gate),
-                                           _view(y), p, _rng(rng), offset, *_ws_args(ws), _stream(y)))
-    return dy, dgate
+    return _native().dropout_gate_add_backward(dout, gate, y, p, rng, offset, dy, dgate)
 
 
 def check_dropout_gate_add_backward(dy, dgate, dout, gate, y, p, rng, offset=0, workspace=None) -> int:
@@ -676,15 +634,10 @@ def _heads(t):
     return _Heads(t.data_ptr() if t.numel() else None, *t.shape, b, s, h, _DTYPES.get(t.dtype, 0))
 
 
-@functools.lru_cache(maxsize=64)
-def _axes_array(axes):
-    return (ctypes.c_int32 * max(1, len(axes)))(*axes)
-
-
 def _rope_args(q, k, positions, freqs, axes, interleaved, inverse, q_out, k_out):
     return (None if q_out is None else _heads(q_out), None if k_out is None else _heads(k_out), _heads(q),
-            None if k is None else _heads(k), _view(positions), _view(freqs), _axes_array(tuple(axes)), len(axes),
-            int(interleaved), int(inverse))
+            None if k is None else _heads(k), _view(positions), _view(freqs),
+            (ctypes.c_int32 * max(1, len(axes)))(*axes), len(axes), int(interleaved), int(inverse))
 
 
 def rope_axes(q, k, positions, freqs, axes, interleaved: bool = True, inverse: bool = False, q_out=None,
@@ -698,11 +651,7 @@ def rope_axes(q, k, positions, freqs, axes, interleaved: bool = True, inverse: b
     freqs: ``rope_axis_freqs(axes)`` or other angles per position, float64.
     ``inverse=True`` turns back, which is the gradient.  Returns (q_out, k_out);
     ``q_out=q, k_out=k`` rotates in place."""
-    L = _load()
-    q_out = torch.empty_like(q) if q_out is None else q_out
-    k_out = torch.empty_like(k) if k_out is None and k is not None else k_out
-    _raise(L.mbx_rope_axes(*_rope_args(q, k, positions, freqs, axes, interleaved, inverse, q_out, k_out), _stream(q)))
-    return q_out, k_out
+    return _native().rope_axes(q, k, positions, freqs, axes, interleaved, inverse, q_out, k_out)
 
 
 def check_rope_axes(q_out, k_out, q, k, positions, freqs, axes, interleaved=True, inverse=False) -> int:

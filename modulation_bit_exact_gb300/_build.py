@@ -1,17 +1,22 @@
 """Build libmbx.so in-tree: one nvcc job per translation unit (in parallel),
-then one link.  sm_103a only; no CPU code path is built."""
+then one link; and _binding.so, the module through which Python calls the
+training path (g++, against the installed torch).  sm_103a only; no CPU code
+path is built."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 KERN = os.path.join(CSRC, "kernels")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmbx.so")
+BINDING = os.path.join(HERE, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = [
@@ -61,6 +66,22 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_commands(cuda: str) -> tuple[list[str], list[str]]:
+    """Compile and link commands of _binding.so, for the torch that is installed."""
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    obj = os.path.join(OBJ, "binding.o")
+    inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                *[a for i in inc for a in ("-I", i)], "-c", BINDING_SRC, "-o", obj]
+    lib = os.path.join(root, "lib")
+    link = ["g++", "-shared", obj, "-L" + HERE, "-l:libmbx.so", "-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu",
+            "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
+    return compile_, link
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     os.makedirs(OBJ, exist_ok=True)
     cc = nvcc()
@@ -79,12 +100,26 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr)
 
+    compile_, link = _binding_commands(os.path.dirname(os.path.dirname(cc)))
+    stamp = os.path.join(OBJ, "binding.cmd")  # another torch gives other commands
+    want = "\n".join(compile_ + link)
+    same = os.path.exists(stamp) and open(stamp).read() == want
+    binding = force or not same or _stale(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "mbx.h")])
+    if binding:
+        jobs.append(compile_)
+
     with cf.ThreadPoolExecutor(max_workers=len(jobs) or 1) as ex:
         list(ex.map(run, jobs))
-    if force or jobs or _stale(LIB, objs):
+    if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         run([cc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    if binding:
+        tmp = BINDING + f".tmp{os.getpid()}"
+        run([*link, "-o", tmp])
+        os.replace(tmp, BINDING)
+        with open(stamp, "w") as f:
+            f.write(want)
     return LIB
 
 

@@ -88,9 +88,16 @@ __device__ __forceinline__ Philox<NQ> make_philox(const DropParams& p, const Lan
     return Philox<NQ>(p, quad);
 }
 
-// v where the element is kept, else `dropped`.
-__device__ __forceinline__ u64 keep_pair(u64 v, uint32_t a, uint32_t b, uint32_t threshold, float dropped) {
-    return f2(a >= threshold ? f2lo(v) : dropped, b >= threshold ? f2hi(v) : dropped);
+// v where the element is kept, else 0.
+__device__ __forceinline__ u64 keep_pair(u64 v, uint32_t a, uint32_t b, uint32_t threshold) {
+    return f2(a >= threshold ? f2lo(v) : 0.0f, b >= threshold ? f2hi(v) : 0.0f);
+}
+// acc + v * w where the element is kept, else acc.
+__device__ __forceinline__ u64 keep_fma(u64 v, u64 w, u64 acc, uint32_t a, uint32_t b, uint32_t threshold) {
+    float lo = f2lo(acc), hi = f2hi(acc);
+    if (a >= threshold) lo = fmaf(f2lo(v), f2lo(w), lo);
+    if (b >= threshold) hi = fmaf(f2hi(v), f2hi(w), hi);
+    return f2(lo, hi);
 }
 
 // GATED: out = x + gate * drop(y); otherwise out = drop(x).  Rows stream
@@ -160,9 +167,9 @@ __global__ void __launch_bounds__(kRingThreads) dropout_kernel(DropParams p, Rin
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t w0 = h ? w.z : w.x, w1 = h ? w.w : w.y;
                     const u64 x = piece_pair<T>(xr, e + h);
-                    if constexpr (GATED)  // -0 leaves every x as it is
-                        o[i + h] = add2(x, keep_pair(mul2(piece_pair<T>(yr, e + h), gate[e + h]), w0, w1, p.threshold, -0.0f));
-                    else o[i + h] = keep_pair(mul2(x, inv), w0, w1, p.threshold, 0.0f);
+                    if constexpr (GATED)
+                        o[i + h] = keep_fma(piece_pair<T>(yr, e + h), gate[e + h], x, w0, w1, p.threshold);
+                    else o[i + h] = keep_pair(mul2(x, inv), w0, w1, p.threshold);
                 }
             }
             if (has_chunk<A>(j, L)) put_chunk<T, CE, A>(dst, o, j, L);
@@ -258,10 +265,10 @@ __global__ void __launch_bounds__(kGradThreads) dropout_backward_kernel(DropPara
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t w0 = h ? w.z : w.x, w1 = h ? w.w : w.y;
                         const u64 d = piece_pair<T>(dr, e + h);
-                        o[i + h] = keep_pair(mul2(d, gate[e + h]), w0, w1, p.threshold, 0.0f);
-                        og[i + h] = keep_pair(mul2(d, piece_pair<T>(yr, e + h)), w0, w1, p.threshold, 0.0f);
-                        if constexpr (!TOKEN) acc[e + h] = add2(acc[e + h], og[i + h]);
-                        else og[i + h] = mul2(og[i + h], inv);
+                        const u64 y = piece_pair<T>(yr, e + h);
+                        o[i + h] = keep_pair(mul2(d, gate[e + h]), w0, w1, p.threshold);
+                        if constexpr (TOKEN) og[i + h] = keep_pair(mul2(mul2(d, inv), y), w0, w1, p.threshold);
+                        else acc[e + h] = keep_fma(d, y, acc[e + h], w0, w1, p.threshold);
                     }
                 }
                 if (!has_chunk<A>(j, L)) continue;
