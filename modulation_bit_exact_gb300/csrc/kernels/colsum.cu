@@ -44,14 +44,14 @@ cudaError_t SmemOptIn::allow(const void* kernel, const RingShape& sh) {
     return cudaSuccess;
 }
 
-RingShape grad_shape(int D, int esize, int rows) {
+RingShape grad_shape(int D, int esize, int rows, bool vec) {
     const int tpr = row_threads(D);
-    return ring_shape(tpr, 16 * esize * tpr, rows, 0, 64, kGradThreads, 1);
+    return ring_shape(tpr, staged_row_bytes(tpr, esize, vec), rows, 0, 64, kGradThreads, 1);
 }
 
 GradPlan grad_plan(int64_t rows, int64_t mod_rows, int D, int esize) {
     const int64_t seq = rows / mod_rows;
-    const RingShape sh = grad_shape(D, esize, 2);
+    const RingShape sh = grad_shape(D, esize, 2, true);
     const int64_t round = sh.groups;  // rows of a block's round
     GradPlan g;
     if (seq <= 4 * sh.groups) {  // few rounds: one block, and no second kernel

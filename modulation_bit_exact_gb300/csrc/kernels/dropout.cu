@@ -101,7 +101,7 @@ __device__ __forceinline__ u64 keep_fma(u64 v, u64 w, u64 acc, uint32_t a, uint3
 }
 
 // GATED: out = x + gate * drop(y); otherwise out = drop(x).  Rows stream
-// through a ring (rowring.cuh); no thread waits for another.
+// through a ring (rowring.cuh).
 template <class T, int NCH, Access A, bool GATED>
 __global__ void __launch_bounds__(kRingThreads) dropout_kernel(DropParams p, RingShape sh) {
     constexpr int CE = ChunkOf<T>::CE, H = CE / 2, P = NCH * H;
@@ -149,9 +149,11 @@ __global__ void __launch_bounds__(kRingThreads) dropout_kernel(DropParams p, Rin
             }
         }
         ring_wait(sh.stages);
+        if constexpr (kShared<A>) group_sync(tpr, g + 1);
         uint4 xr[NCH], yr[GATED ? NCH : 1];
         read_pieces<T, NCH, A>(xr, ring + stage * stage_bytes, L);
         if constexpr (GATED) read_pieces<T, NCH, A>(yr, ring + stage * stage_bytes + row_bytes, L);
+        if constexpr (kShared<A>) group_sync(tpr, g + 1);  // every thread has read the stage
         fill(stage);
         if (++stage == sh.stages) stage = 0;
         philox.row((uint32_t)row);
@@ -247,9 +249,11 @@ __global__ void __launch_bounds__(kGradThreads) dropout_backward_kernel(DropPara
         for (; row < end; row += step) {
             if constexpr (TOKEN) load_gate(row);
             ring_wait(sh.stages);
+            if constexpr (kShared<A>) group_sync(tpr, g + 1);
             uint4 dr[NCH], yr[NCH];
             read_pieces<T, NCH, A>(dr, ring + stage * stage_bytes, L);
             read_pieces<T, NCH, A>(yr, ring + stage * stage_bytes + row_bytes, L);
+            if constexpr (kShared<A>) group_sync(tpr, g + 1);  // every thread has read the stage
             fill(stage);
             if (++stage == sh.stages) stage = 0;
             philox.row((uint32_t)row);
@@ -316,7 +320,7 @@ template <class T, int NCH, Access A, bool GATED>
 static cudaError_t drop_fwd(const DropParams& p, cudaStream_t s) {
     auto k = dropout_kernel<T, NCH, A, GATED>;
     const int tpr = row_threads(p.D);
-    RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, GATED ? 2 : 1, 0, 0, kRingThreads, 2);
+    RingShape sh = ring_shape(tpr, staged_row_bytes(tpr, (int)sizeof(T), A == kVec), GATED ? 2 : 1, 0, 0, kRingThreads, 2);
     sh.smem -= sh.sums_bytes;  // no row sums
     static SmemOptIn opt_in;
     if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
@@ -339,7 +343,7 @@ static cudaError_t drop_bwd(const DropParams& p0, cudaStream_t s) {
     DropParams p = p0;
     auto k = dropout_backward_kernel<T, NCH, A, TOKEN>;
     const int tpr = row_threads(p.D);
-    RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, 2, 0, 0, kGradThreads, TOKEN ? 2 : 1);
+    RingShape sh = ring_shape(tpr, staged_row_bytes(tpr, (int)sizeof(T), A == kVec), 2, 0, 0, kGradThreads, TOKEN ? 2 : 1);
     sh.smem -= sh.sums_bytes;
     static SmemOptIn opt_in;
     if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;

@@ -69,12 +69,12 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
     int stage = 0;
     for (int64_t round = 0; round < rounds; ++round, r += step) {
         ring_wait(sh.stages);
+        if constexpr (kShared<A>) group_sync(tpr, g + 1);
         u64 v[R][P];
         float mean[R], rstd[R];
 #pragma unroll
         for (int k = 0; k < R; ++k) read_row<T, NCH, CE, A>(v[k], ring + stage * stage_bytes + k * row_bytes, L);
-        fill(stage);
-        if (++stage == sh.stages) stage = 0;
+        if constexpr (!kShared<A>) fill(stage);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             u64 s = 0;
@@ -83,6 +83,8 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
             mean[k] = f2lo(s) + f2hi(s);
         }
         sums(mean);
+        if constexpr (kShared<A>) fill(stage);  // every thread has read the stage
+        if (++stage == sh.stages) stage = 0;
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             mean[k] *= inv_d;
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
 template <class T, int NCH, Access A, int R>
 static cudaError_t ln_fwd(const LnFwdParams& p, int tpr, cudaStream_t s) {
     auto k = layer_norm_kernel<T, NCH, A, R>;
-    const RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, R, 0, 0, kRingThreads, 2);
+    const RingShape sh = ring_shape(tpr, staged_row_bytes(tpr, (int)sizeof(T), A == kVec), R, 0, 0, kRingThreads, 2);
     static SmemOptIn opt_in;
     if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
     const int64_t batches = (p.rows + R - 1) / R, need = (batches + sh.groups - 1) / sh.groups;

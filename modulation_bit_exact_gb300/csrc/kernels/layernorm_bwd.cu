@@ -16,14 +16,14 @@
 namespace mbx {
 
 // R rows in registers, x as pairs; gy(k, e) gives pair e of row k's dy * f.  On
-// return x holds xh, and c the coefficients of
+// return x holds xh, and c the coefficients of (then() runs after the first sums)
 //   dx = rstd*gy + k1 + xh*k2,   k1 = -rstd*c1, k2 = -rstd*c2.
 struct RowCoef {
     float rstd, k1, k2;
 };
-template <int R, int NCH, int CE, Access A, class Gy>
+template <int R, int NCH, int CE, Access A, class Gy, class Then>
 __device__ __forceinline__ void ln_row_stats(RowCoef (&c)[R], u64 (&x)[R][NCH * CE / 2], const Lane& L, float inv_d,
-                                             float eps, GroupSums& sums, Gy gy) {
+                                             float eps, GroupSums& sums, Gy gy, Then then) {
     constexpr int H = CE / 2;
     float v[2 * R];
 #pragma unroll
@@ -40,6 +40,7 @@ __device__ __forceinline__ void ln_row_stats(RowCoef (&c)[R], u64 (&x)[R][NCH * 
         v[2 * k + 1] = f2lo(sg[0]) + f2hi(sg[0]);
     }
     sums(v);
+    then();  // every thread of the group has read its rows
 #pragma unroll
     for (int k = 0; k < R; ++k) {
         const float mean = v[2 * k] * inv_d;
@@ -121,6 +122,7 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
     int64_t r = first;
     for (int64_t round = 0; round < rounds; ++round, r += step) {
         ring_wait(sh.stages);
+        if constexpr (kShared<A>) group_sync(tpr, g + 1);
         const char* src = ring + stage * stage_bytes;
         u64 xs[1][NCH * H], dy[NCH * H], gy[NCH * H];
         u64(&x)[NCH * H] = xs[0];
@@ -130,13 +132,15 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
         else read_row<uint16_t, NCH, CE, A>(gy, src + kF * row_bytes, L);
         uint4 res[RES ? NCH : 1];
         if constexpr (RES) read_pieces<T, NCH, A>(res, src + 2 * row_bytes, L);
-        fill(stage);
-        if (++stage == sh.stages) stage = 0;
+        if constexpr (!kShared<A>) fill(stage);
 #pragma unroll
         for (int e = 0; e < NCH * H; ++e) gy[e] = mul2(dy[e], add2(gy[e], one));
         RowCoef ks[1];
         const RowCoef& k = ks[0];
-        ln_row_stats<1, NCH, CE, A>(ks, xs, L, inv_d, p.eps, sums, [&](int, int e) { return gy[e]; });
+        ln_row_stats<1, NCH, CE, A>(ks, xs, L, inv_d, p.eps, sums, [&](int, int e) { return gy[e]; }, [&] {
+            if constexpr (kShared<A>) fill(stage);
+        });
+        if (++stage == sh.stages) stage = 0;
         if (r >= p.rows) continue;
         const u64 rs = f2(k.rstd, k.rstd), a = f2(k.k1, k.k1), b = f2(k.k2, k.k2);
         T* dx_row = static_cast<T*>(p.dx) + r * p.dx_stride + c0;
@@ -233,6 +237,7 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
         int stage = 0;
         for (int round = 0; round < rounds; ++round, dx_row += dx_step) {
             ring_wait(sh.stages);
+            if constexpr (kShared<A>) group_sync(tpr, g + 1);
             const char* src = ring + stage * stage_bytes;
             u64 xs[1][P], dy[P], gy[P];
             u64(&x)[P] = xs[0];
@@ -240,8 +245,7 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
             read_row<T, NCH, CE, A>(dy, src + row_bytes, L);
             uint4 res[RES ? NCH : 1];
             if constexpr (RES) read_pieces<T, NCH, A>(res, src + 2 * row_bytes, L);
-            fill(stage);
-            if (++stage == sh.stages) stage = 0;
+            if constexpr (!kShared<A>) fill(stage);
 #pragma unroll
             for (int e = 0; e < P; e += 2) {
                 const ulonglong2 f = fs[e / 2 * block];
@@ -249,7 +253,10 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
                 gy[e + 1] = mul2(dy[e + 1], f.y);
             }
             RowCoef c[1];
-            ln_row_stats<1, NCH, CE, A>(c, xs, L, inv_d, p.eps, sums, [&](int, int e) { return gy[e]; });
+            ln_row_stats<1, NCH, CE, A>(c, xs, L, inv_d, p.eps, sums, [&](int, int e) { return gy[e]; }, [&] {
+                if constexpr (kShared<A>) fill(stage);
+            });
+            if (++stage == sh.stages) stage = 0;
             if (round * groups + g >= n_rows) continue;
             const u64 rs = f2(c[0].rstd, c[0].rstd), a = f2(c[0].k1, c[0].k1), b = f2(c[0].k2, c[0].k2);
 #pragma unroll
@@ -320,7 +327,7 @@ template <class T, int NCH, Access A, bool RES>
 static cudaError_t ln_bwd_token(const LnBwdParams& p, cudaStream_t s) {
     auto k = ln_backward_token_kernel<T, NCH, A, RES>;
     const int tpr = row_threads(p.D), elem = p.p_f32 ? 4 : 2;
-    const RingShape sh = ring_shape(tpr, 16 * (int)sizeof(T) * tpr, RES ? 3 : 2, 16 * elem * tpr, 0, kRingThreads, 2);
+    const RingShape sh = ring_shape(tpr, staged_row_bytes(tpr, (int)sizeof(T), A == kVec), RES ? 3 : 2, staged_row_bytes(tpr, elem, A == kVec), 0, kRingThreads, 2);
     static SmemOptIn opt_in;
     if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
     const int64_t need = (p.rows + sh.groups - 1) / sh.groups, most = (int64_t)sm_count() * sh.ctas_per_sm;
@@ -333,7 +340,7 @@ static cudaError_t ln_bwd(const LnBwdParams& p0, cudaStream_t s) {
     if (p.seq == 1 && p.factor) return ln_bwd_token<T, NCH, A, RES>(p, s);
     auto k = ln_backward_kernel<T, NCH, A, RES>;
     p.plan = grad_plan(p.rows, p.mod_rows, p.D, (int)sizeof(T));
-    const RingShape sh = grad_shape(p.D, (int)sizeof(T), RES ? 3 : 2);
+    const RingShape sh = grad_shape(p.D, (int)sizeof(T), RES ? 3 : 2, A == kVec);
     static SmemOptIn opt_in;
     if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
     const int64_t units = p.mod_rows * p.plan.parts, most = 1 << 30;

@@ -2,16 +2,21 @@
 //
 // A row group of `tpr` threads (8, 16 or 32 lanes of a warp, or whole warps)
 // works on R rows at a time; thread t owns E = NCH*CE columns of every row.
-// Rows arrive by cp.async in a ring of stages: each thread copies exactly the
-// pieces that it reads, so its own cp.async.wait_group is the only
-// synchronisation, and later rows are in flight while a row is reduced.
+// Rows arrive by cp.async in a ring of stages, and later rows are in flight
+// while a row is reduced.
 //
 // kVec: chunk j of thread t is columns (j*tpr + t)*CE ..., moved in 16-byte
-// pieces.  kScalar (a width that is no multiple of CE, or a row that starts at
-// no 16-byte boundary): element e is column e*tpr + t, moved one at a time
-// (binary32 by 4-byte cp.async; bfloat16, which cp.async does not move alone,
-// by a load and a shared store).  kQuad is kScalar with four consecutive
-// columns of a thread at a time, which share one call of the dropout generator.
+// pieces.  Each thread copies exactly the pieces that it reads, so its own
+// cp.async.wait_group is the only synchronisation.
+//
+// kScalar (a width that is no multiple of CE, or a row that starts at no 16-byte
+// boundary): element e is column e*tpr + t.  The row is copied by its aligned
+// 16-byte pieces, and by 4 bytes at its ends, to the same place modulo 16 bytes,
+// whatever thread owns the columns; so the group meets at a barrier before it
+// reads a stage, and again before the stage is filled anew.  Copied element by
+// element instead, [57394, 561] bfloat16 gradients took 335 us, now TIME us.
+// kQuad is kScalar with four consecutive columns of a thread at a time, which
+// share one call of the dropout generator.
 #pragma once
 
 #include "rowgroup.cuh"
@@ -26,6 +31,11 @@ __device__ __forceinline__ void ring_cp4(void* dst, const void* src) {
     const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
 }
+// The first 2 of 4 bytes; the others are zeroed in shared memory and not read.
+__device__ __forceinline__ void ring_cp2(void* dst, const void* src) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, 2;" ::"r"(d), "l"(src) : "memory");
+}
 __device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the newest stages-1 groups have landed (stages <= 4): the oldest
 // stage is ready.  Its rows go to registers at once and the stage is filled
@@ -39,7 +49,7 @@ __device__ __forceinline__ void ring_wait(int stages) {
 
 // This thread's place in its row group and the columns that it owns.
 struct Lane {
-    int t, tpr;
+    int t, tpr, D;
     int nv;  // kVec: chunks that exist; else elements that exist
 };
 template <int E, int CE, Access A>
@@ -52,7 +62,7 @@ __device__ __forceinline__ Lane make_lane(int t, int tpr, int D) {
         const int units = A == kVec ? D / CE : D;
         nv = units > t ? (units - t + tpr - 1) / tpr : 0;
     }
-    return Lane{t, tpr, nv};
+    return Lane{t, tpr, D, nv};
 }
 // This thread's first column, and how far element e lies beyond it.
 template <int CE, Access A>
@@ -73,6 +83,14 @@ __device__ __forceinline__ void prefetch_row(const Q* row, int D, int t) {
         if (t == 0) prefetch_l2_bulk(row, (uint32_t)(D * (int)sizeof(Q)));
 }
 
+// A staged row that is not kVec begins with this, 16 bytes; its element c lies
+// `shift` + c * size bytes behind.
+struct StagedHead {
+    int shift;       // the row's address modulo 16
+    const void* row;  // the row in memory
+};
+static_assert(sizeof(StagedHead) == 16, "");
+
 // Start the copy of this thread's part of a row to its place in a stage; `row`
 // points at its first column.
 template <class Q, int NCH, int CE, Access A>
@@ -87,18 +105,31 @@ __device__ __forceinline__ void ring_fill(char* dst, const Q* row, const Lane& L
                     ring_cp16(dst + ((j * P + h) * L.tpr + L.t) * 16, row + j * L.tpr * CE + h * (16 / (int)sizeof(Q)));
             }
     } else {
+        const Q* start = row - first_col<CE, A>(L);
+        const int shift = (int)(reinterpret_cast<uintptr_t>(start) & 15);
+        if (L.t == 0) *reinterpret_cast<StagedHead*>(dst) = StagedHead{shift, start};
+        const char* src = reinterpret_cast<const char*>(start) - shift;
+        const int end = shift + L.D * (int)sizeof(Q);
+        dst += sizeof(StagedHead);
+        for (int i = L.t * 16; i < end; i += L.tpr * 16) {
+            if (i >= shift && i + 16 <= end) {
+                ring_cp16(dst + i, src + i);
+                continue;
+            }
 #pragma unroll
-        for (int e = 0; e < NCH * CE; ++e) {
-            const int c = e * L.tpr + L.t;
-            if (e < L.nv) {
-                if constexpr (sizeof(Q) == 4) ring_cp4(dst + c * 4, row + elem_off<A>(e, L));
-                else reinterpret_cast<Q*>(dst)[c] = ld_u16_rw(row + elem_off<A>(e, L));
+            for (int w = i; w < i + 16; w += 4) {  // an end of the row: nothing outside it is read
+                if (w >= shift && w + 4 <= end) ring_cp4(dst + w, src + w);
+                else if (sizeof(Q) == 2 && w >= shift && w + 2 <= end) ring_cp2(dst + w, src + w);
             }
         }
     }
 }
 
-// Chunk j of a staged row as CE/2 pairs (0 where no column exists: see
+// Whether a thread reads what others copied (and the group must meet first).
+template <Access A>
+constexpr bool kShared = A != kVec;
+
+// Chunk j of a staged row as CE/2 pairs (0 where no column exists; kVec: see
 // ring_clear).
 template <class Q, int CE, Access A>
 __device__ __forceinline__ void ring_read(u64 (&p)[CE / 2], const char* src, int j, const Lane& L) {
@@ -116,22 +147,33 @@ __device__ __forceinline__ void ring_read(u64 (&p)[CE / 2], const char* src, int
             }
         }
     } else {
+        const StagedHead& head = *reinterpret_cast<const StagedHead*>(src);
+        const Q* row = reinterpret_cast<const Q*>(src + sizeof(StagedHead) + head.shift) + first_col<CE, A>(L);
 #pragma unroll
         for (int i = 0; i < CE; i += 2) {
             float v[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int c = (j * CE + i + h) * L.tpr + L.t;
-                if constexpr (sizeof(Q) == 4) v[h] = reinterpret_cast<const float*>(src)[c];
-                else v[h] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(src)[c] << 16);
+                const int e = j * CE + i + h;
+                v[h] = 0.0f;
+                if (e < L.nv) {
+                    if constexpr (sizeof(Q) == 4) v[h] = row[elem_off<A>(e, L)];
+                    else v[h] = __uint_as_float((uint32_t)row[elem_off<A>(e, L)] << 16);
+                }
+                // a bfloat16 row that starts in the upper half of a word: cp.async
+                // cannot move its first element alone
+                if (sizeof(Q) == 2 && e == 0 && L.t == 0 && (head.shift & 2))
+                    v[h] = load_elem(static_cast<const Q*>(head.row));
             }
             p[i / 2] = f2(v[0], v[1]);
         }
     }
 }
 
-// Zero this thread's places of a staged row that hold no column and that no
-// copy ever writes, so that reading needs no mask.
+// Before the first fill.  kVec: zero this thread's places that hold no column and
+// that no copy ever writes, so that reading needs no mask.  Else: a head that
+// points nowhere, for a group that has no row in a round and reads the stage all
+// the same.
 template <class Q, int NCH, int CE, Access A>
 __device__ __forceinline__ void ring_clear(char* dst, const Lane& L) {
     if constexpr (A == kVec) {
@@ -139,8 +181,8 @@ __device__ __forceinline__ void ring_clear(char* dst, const Lane& L) {
         for (int j = L.nv; j < NCH; ++j)
             for (int h = 0; h < P; ++h)
                 *reinterpret_cast<uint4*>(dst + ((j * P + h) * L.tpr + L.t) * 16) = make_uint4(0, 0, 0, 0);
-    } else {
-        for (int e = L.nv; e < NCH * CE; ++e) reinterpret_cast<Q*>(dst)[e * L.tpr + L.t] = 0;
+    } else if (L.t == 0) {
+        *reinterpret_cast<StagedHead*>(dst) = StagedHead{0, nullptr};
     }
 }
 
@@ -268,6 +310,14 @@ __device__ __forceinline__ void get_param_chunk(u64 (&v)[CE / 2], const void* p,
     if constexpr (sizeof(T) == 4) get_chunk<float, CE, A>(v, static_cast<const float*>(p) + off, j, L);
     else if (p_f32) get_chunk<float, CE, A>(v, static_cast<const float*>(p) + off, j, L);
     else get_chunk<uint16_t, CE, A>(v, static_cast<const uint16_t*>(p) + off, j, L);
+}
+
+// The threads of a row group meet: a named barrier of its warps, or its lanes of
+// one warp.
+__device__ __forceinline__ void group_sync(int tpr, int bar_id) {
+    if (tpr > 32) named_bar(bar_id, tpr);
+    else if (tpr == 32) __syncwarp();
+    else __syncwarp(((1u << tpr) - 1u) << (threadIdx.x % 32 / tpr * tpr));
 }
 
 // Sums of V values (a power of two, at most 4) over a row group, in every

@@ -16,6 +16,10 @@ int sm_count();  // SMs of the current device; 0 if the runtime cannot tell
 // warp for the short rows, else whole warps.
 inline int row_threads(int D) { return D <= 128 ? 8 : D <= 256 ? 16 : (D + 511) / 512 * 32; }
 
+// Shared memory of one staged row (rowring.cuh): its elements, and for rows that
+// are not 16-byte aligned a head and room for the shift.
+inline int staged_row_bytes(int tpr, int esize, bool vec) { return 16 * esize * tpr + (vec ? 0 : 32); }
+
 // Threads of an SM: the row kernels take up to 96 registers a thread, those
 // that also hold the sums of their columns up to 128.
 constexpr int kRingThreads = 640, kGradThreads = 512;
@@ -43,7 +47,7 @@ struct SmemOptIn {
 struct GradPlan {
     int64_t parts, rows_per_part;
 };
-RingShape grad_shape(int D, int esize, int rows);
+RingShape grad_shape(int D, int esize, int rows, bool vec);
 GradPlan grad_plan(int64_t rows, int64_t mod_rows, int D, int esize);
 int64_t grad_workspace_bytes(int64_t rows, int64_t mod_rows, int D, int esize);
 
