@@ -78,13 +78,12 @@ struct Philox {
 };
 
 // A thread's quads: column / 4 of its elements 4i .. 4i+3.
-template <int NQ, int CE, Access A>
+template <int NQ, int CE>
 __device__ __forceinline__ Philox<NQ> make_philox(const DropParams& p, const Lane& L) {
-    static_assert(A != kScalar, "four columns of a thread are consecutive");
     uint32_t quad[NQ];
 #pragma unroll
     for (int i = 0; i < NQ; ++i)
-        quad[i] = A == kVec && CE == 8 ? (uint32_t)(i / 2 * L.tpr + L.t) * 2 + i % 2 : (uint32_t)(i * L.tpr + L.t);
+        quad[i] = CE == 8 ? (uint32_t)(i / 2 * L.tpr + L.t) * 2 + i % 2 : (uint32_t)(i * L.tpr + L.t);
     return Philox<NQ>(p, quad);
 }
 
@@ -102,12 +101,13 @@ __device__ __forceinline__ u64 keep_fma(u64 v, u64 w, u64 acc, uint32_t a, uint3
 
 // GATED: out = x + gate * drop(y); otherwise out = drop(x).  Rows stream
 // through a ring (rowring.cuh).
-template <class T, int NCH, Access A, bool GATED>
+template <class T, int NCH, bool GATED>
 __global__ void __launch_bounds__(kRingThreads) dropout_kernel(DropParams p, RingShape sh) {
+    constexpr Access A = kVec;
     constexpr int CE = ChunkOf<T>::CE, H = CE / 2, P = NCH * H;
     extern __shared__ __align__(16) char smem[];
     const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr;
-    const Lane L = make_lane<16, CE, A>(t, tpr, p.D);
+    const Lane L = make_lane<CE>(t, tpr, p.D, g + 1);
     char* ring = smem + g * sh.group_bytes;
     const int64_t step = (int64_t)gridDim.x * sh.groups;
     int64_t row = (int64_t)blockIdx.x * sh.groups + g, fill_row = row;
@@ -117,14 +117,14 @@ __global__ void __launch_bounds__(kRingThreads) dropout_kernel(DropParams p, Rin
     }
     grid_dep_wait();  // launched programmatically: the previous kernel has finished
     grid_dep_launch();
-    Philox<P / 2> philox = make_philox<P / 2, CE, A>(p, L);
-    const int row_bytes = sh.row_bytes, stage_bytes = (GATED ? 2 : 1) * row_bytes, c0 = first_col<CE, A>(L);
+    Philox<P / 2> philox = make_philox<P / 2, CE>(p, L);
+    const int row_bytes = sh.row_bytes, stage_bytes = (GATED ? 2 : 1) * row_bytes;
     auto fill = [&](int st) {
         char* dst = ring + st * stage_bytes;
         if (fill_row < p.rows) {
-            ring_fill<T, NCH, CE, A>(dst, static_cast<const T*>(p.x) + fill_row * p.x_stride + c0, L);
+            ring_fill<T, NCH, CE, A>(dst, static_cast<const T*>(p.x) + fill_row * p.x_stride, L);
             if constexpr (GATED)
-                ring_fill<T, NCH, CE, A>(dst + row_bytes, static_cast<const T*>(p.y) + fill_row * p.y_stride + c0, L);
+                ring_fill<T, NCH, CE, A>(dst + row_bytes, static_cast<const T*>(p.y) + fill_row * p.y_stride, L);
         }
         fill_row += step;
         ring_commit();
@@ -142,22 +142,20 @@ __global__ void __launch_bounds__(kRingThreads) dropout_kernel(DropParams p, Rin
 #pragma unroll
                 for (int j = 0; j < NCH; ++j) {
                     u64 c[H];
-                    get_param_chunk<T, CE, A>(c, p.gate, m * p.gate_stride + c0, p.p_f32, j, L);
+                    get_param_chunk<T, CE, A>(c, p.gate, m * p.gate_stride, p.p_f32, j, L);
 #pragma unroll
                     for (int i = 0; i < H; ++i) gate[j * H + i] = mul2(c[i], inv);
                 }
             }
         }
         ring_wait(sh.stages);
-        if constexpr (kShared<A>) group_sync(tpr, g + 1);
         uint4 xr[NCH], yr[GATED ? NCH : 1];
         read_pieces<T, NCH, A>(xr, ring + stage * stage_bytes, L);
         if constexpr (GATED) read_pieces<T, NCH, A>(yr, ring + stage * stage_bytes + row_bytes, L);
-        if constexpr (kShared<A>) group_sync(tpr, g + 1);  // every thread has read the stage
         fill(stage);
         if (++stage == sh.stages) stage = 0;
         philox.row((uint32_t)row);
-        T* dst = static_cast<T*>(p.out) + row * p.out_stride + c0;
+        T* dst = static_cast<T*>(p.out) + row * p.out_stride;
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
             u64 o[H];
@@ -174,7 +172,98 @@ __global__ void __launch_bounds__(kRingThreads) dropout_kernel(DropParams p, Rin
                     else o[i + h] = keep_pair(mul2(x, inv), w0, w1, p.threshold);
                 }
             }
-            if (has_chunk<A>(j, L)) put_chunk<T, CE, A>(dst, o, j, L);
+            put_row_chunk<T, CE, A>(dst, nullptr, o, j, L);
+        }
+    }
+}
+
+// The same for rows that are not 16-byte aligned or whose width is no multiple of
+// a chunk.  A thread takes an aligned 16-byte piece of the output row, so both
+// accesses are whole pieces where x and y lie the same way to 16 bytes as out
+// does (elements at the row's ends, and where they do not); there is no stage and
+// no barrier.  A piece starts anywhere within a quad, so its last columns belong
+// to the first quad of the next lane, which passes their bits down: a warp's last
+// lane only computes them, and a warp takes 31 pieces at a time.
+// [4096, 2731] binary32: 22.3 us by single elements, 27.7 through kShift stages,
+// 26.8 when a thread computes both quads, 19.5 here (2728 columns: 18.6).
+template <class T, bool GATED>
+__global__ void __launch_bounds__(256) dropout_shift_kernel(DropParams p, int tpr) {
+    constexpr int CE = ChunkOf<T>::CE, NQ = CE / 4;
+    const int g = threadIdx.x / tpr, groups = blockDim.x / tpr, lane = threadIdx.x % 32;
+    const int warp = threadIdx.x % tpr / 32, warps = tpr / 32;
+    grid_dep_wait();
+    grid_dep_launch();
+    const uint64_t seed = (uint64_t)p.rng[0], ctr = (uint64_t)p.rng[1] + (uint64_t)p.offset;
+    uint32_t k0[10], k1[10];
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        k0[r] = (uint32_t)seed + r * kW0;
+        k1[r] = hi32(seed) + r * kW1;
+        asm volatile("" : "+r"(k0[r]), "+r"(k1[r]));
+    }
+    const int64_t step = (int64_t)gridDim.x * groups;
+    for (int64_t row = (int64_t)blockIdx.x * groups + g; row < p.rows; row += step) {
+        const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
+        const T* y = GATED ? static_cast<const T*>(p.y) + row * p.y_stride : x;
+        T* out = static_cast<T*>(p.out) + row * p.out_stride;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(out);
+        const bool alike = ((reinterpret_cast<uintptr_t>(x) ^ at) & 15) == 0 && ((reinterpret_cast<uintptr_t>(y) ^ at) & 15) == 0;
+        const int shift = (int)(at & 15) / (int)sizeof(T);
+        const int64_t gate = GATED ? (p.mod_rows == p.rows ? row : p.mod_rows == 1 ? 0 : row / p.seq) * p.gate_stride : 0;
+        for (int c = warp * 31 * CE - shift; c < p.D; c += warps * 31 * CE) {  // the same for a warp
+            const int c0 = c + lane * CE;
+            const bool mine = lane < 31 && c0 < p.D, whole = mine && c0 >= 0 && c0 + CE <= p.D;
+            float v[CE], w[CE];
+            if (whole && alike) {
+                const uint4 rx = ld_stream_rw(x + c0);
+                if constexpr (GATED) widen_chunk(ld_stream_rw(y + c0), w);
+                widen_chunk(rx, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < CE; ++i) {
+                    const bool in = mine && c0 + i >= 0 && c0 + i < p.D;
+                    v[i] = in ? load_elem(x + c0 + i) : 0.0f;
+                    if constexpr (GATED) w[i] = in ? load_elem(y + c0 + i) : 0.0f;
+                }
+            }
+            const int quad = c0 >> 2, rem = c0 & 3;  // c0 = 4*quad + rem
+            uint32_t keep = 0;
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                uint32_t u0 = (uint32_t)(quad + q), u1 = (uint32_t)row, u2 = (uint32_t)ctr, u3 = hi32(ctr);
+#pragma unroll
+                for (int r = 0; r < 10; ++r) {
+                    const uint64_t a = (uint64_t)kM0 * u0, b = (uint64_t)kM1 * u2;
+                    u0 = hi32(b) ^ u1 ^ k0[r];
+                    u1 = (uint32_t)b;
+                    u2 = hi32(a) ^ u3 ^ k1[r];
+                    u3 = (uint32_t)a;
+                }
+                const uint32_t thr = p.threshold;
+                keep |= ((u0 >= thr ? 1u : 0u) | (u1 >= thr ? 2u : 0u) | (u2 >= thr ? 4u : 0u) | (u3 >= thr ? 8u : 0u)) << (4 * q);
+            }
+            keep |= (__shfl_down_sync(0xffffffffu, keep, 1) & 15u) << (4 * NQ);
+            keep >>= rem;  // bit i: element i of the piece
+            if (!mine) continue;
+#pragma unroll
+            for (int i = 0; i < CE; ++i) {
+                if constexpr (GATED) {
+                    if (c0 + i >= 0 && c0 + i < p.D && (keep >> i & 1)) {
+                        const float f = p.p_f32 ? load_elem(static_cast<const float*>(p.gate) + gate + c0 + i)
+                                                : load_elem(static_cast<const uint16_t*>(p.gate) + gate + c0 + i);
+                        v[i] = fmaf(w[i], f * p.inv_keep, v[i]);
+                    }
+                } else {
+                    v[i] = (keep >> i & 1) ? v[i] * p.inv_keep : 0.0f;
+                }
+            }
+            if (whole) {
+                st_v4(out + c0, narrow_chunk(v));
+            } else {
+#pragma unroll
+                for (int i = 0; i < CE; ++i)
+                    if (c0 + i >= 0 && c0 + i < p.D) store_elem(out + c0 + i, v[i]);
+            }
         }
     }
 }
@@ -187,7 +276,7 @@ __global__ void __launch_bounds__(kGradThreads) dropout_backward_kernel(DropPara
     constexpr int CE = ChunkOf<T>::CE, H = CE / 2, P = NCH * H;
     extern __shared__ __align__(16) char smem[];
     const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr, groups = sh.groups;
-    const Lane L = make_lane<16, CE, A>(t, tpr, p.D);
+    const Lane L = make_lane<CE>(t, tpr, p.D, g + 1);
     char* ring = smem + g * sh.group_bytes;
     {
         int64_t r = (int64_t)blockIdx.x * groups + g;
@@ -202,8 +291,8 @@ __global__ void __launch_bounds__(kGradThreads) dropout_backward_kernel(DropPara
     }
     grid_dep_wait();
     grid_dep_launch();
-    Philox<P / 2> philox = make_philox<P / 2, CE, A>(p, L);
-    const int row_bytes = sh.row_bytes, stage_bytes = 2 * row_bytes, c0 = first_col<CE, A>(L);
+    Philox<P / 2> philox = make_philox<P / 2, CE>(p, L);
+    const int row_bytes = sh.row_bytes, stage_bytes = 2 * row_bytes;
     const u64 inv = f2(p.inv_keep, p.inv_keep);
     const int64_t units = TOKEN ? 1 : p.mod_rows * p.plan.parts;
     for (int64_t unit = TOKEN ? 0 : blockIdx.x; unit < units; unit += gridDim.x) {
@@ -223,8 +312,8 @@ __global__ void __launch_bounds__(kGradThreads) dropout_backward_kernel(DropPara
         auto fill = [&](int st) {
             char* dst = ring + st * stage_bytes;
             if (fill_row < end) {
-                ring_fill<T, NCH, CE, A>(dst, static_cast<const T*>(p.x) + fill_row * p.x_stride + c0, L);
-                ring_fill<T, NCH, CE, A>(dst + row_bytes, static_cast<const T*>(p.y) + fill_row * p.y_stride + c0, L);
+                ring_fill<T, NCH, CE, A>(dst, static_cast<const T*>(p.x) + fill_row * p.x_stride, L);
+                ring_fill<T, NCH, CE, A>(dst + row_bytes, static_cast<const T*>(p.y) + fill_row * p.y_stride, L);
             }
             fill_row += step;
             ring_commit();
@@ -235,7 +324,7 @@ __global__ void __launch_bounds__(kGradThreads) dropout_backward_kernel(DropPara
 #pragma unroll
             for (int j = 0; j < NCH; ++j) {
                 u64 c[H];
-                get_param_chunk<T, CE, A>(c, p.gate, m * p.gate_stride + c0, p.p_f32, j, L);
+                get_param_chunk<T, CE, A>(c, p.gate, m * p.gate_stride, p.p_f32, j, L);
 #pragma unroll
                 for (int i = 0; i < H; ++i) gate[j * H + i] = mul2(c[i], inv);
             }
@@ -249,18 +338,19 @@ __global__ void __launch_bounds__(kGradThreads) dropout_backward_kernel(DropPara
         for (; row < end; row += step) {
             if constexpr (TOKEN) load_gate(row);
             ring_wait(sh.stages);
-            if constexpr (kShared<A>) group_sync(tpr, g + 1);
+            if constexpr (A == kShift) group_sync(L);
             uint4 dr[NCH], yr[NCH];
             read_pieces<T, NCH, A>(dr, ring + stage * stage_bytes, L);
             read_pieces<T, NCH, A>(yr, ring + stage * stage_bytes + row_bytes, L);
-            if constexpr (kShared<A>) group_sync(tpr, g + 1);  // every thread has read the stage
-            fill(stage);
-            if (++stage == sh.stages) stage = 0;
+            if constexpr (A == kVec) fill(stage);
+            else group_sync(L);  // every thread has read the stage
             philox.row((uint32_t)row);
-            T* dst = static_cast<T*>(p.out) + row * p.out_stride + c0;
+            T* dst = static_cast<T*>(p.out) + row * p.out_stride;
+            char* out = ring + stage * stage_bytes;
+            u64 dgate[TOKEN ? NCH : 1][H];
 #pragma unroll
             for (int j = 0; j < NCH; ++j) {
-                u64 o[H], og[H];
+                u64 o[H];
 #pragma unroll
                 for (int i = 0; i < H; i += 2) {
                     const int e = j * H + i;
@@ -271,15 +361,24 @@ __global__ void __launch_bounds__(kGradThreads) dropout_backward_kernel(DropPara
                         const u64 d = piece_pair<T>(dr, e + h);
                         const u64 y = piece_pair<T>(yr, e + h);
                         o[i + h] = keep_pair(mul2(d, gate[e + h]), w0, w1, p.threshold);
-                        if constexpr (TOKEN) og[i + h] = keep_pair(mul2(mul2(d, inv), y), w0, w1, p.threshold);
+                        if constexpr (TOKEN) dgate[j][i + h] = keep_pair(mul2(mul2(d, inv), y), w0, w1, p.threshold);
                         else acc[e + h] = keep_fma(d, y, acc[e + h], w0, w1, p.threshold);
                     }
                 }
-                if (!has_chunk<A>(j, L)) continue;
-                put_chunk<T, CE, A>(dst, o, j, L);
-                if constexpr (TOKEN)
-                    if (p.dgate) put_param_chunk<T, CE, A>(p.dgate, row * p.dgate_stride + c0, p.p_f32, og, j, L);
+                put_row_chunk<T, CE, A>(dst, out, o, j, L);
             }
+            if constexpr (A == kShift) flush_row(dst, out, L);
+            if constexpr (TOKEN) {
+                if (p.dgate) {
+                    const int64_t off = row * p.dgate_stride;
+#pragma unroll
+                    for (int j = 0; j < NCH; ++j)
+                        put_param_row_chunk<T, CE, A>(p.dgate, off, p.p_f32, out, dgate[j], j, L);
+                    if constexpr (A == kShift) flush_param_row<T>(p.dgate, off, p.p_f32, out, L);
+                }
+            }
+            if constexpr (A == kShift) fill(stage);
+            if (++stage == sh.stages) stage = 0;
         }
         if constexpr (!TOKEN) {
             if (p.dgate == nullptr) continue;
@@ -301,13 +400,13 @@ __global__ void __launch_bounds__(kGradThreads) dropout_backward_kernel(DropPara
             if (g == 0) {
 #pragma unroll
                 for (int j = 0; j < NCH; ++j) {
-                    if (!has_chunk<A>(j, L)) continue;
+                    if (j >= L.nv) continue;
                     u64 c[H];
 #pragma unroll
                     for (int i = 0; i < H; ++i) c[i] = mul2(acc[j * H + i], inv);
                     if (p.plan.parts == 1)
-                        put_param_chunk<T, CE, A>(p.dgate, seg * p.dgate_stride + c0, p.p_f32, c, j, L);
-                    else put_chunk<float, CE, A>(p.ws + unit * p.D + c0, c, j, L);
+                        put_param_chunk<T, CE, A>(p.dgate, seg * p.dgate_stride, p.p_f32, c, j, L);
+                    else put_chunk<float, CE, A>(p.ws + unit * p.D, c, j, L);
                 }
             }
         }
@@ -316,11 +415,11 @@ __global__ void __launch_bounds__(kGradThreads) dropout_backward_kernel(DropPara
 
 // ---------------------------------------------------------------- launch
 
-template <class T, int NCH, Access A, bool GATED>
+template <class T, int NCH, bool GATED>
 static cudaError_t drop_fwd(const DropParams& p, cudaStream_t s) {
-    auto k = dropout_kernel<T, NCH, A, GATED>;
+    auto k = dropout_kernel<T, NCH, GATED>;
     const int tpr = row_threads(p.D);
-    RingShape sh = ring_shape(tpr, staged_row_bytes(tpr, (int)sizeof(T), A == kVec), GATED ? 2 : 1, 0, 0, kRingThreads, 2);
+    RingShape sh = ring_shape(tpr, staged_row_bytes(tpr, (int)sizeof(T), true), GATED ? 2 : 1, 0, 0, kRingThreads, 2);
     sh.smem -= sh.sums_bytes;  // no row sums
     static SmemOptIn opt_in;
     if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
@@ -328,10 +427,20 @@ static cudaError_t drop_fwd(const DropParams& p, cudaStream_t s) {
     return launch_pdl(k, (unsigned)(need < most ? need : most), sh.groups * tpr, sh.smem, s, p, sh);
 }
 
+template <class T, bool GATED>
+static cudaError_t drop_fwd_shift(const DropParams& p, cudaStream_t s) {
+    auto k = dropout_shift_kernel<T, GATED>;
+    const int warps = (p.D / ChunkOf<T>::CE + 2 + 30) / 31;  // 31 pieces of a row each
+    const int tpr = warps >= 8 ? 256 : warps * 32, groups = 256 / tpr;
+    const int grid = grid_for_rows(reinterpret_cast<const void*>(k), p.rows, groups, groups * tpr);
+    if (grid < 0) return cudaErrorUnknown;
+    return launch_pdl(k, grid, groups * tpr, 0, s, p, tpr);
+}
+
 template <class T, int NCH>
 static cudaError_t drop_fwd_any(const DropParams& p, bool vec, cudaStream_t s) {
-    if (vec) return p.gate ? drop_fwd<T, NCH, kVec, true>(p, s) : drop_fwd<T, NCH, kVec, false>(p, s);
-    return p.gate ? drop_fwd<T, NCH, kQuad, true>(p, s) : drop_fwd<T, NCH, kQuad, false>(p, s);
+    if (vec) return p.gate ? drop_fwd<T, NCH, true>(p, s) : drop_fwd<T, NCH, false>(p, s);
+    return p.gate ? drop_fwd_shift<T, true>(p, s) : drop_fwd_shift<T, false>(p, s);
 }
 
 cudaError_t launch_dropout(const DropParams& p, bool f32, bool vec, cudaStream_t s) {
@@ -362,8 +471,8 @@ static cudaError_t drop_bwd(const DropParams& p0, cudaStream_t s) {
 
 template <class T, int NCH>
 static cudaError_t drop_bwd_any(const DropParams& p, bool vec, cudaStream_t s) {
-    if (p.seq == 1) return vec ? drop_bwd<T, NCH, kVec, true>(p, s) : drop_bwd<T, NCH, kQuad, true>(p, s);
-    return vec ? drop_bwd<T, NCH, kVec, false>(p, s) : drop_bwd<T, NCH, kQuad, false>(p, s);
+    if (p.seq == 1) return vec ? drop_bwd<T, NCH, kVec, true>(p, s) : drop_bwd<T, NCH, kShift, true>(p, s);
+    return vec ? drop_bwd<T, NCH, kVec, false>(p, s) : drop_bwd<T, NCH, kShift, false>(p, s);
 }
 
 cudaError_t launch_dropout_backward(const DropParams& p, bool f32, bool vec, cudaStream_t s) {

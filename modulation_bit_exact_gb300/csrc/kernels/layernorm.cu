@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
     constexpr int CE = ChunkOf<T>::CE, P = NCH * CE / 2;
     extern __shared__ __align__(16) char smem[];
     const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr;
-    const Lane L = make_lane<16, CE, A>(t, tpr, p.D);
+    const Lane L = make_lane<CE>(t, tpr, p.D, g + 1);
     GroupSums sums = group_sums(smem, sh, g, t);
     char* ring = smem + sh.sums_bytes + sh.fixed_bytes + g * sh.group_bytes;
     const float inv_d = 1.0f / (float)p.D;
@@ -46,21 +46,22 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
         u64 c[CE / 2];
 #pragma unroll
         for (int i = 0; i < CE / 2; ++i) c[i] = f2(1.0f, 1.0f);
-        if (p.weight) get_param_chunk<T, CE, A>(c, p.weight, first_col<CE, A>(L), p.p_f32, j, L);
+        if (p.weight) get_param_chunk<T, CE, A>(c, p.weight, 0, p.p_f32, j, L);
 #pragma unroll
         for (int i = 0; i < CE / 2; ++i) w[j * (CE / 2) + i] = c[i], c[i] = 0;
-        if (p.bias) get_param_chunk<T, CE, A>(c, p.bias, first_col<CE, A>(L), p.p_f32, j, L);
+        if (p.bias) get_param_chunk<T, CE, A>(c, p.bias, 0, p.p_f32, j, L);
 #pragma unroll
         for (int i = 0; i < CE / 2; ++i) b[j * (CE / 2) + i] = c[i];
     }
 
-    const int row_bytes = sh.row_bytes, stage_bytes = R * row_bytes, c0 = first_col<CE, A>(L);
+    const int row_bytes = sh.row_bytes, stage_bytes = R * row_bytes;
     auto fill = [&](int st) {
         char* dst = ring + st * stage_bytes;
 #pragma unroll
         for (int k = 0; k < R; ++k)
             if (fill_row + k < p.rows)
-                ring_fill<T, NCH, CE, A>(dst + k * row_bytes, static_cast<const T*>(p.x) + (fill_row + k) * p.x_stride + c0, L);
+                ring_fill<T, NCH, CE, A>(dst + k * row_bytes, static_cast<const T*>(p.x) + (fill_row + k) * p.x_stride, L);
+            else if constexpr (A == kShift) ring_clear<T, NCH, CE, A>(dst + k * row_bytes, L);
         fill_row += step;
         ring_commit();
     };
@@ -69,12 +70,12 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
     int stage = 0;
     for (int64_t round = 0; round < rounds; ++round, r += step) {
         ring_wait(sh.stages);
-        if constexpr (kShared<A>) group_sync(tpr, g + 1);
+        if constexpr (A == kShift) group_sync(L);
         u64 v[R][P];
         float mean[R], rstd[R];
 #pragma unroll
         for (int k = 0; k < R; ++k) read_row<T, NCH, CE, A>(v[k], ring + stage * stage_bytes + k * row_bytes, L);
-        if constexpr (!kShared<A>) fill(stage);
+        if constexpr (A == kVec) fill(stage);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             u64 s = 0;
@@ -83,8 +84,6 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
             mean[k] = f2lo(s) + f2hi(s);
         }
         sums(mean);
-        if constexpr (kShared<A>) fill(stage);  // every thread has read the stage
-        if (++stage == sh.stages) stage = 0;
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             mean[k] *= inv_d;
@@ -106,19 +105,21 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
             if (r + k >= p.rows) continue;
             const float rs1 = rsqrtf(rstd[k] * inv_d + p.eps);
             const u64 rs = f2(rs1, rs1);
-            T* dst = static_cast<T*>(p.out) + (r + k) * p.out_stride + c0;
+            T* dst = static_cast<T*>(p.out) + (r + k) * p.out_stride;
 #pragma unroll
             for (int j = 0; j < NCH; ++j) {
-                if (!has_chunk<A>(j, L)) continue;
                 u64 c[CE / 2];
 #pragma unroll
                 for (int i = 0; i < CE / 2; ++i) {
                     const int e = j * (CE / 2) + i;
                     c[i] = fma2(mul2(v[k][e], rs), w[e], b[e]);
                 }
-                put_chunk<T, CE, A>(dst, c, j, L);
+                put_row_chunk<T, CE, A>(dst, ring + stage * stage_bytes + k * row_bytes, c, j, L);
             }
+            if constexpr (A == kShift) flush_row(dst, ring + stage * stage_bytes + k * row_bytes, L);
         }
+        if constexpr (A == kShift) fill(stage);
+        if (++stage == sh.stages) stage = 0;
     }
 }
 
@@ -138,7 +139,7 @@ static cudaError_t ln_fwd_r(const LnFwdParams& p, bool vec, cudaStream_t s) {
     const int tpr = row_threads(p.D);
     // two rows a round while every SM has several
     const bool two = p.rows >= 8 * (int64_t)sm_count();
-    if (!vec) return ln_fwd<T, NCH, kScalar, 1>(p, tpr, s);
+    if (!vec) return ln_fwd<T, NCH, kShift, 1>(p, tpr, s);
     return two ? ln_fwd<T, NCH, kVec, 2>(p, tpr, s) : ln_fwd<T, NCH, kVec, 1>(p, tpr, s);
 }
 

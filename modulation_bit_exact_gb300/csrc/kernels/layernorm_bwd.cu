@@ -16,14 +16,14 @@
 namespace mbx {
 
 // R rows in registers, x as pairs; gy(k, e) gives pair e of row k's dy * f.  On
-// return x holds xh, and c the coefficients of (then() runs after the first sums)
+// return x holds xh, and c the coefficients of
 //   dx = rstd*gy + k1 + xh*k2,   k1 = -rstd*c1, k2 = -rstd*c2.
 struct RowCoef {
     float rstd, k1, k2;
 };
-template <int R, int NCH, int CE, Access A, class Gy, class Then>
+template <int R, int NCH, int CE, Access A, class Gy>
 __device__ __forceinline__ void ln_row_stats(RowCoef (&c)[R], u64 (&x)[R][NCH * CE / 2], const Lane& L, float inv_d,
-                                             float eps, GroupSums& sums, Gy gy, Then then) {
+                                             float eps, GroupSums& sums, Gy gy) {
     constexpr int H = CE / 2;
     float v[2 * R];
 #pragma unroll
@@ -40,7 +40,6 @@ __device__ __forceinline__ void ln_row_stats(RowCoef (&c)[R], u64 (&x)[R][NCH * 
         v[2 * k + 1] = f2lo(sg[0]) + f2hi(sg[0]);
     }
     sums(v);
-    then();  // every thread of the group has read its rows
 #pragma unroll
     for (int k = 0; k < R; ++k) {
         const float mean = v[2 * k] * inv_d;
@@ -80,7 +79,7 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
     constexpr int kF = RES ? 3 : 2;  // a stage: x, dy, the residual's gradient, the factor
     extern __shared__ __align__(16) char smem[];
     const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr;
-    const Lane L = make_lane<16, CE, A>(t, tpr, p.D);
+    const Lane L = make_lane<CE>(t, tpr, p.D, g + 1);
     GroupSums sums = group_sums(smem, sh, g, t);
     char* ring = smem + sh.sums_bytes + sh.fixed_bytes + g * sh.group_bytes;
     const float inv_d = 1.0f / (float)p.D;
@@ -93,7 +92,6 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
     grid_dep_launch();
     const int row_bytes = sh.row_bytes, stage_bytes = kF * row_bytes + sh.extra_bytes;
     const int64_t rounds = (p.rows + step - 1) / step;  // the same for every group
-    const int c0 = first_col<CE, A>(L);
     const u64 one = f2(p.factor_add, p.factor_add);
     int64_t fill_row = first;
     for (int i = 0; i < sh.stages; ++i) {
@@ -105,14 +103,16 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
     auto fill = [&](int st) {
         char* dst = ring + st * stage_bytes;
         if (fill_row < p.rows) {
-            ring_fill<T, NCH, CE, A>(dst, static_cast<const T*>(p.x) + fill_row * p.x_stride + c0, L);
-            ring_fill<T, NCH, CE, A>(dst + row_bytes, static_cast<const T*>(p.dout) + fill_row * p.dout_stride + c0, L);
+            ring_fill<T, NCH, CE, A>(dst, static_cast<const T*>(p.x) + fill_row * p.x_stride, L);
+            ring_fill<T, NCH, CE, A>(dst + row_bytes, static_cast<const T*>(p.dout) + fill_row * p.dout_stride, L);
             if constexpr (RES)
-                ring_fill<T, NCH, CE, A>(dst + 2 * row_bytes, static_cast<const T*>(p.dres) + fill_row * p.dres_stride + c0, L);
-            const int64_t f0 = fill_row * p.factor_stride + c0;
+                ring_fill<T, NCH, CE, A>(dst + 2 * row_bytes, static_cast<const T*>(p.dres) + fill_row * p.dres_stride, L);
+            const int64_t f0 = fill_row * p.factor_stride;
             if (sizeof(T) == 4 || p.p_f32)
                 ring_fill<float, NCH, CE, A>(dst + kF * row_bytes, static_cast<const float*>(p.factor) + f0, L);
             else ring_fill<uint16_t, NCH, CE, A>(dst + kF * row_bytes, static_cast<const uint16_t*>(p.factor) + f0, L);
+        } else if constexpr (A == kShift) {
+            for (int o = 0; o <= kF; ++o) ring_clear<T, NCH, CE, A>(dst + o * row_bytes, L);
         }
         fill_row += step;
         ring_commit();
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
     int64_t r = first;
     for (int64_t round = 0; round < rounds; ++round, r += step) {
         ring_wait(sh.stages);
-        if constexpr (kShared<A>) group_sync(tpr, g + 1);
+        if constexpr (A == kShift) group_sync(L);
         const char* src = ring + stage * stage_bytes;
         u64 xs[1][NCH * H], dy[NCH * H], gy[NCH * H];
         u64(&x)[NCH * H] = xs[0];
@@ -132,34 +132,56 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
         else read_row<uint16_t, NCH, CE, A>(gy, src + kF * row_bytes, L);
         uint4 res[RES ? NCH : 1];
         if constexpr (RES) read_pieces<T, NCH, A>(res, src + 2 * row_bytes, L);
-        if constexpr (!kShared<A>) fill(stage);
+        if constexpr (A == kVec) fill(stage);
 #pragma unroll
         for (int e = 0; e < NCH * H; ++e) gy[e] = mul2(dy[e], add2(gy[e], one));
         RowCoef ks[1];
         const RowCoef& k = ks[0];
-        ln_row_stats<1, NCH, CE, A>(ks, xs, L, inv_d, p.eps, sums, [&](int, int e) { return gy[e]; }, [&] {
-            if constexpr (kShared<A>) fill(stage);
-        });
-        if (++stage == sh.stages) stage = 0;
-        if (r >= p.rows) continue;
-        const u64 rs = f2(k.rstd, k.rstd), a = f2(k.k1, k.k1), b = f2(k.k2, k.k2);
-        T* dx_row = static_cast<T*>(p.dx) + r * p.dx_stride + c0;
+        ln_row_stats<1, NCH, CE, A>(ks, xs, L, inv_d, p.eps, sums, [&](int, int e) { return gy[e]; });
+        if (r < p.rows) {
+            const u64 rs = f2(k.rstd, k.rstd), a = f2(k.k1, k.k1), b = f2(k.k2, k.k2);
+            T* dx_row = static_cast<T*>(p.dx) + r * p.dx_stride;
+            char* out = ring + stage * stage_bytes;  // kShift: x and dy have been read
+            const int64_t f_row = r * p.dfactor_stride, s_row = r * p.dshift_stride;
 #pragma unroll
-        for (int j = 0; j < NCH; ++j) {
-            if (!has_chunk<A>(j, L)) continue;
-            u64 dx[H], xd[H], d[H];
+            for (int j = 0; j < NCH; ++j) {
+                u64 dx[H], xd[H], d[H];
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                const int e = j * H + i;
-                dx[i] = fma2(x[e], b, fma2(gy[e], rs, a));
-                if constexpr (RES) dx[i] = add2(dx[i], piece_pair<T>(res, e));
-                xd[i] = mul2(x[e], dy[e]);
-                d[i] = dy[e];
+                for (int i = 0; i < H; ++i) {
+                    const int e = j * H + i;
+                    dx[i] = fma2(x[e], b, fma2(gy[e], rs, a));
+                    if constexpr (RES) dx[i] = add2(dx[i], piece_pair<T>(res, e));
+                    xd[i] = mul2(x[e], dy[e]);
+                    d[i] = dy[e];
+                }
+                put_row_chunk<T, CE, A>(dx_row, out, dx, j, L);
+                if constexpr (A == kVec) {
+                    if (p.dfactor) put_param_row_chunk<T, CE, A>(p.dfactor, f_row, p.p_f32, nullptr, xd, j, L);
+                    if (p.dshift) put_param_row_chunk<T, CE, A>(p.dshift, s_row, p.p_f32, nullptr, d, j, L);
+                }
             }
-            put_chunk<T, CE, A>(dx_row, dx, j, L);
-            if (p.dfactor) put_param_chunk<T, CE, A>(p.dfactor, r * p.dfactor_stride + c0, p.p_f32, xd, j, L);
-            if (p.dshift) put_param_chunk<T, CE, A>(p.dshift, r * p.dshift_stride + c0, p.p_f32, d, j, L);
+            if constexpr (A == kShift) {
+                flush_row(dx_row, out, L);
+#pragma unroll 1
+                for (int which = 0; which < 2; ++which) {  // the stage holds one row at a time
+                    void* to = which ? p.dshift : p.dfactor;
+                    if (!to) continue;
+                    const int64_t off = which ? s_row : f_row;
+#pragma unroll
+                    for (int j = 0; j < NCH; ++j) {
+                        u64 v[H];
+#pragma unroll
+                        for (int i = 0; i < H; ++i) v[i] = which ? dy[j * H + i] : mul2(x[j * H + i], dy[j * H + i]);
+                        put_param_row_chunk<T, CE, A>(to, off, p.p_f32, out, v, j, L);
+                    }
+                    flush_param_row<T>(to, off, p.p_f32, out, L);
+                }
+            }
+        } else if constexpr (A == kShift) {
+            group_sync(L);  // every thread has read the stage
         }
+        if constexpr (A == kShift) fill(stage);
+        if (++stage == sh.stages) stage = 0;
     }
 }
 
@@ -172,7 +194,7 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
     constexpr int CE = ChunkOf<T>::CE, H = CE / 2, P = NCH * H;
     extern __shared__ __align__(16) char smem[];
     const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr, groups = sh.groups;
-    const Lane L = make_lane<16, CE, A>(t, tpr, p.D);
+    const Lane L = make_lane<CE>(t, tpr, p.D, g + 1);
     GroupSums sums = group_sums(smem, sh, g, t);
     // the factor lives in shared memory, each thread's own copy, so that x, dy
     // and the two sums of every column fit in registers
@@ -191,17 +213,16 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
     grid_dep_wait();
     grid_dep_launch();
     const int row_bytes = sh.row_bytes, stage_bytes = (RES ? 3 : 2) * row_bytes;
-    const int c0 = first_col<CE, A>(L);
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
         const int64_t seg = unit / p.plan.parts, part = unit - seg * p.plan.parts;
         const int64_t r0 = seg * p.seq + part * p.plan.rows_per_part;
         const int64_t left = (seg + 1) * p.seq - r0;
         const int n_rows = (int)(left < p.plan.rows_per_part ? left : p.plan.rows_per_part);
         const int rounds = (n_rows + groups - 1) / groups;
-        const T* nx = static_cast<const T*>(p.x) + (r0 + g) * p.x_stride + c0;
-        const T* nd = static_cast<const T*>(p.dout) + (r0 + g) * p.dout_stride + c0;
-        const T* nr = RES ? static_cast<const T*>(p.dres) + (r0 + g) * p.dres_stride + c0 : nullptr;
-        T* dx_row = static_cast<T*>(p.dx) + (r0 + g) * p.dx_stride + c0;
+        const T* nx = static_cast<const T*>(p.x) + (r0 + g) * p.x_stride;
+        const T* nd = static_cast<const T*>(p.dout) + (r0 + g) * p.dout_stride;
+        const T* nr = RES ? static_cast<const T*>(p.dres) + (r0 + g) * p.dres_stride : nullptr;
+        T* dx_row = static_cast<T*>(p.dx) + (r0 + g) * p.dx_stride;
         for (int i = 0; i < sh.stages * (RES ? 3 : 2); ++i) ring_clear<T, NCH, CE, A>(ring + i * row_bytes, L);
         int fill_row = g;
         const int64_t x_step = groups * p.x_stride, d_step = groups * p.dout_stride, r_step = groups * p.dres_stride,
@@ -212,6 +233,8 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
                 ring_fill<T, NCH, CE, A>(dst, nx, L);
                 ring_fill<T, NCH, CE, A>(dst + row_bytes, nd, L);
                 if constexpr (RES) ring_fill<T, NCH, CE, A>(dst + 2 * row_bytes, nr, L);
+            } else if constexpr (A == kShift) {
+                for (int o = 0; o < (RES ? 3 : 2); ++o) ring_clear<T, NCH, CE, A>(dst + o * row_bytes, L);
             }
             fill_row += groups;
             nx += x_step;
@@ -226,7 +249,7 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
             u64 c[H];
 #pragma unroll
             for (int i = 0; i < H; ++i) c[i] = f2(1.0f, 1.0f);
-            if (p.factor) get_param_chunk<T, CE, A>(c, p.factor, seg * p.factor_stride + c0, p.p_f32, j, L);
+            if (p.factor) get_param_chunk<T, CE, A>(c, p.factor, seg * p.factor_stride, p.p_f32, j, L);
 #pragma unroll
             for (int i = 0; i < H; i += 2) {
                 const u64 one = f2(p.factor_add, p.factor_add);
@@ -237,7 +260,7 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
         int stage = 0;
         for (int round = 0; round < rounds; ++round, dx_row += dx_step) {
             ring_wait(sh.stages);
-            if constexpr (kShared<A>) group_sync(tpr, g + 1);
+            if constexpr (A == kShift) group_sync(L);
             const char* src = ring + stage * stage_bytes;
             u64 xs[1][P], dy[P], gy[P];
             u64(&x)[P] = xs[0];
@@ -245,7 +268,7 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
             read_row<T, NCH, CE, A>(dy, src + row_bytes, L);
             uint4 res[RES ? NCH : 1];
             if constexpr (RES) read_pieces<T, NCH, A>(res, src + 2 * row_bytes, L);
-            if constexpr (!kShared<A>) fill(stage);
+            if constexpr (A == kVec) fill(stage);
 #pragma unroll
             for (int e = 0; e < P; e += 2) {
                 const ulonglong2 f = fs[e / 2 * block];
@@ -253,26 +276,29 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
                 gy[e + 1] = mul2(dy[e + 1], f.y);
             }
             RowCoef c[1];
-            ln_row_stats<1, NCH, CE, A>(c, xs, L, inv_d, p.eps, sums, [&](int, int e) { return gy[e]; }, [&] {
-                if constexpr (kShared<A>) fill(stage);
-            });
-            if (++stage == sh.stages) stage = 0;
-            if (round * groups + g >= n_rows) continue;
-            const u64 rs = f2(c[0].rstd, c[0].rstd), a = f2(c[0].k1, c[0].k1), b = f2(c[0].k2, c[0].k2);
+            ln_row_stats<1, NCH, CE, A>(c, xs, L, inv_d, p.eps, sums, [&](int, int e) { return gy[e]; });
+            if (round * groups + g < n_rows) {
+                const u64 rs = f2(c[0].rstd, c[0].rstd), a = f2(c[0].k1, c[0].k1), b = f2(c[0].k2, c[0].k2);
+                char* out = ring + stage * stage_bytes;  // kShift: x and dy have been read
 #pragma unroll
-            for (int j = 0; j < NCH; ++j) {
-                if (!has_chunk<A>(j, L)) continue;
-                u64 dx[H];
+                for (int j = 0; j < NCH; ++j) {
+                    u64 dx[H];
 #pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    const int e = j * H + i;
-                    dx[i] = fma2(x[e], b, fma2(gy[e], rs, a));
-                    if constexpr (RES) dx[i] = add2(dx[i], piece_pair<T>(res, e));
-                    adf[e] = fma2(x[e], dy[e], adf[e]);
-                    ads[e] = add2(ads[e], dy[e]);
+                    for (int i = 0; i < H; ++i) {
+                        const int e = j * H + i;
+                        dx[i] = fma2(x[e], b, fma2(gy[e], rs, a));
+                        if constexpr (RES) dx[i] = add2(dx[i], piece_pair<T>(res, e));
+                        adf[e] = fma2(x[e], dy[e], adf[e]);
+                        ads[e] = add2(ads[e], dy[e]);
+                    }
+                    put_row_chunk<T, CE, A>(dx_row, out, dx, j, L);
                 }
-                put_chunk<T, CE, A>(dx_row, dx, j, L);
+                if constexpr (A == kShift) flush_row(dx_row, out, L);
+            } else if constexpr (A == kShift) {
+                group_sync(L);  // every thread has read the stage
             }
+            if constexpr (A == kShift) fill(stage);
+            if (++stage == sh.stages) stage = 0;
         }
         if (p.dfactor == nullptr && p.dshift == nullptr) continue;
         if (groups > 1) {
@@ -302,7 +328,7 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
         if (g == 0) {
 #pragma unroll
             for (int j = 0; j < NCH; ++j) {
-                if (!has_chunk<A>(j, L)) continue;
+                if (j >= L.nv) continue;
                 u64 c[2][H];
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
@@ -310,11 +336,11 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
                     c[1][i] = ads[j * H + i];
                 }
                 if (p.plan.parts == 1) {
-                    if (p.dfactor) put_param_chunk<T, CE, A>(p.dfactor, seg * p.dfactor_stride + c0, p.p_f32, c[0], j, L);
-                    if (p.dshift) put_param_chunk<T, CE, A>(p.dshift, seg * p.dshift_stride + c0, p.p_f32, c[1], j, L);
+                    if (p.dfactor) put_param_chunk<T, CE, A>(p.dfactor, seg * p.dfactor_stride, p.p_f32, c[0], j, L);
+                    if (p.dshift) put_param_chunk<T, CE, A>(p.dshift, seg * p.dshift_stride, p.p_f32, c[1], j, L);
                 } else {
-                    put_chunk<float, CE, A>(p.ws + unit * 2 * p.D + c0, c[0], j, L);
-                    put_chunk<float, CE, A>(p.ws + (unit * 2 + 1) * p.D + c0, c[1], j, L);
+                    put_chunk<float, CE, A>(p.ws + unit * 2 * p.D, c[0], j, L);
+                    put_chunk<float, CE, A>(p.ws + (unit * 2 + 1) * p.D, c[1], j, L);
                 }
             }
         }
@@ -353,7 +379,7 @@ static cudaError_t ln_bwd(const LnBwdParams& p0, cudaStream_t s) {
 template <class T, int NCH>
 static cudaError_t ln_bwd_any(const LnBwdParams& p, bool vec, cudaStream_t s) {
     if (vec) return p.dres ? ln_bwd<T, NCH, kVec, true>(p, s) : ln_bwd<T, NCH, kVec, false>(p, s);
-    return p.dres ? ln_bwd<T, NCH, kScalar, true>(p, s) : ln_bwd<T, NCH, kScalar, false>(p, s);
+    return p.dres ? ln_bwd<T, NCH, kShift, true>(p, s) : ln_bwd<T, NCH, kShift, false>(p, s);
 }
 
 cudaError_t launch_ln_backward(const LnBwdParams& p, bool f32, bool vec, cudaStream_t s) {

@@ -1,14 +1,4 @@
-// rowgroup.cuh -- the row machinery of the training kernels.
-//
-// A row group of `tpr` threads (whole warps) owns one row at a time; thread t
-// holds E of its elements in registers as binary32, in chunks of one 16-byte
-// access (CE elements: 8 bfloat16 or 4 binary32).  kVec: chunk j of thread t is
-// chunk j*tpr + t of the row, so a warp's accesses are consecutive 16-byte
-// pieces.  Otherwise (a width that is no multiple of CE, or a row that starts
-// at no 16-byte boundary) accesses are single elements: kScalar gives element e
-// of thread t column e*tpr + t, so a warp's accesses are consecutive; kQuad
-// gives a thread four consecutive columns at a time, which share one call of
-// the dropout generator.  Elements past the row's end are held as 0.
+// rowgroup.cuh -- element access shared by the training kernels.
 #pragma once
 
 #include "numerics.cuh"
@@ -58,7 +48,9 @@ __device__ __forceinline__ void store_elem(float* p, float v) {
     asm volatile("st.global.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
 }
 
-enum Access { kScalar = 0, kVec = 1, kQuad = 2 };
+// How rows are moved (rowring.cuh): kVec by aligned 16-byte chunks; kShift where
+// a width is no multiple of a chunk or a row starts at no 16-byte boundary.
+enum Access { kShift = 0, kVec = 1 };
 
 __device__ __forceinline__ void named_bar(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
