@@ -16,8 +16,6 @@
 // once, in shared memory; a thread then keeps those of its part of a head in
 // registers and walks the heads of Q and K.  Memory bound: every element is
 // read once and written once.
-#include <type_traits>
-
 #include "rowgroup.cuh"
 
 namespace mbx {
@@ -32,28 +30,31 @@ __device__ __forceinline__ float2 cos_sin_turns(double turns) {
     return (quadrant & 2) ? make_float2(-cc, -ss) : make_float2(cc, ss);
 }
 
-// One lane's part of a head, and its rotation.  Vec, interleaved: one 16-byte
-// chunk.  Vec, in halves: the chunk at c and the one at c + n; past the pairs, a
-// chunk that passes through.  Scalar: one pair, or one element that passes.
-template <class T, bool INTERLEAVED, bool VEC>
+// One lane's part of a head, and its rotation.  W elements an access (16 or 8
+// bytes), interleaved: one access; in halves: the access at c and the one at
+// c + n, or past the pairs one that passes through.  W = 1: one pair, or one
+// element that passes.
+template <class T, bool INTERLEAVED, int W>
 struct HeadPart {
-    static constexpr int CE = ChunkOf<T>::CE;
-    static constexpr int kPairs = VEC ? (INTERLEAVED ? CE / 2 : CE) : 1;
-    static constexpr int kRaw = VEC && !INTERLEAVED ? 2 : 1;
+    static constexpr int kPairs = W == 1 ? 1 : INTERLEAVED ? W / 2 : W;
+    static constexpr int NC = (kPairs + 1) / 2;                           // register pairs of cosines
+    static constexpr int NW = W == 1 ? 1 : W * (int)sizeof(T) / 4;        // words of an access
+    // heads of a thread in flight; halves hold two accesses of each
+    static constexpr int kHeadsAtOnce = INTERLEAVED || W == 1 ? 4 : 2;
     int first, second;  // offsets within a head; second < 0: none
     int pair0, pairs;   // pairs that turn: pair0 .. pair0 + pairs - 1
     __device__ __forceinline__ HeadPart(int lane, int n) {
-        if constexpr (VEC && INTERLEAVED) {
-            first = lane * CE;
+        if constexpr (W > 1 && INTERLEAVED) {
+            first = lane * W;
             second = -1;
             pair0 = first / 2;
             pairs = min(max(n - pair0, 0), kPairs);
-        } else if constexpr (VEC) {
-            const bool turns = lane < n / CE;
-            first = turns ? lane * CE : 2 * n + (lane - n / CE) * CE;
+        } else if constexpr (W > 1) {
+            const bool turns = lane < n / W;
+            first = turns ? lane * W : 2 * n + (lane - n / W) * W;
             second = turns ? first + n : -1;
             pair0 = first;
-            pairs = turns ? CE : 0;
+            pairs = turns ? W : 0;
         } else {
             const bool turns = lane < n;
             first = turns ? (INTERLEAVED ? 2 * lane : lane) : n + lane;
@@ -62,88 +63,89 @@ struct HeadPart {
             pairs = turns ? 1 : 0;
         }
     }
-    struct Raw {
-        typename std::conditional<VEC, uint4, float>::type a, b;
+    struct Raw {  // W = 1: binary32 bits
+        uint32_t a[NW], b[NW];
     };
+    static __device__ __forceinline__ void get(uint32_t (&w)[NW], const T* p) {
+        if constexpr (W == 1) {
+            w[0] = __float_as_uint(load_elem(p));
+        } else if constexpr (NW == 4) {
+            const uint4 v = ld_stream_rw(p);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+            asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+        }
+    }
+    static __device__ __forceinline__ void put(T* p, const uint32_t (&w)[NW]) {
+        if constexpr (W == 1) store_elem(p, __uint_as_float(w[0]));
+        else if constexpr (NW == 4) st_v4(p, make_uint4(w[0], w[1], w[2], w[3]));
+        else st_v2(p, w[0], w[1]);
+    }
     __device__ __forceinline__ Raw load(const T* head) const {
         Raw r;
-        if constexpr (VEC) {
-            r.a = ld_stream_rw(head + first);
-            if constexpr (!INTERLEAVED)
-                if (second >= 0) r.b = ld_stream_rw(head + second);
-        } else {
-            r.a = load_elem(head + first);
-            r.b = second >= 0 ? load_elem(head + second) : 0.0f;
-        }
+        get(r.a, head + first);
+        if constexpr (W == 1 || !INTERLEAVED)
+            if (second >= 0) get(r.b, head + second);
         return r;
     }
-    // cs: the pairs' cosines and sines, two neighbours a register pair.
-    __device__ __forceinline__ void store(T* head, const Raw& r, const u64 (&c)[kPairs / 2 + 1],
-                                          const u64 (&s)[kPairs / 2 + 1]) const {
-        if constexpr (VEC && INTERLEAVED) {
-            uint4 o;
-#pragma unroll
-            for (int i = 0; i < kPairs; i += 2) {  // pairs i and i+1 side by side
-                u64 x0, x1;
-                if constexpr (sizeof(T) == 2) {
-                    x0 = f2(lo_f(w_of(r.a, i)), lo_f(w_of(r.a, i + 1)));
-                    x1 = f2(hi_f(w_of(r.a, i)), hi_f(w_of(r.a, i + 1)));
-                } else {
-                    x0 = f2(__uint_as_float(r.a.x), __uint_as_float(r.a.z));
-                    x1 = f2(__uint_as_float(r.a.y), __uint_as_float(r.a.w));
-                }
-                const u64 o0 = turn0(x0, x1, c[i / 2], s[i / 2]), o1 = turn1(x0, x1, c[i / 2], s[i / 2]);
-                if constexpr (sizeof(T) == 2) {
-                    w_set(o, i, pack_rn(f2lo(o0), f2lo(o1)));
-                    w_set(o, i + 1, pack_rn(f2hi(o0), f2hi(o1)));
-                } else {
-                    o = make_uint4(__float_as_uint(f2lo(o0)), __float_as_uint(f2lo(o1)), __float_as_uint(f2hi(o0)),
-                                   __float_as_uint(f2hi(o1)));
-                }
-            }
-            if (pairs < kPairs) {  // the rest of the chunk passes through
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int pair = sizeof(T) == 2 ? i : i / 2;
-                    if (pair >= pairs) w_set(o, i, w_of(r.a, i));
-                }
-            }
-            st_v4(head + first, o);
-        } else if constexpr (VEC) {
-            if (second < 0) {
-                st_v4(head + first, r.a);
-                return;
-            }
-            uint4 oa, ob;
+    // Elements 0 and 1 of pairs i and i+1 of an interleaved access, side by side.
+    static __device__ __forceinline__ u64 elem(const uint32_t (&w)[NW], int i, int which) {
+        const int j = i + 1 < kPairs ? i + 1 : i;
+        if constexpr (sizeof(T) == 2) return which ? f2(hi_f(w[i]), hi_f(w[j])) : f2(lo_f(w[i]), lo_f(w[j]));
+        else return f2(__uint_as_float(w[2 * i + which]), __uint_as_float(w[2 * j + which]));
+    }
+    // c, s: the cosines and sines of two neighbouring pairs each.
+    __device__ __forceinline__ void store(T* head, const Raw& r, const u64 (&c)[NC], const u64 (&s)[NC]) const {
+        uint32_t oa[NW], ob[NW];
+        if constexpr (W > 1 && INTERLEAVED) {
 #pragma unroll
             for (int i = 0; i < kPairs; i += 2) {
-                u64 x0, x1;
-                if constexpr (sizeof(T) == 2) {
-                    x0 = widen2(w_of(r.a, i / 2));
-                    x1 = widen2(w_of(r.b, i / 2));
-                } else {
-                    x0 = f2(__uint_as_float(w_of(r.a, i)), __uint_as_float(w_of(r.a, i + 1)));
-                    x1 = f2(__uint_as_float(w_of(r.b, i)), __uint_as_float(w_of(r.b, i + 1)));
-                }
+                const u64 x0 = elem(r.a, i, 0), x1 = elem(r.a, i, 1);
                 const u64 o0 = turn0(x0, x1, c[i / 2], s[i / 2]), o1 = turn1(x0, x1, c[i / 2], s[i / 2]);
                 if constexpr (sizeof(T) == 2) {
-                    w_set(oa, i / 2, pack2_rn(o0));
-                    w_set(ob, i / 2, pack2_rn(o1));
+                    oa[i] = pack_rn(f2lo(o0), f2lo(o1));
+                    if (i + 1 < kPairs) oa[i + 1] = pack_rn(f2hi(o0), f2hi(o1));
                 } else {
-                    w_set(oa, i, (uint32_t)o0);
-                    w_set(oa, i + 1, (uint32_t)(o0 >> 32));
-                    w_set(ob, i, (uint32_t)o1);
-                    w_set(ob, i + 1, (uint32_t)(o1 >> 32));
+                    oa[2 * i] = __float_as_uint(f2lo(o0));
+                    oa[2 * i + 1] = __float_as_uint(f2lo(o1));
+                    if (i + 1 < kPairs) {
+                        oa[2 * i + 2] = __float_as_uint(f2hi(o0));
+                        oa[2 * i + 3] = __float_as_uint(f2hi(o1));
+                    }
                 }
             }
-            st_v4(head + first, oa);
-            st_v4(head + second, ob);
+            if (pairs < kPairs) {  // the rest of the access passes through
+#pragma unroll
+                for (int i = 0; i < NW; ++i)
+                    if (i * kPairs / NW >= pairs) oa[i] = r.a[i];
+            }
+            put(head + first, oa);
         } else if (second < 0) {
-            store_elem(head + first, r.a);
+            put(head + first, r.a);
         } else {
-            const float c0 = f2lo(c[0]), s0 = f2lo(s[0]);
-            store_elem(head + first, fmaf(r.a, c0, -(r.b * s0)));
-            store_elem(head + second, fmaf(r.a, s0, r.b * c0));
+            if constexpr (W == 1) {
+                const u64 x0 = f2(__uint_as_float(r.a[0]), 0.0f), x1 = f2(__uint_as_float(r.b[0]), 0.0f);
+                oa[0] = (uint32_t)turn0(x0, x1, c[0], s[0]);
+                ob[0] = (uint32_t)turn1(x0, x1, c[0], s[0]);
+            } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                for (int i = 0; i < NW; ++i) {
+                    const u64 x0 = widen2(r.a[i]), x1 = widen2(r.b[i]);
+                    oa[i] = pack2_rn(turn0(x0, x1, c[i], s[i]));
+                    ob[i] = pack2_rn(turn1(x0, x1, c[i], s[i]));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NW; i += 2) {
+                    const u64 x0 = f2(__uint_as_float(r.a[i]), __uint_as_float(r.a[i + 1]));
+                    const u64 x1 = f2(__uint_as_float(r.b[i]), __uint_as_float(r.b[i + 1]));
+                    const u64 o0 = turn0(x0, x1, c[i / 2], s[i / 2]), o1 = turn1(x0, x1, c[i / 2], s[i / 2]);
+                    oa[i] = (uint32_t)o0, oa[i + 1] = (uint32_t)(o0 >> 32);
+                    ob[i] = (uint32_t)o1, ob[i + 1] = (uint32_t)(o1 >> 32);
+                }
+            }
+            put(head + first, oa);
+            put(head + second, ob);
         }
     }
     // x0*cos - x1*sin and x0*sin + x1*cos
@@ -155,13 +157,12 @@ struct HeadPart {
     }
 };
 
-constexpr int kHeadsAtOnce = 4;  // heads of a thread in flight
-
 // Thread: lane within a head, then the share (1 of `splits`) of the heads, then
 // the token of the block.
-template <class T, bool INTERLEAVED, bool VEC>
-__global__ void __launch_bounds__(256) rope_axes_kernel(RopeParams p, int lanes, int tok_per_block, int splits) {
-    using Part = HeadPart<T, INTERLEAVED, VEC>;
+template <class T, bool INTERLEAVED, int W>
+__global__ void __launch_bounds__(256, 4) rope_axes_kernel(RopeParams p, int lanes, int tok_per_block, int splits) {
+    using Part = HeadPart<T, INTERLEAVED, W>;
+    constexpr int kHeadsAtOnce = Part::kHeadsAtOnce;
     extern __shared__ float2 cs_smem[];  // [tok_per_block][pairs]
     const int n = p.pairs;
     const unsigned tokens = (unsigned)p.tokens, total = (unsigned)p.batch * tokens;
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(256) rope_axes_kernel(RopeParams p, int lanes,
     }
     __syncthreads();
     if (!active) return;
-    u64 c[Part::kPairs / 2 + 1], sn[Part::kPairs / 2 + 1];
+    u64 c[Part::NC], sn[Part::NC];
 #pragma unroll
     for (int i = 0; i < Part::kPairs; i += 2) {
         const float2* q = cs_smem + k * n + part.pair0 + i;
@@ -234,10 +235,9 @@ __global__ void __launch_bounds__(256) rope_axes_kernel(RopeParams p, int lanes,
     }
 }
 
-template <class T, bool INTERLEAVED, bool VEC>
+template <class T, bool INTERLEAVED, int W>
 static cudaError_t launch_rope(const RopeParams& p, cudaStream_t s) {
-    constexpr int CE = ChunkOf<T>::CE;
-    const int lanes = !VEC ? p.hd - p.pairs : INTERLEAVED ? p.hd / CE : p.pairs / CE + (p.hd - 2 * p.pairs) / CE;
+    const int lanes = W == 1 ? p.hd - p.pairs : INTERLEAVED ? p.hd / W : (p.hd - p.pairs) / W;
     // a slot is a token's share of the heads; a block has as many as fit in 256 threads
     const int slots = lanes >= 256 ? 1 : 256 / lanes;
     const int64_t total = p.batch * p.tokens;
@@ -250,17 +250,22 @@ static cudaError_t launch_rope(const RopeParams& p, cudaStream_t s) {
     const int64_t grid = (total + tok_per_block - 1) / tok_per_block;
     const int block = (lanes * splits * tok_per_block + 31) / 32 * 32;
     const size_t smem = (size_t)tok_per_block * p.pairs * sizeof(float2);
-    return launch_pdl(rope_axes_kernel<T, INTERLEAVED, VEC>, (unsigned)grid, block, smem, s, p, lanes, tok_per_block, splits);
+    return launch_pdl(rope_axes_kernel<T, INTERLEAVED, W>, (unsigned)grid, block, smem, s, p, lanes, tok_per_block, splits);
 }
 
 template <class T>
-static cudaError_t rope_t(const RopeParams& p, bool interleaved, bool vec, cudaStream_t s) {
-    if (interleaved) return vec ? launch_rope<T, true, true>(p, s) : launch_rope<T, true, false>(p, s);
-    return vec ? launch_rope<T, false, true>(p, s) : launch_rope<T, false, false>(p, s);
+static cudaError_t rope_t(const RopeParams& p, bool interleaved, int align, cudaStream_t s) {
+    // the widest access that every head's start, the width and (in halves) the
+    // number of pairs are multiples of
+    constexpr int W16 = 16 / (int)sizeof(T), W8 = 8 / (int)sizeof(T);
+    auto fits = [&](int w) { return p.hd % w == 0 && (interleaved || p.pairs % w == 0); };
+    if (align == 16 && fits(W16)) return interleaved ? launch_rope<T, true, W16>(p, s) : launch_rope<T, false, W16>(p, s);
+    if (align >= 8 && fits(W8)) return interleaved ? launch_rope<T, true, W8>(p, s) : launch_rope<T, false, W8>(p, s);
+    return interleaved ? launch_rope<T, true, 1>(p, s) : launch_rope<T, false, 1>(p, s);
 }
 
-cudaError_t launch_rope_axes(const RopeParams& p, bool f32, bool interleaved, bool vec, cudaStream_t s) {
-    return f32 ? rope_t<float>(p, interleaved, vec, s) : rope_t<uint16_t>(p, interleaved, vec, s);
+cudaError_t launch_rope_axes(const RopeParams& p, bool f32, bool interleaved, int align, cudaStream_t s) {
+    return f32 ? rope_t<float>(p, interleaved, align, s) : rope_t<uint16_t>(p, interleaved, align, s);
 }
 
 }  // namespace mbx

@@ -146,6 +146,6 @@ cudaError_t launch_ln_backward(const LnBwdParams& p, bool f32, bool vec, cudaStr
 cudaError_t launch_dropout(const DropParams& p, bool f32, bool vec, cudaStream_t s);
 cudaError_t launch_dropout_backward(const DropParams& p, bool f32, bool vec, cudaStream_t s);
 cudaError_t launch_column_sums(const ColSumParams& p, cudaStream_t s);
-cudaError_t launch_rope_axes(const RopeParams& p, bool f32, bool interleaved, bool vec, cudaStream_t s);
+cudaError_t launch_rope_axes(const RopeParams& p, bool f32, bool interleaved, int align, cudaStream_t s);
 
 }  // namespace mbx

@@ -380,9 +380,10 @@ bool disjoint4(const H4& a, const H4& b) {
     return a.t > 1 && b.t > 1 && a.st == b.st && batches && apart(a.st, lo.head_span(), hi.head_span());
 }
 
-bool vec4(const H4& v) {
-    return reinterpret_cast<uintptr_t>(v.data) % 16 == 0 && v.sb * v.es() % 16 == 0 && v.st * v.es() % 16 == 0 &&
-           v.sh * v.es() % 16 == 0;
+// The power of two up to 16 bytes that every head's start is a multiple of.
+int align4(const H4& v) {
+    const uint64_t bits = reinterpret_cast<uintptr_t>(v.data) | (uint64_t)((v.sb | v.st | v.sh) * v.es()) | 16;
+    return (int)(bits & (~bits + 1));
 }
 
 V flat4(const H4& v) { return V{v.data, 1, v.span(), v.span(), v.dtype}; }
@@ -610,14 +611,13 @@ MBX_API int mbx_rope_axes(const mbx_heads_view* q_out, const mbx_heads_view* k_o
     MBX_TRY(mbx_check_rope_axes(q_out, k_out, q, k, positions, freqs, axes, n_axes, interleaved, inverse));
     mbx::RopeParams p = {};
     const int nt = k ? 2 : 1;
-    const int ce = q->dtype == MBX_F32 ? 4 : 8;
-    bool vec = q->head_dim % ce == 0;
+    int align = 16;
     for (int i = 0; i < nt; ++i) {
         const H4 in = of4(i ? k : q), out = of4(i ? k_out : q_out);
         mbx::RopeTensor& t = i ? p.k : p.q;
         t = mbx::RopeTensor{in.data, const_cast<void*>(out.data), in.sb, in.st, in.sh, out.sb, out.st, out.sh,
                             (int)in.h};
-        vec = vec && vec4(in) && vec4(out);
+        for (int a : {align4(in), align4(out)}) align = a < align ? a : align;
     }
     p.batch = q->batch;
     p.tokens = q->tokens;
@@ -626,14 +626,13 @@ MBX_API int mbx_rope_axes(const mbx_heads_view* q_out, const mbx_heads_view* k_o
     for (int i = 0; i < n_axes; ++i) p.axis_end[i] = end += axes[i] / 2;
     p.axes = n_axes;
     p.pairs = end;
-    if (!interleaved) vec = vec && p.pairs % ce == 0;
     p.pos = positions->data;
     p.pos_stride = positions->row_stride;
     p.pos_f32 = positions->dtype == MBX_F32;
     p.pos_batched = positions->rows != p.tokens;
     p.freqs = static_cast<const double*>(freqs->data);
     p.inverse = inverse != 0;
-    return cuda_status(mbx::launch_rope_axes(p, q->dtype == MBX_F32, interleaved != 0, vec, (cudaStream_t)stream));
+    return cuda_status(mbx::launch_rope_axes(p, q->dtype == MBX_F32, interleaved != 0, align, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -86,6 +86,20 @@ def test_layer_norm_views(mbx, dt):
     assert torch.equal(mbx.layer_norm(x.view(37, 1, 768), w, b, EPS).view(37, 768), mbx.layer_norm(x, w, b, EPS))
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("D", [40, 200, 520, 1021, 4096])
+def test_layer_norm_many_rows(mbx, D, dt):
+    """Enough rows for every SM to take two at a time, and one over."""
+    g = gen(17)
+    x, w, b = acts(g, 2433, D, dt), rnd(g, (D,), dt, 0.05, 1.0), rnd(g, (D,), dt, 0.1)
+    tr.assert_close(mbx.layer_norm(x, w, b, EPS), *tr.layer_norm(x, w, b, EPS))
+
+
+def test_layer_norm_one_row_tensor(mbx):
+    x = rnd(gen(18), (768,), BF)
+    tr.assert_close(mbx.layer_norm(x), *tr.layer_norm(x[None], None, None, EPS))
+
+
 def test_layer_norm_non_finite_rows_stay_alone(mbx):
     x = acts(gen(4), 9, 512, BF)
     x[5, 100], x[7, 3] = float("inf"), float("nan")
@@ -158,6 +172,44 @@ def test_ln_backward_views_and_in_place(mbx, dt, mod_rows):
     r2 = dres.clone()
     got = mbx.ln_modulate_backward(do, x, sc, EPS, r2, dx=r2)  # in place on the stream's gradient
     assert torch.equal(got[0], base[0]) and got[0].data_ptr() == r2.data_ptr()
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("mod_rows", [1, 40])
+@pytest.mark.parametrize("D", [7, 561, 1027])
+def test_ln_backward_unaligned_rows(mbx, D, mod_rows, dt):
+    """Rows that all lie differently to 16 bytes; each operand another way; in place."""
+    g = gen(D)
+    rows = 40
+    x, do, dres = acts(g, rows, D, dt), rnd(g, (rows, D), dt, 0.1), rnd(g, (rows, D), dt, 0.1)
+    sc = rnd(g, (mod_rows, D), dt, 0.1)
+    f = 1 + tr.d(sc)
+    base = check_ln_backward(mbx, x, do, f, dres, scale=sc)
+    bufs = [padded(torch.zeros_like(t), pad=k, fill=7.0) for t, k in ((x, 3), (sc, 1), (sc, 2))]
+    got = check_ln_backward(mbx, padded(x, 5)[1], misaligned(do), f, padded(dres, 8)[1], scale=padded(sc, 2)[1],
+                            dx=bufs[0][1], dscale=bufs[1][1], dshift=bufs[2][1])
+    assert all(torch.equal(a, b) for a, b in zip(base, got))
+    for b, v in bufs:
+        assert torch.all(b[:, D:] == 7.0)
+    r2 = dres.clone()
+    got = mbx.ln_modulate_backward(do, x, sc, EPS, r2, dx=r2)
+    assert torch.equal(got[0], base[0])
+
+
+def test_ln_backward_rows_beyond_32_bits(mbx):
+    """Three rows 2^31 - 8 elements apart: every offset past the first row needs 64 bits."""
+    stride, D = 2 ** 31 - 8, 256
+    buf = torch.empty(2 * stride + D, dtype=BF, device=DEV)
+    x = torch.as_strided(buf, (3, D), (stride, 1))
+    g = gen(19)
+    small = rnd(g, (3, D), BF)
+    x.copy_(small)
+    do, w = rnd(g, (3, D), BF), rnd(g, (D,), BF, 0.05, 1.0)
+    for a, b in zip(mbx.layer_norm_backward(do, x, w), mbx.layer_norm_backward(do, small, w)):
+        assert torch.equal(a, b)
+    assert torch.equal(mbx.layer_norm(x, w), mbx.layer_norm(small, w))
+    s = state(1, 1)
+    assert torch.equal(mbx.dropout(x, 0.5, s), mbx.dropout(small, 0.5, s))
 
 
 def test_ln_backward_is_deterministic_and_chained(mbx):
@@ -275,7 +327,7 @@ def test_dropout_views(mbx):
 
 def test_dropout_far_rows(mbx):
     """Rows beyond 2^16 and element offsets beyond 2^31: the tail's mask."""
-    rows, D = 70000, 31000 // 1000 * 1000 // 4
+    D = 7750
     rows = 2 ** 31 // D + 5000
     x = torch.ones((rows, D), dtype=BF, device=DEV)
     got = mbx.dropout(x, 0.5, state(6, 6))
@@ -348,6 +400,19 @@ def test_rope_misaligned_and_gradient(mbx):
     lhs, rhs = (tr.d(a) * tr.d(r)).sum(), (tr.d(q) * tr.d(c)).sum()
     pair = lambda t: tr.d(t).abs().unflatten(-1, (-1, 2)).sum(-1, keepdim=True).expand(-1, -1, -1, -1, 2).flatten(-2)
     assert abs(lhs - rhs) <= 9 * tr.U * ((pair(q) * tr.d(r).abs()) + (pair(r) * tr.d(q).abs())).sum()
+
+
+def test_rope_broadcast_batch_and_positions(mbx):
+    """A batch of stride 0 (an input only), positions given for the batch, three-dimensional Q."""
+    g = gen(23)
+    axes, fr = (16, 24, 24), mbx.rope_axis_freqs((16, 24, 24))
+    q = rnd(g, (1, 9, 4, 64), BF)
+    pos = torch.randint(0, 50, (9, 3), generator=g).int().to(DEV)
+    one, _ = mbx.rope_axes(q, None, pos, fr, axes)
+    four, _ = mbx.rope_axes(q.expand(4, -1, -1, -1), None, pos[None].expand(4, -1, -1).contiguous(), fr, axes)
+    assert torch.equal(four, one.expand(4, -1, -1, -1))
+    three, _ = mbx.rope_axes(q[0], None, pos, fr, axes)
+    assert three.shape == (9, 4, 64) and torch.equal(three, one[0])
 
 
 def test_rope_infinite_position_stays_alone(mbx):
@@ -440,3 +505,69 @@ def test_workspace_is_checked(mbx):
     ws = torch.empty(need // 4, device=DEV)
     chk = lambda w: mbx.check_ln_modulate_backward(*out, x, x.clone(), sc, workspace=w)
     assert chk(ws) == 0 and chk(None) == -1 and chk(ws[:-1]) == -10 and chk(torch.empty(need // 4 + 1, device=DEV)[1:]) == -7
+
+
+def test_calls_from_several_threads(mbx):
+    """Host threads with a stream each, the same kernels for the first time at once."""
+    from concurrent.futures import ThreadPoolExecutor
+    g = gen(91)
+    x, do = rnd(g, (4000, 1536), BF), rnd(g, (4000, 1536), BF)
+    scs = [rnd(g, (1, 1536), BF, 0.1) for _ in range(6)]
+
+    def work(sc):
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.default_stream())
+        with torch.cuda.stream(st):
+            for _ in range(10):
+                r = mbx.ln_modulate_backward(do, x, sc)
+        st.synchronize()
+        return r
+
+    torch.cuda.synchronize()
+    with ThreadPoolExecutor(6) as ex:
+        got = list(ex.map(work, scs))
+    for sc, r in zip(scs, got):
+        assert all(torch.equal(a, b) for a, b in zip(r, mbx.ln_modulate_backward(do, x, sc)))
+
+
+COLD = """
+import torch, modulation_bit_exact_gb300 as mbx
+x = torch.randn(3000, 512, device="cuda").bfloat16()
+sc = torch.zeros(1, 512, device="cuda").bfloat16()
+rng = torch.tensor([1, 2], device="cuda")
+pos = torch.zeros(3000, 1, dtype=torch.int32, device="cuda")
+fr = mbx.rope_axis_freqs((64,))
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    a = mbx.layer_norm(x)
+    b = mbx.ln_modulate_backward(x, x, sc)
+    c = mbx.dropout_gate_add(x, sc, x, 0.5, rng)
+    d = mbx.dropout_gate_add_backward(x, sc, x, 0.5, rng)
+    e = mbx.rope_axes(x.view(1, 3000, 8, 64), None, pos, fr, (64,))
+g.replay()
+torch.cuda.synchronize()
+want = (mbx.layer_norm(x), *mbx.ln_modulate_backward(x, x, sc), mbx.dropout_gate_add(x, sc, x, 0.5, rng),
+        *mbx.dropout_gate_add_backward(x, sc, x, 0.5, rng))
+assert all(torch.equal(p, q) for p, q in zip((a, *b, c, *d), want))
+"""
+
+
+def test_first_calls_inside_a_capture(mbx):
+    """A program whose first calls are captured: nothing needs a warm-up outside."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", COLD], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_state_on_the_host_is_refused(mbx):
+    x = torch.zeros((4, 64), device=DEV)
+    with pytest.raises(mbx.MbxError) as e:
+        mbx.dropout(x, 0.5, torch.zeros(2, dtype=torch.int64))
+    assert e.value.status == -9
+    with pytest.raises(mbx.MbxError) as e:
+        mbx.layer_norm(x, torch.ones(64))  # a weight on the host
+    assert e.value.status == -9

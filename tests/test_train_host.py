@@ -232,6 +232,49 @@ def test_host_tensors_and_bad_states_are_refused(mbx):
     with pytest.raises(mbx.MbxError) as e:
         mbx.rope_axes(x, None, rng, rng, (2,))
     assert e.value.status == -5
+    q = x.view(1, 4, 2, 32)
+    fr = mbx.rope_axis_freqs((32,), device="cpu")
+    pos = torch.zeros(4, 1, dtype=torch.int32)
+    for axes in ((), (8,) * 5, (-2,), (2 ** 40,)):
+        with pytest.raises(mbx.MbxError) as e:
+            mbx.rope_axes(q, None, pos, fr, axes)
+        assert e.value.status == -12
+    with pytest.raises(mbx.MbxError) as e:
+        mbx.rope_axes(q.transpose(2, 3), None, pos, fr, (32,))
+    assert e.value.status == -6
+
+
+def test_binding_follows_the_flat_row_rule(mbx):
+    """The native binding's views are those of _rows_cols: what that gives a stride of -1 is refused."""
+    buf = torch.zeros(6, 72)
+    ok = (torch.zeros(2, 3, 8), buf[:, :64], torch.zeros(8), torch.zeros(2, 1, 8), torch.zeros(3, 4, 10)[:, :, :8],
+          torch.zeros(4, 1, 6, 8)[:, :, ::2][:, :, :1])
+    bad = (torch.zeros(4, 8).t(), torch.zeros(2, 5, 16)[:, :4, :], torch.zeros(3, 4, 8).transpose(0, 1))
+    for t in ok:
+        assert mbx._rows_cols(t)[2] >= 0
+        with pytest.raises(mbx.MbxError) as e:
+            mbx.layer_norm(t)
+        assert e.value.status == -9                                        # only the device check refuses
+    for t in bad:
+        assert mbx._rows_cols(t)[2] == -1
+        with pytest.raises(mbx.MbxError) as e:
+            mbx.layer_norm(t)
+        assert e.value.status == -6
+
+
+def test_binding_arguments(mbx):
+    x, rng = torch.zeros(4, 8), torch.zeros(2, dtype=torch.int64)
+    for call in (lambda: mbx.layer_norm(None), lambda: mbx.layer_norm(x, 3), lambda: mbx.layer_norm(x, eps="a"),
+                 lambda: mbx.dropout(x, None, rng), lambda: mbx.dropout(x, 0.5, None),
+                 lambda: mbx.ln_modulate_backward(x, x, None), lambda: mbx.rope_axes(x, None, x, x, 3),
+                 lambda: mbx._native().layer_norm(x)):
+        with pytest.raises((TypeError, mbx.MbxError)):
+            call()
+    with pytest.raises(OverflowError):
+        mbx.dropout(x, 0.5, rng, offset=2 ** 63)
+    with pytest.raises(mbx.MbxError) as e:
+        mbx.layer_norm(torch.zeros(0, 8))
+    assert e.value.status == -1                                            # no data, as everywhere
 
 
 def test_workspace_query_refusals(mbx):
