@@ -243,7 +243,8 @@ static cudaError_t launch_rope(const RopeParams& p, cudaStream_t s) {
     const int64_t total = p.batch * p.tokens;
     const int most = p.q.heads > p.k.heads ? p.q.heads : p.k.heads;
     int splits = slots < 4 ? slots : 4;
-    // few tokens: spread each over more threads while the SMs are not full
+    // few tokens: spread each over more threads until every SM has two blocks
+    // (1000 tokens of 48 heads of 128: 5.8 us; until it has eight: 7.6)
     while (splits * 2 <= slots && (total * splits + slots - 1) / slots < 2 * sm_count()) splits *= 2;
     if (splits > most) splits = most;
     const int tok_per_block = slots / splits;

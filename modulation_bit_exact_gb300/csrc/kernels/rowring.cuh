@@ -188,6 +188,11 @@ __device__ __forceinline__ uint4 ring_piece(const char* src, int j, int h, const
     }
 }
 
+// A 16-byte store that marks its line as streamed.
+__device__ __forceinline__ void st_stream(void* p, uint4 v) {
+    asm volatile("st.global.cs.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 __device__ __forceinline__ u64 word_pair(uint32_t a, uint32_t b) { return f2(__uint_as_float(a), __uint_as_float(b)); }
 
 // A staged row as pairs.
@@ -247,23 +252,24 @@ __device__ __forceinline__ uint4 narrow(const u64 (&p)[CE / 2], int h) {
 // Chunk j of an output row.  kVec: to the row itself (`row` points at its first
 // element).  kShift: to `stage`, from where flush_row() moves the row when every
 // thread of the group has put its chunks.
-template <class Q, int CE, Access A>
+template <class Q, int CE, Access A, bool STREAM = false>
 __device__ __forceinline__ void put_row_chunk(Q* row, char* stage, const u64 (&p)[CE / 2], int j, const Lane& L) {
     if (j >= L.nv) return;
     constexpr int P = CE * (int)sizeof(Q) / 16;
     const int i = j * L.tpr + L.t;
 #pragma unroll
     for (int h = 0; h < P; ++h) {
-        if constexpr (A == kVec) st_v4(row + i * CE + h * (16 / (int)sizeof(Q)), narrow<Q, CE>(p, h));
+        if constexpr (A == kVec && STREAM) st_stream(row + i * CE + h * (16 / (int)sizeof(Q)), narrow<Q, CE>(p, h));
+        else if constexpr (A == kVec) st_v4(row + i * CE + h * (16 / (int)sizeof(Q)), narrow<Q, CE>(p, h));
         else reinterpret_cast<uint4*>(stage)[i * P + h] = narrow<Q, CE>(p, h);
     }
 }
 // The same for an output in a parameter's type, bfloat16 or binary32.
-template <class T, int CE, Access A>
+template <class T, int CE, Access A, bool STREAM = false>
 __device__ __forceinline__ void put_param_row_chunk(void* p, int64_t off, bool p_f32, char* stage,
                                                     const u64 (&v)[CE / 2], int j, const Lane& L) {
-    if (sizeof(T) == 4 || p_f32) put_row_chunk<float, CE, A>(static_cast<float*>(p) + off, stage, v, j, L);
-    else if constexpr (sizeof(T) == 2) put_row_chunk<uint16_t, CE, A>(static_cast<uint16_t*>(p) + off, stage, v, j, L);
+    if (sizeof(T) == 4 || p_f32) put_row_chunk<float, CE, A, STREAM>(static_cast<float*>(p) + off, stage, v, j, L);
+    else if constexpr (sizeof(T) == 2) put_row_chunk<uint16_t, CE, A, STREAM>(static_cast<uint16_t*>(p) + off, stage, v, j, L);
 }
 
 __device__ __forceinline__ void st_bits(uint16_t* p, uint16_t v) { st_u16(p, v); }
