@@ -1,21 +1,17 @@
-// layernorm.cu -- affine LayerNorm, and the gradients of LayerNorm with a
-// factor and a shift: the affine weight and bias, or AdaLN's 1 + scale and
-// shift with one row of each for a sample or for a token.
+// layernorm.cu -- affine LayerNorm.
 //
 //   mean, var over the row (biased); rstd = 1/sqrt(var + eps);
-//   xh = (x - mean) * rstd;  y = xh * f + b
-//   gy = dy * f;  c1 = mean(gy);  c2 = mean(gy * xh)
-//   dx = rstd * (gy - c1 - xh * c2)  (+ the residual stream's gradient)
-//   df = sum over the factor's rows of dy * xh;  db = sum of dy
+//   xh = (x - mean) * rstd;  y = xh * weight + bias
 //
-// All of it is binary32 with one rounding at each output.  The variance is the
-// mean of the squared deviations of registers that hold the whole row (no
-// E[x^2] - mean^2), so a row with a large mean loses nothing.
+// binary32 with one rounding at the output.  The variance is the mean of the
+// squared deviations of registers that hold the whole row (no E[x^2] - mean^2),
+// so a row with a large mean loses nothing.
 //
-// The backward pass takes the statistics from x again instead of reading saved
-// ones: x is in registers for xh anyway, sum(x) travels with sum(gy) and
-// sum((x-mean)^2) with sum(gy*(x-mean)), so it costs one more row sum of two
-// and no memory, and a forward pass need not save anything.
+// Bound by memory: a row is read once and written once.  A row's two sums depend
+// on each other, so what hides them is rows in flight: the ring of rowring.cuh,
+// filled again as soon as a row is in registers, and two rows a round where an
+// SM has few groups.  [32760, 5120] bfloat16: 105 us, 6.38 TB/s of 6.77 that a
+// copy reaches; [77, 1024]: 2.9 us in a graph, a launch's latency.
 #include "lnorm.cuh"
 
 namespace mbx {
@@ -137,10 +133,16 @@ static cudaError_t ln_fwd(const LnFwdParams& p, int tpr, cudaStream_t s) {
 template <class T, int NCH>
 static cudaError_t ln_fwd_r(const LnFwdParams& p, bool vec, cudaStream_t s) {
     const int tpr = row_threads(p.D);
-    // two rows a round while every SM has several
-    const bool two = p.rows >= 8 * (int64_t)sm_count();
     if (!vec) return ln_fwd<T, NCH, kShift, 1>(p, tpr, s);
-    return two ? ln_fwd<T, NCH, kVec, 2>(p, tpr, s) : ln_fwd<T, NCH, kVec, 1>(p, tpr, s);
+    // Two rows a round where an SM has fewer than four row groups, so that a row's
+    // sums are latency, and several rows for each.  bfloat16, us, two / one, 160M
+    // elements: D = 1024 119 / 115, 2048 116 / 101, 2560 118 / 101, 3584 107 / 130,
+    // 5120 101 / 115, 8192 110 / 126; 5120 columns of 304 rows 3.8 / 3.5, of 608
+    // 4.4 / 4.6, of 1216 6.2 / 6.8.  binary32 rows arrive in twice the time: 40M
+    // elements of 1024 55.5 / 55.5, of 2048 57.5 / 55.1, of 8192 54.7 / 55.3.
+    if constexpr (sizeof(T) == 2)
+        if (kRingThreads / tpr < 4 && p.rows >= 4 * (int64_t)sm_count()) return ln_fwd<T, NCH, kVec, 2>(p, tpr, s);
+    return ln_fwd<T, NCH, kVec, 1>(p, tpr, s);
 }
 
 cudaError_t launch_layer_norm(const LnFwdParams& p, bool f32, bool vec, cudaStream_t s) {

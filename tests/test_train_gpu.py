@@ -512,6 +512,32 @@ def test_two_graphs_of_one_call_keep_their_workspaces(mbx):
         assert all(torch.equal(a, b) for a, b in zip(o, w))
 
 
+@pytest.mark.parametrize("D", [520, 561, 5120])
+@pytest.mark.parametrize("mod_rows,seq", [(1, 900), (40, 3), (120, 1)])
+def test_gradients_that_are_not_wanted(mbx, D, mod_rows, seq):
+    """The C entry points take null for a parameter gradient; the others keep their bits."""
+    g = gen(D + seq)
+    rows = mod_rows * seq
+    x, y, do = rnd(g, (rows, D), BF), rnd(g, (rows, D), BF), rnd(g, (rows, D), BF, 0.1)
+    f = rnd(g, (mod_rows, D), BF, 0.1)
+    rng = state(3, 4)
+    L, v, s = mbx.lib(), mbx._view, torch.cuda.current_stream().cuda_stream
+    full = mbx.ln_modulate_backward(do, x, f, EPS)
+    need = mbx.param_grad_workspace(rows, D, mod_rows, BF)
+    ws = torch.empty(max(need, 4) // 4, device=DEV)
+    for want in ((True, False), (False, True), (False, False)):
+        dx = torch.full_like(x, float("nan"))
+        dp = [torch.full_like(f, float("nan")) if w else None for w in want]
+        wargs = (ws.data_ptr(), need) if any(want) and need else (None, 0)
+        st = L.mbx_ln_modulate_backward(v(dx), *[None if t is None else v(t) for t in dp], v(do), v(x), v(f), None, EPS,
+                                        *wargs, s)
+        assert st == 0 and torch.equal(dx, full[0])
+        assert all(t is None or torch.equal(t, full[1 + i]) for i, t in enumerate(dp))
+    dy = torch.full_like(y, float("nan"))
+    assert L.mbx_dropout_gate_add_backward(v(dy), None, v(do), v(f), v(y), 0.3, rng.data_ptr(), 0, None, 0, s) == 0
+    assert torch.equal(dy, mbx.dropout_gate_add_backward(do, f, y, 0.3, rng)[0])
+
+
 def test_workspace_is_checked(mbx):
     x, sc = torch.zeros((3000, 512), dtype=BF, device=DEV), torch.zeros((1, 512), dtype=BF, device=DEV)
     need = mbx.param_grad_workspace(3000, 512, 1, BF)
