@@ -11,6 +11,13 @@
 // anyway, sum(x) travels with sum(gy) and sum((x-mean)^2) with
 // sum(gy*(x-mean)), so it costs one more row sum and no memory, and a forward
 // pass need not save anything.
+//
+// Bound by memory where rows are many: x and dy are read once and dx is written
+// once (a token's factor and its two gradients once each).  [65536, 1024]
+// bfloat16 into one row: 67 us, 5.9 TB/s; [32760, 5120] a row each: 341 us, 5.9
+// TB/s of 6.77 that a copy reaches.  With few rows a segment it is bound by a
+// row's two dependent sums and by the second kernel: [8704, 4096] into two rows,
+// 53 us.
 #include "lnorm.cuh"
 
 namespace mbx {
@@ -181,10 +188,11 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
 //
 // A row's two sums are latency, so an SM wants two rows in work at least.  LEAN:
 // dy * f is formed anew in each pass and the residual's gradient read last, so
-// that 640 threads fit on an SM instead of 512.
-template <class T, int NCH, Access A, bool RES, bool LEAN>
-__global__ void __launch_bounds__(LEAN ? kRingThreads : kGradThreads) ln_backward_kernel(LnBwdParams p, RingShape sh) {
+// that more threads fit on an SM than kGradThreads.
+template <class T, int NCH, Access A, bool RES, int THREADS>
+__global__ void __launch_bounds__(THREADS) ln_backward_kernel(LnBwdParams p, RingShape sh) {
     constexpr int CE = ChunkOf<T>::CE, H = CE / 2, P = NCH * H;
+    constexpr bool LEAN = THREADS > kGradThreads;
     extern __shared__ __align__(16) char smem[];
     const int tpr = sh.tpr, g = threadIdx.x / tpr, t = threadIdx.x % tpr, groups = sh.groups;
     const Lane L = make_lane<CE>(t, tpr, p.D, g + 1);
@@ -361,12 +369,12 @@ static cudaError_t ln_bwd_token(const LnBwdParams& p, cudaStream_t s) {
     return launch_pdl(k, (unsigned)(need < most ? need : most), sh.groups * tpr, sh.smem, s, p, sh);
 }
 
-template <class T, int NCH, Access A, bool RES, bool LEAN>
+template <class T, int NCH, Access A, bool RES, int THREADS>
 static cudaError_t ln_bwd_sums(const LnBwdParams& p, cudaStream_t s) {
-    auto k = ln_backward_kernel<T, NCH, A, RES, LEAN>;
-    const int tpr = row_threads(p.D);
-    const RingShape sh = ring_shape(tpr, staged_row_bytes(tpr, (int)sizeof(T), A == kVec), RES ? 3 : 2, 0, 64,
-                                    LEAN ? kRingThreads : kGradThreads, 1);
+    auto k = ln_backward_kernel<T, NCH, A, RES, THREADS>;
+    constexpr int per = NCH * ChunkOf<T>::CE;
+    const int tpr = row_threads(p.D, per);
+    const RingShape sh = ring_shape(tpr, staged_row_bytes(tpr, (int)sizeof(T), A == kVec, per), RES ? 3 : 2, 0, 4 * per, THREADS, 1);
     static SmemOptIn opt_in;
     if (cudaError_t e = opt_in.allow(reinterpret_cast<const void*>(k), sh)) return e;
     const int64_t units = p.mod_rows * p.plan.parts, most = 1 << 30;
@@ -374,20 +382,30 @@ static cudaError_t ln_bwd_sums(const LnBwdParams& p, cudaStream_t s) {
 }
 
 template <class T, int NCH, Access A, bool RES>
-static cudaError_t ln_bwd(const LnBwdParams& p0, cudaStream_t s) {
-    LnBwdParams p = p0;
-    if (p.seq == 1 && p.factor) return ln_bwd_token<T, NCH, A, RES>(p, s);
-    p.plan = grad_plan(p.rows, p.mod_rows, p.D, (int)sizeof(T));
-    cudaError_t e = cudaSuccess;
-    bool done = false;
-    if constexpr (sizeof(T) == 2 && A == kVec) {
+static cudaError_t ln_bwd_rows(const LnBwdParams& p, cudaStream_t s) {
+    if constexpr (A == kVec) {
+        // 8 elements a thread in place of 16: eight lanes are the fewest of a row,
+        // and with 16 they take 128 columns.  bfloat16, us, 8 / 16: 1M rows of 40
+        // 67 / 97, 62496 of 128 16.9 / 18.0, 312496 of 128 45.4 / 45.8; not wider,
+        // where more lanes share a row's sums: 208328 of 192 58 / 51, 39056 of 1024
+        // 54 / 46.  binary32: 1M of 40 92 / 112, 312496 of 128 83 / 82.
+        if (p.D <= 128) return ln_bwd_sums<T, NCH / 2, A, RES, 1024>(p, s);
         // The widths of which two rows fit in 640 threads but not in 512.  160M
         // elements, us, LEAN / not: D = 4608 214 / 273, 5120 200 / 250, with a
         // residual 240 / 288 and 230 / 265.  One row fits either way at D = 6144
         // and 8192 (214, 199 not LEAN), and two at 4096 (172).
-        if ((done = p.D > 4096 && p.D <= 5120)) e = ln_bwd_sums<T, NCH, A, RES, true>(p, s);
+        if constexpr (sizeof(T) == 2)
+            if (p.D > 4096 && p.D <= 5120) return ln_bwd_sums<T, NCH, A, RES, kRingThreads>(p, s);
     }
-    if (!done) e = ln_bwd_sums<T, NCH, A, RES, false>(p, s);
+    return ln_bwd_sums<T, NCH, A, RES, kGradThreads>(p, s);
+}
+
+template <class T, int NCH, Access A, bool RES>
+static cudaError_t ln_bwd(const LnBwdParams& p0, cudaStream_t s) {
+    LnBwdParams p = p0;
+    if (p.seq == 1 && p.factor) return ln_bwd_token<T, NCH, A, RES>(p, s);
+    p.plan = grad_plan(p.rows, p.mod_rows, p.D, (int)sizeof(T));
+    const cudaError_t e = ln_bwd_rows<T, NCH, A, RES>(p, s);
     if (e != cudaSuccess || p.plan.parts == 1 || (!p.dfactor && !p.dshift)) return e;
     ColSumParams c{p.ws, p.plan.parts, p.mod_rows, p.D, 2, {p.dfactor, p.dshift}, {p.dfactor_stride, p.dshift_stride}, p.p_f32};
     return launch_column_sums(c, s);

@@ -12,16 +12,21 @@ namespace mbx {
 
 int sm_count();  // SMs of the current device; 0 if the runtime cannot tell
 
-// Threads that own one row of D elements, 16 elements each: 8 or 16 lanes of a
+// Threads that own one row of D elements, `per` elements each: 8 or 16 lanes of a
 // warp for the short rows, else whole warps.
-inline int row_threads(int D) { return D <= 128 ? 8 : D <= 256 ? 16 : (D + 511) / 512 * 32; }
+inline int row_threads(int D, int per = 16) {
+    return D <= 8 * per ? 8 : D <= 16 * per ? 16 : (D + 32 * per - 1) / (32 * per) * 32;
+}
 
 // Shared memory of one staged row (rowring.cuh): its elements, and for rows that
 // are not 16-byte aligned a head and room for the shift.
-inline int staged_row_bytes(int tpr, int esize, bool vec) { return 16 * esize * tpr + (vec ? 0 : 32); }
+inline int staged_row_bytes(int tpr, int esize, bool vec, int per = 16) {
+    return per * esize * tpr + (vec ? 0 : 32);
+}
 
 // Threads of an SM: the row kernels take up to 96 registers a thread, those
-// that also hold the sums of their columns up to 128.
+// that also hold the sums of their columns up to 128.  Row groups of several
+// warps use the named barriers 1 to 15, so there are at most ten of them.
 constexpr int kRingThreads = 640, kGradThreads = 512;
 
 // How a kernel that streams rows through shared memory fills an SM: blocks of

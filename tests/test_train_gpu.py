@@ -150,6 +150,20 @@ def test_ln_modulate_backward(mbx, D, dt, pdt, mod_rows, seq):
     check_ln_backward(mbx, x, do, 1 + tr.d(sc), dres, scale=sc)
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("D", [8, 40, 64, 72, 96, 128, 136])
+def test_layer_norm_of_narrow_rows(mbx, D, dt):
+    """Rows of a head's width: many to a block, several parts, a last part that is not full."""
+    g = gen(D)
+    for rows in (3, 129, 20011):
+        x, do, dres = acts(g, rows, D, dt), rnd(g, (rows, D), dt, 0.1), rnd(g, (rows, D), dt, 0.1)
+        w, b = rnd(g, (D,), F32, 0.05, 1.0), rnd(g, (D,), F32, 0.1)
+        want, tol = tr.layer_norm(x, w, b, EPS)
+        tr.assert_close(mbx.layer_norm(x, w, b, EPS), want, tol)
+        check_ln_backward(mbx, x, do, tr.d(w)[None], None, weight=w)
+        check_ln_backward(mbx, x, do, tr.d(w)[None], dres, weight=w)
+
+
 @pytest.mark.parametrize("residual", [False, True])
 @pytest.mark.parametrize("D,mod_rows,seq", [(4104, 1, 1601), (4608, 3, 333), (5112, 160, 6), (5120, 200, 3)])
 def test_ln_modulate_backward_wide_rows(mbx, D, mod_rows, seq, residual):
