@@ -463,8 +463,9 @@ typedef struct {
  * MBX_I32 or MBX_F32; freqs [1, n] MBX_F64, radians per position.  q and k
  * (NULL with k_out: none) have the same batch, tokens, head_dim and dtype, and
  * any numbers of heads.  Each output may be exactly its input, also inside one
- * merged buffer; no other overlap is allowed, nor an output that overlaps
- * itself (MBX_E_STRIDE).  head_dim <= 256; batch * tokens below 2^31.
+ * merged buffer (Q and K side by side in a batch entry, a token or a head); no
+ * other overlap is allowed, nor an output that overlaps itself (MBX_E_STRIDE).
+ * head_dim <= 256; batch * tokens below 2^31.
  */
 MBX_API int mbx_rope_axes(const mbx_heads_view* q_out, const mbx_heads_view* k_out,
                           const mbx_heads_cview* q, const mbx_heads_cview* k,

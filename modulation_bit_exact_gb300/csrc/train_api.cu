@@ -363,8 +363,8 @@ bool same4(const H4& a, const H4& b) {
 }
 
 // Whether two views share no element: their address ranges are apart, or they
-// repeat with one period (the batch's or the token's stride) and lie in
-// disjoint parts of it, as Q and K inside a merged QKV buffer do.
+// repeat with one period (the batch's, the token's or the head's stride) and lie
+// in disjoint parts of it, as Q and K inside a merged QKV buffer do.
 bool disjoint4(const H4& a, const H4& b) {
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.data), b0 = reinterpret_cast<uintptr_t>(b.data);
     if (a0 + a.span() * a.es() <= b0 || b0 + b.span() * b.es() <= a0) return true;
@@ -376,8 +376,15 @@ bool disjoint4(const H4& a, const H4& b) {
         return period > 0 && delta >= span_lo && delta + span_hi <= period;
     };
     if (a.b > 1 && b.b > 1 && a.sb == b.sb && apart(a.sb, lo.token_span(), hi.token_span())) return true;
-    const bool batches = (a.b == 1 && b.b == 1) || (a.sb == b.sb && a.st > 0 && a.sb % a.st == 0);
-    return a.t > 1 && b.t > 1 && a.st == b.st && batches && apart(a.st, lo.head_span(), hi.head_span());
+    // a dimension of n entries, stride s, whose entries lie whole periods apart
+    auto whole = [](int64_t na, int64_t nb, int64_t sa, int64_t sb, int64_t period) {
+        return (na == 1 && nb == 1) || (sa == sb && period > 0 && sa % period == 0);
+    };
+    if (a.t > 1 && b.t > 1 && a.st == b.st && whole(a.b, b.b, a.sb, b.sb, a.st) &&
+        apart(a.st, lo.head_span(), hi.head_span()))
+        return true;
+    return a.h > 1 && b.h > 1 && a.sh == b.sh && whole(a.b, b.b, a.sb, b.sb, a.sh) &&
+           whole(a.t, b.t, a.st, b.st, a.sh) && apart(a.sh, a.hd, b.hd);
 }
 
 // The power of two up to 16 bytes that every head's start is a multiple of.

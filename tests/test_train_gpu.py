@@ -396,13 +396,16 @@ def test_rope(mbx, hd, axes, interleaved, dt):
 
 
 @pytest.mark.parametrize("interleaved", [True, False])
-@pytest.mark.parametrize("order", ["bshd", "bhsd"])
+@pytest.mark.parametrize("order", ["bshd", "bhsd", "bsh3d"])
 def test_rope_in_place_in_a_merged_buffer(mbx, order, interleaved):
     g = gen(2)
     B, S, hd, axes = 2, 33, 128, (44, 42, 42)
     if order == "bshd":
         buf = rnd(g, (B, S, 12, hd), BF)
         q, k = buf[:, :, :6], buf[:, :, 6:9]
+    elif order == "bsh3d":
+        buf = rnd(g, (B, S, 12, hd), BF)
+        q, k = buf.view(B, S, 4, 3, hd)[:, :, :, 0], buf.view(B, S, 4, 3, hd)[:, :, :, 1]
     else:
         buf = rnd(g, (B, 12, S, hd), BF)
         q, k = buf[:, :6].transpose(1, 2), buf[:, 6:9].transpose(1, 2)
@@ -411,7 +414,8 @@ def test_rope_in_place_in_a_merged_buffer(mbx, order, interleaved):
     want = mbx.rope_axes(q, k, pos, fr, axes, interleaved)
     mbx.rope_axes(q, k, pos, fr, axes, interleaved, q_out=q, k_out=k)
     assert torch.equal(q, want[0]) and torch.equal(k, want[1])
-    v = (slice(None), slice(None), slice(9, None)) if order == "bshd" else (slice(None), slice(9, None))
+    v = {"bshd": (slice(None), slice(None), slice(9, None)), "bhsd": (slice(None), slice(9, None)),
+         "bsh3d": (slice(None), slice(None), slice(2, None, 3))}[order]
     assert torch.equal(buf[v], before[v])             # V is left as it was
 
 

@@ -209,6 +209,12 @@ def test_rope_in_place_inside_a_merged_buffer(mbx):
     hm = (3 * 4 * S * hd, hd, S * hd)                                      # [B, 3, 4, S, hd]
     assert st(H(0, strides=hm), H(0, strides=hm, off=4 * S * hd * 2)) == -9
     assert st(H(0, strides=hm), H(0, strides=hm, off=3 * S * hd * 2)) == -8
+    hd3 = (S * 4 * 3 * hd, 4 * 3 * hd, 3 * hd)                             # [B, S, 4, 3, hd]
+    assert st(H(0, strides=hd3), H(0, strides=hd3, off=hd * 2)) == -9
+    assert st(H(0, strides=hd3), H(0, strides=hd3, off=hd * 2 - 2)) == -8
+    assert st(H(0, strides=hd3, off=hd * 4), H(0, strides=hd3, off=hd * 6 - 2)) == -8  # wraps into the next head's
+    odd = (S * (4 * 3 * hd + 8), 4 * 3 * hd + 8, 3 * hd)                   # tokens no whole heads apart
+    assert st(H(0, strides=odd), H(0, strides=odd, off=hd * 2)) == -8
     one = (S * 8 * hd, 8 * hd, hd)
     assert st(H(0, B=1, strides=one), H(0, B=1, h=2, strides=one, off=4 * hd * 2)) == -9
 
