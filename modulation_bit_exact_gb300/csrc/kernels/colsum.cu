@@ -53,19 +53,29 @@ GradPlan grad_plan(int64_t rows, int64_t mod_rows, int D, int esize) {
     const int64_t seq = rows / mod_rows;
     const RingShape sh = grad_shape(D, esize, 2, true);
     const int64_t round = sh.groups;  // rows of a block's round
-    GradPlan g;
-    // Few rounds: one block, and no second kernel.  D = 1024, two segments, a
-    // round takes 1.06 us of the block: at four rounds 8.4 us on the device
-    // against 6.7 of two kernels, but 9.7 against 13.4 for a call on its own.
-    if (seq <= 4 * sh.groups) {
-        g.parts = 1;
-        g.rows_per_part = seq;
-        return g;
-    }
-    int64_t parts = ((int64_t)sm_count() * sh.ctas_per_sm + mod_rows - 1) / mod_rows;
-    if (parts > (seq + round - 1) / round) parts = (seq + round - 1) / round;
-    g.rows_per_part = ((seq + parts - 1) / parts + round - 1) / round * round;
-    g.parts = (seq + g.rows_per_part - 1) / g.rows_per_part;
+    const int64_t slots = (int64_t)sm_count() * sh.ctas_per_sm;
+    // One part, which needs no second kernel, or as many as fill the device once,
+    // twice, ...: the cost in half rounds (a round takes a block 1.1 to 1.3 us) of
+    // the rounds, of each block's start and end (3.5 rounds), of the second kernel
+    // (4.5) and of the parts' sums, written and read.  bfloat16 gradients of AdaLN,
+    // us: 64 segments of 128 rows of 4096: one part 85, two 53, three (the device
+    // once and a quarter) 71; 150 of 128: one 87, two 107; 4 of 256: one 162, 32 15.
+    GradPlan g{1, seq};
+    int64_t best = INT64_MAX;
+    auto consider = [&](int64_t parts) {
+        const int64_t per = ((seq + parts - 1) / parts + round - 1) / round;  // rounds of a part
+        parts = (seq + per * round - 1) / (per * round);
+        const int64_t cost = (mod_rows * parts + slots - 1) / slots * (2 * per + 7) +
+                             (parts > 1 ? 9 + mod_rows * parts * D / 250000 : 0);
+        if (cost < best) {
+            best = cost;
+            g = parts == 1 ? GradPlan{1, seq} : GradPlan{parts, per * round};
+        }
+    };
+    consider(1);
+    const int64_t fewest = (mod_rows + slots - 1) / slots;
+    for (int64_t times = fewest; times < fewest + 4; ++times)
+        if (times * slots / mod_rows > 1) consider(times * slots / mod_rows);
     return g;
 }
 
@@ -75,70 +85,86 @@ int64_t grad_workspace_bytes(int64_t rows, int64_t mod_rows, int D, int esize) {
     return g.parts == 1 ? 0 : mod_rows * g.parts * 2 * D * (int64_t)sizeof(float);
 }
 
-// A block adds 8*W columns: 8 threads side by side hold W columns each, 32
-// rows of such threads take every 32nd part, with up to eight loads of each in
-// flight, and the 32 sums are added in shared memory in a fixed order.  The
-// parts' sums are 2 to 10 MB that the first kernel has just written, so they
-// come from L2; latency bounds this kernel, not bandwidth.
-constexpr int kColThreads = 8, kColLanes = 32;
+// A block of 256 threads: 256 / LANES threads side by side hold W columns each,
+// LANES rows of such threads take every LANES-th part, with up to kColAtOnce loads
+// of each in flight, and the lanes' sums are added in shared memory in a fixed
+// order.  The parts' sums are 2 to 10 MB that the first kernel has just written,
+// so they come from L2; latency bounds this kernel, not bandwidth: it adds 4.2 us
+// to the first kernel's 49 for [8704, 4096] bfloat16 into two rows.  With 4 lanes
+// for up to 40 parts, 64 segments of 10 rows of 4096 in 3 parts take 20 us, with 32
+// lanes 48; 76 parts take 57 and 53.
+constexpr int kColBlock = 256, kColAtOnce = 5, kFewParts = 40;
 
-template <int W>
-__global__ void __launch_bounds__(kColThreads* kColLanes) column_sums_kernel(ColSumParams p) {
-    __shared__ float part[kColLanes][kColThreads * W];
+template <int W, int LANES>
+__global__ void __launch_bounds__(kColBlock) column_sums_kernel(ColSumParams p) {
+    constexpr int kThreads = kColBlock / LANES;
+    __shared__ float part[LANES][kThreads * W];
     grid_dep_wait();
     grid_dep_launch();
     const int cols = p.nacc * p.D;
-    const int c0 = (blockIdx.x * kColThreads + threadIdx.x) * W;
+    const int c0 = (blockIdx.x * kThreads + threadIdx.x) * W;
     const int64_t seg = blockIdx.y;
     const float* w = p.ws + seg * p.parts * cols + c0;
     float s[W] = {};
     if (c0 < cols) {
-#pragma unroll 8
-        for (int64_t i = threadIdx.y; i < p.parts; i += kColLanes) {
-            if constexpr (W == 4) {
-                const float4 v = *reinterpret_cast<const float4*>(w + i * cols);
-                s[0] += v.x;
-                s[1] += v.y;
-                s[2] += v.z;
-                s[3] += v.w;
-            } else {
-                s[0] += w[i * cols];
+        for (int64_t i = threadIdx.y; i < p.parts; i += kColAtOnce * LANES) {
+            float v[kColAtOnce][W];
+#pragma unroll
+            for (int u = 0; u < kColAtOnce; ++u) {
+                const int64_t k = i + u * LANES;
+                if constexpr (W == 4) {
+                    const float4 q = k < p.parts ? *reinterpret_cast<const float4*>(w + k * cols) : make_float4(0, 0, 0, 0);
+                    v[u][0] = q.x, v[u][1] = q.y, v[u][2] = q.z, v[u][3] = q.w;
+                } else {
+                    v[u][0] = k < p.parts ? w[k * cols] : 0.0f;
+                }
             }
+#pragma unroll
+            for (int u = 0; u < kColAtOnce; ++u)
+#pragma unroll
+                for (int j = 0; j < W; ++j) s[j] += v[u][j];
         }
     }
 #pragma unroll
     for (int i = 0; i < W; ++i) part[threadIdx.y][threadIdx.x * W + i] = s[i];
     __syncthreads();
-    const int t = threadIdx.y * kColThreads + threadIdx.x, c = blockIdx.x * kColThreads * W + t;
-    if (t >= kColThreads * W || c >= cols) return;
-    float a = 0.0f;
+    for (int t = threadIdx.y * kThreads + threadIdx.x; t < kThreads * W; t += kColBlock) {
+        const int c = blockIdx.x * kThreads * W + t;
+        if (c >= cols) break;
+        float a = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kColLanes; ++i) a += part[i][t];
-    const int k = c / p.D, d = c - k * p.D;
-    if (!p.out[k]) return;
-    const int64_t o = seg * p.out_stride[k] + d;
-    if (p.p_f32) store_elem(static_cast<float*>(p.out[k]) + o, a);
-    else store_elem(static_cast<uint16_t*>(p.out[k]) + o, a);
+        for (int i = 0; i < LANES; ++i) a += part[i][t];
+        const int k = c / p.D, d = c - k * p.D;
+        if (!p.out[k]) continue;
+        const int64_t o = seg * p.out_stride[k] + d;
+        if (p.p_f32) store_elem(static_cast<float*>(p.out[k]) + o, a);
+        else store_elem(static_cast<uint16_t*>(p.out[k]) + o, a);
+    }
 }
 
-cudaError_t launch_column_sums(const ColSumParams& p, cudaStream_t s) {
-    if (t_dry_run) return cudaSuccess;
-    const int cols = p.nacc * p.D;
-    const bool wide = cols % 4 == 0;  // 16-byte loads (the workspace is 16-byte aligned)
-    const int tile = kColThreads * (wide ? 4 : 1);
+template <int W, int LANES>
+static cudaError_t column_sums(const ColSumParams& p, cudaStream_t s) {
+    constexpr int kThreads = kColBlock / LANES, tile = kThreads * W;
     cudaLaunchConfig_t cfg = {};
     // more than one part a segment: no more segments than blocks on the device
-    cfg.gridDim = dim3((cols + tile - 1) / tile, (unsigned)p.segments);
-    cfg.blockDim = dim3(kColThreads, kColLanes);
+    cfg.gridDim = dim3((p.nacc * p.D + tile - 1) / tile, (unsigned)p.segments);
+    cfg.blockDim = dim3(kThreads, LANES);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, wide ? column_sums_kernel<4> : column_sums_kernel<1>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, column_sums_kernel<W, LANES>, p);
     const cudaError_t last = cudaGetLastError();
     return e != cudaSuccess ? e : last;
+}
+
+cudaError_t launch_column_sums(const ColSumParams& p, cudaStream_t s) {
+    if (t_dry_run) return cudaSuccess;
+    const bool wide = p.nacc * p.D % 4 == 0;  // 16-byte loads (the workspace is 16-byte aligned)
+    if (p.parts <= kFewParts) return wide ? column_sums<4, 4>(p, s) : column_sums<1, 4>(p, s);
+    return wide ? column_sums<4, 32>(p, s) : column_sums<1, 32>(p, s);
 }
 
 }  // namespace mbx

@@ -150,6 +150,24 @@ def test_ln_modulate_backward(mbx, D, dt, pdt, mod_rows, seq):
     check_ln_backward(mbx, x, do, 1 + tr.d(sc), dres, scale=sc)
 
 
+@pytest.mark.parametrize("D", [64, 257, 520, 4096])
+@pytest.mark.parametrize("mod_rows,seq", [(3, 200), (40, 50), (64, 33), (100, 300), (153, 70), (310, 40)])
+def test_gradients_of_many_segments(mbx, D, mod_rows, seq):
+    """One part a segment and several, few and many of them, more segments than the device has blocks."""
+    seq = max(2, min(seq, 16_000_000 // (mod_rows * D)))
+    g = gen(D + mod_rows)
+    rows = mod_rows * seq
+    x, do = acts(g, rows, D, BF), rnd(g, (rows, D), BF, 0.1)
+    sc = rnd(g, (mod_rows, D), BF, 0.1)
+    base = check_ln_backward(mbx, x, do, 1 + tr.d(sc), None, scale=sc)
+    assert all(torch.equal(a, b) for a, b in zip(mbx.ln_modulate_backward(do, x, sc, EPS), base))
+    rng = state(6, 1)
+    keep = tr.keep_mask(rows, D, 0.25, 6, 1)
+    _, dg = mbx.dropout_gate_add_backward(do, sc, x, 0.25, rng)
+    terms = torch.where(keep, tr.d(do) * tr.d(x) / 0.75, 0.0).reshape(mod_rows, seq, D)
+    tr.assert_close(dg, terms.sum(1), (8 + seq) * tr.U * terms.abs().sum(1))
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("D", [8, 40, 64, 72, 96, 128, 136])
 def test_layer_norm_of_narrow_rows(mbx, D, dt):
