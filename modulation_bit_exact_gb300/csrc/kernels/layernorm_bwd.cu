@@ -7,6 +7,10 @@
 //   dx = rstd * (gy - c1 - xh * c2)  (+ the residual stream's gradient)
 //   df = sum over the factor's rows of dy * xh;  db = sum of dy
 //
+// gy is a rounded product in every kernel here: it is formed as a fused
+// multiply-add of a -0 that the compiler does not know, since ptxas would fuse a
+// packed product with the sum it goes into, in one kernel and not in another.
+//
 // The statistics come from x again, not from saved ones: x is here for xh
 // anyway, sum(x) travels with sum(gy) and sum((x-mean)^2) with
 // sum(gy*(x-mean)), so it costs one more row sum and no memory, and a forward
@@ -89,7 +93,7 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
     grid_dep_launch();
     const int row_bytes = sh.row_bytes, stage_bytes = kF * row_bytes + sh.extra_bytes;
     const int64_t rounds = (p.rows + step - 1) / step;  // the same for every group
-    const u64 one = f2(p.factor_add, p.factor_add);
+    const u64 one = f2(p.factor_add, p.factor_add), nz = f2(p.neg_zero, p.neg_zero);
     int64_t fill_row = first;
     for (int i = 0; i < sh.stages; ++i) {
         char* dst = ring + i * stage_bytes;
@@ -130,7 +134,7 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
         if constexpr (RES) read_pieces<T, NCH, A>(res, src + 2 * row_bytes, L);
         if constexpr (A == kVec) fill(stage);
 #pragma unroll
-        for (int e = 0; e < NCH * H; ++e) gy[e] = mul2(dy[e], add2(gy[e], one));
+        for (int e = 0; e < NCH * H; ++e) gy[e] = fma2(dy[e], add2(gy[e], one), nz);
         const RowCoef k = ln_row_stats<NCH, CE, A>(x, L, inv_d, p.eps, sums, [&](int e) { return gy[e]; }, [] {});
         if (r < p.rows) {
             const u64 rs = f2(k.rstd, k.rstd), a = f2(k.k1, k.k1), b = f2(k.k2, k.k2);
@@ -258,6 +262,7 @@ __global__ void __launch_bounds__(THREADS) ln_backward_kernel(LnBwdParams p, Rin
                 adf[j * H + i] = adf[j * H + i + 1] = ads[j * H + i] = ads[j * H + i + 1] = 0;
             }
         }
+        const u64 nz = f2(p.neg_zero, p.neg_zero);
         constexpr bool kFillLast = A == kShift || (LEAN && RES);  // the stage is read, or written, to the end
         int stage = 0;
         for (int round = 0; round < rounds; ++round, dx_row += dx_step) {
@@ -272,7 +277,7 @@ __global__ void __launch_bounds__(THREADS) ln_backward_kernel(LnBwdParams p, Rin
             if constexpr (!kFillLast) fill(stage);
             auto times_factor = [&](int e) {
                 const ulonglong2 f = fs[e / 2 * block];
-                return mul2(dy[e], e % 2 ? f.y : f.x);
+                return fma2(dy[e], e % 2 ? f.y : f.x, nz);
             };
             if constexpr (!LEAN) {
 #pragma unroll
@@ -383,19 +388,19 @@ static cudaError_t ln_bwd_sums(const LnBwdParams& p, cudaStream_t s) {
 
 template <class T, int NCH, Access A, bool RES>
 static cudaError_t ln_bwd_rows(const LnBwdParams& p, cudaStream_t s) {
-    if constexpr (A == kVec) {
-        // 8 elements a thread in place of 16: eight lanes are the fewest of a row,
-        // and with 16 they take 128 columns.  bfloat16, us, 8 / 16: 1M rows of 40
-        // 67 / 97, 62496 of 128 16.9 / 18.0, 312496 of 128 45.4 / 45.8; not wider,
-        // where more lanes share a row's sums: 208328 of 192 58 / 51, 39056 of 1024
-        // 54 / 46.  binary32: 1M of 40 92 / 112, 312496 of 128 83 / 82.
-        if (p.D <= 128) return ln_bwd_sums<T, NCH / 2, A, RES, 1024>(p, s);
+    // 8 elements a thread in place of 16: eight lanes are the fewest of a row, and
+    // with 16 they take 128 columns.  bfloat16, us, 8 / 16: 1M rows of 40 67 / 97,
+    // 62496 of 128 16.9 / 18.0, 312496 of 128 45.4 / 45.8; not wider, where more
+    // lanes share a row's sums: 208328 of 192 58 / 51, 39056 of 1024 54 / 46.
+    // binary32: 1M of 40 92 / 112, 312496 of 128 83 / 82.  kShift the same (in the
+    // registers of 512 threads), so that a row's bits do not depend on where it starts.
+    if (p.D <= 128) return ln_bwd_sums<T, NCH / 2, A, RES, A == kVec ? 1024 : kGradThreads>(p, s);
+    if constexpr (sizeof(T) == 2 && A == kVec) {
         // The widths of which two rows fit in 640 threads but not in 512.  160M
         // elements, us, LEAN / not: D = 4608 214 / 273, 5120 200 / 250, with a
         // residual 240 / 288 and 230 / 265.  One row fits either way at D = 6144
         // and 8192 (214, 199 not LEAN), and two at 4096 (172).
-        if constexpr (sizeof(T) == 2)
-            if (p.D > 4096 && p.D <= 5120) return ln_bwd_sums<T, NCH, A, RES, kRingThreads>(p, s);
+        if (p.D > 4096 && p.D <= 5120) return ln_bwd_sums<T, NCH, A, RES, kRingThreads>(p, s);
     }
     return ln_bwd_sums<T, NCH, A, RES, kGradThreads>(p, s);
 }

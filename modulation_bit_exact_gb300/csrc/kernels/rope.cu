@@ -150,9 +150,10 @@ struct HeadPart {
             put(head + second, ob);
         }
     }
-    // x0*cos - x1*sin and x0*sin + x1*cos
+    // x0*cos - x1*sin and x0*sin + x1*cos, each one product and one fused
+    // multiply-add, written so that no access width lets ptxas fuse another pair
     static __device__ __forceinline__ u64 turn0(u64 x0, u64 x1, u64 c, u64 s) {
-        return sub2(mul2(x0, c), mul2(x1, s));
+        return fma2(x1 ^ 0x8000000080000000ull, s, mul2(x0, c));
     }
     static __device__ __forceinline__ u64 turn1(u64 x0, u64 x1, u64 c, u64 s) {
         return fma2(x0, s, mul2(x1, c));

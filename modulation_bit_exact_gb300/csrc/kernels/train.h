@@ -91,6 +91,7 @@ struct LnBwdParams {
     int64_t rows, mod_rows, seq;
     int D;
     float eps;
+    float neg_zero;  // -0.0f
     float* ws;
     GradPlan plan;  // filled by the launcher
 };

@@ -155,6 +155,7 @@ int ln_backward(const mbx_view* dx, const mbx_view* dfactor, const mbx_view* dsh
     p.D = (int)x->cols;
     p.eps = eps;
     p.factor_add = factor_add;
+    p.neg_zero = -0.0f;
     p.mod_rows = 1;
     const int ce = x->dtype == MBX_F32 ? 4 : 8;
     bool vec = p.D % ce == 0 && vec_row(of(dx)) && vec_row(of(dout)) && vec_row(of(x));

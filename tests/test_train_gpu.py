@@ -150,6 +150,76 @@ def test_ln_modulate_backward(mbx, D, dt, pdt, mod_rows, seq):
     check_ln_backward(mbx, x, do, 1 + tr.d(sc), dres, scale=sc)
 
 
+def inside(t, shift, stride, fill):
+    """The same rows `shift` elements behind a 16-byte boundary, `stride` apart, in a buffer of `fill`."""
+    rows, D = t.shape
+    buf = torch.full((rows * stride + 32,), fill, dtype=t.dtype, device=t.device)
+    v = buf[8 + shift:8 + shift + rows * stride].view(rows, stride)[:, :D]
+    v.copy_(t)
+    return buf, v
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("D,pad", [(1, 0), (2, 3), (9, 2), (121, 0), (561, 6), (1027, 1), (4099, 0), (8185, 1)])
+def test_rows_at_every_start(mbx, D, pad, dt):
+    """All operands of a row start at the same byte, at each of a 16-byte piece's and from row to
+    row another; NaN lies around every input, and nothing around an output is written."""
+    g = gen(D + pad)
+    rows, stride = (3001 if D < 2000 else 700), D + pad
+    x, do, dres, f = (rnd(g, (rows, D), dt, s, m) for s, m in ((1.0, 0.5), (0.1, 0.0), (0.1, 0.0), (0.1, 0.0)))
+    w, b = rnd(g, (D,), dt, 0.05, 1.0), rnd(g, (D,), dt, 0.1)
+    want = tr.layer_norm(x, w, b, EPS)
+    grads, alone = tr.ln_backward(do, x, 1 + tr.d(f), EPS, dres), tr.ln_backward(do, x, 1 + tr.d(f), EPS)[0]
+    nan = float("nan")
+
+    def clean(buf, v):
+        v.fill_(7.0)
+        return bool((buf == 7.0).all())
+
+    for shift in (range(8) if D < 2000 else (0, 1, 5, 6)):
+        xi, doi, ri, fi = (inside(t, shift, stride, nan)[1] for t in (x, do, dres, f))
+        ob, o = inside(x, shift, stride, 7.0)
+        mbx.layer_norm(xi, w, b, EPS, out=o)
+        tr.assert_close(o, *want, what=f"shift {shift}")
+        assert clean(ob, o)
+        outs = [inside(x, shift, stride, 7.0) for _ in range(3)]
+        mbx.ln_modulate_backward(doi, xi, fi, EPS, ri, *[v for _, v in outs])
+        for (buf, v), (wv, tol), name in zip(outs, grads, ("dx", "dscale", "dshift")):
+            tr.assert_close(v, wv, tol, what=f"{name} shift {shift}")
+            assert clean(buf, v)
+        mbx.ln_modulate_backward(doi, xi, fi, EPS, None, *[v for _, v in outs])
+        tr.assert_close(outs[0][1], *alone, what=f"no residual, shift {shift}")
+        # in place on the residual's gradient
+        mbx.ln_modulate_backward(doi, xi, fi, EPS, ri, ri, *[v for _, v in outs[1:]])
+        tr.assert_close(ri, *grads[0], what=f"in place, shift {shift}")
+    # one operand apart from the others
+    mbx.layer_norm(inside(x, 1, stride, nan)[1], w, b, EPS, out=o)
+    tr.assert_close(o, *want)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("D", [16, 64, 72, 128, 264, 1024, 4096, 5120, 8192])
+def test_a_row_keeps_its_bits(mbx, D, dt):
+    """A row's output does not depend on where it starts, nor on the rows beside it."""
+    g = gen(D)
+    rows = 1300 if D > 300 else 3000
+    x, do = acts(g, rows, D, dt), rnd(g, (rows, D), dt, 0.1)
+    w, b = rnd(g, (D,), dt, 0.05, 1.0), rnd(g, (D,), dt, 0.1)
+    some = slice(5, 12)
+    y = mbx.layer_norm(x, w, b)
+    assert torch.equal(mbx.layer_norm(x[some], w, b), y[some])
+    assert torch.equal(mbx.layer_norm(misaligned(x), w, b), y)
+    dx = mbx.layer_norm_backward(do, x, w)[0]
+    assert torch.equal(mbx.layer_norm_backward(do[some], x[some], w)[0], dx[some])
+    assert torch.equal(mbx.layer_norm_backward(do, misaligned(x), w)[0], dx)
+    sc = w.expand(rows, D).contiguous() - 1.0
+    token = mbx.ln_modulate_backward(do, x, sc)
+    for a, t in zip(mbx.ln_modulate_backward(do, misaligned(x), sc), token):
+        assert torch.equal(a, t)
+    for a, t in zip(mbx.ln_modulate_backward(do[some], x[some], sc[some]), token):
+        assert torch.equal(a, t[some])
+
+
 @pytest.mark.parametrize("D", [64, 257, 520, 4096])
 @pytest.mark.parametrize("mod_rows,seq", [(3, 200), (40, 50), (64, 33), (100, 300), (153, 70), (310, 40)])
 def test_gradients_of_many_segments(mbx, D, mod_rows, seq):
@@ -435,6 +505,23 @@ def test_rope_in_place_in_a_merged_buffer(mbx, order, interleaved):
     v = {"bshd": (slice(None), slice(None), slice(9, None)), "bhsd": (slice(None), slice(9, None)),
          "bsh3d": (slice(None), slice(None), slice(2, None, 3))}[order]
     assert torch.equal(buf[v], before[v])             # V is left as it was
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_rope_keeps_its_bits(mbx, dt, interleaved):
+    """A head's output depends neither on the access width that its place allows nor on the other heads."""
+    g = gen(31)
+    q = rnd(g, (1, 50, 6, 64), dt)
+    pos, fr = torch.randint(0, 200, (50, 2), generator=g).int().to(DEV), mbx.rope_axis_freqs((32, 32))
+    want, _ = mbx.rope_axes(q, None, pos, fr, (32, 32), interleaved)
+    for lead in (1, 8 // q.element_size(), 16 // q.element_size()):
+        buf = torch.zeros(q.numel() + lead, dtype=dt, device=DEV)
+        v = buf[lead:].view(q.shape)
+        v.copy_(q)
+        got, _ = mbx.rope_axes(v, None, pos, fr, (32, 32), interleaved)
+        assert torch.equal(got, want)
+    assert torch.equal(mbx.rope_axes(q[:, 3:9, 2:3], None, pos[3:9], fr, (32, 32), interleaved)[0], want[:, 3:9, 2:3])
 
 
 def test_rope_misaligned_and_gradient(mbx):
