@@ -79,7 +79,7 @@ enum {
     MBX_E_EMPTY = -3,         /* rows or cols is zero (or negative)               */
     MBX_E_DIM_TOO_LARGE = -4, /* cols (hidden size) above 8192                    */
     MBX_E_SHAPE = -5,         /* shapes disagree, or rows % mod_rows != 0         */
-    MBX_E_STRIDE = -6,        /* row_stride < cols                                */
+    MBX_E_STRIDE = -6,        /* row_stride < cols, or negative for a single row  */
     MBX_E_ALIGN = -7,         /* a pointer is not aligned to its element type     */
     MBX_E_ALIAS = -8,         /* an output overlaps an input                      */
     MBX_E_DEVICE = -9,        /* a pointer is not device memory of this device    */
@@ -90,7 +90,7 @@ enum {
 };
 
 /* Read-only view of a [rows, cols] array of `dtype` elements (row_stride in
- * elements). */
+ * elements; of a single row it addresses nothing, and is not negative). */
 typedef struct {
     const void* data;
     int64_t rows;

@@ -163,7 +163,7 @@ int check_fp8(const mbx_view* out_fp8, const float* fp8_scale, const V* others, 
     V q = of(out_fp8);
     if (q.dtype != MBX_E4M3) return MBX_E_DTYPE;
     if (q.rows <= 0 || q.cols <= 0) return MBX_E_EMPTY;
-    if (q.rows > 1 && q.stride < q.cols) return MBX_E_STRIDE;
+    if (!stride_ok(q)) return MBX_E_STRIDE;
     MBX_TRY(extent_ok(q));
     if (reinterpret_cast<uintptr_t>(fp8_scale) % 4) return MBX_E_ALIGN;
     if (q.rows != others[0].rows || q.cols != others[0].cols) return MBX_E_SHAPE;  // others[0] = out
@@ -184,7 +184,7 @@ int check_fp4(const mbx_view* out_fp4, const mbx_view* out_sf, const float* fp4_
     V q = of(out_fp4), f = of(out_sf);
     if (q.dtype != MBX_E2M1X2 || f.dtype != MBX_E4M3) return MBX_E_DTYPE;
     if (q.rows <= 0 || q.cols <= 0 || f.rows <= 0 || f.cols <= 0) return MBX_E_EMPTY;
-    if ((q.rows > 1 && q.stride < q.cols) || (f.rows > 1 && f.stride != f.cols)) return MBX_E_STRIDE;
+    if (!stride_ok(q) || (f.rows > 1 && f.stride != f.cols)) return MBX_E_STRIDE;
     MBX_TRY(extent_ok(q));
     MBX_TRY(extent_ok(f));
     if (reinterpret_cast<uintptr_t>(fp4_scale) % 4) return MBX_E_ALIGN;

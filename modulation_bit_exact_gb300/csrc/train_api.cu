@@ -414,7 +414,7 @@ int check_rope(const mbx_heads_view* q_out, const mbx_heads_view* k_out, const m
     if (fv.dtype != MBX_F64) return MBX_E_DTYPE;
     for (const V* v : {&pv, &fv}) {
         if (v->rows <= 0 || v->cols <= 0) return MBX_E_EMPTY;
-        if (v->rows > 1 && v->stride < v->cols) return MBX_E_STRIDE;
+        if (!stride_ok(*v)) return MBX_E_STRIDE;
         if (reinterpret_cast<uintptr_t>(v->data) % esize(v->dtype)) return MBX_E_ALIGN;
         MBX_TRY(extent_ok(*v));
     }

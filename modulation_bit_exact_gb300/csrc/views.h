@@ -57,12 +57,16 @@ inline int extent_ok(const V& v) {
     return MBX_OK;
 }
 
+// Whether the rows lie in order.  A single row has no stride, but a negative one
+// says that the caller's row is not contiguous.
+inline bool stride_ok(const V& v) { return v.rows > 1 ? v.stride >= v.cols : v.stride >= 0; }
+
 // Step 1 of a view: dtype, non-empty, stride, alignment, extent.
 inline int basic(const V& v) {
     if (v.data == nullptr) return MBX_E_NULL;
     if (v.dtype != MBX_BF16) return MBX_E_DTYPE;
     if (v.rows <= 0 || v.cols <= 0) return MBX_E_EMPTY;
-    if (v.rows > 1 && v.stride < v.cols) return MBX_E_STRIDE;
+    if (!stride_ok(v)) return MBX_E_STRIDE;
     if (reinterpret_cast<uintptr_t>(v.data) % 2) return MBX_E_ALIGN;
     return extent_ok(v);
 }
@@ -87,7 +91,7 @@ inline int basic_any(const V& v) {
     if (v.data == nullptr) return MBX_E_NULL;
     if (v.dtype != MBX_BF16 && v.dtype != MBX_F32) return MBX_E_DTYPE;
     if (v.rows <= 0 || v.cols <= 0) return MBX_E_EMPTY;
-    if (v.rows > 1 && v.stride < v.cols) return MBX_E_STRIDE;
+    if (!stride_ok(v)) return MBX_E_STRIDE;
     if (reinterpret_cast<uintptr_t>(v.data) % esize(v.dtype)) return MBX_E_ALIGN;
     return extent_ok(v);
 }

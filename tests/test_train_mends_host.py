@@ -1,0 +1,51 @@
+"""Host-side properties of the Python calls and the build: nothing here reaches a device."""
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def mbx():
+    from modulation_bit_exact_gb300 import _build
+    _build.build()
+    import modulation_bit_exact_gb300 as m
+    m.lib()
+    return m
+
+
+def refused(mbx, call):
+    with pytest.raises(mbx.MbxError) as e:
+        call()
+    return e.value.status
+
+
+def test_a_single_row_that_is_not_contiguous_is_refused(mbx):
+    """One row has no row stride to be wrong, but its elements have to lie side by side: each operand,
+    through the native calls and through ctypes."""
+    bf, f64 = torch.bfloat16, torch.float64
+    x, row, far = torch.zeros(4, 64), torch.zeros(64), torch.zeros(128)[::2]
+    one, far1 = torch.zeros(1, 64), torch.zeros(1, 128)[:, ::2]
+    rng = torch.zeros(2, dtype=torch.int64)
+    assert mbx._rows_cols(far) == (1, 64, -1)
+    for call in (lambda w, b: mbx.layer_norm(x, w, b), lambda w, b: mbx.layer_norm_backward(x, x, w, dbias=b)):
+        assert refused(mbx, lambda: call(row, torch.zeros(64))) == -9      # only the device check refuses
+        assert refused(mbx, lambda: call(far, row)) == refused(mbx, lambda: call(row, far)) == -6
+    for call in (lambda t, o: mbx.layer_norm(t, out=o), lambda t, o: mbx.dropout(t, 0.5, rng, out=o),
+                 lambda t, o: mbx.layer_norm_backward(t, one, dx=o), lambda t, o: mbx.layer_norm_backward(one, t, dx=o),
+                 lambda t, o: mbx.ln_modulate_backward(one, one, t, dscale=o),
+                 lambda t, o: mbx.dropout_gate_add(one, t, one, 0.5, rng, out=o),
+                 lambda t, o: mbx.dropout_gate_add_backward(one, one, t, 0.5, rng, dgate=o)):
+        assert refused(mbx, lambda: call(one, torch.zeros(1, 64))) == -9
+        assert refused(mbx, lambda: call(far1, None)) == refused(mbx, lambda: call(one, torch.zeros(1, 128)[:, ::2])) == -6
+    b = lambda t: t.to(bf) if t.is_contiguous() else torch.zeros(*t.shape[:-1], 128, dtype=bf)[..., ::2]
+    for t, want in ((one, -9), (far1, -6)):
+        assert refused(mbx, lambda: mbx.ln_modulate(b(t), b(one), b(one))) == want
+        assert refused(mbx, lambda: mbx.ln_modulate(b(x), b(one), b(t))) == want
+        assert refused(mbx, lambda: mbx.rmsnorm_scale(b(x), b(t), b(one))) == want
+        assert refused(mbx, lambda: mbx.residual_gate_add(b(one), b(one), b(one), out=b(t))) == want
+        assert mbx.check_layer_norm(torch.zeros_like(x), x, t) == want
+    q, pos, fr = torch.zeros(1, 1, 2, 64), torch.zeros(1, 2, dtype=torch.int32), torch.zeros(32, dtype=f64)
+    assert refused(mbx, lambda: mbx.rope_axes(q, None, pos, fr, (32, 32))) == -9
+    assert refused(mbx, lambda: mbx.rope_axes(q, None, torch.zeros(1, 4, dtype=torch.int32)[:, ::2], fr, (32, 32))) == -6
+    assert refused(mbx, lambda: mbx.rope_axes(q, None, pos, torch.zeros(64, dtype=f64)[::2], (32, 32))) == -6
+    fp8 = torch.zeros(1, 128, dtype=torch.uint8)[:, ::2]
+    assert refused(mbx, lambda: mbx.ln_modulate_fp8(b(one), b(one), b(one), torch.ones(1), out_fp8=fp8)) == -6
