@@ -388,13 +388,14 @@ static cudaError_t ln_bwd_sums(const LnBwdParams& p, cudaStream_t s) {
 
 template <class T, int NCH, Access A, bool RES>
 static cudaError_t ln_bwd_rows(const LnBwdParams& p, cudaStream_t s) {
-    // 8 elements a thread in place of 16: eight lanes are the fewest of a row, and
-    // with 16 they take 128 columns.  bfloat16, us, 8 / 16: 1M rows of 40 67 / 97,
-    // 62496 of 128 16.9 / 18.0, 312496 of 128 45.4 / 45.8; not wider, where more
-    // lanes share a row's sums: 208328 of 192 58 / 51, 39056 of 1024 54 / 46.
-    // binary32: 1M of 40 92 / 112, 312496 of 128 83 / 82.  kShift the same (in the
-    // registers of 512 threads), so that a row's bits do not depend on where it starts.
-    if (p.D <= 128) return ln_bwd_sums<T, NCH / 2, A, RES, A == kVec ? 1024 : kGradThreads>(p, s);
+    // 8 elements a thread in place of 16 where half of eight lanes' 16 would hold no
+    // column: bfloat16, us, 8 / 16, 1M rows of 40 67 / 97; binary32 92 / 112.  The
+    // columns lie with the same lanes either way, so a row's sums, and its bits, are
+    // those of ln_bwd_token().  Up to 128 columns 8 elements would take 16 lanes and
+    // another order, for little: bfloat16 312496 rows of 128 46.7 / 46.1, 62496 16.3 /
+    // 17.1, 600000 of 72 80 / 69.  kShift the same (in the registers of 512 threads),
+    // so that a row's bits do not depend on where it starts.
+    if (p.D <= 64) return ln_bwd_sums<T, NCH / 2, A, RES, A == kVec ? 1024 : kGradThreads>(p, s);
     if constexpr (sizeof(T) == 2 && A == kVec) {
         // The widths of which two rows fit in 640 threads but not in 512.  160M
         // elements, us, LEAN / not: D = 4608 214 / 273, 5120 200 / 250, with a

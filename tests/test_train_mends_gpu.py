@@ -46,3 +46,24 @@ def test_gated_dropout_gradients_are_the_formulas_products(mbx, p, D, dt, pdt):
         assert torch.equal(dy, want)
         if seq == 1:
             assert torch.equal(dgate, torch.where(keep, do.float() * (y.float() * inv), zero).to(pdt))
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("D", [8, 64, 72, 96, 121, 128, 136, 1024])
+def test_a_row_keeps_its_bits_whoever_shares_its_factor(mbx, D, dt):
+    """dx of a row alone, among others, and with a factor of its own."""
+    g = gen(D)
+    rows = 300
+    x, do, dres, w = rnd(g, (rows, D), dt), rnd(g, (rows, D), dt), rnd(g, (rows, D), dt), rnd(g, (D,), dt, 0.05, 1.0)
+    sc = rnd(g, (1, D), dt, 0.1)
+    for r in (None, dres):
+        dx = mbx.layer_norm_backward(do, x, w, dresidual=r)[0]
+        for i in range(0, rows, 7):
+            one = slice(i, i + 1)
+            alone = mbx.layer_norm_backward(do[one], x[one], w, dresidual=None if r is None else r[one])[0]
+            assert torch.equal(alone, dx[one])
+        shared = mbx.ln_modulate_backward(do, x, sc, dresidual=r)[0]
+        token = mbx.ln_modulate_backward(do, x, sc.expand(rows, D).contiguous(), dresidual=r)
+        assert torch.equal(token[0], shared)
+        pairs = sc.expand(rows // 2, D).contiguous()
+        assert torch.equal(mbx.ln_modulate_backward(do, x, pairs, dresidual=r)[0], shared)
