@@ -4,13 +4,14 @@
 //   xh = (x - mean) * rstd;  y = xh * weight + bias
 //
 // binary32 with one rounding at the output.  The variance is the mean of the
-// squared deviations of registers that hold the whole row (no E[x^2] - mean^2),
-// so a row with a large mean loses nothing.
+// squared deviations of registers that hold the whole row (no E[x^2] - mean^2), and
+// what the rounded mean is off by is taken out of the deviations (lnorm.cuh), so
+// that a row far from zero loses nothing.
 //
 // Bound by memory: a row is read once and written once.  A row's two sums depend
 // on each other, so what hides them is rows in flight: the ring of rowring.cuh,
 // filled again as soon as a row is in registers, and two rows a round where an
-// SM has few groups.  [32760, 5120] bfloat16: 105 us, 6.38 TB/s of 6.77 that a
+// SM has few groups.  [32760, 5120] bfloat16: 108 us, 6.2 TB/s of 6.77 that a
 // copy reaches; [77, 1024]: 2.9 us in a graph, a launch's latency.
 #include "lnorm.cuh"
 
@@ -68,7 +69,8 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
         ring_wait(sh.stages);
         if constexpr (A == kShift) group_sync(L);
         u64 v[R][P];
-        float mean[R], rstd[R];
+        constexpr bool kSum = kSumDeviations<T>;
+        float total[R], delta[R], second[kSum ? 2 * R : R];  // the squares' sums, the deviations'
 #pragma unroll
         for (int k = 0; k < R; ++k) read_row<T, NCH, CE, A>(v[k], ring + stage * stage_bytes + k * row_bytes, L);
         if constexpr (A == kVec) fill(stage);
@@ -77,30 +79,34 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
             u64 s = 0;
 #pragma unroll
             for (int e = 0; e < P; ++e) s = add2(s, v[k][e]);
-            mean[k] = f2lo(s) + f2hi(s);
+            total[k] = f2lo(s) + f2hi(s);
         }
-        sums(mean);
+        sums(total);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            mean[k] *= inv_d;
-            u64 q = 0;
+            const float mean = total[k] * inv_d;
+            delta[k] = mean_rest(total[k], p.D, inv_d);
+            u64 q = 0, d = 0;
 #pragma unroll
             for (int j = 0; j < NCH; ++j) {
 #pragma unroll
                 for (int i = 0; i < CE / 2; ++i) {
                     u64& c = v[k][j * (CE / 2) + i];
-                    c = sub2(c, where_column<CE, A>(mean[k], j, i, L));
+                    c = sub2(c, where_column<CE, A>(mean, j, i, L));
                     q = fma2(c, c, q);
+                    if constexpr (kSum) d = add2(d, c);
                 }
             }
-            rstd[k] = f2lo(q) + f2hi(q);
+            second[k] = f2lo(q) + f2hi(q);
+            if constexpr (kSum) second[R + k] = f2lo(d) + f2hi(d);
         }
-        sums(rstd);
+        sums(second);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             if (r + k >= p.rows) continue;
-            const float rs1 = rsqrtf(rstd[k] * inv_d + p.eps);
-            const u64 rs = f2(rs1, rs1);
+            if constexpr (kSum) delta[k] = second[R + k] * inv_d;
+            const float rs1 = rstd_of(second[k] * inv_d, delta[k], p.eps);
+            const u64 rs = f2(rs1, rs1), nd = f2(-delta[k] * rs1, -delta[k] * rs1);
             T* dst = static_cast<T*>(p.out) + (r + k) * p.out_stride;
 #pragma unroll
             for (int j = 0; j < NCH; ++j) {
@@ -108,7 +114,7 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_kernel(LnFwdParams p,
 #pragma unroll
                 for (int i = 0; i < CE / 2; ++i) {
                     const int e = j * (CE / 2) + i;
-                    c[i] = fma2(mul2(v[k][e], rs), w[e], b[e]);
+                    c[i] = fma2(fma2(v[k][e], rs, nd), w[e], b[e]);
                 }
                 put_row_chunk<T, CE, A>(dst, ring + stage * stage_bytes + k * row_bytes, c, j, L);
             }

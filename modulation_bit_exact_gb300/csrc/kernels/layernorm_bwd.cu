@@ -18,10 +18,10 @@
 //
 // Bound by memory where rows are many: x and dy are read once and dx is written
 // once (a token's factor and its two gradients once each).  [65536, 1024]
-// bfloat16 into one row: 67 us, 5.9 TB/s; [32760, 5120] a row each: 341 us, 5.9
+// bfloat16 into one row: 69 us, 5.8 TB/s; [32760, 5120] a row each: 347 us, 5.8
 // TB/s of 6.77 that a copy reaches.  With few rows a segment it is bound by a
 // row's two dependent sums and by the second kernel: [8704, 4096] into two rows,
-// 53 us.
+// 55 us.
 #include "lnorm.cuh"
 
 namespace mbx {
@@ -32,10 +32,11 @@ namespace mbx {
 struct RowCoef {
     float rstd, k1, k2;
 };
-template <int NCH, int CE, Access A, class Gy, class NextPass>
-__device__ __forceinline__ RowCoef ln_row_stats(u64 (&x)[NCH * CE / 2], const Lane& L, float inv_d, float eps,
-                                                GroupSums& sums, Gy gy, NextPass next_pass) {
-    constexpr int H = CE / 2;
+template <class T, int NCH, Access A, class Gy, class NextPass>
+__device__ __forceinline__ RowCoef ln_row_stats(u64 (&x)[NCH * ChunkOf<T>::CE / 2], const Lane& L, float inv_d,
+                                                float eps, GroupSums& sums, Gy gy, NextPass next_pass) {
+    constexpr int CE = ChunkOf<T>::CE, H = CE / 2;
+    constexpr bool kSum = kSumDeviations<T>;
     u64 s[2] = {0, 0}, sg[2] = {0, 0};
 #pragma unroll
     for (int e = 0; e < NCH * H; ++e) {
@@ -47,29 +48,41 @@ __device__ __forceinline__ RowCoef ln_row_stats(u64 (&x)[NCH * CE / 2], const La
     float v[2] = {f2lo(s[0]) + f2hi(s[0]), f2lo(sg[0]) + f2hi(sg[0])};
     sums(v);
     next_pass();
-    const float mean = v[0] * inv_d, c1 = v[1] * inv_d;
-    u64 q[2] = {0, 0}, qg[2] = {0, 0};
+    const float mean = v[0] * inv_d, c1 = v[1] * inv_d, rest = kSum ? 0.0f : mean_rest(v[0], L.D, inv_d);
+    u64 q[2] = {0, 0}, qg[2] = {0, 0}, d = 0;
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
 #pragma unroll
         for (int i = 0; i < H; ++i) {
             const int e = j * H + i;
             x[e] = sub2(x[e], where_column<CE, A>(mean, j, i, L));
+            if constexpr (!kSum) x[e] = sub2(x[e], where_column<CE, A>(rest, j, i, L));
             q[e % 2] = fma2(x[e], x[e], q[e % 2]);
             qg[e % 2] = fma2(gy(e), x[e], qg[e % 2]);
+            if constexpr (kSum) d = add2(d, x[e]);
         }
     }
     q[0] = add2(q[0], q[1]);
     qg[0] = add2(qg[0], qg[1]);
-    v[0] = f2lo(q[0]) + f2hi(q[0]);
-    v[1] = f2lo(qg[0]) + f2hi(qg[0]);
-    sums(v);
+    float w[kSum ? 4 : 2] = {f2lo(q[0]) + f2hi(q[0]), f2lo(qg[0]) + f2hi(qg[0])};
+    if constexpr (kSum) w[2] = f2lo(d) + f2hi(d);
+    sums(w);
     next_pass();
-    const float rstd = rsqrtf(v[0] * inv_d + eps);
-    const u64 rs = f2(rstd, rstd);
+    float rstd, m = w[1] * inv_d;  // m: mean(gy * (x - mean))
+    if constexpr (kSum) {
+        const float delta = w[2] * inv_d;
+        rstd = rstd_of(w[0] * inv_d, delta, eps);
+        const u64 rs = f2(rstd, rstd), nd = f2(-delta * rstd, -delta * rstd);
 #pragma unroll
-    for (int e = 0; e < NCH * H; ++e) x[e] = mul2(x[e], rs);
-    return RowCoef{rstd, -rstd * c1, -rstd * (v[1] * inv_d * rstd)};
+        for (int e = 0; e < NCH * H; ++e) x[e] = fma2(x[e], rs, nd);
+        m = fmaf(-delta, c1, m);
+    } else {
+        rstd = rsqrtf(w[0] * inv_d + eps);
+        const u64 rs = f2(rstd, rstd);
+#pragma unroll
+        for (int e = 0; e < NCH * H; ++e) x[e] = mul2(x[e], rs);
+    }
+    return RowCoef{rstd, -rstd * c1, -rstd * (m * rstd)};
 }
 
 // One modulation row for every row: nothing is summed, every output is a row,
@@ -135,7 +148,7 @@ __global__ void __launch_bounds__(kRingThreads) ln_backward_token_kernel(LnBwdPa
         if constexpr (A == kVec) fill(stage);
 #pragma unroll
         for (int e = 0; e < NCH * H; ++e) gy[e] = fma2(dy[e], add2(gy[e], one), nz);
-        const RowCoef k = ln_row_stats<NCH, CE, A>(x, L, inv_d, p.eps, sums, [&](int e) { return gy[e]; }, [] {});
+        const RowCoef k = ln_row_stats<T, NCH, A>(x, L, inv_d, p.eps, sums, [&](int e) { return gy[e]; }, [] {});
         if (r < p.rows) {
             const u64 rs = f2(k.rstd, k.rstd), a = f2(k.k1, k.k1), b = f2(k.k2, k.k2);
             T* dx_row = static_cast<T*>(p.dx) + r * p.dx_stride;
@@ -287,7 +300,7 @@ __global__ void __launch_bounds__(THREADS) ln_backward_kernel(LnBwdParams p, Rin
                 if constexpr (LEAN) return times_factor(e);
                 else return gy[e];
             };
-            const RowCoef c = ln_row_stats<NCH, CE, A>(x, L, inv_d, p.eps, sums, gy_at, [] {
+            const RowCoef c = ln_row_stats<T, NCH, A>(x, L, inv_d, p.eps, sums, gy_at, [] {
                 if constexpr (LEAN) asm volatile("" ::: "memory");  // the factor is read again
             });
             if (round * groups + g < n_rows) {
@@ -398,9 +411,9 @@ static cudaError_t ln_bwd_rows(const LnBwdParams& p, cudaStream_t s) {
     if (p.D <= 64) return ln_bwd_sums<T, NCH / 2, A, RES, A == kVec ? 1024 : kGradThreads>(p, s);
     if constexpr (sizeof(T) == 2 && A == kVec) {
         // The widths of which two rows fit in 640 threads but not in 512.  160M
-        // elements, us, LEAN / not: D = 4608 214 / 273, 5120 200 / 250, with a
-        // residual 240 / 288 and 230 / 265.  One row fits either way at D = 6144
-        // and 8192 (214, 199 not LEAN), and two at 4096 (172).
+        // elements, us, LEAN / not: D = 4608 224 / 277, 5120 212 / 253, with a
+        // residual 250 / 297 and 241 / 273.  One row fits either way at D = 6144
+        // and 8192 (221, 204 not LEAN), and two at 4096 (174).
         if (p.D > 4096 && p.D <= 5120) return ln_bwd_sums<T, NCH, A, RES, kRingThreads>(p, s);
     }
     return ln_bwd_sums<T, NCH, A, RES, kGradThreads>(p, s);

@@ -384,6 +384,17 @@ struct GroupSums {
     // The sums of W published warps (those that are not there hold 0).
     template <int V, int W>
     __device__ __forceinline__ void add_warps(float (&v)[V], const float* slot) {
+        if constexpr (V == 4) {  // five warps at a time: all 64 values at once spill registers
+            const float4* s = reinterpret_cast<const float4*>(slot);
+            float4 a = s[0];
+#pragma unroll 5
+            for (int i = 1; i < W; ++i) {
+                const float4 q = s[i];
+                a = make_float4(a.x + q.x, a.y + q.y, a.z + q.z, a.w + q.w);
+            }
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+            return;
+        }
         float r[W * V];
 #pragma unroll
         for (int i = 0; i < W * V; i += 4) {

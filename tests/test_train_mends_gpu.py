@@ -19,6 +19,9 @@ def mbx():
     return m
 
 
+EPS = 1e-6
+
+
 def gen(seed):
     return torch.Generator().manual_seed(seed)
 
@@ -67,3 +70,71 @@ def test_a_row_keeps_its_bits_whoever_shares_its_factor(mbx, D, dt):
         assert torch.equal(token[0], shared)
         pairs = sc.expand(rows // 2, D).contiguous()
         assert torch.equal(mbx.ln_modulate_backward(do, x, pairs, dresidual=r)[0], shared)
+
+
+def far_rows(D, dt):
+    """Rows of a far mean: constant ones, and ones whose elements lie within a factor of two."""
+    g = gen(D)
+    rows = [torch.full((1, D), v) for v in (0.7, 300.0, -1000.0, 10000.0)]
+    rows += [m + m * s * torch.randn(1, D, generator=g).clamp(-4, 4)
+             for m, s in ((1000.0, 2.0 ** -6), (-300.0, 0.08), (20.0, 0.05), (1e6, 2.0 ** -7))]
+    if dt == F32:
+        rows += [m + s * torch.randn(1, D, generator=g) for m, s in ((1000.0, 0.01), (-30000.0, 1.0), (5.0, 1e-3))]
+    return torch.cat(rows).to(dt).to(DEV)
+
+
+def far_scale(x):
+    """With e = 41u * mean|x| * rstd, the error of a rounded mean in standard deviations (40 roundings
+    of the sum, one of 1/D): the deviations from the rounded mean are e away at most; their own mean,
+    which is taken off, is known to 42u * (1 + e), and the variance to 45u * (1 + e)^2 and 84u * e.  So
+    xh is off by less than 64u * (1 + e)^2 * (|xh| + 1), whatever the mean."""
+    xh, rstd, X = tr.ln_stats(x, EPS)
+    return xh, rstd, (1 + 41 * tr.U * X).square()
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("D", [40, 64, 104, 112, 120, 1000, 1031, 2056, 5120, 8192])
+def test_rows_far_from_zero(mbx, D, dt):
+    x = far_rows(D, dt)
+    rows = len(x)
+    g = gen(D + 1)
+    w, b = rnd(g, (D,), dt, 0.05, 1.0), rnd(g, (D,), dt, 0.1)
+    xh, rstd, e2 = far_scale(x)
+    want = xh * tr.d(w) + tr.d(b)
+    many = x.repeat(620 // rows + 60, 1)  # enough for two rows at a time
+    for t in (x, many):
+        got = mbx.layer_norm(t, w, b, EPS)
+        tr.assert_close(got[:rows], want, tr.K * tr.U * (e2 * (xh.abs() + 1) * tr.d(w).abs() + tr.d(b).abs()))
+        assert torch.equal(got[-rows:], got[:rows])
+    do, dres = rnd(g, (rows, D), dt, 0.1), rnd(g, (rows, D), dt, 0.1)
+    gy = tr.d(do) * tr.d(w)
+    a = e2 * (xh.abs() + 1)
+    c1, c2 = gy.mean(-1, keepdim=True), (gy * xh).mean(-1, keepdim=True)
+    dx = rstd * (gy - c1 - xh * c2)
+    tol = tr.K * tr.U * rstd * (gy.abs() + e2 * gy.abs().mean(-1, keepdim=True) + a * (gy.abs() * a).mean(-1, keepdim=True))
+    sc = (w.float() - 1.0)
+    for r in (None, dres):
+        want = dx if r is None else dx + tr.d(r)
+        lim = tol if r is None else tol + 2 * tr.U * want.abs()
+        gx, gw, gb = mbx.layer_norm_backward(do, x, w, EPS, r)
+        tr.assert_close(gx, want, lim, "dx")
+        tr.assert_close(gw, (tr.d(do) * xh).sum(0), (tr.K + rows) * tr.U * (tr.d(do).abs() * a).sum(0), "dweight")
+        # a row each: the factor 1 + (w - 1) in binary32
+        f = 1 + tr.d(sc)
+        gy1 = tr.d(do) * f
+        c1t, c2t = gy1.mean(-1, keepdim=True), (gy1 * xh).mean(-1, keepdim=True)
+        want1 = rstd * (gy1 - c1t - xh * c2t)
+        want1 = want1 if r is None else want1 + tr.d(r)
+        gx, gs, gh = mbx.ln_modulate_backward(do, x, sc.expand(rows, D).contiguous(), EPS, r)
+        tr.assert_close(gx, want1, lim + 2 * tr.U * (rstd * gy1.abs()), "dx, a row each")
+        tr.assert_close(gs, tr.d(do) * xh, tr.K * tr.U * tr.d(do).abs() * a, "dscale")
+
+
+@pytest.mark.parametrize("D", [64, 104, 1000, 5120, 8192])
+def test_a_constant_bfloat16_row_is_zero(mbx, D):
+    """The sum of equal bfloat16 values is exact: each deviation is 2u of the value at most (the mean's
+    rounding, that of 1/D), and is known to 4u (1/D and three products)."""
+    x = torch.tensor([[1000.0], [10000.0], [-0.3], [3e-5]], device=DEV).to(BF).expand(4, D).contiguous()
+    y = mbx.layer_norm(x, None, None, EPS)
+    X = tr.d(x).abs() / EPS ** 0.5
+    assert (tr.d(y).abs() <= 9 * tr.U * tr.U * X).all()
