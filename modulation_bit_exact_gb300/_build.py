@@ -82,6 +82,13 @@ def _binding_commands(cuda: str) -> tuple[list[str], list[str]]:
     return compile_, link
 
 
+def _binding_key(commands: list[str]) -> str:
+    """What _binding.so depends on besides its sources: the commands, and the torch
+    whose headers they read (an upgrade in place changes no path)."""
+    import torch
+    return "\n".join([*commands, torch.__version__, str(torch.version.git_version)])
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     os.makedirs(OBJ, exist_ok=True)
     cc = nvcc()
@@ -101,8 +108,8 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             print(r.stdout + r.stderr)
 
     compile_, link = _binding_commands(os.path.dirname(os.path.dirname(cc)))
-    stamp = os.path.join(OBJ, "binding.cmd")  # another torch gives other commands
-    want = "\n".join(compile_ + link)
+    stamp = os.path.join(OBJ, "binding.cmd")
+    want = _binding_key(compile_ + link)
     same = os.path.exists(stamp) and open(stamp).read() == want
     binding = force or not same or _stale(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "mbx.h")])
     if binding:

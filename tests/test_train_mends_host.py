@@ -49,3 +49,24 @@ def test_a_single_row_that_is_not_contiguous_is_refused(mbx):
     assert refused(mbx, lambda: mbx.rope_axes(q, None, pos, torch.zeros(64, dtype=f64)[::2], (32, 32))) == -6
     fp8 = torch.zeros(1, 128, dtype=torch.uint8)[:, ::2]
     assert refused(mbx, lambda: mbx.ln_modulate_fp8(b(one), b(one), b(one), torch.ones(1), out_fp8=fp8)) == -6
+
+
+def test_another_torch_rebuilds_the_binding(mbx, monkeypatch):
+    """Also one that was installed in the place of the old one, under the same paths."""
+    from modulation_bit_exact_gb300 import _build
+    ran = []
+
+    def run(cmd, **kw):
+        ran.append(cmd)
+        raise RuntimeError("stop")
+
+    monkeypatch.setattr(_build.subprocess, "run", run)
+    _build.build()                                                         # everything is in place
+    assert not ran
+    for name, value in (("__version__", "0.0.1"), ("version.git_version", "0" * 40)):
+        with monkeypatch.context() as m:
+            m.setattr("torch." + name, value)
+            with pytest.raises(RuntimeError, match="stop"):
+                _build.build()
+        assert ran and all(_build.BINDING_SRC in c for c in ran)
+        ran.clear()
