@@ -146,7 +146,6 @@ template <int W, int LANES>
 static cudaError_t column_sums(const ColSumParams& p, cudaStream_t s) {
     constexpr int kThreads = kColBlock / LANES, tile = kThreads * W;
     cudaLaunchConfig_t cfg = {};
-    // more than one part a segment: no more segments than blocks on the device
     cfg.gridDim = dim3((p.nacc * p.D + tile - 1) / tile, (unsigned)p.segments);
     cfg.blockDim = dim3(kThreads, LANES);
     cfg.stream = s;
@@ -161,6 +160,10 @@ static cudaError_t column_sums(const ColSumParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_column_sums(const ColSumParams& p, cudaStream_t s) {
+    // gridDim.y is the segment.  grad_plan() makes two parts of a segment at least, out
+    // of at most three blocks an SM more than there are segments, so the segments that
+    // come here are at most four times the SMs.
+    if (p.segments > 65535) return cudaErrorInvalidConfiguration;
     if (t_dry_run) return cudaSuccess;
     const bool wide = p.nacc * p.D % 4 == 0;  // 16-byte loads (the workspace is 16-byte aligned)
     if (p.parts <= kFewParts) return wide ? column_sums<4, 4>(p, s) : column_sums<1, 4>(p, s);

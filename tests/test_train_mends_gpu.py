@@ -138,3 +138,14 @@ def test_a_constant_bfloat16_row_is_zero(mbx, D):
     y = mbx.layer_norm(x, None, None, EPS)
     X = tr.d(x).abs() / EPS ** 0.5
     assert (tr.d(y).abs() <= 9 * tr.U * tr.U * X).all()
+
+
+@pytest.mark.parametrize("D", [64, 1000, 4096, 8192])
+def test_only_few_segments_are_split(mbx, D):
+    """A second kernel joins the parts of a segment, with the segment as a block row of its grid: more
+    than four segments an SM are one part each, however many rows they have."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for seq in (2, 40, 3000, 100_000):
+        for m in (4 * sms + 1, 5 * sms, 7 * sms + 3, 32768, 65535, 65536, 1_000_000):
+            if m * seq < 2 ** 32:
+                assert mbx.param_grad_workspace(m * seq, D, m, BF) == 0
