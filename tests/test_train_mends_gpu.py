@@ -149,3 +149,34 @@ def test_only_few_segments_are_split(mbx, D):
         for m in (4 * sms + 1, 5 * sms, 7 * sms + 3, 32768, 65535, 65536, 1_000_000):
             if m * seq < 2 ** 32:
                 assert mbx.param_grad_workspace(m * seq, D, m, BF) == 0
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("D", [8, 62, 64, 96, 128, 562, 1024, 4096, 4106, 5120, 8192])
+def test_parameter_gradients_count_every_row_once(mbx, D, dt):
+    """Whole numbers whose sums are exact in any order: with rows of +-1 in equal numbers and eps = 0,
+    xh is +-1, and with p = 1/2 a kept element counts twice.  One part and many, parts and rounds that
+    are not full, more segments than blocks."""
+    g = torch.Generator(device=DEV).manual_seed(D)
+    whole = lambda *s: torch.randint(-3, 4, s, generator=g, device=DEV).to(dt)
+    rng = torch.tensor([5, 6], device=DEV)
+    half = torch.ones(D, device=DEV)
+    half[D // 2:] = -1.0
+    for m, seq in ((1, 20011), (1, 701), (2, 9), (3, 333), (40, 50), (64, 131), (153, 70), (310, 3), (700, 2)):
+        seq = max(2, min(seq, 24_000_000 // (m * D)))
+        rows = m * seq
+        sign = torch.randint(0, 2, (rows, 1), generator=g, device=DEV) * 2 - 1
+        xh = half * sign
+        x, do, y, dres = xh.to(dt), whole(rows, D), whole(rows, D), whole(rows, D)
+        sc = torch.zeros(m, D, device=DEV)
+        seg = lambda t: t.float().view(m, seq, D).sum(1)
+        for r in (None, dres):
+            _, dsc, dsh = mbx.ln_modulate_backward(do, x, sc, 0.0, r)
+            assert torch.equal(dsc, seg(do.float() * xh)), (m, seq)
+            assert torch.equal(dsh, seg(do)), (m, seq)
+        if m == 1:
+            _, dw, db = mbx.layer_norm_backward(do, x, torch.ones(D, device=DEV), 0.0)
+            assert torch.equal(dw, dsc[0]) and torch.equal(db, dsh[0])
+        keep = mbx.dropout(torch.ones(rows, D, device=DEV), 0.5, rng)  # 2 or 0
+        _, dg = mbx.dropout_gate_add_backward(do, sc, y, 0.5, rng)
+        assert torch.equal(dg, seg(do.float() * y.float() * keep)), (m, seq)
