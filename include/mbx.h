@@ -377,8 +377,8 @@ MBX_API int mbx_param_grad_workspace(int64_t rows, int64_t cols, int64_t mod_row
  *   dweight = sum over the rows of dout * xh,   dbias = sum of dout
  * dresidual [rows, D] or NULL is added to dx (the gradient that the residual
  * stream carries past the norm); dx may be exactly dresidual.  dweight and
- * dbias [1, D] of weight's dtype, either NULL (not computed); both NULL when
- * weight is NULL.
+ * dbias [1, D] of weight's dtype, either NULL (not computed).  When weight is
+ * NULL so is dweight, and dbias (of a bias alone) has x's dtype or MBX_F32.
  */
 MBX_API int mbx_layer_norm_backward(const mbx_view* dx, const mbx_view* dweight,
                                     const mbx_view* dbias, const mbx_cview* dout,

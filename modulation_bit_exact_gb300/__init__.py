@@ -548,7 +548,8 @@ def _ws_args(ws):
 def layer_norm_backward(dout, x, weight=None, eps: float = 1e-6, dresidual=None, dx=None, dweight=None,
                         dbias=None):
     """Gradients of ``layer_norm`` (see mbx_layer_norm_backward): (dx, dweight,
-    dbias), the last two None without a weight.  ``dresidual`` is added to dx,
+    dbias).  Without a weight dweight is None, and dbias too unless it is given:
+    a bias alone has its gradient written there.  ``dresidual`` is added to dx,
     and ``dx=dresidual`` updates it in place."""
     return _native().layer_norm_backward(dout, x, weight, eps, dresidual, dx, dweight, dbias)
 

@@ -228,11 +228,11 @@ PyObject* ln_backward(PyObject* const* a) {
     const In res(tensor_or_none(a[4]));
     at::Tensor dx = tensor_or_none(a[5]), df = tensor_or_none(a[6]), ds = tensor_or_none(a[7]);
     default_like(dx, x);
-    const Workspace ws(x, factor);
     if (factor.defined()) {
         default_like(df, factor);
         default_like(ds, factor);
     }
+    const Workspace ws(x, ds);
     const Out o(dx), of(df), os(ds);
     const In d(dout), xv(x), f(factor);
     void* s = stream_of(x);

@@ -94,12 +94,13 @@ int check_layer_norm(const mbx_view* out, const mbx_cview* x, const mbx_cview* w
 }
 
 // dx, then the operands it is computed from, then the two parameter gradients
-// (either may be null).  `factor` has mod_rows rows (LayerNorm: one).
+// (either may be null).  `factor` has mod_rows rows (LayerNorm: one, or none, where
+// dshift, the gradient of a bias alone, has a type of its own).
 int check_ln_backward(const mbx_view* dx, const mbx_view* dfactor, const mbx_view* dshift, const mbx_cview* dout,
                       const mbx_cview* x, const mbx_cview* factor, const mbx_cview* dres, bool one_row, float eps,
                       const float* ws, int64_t ws_bytes, bool dev) {
     if (!dx || !dout || !x) return MBX_E_NULL;
-    if (!factor && (!one_row || dfactor || dshift)) return MBX_E_NULL;
+    if (!factor && (!one_row || dfactor)) return MBX_E_NULL;
     Operands o;
     const V dxv = o.add(of(dx)), dov = o.add(of(dout)), xv = o.add(of(x));
     const int i_f = factor ? o.n : -1;
@@ -114,14 +115,15 @@ int check_ln_backward(const mbx_view* dx, const mbx_view* dfactor, const mbx_vie
     if (dres && o.v[i_r].dtype != xv.dtype) return MBX_E_DTYPE;
     if (factor && !param_dtype(o.v[i_f].dtype, xv.dtype)) return MBX_E_DTYPE;
     for (int i = i_out; i < o.n; ++i)
-        if (o.v[i].dtype != o.v[i_f].dtype) return MBX_E_DTYPE;
+        if (factor ? o.v[i].dtype != o.v[i_f].dtype : !param_dtype(o.v[i].dtype, xv.dtype)) return MBX_E_DTYPE;
     MBX_TRY(o.basic_checks());
     MBX_TRY(check_extent(xv));
     MBX_TRY(check_same_shape(dxv, xv));
     MBX_TRY(check_same_shape(dov, xv));
     if (dres) MBX_TRY(check_same_shape(o.v[i_r], xv));
     if (factor) MBX_TRY(one_row ? check_weight(o.v[i_f], xv) : check_mod(o.v[i_f], xv));
-    for (int i = i_out; i < o.n; ++i) MBX_TRY(check_same_shape(o.v[i], o.v[i_f]));
+    for (int i = i_out; i < o.n; ++i)
+        MBX_TRY(factor ? check_same_shape(o.v[i], o.v[i_f]) : check_weight(o.v[i], xv));
     MBX_TRY(check_eps(eps));
     // dx may be exactly the residual stream's gradient; nothing else overlaps an output
     for (int i = 1; i < o.n; ++i)
@@ -130,7 +132,7 @@ int check_ln_backward(const mbx_view* dx, const mbx_view* dfactor, const mbx_vie
         for (int i = 1; i < o.n; ++i)
             if (i != k && overlaps(o.v[k], o.v[i])) return MBX_E_ALIAS;
     if (dfactor || dshift) {
-        const int64_t m = o.v[i_f].rows;
+        const int64_t m = factor ? o.v[i_f].rows : 1;
         // without a device the size is unknown: the device check refuses the call
         const int64_t need = workspace_need(xv.rows, m, xv.cols, xv.dtype);
         if (need > 0) {
@@ -174,6 +176,7 @@ int ln_backward(const mbx_view* dx, const mbx_view* dfactor, const mbx_view* dsh
     if (dshift) {
         p.dshift = dshift->data;
         p.dshift_stride = dshift->row_stride;
+        p.p_f32 = dshift->dtype == MBX_F32;
         vec = vec && vec_row(of(dshift));
     }
     if (dres) {

@@ -180,3 +180,17 @@ def test_parameter_gradients_count_every_row_once(mbx, D, dt):
         keep = mbx.dropout(torch.ones(rows, D, device=DEV), 0.5, rng)  # 2 or 0
         _, dg = mbx.dropout_gate_add_backward(do, sc, y, 0.5, rng)
         assert torch.equal(dg, seg(do.float() * y.float() * keep)), (m, seq)
+
+
+@pytest.mark.parametrize("dt,pdt", [(BF, BF), (BF, F32), (F32, F32)])
+@pytest.mark.parametrize("D", [8, 72, 561, 4104])
+def test_gradient_of_a_bias_alone(mbx, D, dt, pdt):
+    g = gen(D)
+    for rows in (1, 2, 40, 3001):
+        x, do = rnd(g, (rows, D), dt), rnd(g, (rows, D), dt)
+        db = torch.full((D,), float("nan"), dtype=pdt, device=DEV)
+        dx, dw, out = mbx.layer_norm_backward(do, x, None, EPS, dbias=db)
+        assert dw is None and out.data_ptr() == db.data_ptr()
+        want = mbx.layer_norm_backward(do, x, torch.ones(D, dtype=pdt, device=DEV), EPS)
+        assert torch.equal(db, want[2]) and torch.equal(dx, want[0])
+        assert torch.equal(mbx.layer_norm_backward(do, x, None, EPS)[0], dx)

@@ -70,3 +70,27 @@ def test_another_torch_rebuilds_the_binding(mbx, monkeypatch):
                 _build.build()
         assert ran and all(_build.BINDING_SRC in c for c in ran)
         ran.clear()
+
+
+def test_gradient_of_a_bias_alone(mbx):
+    """layer_norm takes a bias without a weight; so does its backward call."""
+    from .test_train_host import F32, I32, V, WS, ref
+    L = mbx.lib()
+
+    def st(dx, dw, db, do, x, ws=WS, n=1 << 30):
+        args = [ref(v) for v in (dx, dw, db, do, x, None, None)]
+        a = L.mbx_check_layer_norm_backward(*args, 1e-6, ws, n)
+        assert a == L.mbx_layer_norm_backward(*args, 1e-6, ws, n, None)
+        return a
+
+    dx, db, do, x = V(0), V(2, 1), V(3), V(4)
+    assert st(dx, None, db, do, x) == st(dx, None, V(2, 1, dtype=F32), do, x) == -9  # host checks pass
+    assert st(dx, V(1, 1), db, do, x) == st(dx, V(1, 1), None, do, x) == -1          # no weight to have a gradient
+    assert st(dx, None, V(2, 1, dtype=I32), do, x) == -2
+    assert st(V(0, dtype=F32), None, db, V(3, dtype=F32), V(4, dtype=F32)) == -2
+    assert st(dx, None, V(2, 2), do, x) == st(dx, None, V(2, 1, 32), do, x) == -5
+    assert st(dx, None, V(0, 1), do, x) == st(dx, None, V(4, 1), do, x) == -8
+    args = [ref(v) for v in (dx, None, V(2, 4), do, x, None, None)]
+    assert L.mbx_check_ln_modulate_backward(*args, 1e-6, WS, 1 << 30) == -1          # AdaLN has a scale
+    t = torch.zeros(4, 64)
+    assert refused(mbx, lambda: mbx.layer_norm_backward(t, t, dbias=torch.zeros(64))) == -9
