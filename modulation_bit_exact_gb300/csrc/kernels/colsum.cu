@@ -44,14 +44,13 @@ cudaError_t SmemOptIn::allow(const void* kernel, const RingShape& sh) {
     return cudaSuccess;
 }
 
-RingShape grad_shape(int D, int esize, int rows, bool vec) {
-    const int tpr = row_threads(D);
-    return ring_shape(tpr, staged_row_bytes(tpr, esize, vec), rows, 0, 64, kGradThreads, 1);
-}
-
 GradPlan grad_plan(int64_t rows, int64_t mod_rows, int D, int esize) {
     const int64_t seq = rows / mod_rows;
-    const RingShape sh = grad_shape(D, esize, 2, true);
+    // the shape of a block that streams aligned rows of two operands, 16 elements a
+    // thread.  Some are launched with more row groups (layernorm_bwd.cu: up to 64
+    // columns, and 4104 to 5120); their last round of a part may be half empty.
+    const int tpr = row_threads(D);
+    const RingShape sh = ring_shape(tpr, staged_row_bytes(tpr, esize, true), 2, 0, 64, kGradThreads, 1);
     const int64_t round = sh.groups;  // rows of a block's round
     const int64_t slots = (int64_t)sm_count() * sh.ctas_per_sm;
     // One part, which needs no second kernel, or as many as fill the device once,

@@ -52,7 +52,6 @@ struct SmemOptIn {
 struct GradPlan {
     int64_t parts, rows_per_part;
 };
-RingShape grad_shape(int D, int esize, int rows, bool vec);
 GradPlan grad_plan(int64_t rows, int64_t mod_rows, int D, int esize);
 int64_t grad_workspace_bytes(int64_t rows, int64_t mod_rows, int D, int esize);
 
