@@ -13,6 +13,10 @@ section 关键源码片段: the last dimension must be contiguous; rows may be
 padded (any row stride), and every outer dimension must be flat over the rows.
 A tensor that breaks the rule is passed with a negative row stride, which the
 library rejects (MBX_E_STRIDE).
+
+No call records an autograd graph: outputs have no grad_fn, whatever the inputs
+require.  The training path has the backward calls, for the backward() of a
+torch.autograd.Function or for a training loop that calls them itself.
 """
 from __future__ import annotations
 

@@ -194,3 +194,30 @@ def test_gradient_of_a_bias_alone(mbx, D, dt, pdt):
         want = mbx.layer_norm_backward(do, x, torch.ones(D, dtype=pdt, device=DEV), EPS)
         assert torch.equal(db, want[2]) and torch.equal(dx, want[0])
         assert torch.equal(mbx.layer_norm_backward(do, x, None, EPS)[0], dx)
+
+
+def test_calls_record_no_graph_and_serve_a_function(mbx):
+    """Outputs carry no grad_fn; a torch.autograd.Function around a pair of calls has the gradients."""
+
+    class LayerNorm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight, bias):
+            ctx.save_for_backward(x, weight)
+            return mbx.layer_norm(x, weight, bias)
+
+        @staticmethod
+        def backward(ctx, dout):
+            return mbx.layer_norm_backward(dout.contiguous(), *ctx.saved_tensors)
+
+    g = gen(3)
+    leaves = [rnd(g, s, F32) for s in ((30, 200), (200,), (200,))]
+    for t in leaves:
+        t.requires_grad_()
+    assert mbx.layer_norm(*leaves).grad_fn is None and not mbx.layer_norm(*leaves).requires_grad
+    loss = LayerNorm.apply(*leaves).sum()                                  # its gradient is expanded from one number
+    got = torch.autograd.grad(loss, leaves)
+    ones = torch.ones(30, 200)
+    (dx, tol), (dw, wtol), (db, btol) = tr.ln_backward(ones, leaves[0], leaves[1].detach()[None], EPS)
+    tr.assert_close(got[0], dx, tol)
+    tr.assert_close(got[1], dw[0], wtol[0])
+    tr.assert_close(got[2], db[0], btol[0])
