@@ -408,7 +408,10 @@ MBX_API int mbx_ln_modulate_backward(const mbx_view* dx, const mbx_view* dscale,
  * is at least floor(p * 2^32).
  *   mbx_dropout:           out = kept ? x / (1 - p) : 0
  *   mbx_dropout_gate_add:  out = kept ? x + gate * y / (1 - p) : x
- * A dropped element contributes nothing, whatever gate and y hold there.
+ * A dropped element contributes nothing, whatever gate and y hold there.  r is
+ * the row's index within the call: a part of a tensor in a call of its own does
+ * not have the whole tensor's mask, and equal seeds and counters give equal
+ * masks to parts, so that ranks which share out one tensor take a seed each.
  * rng: device pointer to 2 int64 (seed, counter), 8-byte aligned, read on the
  * stream, so that a captured graph draws another mask when they change;
  * `offset` tells the layers of one step apart.  0 <= p < 1; p = 0 keeps all.

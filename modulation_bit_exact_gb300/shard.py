@@ -1,12 +1,22 @@
 """Row sharding of the norm/modulation path across ranks.
 
-Every operation is independent per row (the QKV epilogue per token and head),
-so N processes split the rows into contiguous blocks and run the same calls on
-their blocks with no collective on the data path.  The only constraint is the
-modulation mapping: row r uses modulation row r // (rows // mod_rows), and a
+Every operation of the forward path is independent per row (the QKV epilogue
+per token and head), so N processes split the rows into contiguous blocks and
+run the same calls on their blocks with no collective on the data path.  The
+only constraint is the modulation mapping: row r uses modulation row r // (rows // mod_rows), and a
 shard must keep that mapping expressible for its own call, i.e. it must be
 whole samples (their modulation rows) or lie inside one sample (its one
 modulation row).  `row_shard` returns such a split.
+
+Two kinds of call of the training path do not follow from their rows alone:
+
+* Dropout's mask is a function of a row's index within the call, so a block does
+  not have the mask of the unsharded call, and ranks that pass the same rng and
+  offset have the same mask on every block.  Give each rank a seed of its own
+  (``rng[0]``) and use it again in that rank's backward call.
+* The gradient of a parameter that several ranks' rows share (a weight, a bias,
+  the modulation row of a sample split among ranks) is this rank's part of the
+  sum: the ranks' parts have to be added (an all-reduce).
 """
 from __future__ import annotations
 

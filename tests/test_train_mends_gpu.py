@@ -221,3 +221,31 @@ def test_calls_record_no_graph_and_serve_a_function(mbx):
     tr.assert_close(got[0], dx, tol)
     tr.assert_close(got[1], dw[0], wtol[0])
     tr.assert_close(got[2], db[0], btol[0])
+
+
+def test_row_shards_of_the_training_path(mbx):
+    """What shard.py says of blocks of rows: dx and per-token gradients are the unsharded call's, the
+    parts of a shared parameter's gradient add up to it, and a block's dropout mask is that of its own
+    rows, the same for equal states, another for another seed."""
+    from modulation_bit_exact_gb300.shard import row_shard
+    g = gen(8)
+    rows, D, world = 96, 136, 4
+    x, y = rnd(g, (rows, D), BF), rnd(g, (rows, D), BF)
+    do = torch.randint(-3, 4, (rows, D), generator=g).to(BF).to(DEV)
+    sc = rnd(g, (2, D), F32, 0.1)
+    dx, dsc, dsh = mbx.ln_modulate_backward(do, x, sc)
+    parts, masks = torch.zeros_like(dsh), []
+    for rank in range(world):
+        lo, hi, m0, m1 = row_shard(rows, 2, world, rank)
+        sx, _, sh = mbx.ln_modulate_backward(do[lo:hi], x[lo:hi], sc[m0:m1])
+        assert torch.equal(sx, dx[lo:hi])
+        parts[m0:m1] += sh
+        mask = lambda seed: mbx.dropout(torch.ones_like(x[lo:hi]), 0.5, torch.tensor([seed, 3], device=DEV)) != 0
+        assert torch.equal(mask(9).cpu(), tr.keep_mask(hi - lo, D, 0.5, 9, 3))
+        masks.append(mask(100 + rank))
+        rng = torch.tensor([100 + rank, 3], device=DEV)
+        out = mbx.dropout_gate_add(torch.zeros_like(y[lo:hi]), sc[m0:m1], torch.ones_like(y[lo:hi]), 0.5, rng)
+        dy, _ = mbx.dropout_gate_add_backward(torch.ones_like(y[lo:hi]), sc[m0:m1], y[lo:hi], 0.5, rng)
+        assert torch.equal(out, dy) and torch.equal(dy != 0, masks[-1])
+    assert torch.equal(parts, dsh)                                         # whole numbers: exact in any order
+    assert not any(torch.equal(masks[0], m) for m in masks[1:])
