@@ -414,7 +414,9 @@ MBX_API int mbx_ln_modulate_backward(const mbx_view* dx, const mbx_view* dscale,
  * masks to parts, so that ranks which share out one tensor take a seed each.
  * rng: device pointer to 2 int64 (seed, counter), 8-byte aligned, read on the
  * stream, so that a captured graph draws another mask when they change;
- * `offset` tells the layers of one step apart.  0 <= p < 1; p = 0 keeps all.
+ * `offset` tells the layers of one step apart; the next step's counter is higher
+ * by the number of offsets in use, or a layer would have the mask that its
+ * neighbour had the step before.  0 <= p < 1; p = 0 keeps all.
  * The gradient of mbx_dropout is mbx_dropout of the incoming gradient with the
  * same p, rng and offset.  out may be exactly x.  gate [mod_rows, D].
  */

@@ -249,3 +249,16 @@ def test_row_shards_of_the_training_path(mbx):
         assert torch.equal(out, dy) and torch.equal(dy != 0, masks[-1])
     assert torch.equal(parts, dsh)                                         # whole numbers: exact in any order
     assert not any(torch.equal(masks[0], m) for m in masks[1:])
+
+
+def test_masks_of_steps_and_layers_differ(mbx):
+    """A counter that each step advances by the number of layers, a layer's offset on top: no two calls
+    share a mask, and rng[1] + offset alone decides."""
+    ones, layers, seen = torch.ones(8, 256, device=DEV), 3, {}
+    for step in range(4):
+        for layer in range(layers):
+            rng = torch.tensor([7, step * layers], device=DEV)
+            seen[step, layer] = mbx.dropout(ones, 0.5, rng, offset=layer)
+    all_ = list(seen.values())
+    assert not any(torch.equal(a, b) for i, a in enumerate(all_) for b in all_[:i])
+    assert torch.equal(seen[1, 1], mbx.dropout(ones, 0.5, torch.tensor([7, layers + 1], device=DEV)))
