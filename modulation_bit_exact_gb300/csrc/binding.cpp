@@ -2,8 +2,8 @@
 //
 // A call on a few rows is bound by the host.  Marshalling its tensors through
 // ctypes costs more than everything else: affine LayerNorm of [77, 1024] took
-// 12.2 us a call on the GB300's host, of which 2.8 us ran on the GPU; through
-// this module it takes 5.4 us (torch's own one-operand elementwise call: 8.4).
+// 12.2 us a call on the GB300's host, of which 2.9 us ran on the GPU; through
+// this module it takes 5.7 to 6.1 us (torch's negation of the same: 6.7 to 7.1).
 //
 // Each function takes its arguments by position (the defaults and the
 // documentation are in __init__.py), turns the tensors into views of mbx.h

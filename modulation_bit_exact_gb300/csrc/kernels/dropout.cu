@@ -18,8 +18,10 @@
 //
 // A row of 5120 bfloat16 takes 19,200 of the generator's 32-bit products to 30 KB
 // of memory: the forward pass comes near memory ([32760, 5120]: 152 us, 6.6 TB/s
-// of 6.77 that a copy reaches), the gradients, which also sum, are bound by the
-// issue of instructions ([8704, 4096] into two rows: 44.5 us, 4.8 TB/s).
+// of 6.77 that a copy reaches).  The gradients, which also sum, have registers for
+// 16 warps an SM; these issue in 59% of the cycles and wait for the integer
+// multiplier, each quad's products being a chain ([8704, 4096] into two rows: 44.5
+// us, 4.8 TB/s).
 #include "rowring.cuh"
 
 namespace mbx {

@@ -140,8 +140,8 @@ template <class T, int NCH>
 static cudaError_t ln_fwd_r(const LnFwdParams& p, bool vec, cudaStream_t s) {
     if constexpr (sizeof(T) == 2) {
         // 8 elements a thread in place of 16 where half of eight lanes would hold none:
-        // bfloat16, us, 8 / 16, 125000 rows of 64 7.7 / 9.1, 625000 37 / 34, 1562496 67 /
-        // 80, 1M rows of 40 45 / 53; binary32 gains nothing (625000 of 64 61 / 57).
+        // bfloat16, us, 8 / 16, 125000 rows of 64 8.3 / 9.4, 625000 31 to 37 / 36, 1562496
+        // 70 / 82, 1M rows of 40 47 / 55; binary32 gains nothing (625000 of 64 61 / 57).
         // kShift the same, so that a row's bits do not depend on where it starts.
         if (p.D <= 64) {
             const int tpr = row_threads(p.D, 8);
@@ -152,9 +152,9 @@ static cudaError_t ln_fwd_r(const LnFwdParams& p, bool vec, cudaStream_t s) {
     if (!vec) return ln_fwd<T, NCH, kShift, 1>(p, tpr, s);
     // Two rows a round where an SM has fewer than four row groups, so that a row's
     // sums are latency, and several rows for each.  bfloat16, us, two / one, 160M
-    // elements: D = 1024 119 / 115, 2048 116 / 101, 2560 118 / 101, 3584 107 / 130,
-    // 5120 101 / 115, 8192 110 / 126; 5120 columns of 304 rows 3.8 / 3.5, of 608
-    // 4.4 / 4.6, of 1216 6.2 / 6.8.  binary32 rows arrive in twice the time: 40M
+    // elements: D = 1024 119 / 114, 2048 115 / 102, 2560 115 / 103, 3584 110 / 131,
+    // 5120 104 / 116, 8192 112 / 128; 5120 columns of 304 rows 3.5 / 3.2, of 608
+    // 4.1 / 4.2, of 1216 5.9 / 6.4.  binary32 rows arrive in twice the time: 40M
     // elements of 1024 55.5 / 55.5, of 2048 57.5 / 55.1, of 8192 54.7 / 55.3.
     if constexpr (sizeof(T) == 2)
         if (kRingThreads / tpr < 4 && p.rows >= 4 * (int64_t)sm_count()) return ln_fwd<T, NCH, kVec, 2>(p, tpr, s);

@@ -329,9 +329,11 @@ __global__ void __launch_bounds__(THREADS) ln_backward_kernel(LnBwdParams p, Rin
         }
         if (p.dfactor == nullptr && p.dshift == nullptr) continue;
         if (groups > 1) {
-            // every group's sums in shared memory, in the place of the ring
-            // (two stages of two rows at least, so it holds them; drained:
-            // every thread waited for its last rows), added in group order
+            // every group's sums in shared memory, in the place of the ring (drained:
+            // every thread waited for its last rows), added in group order.  They take
+            // 8 bytes for each element of a row; a stage's two rows or three hold 4
+            // bytes at least in bfloat16, where there are two stages at least, and 8 in
+            // binary32, where there may be one
             u64* acc = reinterpret_cast<u64*>(smem + sh.sums_bytes + sh.fixed_bytes);  // [2P][block]
             const int n = block;
             asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -402,12 +404,13 @@ static cudaError_t ln_bwd_sums(const LnBwdParams& p, cudaStream_t s) {
 template <class T, int NCH, Access A, bool RES>
 static cudaError_t ln_bwd_rows(const LnBwdParams& p, cudaStream_t s) {
     // 8 elements a thread in place of 16 where half of eight lanes' 16 would hold no
-    // column: bfloat16, us, 8 / 16, 1M rows of 40 67 / 97; binary32 92 / 112.  The
-    // columns lie with the same lanes either way, so a row's sums, and its bits, are
-    // those of ln_bwd_token().  Up to 128 columns 8 elements would take 16 lanes and
-    // another order, for little: bfloat16 312496 rows of 128 46.7 / 46.1, 62496 16.3 /
-    // 17.1, 600000 of 72 80 / 69.  kShift the same (in the registers of 512 threads),
-    // so that a row's bits do not depend on where it starts.
+    // column: us, 8 / 16, bfloat16 1M rows of 40 70 / 100, 600000 of 64 48 / 66;
+    // binary32 98 / 124, 83 / 82.  The columns lie with the same lanes either way, so
+    // a row's sums, and its bits, are those of ln_bwd_token().  Up to 128 columns 8
+    // elements would take 16 lanes and another order, for little: bfloat16 312496 rows
+    // of 128 46.7 / 46.1, 62496 16.3 / 17.1, 600000 of 72 80 / 69.  kShift the same (in
+    // the registers of 512 threads), so that a row's bits do not depend on where it
+    // starts.
     if (p.D <= 64) return ln_bwd_sums<T, NCH / 2, A, RES, A == kVec ? 1024 : kGradThreads>(p, s);
     if constexpr (sizeof(T) == 2 && A == kVec) {
         // The widths of which two rows fit in 640 threads but not in 512.  160M
