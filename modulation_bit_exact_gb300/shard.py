@@ -3,10 +3,10 @@
 Every operation of the forward path is independent per row (the QKV epilogue
 per token and head), so N processes split the rows into contiguous blocks and
 run the same calls on their blocks with no collective on the data path.  The
-only constraint is the modulation mapping: row r uses modulation row r // (rows // mod_rows), and a
-shard must keep that mapping expressible for its own call, i.e. it must be
-whole samples (their modulation rows) or lie inside one sample (its one
-modulation row).  `row_shard` returns such a split.
+only constraint is the modulation mapping: row r uses modulation row
+r // (rows // mod_rows), and a shard must keep that mapping expressible for its
+own call, i.e. it must be whole samples (their modulation rows) or lie inside
+one sample (its one modulation row).  `row_shard` returns such a split.
 
 Two kinds of call of the training path do not follow from their rows alone:
 
