@@ -338,8 +338,9 @@ MBX_API int mbx_check_qk_norm_rope_qkv_epilogue(
 
 /* ------------------------------------------------------------------------
  * The training path: affine LayerNorm, the gradients of LayerNorm and of
- * AdaLN modulation, dropout in the gated residual with its gradients, and
- * rotary positions on several axes (their gradient is the inverse rotation).
+ * AdaLN modulation, dropout in the gated residual with its gradients, rotary
+ * positions on several axes (their gradient is the inverse rotation), and the
+ * norm of Q and K heads with that rotation, with its gradients.
  *
  * These have one numeric variant: every operation is binary32 and each output
  * is rounded once to its type.  Activations (x, y, out and their gradients)
@@ -477,6 +478,46 @@ MBX_API int mbx_rope_axes(const mbx_heads_view* q_out, const mbx_heads_view* k_o
                           const mbx_cview* positions, const mbx_cview* freqs, const int32_t* axes,
                           int n_axes, int interleaved, int inverse, void* stream);
 
+/*
+ * RMSNorm of every head of Q and K and the rotation of mbx_rope_axes, in one
+ * pass:
+ *   n = x * rstd * w,  rstd = 1 / sqrt(mean(x^2) + eps) over the head's elements,
+ *   out = the pairs of n turned by positions[token] * freqs; the rest passes.
+ * wq, wk [1, head_dim] (contiguous) of the heads' dtype, or MBX_F32 with
+ * MBX_BF16 heads, both of one dtype; either NULL (1).  Everything else, and
+ * in-place use, as in mbx_rope_axes.  One variant: binary32, one rounding.  A
+ * head's bits do not depend on its address, its strides or its neighbours.
+ */
+MBX_API int mbx_qk_norm_rope(const mbx_heads_view* q_out, const mbx_heads_view* k_out,
+                             const mbx_heads_cview* q, const mbx_heads_cview* k,
+                             const mbx_cview* wq, const mbx_cview* wk, const mbx_cview* positions,
+                             const mbx_cview* freqs, const int32_t* axes, int n_axes,
+                             int interleaved, float eps, void* stream);
+
+/* Workspace bytes of the call below where it computes dwq or dwk. */
+MBX_API int mbx_qk_norm_grad_workspace(int64_t batch, int64_t tokens, int64_t head_dim,
+                                       int64_t* bytes);
+
+/*
+ * Gradients of mbx_qk_norm_rope.  With g = the incoming gradient turned back,
+ * xh = x * rstd (statistics taken from x again) and gy = g * w:
+ *   dx = rstd * (gy - xh * mean(gy * xh)),
+ *   dw = sum over batch, tokens and heads of g * xh
+ * dq_out, dk_out are the gradients of the forward call's outputs; dq (dk) may
+ * be exactly dq_out (dk_out), no other overlap is allowed.  dwq, dwk [1,
+ * head_dim] of the weights' dtype, either NULL (not computed; it is where the
+ * weight is).  The workspace is that of the gradients above; with neither dwq
+ * nor dwk it may be NULL.
+ */
+MBX_API int mbx_qk_norm_rope_backward(const mbx_heads_view* dq, const mbx_heads_view* dk,
+                                      const mbx_view* dwq, const mbx_view* dwk,
+                                      const mbx_heads_cview* dq_out, const mbx_heads_cview* dk_out,
+                                      const mbx_heads_cview* q, const mbx_heads_cview* k,
+                                      const mbx_cview* wq, const mbx_cview* wk,
+                                      const mbx_cview* positions, const mbx_cview* freqs,
+                                      const int32_t* axes, int n_axes, int interleaved, float eps,
+                                      float* workspace, int64_t workspace_bytes, void* stream);
+
 /* Validation only, as above. */
 MBX_API int mbx_check_layer_norm(const mbx_view* out, const mbx_cview* x, const mbx_cview* weight,
                                  const mbx_cview* bias, float eps);
@@ -504,6 +545,17 @@ MBX_API int mbx_check_rope_axes(const mbx_heads_view* q_out, const mbx_heads_vie
                                 const mbx_heads_cview* q, const mbx_heads_cview* k,
                                 const mbx_cview* positions, const mbx_cview* freqs,
                                 const int32_t* axes, int n_axes, int interleaved, int inverse);
+MBX_API int mbx_check_qk_norm_rope(const mbx_heads_view* q_out, const mbx_heads_view* k_out,
+                                   const mbx_heads_cview* q, const mbx_heads_cview* k,
+                                   const mbx_cview* wq, const mbx_cview* wk,
+                                   const mbx_cview* positions, const mbx_cview* freqs,
+                                   const int32_t* axes, int n_axes, int interleaved, float eps);
+MBX_API int mbx_check_qk_norm_rope_backward(
+    const mbx_heads_view* dq, const mbx_heads_view* dk, const mbx_view* dwq, const mbx_view* dwk,
+    const mbx_heads_cview* dq_out, const mbx_heads_cview* dk_out, const mbx_heads_cview* q,
+    const mbx_heads_cview* k, const mbx_cview* wq, const mbx_cview* wk, const mbx_cview* positions,
+    const mbx_cview* freqs, const int32_t* axes, int n_axes, int interleaved, float eps,
+    const float* workspace, int64_t workspace_bytes);
 
 /*
  * Exhaustive self-test of the kernels' arithmetic building blocks against the

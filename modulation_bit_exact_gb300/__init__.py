@@ -40,6 +40,8 @@ __all__ = [
     "dropout", "dropout_gate_add", "dropout_gate_add_backward", "rope_axes", "rope_axis_freqs",
     "check_layer_norm", "check_layer_norm_backward", "check_ln_modulate_backward", "check_dropout",
     "check_dropout_gate_add", "check_dropout_gate_add_backward", "check_rope_axes",
+    "qk_norm_rope", "qk_norm_rope_backward", "qk_norm_grad_workspace", "check_qk_norm_rope",
+    "check_qk_norm_rope_backward",
     "LOSSLESS", "HIGH", "library_path",
 ]
 
@@ -139,6 +141,13 @@ def _load() -> ctypes.CDLL:
             "mbx_check_dropout_gate_add_backward": [_P, _P, _P, _P, _P, _f64, _vp, _i64, _vp, _i64],
             "mbx_rope_axes": [_H, _H, _H, _H, _P, _P, ctypes.POINTER(ctypes.c_int32), _int, _int, _int, _vp],
             "mbx_check_rope_axes": [_H, _H, _H, _H, _P, _P, ctypes.POINTER(ctypes.c_int32), _int, _int, _int],
+            "mbx_qk_norm_rope": [_H, _H, _H, _H, _P, _P, _P, _P, ctypes.POINTER(ctypes.c_int32), _int, _int, _f32, _vp],
+            "mbx_check_qk_norm_rope": [_H, _H, _H, _H, _P, _P, _P, _P, ctypes.POINTER(ctypes.c_int32), _int, _int, _f32],
+            "mbx_qk_norm_grad_workspace": [_i64, _i64, _i64, ctypes.POINTER(_i64)],
+            "mbx_qk_norm_rope_backward": [_H, _H, _P, _P, _H, _H, _H, _H, _P, _P, _P, _P,
+                                          ctypes.POINTER(ctypes.c_int32), _int, _int, _f32, _vp, _i64, _vp],
+            "mbx_check_qk_norm_rope_backward": [_H, _H, _P, _P, _H, _H, _H, _H, _P, _P, _P, _P,
+                                                ctypes.POINTER(ctypes.c_int32), _int, _int, _f32, _vp, _i64],
             "mbx_selftest": [_int, _vp, _vp],
             "mbx_abi_version": [],
         }
@@ -661,6 +670,57 @@ def rope_axes(q, k, positions, freqs, axes, interleaved: bool = True, inverse: b
 
 def check_rope_axes(q_out, k_out, q, k, positions, freqs, axes, interleaved=True, inverse=False) -> int:
     return _load().mbx_check_rope_axes(*_rope_args(q, k, positions, freqs, axes, interleaved, inverse, q_out, k_out))
+
+
+def _opt_heads(t):
+    return None if t is None else _heads(t)
+
+
+def _axes(axes):
+    return (ctypes.c_int32 * max(1, len(axes)))(*axes), len(axes)
+
+
+def qk_norm_rope(q, k, wq, wk, positions, freqs, axes, interleaved: bool = True, eps: float = 1e-6, q_out=None,
+                 k_out=None):
+    """RMSNorm of every head of Q and K and the rotation of ``rope_axes``, in one
+    pass (see mbx_qk_norm_rope).
+
+    q [B, S, Hq, hd] and k [B, S, Hk, hd] (or None), strided as ``rope_axes``
+    takes them; wq, wk [hd] of their dtype or float32, or None (1); positions,
+    freqs and axes as there.  Returns (q_out, k_out); ``q_out=q, k_out=k`` is in
+    place."""
+    return _native().qk_norm_rope(q, k, wq, wk, positions, freqs, axes, interleaved, eps, q_out, k_out)
+
+
+def check_qk_norm_rope(q_out, k_out, q, k, wq, wk, positions, freqs, axes, interleaved=True, eps=1e-6) -> int:
+    return _load().mbx_check_qk_norm_rope(
+        _heads(q_out), _opt_heads(k_out), _heads(q), _opt_heads(k), _opt(wq), _opt(wk), _view(positions), _view(freqs),
+        *_axes(axes), int(interleaved), eps)
+
+
+def qk_norm_grad_workspace(batch: int, tokens: int, head_dim: int) -> int:
+    """Workspace bytes of ``qk_norm_rope_backward`` on the current device (see
+    mbx_qk_norm_grad_workspace)."""
+    n = ctypes.c_int64()
+    _raise(_load().mbx_qk_norm_grad_workspace(batch, tokens, head_dim, ctypes.byref(n)))
+    return n.value
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, positions, freqs, axes, interleaved: bool = True,
+                          eps: float = 1e-6, dq=None, dk=None, dwq=None, dwk=None):
+    """Gradients of ``qk_norm_rope`` (see mbx_qk_norm_rope_backward): (dq, dk,
+    dwq, dwk), the last two summed over batch, tokens and heads.  dq_out, dk_out
+    are the gradients of its outputs, the rest its inputs.  What has no input
+    (no K, no weight) is None.  ``dq=dq_out, dk=dk_out`` is in place."""
+    return _native().qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, positions, freqs, axes, interleaved, eps,
+                                           dq, dk, dwq, dwk)
+
+
+def check_qk_norm_rope_backward(dq, dk, dwq, dwk, dq_out, dk_out, q, k, wq, wk, positions, freqs, axes,
+                                interleaved=True, eps=1e-6, workspace=None) -> int:
+    return _load().mbx_check_qk_norm_rope_backward(
+        _heads(dq), _opt_heads(dk), _opt(dwq), _opt(dwk), _heads(dq_out), _opt_heads(dk_out), _heads(q), _opt_heads(k),
+        _opt(wq), _opt(wk), _view(positions), _view(freqs), *_axes(axes), int(interleaved), eps, *_ws_args(workspace))
 
 
 # ---------------------------------------------------------------- validation only

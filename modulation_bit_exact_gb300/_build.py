@@ -22,6 +22,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = [
     os.path.join(CSRC, "mbx_api.cu"),
     os.path.join(CSRC, "train_api.cu"),
+    os.path.join(CSRC, "qknorm_api.cu"),
     os.path.join(KERN, "ln_modulate.cu"),
     os.path.join(KERN, "ln_nvfp4.cu"),
     os.path.join(KERN, "rmsnorm.cu"),
@@ -33,10 +34,12 @@ SOURCES = [
     os.path.join(KERN, "dropout.cu"),
     os.path.join(KERN, "colsum.cu"),
     os.path.join(KERN, "rope.cu"),
+    os.path.join(KERN, "qknorm.cu"),
+    os.path.join(KERN, "qknorm_bwd.cu"),
     os.path.join(KERN, "selftest.cu"),
 ]
 HEADERS = [os.path.join(KERN, f) for f in os.listdir(KERN) if f.endswith((".cuh", ".h", ".inc"))]
-HEADERS += [os.path.join(CSRC, "views.h"), os.path.join(INCLUDE, "mbx.h")]
+HEADERS += [os.path.join(CSRC, "views.h"), os.path.join(CSRC, "heads.h"), os.path.join(INCLUDE, "mbx.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [

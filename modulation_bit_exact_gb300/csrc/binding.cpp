@@ -172,6 +172,17 @@ PyObject* wrap3(const at::Tensor& a, const at::Tensor& b, const at::Tensor& c) {
     return r;
 }
 
+PyObject* wrap4(const at::Tensor& a, const at::Tensor& b, const at::Tensor& c, const at::Tensor& d) {
+    PyObject* r = PyTuple_New(4);
+    Py_ssize_t i = 0;
+    for (const at::Tensor* t : {&a, &b, &c, &d}) {
+        PyObject* o = r ? wrap(*t) : nullptr;
+        if (r && !o) Py_CLEAR(r);
+        if (r) PyTuple_SET_ITEM(r, i++, o);
+    }
+    return r;
+}
+
 bool count_is(Py_ssize_t n, Py_ssize_t want) {
     if (n == want) return true;
     PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, n);
@@ -314,23 +325,30 @@ int heads(H& h, const at::Tensor& t) {
     return MBX_OK;
 }
 
+// The widths of the axes: false with a Python error set.  Out of range: 0, which
+// the library refuses.
+bool axis_widths(PyObject* o, std::vector<int32_t>& axes) {
+    PyObject* seq = PySequence_Fast(o, "axes: expected a sequence of integers");
+    if (!seq) return false;
+    for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(seq); ++i) {
+        const long v = PyLong_AsLong(PySequence_Fast_GET_ITEM(seq, i));
+        if (v == -1 && PyErr_Occurred()) {
+            Py_DECREF(seq);
+            return false;
+        }
+        axes.push_back(v < 0 || v > 1 << 20 ? 0 : (int32_t)v);
+    }
+    Py_DECREF(seq);
+    return true;
+}
+
 // q, k, positions, freqs, axes, interleaved, inverse, q_out, k_out
 PyObject* rope_axes(PyObject* const* a) {
     const at::Tensor& q = tensor(a[0]);
     const at::Tensor k = tensor_or_none(a[1]);
     const In pos(tensor(a[2])), freqs(tensor(a[3]));
     std::vector<int32_t> axes;
-    PyObject* seq = PySequence_Fast(a[4], "axes: expected a sequence of integers");
-    if (!seq) return nullptr;
-    for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(seq); ++i) {
-        const long v = PyLong_AsLong(PySequence_Fast_GET_ITEM(seq, i));
-        if (v == -1 && PyErr_Occurred()) {
-            Py_DECREF(seq);
-            return nullptr;
-        }
-        axes.push_back(v < 0 || v > 1 << 20 ? 0 : (int32_t)v);  // out of range: refused
-    }
-    Py_DECREF(seq);
+    if (!axis_widths(a[4], axes)) return nullptr;
     if (axes.empty() || axes.size() > 4) return raise_status(MBX_E_ARG);
     const int interleaved = PyObject_IsTrue(a[5]), inverse = PyObject_IsTrue(a[6]);
     if (interleaved < 0 || inverse < 0) return nullptr;
@@ -353,6 +371,84 @@ PyObject* rope_axes(PyObject* const* a) {
     return wrap2(qo, ko);
 }
 
+// An optional tensor of heads: its view, or a null pointer.
+template <class H>
+struct OptHeads {
+    H v{};
+    bool has;
+    int status;
+    explicit OptHeads(const at::Tensor& t) : has(t.defined()), status(has ? heads(v, t) : MBX_OK) {}
+    const H* ptr() const { return has ? &v : nullptr; }
+};
+using HeadsIn = OptHeads<mbx_heads_cview>;
+using HeadsOut = OptHeads<mbx_heads_view>;
+
+// q, k, wq, wk, positions, freqs, axes, interleaved, eps, q_out, k_out
+PyObject* qk_norm_rope(PyObject* const* a) {
+    const at::Tensor& q = tensor(a[0]);
+    const at::Tensor k = tensor_or_none(a[1]);
+    const In wq(tensor_or_none(a[2])), wk(tensor_or_none(a[3])), pos(tensor(a[4])), freqs(tensor(a[5]));
+    std::vector<int32_t> axes;
+    if (!axis_widths(a[6], axes)) return nullptr;
+    if (axes.empty() || axes.size() > 4) return raise_status(MBX_E_ARG);
+    const int interleaved = PyObject_IsTrue(a[7]);
+    if (interleaved < 0) return nullptr;
+    const float eps = (float)number(a[8]);
+    at::Tensor qo = tensor_or_none(a[9]), ko = tensor_or_none(a[10]);
+    if (!qo.defined()) qo = at::empty_like(q);
+    if (!ko.defined() && k.defined()) ko = at::empty_like(k);
+    const HeadsIn qv(q), kv(k);
+    const HeadsOut qov(qo), kov(ko);
+    for (int st : {qv.status, qov.status, kv.status, kov.status})
+        if (st) return raise_status(st);
+    void* s = stream_of(q);
+    if (int st = call([&] {
+            return mbx_qk_norm_rope(qov.ptr(), kov.ptr(), qv.ptr(), kv.ptr(), wq.ptr(), wk.ptr(), pos.ptr(), freqs.ptr(),
+                                    axes.data(), (int)axes.size(), interleaved, eps, s);
+        }))
+        return raise_status(st);
+    return wrap2(qo, ko);
+}
+
+// dq_out, dk_out, q, k, wq, wk, positions, freqs, axes, interleaved, eps, dq, dk, dwq, dwk
+PyObject* qk_norm_rope_backward(PyObject* const* a) {
+    const at::Tensor &dqo = tensor(a[0]), &q = tensor(a[2]);
+    const at::Tensor dko = tensor_or_none(a[1]), k = tensor_or_none(a[3]);
+    const at::Tensor wq = tensor_or_none(a[4]), wk = tensor_or_none(a[5]);
+    const In pos(tensor(a[6])), freqs(tensor(a[7]));
+    std::vector<int32_t> axes;
+    if (!axis_widths(a[8], axes)) return nullptr;
+    if (axes.empty() || axes.size() > 4) return raise_status(MBX_E_ARG);
+    const int interleaved = PyObject_IsTrue(a[9]);
+    if (interleaved < 0) return nullptr;
+    const float eps = (float)number(a[10]);
+    at::Tensor dq = tensor_or_none(a[11]), dk = tensor_or_none(a[12]), dwq = tensor_or_none(a[13]), dwk = tensor_or_none(a[14]);
+    if (!dq.defined()) dq = at::empty_like(q);
+    if (!dk.defined() && k.defined()) dk = at::empty_like(k);
+    if (!dwq.defined() && wq.defined()) dwq = like(wq);
+    if (!dwk.defined() && wk.defined()) dwk = like(wk);
+    const HeadsIn qv(q), kv(k), dqov(dqo), dkov(dko);
+    const HeadsOut dqv(dq), dkv(dk);
+    for (int st : {qv.status, dqov.status, dqv.status, kv.status, dkov.status, dkv.status})
+        if (st) return raise_status(st);
+    const In wqv(wq), wkv(wk);
+    const Out dwqv(dwq), dwkv(dwk);
+    at::Tensor ws;
+    int64_t bytes = 0;
+    if ((dwq.defined() || dwk.defined()) && q.is_cuda() &&
+        mbx_qk_norm_grad_workspace(qv.v.batch, qv.v.tokens, qv.v.head_dim, &bytes) == MBX_OK)
+        ws = at::empty({bytes / 4}, q.options().dtype(at::kFloat));
+    float* wp = ws.defined() ? static_cast<float*>(ws.data_ptr()) : nullptr;
+    void* s = stream_of(q);
+    if (int st = call([&] {
+            return mbx_qk_norm_rope_backward(dqv.ptr(), dkv.ptr(), dwqv.ptr(), dwkv.ptr(), dqov.ptr(), dkov.ptr(), qv.ptr(),
+                                             kv.ptr(), wqv.ptr(), wkv.ptr(), pos.ptr(), freqs.ptr(), axes.data(),
+                                             (int)axes.size(), interleaved, eps, wp, bytes, s);
+        }))
+        return raise_status(st);
+    return wrap4(dq, dk, dwq, dwk);
+}
+
 PyObject* set_error(PyObject*, PyObject* cls) {
     Py_INCREF(cls);
     Py_XSETREF(g_error, cls);
@@ -372,6 +468,8 @@ PyMethodDef g_methods[] = {
     method<7, dropout_gate_add>("dropout_gate_add"),
     method<8, dropout_gate_add_backward>("dropout_gate_add_backward"),
     method<9, rope_axes>("rope_axes"),
+    method<11, qk_norm_rope>("qk_norm_rope"),
+    method<15, qk_norm_rope_backward>("qk_norm_rope_backward"),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

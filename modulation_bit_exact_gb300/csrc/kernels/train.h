@@ -146,11 +146,30 @@ struct RopeParams {
     bool inverse;
 };
 
+// Norm and rotation of Q and K heads.  Forward: rope's tensors are x and out;
+// backward: x and dx, with dout beside them, and rope.inverse is set.
+struct GradIn {
+    const void* in;
+    int64_t ib, it, ih;  // batch, token and head strides (elements)
+};
+struct QkNormParams {
+    RopeParams rope;
+    GradIn dout[2];
+    const void* w[2];  // [hd] or null (1), of Q and of K
+    bool w_f32;
+    float eps, inv_hd;
+    float* ws;  // backward: [parts][2][hd] sums for the weights' gradients, or null
+};
+int64_t qk_norm_grad_parts(int64_t batch, int64_t tokens);
+
 cudaError_t launch_layer_norm(const LnFwdParams& p, bool f32, bool vec, cudaStream_t s);
 cudaError_t launch_ln_backward(const LnBwdParams& p, bool f32, bool vec, cudaStream_t s);
 cudaError_t launch_dropout(const DropParams& p, bool f32, bool vec, cudaStream_t s);
 cudaError_t launch_dropout_backward(const DropParams& p, bool f32, bool vec, cudaStream_t s);
 cudaError_t launch_column_sums(const ColSumParams& p, cudaStream_t s);
 cudaError_t launch_rope_axes(const RopeParams& p, bool f32, bool interleaved, int align, cudaStream_t s);
+cudaError_t launch_qk_norm_rope(const QkNormParams& p, bool f32, bool interleaved, int align, cudaStream_t s);
+cudaError_t launch_qk_norm_rope_backward(const QkNormParams& p, bool f32, bool interleaved, int align,
+                                         const ColSumParams& sums, cudaStream_t s);
 
 }  // namespace mbx

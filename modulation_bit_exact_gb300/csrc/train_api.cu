@@ -7,16 +7,11 @@
 #include <atomic>
 #include <cmath>
 
-#include "mbx.h"
+#include "heads.h"
 #include "kernels/train.h"
-#include "views.h"
+#include "mbx.h"
 
 namespace {
-
-// Activations are bfloat16 or binary32, one type a call; parameters have the
-// activations' type, or binary32 with bfloat16 activations.
-bool act_dtype(int32_t d) { return d == MBX_BF16 || d == MBX_F32; }
-bool param_dtype(int32_t p, int32_t act) { return p == act || p == MBX_F32; }
 
 // A set of views with the checks of one call.  add() in the order in which the
 // entry point names its operands.
@@ -40,22 +35,7 @@ struct Operands {
 
 int check_same_shape(const V& a, const V& x) { return a.rows == x.rows && a.cols == x.cols ? MBX_OK : MBX_E_SHAPE; }
 
-int check_eps(float eps) { return eps >= 0.0f && std::isfinite(eps) ? MBX_OK : MBX_E_ARG; }
-
 bool vec_row(const V& v) { return aligned16(v); }
-
-// The workspace of a call that needs `need` bytes of it, overlapping none of
-// the n views.
-int check_workspace(const float* ws, int64_t bytes, int64_t need, const V* views, int n) {
-    if (!ws) return MBX_E_NULL;
-    if (bytes < need) return MBX_E_BOUNDS;
-    if (reinterpret_cast<uintptr_t>(ws) % 16) return MBX_E_ALIGN;
-    const V w{ws, 1, need / 4, need / 4, MBX_F32};
-    MBX_TRY(extent_ok(w));
-    for (int i = 0; i < n; ++i)
-        if (overlaps(w, views[i])) return MBX_E_ALIAS;
-    return MBX_OK;
-}
 
 // Rows, columns and counts that the kernels' index arithmetic takes.
 int check_extent(const V& x) {
@@ -295,110 +275,6 @@ mbx::DropParams drop_params(const mbx_view* out, const mbx_cview* x, const mbx_c
 
 // ---------------------------------------------------------------- rotary positions
 
-// A heads view in one form.  Strides of dimensions of size 1 address nothing
-// and are taken as 0.
-struct H4 {
-    const void* data;
-    int64_t b, t, h, hd, sb, st, sh;
-    int32_t dtype;
-    int64_t es() const { return esize(dtype); }
-    int64_t head_span() const { return (h - 1) * sh + hd; }
-    int64_t token_span() const { return (t - 1) * st + head_span(); }
-    int64_t span() const { return (b - 1) * sb + token_span(); }
-};
-
-template <class W>
-H4 of4(const W* w) {
-    return H4{w->data,
-              w->batch,
-              w->tokens,
-              w->heads,
-              w->head_dim,
-              w->batch > 1 ? w->batch_stride : 0,
-              w->tokens > 1 ? w->token_stride : 0,
-              w->heads > 1 ? w->head_stride : 0,
-              w->dtype};
-}
-
-int basic4(const H4& v) {
-    if (!v.data) return MBX_E_NULL;
-    if (!act_dtype(v.dtype)) return MBX_E_DTYPE;
-    if (v.b <= 0 || v.t <= 0 || v.h <= 0 || v.hd <= 0) return MBX_E_EMPTY;
-    if (v.hd > 256) return MBX_E_DIM_TOO_LARGE;
-    if (v.h > (int64_t)1 << 20 || v.b > (int64_t)1 << 40 || v.t > (int64_t)1 << 40) return MBX_E_ARG;
-    if (v.sb < 0 || v.st < 0 || v.sh < 0) return MBX_E_STRIDE;
-    if (reinterpret_cast<uintptr_t>(v.data) % v.es()) return MBX_E_ALIGN;
-    int64_t a = 0, bb = 0, c = 0, n = 0, bytes = 0;
-    uintptr_t end = 0;
-    if (__builtin_mul_overflow(v.b - 1, v.sb, &a) || __builtin_mul_overflow(v.t - 1, v.st, &bb) ||
-        __builtin_mul_overflow(v.h - 1, v.sh, &c) || __builtin_add_overflow(a, bb, &n) ||
-        __builtin_add_overflow(n, c, &n) || __builtin_add_overflow(n, v.hd, &n) ||
-        __builtin_mul_overflow(n, v.es(), &bytes) ||
-        __builtin_add_overflow(reinterpret_cast<uintptr_t>(v.data), (uintptr_t)bytes, &end))
-        return MBX_E_BOUNDS;
-    return MBX_OK;
-}
-
-// No two elements of an output share an address: sorted by stride, each
-// dimension's stride covers the span of those below it.
-int injective4(const H4& v) {
-    int64_t n[3] = {v.h, v.t, v.b}, s[3] = {v.sh, v.st, v.sb};
-    for (int i = 0; i < 3; ++i)
-        for (int j = i + 1; j < 3; ++j)
-            if (s[j] < s[i]) {
-                const int64_t a = n[i], c = s[i];
-                n[i] = n[j];
-                s[i] = s[j];
-                n[j] = a;
-                s[j] = c;
-            }
-    int64_t span = v.hd;
-    for (int i = 0; i < 3; ++i) {
-        if (n[i] == 1) continue;
-        if (s[i] < span) return MBX_E_STRIDE;
-        span += (n[i] - 1) * s[i];
-    }
-    return MBX_OK;
-}
-
-bool same4(const H4& a, const H4& b) {
-    return a.data == b.data && a.b == b.b && a.t == b.t && a.h == b.h && a.hd == b.hd && a.sb == b.sb &&
-           a.st == b.st && a.sh == b.sh;
-}
-
-// Whether two views share no element: their address ranges are apart, or they
-// repeat with one period (the batch's, the token's or the head's stride) and lie
-// in disjoint parts of it, as Q and K inside a merged QKV buffer do.
-bool disjoint4(const H4& a, const H4& b) {
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.data), b0 = reinterpret_cast<uintptr_t>(b.data);
-    if (a0 + a.span() * a.es() <= b0 || b0 + b.span() * b.es() <= a0) return true;
-    if (a.dtype != b.dtype || (b0 > a0 ? b0 - a0 : a0 - b0) % a.es()) return false;
-    const bool a_first = a0 <= b0;
-    const H4 &lo = a_first ? a : b, &hi = a_first ? b : a;
-    const int64_t delta = (int64_t)((a_first ? b0 - a0 : a0 - b0) / a.es());
-    auto apart = [&](int64_t period, int64_t span_lo, int64_t span_hi) {
-        return period > 0 && delta >= span_lo && delta + span_hi <= period;
-    };
-    if (a.b > 1 && b.b > 1 && a.sb == b.sb && apart(a.sb, lo.token_span(), hi.token_span())) return true;
-    // a dimension of n entries, stride s, whose entries lie whole periods apart
-    auto whole = [](int64_t na, int64_t nb, int64_t sa, int64_t sb, int64_t period) {
-        return (na == 1 && nb == 1) || (sa == sb && period > 0 && sa % period == 0);
-    };
-    if (a.t > 1 && b.t > 1 && a.st == b.st && whole(a.b, b.b, a.sb, b.sb, a.st) &&
-        apart(a.st, lo.head_span(), hi.head_span()))
-        return true;
-    return a.h > 1 && b.h > 1 && a.sh == b.sh && whole(a.b, b.b, a.sb, b.sb, a.sh) &&
-           whole(a.t, b.t, a.st, b.st, a.sh) && apart(a.sh, a.hd, b.hd);
-}
-
-// The power of two up to 16 bytes that every head's start is a multiple of.
-int align4(const H4& v) {
-    const uint64_t bits = reinterpret_cast<uintptr_t>(v.data) | (uint64_t)((v.sb | v.st | v.sh) * v.es()) | 16;
-    return (int)(bits & (~bits + 1));
-}
-
-V flat4(const H4& v) { return V{v.data, 1, v.span(), v.span(), v.dtype}; }
-
 int check_rope(const mbx_heads_view* q_out, const mbx_heads_view* k_out, const mbx_heads_cview* q,
                const mbx_heads_cview* k, const mbx_cview* positions, const mbx_cview* freqs, const int32_t* axes,
                int n_axes, bool dev) {
@@ -413,31 +289,14 @@ int check_rope(const mbx_heads_view* q_out, const mbx_heads_view* k_out, const m
         MBX_TRY(basic4(in[i]));
     }
     const V pv = of(positions), fv = of(freqs);
-    if (pv.dtype != MBX_I32 && pv.dtype != MBX_F32) return MBX_E_DTYPE;
-    if (fv.dtype != MBX_F64) return MBX_E_DTYPE;
-    for (const V* v : {&pv, &fv}) {
-        if (v->rows <= 0 || v->cols <= 0) return MBX_E_EMPTY;
-        if (!stride_ok(*v)) return MBX_E_STRIDE;
-        if (reinterpret_cast<uintptr_t>(v->data) % esize(v->dtype)) return MBX_E_ALIGN;
-        MBX_TRY(extent_ok(*v));
-    }
+    MBX_TRY(check_turn_views(pv, fv));
     for (int i = 0; i < nt; ++i) {
         const H4& a = in[i];
         if (a.b != in[0].b || a.t != in[0].t || a.hd != in[0].hd) return MBX_E_SHAPE;
         if (out[i].b != a.b || out[i].t != a.t || out[i].h != a.h || out[i].hd != a.hd) return MBX_E_SHAPE;
         MBX_TRY(injective4(out[i]));
     }
-    int64_t tokens = 0;
-    if (__builtin_mul_overflow(in[0].b, in[0].t, &tokens) || tokens > 0x7fffffff) return MBX_E_ARG;
-    if (n_axes < 1 || n_axes > 4) return MBX_E_ARG;
-    int64_t rot = 0;
-    for (int i = 0; i < n_axes; ++i) {
-        if (axes[i] < 2 || axes[i] % 2) return MBX_E_ARG;
-        rot += axes[i];
-    }
-    if (rot > in[0].hd) return MBX_E_ARG;
-    if (pv.cols != n_axes || (pv.rows != in[0].t && pv.rows != tokens)) return MBX_E_SHAPE;
-    if (fv.rows != 1 || fv.cols != rot / 2) return MBX_E_SHAPE;
+    MBX_TRY(check_turn(in[0], pv, fv, axes, n_axes));
     // an output may be exactly its own input; nothing else overlaps an output
     for (int i = 0; i < nt; ++i) {
         for (int j = 0; j < nt; ++j) {
