@@ -325,6 +325,10 @@ MBX_API int mbx_check_gated_residual_ln_modulate_nvfp4(
     const mbx_cview* scale, const mbx_cview* shift, const float* fp4_scale, float eps, int variant);
 MBX_API int mbx_check_modulation_table_add(const mbx_view* out, const mbx_cview* table,
                                            const mbx_cview* temb);
+MBX_API int mbx_check_linear_nvfp4(const mbx_view* out, const mbx_cview* x, const mbx_cview* w4,
+                                   const mbx_cview* w_sf, const float* fp4_scale,
+                                   const mbx_cview* bias, int silu, const float* workspace,
+                                   int64_t workspace_bytes);
 MBX_API int mbx_check_gated_residual_ln_modulate(const mbx_view* residual_out,
                                                  const mbx_view* out, const mbx_cview* residual,
                                                  const mbx_cview* gate, const mbx_cview* update,
@@ -335,6 +339,32 @@ MBX_API int mbx_check_qk_norm_rope_qkv_epilogue(
     int64_t heads, const mbx_cview* wq_txt, const mbx_cview* wk_txt, const mbx_cview* wq_img,
     const mbx_cview* wk_img, const float* cos_txt, const float* sin_txt, const float* cos_img,
     const float* sin_img, float eps, int variant);
+
+/*
+ * Product of a few rows with a weight in NVFP4, as the producers above write a
+ * matrix: the projection that makes a block's scale, shift and gate vectors
+ * from its conditioning, Linear(SiLU(temb)).
+ *   out[r][n] = (sum over k of a(x[r][k]) * q[n][k] * s[n][k/16]) / gs + bias[n]
+ * a is the identity, or with silu 1 a(v) = v / (1 + exp(-v)); q the E2M1 values
+ * (w4: MBX_E2M1X2 [N, K/2], byte i of a row = q[2i] | q[2i+1] << 4), s the E4M3
+ * block scales (w_sf: MBX_E4M3 [pad128(N), pad4(K/16)], contiguous, tiled as the
+ * producers' out_sf; not negative; padding bytes are not used), gs = *fp4_scale,
+ * read on the stream.
+ * x [rows, K] MBX_BF16 or MBX_F32; out [rows, N] of x's dtype or MBX_F32; bias
+ * [1, N] of either type or NULL.  One variant: products and sums to binary32's
+ * accuracy (x is cut into exact parts where the tensor cores multiply), one
+ * rounding at the output.  An infinity or NaN of x reaches the outputs of its
+ * own row alone.  K a multiple of 16, at most 8192; rows at most 256 (more are
+ * a matrix product's work); N at most 2^24.  out overlaps nothing.
+ * The workspace (mbx_linear_nvfp4_workspace gives its bytes for the current
+ * device; 0: pass NULL) is scratch of one call: 16-byte aligned, overlapping no
+ * operand, free again when the call's work on `stream` is done.  Sums are formed
+ * in a fixed order: the same call on the same device model gives the same bits.
+ */
+MBX_API int mbx_linear_nvfp4(const mbx_view* out, const mbx_cview* x, const mbx_cview* w4,
+                             const mbx_cview* w_sf, const float* fp4_scale, const mbx_cview* bias,
+                             int silu, float* workspace, int64_t workspace_bytes, void* stream);
+MBX_API int mbx_linear_nvfp4_workspace(int64_t rows, int64_t outputs, int64_t cols, int64_t* bytes);
 
 /* ------------------------------------------------------------------------
  * The training path: affine LayerNorm, the gradients of LayerNorm and of

@@ -41,7 +41,7 @@ __all__ = [
     "check_layer_norm", "check_layer_norm_backward", "check_ln_modulate_backward", "check_dropout",
     "check_dropout_gate_add", "check_dropout_gate_add_backward", "check_rope_axes",
     "qk_norm_rope", "qk_norm_rope_backward", "qk_norm_grad_workspace", "check_qk_norm_rope",
-    "check_qk_norm_rope_backward",
+    "check_qk_norm_rope_backward", "linear_nvfp4", "check_linear_nvfp4", "linear_nvfp4_workspace", "nvfp4_weight",
     "LOSSLESS", "HIGH", "library_path",
 ]
 
@@ -148,6 +148,9 @@ def _load() -> ctypes.CDLL:
                                           ctypes.POINTER(ctypes.c_int32), _int, _int, _f32, _vp, _i64, _vp],
             "mbx_check_qk_norm_rope_backward": [_H, _H, _P, _P, _H, _H, _H, _H, _P, _P, _P, _P,
                                                 ctypes.POINTER(ctypes.c_int32), _int, _int, _f32, _vp, _i64],
+            "mbx_linear_nvfp4": [_P, _P, _P, _P, _vp, _P, _int, _vp, _i64, _vp],
+            "mbx_check_linear_nvfp4": [_P, _P, _P, _P, _vp, _P, _int, _vp, _i64],
+            "mbx_linear_nvfp4_workspace": [_i64, _i64, _i64, ctypes.POINTER(_i64)],
             "mbx_selftest": [_int, _vp, _vp],
             "mbx_abi_version": [],
         }
@@ -469,6 +472,69 @@ def check_gated_residual_ln_modulate(residual_out, out, residual, gate, update, 
         _ref(sh), eps, _variant(variant))
 
 
+# ---------------------------------------------------------------- products with NVFP4 weights
+
+
+def nvfp4_weight(weight, fp4_scale=None):
+    """A weight [N, K] (K a multiple of 16) in NVFP4 for ``linear_nvfp4``, by the
+    rule of the NVFP4 producers (see mbx_ln_modulate_nvfp4): (w4 [N, K/2] uint8,
+    w_sf in the 128x4 tile layout, fp4_scale).  Done once, when a model is
+    loaded, with torch operators on weight's device.  fp4_scale: a one-element
+    float32 tensor; by default 448 * 6 / max|weight|."""
+    N, K = weight.shape
+    if K % 16:
+        raise MbxError(-5, "MBX_E_SHAPE: the weight's last dimension must be a multiple of 16")
+    if fp4_scale is None:
+        amax = weight.detach().abs().amax().float()
+        fp4_scale = torch.where(amax > 0, 2688.0 / amax, torch.ones_like(amax)).reshape(1)
+    b = weight.detach().float().reshape(N, K // 16, 16)
+    s = (b.abs().amax(-1) * fp4_scale / 6.0).clamp(max=448.0).to(torch.float8_e4m3fn)
+    sf = s.float()
+    v = b * torch.where(sf > 0, fp4_scale / sf, torch.zeros_like(sf))[..., None]
+    m = v.abs()
+    # nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6, ties to the even code
+    code = sum(((m >= t) if i % 2 else (m > t)).to(torch.uint8)
+               for i, t in enumerate((0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)))
+    code = ((code | torch.signbit(v).to(torch.uint8) << 3) * (sf > 0)[..., None]).reshape(N, K)
+    rows, cols = nvfp4_sf_shape(N, K)
+    tiles = torch.zeros((rows, cols), dtype=torch.uint8, device=weight.device)
+    tiles[:N, :K // 16] = s.view(torch.uint8)
+    tiles = tiles.view(rows // 128, 4, 32, cols // 4, 4).permute(0, 3, 2, 1, 4).reshape(rows, cols)
+    return code[:, 0::2] | code[:, 1::2] << 4, tiles.contiguous(), fp4_scale
+
+
+def linear_nvfp4(x, w4, w_sf, fp4_scale, bias=None, silu: bool = False, out=None):
+    """out = a(x) W^T / fp4_scale + bias for a few rows x and a weight in NVFP4
+    (see mbx_linear_nvfp4); a is the identity, or SiLU with ``silu=True``: a
+    block's modulation vectors are ``linear_nvfp4(temb, ..., silu=True)``.
+
+    x [..., K] bfloat16 or float32, at most 256 rows; w4 [N, K/2] and w_sf
+    uint8 as ``nvfp4_weight`` or an NVFP4 producer makes them; fp4_scale a
+    one-element float32 CUDA tensor; bias [N] bfloat16, float32 or None.  Returns
+    out [..., N] of x's dtype; a given out may also be float32."""
+    return _native().linear_nvfp4(x, w4, w_sf, fp4_scale, bias, silu, out)
+
+
+def linear_nvfp4_workspace(rows: int, outputs: int, cols: int) -> int:
+    """Workspace bytes of ``linear_nvfp4`` on the current device (see
+    mbx_linear_nvfp4_workspace)."""
+    n = ctypes.c_int64()
+    _raise(_load().mbx_linear_nvfp4_workspace(rows, outputs, cols, ctypes.byref(n)))
+    return n.value
+
+
+def _weight_views(w4, w_sf):
+    w, f = _view(w4), _view(w_sf)
+    byte = (torch.uint8, torch.float8_e4m3fn)
+    w.dtype, f.dtype = MBX_E2M1X2 if w4.dtype in byte else 0, MBX_E4M3 if w_sf.dtype in byte else 0
+    return w, f
+
+
+def check_linear_nvfp4(out, x, w4, w_sf, fp4_scale, bias=None, silu=False, workspace=None) -> int:
+    return _load().mbx_check_linear_nvfp4(_view(out), _view(x), *_weight_views(w4, w_sf), _ptr(fp4_scale), _opt(bias),
+                                          int(silu), *_ws_args(workspace))
+
+
 def _ptr(t):
     return None if t is None or t.numel() == 0 else t.data_ptr()
 
@@ -509,7 +575,7 @@ def qk_norm_rope_qkv_epilogue(txt_qkv, img_qkv, batch: int, heads: int, head_dim
 # ---------------------------------------------------------------- training path
 
 
-# These go through _binding.so (csrc/binding.cpp), which does in native code what
+# These, and linear_nvfp4, go through _binding.so (csrc/binding.cpp), which does in native code what
 # the functions above do through ctypes: views, outputs, the current stream, the
 # call, MbxError.  The check_ functions use ctypes; a structure passes for a
 # pointer to it.

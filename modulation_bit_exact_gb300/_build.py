@@ -23,6 +23,7 @@ SOURCES = [
     os.path.join(CSRC, "mbx_api.cu"),
     os.path.join(CSRC, "train_api.cu"),
     os.path.join(CSRC, "qknorm_api.cu"),
+    os.path.join(CSRC, "linear_api.cu"),
     os.path.join(KERN, "ln_modulate.cu"),
     os.path.join(KERN, "ln_nvfp4.cu"),
     os.path.join(KERN, "rmsnorm.cu"),
@@ -36,6 +37,7 @@ SOURCES = [
     os.path.join(KERN, "rope.cu"),
     os.path.join(KERN, "qknorm.cu"),
     os.path.join(KERN, "qknorm_bwd.cu"),
+    os.path.join(KERN, "linear_nvfp4.cu"),
     os.path.join(KERN, "selftest.cu"),
 ]
 HEADERS = [os.path.join(KERN, f) for f in os.listdir(KERN) if f.endswith((".cuh", ".h", ".inc"))]

@@ -149,6 +149,12 @@ const int64_t* rng_state(const at::Tensor& rng) {
 }
 constexpr const char* kBadRng = "MBX_E_ARG: rng must be a contiguous int64 tensor (seed, counter)";
 
+// Packed values and block scales are bytes; the scales may be torch's E4M3 type.
+bool bytes_of(const at::Tensor& t) {
+    return t.scalar_type() == at::kByte || t.scalar_type() == at::kFloat8_e4m3fn;
+}
+constexpr const char* kBadScale = "MBX_E_ARG: fp4_scale must be a one-element float32 tensor";
+
 PyObject* wrap(const at::Tensor& t) {
     if (t.defined()) return THPVariable_Wrap(t);
     Py_RETURN_NONE;
@@ -449,6 +455,39 @@ PyObject* qk_norm_rope_backward(PyObject* const* a) {
     return wrap4(dq, dk, dwq, dwk);
 }
 
+// x, w4, w_sf, fp4_scale, bias, silu, out
+PyObject* linear_nvfp4(PyObject* const* a) {
+    const at::Tensor &x = tensor(a[0]), &w4 = tensor(a[1]), &gs = tensor(a[3]);
+    const In xv(x);
+    In wv(w4), sf(tensor(a[2]));
+    wv.v.dtype = bytes_of(w4) ? MBX_E2M1X2 : 0;
+    sf.v.dtype = bytes_of(tensor(a[2])) ? MBX_E4M3 : 0;
+    if (gs.scalar_type() != at::kFloat || gs.numel() != 1) return raise_status(MBX_E_ARG, kBadScale);
+    const In bias(tensor_or_none(a[4]));
+    const int silu = PyObject_IsTrue(a[5]);
+    if (silu < 0) return nullptr;
+    at::Tensor out = tensor_or_none(a[6]);
+    if (!out.defined()) {
+        std::vector<int64_t> shape(x.sizes().begin(), x.sizes().end());
+        if (shape.empty()) return raise_status(MBX_E_SHAPE);
+        shape.back() = wv.v.rows;
+        out = at::empty(shape, x.options());
+    }
+    const Out o(out);
+    int64_t bytes = 0;
+    at::Tensor ws;
+    if (x.is_cuda() && mbx_linear_nvfp4_workspace(xv.v.rows, wv.v.rows, xv.v.cols, &bytes) == MBX_OK && bytes)
+        ws = at::empty({bytes / 4}, x.options().dtype(at::kFloat));
+    float* wp = ws.defined() ? static_cast<float*>(ws.data_ptr()) : nullptr;
+    void* s = stream_of(x);
+    if (int st = call([&] {
+            return mbx_linear_nvfp4(o.ptr(), xv.ptr(), wv.ptr(), sf.ptr(), static_cast<const float*>(gs.data_ptr()),
+                                    bias.ptr(), silu, wp, bytes, s);
+        }))
+        return raise_status(st);
+    return wrap(out);
+}
+
 PyObject* set_error(PyObject*, PyObject* cls) {
     Py_INCREF(cls);
     Py_XSETREF(g_error, cls);
@@ -470,6 +509,7 @@ PyMethodDef g_methods[] = {
     method<9, rope_axes>("rope_axes"),
     method<11, qk_norm_rope>("qk_norm_rope"),
     method<15, qk_norm_rope_backward>("qk_norm_rope_backward"),
+    method<7, linear_nvfp4>("linear_nvfp4"),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
