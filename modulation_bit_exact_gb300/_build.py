@@ -38,6 +38,7 @@ SOURCES = [
     os.path.join(KERN, "qknorm.cu"),
     os.path.join(KERN, "qknorm_bwd.cu"),
     os.path.join(KERN, "linear_nvfp4.cu"),
+    os.path.join(KERN, "linear_tc.cu"),
     os.path.join(KERN, "selftest.cu"),
 ]
 HEADERS = [os.path.join(KERN, f) for f in os.listdir(KERN) if f.endswith((".cuh", ".h", ".inc"))]

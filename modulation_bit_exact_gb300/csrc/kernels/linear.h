@@ -27,6 +27,8 @@ struct LinearParams {
 
 int64_t linear_nvfp4_workspace_bytes(int rows, int64_t N, int K);
 
+bool linear_tc_takes(const LinearParams& p);
+cudaError_t launch_linear_tc(const LinearParams& p, bool x_f32, bool out_f32, cudaStream_t s);
 cudaError_t launch_linear_nvfp4(const LinearParams& p, bool x_f32, bool out_f32, cudaStream_t s);
 
 }  // namespace mbx

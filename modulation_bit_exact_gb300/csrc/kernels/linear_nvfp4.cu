@@ -124,9 +124,8 @@ static cudaError_t linear_rows(const LinearParams& p, cudaStream_t s) {
     return e != cudaSuccess ? e : last;
 }
 
-int64_t linear_nvfp4_workspace_bytes(int, int64_t, int) { return 0; }
-
 cudaError_t launch_linear_nvfp4(const LinearParams& p, bool x_f32, bool out_f32, cudaStream_t s) {
+    if (linear_tc_takes(p)) return launch_linear_tc(p, x_f32, out_f32, s);
     return x_f32 ? linear_rows<float, float>(p, s) : out_f32 ? linear_rows<uint16_t, float>(p, s) : linear_rows<uint16_t, uint16_t>(p, s);
 }
 

@@ -1,0 +1,573 @@
+// linear_tc.cu -- the NVFP4 product on the tensor cores, without decoding the weight.
+//
+// tcgen05.mma.kind::mxf4nvf4 multiplies E2M1 values with an E4M3 scale for every 16
+// of them: the weight goes from memory to the tensor cores as it is stored, by TMA,
+// and its scales, whose tiles of 128 x 4 are the order that the tensor memory
+// wants, by tcgen05.cp.  So the few activations have to be E2M1 too.  They are cut
+// into digits: a block of 16 with |x| < 2^e is x = 2^(e-22) * I with whole I,
+// |I| <= 2^22, and I = sum over i < 8 of d_i * 8^i with digits d_i from -4 to 3, whose halves
+// are E2M1 values.  The block's 2^e, as far as 2^-17 of the row's largest, is the
+// block's E4M3 scale.  A row of x becomes eight columns of the product, one a
+// digit, whose sums the epilogue adds up by their powers of 8: the accuracy is that
+// of binary32 products, and one to sixteen rows cost the same, 8 to 128 columns.
+//
+// An infinity or NaN has no digits: it counts as 0 there, and the epilogue adds its
+// products, from the weight in memory, to the outputs of its row.
+//
+// A block of threads keeps the digits of one slice of K (up to 4 pieces of 256) and
+// walks the tiles of 128 outputs of its group; the slices' sums are added in order
+// by a second kernel.  Warps 0 to 3 read the accumulators and write, warp 4 copies,
+// warp 5 multiplies; all but the copying warp make the digits first, while the
+// first weights are on their way.  Bound by the weight's bytes.
+#include <cuda.h>
+
+#include <atomic>
+#include <mutex>
+
+#include "linear.h"
+#include "rowgroup.cuh"
+
+namespace mbx {
+
+constexpr int kTile = 128, kPiece = 256, kMaxPieces = 4, kPassRows = 16, kMaxStages = 12;
+constexpr int kTcThreads = 256, kDigitThreads = 224;
+constexpr int kStageBytes = 16384, kStageScales = 2048;
+constexpr int kMaxSmem = 227 * 1024;
+// tensor memory: two accumulators, the stages' scales (16 columns each), the digits' scales
+constexpr uint32_t kAccCols = 128, kScaleCol = 256, kDigitScaleCol = 448;
+
+struct TcParams {
+    LinearParams l;
+    int slices, pieces_per_slice, groups, stages, tiles;
+    bool x_f32, out_f32, x_vec;
+};
+
+// How K is cut into slices and the tiles shared out: the fewest pieces in a row for
+// a block, a second kernel counting as four of them (it takes about as long).  The
+// rows do not matter, so that a row's sums have one order.
+struct TcPlan {
+    int slices, pieces_per_slice, groups, tiles;
+};
+static TcPlan tc_plan(int64_t N, int K) {
+    const int pieces = (K + kPiece - 1) / kPiece, sms = sm_count();
+    const int64_t tiles = (N + kTile - 1) / kTile;
+    TcPlan best = {};
+    int64_t cost = INT64_MAX;
+    for (int len = 1; len <= kMaxPieces && len <= pieces; ++len) {
+        const int slices = (pieces + len - 1) / len;
+        int64_t groups = sms / slices;
+        if (groups < 1) continue;
+        if (groups > tiles) groups = tiles;
+        const int64_t c = (tiles + groups - 1) / groups * len + (slices > 1 ? 4 : 0);
+        if (c < cost) {
+            cost = c;
+            best = TcPlan{slices, len, (int)groups, (int)tiles};
+        }
+    }
+    return best;
+}
+
+int64_t linear_nvfp4_workspace_bytes(int rows, int64_t N, int K) {
+    const TcPlan p = tc_plan(N, K);
+    return p.slices > 1 ? ((int64_t)p.slices * rows * N * 4 + 15) / 16 * 16 : 0;
+}
+
+// ---------------------------------------------------------------- barriers, copies, tensor memory
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(uint32_t bar, int n) { asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(n)); }
+__device__ __forceinline__ void bar_arrive(uint32_t bar) { asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory"); }
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok;
+}
+// Waits for the phase, for a second at most; false, and *failed set, when it did not
+// come or another wait of the block had failed.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
+    for (int i = 0; i < 64; ++i)
+        if (bar_try(bar, parity)) return true;
+    unsigned long long t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    do {
+        for (int i = 0; i < 64; ++i)
+            if (bar_try(bar, parity)) return true;
+        if (*failed) return false;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    } while (t - t0 < 1000000000ull);
+    *failed = 1;
+    return false;
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// K-major operand in 128-byte rows, 128-byte swizzle: 8 rows every 1024 bytes.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// 32 rows of 16 bytes, no swizzle: 8 rows every 128 bytes.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(128 >> 4) << 32 | 1ull << 46;
+}
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t smem) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(scale_desc(smem)) : "memory");
+}
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, bool add) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.u32 p, %6, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// ---------------------------------------------------------------- activations and their digits
+
+__device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
+
+// One block of 16 activations: x[row][16 * blk ...].
+__device__ __forceinline__ void load_block(float (&v)[16], const TcParams& p, int row, int blk) {
+    const int64_t at = (int64_t)row * p.l.x_stride + 16 * blk;
+    if (p.x_f32) {
+        const float* x = static_cast<const float*>(p.l.x) + at;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (p.x_vec) {
+                const uint4 q = ld_stream_rw(x + 4 * i);
+                v[4 * i] = __uint_as_float(q.x), v[4 * i + 1] = __uint_as_float(q.y);
+                v[4 * i + 2] = __uint_as_float(q.z), v[4 * i + 3] = __uint_as_float(q.w);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[4 * i + j] = load_elem(x + 4 * i + j);
+            }
+        }
+    } else {
+        const uint16_t* x = static_cast<const uint16_t*>(p.l.x) + at;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (p.x_vec) {
+                const uint4 q = ld_stream_rw(x + 8 * i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[8 * i + 2 * j] = lo_f(w_of(q, j)), v[8 * i + 2 * j + 1] = hi_f(w_of(q, j));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[8 * i + j] = load_elem(x + 8 * i + j);
+            }
+        }
+    }
+    if (p.l.silu) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = silu(v[i]);
+    }
+}
+
+// The largest magnitude of a block's finite values, as bits; *odd set where one is not finite.
+__device__ __forceinline__ uint32_t block_max(const float (&v)[16], int* odd) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
+        if (b >= 0x7f800000u) *odd = 1;
+        else m = max(m, b);
+    }
+    return m;
+}
+// e with |v| < 2^e; magnitudes below 2^-85 (of a row) take that.
+__device__ __forceinline__ int above(uint32_t bits) { return (int)(bits >> 23) - 126; }
+
+// The digits of v * 2^(22-e), digit i in nibble i as an E2M1 code of d_i / 2.
+__device__ __forceinline__ uint32_t digits(float v, float to_int) {
+    // digits + 4 are the octal places of I + 044444444, spread from 3 to 4 bits each
+    uint32_t x = (uint32_t)(__float2int_rn(v * to_int) + 9586980);
+    x = (x & 0x00000fffu) | (x & 0x00fff000u) << 4;
+    x = (x & 0x003f003fu) | (x & 0x0fc00fc0u) << 2;
+    x = (x & 0x07070707u) | (x & 0x38383838u) << 1;
+    // 4..7: the code is the place - 4; 0..3: 8 + (4 - the place)
+    const uint32_t m = (x >> 2) & 0x11111111u, up = (m << 4) - m;
+    return (x & 0x33333333u & up) | ((0xccccccccu - x) & ~up);
+}
+// Nibble j of w[i] becomes nibble i of w[j].
+__device__ __forceinline__ void transpose_nibbles(uint32_t (&w)[8]) {
+    uint32_t t[8], u[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        t[j] = __byte_perm(w[j], w[j + 4], 0x5410);
+        t[j + 4] = __byte_perm(w[j], w[j + 4], 0x7632);
+    }
+#pragma unroll
+    for (int h = 0; h < 8; h += 4)
+#pragma unroll
+        for (int j = h; j < h + 2; ++j) {
+            u[j] = __byte_perm(t[j], t[j + 2], 0x6240);
+            u[j + 2] = __byte_perm(t[j], t[j + 2], 0x7351);
+        }
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        w[j] = (u[j] & 0x0f0f0f0fu) | (u[j + 1] & 0x0f0f0f0fu) << 4;
+        w[j + 1] = (u[j] >> 4 & 0x0f0f0f0fu) | (u[j + 1] & 0xf0f0f0f0u);
+    }
+}
+
+// sum over the slice's k with a non-finite activation of a(x[row][k]) * w[n][k]
+__device__ __noinline__ float odd_products(const TcParams& p, int row, int64_t n, int blk0, int blk1) {
+    float sum = 0.0f;
+    for (int blk = blk0; blk < blk1; ++blk) {
+        float v[16];
+        load_block(v, p, row, blk);
+        int odd = 0;
+        block_max(v, &odd);
+        if (!odd) continue;
+        const uint8_t b = p.l.sf[(n / 128 * p.l.sf_col_tiles + blk / 4) * 512 + n % 32 * 16 + n % 128 / 32 * 4 + blk % 4];
+        uint32_t h;
+        float s;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)b));
+        asm("{\n.reg .f16 a, b;\nmov.b32 {a, b}, %1;\ncvt.f32.f16 %0, a;\n}" : "=f"(s) : "r"(h));
+        for (int i = 0; i < 16; ++i) {
+            if ((__float_as_uint(v[i]) & 0x7f800000u) != 0x7f800000u) continue;
+            const uint32_t c = p.l.w4[n * p.l.w_stride + blk * 8 + i / 2] >> (i % 2 * 4) & 15u;
+            const uint32_t e = c >> 1 & 3u;
+            const float m = e ? __uint_as_float((e + 126u) << 23 | (c & 1u) << 22) : (float)(c & 1u) * 0.5f;
+            sum += v[i] * ((c & 8u ? -m : m) * s);
+        }
+    }
+    return sum;
+}
+
+__device__ __forceinline__ void store_output(const TcParams& p, int row, int64_t n, float sum, float gs) {
+    float v = sum / gs;
+    if (p.l.bias) v += p.l.bias_f32 ? load_elem(static_cast<const float*>(p.l.bias) + n)
+                                    : load_elem(static_cast<const uint16_t*>(p.l.bias) + n);
+    const int64_t at = (int64_t)row * p.l.out_stride + n;
+    if (p.out_f32) store_elem(static_cast<float*>(p.l.out) + at, v);
+    else store_elem(static_cast<uint16_t*>(p.l.out) + at, v);
+}
+
+// ---------------------------------------------------------------- the product
+
+struct TcShared {
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
+    uint32_t tmem;
+    int failed;
+    uint32_t row_max[kPassRows];
+    int odd[kPassRows];
+};
+
+__global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_constant__ CUtensorMap map, const TcParams p) {
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t* smem = raw_smem + ((1024u - (smem_addr(raw_smem) & 1023u)) & 1023u);
+    __shared__ TcShared sh;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int row0 = blockIdx.y * kPassRows, rows = min(p.l.rows - row0, kPassRows);
+    const int cols = (rows * 8 + 15) / 16 * 16;  // of the product
+    const int slice = blockIdx.x % p.slices, group = blockIdx.x / p.slices;
+    const int blocks = p.l.K / 16, piece0 = slice * p.pieces_per_slice;
+    const int piece1 = min(piece0 + p.pieces_per_slice, (p.l.K + kPiece - 1) / kPiece);
+    const int blk0 = piece0 * 16, blk1 = min(piece1 * 16, blocks), steps = (blk1 - blk0 + 3) / 4;
+    const int my_tiles = (p.tiles - group + p.groups - 1) / p.groups;
+    uint8_t* ring = smem;
+    uint8_t* dig = ring + p.stages * kStageBytes;            // [pieces][cols][128 bytes], swizzled
+    uint8_t* scales = dig + p.pieces_per_slice * cols * 128;  // the stages'
+    uint8_t* dig_scales = scales + p.stages * kStageScales;   // [steps][512]
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            bar_init(smem_addr(&sh.full[i]), 1);
+            bar_init(smem_addr(&sh.empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(smem_addr(&sh.acc_full[i]), 1);
+            bar_init(smem_addr(&sh.acc_empty[i]), 4);
+        }
+        bar_init(smem_addr(&sh.drained), 1);
+        sh.failed = 0;
+        for (int i = 0; i < kPassRows; ++i) sh.row_max[i] = sh.odd[i] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
+    }
+    if (warp == 5) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    volatile int* failed = &sh.failed;
+    grid_dep_wait();
+    grid_dep_launch();
+
+    if (warp == 4) {
+        if (lane == 0) {
+            int u = 0;
+            for (int t = 0; t < my_tiles; ++t) {
+                const int tile = group + t * p.groups;
+                for (int piece = piece0; piece < piece1; ++piece, ++u) {
+                    const int s = u % p.stages;
+                    if (u >= p.stages && !bar_wait(smem_addr(&sh.empty[s]), (u / p.stages - 1) & 1, failed)) break;
+                    const uint32_t bar = smem_addr(&sh.full[s]);
+                    const uint32_t bytes = (uint32_t)min(4, p.l.sf_col_tiles - piece * 4) * 512;
+                    bar_expect(bar, kStageBytes + bytes);
+                    asm volatile(
+                        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                            smem_addr(ring + s * kStageBytes)),
+                        "l"(&map), "r"(piece * 128), "r"(tile * kTile), "r"(bar)
+                        : "memory");
+                    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                     smem_addr(scales + s * kStageScales)),
+                                 "l"(p.l.sf + ((int64_t)tile * p.l.sf_col_tiles + piece * 4) * 512), "r"(bytes), "r"(bar)
+                                 : "memory");
+                }
+                if (*failed) break;
+            }
+            // after a failure: the copies that are under way have to land before the block ends
+            if (*failed)
+                for (int i = u > p.stages ? u - p.stages : 0; i < u; ++i)
+                    for (int k = 0; k < 100000 && !bar_try(smem_addr(&sh.full[i % p.stages]), (i / p.stages) & 1); ++k) {
+                    }
+        }
+    } else {
+        // the digits: a thread takes a row's block at a time
+        const int id = threadIdx.x - (warp > 4 ? 32 : 0), per_row = steps * 4, items = rows * per_row;
+        float v[16];
+        for (int it = id; it < items; it += kDigitThreads) {
+            const int r = it / per_row, blk = blk0 + it - r * per_row;
+            if (blk >= blk1) continue;
+            load_block(v, p, row0 + r, blk);
+            int odd = 0;
+            atomicMax(&sh.row_max[r], block_max(v, &odd));
+            if (odd) sh.odd[r] = 1;
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(kDigitThreads) : "memory");
+        for (int it = id; it < items; it += kDigitThreads) {
+            const int r = it / per_row, b = it - r * per_row, blk = blk0 + b;
+            const bool real = blk < blk1;
+            if (items > kDigitThreads && real) load_block(v, p, row0 + r, blk);
+            if (!real) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+            }
+            int odd = 0;
+            const int top = max(above(sh.row_max[r]), -85);
+            const int e = max(min(above(block_max(v, &odd)), top), top - 17);
+            const float to_int = __uint_as_float((uint32_t)(127 + 22 - e) << 23);
+            uint32_t w[2][8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float a = v[8 * h + j];
+                    w[h][j] = digits((__float_as_uint(a) & 0x7f800000u) == 0x7f800000u ? 0.0f : a, to_int);
+                }
+                transpose_nibbles(w[h]);
+            }
+            const int up = 8 + e - top;  // -9 .. 8: the scale 2^up as E4M3
+            const uint8_t sc = (uint8_t)(up >= -6 ? (up + 7) << 3 : 1 << (up + 9));
+            uint8_t* col = dig + b / 16 * cols * 128 + r * 8 * 128 + (b % 2) * 8;
+            uint8_t* ss = dig_scales + b / 4 * 512 + (r % 4) * 128 + (r / 4) * 4 + b % 4;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                *reinterpret_cast<uint2*>(col + i * 128 + ((b % 16 / 2) ^ i) * 16) = make_uint2(w[0][i], w[1][i]);
+                ss[i * 16] = sc;
+            }
+        }
+        fence_async();
+        asm volatile("bar.sync 1, %0;" ::"n"(kDigitThreads) : "memory");
+    }
+
+    if (warp == 5) {
+        const uint32_t idesc = 1u << 7 | 1u << 10 | (uint32_t)(cols / 8) << 17 | (uint32_t)(kTile / 16) << 24;
+        if (lane == 0)
+            for (int k = 0; k < steps; ++k) scales_to_tmem(tmem + kDigitScaleCol + 4 * k, smem_addr(dig_scales + k * 512));
+        int u = 0;
+        bool ok = true;
+        for (int t = 0; t < my_tiles && ok; ++t) {
+            const int a = t & 1;
+            if (t >= 2) ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.acc_empty[a]), (t / 2 - 1) & 1, failed));
+            tc_fence_after();
+            for (int piece = piece0; piece < piece1 && ok; ++piece, ++u) {
+                const int s = u % p.stages, n = min(4, p.l.sf_col_tiles - piece * 4);
+                ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.full[s]), (u / p.stages) & 1, failed));
+                if (!ok) break;
+                uint8_t* sc = scales + s * kStageScales;
+                if (blocks % 4 && piece * 16 + n * 4 > blocks) {  // the last step's blocks past K: their scales are anything
+                    const uint32_t keep = (1u << blocks % 4 * 8) - 1;
+                    for (int i = lane; i < 128; i += 32) reinterpret_cast<uint32_t*>(sc + (n - 1) * 512)[i] &= keep;
+                    fence_async();
+                    __syncwarp();
+                }
+                if (lane == 0) {
+                    const uint32_t sa = tmem + kScaleCol + 16 * s;
+                    for (int k = 0; k < n; ++k) scales_to_tmem(sa + 4 * k, smem_addr(sc + k * 512));
+                    const uint32_t wa = smem_addr(ring + s * kStageBytes), da = smem_addr(dig + (piece - piece0) * cols * 128);
+                    for (int k = 0; k < n; ++k)
+                        mma_fp4(tmem + a * kAccCols, operand_desc(wa + 32 * k), operand_desc(da + 32 * k), idesc, sa + 4 * k,
+                                tmem + kDigitScaleCol + 4 * ((piece - piece0) * 4 + k), piece > piece0 || k > 0);
+                    mma_commit(smem_addr(&sh.empty[s]));
+                }
+                __syncwarp();
+            }
+            if (lane == 0 && ok) mma_commit(smem_addr(&sh.acc_full[a]));
+            __syncwarp();
+        }
+        // nothing of the block may be under way when it gives the tensor memory back
+        if (lane == 0) {
+            mma_commit(smem_addr(&sh.drained));
+            bar_wait(smem_addr(&sh.drained), 0, failed);
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        const float gs = p.slices == 1 ? *p.l.gs : 1.0f;
+        for (int t = 0; t < my_tiles; ++t) {
+            const int a = t & 1;
+            const bool ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.acc_full[a]), (t / 2) & 1, failed));
+            tc_fence_after();
+            const int64_t n = (int64_t)(group + t * p.groups) * kTile + threadIdx.x;
+            const uint32_t acc = tmem + a * kAccCols + ((uint32_t)(warp * 32) << 16);
+            for (int r = 0; r < rows; r += 2) {
+                uint32_t d[16];
+                __syncwarp();
+                asm volatile(
+                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                    : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]), "=r"(d[4]), "=r"(d[5]), "=r"(d[6]), "=r"(d[7]), "=r"(d[8]),
+                      "=r"(d[9]), "=r"(d[10]), "=r"(d[11]), "=r"(d[12]), "=r"(d[13]), "=r"(d[14]), "=r"(d[15])
+                    : "r"(acc + r * 8));
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (r + h >= rows || n >= p.l.N) continue;
+                    float s = __uint_as_float(d[8 * h + 7]);
+#pragma unroll
+                    for (int i = 6; i >= 0; --i) s = __fmaf_rn(s, 8.0f, __uint_as_float(d[8 * h + i]));
+                    const int top = max(above(sh.row_max[r + h]), -85);
+                    s *= __uint_as_float((uint32_t)(127 + top - 29) << 23);
+                    const int row = row0 + r + h;
+                    if (sh.odd[r + h]) s += odd_products(p, row, n, blk0, blk1);
+                    if (!ok) s = __uint_as_float(0x7fffffffu);
+                    if (p.slices > 1) p.l.ws[((int64_t)slice * p.l.rows + row) * p.l.N + n] = s;
+                    else store_output(p, row, n, s, gs);
+                }
+            }
+            __syncwarp();
+            tc_fence_before();
+            if (lane == 0) bar_arrive(smem_addr(&sh.acc_empty[a]));
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+}
+
+// out = the slices' sums, in order, over gs, and the bias
+__global__ void __launch_bounds__(256) linear_join_kernel(const TcParams p) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (n >= p.l.N) return;
+    const int row = blockIdx.y;
+    float s = 0.0f;
+    for (int i = 0; i < p.slices; ++i) s += p.l.ws[((int64_t)i * p.l.rows + row) * p.l.N + n];
+    store_output(p, row, n, s, *p.l.gs);
+}
+
+// ---------------------------------------------------------------- launch
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiled encode_tiled() {
+    static EncodeTiled fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiled>(f);
+        cudaGetLastError();
+    });
+    return fn;
+}
+
+// The tensor map wants the weight's rows at multiples of 16 bytes, the copies of scales too.
+bool linear_tc_takes(const LinearParams& p) {
+    return tc_plan(p.N, p.K).slices > 0 && reinterpret_cast<uintptr_t>(p.w4) % 16 == 0 && (p.N == 1 || p.w_stride % 16 == 0) &&
+           reinterpret_cast<uintptr_t>(p.sf) % 16 == 0;
+}
+
+template <class... KArgs, class... Args>
+static cudaError_t launch2(void (*k)(KArgs...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k, args...);
+    const cudaError_t last = cudaGetLastError();
+    return e != cudaSuccess ? e : last;
+}
+
+cudaError_t launch_linear_tc(const LinearParams& l, bool x_f32, bool out_f32, cudaStream_t s) {
+    static std::atomic<bool> allowed[64] = {};
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    constexpr int kFixed = (int)sizeof(TcShared) + 256;  // the static part, rounded up
+    constexpr int kMost = kMaxSmem - kFixed;
+    if (!allowed[dev].load(std::memory_order_acquire)) {
+        if (cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost)) return e;
+        allowed[dev].store(true, std::memory_order_release);
+    }
+    const TcPlan plan = tc_plan(l.N, l.K);
+    TcParams p = {};
+    p.l = l;
+    p.slices = plan.slices;
+    p.pieces_per_slice = plan.pieces_per_slice;
+    p.groups = plan.groups;
+    p.tiles = plan.tiles;
+    p.x_f32 = x_f32;
+    p.out_f32 = out_f32;
+    p.x_vec = reinterpret_cast<uintptr_t>(l.x) % 16 == 0 && (l.rows == 1 || l.x_stride * (x_f32 ? 4 : 2) % 16 == 0);
+    const int rows = l.rows < kPassRows ? l.rows : kPassRows, cols = (rows * 8 + 15) / 16 * 16;
+    const int dig = plan.pieces_per_slice * (cols * 128 + 4 * 512);
+    p.stages = (kMost - 1024 - dig) / (kStageBytes + kStageScales);
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
+    const int work = (plan.tiles + plan.groups - 1) / plan.groups * plan.pieces_per_slice;
+    if (p.stages > work) p.stages = work;
+    const size_t smem = 1024 + dig + (size_t)p.stages * (kStageBytes + kStageScales);
+
+    EncodeTiled encode = encode_tiled();
+    if (!encode) return cudaErrorNotSupported;
+    CUtensorMap map;
+    const cuuint64_t dims[2] = {(cuuint64_t)l.K / 2, (cuuint64_t)l.N};
+    const cuuint64_t strides[1] = {(cuuint64_t)(l.N > 1 ? l.w_stride : (l.K / 2 + 15) / 16 * 16)};
+    const cuuint32_t box[2] = {128, kTile}, one[2] = {1, 1};
+    if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(l.w4), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    const unsigned passes = (unsigned)((l.rows + kPassRows - 1) / kPassRows);
+    const cudaError_t e = launch2(linear_tc_kernel, dim3((unsigned)(p.slices * p.groups), passes), kTcThreads, smem, s, map, p);
+    if (e != cudaSuccess || p.slices == 1) return e;
+    return launch2(linear_join_kernel, dim3((unsigned)((l.N + 255) / 256), (unsigned)l.rows), 256, 0, s, p);
+}
+
+}  // namespace mbx
