@@ -16,9 +16,9 @@
 //
 // A block of threads keeps the digits of one slice of K (up to 4 pieces of 256) and
 // walks the tiles of 128 outputs of its group; the slices' sums are added in order
-// by a second kernel.  Warps 0 to 3 read the accumulators and write, warp 4 copies,
-// warp 5 multiplies; all but the copying warp make the digits first, while the
-// first weights are on their way.  Bound by the weight's bytes.
+// by a second kernel.  One warp copies and one multiplies; the sixteen others make the
+// digits, while the first weights are on their way, and then read the accumulators
+// and write, each four of them a quarter of the rows.  Bound by the weight's bytes.
 #include <cuda.h>
 
 #include <atomic>
@@ -30,7 +30,8 @@
 namespace mbx {
 
 constexpr int kTile = 128, kPiece = 256, kMaxPieces = 4, kPassRows = 16, kMaxStages = 12;
-constexpr int kTcThreads = 256, kDigitThreads = 224;
+constexpr int kWorkers = 512, kTcThreads = kWorkers + 64;  // then the copying warp and the multiplying one
+constexpr int kCopyWarp = kWorkers / 32, kMmaWarp = kCopyWarp + 1;
 constexpr int kStageBytes = 16384, kStageScales = 2048;
 constexpr int kMaxSmem = 227 * 1024;
 // tensor memory: two accumulators, the stages' scales (16 columns each), the digits' scales
@@ -116,8 +117,14 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
 __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
     return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(128 >> 4) << 32 | 1ull << 46;
 }
-__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t smem) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(scale_desc(smem)) : "memory");
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// One lane of a whole warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one;
 }
 __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, bool add) {
     asm volatile(
@@ -285,7 +292,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(smem_addr(&sh.acc_full[i]), 1);
-            bar_init(smem_addr(&sh.acc_empty[i]), 4);
+            bar_init(smem_addr(&sh.acc_empty[i]), kWorkers / 32);
         }
         bar_init(smem_addr(&sh.drained), 1);
         sh.failed = 0;
@@ -293,7 +300,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
     }
-    if (warp == 5) {
+    if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -305,7 +312,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
     grid_dep_wait();
     grid_dep_launch();
 
-    if (warp == 4) {
+    if (warp == kCopyWarp) {
         if (lane == 0) {
             int u = 0;
             for (int t = 0; t < my_tiles; ++t) {
@@ -334,11 +341,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
                     for (int k = 0; k < 100000 && !bar_try(smem_addr(&sh.full[i % p.stages]), (i / p.stages) & 1); ++k) {
                     }
         }
-    } else {
+    } else if (warp < kCopyWarp) {
         // the digits: a thread takes a row's block at a time
-        const int id = threadIdx.x - (warp > 4 ? 32 : 0), per_row = steps * 4, items = rows * per_row;
+        const int id = threadIdx.x, per_row = steps * 4, items = rows * per_row;
         float v[16];
-        for (int it = id; it < items; it += kDigitThreads) {
+        for (int it = id; it < items; it += kWorkers) {
             const int r = it / per_row, blk = blk0 + it - r * per_row;
             if (blk >= blk1) continue;
             load_block(v, p, row0 + r, blk);
@@ -346,11 +353,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
             atomicMax(&sh.row_max[r], block_max(v, &odd));
             if (odd) sh.odd[r] = 1;
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(kDigitThreads) : "memory");
-        for (int it = id; it < items; it += kDigitThreads) {
+        asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory");
+        for (int it = id; it < items; it += kWorkers) {
             const int r = it / per_row, b = it - r * per_row, blk = blk0 + b;
             const bool real = blk < blk1;
-            if (items > kDigitThreads && real) load_block(v, p, row0 + r, blk);
+            if (items > kWorkers && real) load_block(v, p, row0 + r, blk);
             if (!real) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[i] = 0.0f;
@@ -380,59 +387,71 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
             }
         }
         fence_async();
-        asm volatile("bar.sync 1, %0;" ::"n"(kDigitThreads) : "memory");
+        asm volatile("bar.arrive 2, %0;" ::"n"(kWorkers + 32) : "memory");
     }
 
-    if (warp == 5) {
+    if (warp == kMmaWarp) {
+        asm volatile("bar.sync 2, %0;" ::"n"(kWorkers + 32) : "memory");
         const uint32_t idesc = 1u << 7 | 1u << 10 | (uint32_t)(cols / 8) << 17 | (uint32_t)(kTile / 16) << 24;
-        if (lane == 0)
-            for (int k = 0; k < steps; ++k) scales_to_tmem(tmem + kDigitScaleCol + 4 * k, smem_addr(dig_scales + k * 512));
-        int u = 0;
+        const bool leader = elect_one();
+        if (leader)
+            for (int k = 0; k < steps; ++k) scales_to_tmem(tmem + kDigitScaleCol + 4 * k, scale_desc(smem_addr(dig_scales)) + 32 * k);
+        const bool ragged = blocks % 4 != 0 && blk1 == blocks;  // the last step's blocks past K: their scales are anything
+        int s = 0, phase = 0;
         bool ok = true;
         for (int t = 0; t < my_tiles && ok; ++t) {
             const int a = t & 1;
             if (t >= 2) ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.acc_empty[a]), (t / 2 - 1) & 1, failed));
             tc_fence_after();
-            for (int piece = piece0; piece < piece1 && ok; ++piece, ++u) {
-                const int s = u % p.stages, n = min(4, p.l.sf_col_tiles - piece * 4);
-                ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.full[s]), (u / p.stages) & 1, failed));
+            for (int piece = piece0; piece < piece1 && ok; ++piece) {
+                const int n = min(4, p.l.sf_col_tiles - piece * 4);
+                ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.full[s]), phase, failed));
                 if (!ok) break;
-                uint8_t* sc = scales + s * kStageScales;
-                if (blocks % 4 && piece * 16 + n * 4 > blocks) {  // the last step's blocks past K: their scales are anything
+                const uint32_t sc = smem_addr(scales + s * kStageScales);
+                if (ragged && piece == piece1 - 1) {
                     const uint32_t keep = (1u << blocks % 4 * 8) - 1;
-                    for (int i = lane; i < 128; i += 32) reinterpret_cast<uint32_t*>(sc + (n - 1) * 512)[i] &= keep;
+                    uint32_t* w = reinterpret_cast<uint32_t*>(scales + s * kStageScales + (n - 1) * 512);
+                    for (int i = lane; i < 128; i += 32) w[i] &= keep;
                     fence_async();
                     __syncwarp();
                 }
-                if (lane == 0) {
-                    const uint32_t sa = tmem + kScaleCol + 16 * s;
-                    for (int k = 0; k < n; ++k) scales_to_tmem(sa + 4 * k, smem_addr(sc + k * 512));
-                    const uint32_t wa = smem_addr(ring + s * kStageBytes), da = smem_addr(dig + (piece - piece0) * cols * 128);
-                    for (int k = 0; k < n; ++k)
-                        mma_fp4(tmem + a * kAccCols, operand_desc(wa + 32 * k), operand_desc(da + 32 * k), idesc, sa + 4 * k,
-                                tmem + kDigitScaleCol + 4 * ((piece - piece0) * 4 + k), piece > piece0 || k > 0);
+                if (leader) {
+                    const uint32_t sa = tmem + kScaleCol + 16 * s, sb = tmem + kDigitScaleCol + 16 * (piece - piece0);
+                    const uint64_t wa = operand_desc(smem_addr(ring + s * kStageBytes));
+                    const uint64_t da = operand_desc(smem_addr(dig + (piece - piece0) * cols * 128));
+                    const uint32_t acc = tmem + a * kAccCols;
+                    const uint64_t sd = scale_desc(sc);
+                    if (n == 4) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) scales_to_tmem(sa + 4 * k, sd + 32 * k);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mma_fp4(acc, wa + 2 * k, da + 2 * k, idesc, sa + 4 * k, sb + 4 * k, piece > piece0 || k > 0);
+                    } else {
+                        for (int k = 0; k < n; ++k) scales_to_tmem(sa + 4 * k, sd + 32 * k);
+                        for (int k = 0; k < n; ++k) mma_fp4(acc, wa + 2 * k, da + 2 * k, idesc, sa + 4 * k, sb + 4 * k, piece > piece0 || k > 0);
+                    }
                     mma_commit(smem_addr(&sh.empty[s]));
+                    if (piece == piece1 - 1) mma_commit(smem_addr(&sh.acc_full[a]));
                 }
                 __syncwarp();
+                if (++s == p.stages) s = 0, phase ^= 1;
             }
-            if (lane == 0 && ok) mma_commit(smem_addr(&sh.acc_full[a]));
-            __syncwarp();
         }
         // nothing of the block may be under way when it gives the tensor memory back
-        if (lane == 0) {
+        if (leader) {
             mma_commit(smem_addr(&sh.drained));
             bar_wait(smem_addr(&sh.drained), 0, failed);
         }
         __syncwarp();
-    } else if (warp < 4) {
+    } else if (warp < kCopyWarp) {
         const float gs = p.slices == 1 ? *p.l.gs : 1.0f;
         for (int t = 0; t < my_tiles; ++t) {
             const int a = t & 1;
             const bool ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.acc_full[a]), (t / 2) & 1, failed));
             tc_fence_after();
-            const int64_t n = (int64_t)(group + t * p.groups) * kTile + threadIdx.x;
-            const uint32_t acc = tmem + a * kAccCols + ((uint32_t)(warp * 32) << 16);
-            for (int r = 0; r < rows; r += 2) {
+            const int64_t n = (int64_t)(group + t * p.groups) * kTile + threadIdx.x % 128;
+            const uint32_t acc = tmem + a * kAccCols + ((uint32_t)(warp % 4 * 32) << 16);
+            for (int r = warp / 4 * 2; r < rows; r += 8) {
                 uint32_t d[16];
                 __syncwarp();
                 asm volatile(
@@ -464,7 +483,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
