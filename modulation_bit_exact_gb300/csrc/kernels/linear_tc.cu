@@ -14,7 +14,7 @@
 // An infinity or NaN has no digits: it counts as 0 there, and the epilogue adds its
 // products, from the weight in memory, to the outputs of its row.
 //
-// A block of threads keeps the digits of one slice of K (up to 4 pieces of 256) and
+// A block of threads keeps the digits of one slice of K (up to 8 pieces of 256) and
 // walks the tiles of 128 outputs of its group; the slices' sums are added in order
 // by a second kernel.  One warp copies and one multiplies; the sixteen others make the
 // digits, while the first weights are on their way, and then read the accumulators
@@ -29,13 +29,13 @@
 
 namespace mbx {
 
-constexpr int kTile = 128, kPiece = 256, kMaxPieces = 4, kPassRows = 16, kMaxStages = 12;
+constexpr int kTile = 128, kPiece = 256, kMaxPieces = 8, kPassRows = 16, kMaxStages = 8;
 constexpr int kWorkers = 512, kTcThreads = kWorkers + 64;  // then the copying warp and the multiplying one
 constexpr int kCopyWarp = kWorkers / 32, kMmaWarp = kCopyWarp + 1;
 constexpr int kStageBytes = 16384, kStageScales = 2048;
 constexpr int kMaxSmem = 227 * 1024;
 // tensor memory: two accumulators, the stages' scales (16 columns each), the digits' scales
-constexpr uint32_t kAccCols = 128, kScaleCol = 256, kDigitScaleCol = 448;
+constexpr uint32_t kAccCols = 128, kScaleCol = 256, kDigitScaleCol = 384;
 
 struct TcParams {
     LinearParams l;
@@ -43,9 +43,9 @@ struct TcParams {
     bool x_f32, out_f32, x_vec;
 };
 
-// How K is cut into slices and the tiles shared out: the fewest pieces in a row for
-// a block, a second kernel counting as four of them (it takes about as long).  The
-// rows do not matter, so that a row's sums have one order.
+// How K is cut into slices and the tiles shared out: by the pieces that a block
+// works through one after another, a tile's end counting as a third of a piece, a
+// piece's digits as two thirds and a second kernel as six.  The rows do not matter, so that a row's sums have one order.
 struct TcPlan {
     int slices, pieces_per_slice, groups, tiles;
 };
@@ -59,7 +59,7 @@ static TcPlan tc_plan(int64_t N, int K) {
         int64_t groups = sms / slices;
         if (groups < 1) continue;
         if (groups > tiles) groups = tiles;
-        const int64_t c = (tiles + groups - 1) / groups * len + (slices > 1 ? 4 : 0);
+        const int64_t c = (tiles + groups - 1) / groups * (3 * len + 1) + 2 * len + (slices > 1 ? 18 : 0);
         if (c < cost) {
             cost = c;
             best = TcPlan{slices, len, (int)groups, (int)tiles};
@@ -285,72 +285,92 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
     uint8_t* scales = dig + p.pieces_per_slice * cols * 128;  // the stages'
     uint8_t* dig_scales = scales + p.stages * kStageScales;   // [steps][512]
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < p.stages; ++i) {
-            bar_init(smem_addr(&sh.full[i]), 1);
-            bar_init(smem_addr(&sh.empty[i]), 1);
+    volatile int* failed = &sh.failed;
+    const int total = my_tiles * (piece1 - piece0);  // pieces of weight that this block takes
+    auto fetch = [&](int u) {                         // the u-th, into stage u % stages
+        const int t = u / (piece1 - piece0), piece = piece0 + u - t * (piece1 - piece0), tile = group + t * p.groups;
+        const int s = u % p.stages;
+        const uint32_t bar = smem_addr(&sh.full[s]), bytes = (uint32_t)min(4, p.l.sf_col_tiles - piece * 4) * 512;
+        bar_expect(bar, kStageBytes + bytes);
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                         smem_addr(ring + s * kStageBytes)),
+                     "l"(&map), "r"(piece * 128), "r"(tile * kTile), "r"(bar)
+                     : "memory");
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         smem_addr(scales + s * kStageScales)),
+                     "l"(p.l.sf + ((int64_t)tile * p.l.sf_col_tiles + piece * 4) * 512), "r"(bytes), "r"(bar)
+                     : "memory");
+    };
+    // the worker's first block of activations: row r, block blk of K
+    const int per_row = steps * 4, items = rows * per_row;
+    float v[16];
+
+    if (warp == kCopyWarp) {
+        if (lane == 0) {
+            for (int i = 0; i < p.stages; ++i) {
+                bar_init(smem_addr(&sh.full[i]), 1);
+                bar_init(smem_addr(&sh.empty[i]), 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                bar_init(smem_addr(&sh.acc_full[i]), 1);
+                bar_init(smem_addr(&sh.acc_empty[i]), kWorkers / 32);
+            }
+            bar_init(smem_addr(&sh.drained), 1);
+            sh.failed = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            grid_dep_wait();
+            for (int u = 0; u < p.stages && u < total; ++u) fetch(u);
         }
-        for (int i = 0; i < 2; ++i) {
-            bar_init(smem_addr(&sh.acc_full[i]), 1);
-            bar_init(smem_addr(&sh.acc_empty[i]), kWorkers / 32);
-        }
-        bar_init(smem_addr(&sh.drained), 1);
-        sh.failed = 0;
-        for (int i = 0; i < kPassRows; ++i) sh.row_max[i] = sh.odd[i] = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
-    }
-    if (warp == kMmaWarp) {
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else {
+        if (threadIdx.x < kPassRows) sh.row_max[threadIdx.x] = sh.odd[threadIdx.x] = 0;
+        grid_dep_wait();
+        if ((int)threadIdx.x < items) {
+            const int r = threadIdx.x / per_row, blk = blk0 + threadIdx.x - r * per_row;
+            if (blk < blk1) load_block(v, p, row0 + r, blk);
+        }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    volatile int* failed = &sh.failed;
-    grid_dep_wait();
     grid_dep_launch();
 
     if (warp == kCopyWarp) {
         if (lane == 0) {
-            int u = 0;
-            for (int t = 0; t < my_tiles; ++t) {
-                const int tile = group + t * p.groups;
-                for (int piece = piece0; piece < piece1; ++piece, ++u) {
-                    const int s = u % p.stages;
-                    if (u >= p.stages && !bar_wait(smem_addr(&sh.empty[s]), (u / p.stages - 1) & 1, failed)) break;
-                    const uint32_t bar = smem_addr(&sh.full[s]);
-                    const uint32_t bytes = (uint32_t)min(4, p.l.sf_col_tiles - piece * 4) * 512;
-                    bar_expect(bar, kStageBytes + bytes);
-                    asm volatile(
-                        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-                            smem_addr(ring + s * kStageBytes)),
-                        "l"(&map), "r"(piece * 128), "r"(tile * kTile), "r"(bar)
-                        : "memory");
-                    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                                     smem_addr(scales + s * kStageScales)),
-                                 "l"(p.l.sf + ((int64_t)tile * p.l.sf_col_tiles + piece * 4) * 512), "r"(bytes), "r"(bar)
-                                 : "memory");
-                }
-                if (*failed) break;
+            int u = p.stages;
+            for (; u < total; ++u) {
+                if (!bar_wait(smem_addr(&sh.empty[u % p.stages]), (u / p.stages - 1) & 1, failed)) break;
+                fetch(u);
             }
             // after a failure: the copies that are under way have to land before the block ends
             if (*failed)
-                for (int i = u > p.stages ? u - p.stages : 0; i < u; ++i)
+                for (int i = u - p.stages; i < u && i < total; ++i)
                     for (int k = 0; k < 100000 && !bar_try(smem_addr(&sh.full[i % p.stages]), (i / p.stages) & 1); ++k) {
                     }
         }
+        __syncwarp();
     } else if (warp < kCopyWarp) {
         // the digits: a thread takes a row's block at a time
-        const int id = threadIdx.x, per_row = steps * 4, items = rows * per_row;
-        float v[16];
+        const int id = threadIdx.x;
+        const bool whole_rows = per_row % 32 == 0;  // a warp's blocks are of one row
         for (int it = id; it < items; it += kWorkers) {
             const int r = it / per_row, blk = blk0 + it - r * per_row;
-            if (blk >= blk1) continue;
-            load_block(v, p, row0 + r, blk);
             int odd = 0;
-            atomicMax(&sh.row_max[r], block_max(v, &odd));
+            uint32_t m = 0;
+            if (blk < blk1) {
+                if (it != id) load_block(v, p, row0 + r, blk);
+                m = block_max(v, &odd);
+            }
+            if (whole_rows) {
+                m = __reduce_max_sync(0xffffffffu, m);
+                if (lane == 0) atomicMax(&sh.row_max[r], m);
+            } else {
+                atomicMax(&sh.row_max[r], m);
+            }
             if (odd) sh.odd[r] = 1;
         }
         asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory");
@@ -496,9 +516,17 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const TcParams p) {
     const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (n >= p.l.N) return;
     const int row = blockIdx.y;
+    const float gs = *p.l.gs;
+    const float* w = p.l.ws + (int64_t)row * p.l.N + n;
     float s = 0.0f;
-    for (int i = 0; i < p.slices; ++i) s += p.l.ws[((int64_t)i * p.l.rows + row) * p.l.N + n];
-    store_output(p, row, n, s, *p.l.gs);
+    for (int i0 = 0; i0 < p.slices; i0 += 8) {  // eight loads under way
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i0 + i < p.slices ? w[(int64_t)(i0 + i) * p.l.rows * p.l.N] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += v[i];
+    }
+    store_output(p, row, n, s, gs);
 }
 
 // ---------------------------------------------------------------- launch
