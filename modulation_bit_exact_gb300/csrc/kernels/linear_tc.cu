@@ -41,6 +41,14 @@ struct TcParams {
     LinearParams l;
     int slices, pieces_per_slice, groups, stages, tiles;
     bool x_f32, out_f32, x_vec;
+    // the digits made beforehand (linear_digits_kernel), or null: images of a slice for
+    // every 16 rows and slice, image_bytes apart, each followed by its SliceRows
+    uint8_t* images;
+    int image_bytes;
+};
+struct SliceRows {
+    uint32_t most[kPassRows];  // bits of the largest magnitude of a row in the slice
+    int odd[kPassRows];        // whether the row has an infinity or NaN there
 };
 
 // How K is cut into slices and the tiles shared out: by the pieces that a block
@@ -68,9 +76,24 @@ static TcPlan tc_plan(int64_t N, int K) {
     return best;
 }
 
+// The workspace: the slices' sums [slices][rows][N], then the digits' images.
+// A block makes its digits itself while each of its workers has one block of 16 at
+// most (8 rows of 4 pieces: 21.0 us for [8, 5120] x [30720, 5120], a kernel before it
+// 22.6); more are made beforehand ([16, 1024] x [2048, 1024]: 6.8 us against 14.0).
+static bool digits_before(const TcPlan& p, int rows) {
+    return (rows < kPassRows ? rows : kPassRows) * p.pieces_per_slice * 16 > kWorkers;
+}
+static int64_t sums_bytes(const TcPlan& p, int rows, int64_t N) {
+    return p.slices > 1 ? ((int64_t)p.slices * rows * N * 4 + 127) / 128 * 128 : 0;
+}
+static int image_bytes(const TcPlan& p, int rows) {
+    const int cols = rows >= kPassRows ? 8 * kPassRows : (rows * 8 + 15) / 16 * 16;
+    return p.pieces_per_slice * (cols * 128 + 2048) + (int)sizeof(SliceRows);
+}
 int64_t linear_nvfp4_workspace_bytes(int rows, int64_t N, int K) {
     const TcPlan p = tc_plan(N, K);
-    return p.slices > 1 ? ((int64_t)p.slices * rows * N * 4 + 15) / 16 * 16 : 0;
+    const int64_t passes = (rows + kPassRows - 1) / kPassRows;
+    return sums_bytes(p, rows, N) + (digits_before(p, rows) ? passes * p.slices * image_bytes(p, rows) : 0);
 }
 
 // ---------------------------------------------------------------- barriers, copies, tensor memory
@@ -224,6 +247,40 @@ __device__ __forceinline__ void transpose_nibbles(uint32_t (&w)[8]) {
     }
 }
 
+// The digits of one block of a row whose largest magnitude in this slice of K has the
+// bits `most`, into the row's eight columns: `col` is digit 0's column in the piece
+// (columns 128 bytes apart, 16-byte units swizzled), `scale` its scale (columns 16
+// bytes apart); b is the block's place in the slice.
+__device__ __forceinline__ void put_digits(const float (&v)[16], uint32_t most, int b, uint8_t* col, uint8_t* scale) {
+    int odd = 0;
+    const int top = max(above(most), -85);
+    const int e = max(min(above(block_max(v, &odd)), top), top - 17);
+    const float to_int = __uint_as_float((uint32_t)(127 + 22 - e) << 23);
+    uint32_t w[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float a = v[8 * h + j];
+            w[h][j] = digits((__float_as_uint(a) & 0x7f800000u) == 0x7f800000u ? 0.0f : a, to_int);
+        }
+        transpose_nibbles(w[h]);
+    }
+    const int up = 8 + e - top;  // -9 .. 8: the scale 2^up as E4M3
+    const uint8_t sc = (uint8_t)(up >= -6 ? (up + 7) << 3 : 1 << (up + 9));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        *reinterpret_cast<uint2*>(col + i * 128 + ((b % 16 / 2) ^ i) * 16 + b % 2 * 8) = make_uint2(w[0][i], w[1][i]);
+        scale[i * 16] = sc;
+    }
+}
+// Where a row's columns of a slice's digits begin, and its scales: [pieces][cols][128
+// bytes], then [steps of 64][512 bytes] in the order of the weight's scale tiles.
+__device__ __forceinline__ uint8_t* digit_at(uint8_t* image, int cols, int r, int b) { return image + (b / 16 * cols + r * 8) * 128; }
+__device__ __forceinline__ uint8_t* digit_scale_at(uint8_t* image, int cols, int pieces, int r, int b) {
+    return image + pieces * cols * 128 + b / 4 * 512 + r % 4 * 128 + r / 4 * 4 + b % 4;
+}
+
 // sum over the slice's k with a non-finite activation of a(x[row][k]) * w[n][k]
 __device__ __noinline__ float odd_products(const TcParams& p, int row, int64_t n, int blk0, int blk1) {
     float sum = 0.0f;
@@ -261,11 +318,10 @@ __device__ __forceinline__ void store_output(const TcParams& p, int row, int64_t
 // ---------------------------------------------------------------- the product
 
 struct TcShared {
-    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained, digits;
     uint32_t tmem;
     int failed;
-    uint32_t row_max[kPassRows];
-    int odd[kPassRows];
+    SliceRows rows;
 };
 
 __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_constant__ CUtensorMap map, const TcParams p) {
@@ -281,9 +337,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
     const int blk0 = piece0 * 16, blk1 = min(piece1 * 16, blocks), steps = (blk1 - blk0 + 3) / 4;
     const int my_tiles = (p.tiles - group + p.groups - 1) / p.groups;
     uint8_t* ring = smem;
-    uint8_t* dig = ring + p.stages * kStageBytes;            // [pieces][cols][128 bytes], swizzled
-    uint8_t* scales = dig + p.pieces_per_slice * cols * 128;  // the stages'
-    uint8_t* dig_scales = scales + p.stages * kStageScales;   // [steps][512]
+    uint8_t* dig = ring + p.stages * kStageBytes;  // the slice's digits and their scales (digit_at)
+    uint8_t* dig_scales = dig + p.pieces_per_slice * cols * 128;
+    uint8_t* scales = dig_scales + p.pieces_per_slice * 2048;  // the stages'
 
     volatile int* failed = &sh.failed;
     const int total = my_tiles * (piece1 - piece0);  // pieces of weight that this block takes
@@ -301,9 +357,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
                      "l"(p.l.sf + ((int64_t)tile * p.l.sf_col_tiles + piece * 4) * 512), "r"(bytes), "r"(bar)
                      : "memory");
     };
-    // the worker's first block of activations: row r, block blk of K
+    // the worker's block of activations, 0 past K
     const int per_row = steps * 4, items = rows * per_row;
     float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    const uint8_t* image = p.images ? p.images + ((int64_t)blockIdx.y * p.slices + slice) * p.image_bytes : nullptr;
 
     if (warp == kCopyWarp) {
         if (lane == 0) {
@@ -316,19 +375,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
                 bar_init(smem_addr(&sh.acc_empty[i]), kWorkers / 32);
             }
             bar_init(smem_addr(&sh.drained), 1);
+            bar_init(smem_addr(&sh.digits), 1);
             sh.failed = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-            grid_dep_wait();
+            // the kernel that made the digits began when all before it had finished
+            if (!p.images) grid_dep_wait();
             for (int u = 0; u < p.stages && u < total; ++u) fetch(u);
+            if (p.images) {
+                grid_dep_wait();
+                const uint32_t bytes = p.pieces_per_slice * (cols * 128 + 2048);
+                bar_expect(smem_addr(&sh.digits), bytes);
+                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                 smem_addr(dig)),
+                             "l"(image), "r"(bytes), "r"(smem_addr(&sh.digits))
+                             : "memory");
+            }
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     } else {
-        if (threadIdx.x < kPassRows) sh.row_max[threadIdx.x] = sh.odd[threadIdx.x] = 0;
+        if (threadIdx.x < kPassRows && !p.images) sh.rows.most[threadIdx.x] = sh.rows.odd[threadIdx.x] = 0;
         grid_dep_wait();
-        if ((int)threadIdx.x < items) {
+        if (p.images) {
+            if (threadIdx.x < sizeof(SliceRows) / 4)
+                reinterpret_cast<uint32_t*>(&sh.rows)[threadIdx.x] = reinterpret_cast<const volatile uint32_t*>(image + p.image_bytes - sizeof(SliceRows))[threadIdx.x];
+        } else if ((int)threadIdx.x < items) {
             const int r = threadIdx.x / per_row, blk = blk0 + threadIdx.x - r * per_row;
             if (blk < blk1) load_block(v, p, row0 + r, blk);
         }
@@ -347,78 +420,43 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
                 fetch(u);
             }
             // after a failure: the copies that are under way have to land before the block ends
+            if (*failed && p.images) bar_wait(smem_addr(&sh.digits), 0, failed);
             if (*failed)
                 for (int i = u - p.stages; i < u && i < total; ++i)
                     for (int k = 0; k < 100000 && !bar_try(smem_addr(&sh.full[i % p.stages]), (i / p.stages) & 1); ++k) {
                     }
         }
         __syncwarp();
-    } else if (warp < kCopyWarp) {
-        // the digits: a thread takes a row's block at a time
-        const int id = threadIdx.x;
-        const bool whole_rows = per_row % 32 == 0;  // a warp's blocks are of one row
-        for (int it = id; it < items; it += kWorkers) {
-            const int r = it / per_row, blk = blk0 + it - r * per_row;
-            int odd = 0;
-            uint32_t m = 0;
-            if (blk < blk1) {
-                if (it != id) load_block(v, p, row0 + r, blk);
-                m = block_max(v, &odd);
-            }
-            if (whole_rows) {
-                m = __reduce_max_sync(0xffffffffu, m);
-                if (lane == 0) atomicMax(&sh.row_max[r], m);
-            } else {
-                atomicMax(&sh.row_max[r], m);
-            }
-            if (odd) sh.odd[r] = 1;
+    } else if (warp < kCopyWarp && !p.images) {
+        // the digits: a row's block for each thread
+        const int r = threadIdx.x / per_row, b = threadIdx.x - r * per_row;
+        const bool mine = (int)threadIdx.x < items;
+        int odd = 0;
+        uint32_t m = mine ? block_max(v, &odd) : 0;
+        if (per_row % 32 == 0) {  // a warp's blocks are of one row
+            m = __reduce_max_sync(0xffffffffu, m);
+            if (lane == 0 && mine) atomicMax(&sh.rows.most[r], m);
+        } else if (mine) {
+            atomicMax(&sh.rows.most[r], m);
         }
+        if (odd) sh.rows.odd[r] = 1;
         asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory");
-        for (int it = id; it < items; it += kWorkers) {
-            const int r = it / per_row, b = it - r * per_row, blk = blk0 + b;
-            const bool real = blk < blk1;
-            if (items > kWorkers && real) load_block(v, p, row0 + r, blk);
-            if (!real) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-            }
-            int odd = 0;
-            const int top = max(above(sh.row_max[r]), -85);
-            const int e = max(min(above(block_max(v, &odd)), top), top - 17);
-            const float to_int = __uint_as_float((uint32_t)(127 + 22 - e) << 23);
-            uint32_t w[2][8];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float a = v[8 * h + j];
-                    w[h][j] = digits((__float_as_uint(a) & 0x7f800000u) == 0x7f800000u ? 0.0f : a, to_int);
-                }
-                transpose_nibbles(w[h]);
-            }
-            const int up = 8 + e - top;  // -9 .. 8: the scale 2^up as E4M3
-            const uint8_t sc = (uint8_t)(up >= -6 ? (up + 7) << 3 : 1 << (up + 9));
-            uint8_t* col = dig + b / 16 * cols * 128 + r * 8 * 128 + (b % 2) * 8;
-            uint8_t* ss = dig_scales + b / 4 * 512 + (r % 4) * 128 + (r / 4) * 4 + b % 4;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                *reinterpret_cast<uint2*>(col + i * 128 + ((b % 16 / 2) ^ i) * 16) = make_uint2(w[0][i], w[1][i]);
-                ss[i * 16] = sc;
-            }
-        }
+        if (mine)
+            put_digits(v, sh.rows.most[r], b, digit_at(dig, cols, r, b), digit_scale_at(dig, cols, p.pieces_per_slice, r, b));
         fence_async();
         asm volatile("bar.arrive 2, %0;" ::"n"(kWorkers + 32) : "memory");
     }
 
     if (warp == kMmaWarp) {
-        asm volatile("bar.sync 2, %0;" ::"n"(kWorkers + 32) : "memory");
+        bool ok = true;
+        if (p.images) ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.digits), 0, failed));
+        else asm volatile("bar.sync 2, %0;" ::"n"(kWorkers + 32) : "memory");
         const uint32_t idesc = 1u << 7 | 1u << 10 | (uint32_t)(cols / 8) << 17 | (uint32_t)(kTile / 16) << 24;
         const bool leader = elect_one();
         if (leader)
             for (int k = 0; k < steps; ++k) scales_to_tmem(tmem + kDigitScaleCol + 4 * k, scale_desc(smem_addr(dig_scales)) + 32 * k);
         const bool ragged = blocks % 4 != 0 && blk1 == blocks;  // the last step's blocks past K: their scales are anything
         int s = 0, phase = 0;
-        bool ok = true;
         for (int t = 0; t < my_tiles && ok; ++t) {
             const int a = t & 1;
             if (t >= 2) ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.acc_empty[a]), (t / 2 - 1) & 1, failed));
@@ -486,10 +524,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
                     float s = __uint_as_float(d[8 * h + 7]);
 #pragma unroll
                     for (int i = 6; i >= 0; --i) s = __fmaf_rn(s, 8.0f, __uint_as_float(d[8 * h + i]));
-                    const int top = max(above(sh.row_max[r + h]), -85);
+                    const int top = max(above(sh.rows.most[r + h]), -85);
                     s *= __uint_as_float((uint32_t)(127 + top - 29) << 23);
                     const int row = row0 + r + h;
-                    if (sh.odd[r + h]) s += odd_products(p, row, n, blk0, blk1);
+                    if (sh.rows.odd[r + h]) s += odd_products(p, row, n, blk0, blk1);
                     if (!ok) s = __uint_as_float(0x7fffffffu);
                     if (p.slices > 1) p.l.ws[((int64_t)slice * p.l.rows + row) * p.l.N + n] = s;
                     else store_output(p, row, n, s, gs);
@@ -506,6 +544,46 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
     if (warp == kMmaWarp) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+}
+
+// The digits of one row's part of a slice, for all blocks of the product that use it.
+// Sixteen rows' digits take a block of the product 6 us, which its first copies do
+// not cover; made once here they take 2.
+__global__ void __launch_bounds__(16 * kMaxPieces) linear_digits_kernel(const TcParams p) {
+    __shared__ uint32_t most_of[kMaxPieces / 2];
+    __shared__ int odd_of[kMaxPieces / 2];
+    const int slice = blockIdx.x, row = blockIdx.y, pass = row / kPassRows, r = row % kPassRows;
+    const int cols = (min(p.l.rows - pass * kPassRows, kPassRows) * 8 + 15) / 16 * 16;
+    const int blocks = p.l.K / 16, blk0 = slice * p.pieces_per_slice * 16, blk1 = min(blk0 + p.pieces_per_slice * 16, blocks);
+    const int b = threadIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    grid_dep_wait();
+    grid_dep_launch();
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    if (blk0 + b < blk1) load_block(v, p, row, blk0 + b);
+    int odd = 0;
+    const uint32_t m = __reduce_max_sync(0xffffffffu, block_max(v, &odd));
+    odd = __any_sync(0xffffffffu, odd);
+    if (lane == 0) {
+        most_of[warp] = m;
+        odd_of[warp] = odd;
+    }
+    __syncthreads();
+    uint32_t most = 0;
+    odd = 0;
+    for (int i = 0; i < (int)blockDim.x / 32; ++i) {
+        most = max(most, most_of[i]);
+        odd |= odd_of[i];
+    }
+    uint8_t* image = p.images + ((int64_t)pass * p.slices + slice) * p.image_bytes;
+    if (b < (blk1 - blk0 + 3) / 4 * 4)
+        put_digits(v, most, b, digit_at(image, cols, r, b), digit_scale_at(image, cols, p.pieces_per_slice, r, b));
+    if (b == 0) {
+        SliceRows* s = reinterpret_cast<SliceRows*>(image + p.image_bytes - sizeof(SliceRows));
+        s->most[r] = most;
+        s->odd[r] = odd;
     }
 }
 
@@ -612,6 +690,12 @@ cudaError_t launch_linear_tc(const LinearParams& l, bool x_f32, bool out_f32, cu
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     const unsigned passes = (unsigned)((l.rows + kPassRows - 1) / kPassRows);
+    if (digits_before(plan, l.rows)) {
+        p.images = reinterpret_cast<uint8_t*>(l.ws) + sums_bytes(plan, l.rows, l.N);
+        p.image_bytes = image_bytes(plan, l.rows);
+        const unsigned threads = (unsigned)(plan.pieces_per_slice * 16 + 31) / 32 * 32;
+        if (cudaError_t e = launch2(linear_digits_kernel, dim3((unsigned)plan.slices, (unsigned)l.rows), threads, 0, s, p)) return e;
+    }
     const cudaError_t e = launch2(linear_tc_kernel, dim3((unsigned)(p.slices * p.groups), passes), kTcThreads, smem, s, map, p);
     if (e != cudaSuccess || p.slices == 1) return e;
     return launch2(linear_join_kernel, dim3((unsigned)((l.N + 255) / 256), (unsigned)l.rows), 256, 0, s, p);

@@ -12,6 +12,8 @@
 // or one for each element, so its bits are the same at any address.
 #pragma once
 
+#include <type_traits>
+
 #include "rope.cuh"
 
 namespace mbx {
@@ -81,17 +83,19 @@ struct Access1 {
     }
 };
 
-// A lane's units of a head.  Values in the order of the accesses: of the A*W
-// values of a unit, pair i is (2i, 2i+1) in one access and (i, W+i) in two.
+// A lane's units of a head.  The P pairs of a unit are held as packed binary32: a
+// Values' first[u][i] has the first elements of pairs 2i and 2i+1, second the
+// second ones (the pairs of elements that pass are those of their accesses).  Words
+// of elements that the lane does not have stay 0.
 template <class T, bool INTERLEAVED, int W, int U, bool VEC>
 struct HeadUnits {
     static constexpr bool kTwo = !INTERLEAVED || W == 1;  // two accesses a unit
-    static constexpr int A = kTwo ? 2 : 1, E = A * W, P = E / 2;
-    static constexpr int lo(int i) { return kTwo ? i : 2 * i; }
-    static constexpr int hi(int i) { return kTwo ? W + i : 2 * i + 1; }
+    static constexpr int A = kTwo ? 2 : 1, E = A * W, P = E / 2, NP = (P + 1) / 2;
     int off0[U], off1[U];    // offsets within a head, < 0: none
     int pair0[U], turns[U];  // pairs pair0 .. pair0 + turns - 1 of the unit turn
+    bool all_turn;           // of every lane that has elements: no element passes
     __device__ __forceinline__ HeadUnits(int lane, int G, int hd, int n) {
+        all_turn = 2 * n == hd;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int a = lane + G * u;
@@ -113,8 +117,19 @@ struct HeadUnits {
     }
     struct Raw {
         Access1<T, W, VEC> a[U][A];
+        __device__ __forceinline__ void clear() {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < A; ++k)
+#pragma unroll
+                    for (int i = 0; i < Access1<T, W, VEC>::NW; ++i) a[u][k].w[i] = 0;
+        }
     };
-    __device__ __forceinline__ void load(Raw& r, const T* head) const {
+    struct Values {
+        u64 first[U][NP], second[U][NP];
+    };
+    __device__ __forceinline__ void load(Raw& r, const T* head) const {  // into a Raw that was cleared once
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (off0[u] >= 0) r.a[u][0].load(head + off0[u]);
@@ -122,25 +137,40 @@ struct HeadUnits {
                 if (off1[u] >= 0) r.a[u][1].load(head + off1[u]);
         }
     }
-    // Values of the head's elements; 0 where the lane has none.
-    __device__ __forceinline__ void values(float (&f)[U][E], const Raw& r) const {
+    static __device__ __forceinline__ Values pack(const float (&f)[U][E]) {
+        Values v;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            r.a[u][0].widen(f[u]);
-            if (off0[u] < 0) {
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < W; ++i) f[u][i] = 0.0f;
+            for (int i = 0; i < NP; ++i) {
+                const int j = 2 * i, k = 2 * i + 1 < P ? 2 * i + 1 : -1;
+                const int s0 = kTwo ? 1 : 2, d = kTwo ? W : 1;  // pair j: elements s0*j and s0*j + d
+                v.first[u][i] = f2(f[u][s0 * j], k < 0 ? 0.0f : f[u][s0 * k]);
+                v.second[u][i] = f2(f[u][s0 * j + d], k < 0 ? 0.0f : f[u][s0 * k + d]);
             }
-            if constexpr (kTwo) {
-                r.a[u][1].widen(f[u] + W);
-                if (off1[u] < 0) {
-#pragma unroll
-                    for (int i = 0; i < W; ++i) f[u][W + i] = 0.0f;
-                }
-            }
-        }
+        return v;
     }
-    __device__ __forceinline__ void store(T* head, const float (&f)[U][E]) const {
+    static __device__ __forceinline__ void unpack(float (&f)[U][E], const Values& v) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const int s0 = kTwo ? 1 : 2, d = kTwo ? W : 1;
+                f[u][s0 * j] = j & 1 ? f2hi(v.first[u][j / 2]) : f2lo(v.first[u][j / 2]);
+                f[u][s0 * j + d] = j & 1 ? f2hi(v.second[u][j / 2]) : f2lo(v.second[u][j / 2]);
+            }
+    }
+    static __device__ __forceinline__ Values values(const Raw& r) {
+        float f[U][E];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < A; ++k) r.a[u][k].widen(f[u] + k * W);
+        return pack(f);
+    }
+    __device__ __forceinline__ void store(T* head, const Values& v) const {
+        float f[U][E];
+        unpack(f, v);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             Access1<T, W, VEC> a;
@@ -155,8 +185,9 @@ struct HeadUnits {
                 }
         }
     }
-    // f = w's elements, 1 where w is null
-    __device__ __forceinline__ void weight(float (&f)[U][E], const void* w, bool w_f32) const {
+    // w's elements, 1 where w is null
+    __device__ __forceinline__ Values weight(const void* w, bool w_f32) const {
+        float f[U][E];
         auto one = [&](int e) {
             return !w ? 1.0f : w_f32 ? load_elem(static_cast<const float*>(w) + e) : load_elem(static_cast<const uint16_t*>(w) + e);
         };
@@ -167,37 +198,90 @@ struct HeadUnits {
                 f[u][i] = off0[u] >= 0 ? one(off0[u] + i) : 0.0f;
                 if constexpr (kTwo) f[u][W + i] = off1[u] >= 0 ? one(off1[u] + i) : 0.0f;
             }
+        return pack(f);
     }
+    struct Angles {
+        u64 c[U][NP], s[U][NP];
+    };
     // This lane's cosines and sines out of those of the token's n pairs.
-    __device__ __forceinline__ void angles(float (&c)[U][P], float (&s)[U][P], const float2* cs) const {
+    __device__ __forceinline__ Angles angles(const float2* cs) const {
+        Angles a;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const float2 v = i < turns[u] ? cs[pair0[u] + i] : make_float2(1.0f, 0.0f);
-                c[u][i] = v.x;
-                s[u][i] = v.y;
+            for (int i = 0; i < NP; ++i) {
+                const float2 x = 2 * i < turns[u] ? cs[pair0[u] + 2 * i] : make_float2(1.0f, 0.0f);
+                const float2 y = 2 * i + 1 < turns[u] ? cs[pair0[u] + 2 * i + 1] : make_float2(1.0f, 0.0f);
+                a.c[u][i] = f2(x.x, y.x);
+                a.s[u][i] = f2(x.y, y.y);
             }
+        return a;
     }
-    // Turns the pairs of f: each result one product and one fused multiply-add.
-    __device__ __forceinline__ void turn(float (&f)[U][E], const float (&c)[U][P], const float (&s)[U][P]) const {
+    // Turns the pairs: each result one product and one fused multiply-add.
+    __device__ __forceinline__ void turn(Values& v, const Angles& a) const {
+        constexpr u64 kMinus = 0x8000000080000000ull;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const float x0 = f[u][lo(i)], x1 = f[u][hi(i)];
-                if (i < turns[u]) {
-                    f[u][lo(i)] = __fmaf_rn(-x1, s[u][i], __fmul_rn(x0, c[u][i]));
-                    f[u][hi(i)] = __fmaf_rn(x0, s[u][i], __fmul_rn(x1, c[u][i]));
+            for (int i = 0; i < NP; ++i) {
+                const u64 x0 = v.first[u][i], x1 = v.second[u][i];
+                v.first[u][i] = fma2(x1 ^ kMinus, a.s[u][i], mul2(x0, a.c[u][i]));
+                v.second[u][i] = fma2(x0, a.s[u][i], mul2(x1, a.c[u][i]));
+                if (!all_turn) {  // an infinite partner does not reach an element that passes
+                    auto keep = [&](u64& now, u64 was) {
+                        if (2 * i >= turns[u]) now = (now & 0xffffffff00000000ull) | (was & 0xffffffffull);
+                        if (2 * i + 1 >= turns[u]) now = (now & 0xffffffffull) | (was & 0xffffffff00000000ull);
+                    };
+                    keep(v.first[u][i], x0);
+                    keep(v.second[u][i], x1);
                 }
             }
     }
 };
 
-// Sum over the G lanes of a group, in every lane.
+// The sum of products of a lane's values, the packed halves apart: one chain of each,
+// first elements and second ones in turn.
+template <class V, int U, int NP>
+__device__ __forceinline__ float dot(const u64 (&a0)[U][NP], const u64 (&a1)[U][NP], const V& b) {
+    u64 s = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            s = fma2(a0[u][i], b.first[u][i], s);
+            s = fma2(a1[u][i], b.second[u][i], s);
+        }
+    return f2lo(s) + f2hi(s);
+}
+
+// Sum over the lanes of a group of GT (GT 0: of G), in every lane.
+template <int GT>
 __device__ __forceinline__ float group_sum(float v, int G) {
-    for (int m = 1; m < G; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    if constexpr (GT > 0) {
+#pragma unroll
+        for (int m = 1; m < GT; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    } else {
+        for (int m = 1; m < G; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    }
     return v;
+}
+
+// How many warps share a token, and the sines and cosines of its pairs: a power of
+// two up to kQkWarps.
+constexpr int kQkWarps = 8;
+
+// The sines and cosines of token `tok`, by the warps that share it (`id` of `wpt`).
+__device__ __forceinline__ void token_angles(float2* cs, const RopeParams& r, unsigned tok, unsigned s, bool has, int id, int wpt) {
+    const int lane = threadIdx.x % 32;
+    auto meet = [&] {
+        if (wpt == 1) __syncwarp();
+        else if (wpt == kQkWarps) __syncthreads();
+        else named_bar(1 + threadIdx.x / 32 / wpt, wpt * 32);
+    };
+    meet();  // the token before has been read
+    if (has)
+        for (int j = id * 32 + lane; j < r.pairs; j += 32 * wpt) cs[j] = token_cos_sin(r, tok, s, j);
+    meet();
 }
 
 // The widest access (in elements) that divides the head and, where pairs lie in
@@ -224,11 +308,27 @@ cudaError_t for_head_shape(int hd, int n, bool f32, bool interleaved, int align,
     const int u = units <= 32 ? 1 : units <= 64 ? 2 : 4;  // hd <= 256: at most 128 units
     int g = 1;
     while (g * u < units) g *= 2;
+    auto with_g = [&](auto t, auto inter, auto width, auto v) {  // aligned heads of 64 elements and more
+        if (g == 8) return f(t, inter, width, Int<1>(), v, Int<8>(), g);
+        if (g == 16) return f(t, inter, width, Int<1>(), v, Int<16>(), g);
+        if (g == 32) return f(t, inter, width, Int<1>(), v, Int<32>(), g);
+        return f(t, inter, width, Int<1>(), v, Int<0>(), g);
+    };
     auto with_u = [&](auto t, auto inter, auto width, auto v) {
-        if constexpr (decltype(width)::value == 8) return f(t, inter, width, Int<1>(), v, g);
-        else if (u == 1) return f(t, inter, width, Int<1>(), v, g);
-        else if (decltype(width)::value > 1 || u == 2) return f(t, inter, width, Int<2>(), v, g);
-        else return f(t, inter, Int<1>(), Int<4>(), v, g);
+        constexpr int kW = decltype(width)::value;
+        // two units a lane: interleaved heads of more than 32 accesses
+        constexpr bool kTwoUnits = decltype(inter)::value && kW == 4;
+        if constexpr (kW > 1) {
+            if constexpr (kTwoUnits)
+                if (u == 2) return f(t, inter, width, Int<2>(), v, Int<0>(), g);
+            if (u > 1) return cudaErrorInvalidConfiguration;  // not reached: hd <= 256
+            if constexpr (decltype(v)::value) return with_g(t, inter, width, v);
+            else return f(t, inter, width, Int<1>(), v, Int<0>(), g);
+        } else {
+            if (u == 1) return f(t, inter, width, Int<1>(), v, Int<0>(), g);
+            if (u == 2) return f(t, inter, width, Int<2>(), v, Int<0>(), g);
+            return f(t, inter, width, Int<4>(), v, Int<0>(), g);
+        }
     };
     auto with_w = [&](auto t, auto inter) {
         constexpr bool kF32 = sizeof(t) == 4;

@@ -160,7 +160,7 @@ struct QkNormParams {
     float eps, inv_hd;
     float* ws;  // backward: [parts][2][hd] sums for the weights' gradients, or null
 };
-int64_t qk_norm_grad_parts(int64_t batch, int64_t tokens);
+int64_t qk_norm_grad_parts(int64_t batch, int64_t tokens);  // the most parts of a call
 
 cudaError_t launch_layer_norm(const LnFwdParams& p, bool f32, bool vec, cudaStream_t s);
 cudaError_t launch_ln_backward(const LnBwdParams& p, bool f32, bool vec, cudaStream_t s);
@@ -170,6 +170,6 @@ cudaError_t launch_column_sums(const ColSumParams& p, cudaStream_t s);
 cudaError_t launch_rope_axes(const RopeParams& p, bool f32, bool interleaved, int align, cudaStream_t s);
 cudaError_t launch_qk_norm_rope(const QkNormParams& p, bool f32, bool interleaved, int align, cudaStream_t s);
 cudaError_t launch_qk_norm_rope_backward(const QkNormParams& p, bool f32, bool interleaved, int align,
-                                         const ColSumParams& sums, cudaStream_t s);
+                                         ColSumParams sums, cudaStream_t s);  // fills sums.parts
 
 }  // namespace mbx

@@ -218,7 +218,6 @@ MBX_API int mbx_qk_norm_rope_backward(const mbx_heads_view* dq, const mbx_heads_
     if (dwq || dwk) {
         p.ws = workspace;
         s.ws = workspace;
-        s.parts = mbx::qk_norm_grad_parts(q->batch, q->tokens);
         s.segments = 1;
         s.D = p.rope.hd;
         s.nacc = 2;
