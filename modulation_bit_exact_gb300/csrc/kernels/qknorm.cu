@@ -4,73 +4,90 @@
 //   out = the pairs of n turned as in rope.cu; elements past the pairs pass.
 // binary32, one rounding at the output.
 //
-// A warp takes one token, or a share of its heads where tokens are few: with the
-// other warps of the token it computes the sines and cosines once, keeps its own in
-// registers and walks the heads, 32 / G of them side by side (qknorm.cuh).
+// A warp walks tokens, of Q or of K, or a share of their heads where that divides
+// the tokens better: with the other warps of a token it computes the sines and cosines,
+// keeps its own in registers and takes the heads, 32 / G of them side by side, out of a
+// ring in shared memory that it fills ahead (qknorm.cuh).
 #include "qknorm.cuh"
 
 namespace mbx {
 
+QkShare qk_share(int64_t total, int64_t most, int q_heads, int k_heads) {
+    QkShare best = {1, 1, k_heads ? 1 : 0};
+    double cost = 1e30;
+    for (int wpt = 1; wpt <= kQkWarps; wpt *= 2) {
+        const int64_t per_block = kQkWarps / wpt, need = (total + per_block - 1) / per_block;
+        int64_t q = k_heads ? most * q_heads / (q_heads + k_heads) : most;
+        q = q < 1 ? 1 : k_heads && q >= most ? most - 1 : q;
+        int64_t k = k_heads ? most - q : 0;
+        if (q > need) q = need;
+        if (k > need) k = need;
+        double c = (double)((need + q - 1) / q) * (1.0 / wpt + 0.1) * q_heads;
+        if (k) {
+            const double ck = (double)((need + k - 1) / k) * (1.0 / wpt + 0.1) * k_heads;
+            if (ck > c) c = ck;
+        }
+        if (c < cost) {
+            cost = c;
+            best = QkShare{wpt, (int)q, (int)k};
+        }
+    }
+    return best;
+}
+
 template <class T, bool INTERLEAVED, int W, int U, bool VEC, int GT>
-__global__ void __launch_bounds__(32 * kQkWarps) qk_norm_rope_kernel(QkNormParams p, int g, int wpt) {
+__global__ void __launch_bounds__(32 * kQkWarps, HeadUnits<T, INTERLEAVED, W, U, VEC>::E * U <= 8 ? 3 : 2)
+    qk_norm_rope_kernel(QkNormParams p, int g, QkShare sh) {
     using Head = HeadUnits<T, INTERLEAVED, W, U, VEC>;
-    constexpr int kAtOnce = U * Head::E <= 8 ? 4 : U * Head::E <= 16 ? 2 : 1;  // heads of a group in flight
-    extern __shared__ float2 cs_smem[];                                        // [tokens of the block][pairs]
+    constexpr int kStages = 96 / (U * Head::E * (int)sizeof(T)) < 2 ? 2 : 96 / (U * Head::E * (int)sizeof(T));
+    extern __shared__ uint4 smem[];  // [warps][stages] slots, then [tokens of the block][pairs]
     const RopeParams& r = p.rope;
-    const int G = GT ? GT : g, groups = 32 / G;
+    const int G = GT ? GT : g, groups = 32 / G, wpt = sh.wpt, per_block = kQkWarps / wpt;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, slot = warp / wpt, share = warp % wpt;
+    const bool which = (int)blockIdx.x >= sh.q_blocks;
+    const int block = which ? blockIdx.x - sh.q_blocks : blockIdx.x, blocks = which ? sh.k_blocks : sh.q_blocks;
+    const RopeTensor& t = which ? r.k : r.q;
     const unsigned tokens = (unsigned)r.tokens, total = (unsigned)r.batch * tokens;
-    const unsigned tok = blockIdx.x * (unsigned)(kQkWarps / wpt) + slot;
     const Head head(lane % G, G, r.hd, r.pairs);
+    float2* cs = reinterpret_cast<float2*>(reinterpret_cast<char*>(smem) + kQkWarps * kStages * Head::kSlotBytes) + slot * r.pairs;
+    const int h0 = share * groups + lane / G, step = wpt * groups;
+    HeadStream<Head, T, 1, kStages> in(
+        head, (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * Head::kSlotBytes + lane * Head::kAccessBytes,
+        block * per_block + slot, blocks * per_block, tokens, total, h0, lane / G, step, t.heads);
+    in.tensor(0, t.in, t.ib, t.it, t.ih);
+    typename Head::Raw raw[1];
+    raw[0].clear();
     grid_dep_wait();
     grid_dep_launch();
-    const bool has = tok < total;
-    const unsigned b = has ? tok / tokens : 0, s = has ? tok - b * tokens : 0;
-    const int h0 = share * groups + lane / G, step = wpt * groups;
+    in.start();
+    const typename Head::Values w = head.weight(p.w[which], p.w_f32);
 
-    typename Head::Raw raw[kAtOnce];
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) raw[i].clear();
-    const T* in = static_cast<const T*>(r.q.in) + b * r.q.ib + s * r.q.it;
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i)
-        if (has && h0 + i * step < r.q.heads) head.load(raw[i], in + (h0 + i * step) * r.q.ih);
-    float2* cs = cs_smem + slot * r.pairs;
-    token_angles(cs, r, tok, s, has, share, wpt);
-    if (!has) return;
-    const typename Head::Angles angles = head.angles(cs);
-
+    // the same number of rounds for all warps of the block, which may meet in them
 #pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-        const RopeTensor& t = which ? r.k : r.q;
-        if (t.heads == 0) break;
-        const typename Head::Values w = head.weight(p.w[which], p.w_f32);
-        in = static_cast<const T*>(t.in) + b * t.ib + s * t.it;
-        T* out = static_cast<T*>(t.out) + b * t.ob + s * t.ot;
-        // every lane of the warp takes part in the sums, also one past the last head
+    for (unsigned tok0 = block * per_block; tok0 < total; tok0 += blocks * per_block) {
+        const unsigned tok = tok0 + slot, b = tok / tokens, s = tok - b * tokens;
+        const bool has = tok < total;
+        token_angles(cs, r, tok, s, has, share, wpt);
+        if (!has) continue;
+        const typename Head::Angles angles = head.angles(cs);
+        T* out = static_cast<T*>(t.out) + b * t.ob + s * t.ot + h0 * t.oh;
 #pragma unroll 1
-        for (int h = h0; h - lane / G < t.heads; h += kAtOnce * step) {
-            if (which || h != h0) {
+        for (int i = 0; i < in.steps; ++i, out += step * t.oh) {
+            in.take(raw);
+            typename Head::Values x = Head::values(raw[0]);
+            const float ss = group_sum<GT>(dot(x.first, x.second, x), G);
+            in.fetch();
+            const float rstd = rsqrtf(__fmaf_rn(ss, p.inv_hd, p.eps));
+            const u64 r2 = f2(rstd, rstd);
 #pragma unroll
-                for (int i = 0; i < kAtOnce; ++i)
-                    if (h + i * step < t.heads) head.load(raw[i], in + (h + i * step) * t.ih);
-            }
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                typename Head::Values x = Head::values(raw[i]);
-                const float ss = group_sum<GT>(dot(x.first, x.second, x), G);
-                const float rstd = rsqrtf(__fmaf_rn(ss, p.inv_hd, p.eps));
-                const u64 r2 = f2(rstd, rstd);
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int j = 0; j < Head::NP; ++j) {
-                        x.first[u][j] = mul2(mul2(x.first[u][j], r2), w.first[u][j]);
-                        x.second[u][j] = mul2(mul2(x.second[u][j], r2), w.second[u][j]);
-                    }
-                head.turn(x, angles);
-                if (h + i * step < t.heads) head.store(out + (h + i * step) * t.oh, x);
-            }
+                for (int j = 0; j < Head::NP; ++j) {
+                    x.first[u][j] = mul2(mul2(x.first[u][j], r2), w.first[u][j]);
+                    x.second[u][j] = mul2(mul2(x.second[u][j], r2), w.second[u][j]);
+                }
+            head.turn(x, angles);
+            if (i < in.mine) head.store(out, x);
         }
     }
 }
@@ -79,14 +96,21 @@ cudaError_t launch_qk_norm_rope(const QkNormParams& p, bool f32, bool interleave
     const RopeParams& r = p.rope;
     return for_head_shape(r.hd, r.pairs, f32, interleaved, align,
                           [&](auto t, auto inter, auto w, auto u, auto vec, auto gt, int G) {
-        const int64_t total = r.batch * r.tokens;
-        const int most = r.q.heads > r.k.heads ? r.q.heads : r.k.heads;
-        int wpt = 1;
-        while (wpt < kQkWarps && wpt * (32 / G) < most && total * wpt < 8 * sm_count()) wpt *= 2;
-        const int64_t per_block = kQkWarps / wpt, grid = (total + per_block - 1) / per_block;
+        using Head = HeadUnits<decltype(t), decltype(inter)::value, decltype(w)::value, decltype(u)::value, decltype(vec)::value>;
+        constexpr int kElems = Head::E * decltype(u)::value, kBytes = kElems * (int)sizeof(t);
+        constexpr int kStages = 96 / kBytes < 2 ? 2 : 96 / kBytes;
+        const QkShare sh = qk_share(r.batch * r.tokens, (kElems <= 8 ? 3 : 2) * (int64_t)sm_count(), r.q.heads, r.k.heads);
         auto* k = qk_norm_rope_kernel<decltype(t), decltype(inter)::value, decltype(w)::value, decltype(u)::value,
                                       decltype(vec)::value, decltype(gt)::value>;
-        return launch_pdl(k, (unsigned)grid, 32 * kQkWarps, per_block * r.pairs * sizeof(float2), s, p, G, wpt);
+        const size_t smem = kQkWarps * kStages * Head::kSlotBytes + kQkWarps / sh.wpt * r.pairs * sizeof(float2);
+        static SmemOptIn opt;
+        if (smem > 48 * 1024) {
+            RingShape shape = {};
+            shape.stages = 1;
+            shape.smem = (int)smem;
+            if (cudaError_t e = opt.allow(reinterpret_cast<const void*>(k), shape)) return e;
+        }
+        return launch_pdl(k, (unsigned)(sh.q_blocks + sh.k_blocks), 32 * kQkWarps, smem, s, p, G, sh);
     });
 }
 

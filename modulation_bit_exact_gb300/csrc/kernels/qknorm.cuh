@@ -18,6 +18,70 @@
 
 namespace mbx {
 
+// cos and sin of pair j's angle at a token (its index `tok` in the batch, `s` in its
+// sequence).  The angle is position * frequency / (2 pi) turns, modulo a turn, in
+// 64-bit fixed point: the product of the frequency's 53 bits with 64 bits of
+// 1 / (2 pi) and that with the position are integer products, so no position loses
+// anything and the little binary64 that this GPU has is not used (65536 tokens of one
+// head of 128 each for Q and K, whose angles are most of the work: 121 us with
+// binary64, see launch).  The remainder, at most an eighth of a turn, goes through the
+// Taylor series, whose first terms left out, t^11 / 11! and t^12 / 12!, are below 2^-29.
+__device__ __forceinline__ float2 fixed_angle(const RopeParams& p, unsigned tok, unsigned s, int j) {
+    int a = 0;
+    while (a < p.axes - 1 && j >= p.axis_end[a]) ++a;
+    const int64_t prow = (p.pos_batched ? tok : s) * p.pos_stride + a;
+    const uint64_t fb = __double_as_longlong(p.freqs[j]);
+    const int fe = (int)(fb >> 52 & 2047) - 1023;  // the frequency is 1.m * 2^fe
+    // position: pm * 2^pe
+    uint64_t pm;
+    int pe = 0;
+    bool minus = (int64_t)fb < 0, bad = fe > 53;
+    if (p.pos_f32) {
+        const uint32_t pb = __float_as_uint(load_elem(static_cast<const float*>(p.pos) + prow));
+        const int e = (int)(pb >> 23 & 255);
+        minus ^= (int)pb < 0;
+        bad |= e == 255;
+        pm = e ? (pb & 0x7fffffu) | 0x800000u : (pb & 0x7fffffu) << 1;
+        pe = e - 150;
+    } else {
+        int v;
+        asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(static_cast<const int*>(p.pos) + prow));
+        minus ^= v < 0;
+        pm = (uint32_t)(v < 0 ? -(int64_t)v : v);
+    }
+    // frequency / (2 pi) = m * C * 2^(fe - 52 - 66), C = 2^66 / (2 pi); turns in units of 2^-64
+    const uint64_t m = fe < -1022 ? 0 : (fb & 0xfffffffffffffull) | 1ull << 52;
+    constexpr uint64_t C = 0xa2f9836e4e44152aull;
+    const uint64_t lo = m * C, hi = __umul64hi(m, C);
+    // T = (hi:lo * pm) >> sh, modulo 2^64
+    const int sh = 54 - fe - pe;
+    uint64_t T;
+    if (pe == 0) {  // whole positions: the step of one position first
+        const uint64_t step = sh >= 128 ? 0 : sh >= 64 ? hi >> (sh - 64) : sh > 0 ? hi << 1 << (63 - sh) | lo >> sh : lo << -sh;
+        T = step * pm;
+    } else {
+        // 192-bit product, of which 64 bits from bit sh are wanted
+        const uint64_t w0 = lo * pm, c0 = __umul64hi(lo, pm), w1 = hi * pm + c0;
+        const uint64_t w2 = __umul64hi(hi, pm) + (w1 < c0);
+        T = sh >= 192 ? 0 : sh >= 128 ? w2 >> (sh - 128) : sh > 64 ? w2 << 1 << (127 - sh) | w1 >> (sh - 64)
+            : sh == 64 ? w1 : sh > 0 ? w1 << 1 << (63 - sh) | w0 >> sh : sh > -64 ? w0 << -sh : 0;
+    }
+    if (minus) T = 0 - T;
+    const uint32_t quadrant = (uint32_t)((T + (1ull << 61)) >> 62);
+    const float t = (float)(int)((T - ((uint64_t)quadrant << 62)) >> 32) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+    const float z = t * t;
+    float c = __fmaf_rn(z, -2.7557319e-7f, 2.4801587e-5f), n = __fmaf_rn(z, 2.7557319e-6f, -1.9841270e-4f);
+    c = __fmaf_rn(z, c, -1.3888889e-3f), n = __fmaf_rn(z, n, 8.3333333e-3f);
+    c = __fmaf_rn(z, c, 4.1666667e-2f), n = __fmaf_rn(z, n, -1.6666667e-1f);
+    c = __fmaf_rn(z, c, -0.5f), n = __fmaf_rn(t * z, n, t);
+    c = __fmaf_rn(z, c, 1.0f);
+    const float cc = quadrant & 1 ? -n : c, ss = quadrant & 1 ? c : n;
+    float2 v = quadrant & 2 ? make_float2(-cc, -ss) : make_float2(cc, ss);
+    if (p.inverse) v.y = -v.y;
+    if (bad) v.x = v.y = __uint_as_float(0x7fffffffu);
+    return v;
+}
+
 // An access of W elements as 32-bit words, and as binary32 values.
 template <class T, int W, bool VEC>
 struct Access1 {
@@ -129,7 +193,42 @@ struct HeadUnits {
     struct Values {
         u64 first[U][NP], second[U][NP];
     };
-    __device__ __forceinline__ void load(Raw& r, const T* head) const {  // into a Raw that was cleared once
+    // Heads on their way: where accesses are aligned each lane copies its own to its
+    // place in shared memory, asynchronously, and reads them back itself, so nothing
+    // but its own wait orders the two.  One slot has a head of every group of the warp.
+    static constexpr bool kRing = VEC && W > 1;
+    static constexpr int kAccessBytes = W * (int)sizeof(T), kSlotBytes = kRing ? U * A * 32 * kAccessBytes : 0;
+    __device__ __forceinline__ void copy(uint32_t slot, const T* head) const {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < A; ++k) {
+                const int off = k ? off1[u] : off0[u];
+                const uint32_t to = slot + (u * A + k) * 32 * kAccessBytes;
+                if (off >= 0) {
+                    if constexpr (kAccessBytes == 16)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(head + off) : "memory");
+                    else
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(head + off) : "memory");
+                }
+            }
+    }
+    __device__ __forceinline__ void read(Raw& r, uint32_t slot) const {  // into a Raw that was cleared once
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < A; ++k) {
+                const uint32_t from = slot + (u * A + k) * 32 * kAccessBytes;
+                uint32_t* w = r.a[u][k].w;
+                if ((k ? off1[u] : off0[u]) >= 0) {
+                    if constexpr (kAccessBytes == 16)
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from) : "memory");
+                    else
+                        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(from) : "memory");
+                }
+            }
+    }
+    __device__ __forceinline__ void load(Raw& r, const T* head) const {  // the same
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (off0[u] >= 0) r.a[u][0].load(head + off0[u]);
@@ -266,11 +365,22 @@ __device__ __forceinline__ float group_sum(float v, int G) {
     return v;
 }
 
-// How many warps share a token, and the sines and cosines of its pairs: a power of
-// two up to kQkWarps.
-constexpr int kQkWarps = 8;
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// The sines and cosines of token `tok`, by the warps that share it (`id` of `wpt`).
+// Blocks of kQkWarps warps; `wpt` of them (a power of two) share a token.  Q and K have
+// blocks of their own, in proportion to their heads.
+constexpr int kQkWarps = 8;
+struct QkShare {
+    int wpt, q_blocks, k_blocks;
+};
+// For `total` tokens and `most` blocks: a block walks tokens, and the fewest rounds of
+// them win, a share of a token's heads counting by its size and a tenth of the token
+// for what every share pays.
+QkShare qk_share(int64_t total, int64_t most, int q_heads, int k_heads);
+
+// The sines and cosines of a token's pairs, by the warps that share it (`id` of `wpt`).
 __device__ __forceinline__ void token_angles(float2* cs, const RopeParams& r, unsigned tok, unsigned s, bool has, int id, int wpt) {
     const int lane = threadIdx.x % 32;
     auto meet = [&] {
@@ -280,9 +390,89 @@ __device__ __forceinline__ void token_angles(float2* cs, const RopeParams& r, un
     };
     meet();  // the token before has been read
     if (has)
-        for (int j = id * 32 + lane; j < r.pairs; j += 32 * wpt) cs[j] = token_cos_sin(r, tok, s, j);
+        for (int j = id * 32 + lane; j < r.pairs; j += 32 * wpt) cs[j] = fixed_angle(r, tok, s, j);
     meet();
 }
+
+// The heads that a warp works through, of N tensors of one shape (the input, and the
+// incoming gradient): those of its share of a token, `step` apart, token after token.
+// fetch() brings the next ones, kStages of them ahead of take(), which gives them in
+// order.  Lanes whose group has no head at a step, and steps past the last, copy
+// nothing.
+template <class Head, class T, int N, int kStages>
+struct HeadStream {
+    const Head& head;
+    const T* base[N];
+    int64_t sb[N], st[N], sh[N];
+    const T* at[N];
+    uint32_t ring;  // this lane's places in the warp's slots
+    unsigned tok, stride, tokens, total;
+    int i, steps, step, mine;  // step of the token, steps of a token, heads between steps, steps with a head of this lane
+    int fill, drain;           // slots
+    int64_t first;             // the lane's first head
+    __device__ __forceinline__ HeadStream(const Head& hd, uint32_t ring_, unsigned tok_, unsigned stride_, unsigned tokens_,
+                                          unsigned total_, int h0, int group, int step_, int heads)
+        : head(hd), ring(ring_), tok(tok_), stride(stride_), tokens(tokens_), total(total_), i(0), step(step_), fill(0),
+          drain(0), first(h0) {
+        steps = heads > h0 - group ? (heads - (h0 - group) + step - 1) / step : 0;
+        mine = heads > h0 ? (heads - h0 + step - 1) / step : 0;
+    }
+    __device__ __forceinline__ void tensor(int k, const void* p, int64_t b, int64_t t, int64_t h) {
+        base[k] = static_cast<const T*>(p);
+        sb[k] = b, st[k] = t, sh[k] = h;
+    }
+    __device__ __forceinline__ void aim() {
+        if (tok >= total) return;
+        const unsigned b = tok / tokens;
+#pragma unroll
+        for (int k = 0; k < N; ++k) at[k] = base[k] + b * sb[k] + (tok - b * tokens) * st[k] + first * sh[k];
+    }
+    __device__ __forceinline__ void next() {
+        if (++i == steps) {
+            i = 0;
+            tok += stride;
+            aim();
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) at[k] += step * sh[k];
+        }
+    }
+    __device__ __forceinline__ void fetch() {
+        if constexpr (Head::kRing) {
+            if (steps && tok < total) {
+                if (i < mine) {
+#pragma unroll
+                    for (int k = 0; k < N; ++k) head.copy(ring + (fill * N + k) * Head::kSlotBytes, at[k]);
+                }
+                next();
+            }
+            copies_commit();
+            fill = fill + 1 == kStages ? 0 : fill + 1;
+        }
+    }
+    __device__ __forceinline__ void start() {
+        aim();
+        if constexpr (Head::kRing) {
+#pragma unroll 1
+            for (int k = 0; k < kStages; ++k) fetch();
+        }
+    }
+    // The values of the next step; call fetch() once they have been used.
+    __device__ __forceinline__ void take(typename Head::Raw (&r)[N]) {
+        if constexpr (Head::kRing) {
+            copies_wait<kStages - 1>();
+#pragma unroll
+            for (int k = 0; k < N; ++k) head.read(r[k], ring + (drain * N + k) * Head::kSlotBytes);
+            drain = drain + 1 == kStages ? 0 : drain + 1;
+        } else {
+            if (i < mine) {
+#pragma unroll
+                for (int k = 0; k < N; ++k) head.load(r[k], at[k]);
+            }
+            next();
+        }
+    }
+};
 
 // The widest access (in elements) that divides the head and, where pairs lie in
 // halves, the number of pairs; 1 where only single elements do.
