@@ -5,9 +5,8 @@
 // side by side, so a unit is one access of W elements; pairs in halves (j, j+n)
 // are the access at j and the one at j+n; elements past the pairs come two
 // accesses a unit.  With W = 1 a unit is one pair, or two elements that pass.
-// A group of G lanes (a power of two up to 32) has the head's units, unit
-// lane + G*u in place u < U, so a row sum is a chain within the lane and a
-// butterfly over the group.  W, G and U follow the head's size, its pairs and the
+// A group of G lanes has the head's units, unit lane + G*u in place u < U, so a row
+// sum is a chain within the lane and a tree over the group.  W, G and U follow the head's size, its pairs and the
 // type alone: where a head lies decides only whether an access is one load
 // or one for each element, so its bits are the same at any address.
 #pragma once
@@ -18,55 +17,65 @@
 
 namespace mbx {
 
-// cos and sin of pair j's angle at a token (its index `tok` in the batch, `s` in its
-// sequence).  The angle is position * frequency / (2 pi) turns, modulo a turn, in
-// 64-bit fixed point: the product of the frequency's 53 bits with 64 bits of
-// 1 / (2 pi) and that with the position are integer products, so no position loses
-// anything and the little binary64 that this GPU has is not used (65536 tokens of one
-// head of 128 each for Q and K, whose angles are most of the work: 121 us with
-// binary64, see launch).  The remainder, at most an eighth of a turn, goes through the
-// Taylor series, whose first terms left out, t^11 / 11! and t^12 / 12!, are below 2^-29.
-__device__ __forceinline__ float2 fixed_angle(const RopeParams& p, unsigned tok, unsigned s, int j) {
+// The angles.  Position * frequency / (2 pi) turns, modulo a turn, in 64-bit fixed
+// point: the product of the frequency's 53 bits with 64 bits of 1 / (2 pi) is formed
+// once in a block for each pair, that with the position for each token, in integers,
+// so no position loses anything and the little binary64 that this GPU has is not used
+// (65536 tokens of one head of 128 each for Q and K, whose angles are most of the
+// work: 121 us with binary64, 89 in integers, the frequency's part for each token).
+struct PairFreq {
+    uint64_t hi, lo;  // whole positions: hi = the step of one position in 2^-64 turns; others: the 128-bit product
+    int sh;           // its place: turns * 2^64 = hi:lo >> sh
+    int16_t axis;
+    bool minus, bad;
+};
+__device__ __forceinline__ PairFreq pair_freq(const RopeParams& p, int j) {
+    PairFreq q;
     int a = 0;
     while (a < p.axes - 1 && j >= p.axis_end[a]) ++a;
-    const int64_t prow = (p.pos_batched ? tok : s) * p.pos_stride + a;
+    q.axis = (int16_t)a;
     const uint64_t fb = __double_as_longlong(p.freqs[j]);
     const int fe = (int)(fb >> 52 & 2047) - 1023;  // the frequency is 1.m * 2^fe
-    // position: pm * 2^pe
-    uint64_t pm;
-    int pe = 0;
-    bool minus = (int64_t)fb < 0, bad = fe > 53;
-    if (p.pos_f32) {
-        const uint32_t pb = __float_as_uint(load_elem(static_cast<const float*>(p.pos) + prow));
-        const int e = (int)(pb >> 23 & 255);
-        minus ^= (int)pb < 0;
-        bad |= e == 255;
-        pm = e ? (pb & 0x7fffffu) | 0x800000u : (pb & 0x7fffffu) << 1;
-        pe = e - 150;
-    } else {
-        int v;
-        asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(static_cast<const int*>(p.pos) + prow));
-        minus ^= v < 0;
-        pm = (uint32_t)(v < 0 ? -(int64_t)v : v);
-    }
-    // frequency / (2 pi) = m * C * 2^(fe - 52 - 66), C = 2^66 / (2 pi); turns in units of 2^-64
+    q.minus = (int64_t)fb < 0;
+    q.bad = fe > 53;
+    // frequency / (2 pi) = m * C * 2^(fe - 52 - 66), C = 2^66 / (2 pi)
     const uint64_t m = fe < -1022 ? 0 : (fb & 0xfffffffffffffull) | 1ull << 52;
     constexpr uint64_t C = 0xa2f9836e4e44152aull;
-    const uint64_t lo = m * C, hi = __umul64hi(m, C);
-    // T = (hi:lo * pm) >> sh, modulo 2^64
-    const int sh = 54 - fe - pe;
+    q.lo = m * C;
+    q.hi = __umul64hi(m, C);
+    q.sh = 54 - fe;
+    if (!p.pos_f32) {
+        const int sh = q.sh;
+        q.hi = sh >= 128 ? 0 : sh >= 64 ? q.hi >> (sh - 64) : sh > 0 ? q.hi << 1 << (63 - sh) | q.lo >> sh : 0;
+    }
+    return q;
+}
+// A position's bits on an axis at a token (its index `tok` in the batch, `s` in its sequence).
+__device__ __forceinline__ uint32_t position_bits(const RopeParams& p, unsigned tok, unsigned s, int axis) {
+    uint32_t v;
+    const uint32_t* at = static_cast<const uint32_t*>(p.pos) + (int64_t)(p.pos_batched ? tok : s) * p.pos_stride + axis;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(at));
+    return v;
+}
+// cos and sin of the angle.  The remainder, at most an eighth of a turn, goes through
+// the Taylor series, whose first terms left out, t^11 / 11! and t^12 / 12!, are below 2^-29.
+__device__ __forceinline__ float2 pair_angle(const RopeParams& p, const PairFreq& q, uint32_t pos) {
     uint64_t T;
-    if (pe == 0) {  // whole positions: the step of one position first
-        const uint64_t step = sh >= 128 ? 0 : sh >= 64 ? hi >> (sh - 64) : sh > 0 ? hi << 1 << (63 - sh) | lo >> sh : lo << -sh;
-        T = step * pm;
+    bool minus = q.minus != ((int)pos < 0), bad = q.bad;
+    if (!p.pos_f32) {
+        T = q.hi * ((int)pos < 0 ? 0u - pos : pos);
     } else {
+        const int e = (int)(pos >> 23 & 255);  // the position is pm * 2^(e - 150)
+        bad |= e == 255;
+        const uint64_t pm = e ? (pos & 0x7fffffu) | 0x800000u : (pos & 0x7fffffu) << 1;
+        const int sh = q.sh - (e - 150);
         // 192-bit product, of which 64 bits from bit sh are wanted
-        const uint64_t w0 = lo * pm, c0 = __umul64hi(lo, pm), w1 = hi * pm + c0;
-        const uint64_t w2 = __umul64hi(hi, pm) + (w1 < c0);
+        const uint64_t w0 = q.lo * pm, c0 = __umul64hi(q.lo, pm), w1 = q.hi * pm + c0;
+        const uint64_t w2 = __umul64hi(q.hi, pm) + (w1 < c0);
         T = sh >= 192 ? 0 : sh >= 128 ? w2 >> (sh - 128) : sh > 64 ? w2 << 1 << (127 - sh) | w1 >> (sh - 64)
             : sh == 64 ? w1 : sh > 0 ? w1 << 1 << (63 - sh) | w0 >> sh : sh > -64 ? w0 << -sh : 0;
     }
-    if (minus) T = 0 - T;
+    if (minus != p.inverse) T = 0 - T;
     const uint32_t quadrant = (uint32_t)((T + (1ull << 61)) >> 62);
     const float t = (float)(int)((T - ((uint64_t)quadrant << 62)) >> 32) * 1.4629180792671596e-9f;  // 2 pi / 2^32
     const float z = t * t;
@@ -76,10 +85,8 @@ __device__ __forceinline__ float2 fixed_angle(const RopeParams& p, unsigned tok,
     c = __fmaf_rn(z, c, -0.5f), n = __fmaf_rn(t * z, n, t);
     c = __fmaf_rn(z, c, 1.0f);
     const float cc = quadrant & 1 ? -n : c, ss = quadrant & 1 ? c : n;
-    float2 v = quadrant & 2 ? make_float2(-cc, -ss) : make_float2(cc, ss);
-    if (p.inverse) v.y = -v.y;
-    if (bad) v.x = v.y = __uint_as_float(0x7fffffffu);
-    return v;
+    if (bad) return make_float2(__uint_as_float(0x7fffffffu), __uint_as_float(0x7fffffffu));
+    return quadrant & 2 ? make_float2(-cc, -ss) : make_float2(cc, ss);
 }
 
 // An access of W elements as 32-bit words, and as binary32 values.
@@ -102,8 +109,10 @@ struct Access1 {
         } else if constexpr (NW == 4) {
             const uint4 v = ld_stream_rw(p);
             w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-        } else {
+        } else if constexpr (NW == 2) {
             asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+        } else {
+            asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
         }
     }
     __device__ __forceinline__ void store(T* p) const {
@@ -120,8 +129,10 @@ struct Access1 {
             }
         } else if constexpr (NW == 4) {
             st_v4(p, make_uint4(w[0], w[1], w[2], w[3]));
-        } else {
+        } else if constexpr (NW == 2) {
             st_v2(p, w[0], w[1]);
+        } else {
+            asm volatile("st.global.u32 [%0], %1;" ::"l"(p), "r"(w[0]) : "memory");
         }
     }
     __device__ __forceinline__ void widen(float* f) const {
@@ -209,7 +220,7 @@ struct HeadUnits {
                     if constexpr (kAccessBytes == 16)
                         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(head + off) : "memory");
                     else
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(head + off) : "memory");
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(head + off), "n"(kAccessBytes) : "memory");
                 }
             }
     }
@@ -223,8 +234,10 @@ struct HeadUnits {
                 if ((k ? off1[u] : off0[u]) >= 0) {
                     if constexpr (kAccessBytes == 16)
                         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from) : "memory");
-                    else
+                    else if constexpr (kAccessBytes == 8)
                         asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(from) : "memory");
+                    else
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(from) : "memory");
                 }
             }
     }
@@ -353,16 +366,28 @@ __device__ __forceinline__ float dot(const u64 (&a0)[U][NP], const u64 (&a1)[U][
     return f2lo(s) + f2hi(s);
 }
 
-// Sum over the lanes of a group of GT (GT 0: of G), in every lane.
+// Sum over the lanes of a group of GT (GT 0: of G), in every lane.  Groups of a power
+// of two meet in a butterfly; others fold their upper half onto the lower one until one
+// lane has the sum, which the group then reads.
 template <int GT>
 __device__ __forceinline__ float group_sum(float v, int G) {
-    if constexpr (GT > 0) {
+    if constexpr (GT > 0 && (GT & (GT - 1)) == 0) {
 #pragma unroll
         for (int m = 1; m < GT; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+        return v;
     } else {
-        for (int m = 1; m < G; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+        const int g = GT ? GT : G, lane = threadIdx.x % 32, at = lane % g;
+        if (GT == 0 && (g & (g - 1)) == 0) {
+            for (int m = 1; m < g; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+            return v;
+        }
+#pragma unroll
+        for (int n = g; n > 1; n = (n + 1) / 2) {
+            const float up = __shfl_down_sync(0xffffffffu, v, (n + 1) / 2);
+            if (at < n / 2) v += up;
+        }
+        return __shfl_sync(0xffffffffu, v, lane - at);
     }
-    return v;
 }
 
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -380,19 +405,40 @@ struct QkShare {
 // for what every share pays.
 QkShare qk_share(int64_t total, int64_t most, int q_heads, int k_heads);
 
-// The sines and cosines of a token's pairs, by the warps that share it (`id` of `wpt`).
-__device__ __forceinline__ void token_angles(float2* cs, const RopeParams& r, unsigned tok, unsigned s, bool has, int id, int wpt) {
-    const int lane = threadIdx.x % 32;
-    auto meet = [&] {
+// The sines and cosines of the tokens that a warp, with the others that share them
+// (this is `id` of `wpt`), walks.  A lane has pairs `first`, first + gap, ...; the
+// positions of the next token are fetched while this one's heads are worked on.
+struct TokenAngles {
+    static constexpr int kMost = 4;  // pairs of a lane: 128 of a head
+    const RopeParams& r;
+    const PairFreq* freqs;
+    float2* cs;
+    int wpt, first, gap;
+    uint32_t pos[kMost];
+    __device__ __forceinline__ TokenAngles(const RopeParams& r_, const PairFreq* freqs_, float2* cs_, int id, int wpt_)
+        : r(r_), freqs(freqs_), cs(cs_), wpt(wpt_), first(id * 32 + threadIdx.x % 32), gap(32 * wpt_) {}
+    __device__ __forceinline__ void meet() const {
         if (wpt == 1) __syncwarp();
         else if (wpt == kQkWarps) __syncthreads();
         else named_bar(1 + threadIdx.x / 32 / wpt, wpt * 32);
-    };
-    meet();  // the token before has been read
-    if (has)
-        for (int j = id * 32 + lane; j < r.pairs; j += 32 * wpt) cs[j] = fixed_angle(r, tok, s, j);
-    meet();
-}
+    }
+    __device__ __forceinline__ void fetch(unsigned tok, unsigned tokens, unsigned total) {
+        if (tok >= total) return;
+        const unsigned s = tok % tokens;
+#pragma unroll
+        for (int k = 0; k < kMost; ++k)
+            if (first + k * gap < r.pairs) pos[k] = position_bits(r, tok, s, freqs[first + k * gap].axis);
+    }
+    __device__ __forceinline__ void make(bool has) const {
+        meet();  // the token before has been read
+        if (has) {
+#pragma unroll
+            for (int k = 0; k < kMost; ++k)
+                if (first + k * gap < r.pairs) cs[first + k * gap] = pair_angle(r, freqs[first + k * gap], pos[k]);
+        }
+        meet();
+    }
+};
 
 // The heads that a warp works through, of N tensors of one shape (the input, and the
 // incoming gradient): those of its share of a token, `step` apart, token after token.
@@ -411,11 +457,12 @@ struct HeadStream {
     int fill, drain;           // slots
     int64_t first;             // the lane's first head
     __device__ __forceinline__ HeadStream(const Head& hd, uint32_t ring_, unsigned tok_, unsigned stride_, unsigned tokens_,
-                                          unsigned total_, int h0, int group, int step_, int heads)
+                                          unsigned total_, int h0, int group, int step_, int heads,
+                                          bool takes_part)
         : head(hd), ring(ring_), tok(tok_), stride(stride_), tokens(tokens_), total(total_), i(0), step(step_), fill(0),
           drain(0), first(h0) {
         steps = heads > h0 - group ? (heads - (h0 - group) + step - 1) / step : 0;
-        mine = heads > h0 ? (heads - h0 + step - 1) / step : 0;
+        mine = heads > h0 && takes_part ? (heads - h0 + step - 1) / step : 0;
     }
     __device__ __forceinline__ void tensor(int k, const void* p, int64_t b, int64_t t, int64_t h) {
         base[k] = static_cast<const T*>(p);
@@ -474,61 +521,81 @@ struct HeadStream {
     }
 };
 
-// The widest access (in elements) that divides the head and, where pairs lie in
-// halves, the number of pairs; 1 where only single elements do.
-inline int unit_width(int hd, int n, bool f32, bool interleaved) {
+// How a head lies in the lanes.  The widest access (in elements) that divides the head
+// and, where pairs lie in halves, the number of pairs; then as many units a lane as make
+// kElems elements, and the group: a power of two, or as many lanes as there are units
+// where more groups fit in a warp so.
+struct HeadShape {
+    int w, u, g;
+    bool vec;
+};
+template <int kElems, int kWidest>  // of a bfloat16 head; a float32 one has accesses of 4
+inline HeadShape head_shape(int hd, int n, bool f32, bool interleaved, int align) {
     auto fits = [&](int w) { return hd % w == 0 && (interleaved || n % w == 0); };
-    return f32 ? (fits(4) ? 4 : 1) : fits(8) ? 8 : fits(4) ? 4 : 1;
-}
-inline int head_units(int hd, int n, int w, bool interleaved) {
-    if (interleaved && w > 1) return hd / w;
-    return n / w + ((hd - 2 * n) / w + 1) / 2;
+    HeadShape s;
+    s.w = f32 ? 4 : kWidest;
+    while (s.w > 1 && !fits(s.w)) s.w /= 2;
+    s.vec = align >= s.w * (f32 ? 4 : 2);
+    const bool one = interleaved && s.w > 1;  // one access a unit
+    const int units = one ? hd / s.w : n / s.w + ((hd - 2 * n) / s.w + 1) / 2, e = one ? s.w : 2 * s.w;
+    s.u = 1;
+    while (units > 32 * s.u || (s.u < 4 && 2 * s.u * e <= kElems && units % (2 * s.u) == 0)) s.u *= 2;
+    const int lanes = (units + s.u - 1) / s.u;
+    s.g = 1;
+    while (s.g < lanes) s.g *= 2;
+    if (32 / lanes > 32 / s.g) s.g = lanes;
+    return s;
 }
 
-// Calls f(T, INTERLEAVED, W, U, VEC as types) for a head's shape; G is the group.
+// Calls f with a head's shape as types: the element, and Int or Bool of INTERLEAVED, W,
+// U, VEC and the group (0: as given).
 template <int V>
 using Int = std::integral_constant<int, V>;
 template <bool V>
 using Bool = std::integral_constant<bool, V>;
 
-template <class F>
-cudaError_t for_head_shape(int hd, int n, bool f32, bool interleaved, int align, F&& f) {
-    const int w = unit_width(hd, n, f32, interleaved), units = head_units(hd, n, w, interleaved);
-    const bool vec = align >= w * (f32 ? 4 : 2);
-    const int u = units <= 32 ? 1 : units <= 64 ? 2 : 4;  // hd <= 256: at most 128 units
-    int g = 1;
-    while (g * u < units) g *= 2;
-    auto with_g = [&](auto t, auto inter, auto width, auto v) {  // aligned heads of 64 elements and more
-        if (g == 8) return f(t, inter, width, Int<1>(), v, Int<8>(), g);
-        if (g == 16) return f(t, inter, width, Int<1>(), v, Int<16>(), g);
-        if (g == 32) return f(t, inter, width, Int<1>(), v, Int<32>(), g);
-        return f(t, inter, width, Int<1>(), v, Int<0>(), g);
-    };
-    auto with_u = [&](auto t, auto inter, auto width, auto v) {
-        constexpr int kW = decltype(width)::value;
-        // two units a lane: interleaved heads of more than 32 accesses
-        constexpr bool kTwoUnits = decltype(inter)::value && kW == 4;
-        if constexpr (kW > 1) {
-            if constexpr (kTwoUnits)
-                if (u == 2) return f(t, inter, width, Int<2>(), v, Int<0>(), g);
-            if (u > 1) return cudaErrorInvalidConfiguration;  // not reached: hd <= 256
-            if constexpr (decltype(v)::value) return with_g(t, inter, width, v);
-            else return f(t, inter, width, Int<1>(), v, Int<0>(), g);
-        } else {
-            if (u == 1) return f(t, inter, width, Int<1>(), v, Int<0>(), g);
-            if (u == 2) return f(t, inter, width, Int<2>(), v, Int<0>(), g);
-            return f(t, inter, width, Int<4>(), v, Int<0>(), g);
+template <int kElems, int kWidest, bool INTERLEAVED, class F>
+cudaError_t for_head_shape(const HeadShape& s, bool f32, F&& f) {
+    auto with_g = [&](auto t, auto inter, auto w, auto u, auto v) {
+        if constexpr (decltype(v)::value && decltype(w)::value >= 4) {
+            if (s.g == 4) return f(t, inter, w, u, v, Int<4>());
+            if (s.g == 8) return f(t, inter, w, u, v, Int<8>());
+            if (s.g == 10) return f(t, inter, w, u, v, Int<10>());
+            if (s.g == 16) return f(t, inter, w, u, v, Int<16>());
+            if (s.g == 32) return f(t, inter, w, u, v, Int<32>());
         }
+        return f(t, inter, w, u, v, Int<0>());
+    };
+    auto with_u = [&](auto t, auto inter, auto w, auto v) {
+        constexpr int kW = decltype(w)::value, kOne = decltype(inter)::value && kW > 1, kUnit = kOne ? kW : 2 * kW;
+        constexpr int kUnits = 256 / kUnit;  // of the largest head
+        if (s.u == 1) return with_g(t, inter, w, Int<1>(), v);
+        if constexpr (2 * kUnit <= kElems || kUnits > 32)
+            if (s.u == 2) return with_g(t, inter, w, Int<2>(), v);
+        if constexpr (4 * kUnit <= kElems || kUnits > 64)
+            if (s.u == 4) return with_g(t, inter, w, Int<4>(), v);
+        return cudaErrorInvalidConfiguration;  // not reached
+    };
+    auto with_v = [&](auto t, auto inter, auto w) {
+        return s.vec ? with_u(t, inter, w, Bool<true>()) : with_u(t, inter, w, Bool<false>());
     };
     auto with_w = [&](auto t, auto inter) {
-        constexpr bool kF32 = sizeof(t) == 4;
-        if constexpr (!kF32)
-            if (w == 8) return vec ? with_u(t, inter, Int<8>(), Bool<true>()) : with_u(t, inter, Int<8>(), Bool<false>());
-        if (w == 4) return vec ? with_u(t, inter, Int<4>(), Bool<true>()) : with_u(t, inter, Int<4>(), Bool<false>());
+        if constexpr (sizeof(t) == 2 && kWidest == 8)
+            if (s.w == 8) return with_v(t, inter, Int<8>());
+        if (s.w == 4) return with_v(t, inter, Int<4>());
+        if (s.w == 2) return with_v(t, inter, Int<2>());
         return with_u(t, inter, Int<1>(), Bool<true>());
     };
-    if (f32) return interleaved ? with_w(0.0f, Bool<true>()) : with_w(0.0f, Bool<false>());
-    return interleaved ? with_w((uint16_t)0, Bool<true>()) : with_w((uint16_t)0, Bool<false>());
+    return f32 ? with_w(0.0f, Bool<INTERLEAVED>()) : with_w((uint16_t)0, Bool<INTERLEAVED>());
+}
+
+// Lets a kernel have `bytes` of shared memory.
+inline cudaError_t allow_smem(SmemOptIn& opt, const void* kernel, size_t bytes) {
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    RingShape ring = {};
+    ring.stages = 1;
+    ring.smem = (int)bytes;
+    return opt.allow(kernel, ring);
 }
 
 }  // namespace mbx

@@ -22,7 +22,7 @@ __global__ void __launch_bounds__(32 * kQkWarps, grad_blocks(HeadUnits<T, INTERL
     qk_norm_rope_bwd_kernel(QkNormParams p, int g, QkShare sh) {
     using Head = HeadUnits<T, INTERLEAVED, W, U, VEC>;
     constexpr int E = Head::E, NP = Head::NP, kStages = grad_stages(U * E * (int)sizeof(T));
-    extern __shared__ uint4 smem[];  // [warps][stages][2] slots, then [tokens of the block][pairs], then [warps][hd] sums
+    extern __shared__ uint4 smem[];  // [warps][stages][2] slots, the pairs' frequencies, [tokens of the block][pairs], [warps][hd] sums
     const RopeParams& r = p.rope;
     const int G = GT ? GT : g, groups = 32 / G, hd = r.hd, wpt = sh.wpt, per_block = kQkWarps / wpt;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, slot = warp / wpt, share = warp % wpt;
@@ -32,13 +32,14 @@ __global__ void __launch_bounds__(32 * kQkWarps, grad_blocks(HeadUnits<T, INTERL
     const GradIn& d = p.dout[which];
     const unsigned tokens = (unsigned)r.tokens, total = (unsigned)r.batch * tokens;
     const Head head(lane % G, G, hd, r.pairs);
-    float2* cs_all = reinterpret_cast<float2*>(reinterpret_cast<char*>(smem) + kQkWarps * kStages * 2 * Head::kSlotBytes);
+    PairFreq* freqs = reinterpret_cast<PairFreq*>(reinterpret_cast<char*>(smem) + kQkWarps * kStages * 2 * Head::kSlotBytes);
+    float2* cs_all = reinterpret_cast<float2*>(freqs + r.pairs);
     float2* cs = cs_all + slot * r.pairs;
     float* sums = reinterpret_cast<float*>(cs_all + per_block * r.pairs);
     const int h0 = share * groups + lane / G, step = wpt * groups;
     HeadStream<Head, T, 2, kStages> in(
         head, (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * 2 * Head::kSlotBytes + lane * Head::kAccessBytes,
-        block * per_block + slot, blocks * per_block, tokens, total, h0, lane / G, step, t.heads);
+        block * per_block + slot, blocks * per_block, tokens, total, h0, lane / G, step, t.heads, lane / G < groups);
     in.tensor(0, t.in, t.ib, t.it, t.ih);
     in.tensor(1, d.in, d.ib, d.it, d.ih);
     typename Head::Raw raw[2];
@@ -47,6 +48,10 @@ __global__ void __launch_bounds__(32 * kQkWarps, grad_blocks(HeadUnits<T, INTERL
     grid_dep_wait();
     grid_dep_launch();
     in.start();
+    for (int j = threadIdx.x; j < r.pairs; j += blockDim.x) freqs[j] = pair_freq(r, j);
+    __syncthreads();
+    TokenAngles angle(r, freqs, cs, share, wpt);
+    angle.fetch(block * per_block + slot, tokens, total);
     const typename Head::Values w = head.weight(p.w[which], p.w_f32);
     typename Head::Values acc;
 #pragma unroll
@@ -59,7 +64,8 @@ __global__ void __launch_bounds__(32 * kQkWarps, grad_blocks(HeadUnits<T, INTERL
     for (unsigned tok0 = block * per_block; tok0 < total; tok0 += blocks * per_block) {
         const unsigned tok = tok0 + slot, b = tok / tokens, s = tok - b * tokens;
         const bool has = tok < total;
-        token_angles(cs, r, tok, s, has, share, wpt);
+        angle.make(has);
+        angle.fetch(tok + blocks * per_block, tokens, total);
         if (!has) continue;
         const typename Head::Angles angles = head.angles(cs);
         T* out = static_cast<T*>(t.out) + b * t.ob + s * t.ot + h0 * t.oh;
@@ -105,7 +111,9 @@ __global__ void __launch_bounds__(32 * kQkWarps, grad_blocks(HeadUnits<T, INTERL
     for (int u = 0; u < U; ++u) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            for (int m = G; m < 32; m <<= 1) a[u][e] += __shfl_xor_sync(0xffffffffu, a[u][e], m);
+            float v = a[u][e];
+            for (int k = 1; k < groups; ++k) v += __shfl_sync(0xffffffffu, a[u][e], lane % G + k * G);
+            a[u][e] = v;
         }
         if (lane < G) {
 #pragma unroll
@@ -134,28 +142,31 @@ int64_t qk_norm_grad_parts(int64_t batch, int64_t tokens) {
     return total < most ? total : most;
 }
 
-cudaError_t launch_qk_norm_rope_backward(const QkNormParams& p, bool f32, bool interleaved, int align, ColSumParams sums,
-                                         cudaStream_t s) {
+// 8 elements a lane: two tensors, the sums and the weights fill the registers of two
+// blocks an SM.
+template <bool INTERLEAVED>
+static cudaError_t backward(const QkNormParams& p, bool f32, int align, ColSumParams& sums, cudaStream_t s) {
+    constexpr int kWidest = INTERLEAVED ? 8 : 4;
     const RopeParams& r = p.rope;
-    const cudaError_t e = for_head_shape(r.hd, r.pairs, f32, interleaved, align,
-                                         [&](auto t, auto inter, auto w, auto u, auto vec, auto gt, int G) {
+    const HeadShape shape = head_shape<8, kWidest>(r.hd, r.pairs, f32, INTERLEAVED, align);
+    return for_head_shape<8, kWidest, INTERLEAVED>(shape, f32, [&](auto t, auto inter, auto w, auto u, auto vec, auto gt) {
         using Head = HeadUnits<decltype(t), decltype(inter)::value, decltype(w)::value, decltype(u)::value, decltype(vec)::value>;
         constexpr int kElems = Head::E * decltype(u)::value, kStages = grad_stages(kElems * (int)sizeof(t));
         const QkShare sh = qk_share(r.batch * r.tokens, grad_blocks(kElems) * (int64_t)sm_count(), r.q.heads, r.k.heads);
         sums.parts = sh.q_blocks > sh.k_blocks ? sh.q_blocks : sh.k_blocks;
         auto* k = qk_norm_rope_bwd_kernel<decltype(t), decltype(inter)::value, decltype(w)::value, decltype(u)::value,
                                           decltype(vec)::value, decltype(gt)::value>;
-        const size_t smem = kQkWarps * kStages * 2 * Head::kSlotBytes + kQkWarps / sh.wpt * r.pairs * sizeof(float2) +
-                            kQkWarps * r.hd * sizeof(float);
+        const size_t smem = kQkWarps * kStages * 2 * Head::kSlotBytes + r.pairs * sizeof(PairFreq) +
+                            kQkWarps / sh.wpt * r.pairs * sizeof(float2) + kQkWarps * r.hd * sizeof(float);
         static SmemOptIn opt;
-        if (smem > 48 * 1024) {
-            RingShape shape = {};
-            shape.stages = 1;
-            shape.smem = (int)smem;
-            if (cudaError_t e = opt.allow(reinterpret_cast<const void*>(k), shape)) return e;
-        }
-        return launch_pdl(k, (unsigned)(sh.q_blocks + sh.k_blocks), 32 * kQkWarps, smem, s, p, G, sh);
+        if (cudaError_t e = allow_smem(opt, reinterpret_cast<const void*>(k), smem)) return e;
+        return launch_pdl(k, (unsigned)(sh.q_blocks + sh.k_blocks), 32 * kQkWarps, smem, s, p, shape.g, sh);
     });
+}
+
+cudaError_t launch_qk_norm_rope_backward(const QkNormParams& p, bool f32, bool interleaved, int align, ColSumParams sums,
+                                         cudaStream_t s) {
+    const cudaError_t e = interleaved ? backward<true>(p, f32, align, sums, s) : backward<false>(p, f32, align, sums, s);
     if (e != cudaSuccess || !p.ws) return e;
     return launch_column_sums(sums, s);
 }
