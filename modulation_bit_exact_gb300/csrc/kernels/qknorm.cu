@@ -12,26 +12,44 @@
 
 namespace mbx {
 
-QkShare qk_share(int64_t total, int64_t most, int q_heads, int k_heads) {
-    QkShare best = {1, 1, k_heads ? 1 : 0};
+// The cheapest division by a model in steps of a warp (a head of each of its groups):
+// a round of tokens costs its steps and 1.5 more, for the angles and the chain of
+// one token's work, and a quarter for each further token of a warp.
+QkShare qk_share(const RopeParams& r, int64_t most, int groups) {
+    const int64_t total = r.batch * r.tokens;
+    QkShare best = {};
     double cost = 1e30;
     for (int wpt = 1; wpt <= kQkWarps; wpt *= 2) {
-        const int64_t per_block = kQkWarps / wpt, need = (total + per_block - 1) / per_block;
-        int64_t q = k_heads ? most * q_heads / (q_heads + k_heads) : most;
-        q = q < 1 ? 1 : k_heads && q >= most ? most - 1 : q;
-        int64_t k = k_heads ? most - q : 0;
-        if (q > need) q = need;
-        if (k > need) k = need;
-        double c = (double)((need + q - 1) / q) * (1.0 / wpt + 0.1) * q_heads;
-        if (k) {
-            const double ck = (double)((need + k - 1) / k) * (1.0 / wpt + 0.1) * k_heads;
-            if (ck > c) c = ck;
+        auto of = [&](int heads, QkDeal* d) {  // the cost of a token
+            d->tpw = wpt == 1 && heads * 2 <= groups ? groups / heads : 1;
+            const int steps = (heads + groups * wpt - 1) / (groups * wpt);
+            return (steps + 1.5 + 0.25 * (d->tpw - 1)) * wpt / d->tpw;
+        };
+        auto rounds = [&](const QkDeal& d) {
+            const int64_t per = (int64_t)d.blocks * (kQkWarps / wpt) * d.tpw;
+            return (double)((total + per - 1) / per);
+        };
+        auto blocks = [&](QkDeal& d, int64_t share) {
+            const int64_t per = kQkWarps / wpt * d.tpw, need = (total + per - 1) / per;
+            d.blocks = (int)(share < 1 ? 1 : share < need ? share : need);
+        };
+        QkDeal q = {}, k = {};
+        const double cq = of(r.q.heads, &q), ck = r.k.heads ? of(r.k.heads, &k) : 0.0;
+        blocks(q, r.k.heads ? (int64_t)(most * cq / (cq + ck)) : most);
+        double c = rounds(q) * cq * q.tpw / wpt;
+        if (r.k.heads) {
+            blocks(k, most - q.blocks);
+            const double o = rounds(k) * ck * k.tpw / wpt;
+            c = o > c ? o : c;
         }
         if (c < cost) {
             cost = c;
-            best = QkShare{wpt, (int)q, (int)k};
+            best.q = q;
+            best.k = k;
+            best.wpt = wpt;
         }
     }
+    best.by_tokens = make_fastdiv((unsigned)r.tokens);
     return best;
 }
 
@@ -47,19 +65,16 @@ __global__ void __launch_bounds__(32 * kQkWarps, forward_blocks(HeadUnits<T, INT
     constexpr int kStages = forward_stages(U * Head::E * (int)sizeof(T));
     extern __shared__ uint4 smem[];  // [warps][stages] slots, the pairs' frequencies, [tokens of the block][pairs]
     const RopeParams& r = p.rope;
-    const int G = GT ? GT : g, groups = 32 / G, wpt = sh.wpt, per_block = kQkWarps / wpt;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, slot = warp / wpt, share = warp % wpt;
-    const bool which = (int)blockIdx.x >= sh.q_blocks;
-    const int block = which ? blockIdx.x - sh.q_blocks : blockIdx.x, blocks = which ? sh.k_blocks : sh.q_blocks;
-    const RopeTensor& t = which ? r.k : r.q;
+    const int G = GT ? GT : g, groups = 32 / G, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const QkPlace at(sh, r.q.heads, r.k.heads, G, groups);
+    const RopeTensor& t = at.k ? r.k : r.q;
     const unsigned tokens = (unsigned)r.tokens, total = (unsigned)r.batch * tokens;
     const Head head(lane % G, G, r.hd, r.pairs);
     PairFreq* freqs = reinterpret_cast<PairFreq*>(reinterpret_cast<char*>(smem) + kQkWarps * kStages * Head::kSlotBytes);
-    float2* cs = reinterpret_cast<float2*>(freqs + r.pairs) + slot * r.pairs;
-    const int h0 = share * groups + lane / G, step = wpt * groups;
+    float2* cs = reinterpret_cast<float2*>(freqs + r.pairs) + at.slot * at.tpw * r.pairs;
     HeadStream<Head, T, 1, kStages> in(
-        head, (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * Head::kSlotBytes + lane * Head::kAccessBytes,
-        block * per_block + slot, blocks * per_block, tokens, total, h0, lane / G, step, t.heads, lane / G < groups);
+        head, at, (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * Head::kSlotBytes + lane * Head::kAccessBytes, r,
+        t.heads, sh.by_tokens);
     in.tensor(0, t.in, t.ib, t.it, t.ih);
     typename Head::Raw raw[1];
     raw[0].clear();
@@ -68,22 +83,23 @@ __global__ void __launch_bounds__(32 * kQkWarps, forward_blocks(HeadUnits<T, INT
     in.start();
     for (int j = threadIdx.x; j < r.pairs; j += blockDim.x) freqs[j] = pair_freq(r, j);
     __syncthreads();
-    TokenAngles angle(r, freqs, cs, share, wpt);
-    angle.fetch(block * per_block + slot, tokens, total);
-    const typename Head::Values w = head.weight(p.w[which], p.w_f32);
+    TokenAngles angle(r, freqs, cs, at.share, sh.wpt, at.tpw, total, sh.by_tokens);
+    angle.fetch(at.tok - at.sub);
+    const typename Head::Values w = head.weight(p.w[at.k], p.w_f32);
 
     // the same number of rounds for all warps of the block, which may meet in them
+    const unsigned first = at.block * (kQkWarps / sh.wpt) * at.tpw;
 #pragma unroll 1
-    for (unsigned tok0 = block * per_block; tok0 < total; tok0 += blocks * per_block) {
-        const unsigned tok = tok0 + slot, b = tok / tokens, s = tok - b * tokens;
+    for (unsigned round = first, tok = at.tok; round < total; round += at.stride, tok += at.stride) {
+        angle.make(tok - at.sub);
+        angle.fetch(tok - at.sub + at.stride);
+        if (tok - at.sub >= total) continue;
         const bool has = tok < total;
-        angle.make(has);
-        angle.fetch(tok + blocks * per_block, tokens, total);
-        if (!has) continue;
-        const typename Head::Angles angles = head.angles(cs);
-        T* out = static_cast<T*>(t.out) + b * t.ob + s * t.ot + h0 * t.oh;
+        const unsigned b = has ? batch_of(tok, sh.by_tokens) : 0, s = has ? tok - b * tokens : 0;
+        const typename Head::Angles angles = head.angles(cs + at.sub * r.pairs);
+        T* out = static_cast<T*>(t.out) + b * t.ob + s * t.ot + at.h0 * t.oh;
 #pragma unroll 1
-        for (int i = 0; i < in.steps; ++i, out += step * t.oh) {
+        for (int i = 0; i < in.steps; ++i, out += at.step * t.oh) {
             in.take(raw);
             typename Head::Values x = Head::values(raw[0]);
             const float ss = group_sum<GT>(dot(x.first, x.second, x), G);
@@ -98,7 +114,7 @@ __global__ void __launch_bounds__(32 * kQkWarps, forward_blocks(HeadUnits<T, INT
                     x.second[u][j] = mul2(mul2(x.second[u][j], r2), w.second[u][j]);
                 }
             head.turn(x, angles);
-            if (i < in.mine) head.store(out, x);
+            if (has && i < in.mine) head.store(out, x);
         }
     }
 }
@@ -111,14 +127,15 @@ static cudaError_t forward(const QkNormParams& p, bool f32, int align, cudaStrea
     return for_head_shape<16, 8, INTERLEAVED>(shape, f32, [&](auto t, auto inter, auto w, auto u, auto vec, auto gt) {
         using Head = HeadUnits<decltype(t), decltype(inter)::value, decltype(w)::value, decltype(u)::value, decltype(vec)::value>;
         constexpr int kElems = Head::E * decltype(u)::value, kStages = forward_stages(kElems * (int)sizeof(t));
-        const QkShare sh = qk_share(r.batch * r.tokens, forward_blocks(kElems) * (int64_t)sm_count(), r.q.heads, r.k.heads);
+        const QkShare sh = qk_share(r, forward_blocks(kElems) * (int64_t)sm_count(), 32 / shape.g);
         auto* k = qk_norm_rope_kernel<decltype(t), decltype(inter)::value, decltype(w)::value, decltype(u)::value,
                                       decltype(vec)::value, decltype(gt)::value>;
+        const int most = sh.q.tpw > sh.k.tpw ? sh.q.tpw : sh.k.tpw;
         const size_t smem = kQkWarps * kStages * Head::kSlotBytes + r.pairs * sizeof(PairFreq) +
-                            kQkWarps / sh.wpt * r.pairs * sizeof(float2);
+                            kQkWarps / sh.wpt * most * r.pairs * sizeof(float2);
         static SmemOptIn opt;
         if (cudaError_t e = allow_smem(opt, reinterpret_cast<const void*>(k), smem)) return e;
-        return launch_pdl(k, (unsigned)(sh.q_blocks + sh.k_blocks), 32 * kQkWarps, smem, s, p, shape.g, sh);
+        return launch_pdl(k, (unsigned)(sh.q.blocks + sh.k.blocks), 32 * kQkWarps, smem, s, p, shape.g, sh);
     });
 }
 

@@ -394,47 +394,98 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Blocks of kQkWarps warps; `wpt` of them (a power of two) share a token.  Q and K have
-// blocks of their own, in proportion to their heads.
+// How tokens and heads are dealt out.  Blocks of kQkWarps warps; Q and K have blocks of
+// their own.  Either `wpt` warps (a power of two) share a token, or, where a warp has
+// room for the heads of several tokens, it takes `tpw` of them at a time.
 constexpr int kQkWarps = 8;
-struct QkShare {
-    int wpt, q_blocks, k_blocks;
+struct QkDeal {
+    int blocks, tpw;  // of a tensor
 };
-// For `total` tokens and `most` blocks: a block walks tokens, and the fewest rounds of
-// them win, a share of a token's heads counting by its size and a tenth of the token
-// for what every share pays.
-QkShare qk_share(int64_t total, int64_t most, int q_heads, int k_heads);
+struct QkShare {
+    QkDeal q, k;
+    int wpt;
+    FastDiv by_tokens;
+};
+// For `most` blocks and `groups` heads side by side in a warp.
+QkShare qk_share(const RopeParams& r, int64_t most, int groups);
+
+__device__ __forceinline__ unsigned batch_of(unsigned tok, const FastDiv& d) { return (unsigned)((tok * d.m) >> d.shift); }
+
+// What a warp works on: its tokens tok0 + tok, step by step of `stride`, its heads h0,
+// h0 + step, ...  A lane's group has a token and a head of its own where a warp takes
+// several tokens.
+struct QkPlace {
+    bool k;               // of K
+    int block, blocks, tpw, slot, share, sub;
+    unsigned tok, stride;  // of this lane
+    int h0, h_first, step;
+    bool part;            // the lane's group takes part
+    __device__ __forceinline__ QkPlace(const QkShare& sh, int heads_q, int heads_k, int G, int groups) {
+        const int warp = threadIdx.x / 32, group = threadIdx.x % 32 / G;
+        k = (int)blockIdx.x >= sh.q.blocks;
+        block = k ? blockIdx.x - sh.q.blocks : blockIdx.x;
+        blocks = k ? sh.k.blocks : sh.q.blocks;
+        tpw = k ? sh.k.tpw : sh.q.tpw;
+        slot = warp / sh.wpt;
+        share = warp % sh.wpt;
+        const int heads = k ? heads_k : heads_q;
+        sub = tpw > 1 ? group / heads : 0;
+        part = tpw > 1 ? sub < tpw : group < groups;
+        if (!part) sub = 0;
+        h_first = share * groups;
+        h0 = tpw > 1 ? group - sub * heads : h_first + group;
+        step = groups * sh.wpt;
+        const int per_block = kQkWarps / sh.wpt * tpw;
+        tok = block * per_block + slot * tpw + sub;
+        stride = blocks * per_block;
+    }
+};
 
 // The sines and cosines of the tokens that a warp, with the others that share them
-// (this is `id` of `wpt`), walks.  A lane has pairs `first`, first + gap, ...; the
-// positions of the next token are fetched while this one's heads are worked on.
+// (this is `id` of `wpt`), walks: `tpw` tokens' pairs, [tpw][pairs].  Of a single token
+// the next one's positions are fetched while this one's heads are worked on.
 struct TokenAngles {
     static constexpr int kMost = 4;  // pairs of a lane: 128 of a head
     const RopeParams& r;
     const PairFreq* freqs;
     float2* cs;
-    int wpt, first, gap;
+    const FastDiv& by_tokens;
+    int wpt, tpw, first, gap;
+    unsigned total;
     uint32_t pos[kMost];
-    __device__ __forceinline__ TokenAngles(const RopeParams& r_, const PairFreq* freqs_, float2* cs_, int id, int wpt_)
-        : r(r_), freqs(freqs_), cs(cs_), wpt(wpt_), first(id * 32 + threadIdx.x % 32), gap(32 * wpt_) {}
+    __device__ __forceinline__ TokenAngles(const RopeParams& r_, const PairFreq* freqs_, float2* cs_, int id, int wpt_, int tpw_,
+                                           unsigned total_, const FastDiv& d)
+        : r(r_), freqs(freqs_), cs(cs_), by_tokens(d), wpt(wpt_), tpw(tpw_), first(id * 32 + threadIdx.x % 32), gap(32 * wpt_),
+          total(total_) {}
     __device__ __forceinline__ void meet() const {
         if (wpt == 1) __syncwarp();
         else if (wpt == kQkWarps) __syncthreads();
         else named_bar(1 + threadIdx.x / 32 / wpt, wpt * 32);
     }
-    __device__ __forceinline__ void fetch(unsigned tok, unsigned tokens, unsigned total) {
-        if (tok >= total) return;
-        const unsigned s = tok % tokens;
+    __device__ __forceinline__ uint32_t position(unsigned tok, int j) const {
+        return position_bits(r, tok, tok - batch_of(tok, by_tokens) * (unsigned)r.tokens, freqs[j].axis);
+    }
+    __device__ __forceinline__ void fetch(unsigned tok) {
+        if (tpw > 1 || tok >= total) return;
 #pragma unroll
         for (int k = 0; k < kMost; ++k)
-            if (first + k * gap < r.pairs) pos[k] = position_bits(r, tok, s, freqs[first + k * gap].axis);
+            if (first + k * gap < r.pairs) pos[k] = position(tok, first + k * gap);
     }
-    __device__ __forceinline__ void make(bool has) const {
-        meet();  // the token before has been read
-        if (has) {
+    // of tokens tok .. tok + tpw - 1, those that there are
+    __device__ __forceinline__ void make(unsigned tok) const {
+        meet();  // the tokens before have been read
+        if (tpw == 1) {
+            if (tok < total) {
 #pragma unroll
-            for (int k = 0; k < kMost; ++k)
-                if (first + k * gap < r.pairs) cs[first + k * gap] = pair_angle(r, freqs[first + k * gap], pos[k]);
+                for (int k = 0; k < kMost; ++k)
+                    if (first + k * gap < r.pairs) cs[first + k * gap] = pair_angle(r, freqs[first + k * gap], pos[k]);
+            }
+        } else {
+            int sub = 0, j = first;
+            for (int e = first; e < tpw * r.pairs; e += gap, j += gap) {
+                while (j >= r.pairs) j -= r.pairs, ++sub;
+                if (tok + sub < total) cs[e] = pair_angle(r, freqs[j], position(tok + sub, j));
+            }
         }
         meet();
     }
@@ -448,21 +499,22 @@ struct TokenAngles {
 template <class Head, class T, int N, int kStages>
 struct HeadStream {
     const Head& head;
+    const QkPlace& place;
+    const FastDiv& by_tokens;
     const T* base[N];
     int64_t sb[N], st[N], sh[N];
     const T* at[N];
     uint32_t ring;  // this lane's places in the warp's slots
-    unsigned tok, stride, tokens, total;
-    int i, steps, step, mine;  // step of the token, steps of a token, heads between steps, steps with a head of this lane
-    int fill, drain;           // slots
-    int64_t first;             // the lane's first head
-    __device__ __forceinline__ HeadStream(const Head& hd, uint32_t ring_, unsigned tok_, unsigned stride_, unsigned tokens_,
-                                          unsigned total_, int h0, int group, int step_, int heads,
-                                          bool takes_part)
-        : head(hd), ring(ring_), tok(tok_), stride(stride_), tokens(tokens_), total(total_), i(0), step(step_), fill(0),
-          drain(0), first(h0) {
-        steps = heads > h0 - group ? (heads - (h0 - group) + step - 1) / step : 0;
-        mine = heads > h0 && takes_part ? (heads - h0 + step - 1) / step : 0;
+    unsigned tok, tokens, total;
+    int i, steps, mine;  // step of the token, steps of a token, steps with a head of this lane
+    int fill, drain;     // slots
+    __device__ __forceinline__ HeadStream(const Head& hd, const QkPlace& pl, uint32_t ring_, const RopeParams& r, int heads,
+                                          const FastDiv& d)
+        : head(hd), place(pl), by_tokens(d), ring(ring_), tok(pl.tok), tokens((unsigned)r.tokens),
+          total((unsigned)(r.batch * r.tokens)), i(0), fill(0), drain(0) {
+        auto in_steps = [&](int from) { return heads > from ? (heads - from + pl.step - 1) / pl.step : 0; };
+        steps = in_steps(pl.h_first);
+        mine = pl.part ? in_steps(pl.h0) : 0;
     }
     __device__ __forceinline__ void tensor(int k, const void* p, int64_t b, int64_t t, int64_t h) {
         base[k] = static_cast<const T*>(p);
@@ -470,18 +522,18 @@ struct HeadStream {
     }
     __device__ __forceinline__ void aim() {
         if (tok >= total) return;
-        const unsigned b = tok / tokens;
+        const unsigned b = batch_of(tok, by_tokens);
 #pragma unroll
-        for (int k = 0; k < N; ++k) at[k] = base[k] + b * sb[k] + (tok - b * tokens) * st[k] + first * sh[k];
+        for (int k = 0; k < N; ++k) at[k] = base[k] + b * sb[k] + (tok - b * tokens) * st[k] + place.h0 * sh[k];
     }
     __device__ __forceinline__ void next() {
         if (++i == steps) {
             i = 0;
-            tok += stride;
+            tok += place.stride;
             aim();
         } else {
 #pragma unroll
-            for (int k = 0; k < N; ++k) at[k] += step * sh[k];
+            for (int k = 0; k < N; ++k) at[k] += place.step * sh[k];
         }
     }
     __device__ __forceinline__ void fetch() {
@@ -512,11 +564,13 @@ struct HeadStream {
             for (int k = 0; k < N; ++k) head.read(r[k], ring + (drain * N + k) * Head::kSlotBytes);
             drain = drain + 1 == kStages ? 0 : drain + 1;
         } else {
-            if (i < mine) {
+            if (tok < total) {
+                if (i < mine) {
 #pragma unroll
-                for (int k = 0; k < N; ++k) head.load(r[k], at[k]);
+                    for (int k = 0; k < N; ++k) head.load(r[k], at[k]);
+                }
+                next();
             }
-            next();
         }
     }
 };

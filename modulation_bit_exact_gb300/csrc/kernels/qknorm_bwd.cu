@@ -22,24 +22,19 @@ __global__ void __launch_bounds__(32 * kQkWarps, grad_blocks(HeadUnits<T, INTERL
     qk_norm_rope_bwd_kernel(QkNormParams p, int g, QkShare sh) {
     using Head = HeadUnits<T, INTERLEAVED, W, U, VEC>;
     constexpr int E = Head::E, NP = Head::NP, kStages = grad_stages(U * E * (int)sizeof(T));
-    extern __shared__ uint4 smem[];  // [warps][stages][2] slots, the pairs' frequencies, [tokens of the block][pairs], [warps][hd] sums
+    extern __shared__ uint4 smem[];  // [warps][stages][2] slots, the pairs' frequencies, [tokens of the block][pairs]
     const RopeParams& r = p.rope;
-    const int G = GT ? GT : g, groups = 32 / G, hd = r.hd, wpt = sh.wpt, per_block = kQkWarps / wpt;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, slot = warp / wpt, share = warp % wpt;
-    const bool which = (int)blockIdx.x >= sh.q_blocks;
-    const int block = which ? blockIdx.x - sh.q_blocks : blockIdx.x, blocks = which ? sh.k_blocks : sh.q_blocks;
-    const RopeTensor& t = which ? r.k : r.q;
-    const GradIn& d = p.dout[which];
+    const int G = GT ? GT : g, groups = 32 / G, hd = r.hd, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const QkPlace at(sh, r.q.heads, r.k.heads, G, groups);
+    const RopeTensor& t = at.k ? r.k : r.q;
+    const GradIn& d = p.dout[at.k];
     const unsigned tokens = (unsigned)r.tokens, total = (unsigned)r.batch * tokens;
     const Head head(lane % G, G, hd, r.pairs);
     PairFreq* freqs = reinterpret_cast<PairFreq*>(reinterpret_cast<char*>(smem) + kQkWarps * kStages * 2 * Head::kSlotBytes);
-    float2* cs_all = reinterpret_cast<float2*>(freqs + r.pairs);
-    float2* cs = cs_all + slot * r.pairs;
-    float* sums = reinterpret_cast<float*>(cs_all + per_block * r.pairs);
-    const int h0 = share * groups + lane / G, step = wpt * groups;
+    float2* cs = reinterpret_cast<float2*>(freqs + r.pairs) + at.slot * at.tpw * r.pairs;
     HeadStream<Head, T, 2, kStages> in(
-        head, (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * 2 * Head::kSlotBytes + lane * Head::kAccessBytes,
-        block * per_block + slot, blocks * per_block, tokens, total, h0, lane / G, step, t.heads, lane / G < groups);
+        head, at, (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * 2 * Head::kSlotBytes + lane * Head::kAccessBytes, r,
+        t.heads, sh.by_tokens);
     in.tensor(0, t.in, t.ib, t.it, t.ih);
     in.tensor(1, d.in, d.ib, d.it, d.ih);
     typename Head::Raw raw[2];
@@ -50,9 +45,9 @@ __global__ void __launch_bounds__(32 * kQkWarps, grad_blocks(HeadUnits<T, INTERL
     in.start();
     for (int j = threadIdx.x; j < r.pairs; j += blockDim.x) freqs[j] = pair_freq(r, j);
     __syncthreads();
-    TokenAngles angle(r, freqs, cs, share, wpt);
-    angle.fetch(block * per_block + slot, tokens, total);
-    const typename Head::Values w = head.weight(p.w[which], p.w_f32);
+    TokenAngles angle(r, freqs, cs, at.share, sh.wpt, at.tpw, total, sh.by_tokens);
+    angle.fetch(at.tok - at.sub);
+    const typename Head::Values w = head.weight(p.w[at.k], p.w_f32);
     typename Head::Values acc;
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -60,19 +55,20 @@ __global__ void __launch_bounds__(32 * kQkWarps, grad_blocks(HeadUnits<T, INTERL
         for (int j = 0; j < NP; ++j) acc.first[u][j] = acc.second[u][j] = 0;
 
     // the same number of rounds for all warps of the block, which may meet in them
+    const unsigned first = at.block * (kQkWarps / sh.wpt) * at.tpw;
 #pragma unroll 1
-    for (unsigned tok0 = block * per_block; tok0 < total; tok0 += blocks * per_block) {
-        const unsigned tok = tok0 + slot, b = tok / tokens, s = tok - b * tokens;
+    for (unsigned round = first, tok = at.tok; round < total; round += at.stride, tok += at.stride) {
+        angle.make(tok - at.sub);
+        angle.fetch(tok - at.sub + at.stride);
+        if (tok - at.sub >= total) continue;
         const bool has = tok < total;
-        angle.make(has);
-        angle.fetch(tok + blocks * per_block, tokens, total);
-        if (!has) continue;
-        const typename Head::Angles angles = head.angles(cs);
-        T* out = static_cast<T*>(t.out) + b * t.ob + s * t.ot + h0 * t.oh;
+        const unsigned b = has ? batch_of(tok, sh.by_tokens) : 0, s = has ? tok - b * tokens : 0;
+        const typename Head::Angles angles = head.angles(cs + at.sub * r.pairs);
+        T* out = static_cast<T*>(t.out) + b * t.ob + s * t.ot + at.h0 * t.oh;
 #pragma unroll 1
-        for (int i = 0; i < in.steps; ++i, out += step * t.oh) {
+        for (int i = 0; i < in.steps; ++i, out += at.step * t.oh) {
             in.take(raw);
-            const bool real = i < in.mine;
+            const bool real = has && i < in.mine;
             typename Head::Values x = Head::values(raw[0]), gr = Head::values(raw[1]), gy;
             head.turn(gr, angles);
 #pragma unroll
@@ -104,6 +100,8 @@ __global__ void __launch_bounds__(32 * kQkWarps, grad_blocks(HeadUnits<T, INTERL
         }
     }
     if (!p.ws) return;
+    float* sums = reinterpret_cast<float*>(smem);  // [warps][hd], in the slots' place
+    __syncthreads();
     // the warp's groups side by side, then the block's warps in order
     float a[U][E];
     Head::unpack(a, acc);
@@ -125,14 +123,14 @@ __global__ void __launch_bounds__(32 * kQkWarps, grad_blocks(HeadUnits<T, INTERL
         }
     }
     __syncthreads();
-    const bool alone = block >= (which ? sh.q_blocks : sh.k_blocks);  // the other tensor has no such block
+    const bool alone = at.block >= (at.k ? sh.q.blocks : sh.k.blocks);  // the other tensor has no such block
     for (int e = threadIdx.x; e < hd; e += blockDim.x) {
         float v = 0.0f;
 #pragma unroll
         for (int i = 0; i < kQkWarps; ++i) v += sums[i * hd + e];
-        float* part = p.ws + (int64_t)block * 2 * hd + e;
-        part[which * hd] = v;
-        if (alone) part[!which * hd] = 0.0f;
+        float* part = p.ws + (int64_t)at.block * 2 * hd + e;
+        part[at.k * hd] = v;
+        if (alone) part[!at.k * hd] = 0.0f;
     }
 }
 
@@ -152,15 +150,17 @@ static cudaError_t backward(const QkNormParams& p, bool f32, int align, ColSumPa
     return for_head_shape<8, kWidest, INTERLEAVED>(shape, f32, [&](auto t, auto inter, auto w, auto u, auto vec, auto gt) {
         using Head = HeadUnits<decltype(t), decltype(inter)::value, decltype(w)::value, decltype(u)::value, decltype(vec)::value>;
         constexpr int kElems = Head::E * decltype(u)::value, kStages = grad_stages(kElems * (int)sizeof(t));
-        const QkShare sh = qk_share(r.batch * r.tokens, grad_blocks(kElems) * (int64_t)sm_count(), r.q.heads, r.k.heads);
-        sums.parts = sh.q_blocks > sh.k_blocks ? sh.q_blocks : sh.k_blocks;
+        const QkShare sh = qk_share(r, grad_blocks(kElems) * (int64_t)sm_count(), 32 / shape.g);
+        sums.parts = sh.q.blocks > sh.k.blocks ? sh.q.blocks : sh.k.blocks;
         auto* k = qk_norm_rope_bwd_kernel<decltype(t), decltype(inter)::value, decltype(w)::value, decltype(u)::value,
                                           decltype(vec)::value, decltype(gt)::value>;
-        const size_t smem = kQkWarps * kStages * 2 * Head::kSlotBytes + r.pairs * sizeof(PairFreq) +
-                            kQkWarps / sh.wpt * r.pairs * sizeof(float2) + kQkWarps * r.hd * sizeof(float);
+        const int most = sh.q.tpw > sh.k.tpw ? sh.q.tpw : sh.k.tpw;
+        size_t smem = kQkWarps * kStages * 2 * Head::kSlotBytes + r.pairs * sizeof(PairFreq) +
+                      kQkWarps / sh.wpt * most * r.pairs * sizeof(float2);
+        if (smem < kQkWarps * r.hd * sizeof(float)) smem = kQkWarps * r.hd * sizeof(float);  // the sums
         static SmemOptIn opt;
         if (cudaError_t e = allow_smem(opt, reinterpret_cast<const void*>(k), smem)) return e;
-        return launch_pdl(k, (unsigned)(sh.q_blocks + sh.k_blocks), 32 * kQkWarps, smem, s, p, shape.g, sh);
+        return launch_pdl(k, (unsigned)(sh.q.blocks + sh.k.blocks), 32 * kQkWarps, smem, s, p, shape.g, sh);
     });
 }
 

@@ -329,3 +329,51 @@ def test_autograd_function(mbx):
         (dx, tx), (dw, tw) = hr.norm_rope_backward(do, x, w, pos, axes, fr, True, EPS)
         tr.assert_close(gx, dx, tx)
         tr.assert_close(gw, dw, tw)
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("hq,hk", [(1, 1), (2, 1), (3, 1), (4, 3), (5, 2), (32, 1)])
+@pytest.mark.parametrize("hd,axes", [(32, (32,)), (64, (16, 24, 24)), (80, (40,)), (72, (24, 24, 24)), (128, (44, 42, 42))])
+def test_few_heads(mbx, hd, axes, hq, hk, interleaved):
+    """A warp takes several tokens where they have few heads; the last round's tokens are not whole; a batch's
+    end inside a warp's tokens; K alone in the work of a block."""
+    g = gen(hd + hq)
+    fr = mbx.rope_axis_freqs(axes)
+    w = rnd(g, (hd,), F32, 0.1, 1.0)
+    for B, S in ((1, 2), (3, 7), (2, 1501), (1, 20011 if hd == 64 else 3)):
+        q, k = case(g, B, S, hq, hk, hd, BF, "merged")
+        dq, dk = rnd(g, q.shape, BF, 0.1), rnd(g, k.shape, BF, 0.1)
+        pos = torch.randint(-50, 200, (B, S, len(axes)), generator=g).int()
+        out = mbx.qk_norm_rope(q, k, w, w, pos.to(DEV), fr, axes, interleaved, EPS)
+        got = mbx.qk_norm_rope_backward(dq, dk, q, k, w, w, pos.to(DEV), fr, axes, interleaved, EPS)
+        for i, (do, x) in enumerate(((dq, q), (dk, k))):
+            tr.assert_close(out[i], *hr.norm_rope(x, w, pos, axes, fr, interleaved, EPS), what=f"{i} {B, S}")
+            (dx, tx), (dw, tw) = hr.norm_rope_backward(do, x, w, pos, axes, fr, interleaved, EPS)
+            tr.assert_close(got[i], dx, tx, what=f"dx {i} {B, S}")
+            tr.assert_close(got[2 + i], dw, tw, what=f"dw {i} {B, S}")
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_angles(mbx, interleaved):
+    """Far, fractional, tiny and negative positions; frequencies above a turn, negative, tiny and zero."""
+    g = gen(50)
+    n = 32
+    fr = torch.cat([torch.tensor([1.0, -1.0, 0.0, 7.5, 50.0, 1e-9, 1e-300, -3.3e5, 2.0 ** 40, 1e-320], dtype=torch.float64),
+                    torch.rand(n - 10, generator=g, dtype=torch.float64) * 4])
+    whole = torch.tensor([0, 1, -1, 12345, 2 ** 31 - 1, -2 ** 31, 99, -7, 1 << 30, 1000003], dtype=torch.int32)
+    part = torch.tensor([0.0, -0.0, 0.7109375, -1234.56, 1e-12, 1e-40, 3e7, -5.5, 1e9, 16777216.0], dtype=torch.float32)
+    q = rnd(g, (1, 10, 2, 2 * n), F32)
+    for pos in (whole[:, None], part[:, None]):
+        out, _ = mbx.qk_norm_rope(q, None, None, None, pos.to(DEV), fr.to(DEV), (2 * n,), interleaved, EPS)
+        want, tol = hr.norm_rope(q, None, pos, (2 * n,), fr, interleaved, EPS)
+        # the reference's own angle: its product is rounded once, to 2^-53 of it
+        ang = (tr.d(pos) * fr).abs()[None, :, None]
+        slack = (ang * 2.0 ** -53).repeat_interleave(2, -1) if interleaved else torch.cat([ang, ang], -1) * 2.0 ** -53
+        big = q.abs().amax().double().cpu() * 4
+        keep = (slack < 1e-3).expand_as(want)
+        err = (tr.d(out) - want).abs()
+        assert (err <= tol * 2 + slack * big + 1e-30)[keep].all()
+    for bad in (float("inf"), float("nan")):
+        pos = torch.tensor([[0.0], [bad], [2.0]], device=DEV)
+        o, _ = mbx.qk_norm_rope(q[:, :3], None, None, None, pos, fr.to(DEV), (2 * n,), interleaved, EPS)
+        assert o[0, 1].isnan().all() and not o[0, [0, 2]].isnan().any()
