@@ -2,7 +2,8 @@
 // several axes, in one pass:
 //   n = x * rstd * w,  rstd = 1 / sqrt(mean(x^2) + eps) over the head,
 //   out = the pairs of n turned as in rope.cu; elements past the pairs pass.
-// binary32, one rounding at the output.
+// binary32, one rounding at the output: w goes into a token's cosines and sines, once,
+// and rstd follows the turn.
 //
 // A warp walks tokens, of Q or of K, or a share of their heads where that divides
 // the tokens better: with the other warps of a token it computes the sines and cosines,
@@ -13,7 +14,7 @@
 namespace mbx {
 
 // The cheapest division by a model in steps of a warp (a head of each of its groups):
-// a round of tokens costs its steps and 1.5 more, for the angles and the chain of
+// a round of tokens costs its steps and 2.5 more, for the angles and the chain of
 // one token's work, and a quarter for each further token of a warp.
 QkShare qk_share(const RopeParams& r, int64_t most, int groups) {
     const int64_t total = r.batch * r.tokens;
@@ -23,7 +24,7 @@ QkShare qk_share(const RopeParams& r, int64_t most, int groups) {
         auto of = [&](int heads, QkDeal* d) {  // the cost of a token
             d->tpw = wpt == 1 && heads * 2 <= groups ? groups / heads : 1;
             const int steps = (heads + groups * wpt - 1) / (groups * wpt);
-            return (steps + 1.5 + 0.25 * (d->tpw - 1)) * wpt / d->tpw;
+            return (steps + 2.5 + 0.25 * (d->tpw - 1)) * wpt / d->tpw;
         };
         auto rounds = [&](const QkDeal& d) {
             const int64_t per = (int64_t)d.blocks * (kQkWarps / wpt) * d.tpw;
@@ -53,13 +54,11 @@ QkShare qk_share(const RopeParams& r, int64_t most, int groups) {
     return best;
 }
 
-// Blocks of an SM, by the elements of a head that a lane holds: what the registers allow.
 // Heads on their way to a lane: as many as make 96 bytes.
-constexpr int forward_blocks(int elems) { return elems <= 8 ? 3 : 2; }
 constexpr int forward_stages(int bytes) { return 96 / bytes < 2 ? 2 : 96 / bytes; }
 
 template <class T, bool INTERLEAVED, int W, int U, bool VEC, int GT>
-__global__ void __launch_bounds__(32 * kQkWarps, forward_blocks(HeadUnits<T, INTERLEAVED, W, U, VEC>::E * U))
+__global__ void __launch_bounds__(32 * kQkWarps, kQkBlocks)
     qk_norm_rope_kernel(QkNormParams p, int g, QkShare sh) {
     using Head = HeadUnits<T, INTERLEAVED, W, U, VEC>;
     constexpr int kStages = forward_stages(U * Head::E * (int)sizeof(T));
@@ -96,7 +95,7 @@ __global__ void __launch_bounds__(32 * kQkWarps, forward_blocks(HeadUnits<T, INT
         if (tok - at.sub >= total) continue;
         const bool has = tok < total;
         const unsigned b = has ? batch_of(tok, sh.by_tokens) : 0, s = has ? tok - b * tokens : 0;
-        const typename Head::Angles angles = head.angles(cs + at.sub * r.pairs);
+        const typename Head::Turn turn = head.turn_of(cs + at.sub * r.pairs, w);
         T* out = static_cast<T*>(t.out) + b * t.ob + s * t.ot + at.h0 * t.oh;
 #pragma unroll 1
         for (int i = 0; i < in.steps; ++i, out += at.step * t.oh) {
@@ -106,14 +105,14 @@ __global__ void __launch_bounds__(32 * kQkWarps, forward_blocks(HeadUnits<T, INT
             in.fetch();
             const float rstd = rsqrtf(__fmaf_rn(ss, p.inv_hd, p.eps));
             const u64 r2 = f2(rstd, rstd);
+            head.turn(x, turn);
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int j = 0; j < Head::NP; ++j) {
-                    x.first[u][j] = mul2(mul2(x.first[u][j], r2), w.first[u][j]);
-                    x.second[u][j] = mul2(mul2(x.second[u][j], r2), w.second[u][j]);
+                    x.first[u][j] = mul2(x.first[u][j], r2);
+                    x.second[u][j] = mul2(x.second[u][j], r2);
                 }
-            head.turn(x, angles);
             if (has && i < in.mine) head.store(out, x);
         }
     }
@@ -126,8 +125,8 @@ static cudaError_t forward(const QkNormParams& p, bool f32, int align, cudaStrea
     const HeadShape shape = head_shape<16, 8>(r.hd, r.pairs, f32, INTERLEAVED, align);
     return for_head_shape<16, 8, INTERLEAVED>(shape, f32, [&](auto t, auto inter, auto w, auto u, auto vec, auto gt) {
         using Head = HeadUnits<decltype(t), decltype(inter)::value, decltype(w)::value, decltype(u)::value, decltype(vec)::value>;
-        constexpr int kElems = Head::E * decltype(u)::value, kStages = forward_stages(kElems * (int)sizeof(t));
-        const QkShare sh = qk_share(r, forward_blocks(kElems) * (int64_t)sm_count(), 32 / shape.g);
+        constexpr int kStages = forward_stages(Head::E * decltype(u)::value * (int)sizeof(t));
+        const QkShare sh = qk_share(r, kQkBlocks * (int64_t)sm_count(), 32 / shape.g);
         auto* k = qk_norm_rope_kernel<decltype(t), decltype(inter)::value, decltype(w)::value, decltype(u)::value,
                                       decltype(vec)::value, decltype(gt)::value>;
         const int most = sh.q.tpw > sh.k.tpw ? sh.q.tpw : sh.k.tpw;

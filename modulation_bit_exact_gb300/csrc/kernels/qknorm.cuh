@@ -127,12 +127,12 @@ struct Access1 {
                     if constexpr (W > 1) st_u16(p + 2 * i + 1, (uint16_t)(w[i] >> 16));
                 }
             }
-        } else if constexpr (NW == 4) {
-            st_v4(p, make_uint4(w[0], w[1], w[2], w[3]));
+        } else if constexpr (NW == 4) {  // streamed: 32760 x 80 heads of 128, 219 -> 208 us
+            asm volatile("st.global.cs.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
         } else if constexpr (NW == 2) {
-            st_v2(p, w[0], w[1]);
+            asm volatile("st.global.cs.v2.u32 [%0], {%1,%2};" ::"l"(p), "r"(w[0]), "r"(w[1]) : "memory");
         } else {
-            asm volatile("st.global.u32 [%0], %1;" ::"l"(p), "r"(w[0]) : "memory");
+            asm volatile("st.global.cs.u32 [%0], %1;" ::"l"(p), "r"(w[0]) : "memory");
         }
     }
     __device__ __forceinline__ void widen(float* f) const {
@@ -312,40 +312,65 @@ struct HeadUnits {
             }
         return pack(f);
     }
-    struct Angles {
-        u64 c[U][NP], s[U][NP];
+    // What turns a token's pairs: of (x0, x1) the first result is x0*a + x1*b, the second
+    // x0*c + x1*d.
+    struct Turn {
+        u64 a[U][NP], b[U][NP], c[U][NP], d[U][NP];
     };
-    // This lane's cosines and sines out of those of the token's n pairs.
-    __device__ __forceinline__ Angles angles(const float2* cs) const {
-        Angles a;
+    // The rotation by the cosines and sines of the token's n pairs, out of cs, of values
+    // that are multiplied by w first.
+    __device__ __forceinline__ Turn turn_of(const float2* cs, const Values& w) const {
+        Turn t;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 const float2 x = 2 * i < turns[u] ? cs[pair0[u] + 2 * i] : make_float2(1.0f, 0.0f);
                 const float2 y = 2 * i + 1 < turns[u] ? cs[pair0[u] + 2 * i + 1] : make_float2(1.0f, 0.0f);
-                a.c[u][i] = f2(x.x, y.x);
-                a.s[u][i] = f2(x.y, y.y);
+                const u64 co = f2(x.x, y.x), si = f2(x.y, y.y);
+                t.a[u][i] = mul2(w.first[u][i], co);
+                t.b[u][i] = mul2(w.second[u][i], f2(-x.y, -y.y));
+                t.c[u][i] = mul2(w.first[u][i], si);
+                t.d[u][i] = mul2(w.second[u][i], co);
             }
-        return a;
+        return t;
     }
-    // Turns the pairs: each result one product and one fused multiply-add.
-    __device__ __forceinline__ void turn(Values& v, const Angles& a) const {
-        constexpr u64 kMinus = 0x8000000080000000ull;
+    // The rotation alone, a = d and c = -b.
+    struct Rotation {
+        u64 a[U][NP], b[U][NP], c[U][NP];
+    };
+    __device__ __forceinline__ Rotation rotation(const float2* cs) const {
+        Rotation t;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                const u64 x0 = v.first[u][i], x1 = v.second[u][i];
-                v.first[u][i] = fma2(x1 ^ kMinus, a.s[u][i], mul2(x0, a.c[u][i]));
-                v.second[u][i] = fma2(x0, a.s[u][i], mul2(x1, a.c[u][i]));
+                const float2 x = 2 * i < turns[u] ? cs[pair0[u] + 2 * i] : make_float2(1.0f, 0.0f);
+                const float2 y = 2 * i + 1 < turns[u] ? cs[pair0[u] + 2 * i + 1] : make_float2(1.0f, 0.0f);
+                t.a[u][i] = f2(x.x, y.x);
+                t.b[u][i] = f2(-x.y, -y.y);
+                t.c[u][i] = f2(x.y, y.y);
+            }
+        return t;
+    }
+    static __device__ __forceinline__ u64 second_factor(const Turn& t, int u, int i) { return t.d[u][i]; }
+    static __device__ __forceinline__ u64 second_factor(const Rotation& t, int u, int i) { return t.a[u][i]; }
+    template <class R>
+    __device__ __forceinline__ void turn(Values& v, const R& t) const {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const u64 x0 = v.first[u][i], x1 = v.second[u][i], y0 = mul2(x0, t.a[u][i]), y1 = mul2(x1, second_factor(t, u, i));
+                v.first[u][i] = fma2(x1, t.b[u][i], y0);
+                v.second[u][i] = fma2(x0, t.c[u][i], y1);
                 if (!all_turn) {  // an infinite partner does not reach an element that passes
                     auto keep = [&](u64& now, u64 was) {
                         if (2 * i >= turns[u]) now = (now & 0xffffffff00000000ull) | (was & 0xffffffffull);
                         if (2 * i + 1 >= turns[u]) now = (now & 0xffffffffull) | (was & 0xffffffff00000000ull);
                     };
-                    keep(v.first[u][i], x0);
-                    keep(v.second[u][i], x1);
+                    keep(v.first[u][i], y0);
+                    keep(v.second[u][i], y1);
                 }
             }
     }
@@ -390,6 +415,28 @@ __device__ __forceinline__ float group_sum(float v, int G) {
     }
 }
 
+// Two sums at once: the lanes of a pair take one each, and exchange them at the end.
+template <int GT>
+__device__ __forceinline__ void group_sums(float& a, float& b, int G) {
+    const int g = GT ? GT : G;
+    if ((g & (g - 1)) != 0 || g < 4) {
+        a = group_sum<GT>(a, G);
+        b = group_sum<GT>(b, G);
+        return;
+    }
+    const bool odd = threadIdx.x & 1;
+    float v = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+    if constexpr (GT > 0) {
+#pragma unroll
+        for (int m = 2; m < GT; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    } else {
+        for (int m = 2; m < g; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    }
+    const float o = __shfl_xor_sync(0xffffffffu, v, 1);
+    a = odd ? o : v;
+    b = odd ? v : o;
+}
+
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -397,7 +444,7 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_grou
 // How tokens and heads are dealt out.  Blocks of kQkWarps warps; Q and K have blocks of
 // their own.  Either `wpt` warps (a power of two) share a token, or, where a warp has
 // room for the heads of several tokens, it takes `tpw` of them at a time.
-constexpr int kQkWarps = 8;
+constexpr int kQkWarps = 8, kQkBlocks = 2;  // two blocks an SM: with a third the 80 registers a thread spill
 struct QkDeal {
     int blocks, tpw;  // of a tensor
 };
@@ -422,8 +469,11 @@ struct QkPlace {
     bool part;            // the lane's group takes part
     __device__ __forceinline__ QkPlace(const QkShare& sh, int heads_q, int heads_k, int G, int groups) {
         const int warp = threadIdx.x / 32, group = threadIdx.x % 32 / G;
-        k = (int)blockIdx.x >= sh.q.blocks;
-        block = k ? blockIdx.x - sh.q.blocks : blockIdx.x;
+        // the blocks of K are spread evenly among those of Q (gradients of 2 x 4352 x
+        // (24 + 24) heads of 128: 66 us with K's after Q's, 60 so)
+        const unsigned all = sh.q.blocks + sh.k.blocks, k_before = blockIdx.x * sh.k.blocks / all;
+        k = (blockIdx.x + 1) * sh.k.blocks / all > k_before;
+        block = k ? k_before : blockIdx.x - k_before;
         blocks = k ? sh.k.blocks : sh.q.blocks;
         tpw = k ? sh.k.tpw : sh.q.tpw;
         slot = warp / sh.wpt;
@@ -498,55 +548,58 @@ struct TokenAngles {
 // nothing.
 template <class Head, class T, int N, int kStages>
 struct HeadStream {
+    static constexpr uint32_t kRound = kStages * N * Head::kSlotBytes;
     const Head& head;
     const QkPlace& place;
     const FastDiv& by_tokens;
-    const T* base[N];
+    const void* base[N];
     int64_t sb[N], st[N], sh[N];
     const T* at[N];
-    uint32_t ring;  // this lane's places in the warp's slots
+    int64_t ahead[N];     // elements from a step's head to the next one's
+    uint32_t ring;        // this lane's places in the warp's slots
+    uint32_t fill, drain;  // the slots in turn, in bytes
     unsigned tok, tokens, total;
     int i, steps, mine;  // step of the token, steps of a token, steps with a head of this lane
-    int fill, drain;     // slots
     __device__ __forceinline__ HeadStream(const Head& hd, const QkPlace& pl, uint32_t ring_, const RopeParams& r, int heads,
                                           const FastDiv& d)
-        : head(hd), place(pl), by_tokens(d), ring(ring_), tok(pl.tok), tokens((unsigned)r.tokens),
-          total((unsigned)(r.batch * r.tokens)), i(0), fill(0), drain(0) {
+        : head(hd), place(pl), by_tokens(d), ring(ring_), fill(0), drain(0), tok(pl.tok), tokens((unsigned)r.tokens),
+          total((unsigned)(r.batch * r.tokens)), i(0) {
         auto in_steps = [&](int from) { return heads > from ? (heads - from + pl.step - 1) / pl.step : 0; };
         steps = in_steps(pl.h_first);
         mine = pl.part ? in_steps(pl.h0) : 0;
+        if (steps == 0) tok = total;  // nothing to fetch
     }
     __device__ __forceinline__ void tensor(int k, const void* p, int64_t b, int64_t t, int64_t h) {
-        base[k] = static_cast<const T*>(p);
+        base[k] = p;
         sb[k] = b, st[k] = t, sh[k] = h;
+        ahead[k] = place.step * h;
     }
     __device__ __forceinline__ void aim() {
         if (tok >= total) return;
         const unsigned b = batch_of(tok, by_tokens);
 #pragma unroll
-        for (int k = 0; k < N; ++k) at[k] = base[k] + b * sb[k] + (tok - b * tokens) * st[k] + place.h0 * sh[k];
+        for (int k = 0; k < N; ++k) at[k] = static_cast<const T*>(base[k]) + b * sb[k] + (tok - b * tokens) * st[k] + place.h0 * sh[k];
     }
     __device__ __forceinline__ void next() {
+#pragma unroll
+        for (int k = 0; k < N; ++k) at[k] += ahead[k];
         if (++i == steps) {
             i = 0;
             tok += place.stride;
             aim();
-        } else {
-#pragma unroll
-            for (int k = 0; k < N; ++k) at[k] += place.step * sh[k];
         }
     }
     __device__ __forceinline__ void fetch() {
         if constexpr (Head::kRing) {
-            if (steps && tok < total) {
+            if (tok < total) {
                 if (i < mine) {
 #pragma unroll
-                    for (int k = 0; k < N; ++k) head.copy(ring + (fill * N + k) * Head::kSlotBytes, at[k]);
+                    for (int k = 0; k < N; ++k) head.copy(ring + fill + k * Head::kSlotBytes, at[k]);
                 }
                 next();
             }
             copies_commit();
-            fill = fill + 1 == kStages ? 0 : fill + 1;
+            fill = fill + N * Head::kSlotBytes == kRound ? 0 : fill + N * Head::kSlotBytes;
         }
     }
     __device__ __forceinline__ void start() {
@@ -561,8 +614,8 @@ struct HeadStream {
         if constexpr (Head::kRing) {
             copies_wait<kStages - 1>();
 #pragma unroll
-            for (int k = 0; k < N; ++k) head.read(r[k], ring + (drain * N + k) * Head::kSlotBytes);
-            drain = drain + 1 == kStages ? 0 : drain + 1;
+            for (int k = 0; k < N; ++k) head.read(r[k], ring + drain + k * Head::kSlotBytes);
+            drain = drain + N * Head::kSlotBytes == kRound ? 0 : drain + N * Head::kSlotBytes;
         } else {
             if (tok < total) {
                 if (i < mine) {
@@ -575,30 +628,43 @@ struct HeadStream {
     }
 };
 
-// How a head lies in the lanes.  The widest access (in elements) that divides the head
-// and, where pairs lie in halves, the number of pairs; then as many units a lane as make
-// kElems elements, and the group: a power of two, or as many lanes as there are units
-// where more groups fit in a warp so.
+// How a head lies in the lanes: accesses of `w` elements, as wide as divides the head
+// and, where pairs lie in halves, the number of pairs; `u` units a lane, kElems
+// elements at most, or 12 for units of 4; groups of `g` lanes, a power of two, or as
+// many as there are units where more groups fit in a warp so.  The form that leaves the
+// fewest of the lanes' places empty, of equal ones the one with the most elements, an
+// access of 8 bytes only where it fills an eighth more of them (heads of 96,
+// gradients: two groups of 16 lanes with 12 in use 111 us, four of 8 with all).
 struct HeadShape {
     int w, u, g;
     bool vec;
 };
 template <int kElems, int kWidest>  // of a bfloat16 head; a float32 one has accesses of 4
 inline HeadShape head_shape(int hd, int n, bool f32, bool interleaved, int align) {
-    auto fits = [&](int w) { return hd % w == 0 && (interleaved || n % w == 0); };
-    HeadShape s;
-    s.w = f32 ? 4 : kWidest;
-    while (s.w > 1 && !fits(s.w)) s.w /= 2;
-    s.vec = align >= s.w * (f32 ? 4 : 2);
-    const bool one = interleaved && s.w > 1;  // one access a unit
-    const int units = one ? hd / s.w : n / s.w + ((hd - 2 * n) / s.w + 1) / 2, e = one ? s.w : 2 * s.w;
-    s.u = 1;
-    while (units > 32 * s.u || (s.u < 4 && 2 * s.u * e <= kElems && units % (2 * s.u) == 0)) s.u *= 2;
-    const int lanes = (units + s.u - 1) / s.u;
-    s.g = 1;
-    while (s.g < lanes) s.g *= 2;
-    if (32 / lanes > 32 / s.g) s.g = lanes;
-    return s;
+    const int esize = f32 ? 4 : 2;
+    HeadShape best = {};
+    double most = 0.0;
+    for (int w = f32 ? 4 : kWidest; w; w /= 2) {
+        if (hd % w || (!interleaved && n % w)) continue;
+        if (best.w && w * esize < 8) break;
+        const bool one = interleaved && w > 1;  // one access a unit
+        const int units = one ? hd / w : n / w + ((hd - 2 * n) / w + 1) / 2, e = one ? w : 2 * w;
+        for (int u = 1; u <= 4; ++u) {
+            const bool wide = units > 32 * (u == 4 ? 2 : u == 3 ? 2 : u / 2);  // no smaller u takes the head
+            if (u == 3 ? kElems != 8 || e != 4 : u > 1 && u * e > kElems && !wide) continue;
+            const int lanes = (units + u - 1) / u;
+            if (lanes > 32) continue;
+            HeadShape s{w, u, 1, align >= w * esize};
+            while (s.g < lanes) s.g *= 2;
+            if (32 / lanes > 32 / s.g) s.g = lanes;
+            const double used = (double)hd * (32 / s.g) / (32 * e * u) * (best.w && w != best.w ? 1.0 / 1.125 : 1.0);
+            if (used >= most * (best.w == w ? 1.0 : 1.0001)) {
+                most = used;
+                best = s;
+            }
+        }
+    }
+    return best;
 }
 
 // Calls f with a head's shape as types: the element, and Int or Bool of INTERLEAVED, W,
@@ -613,7 +679,10 @@ cudaError_t for_head_shape(const HeadShape& s, bool f32, F&& f) {
     auto with_g = [&](auto t, auto inter, auto w, auto u, auto v) {
         if constexpr (decltype(v)::value && decltype(w)::value >= 4) {
             if (s.g == 4) return f(t, inter, w, u, v, Int<4>());
+            if (s.g == 5) return f(t, inter, w, u, v, Int<5>());
+            if (s.g == 6) return f(t, inter, w, u, v, Int<6>());
             if (s.g == 8) return f(t, inter, w, u, v, Int<8>());
+            if (s.g == 9) return f(t, inter, w, u, v, Int<9>());
             if (s.g == 10) return f(t, inter, w, u, v, Int<10>());
             if (s.g == 16) return f(t, inter, w, u, v, Int<16>());
             if (s.g == 32) return f(t, inter, w, u, v, Int<32>());
@@ -626,6 +695,8 @@ cudaError_t for_head_shape(const HeadShape& s, bool f32, F&& f) {
         if (s.u == 1) return with_g(t, inter, w, Int<1>(), v);
         if constexpr (2 * kUnit <= kElems || kUnits > 32)
             if (s.u == 2) return with_g(t, inter, w, Int<2>(), v);
+        if constexpr (kElems == 8 && kUnit == 4)
+            if (s.u == 3) return with_g(t, inter, w, Int<3>(), v);
         if constexpr (4 * kUnit <= kElems || kUnits > 64)
             if (s.u == 4) return with_g(t, inter, w, Int<4>(), v);
         return cudaErrorInvalidConfiguration;  // not reached

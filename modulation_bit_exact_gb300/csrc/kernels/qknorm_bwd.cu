@@ -11,14 +11,11 @@
 
 namespace mbx {
 
-// Blocks of an SM, by the elements of a head that a lane holds: what the registers allow.
-constexpr int kQkGradBlocks = 2;
-constexpr int grad_blocks(int elems) { return elems <= 16 ? kQkGradBlocks : 1; }
 // Heads on their way to a lane: as many as make 64 bytes of each tensor.
 constexpr int grad_stages(int bytes) { return 64 / bytes < 2 ? 2 : 64 / bytes; }
 
 template <class T, bool INTERLEAVED, int W, int U, bool VEC, int GT>
-__global__ void __launch_bounds__(32 * kQkWarps, grad_blocks(HeadUnits<T, INTERLEAVED, W, U, VEC>::E * U))
+__global__ void __launch_bounds__(32 * kQkWarps, kQkBlocks)
     qk_norm_rope_bwd_kernel(QkNormParams p, int g, QkShare sh) {
     using Head = HeadUnits<T, INTERLEAVED, W, U, VEC>;
     constexpr int E = Head::E, NP = Head::NP, kStages = grad_stages(U * E * (int)sizeof(T));
@@ -63,14 +60,14 @@ __global__ void __launch_bounds__(32 * kQkWarps, grad_blocks(HeadUnits<T, INTERL
         if (tok - at.sub >= total) continue;
         const bool has = tok < total;
         const unsigned b = has ? batch_of(tok, sh.by_tokens) : 0, s = has ? tok - b * tokens : 0;
-        const typename Head::Angles angles = head.angles(cs + at.sub * r.pairs);
+        const typename Head::Rotation turn = head.rotation(cs + at.sub * r.pairs);
         T* out = static_cast<T*>(t.out) + b * t.ob + s * t.ot + at.h0 * t.oh;
 #pragma unroll 1
         for (int i = 0; i < in.steps; ++i, out += at.step * t.oh) {
             in.take(raw);
             const bool real = has && i < in.mine;
             typename Head::Values x = Head::values(raw[0]), gr = Head::values(raw[1]), gy;
-            head.turn(gr, angles);
+            head.turn(gr, turn);
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -78,8 +75,8 @@ __global__ void __launch_bounds__(32 * kQkWarps, grad_blocks(HeadUnits<T, INTERL
                     gy.first[u][j] = mul2(gr.first[u][j], w.first[u][j]);
                     gy.second[u][j] = mul2(gr.second[u][j], w.second[u][j]);
                 }
-            const float ss = group_sum<GT>(dot(x.first, x.second, x), G);
-            const float gx = group_sum<GT>(dot(gy.first, gy.second, x), G);
+            float ss = dot(x.first, x.second, x), gx = dot(gy.first, gy.second, x);
+            group_sums<GT>(ss, gx, G);
             in.fetch();
             const float rstd = rsqrtf(__fmaf_rn(ss, p.inv_hd, p.eps));
             const float c2 = -(gx * p.inv_hd * rstd);
@@ -136,7 +133,7 @@ __global__ void __launch_bounds__(32 * kQkWarps, grad_blocks(HeadUnits<T, INTERL
 
 // A call has at most as many parts as there are blocks for Q or for K.
 int64_t qk_norm_grad_parts(int64_t batch, int64_t tokens) {
-    const int64_t most = (int64_t)kQkGradBlocks * sm_count(), total = batch * tokens;
+    const int64_t most = (int64_t)kQkBlocks * sm_count(), total = batch * tokens;
     return total < most ? total : most;
 }
 
@@ -149,8 +146,8 @@ static cudaError_t backward(const QkNormParams& p, bool f32, int align, ColSumPa
     const HeadShape shape = head_shape<8, kWidest>(r.hd, r.pairs, f32, INTERLEAVED, align);
     return for_head_shape<8, kWidest, INTERLEAVED>(shape, f32, [&](auto t, auto inter, auto w, auto u, auto vec, auto gt) {
         using Head = HeadUnits<decltype(t), decltype(inter)::value, decltype(w)::value, decltype(u)::value, decltype(vec)::value>;
-        constexpr int kElems = Head::E * decltype(u)::value, kStages = grad_stages(kElems * (int)sizeof(t));
-        const QkShare sh = qk_share(r, grad_blocks(kElems) * (int64_t)sm_count(), 32 / shape.g);
+        constexpr int kStages = grad_stages(Head::E * decltype(u)::value * (int)sizeof(t));
+        const QkShare sh = qk_share(r, kQkBlocks * (int64_t)sm_count(), 32 / shape.g);
         sums.parts = sh.q.blocks > sh.k.blocks ? sh.q.blocks : sh.k.blocks;
         auto* k = qk_norm_rope_bwd_kernel<decltype(t), decltype(inter)::value, decltype(w)::value, decltype(u)::value,
                                           decltype(vec)::value, decltype(gt)::value>;
