@@ -29,13 +29,15 @@
 
 namespace mbx {
 
-constexpr int kTile = 128, kPiece = 256, kMaxPieces = 8, kPassRows = 16, kMaxStages = 8;
+constexpr int kTile = 128, kPiece = 256, kMaxPieces = 8, kPassRows = 16, kMaxStages = 15;
 constexpr int kWorkers = 512, kTcThreads = kWorkers + 64;  // then the copying warp and the multiplying one
 constexpr int kCopyWarp = kWorkers / 32, kMmaWarp = kCopyWarp + 1;
+constexpr int kFirstStages = 3;  // copied before the block meets; a copy takes 0.1 us to issue
 constexpr int kStageBytes = 16384, kStageScales = 2048;
 constexpr int kMaxSmem = 227 * 1024;
-// tensor memory: two accumulators, the stages' scales (16 columns each), the digits' scales
-constexpr uint32_t kAccCols = 128, kScaleCol = 256, kDigitScaleCol = 384;
+// tensor memory: two accumulators, the pieces' digits' scales and then the stages' scales,
+// 16 columns each
+constexpr uint32_t kAccCols = 128, kDigitScaleCol = 256, kScaleCols = 16;
 
 struct TcParams {
     LinearParams l;
@@ -51,9 +53,10 @@ struct SliceRows {
     int odd[kPassRows];        // whether the row has an infinity or NaN there
 };
 
-// How K is cut into slices and the tiles shared out: by the pieces that a block
-// works through one after another, a tile's end counting as a third of a piece, a
-// piece's digits as two thirds and a second kernel as six.  The rows do not matter, so that a row's sums have one order.
+// How K is cut into slices and the tiles shared out, by what a block takes, in tenths of
+// a microsecond: 4 for a piece of weight, 2 for a tile's end, 2 for a piece's digits, and
+// 24 for the second kernel with 1 for each slice.  The rows do not matter, so that a
+// row's sums have one order.
 struct TcPlan {
     int slices, pieces_per_slice, groups, tiles;
 };
@@ -67,7 +70,7 @@ static TcPlan tc_plan(int64_t N, int K) {
         int64_t groups = sms / slices;
         if (groups < 1) continue;
         if (groups > tiles) groups = tiles;
-        const int64_t c = (tiles + groups - 1) / groups * (3 * len + 1) + 2 * len + (slices > 1 ? 18 : 0);
+        const int64_t c = (tiles + groups - 1) / groups * (4 * len + 2) + 2 * len + (slices > 1 ? 24 + slices : 0);
         if (c < cost) {
             cost = c;
             best = TcPlan{slices, len, (int)groups, (int)tiles};
@@ -77,11 +80,12 @@ static TcPlan tc_plan(int64_t N, int K) {
 }
 
 // The workspace: the slices' sums [slices][rows][N], then the digits' images.
-// A block makes its digits itself while each of its workers has one block of 16 at
-// most (8 rows of 4 pieces: 21.0 us for [8, 5120] x [30720, 5120], a kernel before it
-// 22.6); more are made beforehand ([16, 1024] x [2048, 1024]: 6.8 us against 14.0).
+// A block makes the digits of up to kOwnBlocks blocks of 16 itself ([1, 5120] x [30720,
+// 5120]: 18.5 us, with a kernel before it 21); more are made beforehand, once for all
+// that use them ([8, 1024] x [2048, 1024]: 6.3 us against 9.1).
+constexpr int kQuarters = 2, kOwnBlocks = kQuarters * kWorkers / 4;
 static bool digits_before(const TcPlan& p, int rows) {
-    return (rows < kPassRows ? rows : kPassRows) * p.pieces_per_slice * 16 > kWorkers;
+    return (rows < kPassRows ? rows : kPassRows) * p.pieces_per_slice * 16 > kOwnBlocks;
 }
 static int64_t sums_bytes(const TcPlan& p, int rows, int64_t N) {
     return p.slices > 1 ? ((int64_t)p.slices * rows * N * 4 + 127) / 128 * 128 : 0;
@@ -164,52 +168,50 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 
 __device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
 
-// One block of 16 activations: x[row][16 * blk ...].
-__device__ __forceinline__ void load_block(float (&v)[16], const TcParams& p, int row, int blk) {
-    const int64_t at = (int64_t)row * p.l.x_stride + 16 * blk;
+// Four activations, a quarter of a block of 16: x[row][k ...].
+__device__ __forceinline__ void load_quarter(float (&v)[4], const TcParams& p, int row, int k) {
+    const int64_t at = (int64_t)row * p.l.x_stride + k;
     if (p.x_f32) {
         const float* x = static_cast<const float*>(p.l.x) + at;
+        if (p.x_vec) {
+            const uint4 q = ld_stream_rw(x);
+            v[0] = __uint_as_float(q.x), v[1] = __uint_as_float(q.y), v[2] = __uint_as_float(q.z), v[3] = __uint_as_float(q.w);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (p.x_vec) {
-                const uint4 q = ld_stream_rw(x + 4 * i);
-                v[4 * i] = __uint_as_float(q.x), v[4 * i + 1] = __uint_as_float(q.y);
-                v[4 * i + 2] = __uint_as_float(q.z), v[4 * i + 3] = __uint_as_float(q.w);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[4 * i + j] = load_elem(x + 4 * i + j);
-            }
+            for (int i = 0; i < 4; ++i) v[i] = load_elem(x + i);
         }
     } else {
         const uint16_t* x = static_cast<const uint16_t*>(p.l.x) + at;
+        if (p.x_vec) {
+            uint32_t a, b;
+            asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "l"(x));
+            v[0] = lo_f(a), v[1] = hi_f(a), v[2] = lo_f(b), v[3] = hi_f(b);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (p.x_vec) {
-                const uint4 q = ld_stream_rw(x + 8 * i);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[8 * i + 2 * j] = lo_f(w_of(q, j)), v[8 * i + 2 * j + 1] = hi_f(w_of(q, j));
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[8 * i + j] = load_elem(x + 8 * i + j);
-            }
+            for (int i = 0; i < 4; ++i) v[i] = load_elem(x + i);
         }
     }
     if (p.l.silu) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = silu(v[i]);
+        for (int i = 0; i < 4; ++i) v[i] = silu(v[i]);
     }
 }
 
-// The largest magnitude of a block's finite values, as bits; *odd set where one is not finite.
-__device__ __forceinline__ uint32_t block_max(const float (&v)[16], int* odd) {
+// The largest magnitude of the finite values, as bits; *odd set where one is not finite.
+__device__ __forceinline__ uint32_t quarter_max(const float (&v)[4], int* odd) {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 4; ++i) {
         const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
         if (b >= 0x7f800000u) *odd = 1;
         else m = max(m, b);
     }
     return m;
+}
+// Of the four lanes that have a block.
+__device__ __forceinline__ uint32_t of_four(uint32_t m) {
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
 // e with |v| < 2^e; magnitudes below 2^-85 (of a row) take that.
 __device__ __forceinline__ int above(uint32_t bits) { return (int)(bits >> 23) - 126; }
@@ -225,53 +227,32 @@ __device__ __forceinline__ uint32_t digits(float v, float to_int) {
     const uint32_t m = (x >> 2) & 0x11111111u, up = (m << 4) - m;
     return (x & 0x33333333u & up) | ((0xccccccccu - x) & ~up);
 }
-// Nibble j of w[i] becomes nibble i of w[j].
-__device__ __forceinline__ void transpose_nibbles(uint32_t (&w)[8]) {
-    uint32_t t[8], u[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        t[j] = __byte_perm(w[j], w[j + 4], 0x5410);
-        t[j + 4] = __byte_perm(w[j], w[j + 4], 0x7632);
-    }
-#pragma unroll
-    for (int h = 0; h < 8; h += 4)
-#pragma unroll
-        for (int j = h; j < h + 2; ++j) {
-            u[j] = __byte_perm(t[j], t[j + 2], 0x6240);
-            u[j + 2] = __byte_perm(t[j], t[j + 2], 0x7351);
-        }
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-        w[j] = (u[j] & 0x0f0f0f0fu) | (u[j + 1] & 0x0f0f0f0fu) << 4;
-        w[j + 1] = (u[j] >> 4 & 0x0f0f0f0fu) | (u[j + 1] & 0xf0f0f0f0u);
-    }
-}
-
-// The digits of one block of a row whose largest magnitude in this slice of K has the
-// bits `most`, into the row's eight columns: `col` is digit 0's column in the piece
-// (columns 128 bytes apart, 16-byte units swizzled), `scale` its scale (columns 16
-// bytes apart); b is the block's place in the slice.
-__device__ __forceinline__ void put_digits(const float (&v)[16], uint32_t most, int b, uint8_t* col, uint8_t* scale) {
-    int odd = 0;
+// The digits of a quarter of a block whose largest magnitude has the bits `block`, of a
+// row whose largest in this slice of K has the bits `most`, into the row's eight columns:
+// `col` is digit 0's column in the piece (columns 128 bytes apart, 16-byte units
+// swizzled), `scale` its scale (columns 16 bytes apart); b is the block's place in the
+// slice, q the quarter.
+__device__ __forceinline__ void put_digits(const float (&v)[4], uint32_t block, uint32_t most, int b, int q, uint8_t* col, uint8_t* scale) {
     const int top = max(above(most), -85);
-    const int e = max(min(above(block_max(v, &odd)), top), top - 17);
+    const int e = max(min(above(block), top), top - 17);
     const float to_int = __uint_as_float((uint32_t)(127 + 22 - e) << 23);
-    uint32_t w[2][8];
+    uint32_t d[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = digits((__float_as_uint(v[i]) & 0x7f800000u) == 0x7f800000u ? 0.0f : v[i], to_int);
+    // two values a byte, the first in the low half: bytes of digits 0, 2, 4, 6 and of 1, 3, 5, 7
+    uint32_t even[2], odd[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float a = v[8 * h + j];
-            w[h][j] = digits((__float_as_uint(a) & 0x7f800000u) == 0x7f800000u ? 0.0f : a, to_int);
-        }
-        transpose_nibbles(w[h]);
+        even[h] = (d[2 * h] & 0x0f0f0f0fu) | (d[2 * h + 1] & 0x0f0f0f0fu) << 4;
+        odd[h] = (d[2 * h] >> 4 & 0x0f0f0f0fu) | (d[2 * h + 1] & 0xf0f0f0f0u);
     }
     const int up = 8 + e - top;  // -9 .. 8: the scale 2^up as E4M3
     const uint8_t sc = (uint8_t)(up >= -6 ? (up + 7) << 3 : 1 << (up + 9));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        *reinterpret_cast<uint2*>(col + i * 128 + ((b % 16 / 2) ^ i) * 16 + b % 2 * 8) = make_uint2(w[0][i], w[1][i]);
-        scale[i * 16] = sc;
+        const uint32_t two = __byte_perm(i & 1 ? odd[0] : even[0], i & 1 ? odd[1] : even[1], i / 2 | (i / 2 + 4) << 4);
+        *reinterpret_cast<uint16_t*>(col + i * 128 + ((b % 16 / 2) ^ i) * 16 + b % 2 * 8 + q * 2) = (uint16_t)two;
+        if (i % 4 == q) scale[i * 16] = sc;
     }
 }
 // Where a row's columns of a slice's digits begin, and its scales: [pieces][cols][128
@@ -286,9 +267,11 @@ __device__ __noinline__ float odd_products(const TcParams& p, int row, int64_t n
     float sum = 0.0f;
     for (int blk = blk0; blk < blk1; ++blk) {
         float v[16];
-        load_block(v, p, row, blk);
         int odd = 0;
-        block_max(v, &odd);
+        for (int q = 0; q < 4; ++q) {
+            load_quarter(reinterpret_cast<float(&)[4]>(v[4 * q]), p, row, 16 * blk + 4 * q);
+            quarter_max(reinterpret_cast<float(&)[4]>(v[4 * q]), &odd);
+        }
         if (!odd) continue;
         const uint8_t b = p.l.sf[(n / 128 * p.l.sf_col_tiles + blk / 4) * 512 + n % 32 * 16 + n % 128 / 32 * 4 + blk % 4];
         uint32_t h;
@@ -357,11 +340,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
                      "l"(p.l.sf + ((int64_t)tile * p.l.sf_col_tiles + piece * 4) * 512), "r"(bytes), "r"(bar)
                      : "memory");
     };
-    // the worker's block of activations, 0 past K
+    // the worker's quarters of blocks of activations, 0 past K: the c-th is quarter
+    // id % 4 of block id / 4, id = c * kWorkers + thread
     const int per_row = steps * 4, items = rows * per_row;
-    float v[16];
+    float v[kQuarters][4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    for (int c = 0; c < kQuarters; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[c][i] = 0.0f;
     const uint8_t* image = p.images ? p.images + ((int64_t)blockIdx.y * p.slices + slice) * p.image_bytes : nullptr;
 
     if (warp == kCopyWarp) {
@@ -380,7 +366,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
             // the kernel that made the digits began when all before it had finished
             if (!p.images) grid_dep_wait();
-            for (int u = 0; u < p.stages && u < total; ++u) fetch(u);
+            for (int u = 0; u < kFirstStages && u < p.stages && u < total; ++u) fetch(u);
             if (p.images) {
                 grid_dep_wait();
                 const uint32_t bytes = p.pieces_per_slice * (cols * 128 + 2048);
@@ -401,9 +387,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
         if (p.images) {
             if (threadIdx.x < sizeof(SliceRows) / 4)
                 reinterpret_cast<uint32_t*>(&sh.rows)[threadIdx.x] = reinterpret_cast<const volatile uint32_t*>(image + p.image_bytes - sizeof(SliceRows))[threadIdx.x];
-        } else if ((int)threadIdx.x < items) {
-            const int r = threadIdx.x / per_row, blk = blk0 + threadIdx.x - r * per_row;
-            if (blk < blk1) load_block(v, p, row0 + r, blk);
+        } else {
+#pragma unroll
+            for (int c = 0; c < kQuarters; ++c) {
+                const int at = (c * kWorkers + (int)threadIdx.x) / 4, r = at / per_row, blk = blk0 + at - r * per_row;
+                if (at < items && blk < blk1) load_quarter(v[c], p, row0 + r, 16 * blk + threadIdx.x % 4 * 4);
+            }
         }
     }
     tc_fence_before();
@@ -414,35 +403,44 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
 
     if (warp == kCopyWarp) {
         if (lane == 0) {
-            int u = p.stages;
+            int u = min(kFirstStages, p.stages);
             for (; u < total; ++u) {
-                if (!bar_wait(smem_addr(&sh.empty[u % p.stages]), (u / p.stages - 1) & 1, failed)) break;
+                if (u >= p.stages && !bar_wait(smem_addr(&sh.empty[u % p.stages]), (u / p.stages - 1) & 1, failed)) break;
                 fetch(u);
             }
             // after a failure: the copies that are under way have to land before the block ends
             if (*failed && p.images) bar_wait(smem_addr(&sh.digits), 0, failed);
             if (*failed)
-                for (int i = u - p.stages; i < u && i < total; ++i)
+                for (int i = max(u - p.stages, 0); i < u && i < total; ++i)
                     for (int k = 0; k < 100000 && !bar_try(smem_addr(&sh.full[i % p.stages]), (i / p.stages) & 1); ++k) {
                     }
         }
         __syncwarp();
     } else if (warp < kCopyWarp && !p.images) {
-        // the digits: a row's block for each thread
-        const int r = threadIdx.x / per_row, b = threadIdx.x - r * per_row;
-        const bool mine = (int)threadIdx.x < items;
-        int odd = 0;
-        uint32_t m = mine ? block_max(v, &odd) : 0;
-        if (per_row % 32 == 0) {  // a warp's blocks are of one row
-            m = __reduce_max_sync(0xffffffffu, m);
-            if (lane == 0 && mine) atomicMax(&sh.rows.most[r], m);
-        } else if (mine) {
-            atomicMax(&sh.rows.most[r], m);
+        uint32_t block[kQuarters];
+#pragma unroll
+        for (int c = 0; c < kQuarters; ++c) {
+            if (c * kWorkers / 4 >= items) break;
+            const int at = (c * kWorkers + (int)threadIdx.x) / 4, r = min(at, items - 1) / per_row;
+            int odd = 0;
+            block[c] = of_four(quarter_max(v[c], &odd));
+            if (per_row % 8 == 0) {  // a warp's eight blocks are of one row
+                const uint32_t m = __reduce_max_sync(0xffffffffu, block[c]);
+                if (lane == 0) atomicMax(&sh.rows.most[r], m);
+            } else if (lane % 4 == 0) {
+                atomicMax(&sh.rows.most[r], block[c]);
+            }
+            if (odd) sh.rows.odd[r] = 1;
         }
-        if (odd) sh.rows.odd[r] = 1;
         asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory");
-        if (mine)
-            put_digits(v, sh.rows.most[r], b, digit_at(dig, cols, r, b), digit_scale_at(dig, cols, p.pieces_per_slice, r, b));
+#pragma unroll
+        for (int c = 0; c < kQuarters; ++c) {
+            const int at = (c * kWorkers + (int)threadIdx.x) / 4;
+            if (at >= items) break;
+            const int r = at / per_row, b = at - r * per_row;
+            put_digits(v[c], block[c], sh.rows.most[r], b, lane % 4, digit_at(dig, cols, r, b),
+                       digit_scale_at(dig, cols, p.pieces_per_slice, r, b));
+        }
         fence_async();
         asm volatile("bar.arrive 2, %0;" ::"n"(kWorkers + 32) : "memory");
     }
@@ -453,46 +451,47 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
         else asm volatile("bar.sync 2, %0;" ::"n"(kWorkers + 32) : "memory");
         const uint32_t idesc = 1u << 7 | 1u << 10 | (uint32_t)(cols / 8) << 17 | (uint32_t)(kTile / 16) << 24;
         const bool leader = elect_one();
-        if (leader)
-            for (int k = 0; k < steps; ++k) scales_to_tmem(tmem + kDigitScaleCol + 4 * k, scale_desc(smem_addr(dig_scales)) + 32 * k);
         const bool ragged = blocks % 4 != 0 && blk1 == blocks;  // the last step's blocks past K: their scales are anything
-        int s = 0, phase = 0;
+        const int pieces = piece1 - piece0;
+        if (leader)  // the digits' scales
+            for (int k = 0; k < steps; ++k) scales_to_tmem(tmem + kDigitScaleCol + 4 * k, scale_desc(smem_addr(dig_scales)) + 32 * k);
+        int stage = 0, phase = 0;
         for (int t = 0; t < my_tiles && ok; ++t) {
             const int a = t & 1;
             if (t >= 2) ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.acc_empty[a]), (t / 2 - 1) & 1, failed));
             tc_fence_after();
-            for (int piece = piece0; piece < piece1 && ok; ++piece) {
-                const int n = min(4, p.l.sf_col_tiles - piece * 4);
-                ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.full[s]), phase, failed));
+            for (int piece = 0; piece < pieces && ok; ++piece) {
+                const int n = min(4, p.l.sf_col_tiles - (piece0 + piece) * 4);
+                ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.full[stage]), phase, failed));
                 if (!ok) break;
-                const uint32_t sc = smem_addr(scales + s * kStageScales);
-                if (ragged && piece == piece1 - 1) {
+                if (ragged && piece == pieces - 1) {
                     const uint32_t keep = (1u << blocks % 4 * 8) - 1;
-                    uint32_t* w = reinterpret_cast<uint32_t*>(scales + s * kStageScales + (n - 1) * 512);
+                    uint32_t* w = reinterpret_cast<uint32_t*>(scales + stage * kStageScales + (n - 1) * 512);
                     for (int i = lane; i < 128; i += 32) w[i] &= keep;
                     fence_async();
                     __syncwarp();
                 }
                 if (leader) {
-                    const uint32_t sa = tmem + kScaleCol + 16 * s, sb = tmem + kDigitScaleCol + 16 * (piece - piece0);
-                    const uint64_t wa = operand_desc(smem_addr(ring + s * kStageBytes));
-                    const uint64_t da = operand_desc(smem_addr(dig + (piece - piece0) * cols * 128));
+                    const uint32_t sb = tmem + kDigitScaleCol + kScaleCols * piece;
+                    const uint32_t sa = tmem + kDigitScaleCol + kScaleCols * (p.pieces_per_slice + stage);
+                    const uint64_t wa = operand_desc(smem_addr(ring + stage * kStageBytes));
+                    const uint64_t da = operand_desc(smem_addr(dig + piece * cols * 128));
+                    const uint64_t sd = scale_desc(smem_addr(scales + stage * kStageScales));
                     const uint32_t acc = tmem + a * kAccCols;
-                    const uint64_t sd = scale_desc(sc);
                     if (n == 4) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) scales_to_tmem(sa + 4 * k, sd + 32 * k);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) mma_fp4(acc, wa + 2 * k, da + 2 * k, idesc, sa + 4 * k, sb + 4 * k, piece > piece0 || k > 0);
+                        for (int k = 0; k < 4; ++k) mma_fp4(acc, wa + 2 * k, da + 2 * k, idesc, sa + 4 * k, sb + 4 * k, piece > 0 || k > 0);
                     } else {
                         for (int k = 0; k < n; ++k) scales_to_tmem(sa + 4 * k, sd + 32 * k);
-                        for (int k = 0; k < n; ++k) mma_fp4(acc, wa + 2 * k, da + 2 * k, idesc, sa + 4 * k, sb + 4 * k, piece > piece0 || k > 0);
+                        for (int k = 0; k < n; ++k) mma_fp4(acc, wa + 2 * k, da + 2 * k, idesc, sa + 4 * k, sb + 4 * k, piece > 0 || k > 0);
                     }
-                    mma_commit(smem_addr(&sh.empty[s]));
-                    if (piece == piece1 - 1) mma_commit(smem_addr(&sh.acc_full[a]));
+                    mma_commit(smem_addr(&sh.empty[stage]));
+                    if (piece == pieces - 1) mma_commit(smem_addr(&sh.acc_full[a]));
                 }
                 __syncwarp();
-                if (++s == p.stages) s = 0, phase ^= 1;
+                if (++stage == p.stages) stage = 0, phase ^= 1;
             }
         }
         // nothing of the block may be under way when it gives the tensor memory back
@@ -550,21 +549,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
 // The digits of one row's part of a slice, for all blocks of the product that use it.
 // Sixteen rows' digits take a block of the product 6 us, which its first copies do
 // not cover; made once here they take 2.
-__global__ void __launch_bounds__(16 * kMaxPieces) linear_digits_kernel(const TcParams p) {
-    __shared__ uint32_t most_of[kMaxPieces / 2];
-    __shared__ int odd_of[kMaxPieces / 2];
+__global__ void __launch_bounds__(64 * kMaxPieces) linear_digits_kernel(const TcParams p) {
+    __shared__ uint32_t most_of[2 * kMaxPieces];
+    __shared__ int odd_of[2 * kMaxPieces];
     const int slice = blockIdx.x, row = blockIdx.y, pass = row / kPassRows, r = row % kPassRows;
     const int cols = (min(p.l.rows - pass * kPassRows, kPassRows) * 8 + 15) / 16 * 16;
     const int blocks = p.l.K / 16, blk0 = slice * p.pieces_per_slice * 16, blk1 = min(blk0 + p.pieces_per_slice * 16, blocks);
-    const int b = threadIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int b = threadIdx.x / 4, q = threadIdx.x % 4, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     grid_dep_wait();
     grid_dep_launch();
-    float v[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-    if (blk0 + b < blk1) load_block(v, p, row, blk0 + b);
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (blk0 + b < blk1) load_quarter(v, p, row, 16 * (blk0 + b) + 4 * q);
     int odd = 0;
-    const uint32_t m = __reduce_max_sync(0xffffffffu, block_max(v, &odd));
+    const uint32_t block = of_four(quarter_max(v, &odd)), m = __reduce_max_sync(0xffffffffu, block);
     odd = __any_sync(0xffffffffu, odd);
     if (lane == 0) {
         most_of[warp] = m;
@@ -579,8 +576,8 @@ __global__ void __launch_bounds__(16 * kMaxPieces) linear_digits_kernel(const Tc
     }
     uint8_t* image = p.images + ((int64_t)pass * p.slices + slice) * p.image_bytes;
     if (b < (blk1 - blk0 + 3) / 4 * 4)
-        put_digits(v, most, b, digit_at(image, cols, r, b), digit_scale_at(image, cols, p.pieces_per_slice, r, b));
-    if (b == 0) {
+        put_digits(v, block, most, b, q, digit_at(image, cols, r, b), digit_scale_at(image, cols, p.pieces_per_slice, r, b));
+    if (threadIdx.x == 0) {
         SliceRows* s = reinterpret_cast<SliceRows*>(image + p.image_bytes - sizeof(SliceRows));
         s->most[r] = most;
         s->odd[r] = odd;
@@ -674,7 +671,7 @@ cudaError_t launch_linear_tc(const LinearParams& l, bool x_f32, bool out_f32, cu
     const int rows = l.rows < kPassRows ? l.rows : kPassRows, cols = (rows * 8 + 15) / 16 * 16;
     const int dig = plan.pieces_per_slice * (cols * 128 + 4 * 512);
     p.stages = (kMost - 1024 - dig) / (kStageBytes + kStageScales);
-    if (p.stages > kMaxStages) p.stages = kMaxStages;
+    if (p.stages > kMaxStages + 1 - plan.pieces_per_slice) p.stages = kMaxStages + 1 - plan.pieces_per_slice;  // 512 columns
     const int work = (plan.tiles + plan.groups - 1) / plan.groups * plan.pieces_per_slice;
     if (p.stages > work) p.stages = work;
     const size_t smem = 1024 + dig + (size_t)p.stages * (kStageBytes + kStageScales);
@@ -693,7 +690,7 @@ cudaError_t launch_linear_tc(const LinearParams& l, bool x_f32, bool out_f32, cu
     if (digits_before(plan, l.rows)) {
         p.images = reinterpret_cast<uint8_t*>(l.ws) + sums_bytes(plan, l.rows, l.N);
         p.image_bytes = image_bytes(plan, l.rows);
-        const unsigned threads = (unsigned)(plan.pieces_per_slice * 16 + 31) / 32 * 32;
+        const unsigned threads = (unsigned)plan.pieces_per_slice * 64;
         if (cudaError_t e = launch2(linear_digits_kernel, dim3((unsigned)plan.slices, (unsigned)l.rows), threads, 0, s, p)) return e;
     }
     const cudaError_t e = launch2(linear_tc_kernel, dim3((unsigned)(p.slices * p.groups), passes), kTcThreads, smem, s, map, p);
