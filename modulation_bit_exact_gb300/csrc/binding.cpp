@@ -377,6 +377,20 @@ PyObject* rope_axes(PyObject* const* a) {
     return wrap2(qo, ko);
 }
 
+// An uninitialised tensor of t's shape, dtype and order of dimensions.  at::empty costs a
+// call 3 us less than at::empty_like, and gives the same where the order is the usual one.
+at::Tensor heads_like(const at::Tensor& t) {
+    const auto z = t.sizes();
+    const auto s = t.strides();
+    int64_t last = INT64_MAX;
+    for (int64_t d = 0; d < t.dim(); ++d) {
+        if (z[d] == 1) continue;
+        if (s[d] > last) return at::empty_like(t);
+        last = s[d];
+    }
+    return at::empty(z, t.options());
+}
+
 // An optional tensor of heads: its view, or a null pointer.
 template <class H>
 struct OptHeads {
@@ -401,8 +415,8 @@ PyObject* qk_norm_rope(PyObject* const* a) {
     if (interleaved < 0) return nullptr;
     const float eps = (float)number(a[8]);
     at::Tensor qo = tensor_or_none(a[9]), ko = tensor_or_none(a[10]);
-    if (!qo.defined()) qo = at::empty_like(q);
-    if (!ko.defined() && k.defined()) ko = at::empty_like(k);
+    if (!qo.defined()) qo = heads_like(q);
+    if (!ko.defined() && k.defined()) ko = heads_like(k);
     const HeadsIn qv(q), kv(k);
     const HeadsOut qov(qo), kov(ko);
     for (int st : {qv.status, qov.status, kv.status, kov.status})
@@ -429,10 +443,10 @@ PyObject* qk_norm_rope_backward(PyObject* const* a) {
     if (interleaved < 0) return nullptr;
     const float eps = (float)number(a[10]);
     at::Tensor dq = tensor_or_none(a[11]), dk = tensor_or_none(a[12]), dwq = tensor_or_none(a[13]), dwk = tensor_or_none(a[14]);
-    if (!dq.defined()) dq = at::empty_like(q);
-    if (!dk.defined() && k.defined()) dk = at::empty_like(k);
-    if (!dwq.defined() && wq.defined()) dwq = like(wq);
-    if (!dwk.defined() && wk.defined()) dwk = like(wk);
+    if (!dq.defined()) dq = heads_like(q);
+    if (!dk.defined() && k.defined()) dk = heads_like(k);
+    if (!dwq.defined() && wq.defined()) dwq = at::empty(wq.sizes(), wq.options());
+    if (!dwk.defined() && wk.defined()) dwk = at::empty(wk.sizes(), wk.options());
     const HeadsIn qv(q), kv(k), dqov(dqo), dkov(dko);
     const HeadsOut dqv(dq), dkv(dk);
     for (int st : {qv.status, dqov.status, dqv.status, kv.status, dkov.status, dkv.status})

@@ -116,19 +116,19 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
                  : "memory");
     return ok;
 }
-// Waits for the phase, for a second at most; false, and *failed set, when it did not
-// come or another wait of the block had failed.
+// Waits for the phase, for a second and a million tries at most (a block that was off the
+// GPU for that second has the tries left); false, and *failed set, when it did not come or
+// another wait of the block had failed.  Nothing is known to make one fail; the outputs of
+// the tiles that it leaves out are NaN.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
-    for (int i = 0; i < 64; ++i)
-        if (bar_try(bar, parity)) return true;
-    unsigned long long t0, t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-    do {
-        for (int i = 0; i < 64; ++i)
+    unsigned long long start = 0, now = 0;
+    for (int i = 0; now - start < 1000000000ull || i < 1 << 14; ++i) {
+        for (int k = 0; k < 64; ++k)
             if (bar_try(bar, parity)) return true;
         if (*failed) return false;
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    } while (t - t0 < 1000000000ull);
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        if (i == 0) start = now;
+    }
     *failed = 1;
     return false;
 }

@@ -13,7 +13,7 @@
 
 #include <type_traits>
 
-#include "rope.cuh"
+#include "rowgroup.cuh"
 
 namespace mbx {
 

@@ -17,9 +17,19 @@
 // registers and walks the heads of Q and K.  Memory bound: every element is
 // read once and written once (32760 tokens of 40 heads of 128, Q and K,
 // bfloat16: 200 us, 6.7 TB/s of 6.77 that a copy reaches).
-#include "rope.cuh"
+#include "rowgroup.cuh"
 
 namespace mbx {
+
+// cos and sin of 2*pi*turns.
+__device__ __forceinline__ float2 cos_sin_turns(double turns) {
+    const double q = turns * 4.0, r = rint(q);
+    const int quadrant = (int)(long long)r & 3;
+    float s, c;
+    sincospif((float)(q - r) * 0.5f, &s, &c);  // |argument| <= 1/4
+    const float cc = (quadrant & 1) ? -s : c, ss = (quadrant & 1) ? c : s;
+    return (quadrant & 2) ? make_float2(-cc, -ss) : make_float2(cc, ss);
+}
 
 // One lane's part of a head, and its rotation.  W elements an access (16 or 8
 // bytes), interleaved: one access; in halves: the access at c and the one at
@@ -182,7 +192,13 @@ __global__ void __launch_bounds__(256, 4) rope_axes_kernel(RopeParams p, int lan
         const int kk = i / n, j = i - kk * n;
         const unsigned tk = tok0 + kk;
         if (tk >= total) break;
-        const float2 v = token_cos_sin(p, tk, tk % tokens, j);
+        int a = 0;
+        while (a < p.axes - 1 && j >= p.axis_end[a]) ++a;
+        const int64_t prow = p.pos_batched ? tk : tk % tokens;
+        const double pos = p.pos_f32 ? (double)static_cast<const float*>(p.pos)[prow * p.pos_stride + a]
+                                     : (double)static_cast<const int*>(p.pos)[prow * p.pos_stride + a];
+        float2 v = cos_sin_turns(pos * (p.freqs[j] * 0.15915494309189533577));  // 1 / (2 pi)
+        if (p.inverse) v.y = -v.y;
         cs_smem[i] = v;
     }
     __syncthreads();

@@ -277,3 +277,41 @@ def test_a_blocks_modulation_and_heads(mbx):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(again, got))
+
+
+def test_weight_laid_out_on_the_gpu(mbx):
+    w = torch.randn((300, 208), generator=gen(11)).bfloat16()
+    for a, b in zip(mbx.nvfp4_weight(w), mbx.nvfp4_weight(w.to(DEV))):
+        assert b.is_cuda and torch.equal(a, b.cpu())
+
+
+@pytest.mark.parametrize("rows,N,K", [(1, 3000, 2048), (16, 3000, 2048), (19, 700, 8192), (16, 300, 512)])
+def test_workspace_of_the_stated_size(mbx, rows, N, K):
+    """Nothing past it is written, what it held does not matter, and a smaller one is refused."""
+    g = gen(12)
+    w4, sf, gs = weight(mbx, g, N, K)
+    x = rnd(g, (rows, K), BF)
+    out = torch.empty((rows, N), dtype=BF, device=DEV)
+    need = mbx.linear_nvfp4_workspace(rows, N, K)
+    want = mbx.linear_nvfp4(x, w4, sf, gs)
+    L, st = mbx.lib(), torch.cuda.current_stream().cuda_stream
+    for fill in (0xFF, 0x7F):
+        ws = torch.full((need + 4096,), fill, dtype=torch.uint8, device=DEV)
+        call = lambda n: L.mbx_linear_nvfp4(mbx._view(out), mbx._view(x), *mbx._weight_views(w4, sf), gs.data_ptr(), None, 0,
+                                            ws.data_ptr(), n, st)
+        assert call(need) == 0
+        assert torch.equal(out, want) and (ws[need:] == fill).all()
+        if need:
+            assert call(need - 16) == -10
+
+
+def test_zero_and_extreme_scales(mbx):
+    """A global scale of 0 divides by it; blocks whose scale is 0 or the largest."""
+    g = gen(13)
+    w4, sf, gs = weight(mbx, g, 200, 256)
+    x = rnd(g, (2, 256), F32)
+    out = mbx.linear_nvfp4(x, w4, sf, torch.zeros(1, device=DEV))
+    assert (out.isinf() | out.isnan()).all()
+    for byte in (0x00, 0x01, 0x7E):
+        f = torch.full_like(sf, byte)
+        check(mbx, x, (w4, f, gs), None, False)

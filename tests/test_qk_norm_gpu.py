@@ -377,3 +377,49 @@ def test_angles(mbx, interleaved):
         pos = torch.tensor([[0.0], [bad], [2.0]], device=DEV)
         o, _ = mbx.qk_norm_rope(q[:, :3], None, None, None, pos, fr.to(DEV), (2 * n,), interleaved, EPS)
         assert o[0, 1].isnan().all() and not o[0, [0, 2]].isnan().any()
+
+
+def test_workspace_of_the_stated_size(mbx):
+    """Nothing past it is written, what it held does not matter, and a smaller one is refused."""
+    import ctypes
+    g = gen(60)
+    axes = (16, 24, 24)
+    fr, ax = mbx.rope_axis_freqs(axes), (ctypes.c_int32 * 3)(16, 24, 24)
+    L, st = mbx.lib(), torch.cuda.current_stream().cuda_stream
+    for B, S, hq, hk in ((1, 1, 2, 1), (2, 77, 16, 4), (1, 9000, 1, 1), (1, 9000, 24, 24)):
+        q, k = case(g, B, S, hq, hk, 64, BF)
+        dq, dk, w = rnd(g, q.shape, BF, 0.1), rnd(g, k.shape, BF, 0.1), rnd(g, (64,), F32, 0.1, 1.0)
+        pos = torch.randint(0, 64, (S, 3), generator=g).int().to(DEV)
+        want = mbx.qk_norm_rope_backward(dq, dk, q, k, w, w, pos, fr, axes)
+        need = mbx.qk_norm_grad_workspace(B, S, 64)
+        out = [torch.empty_like(t) for t in want]
+        for fill in (0xFF, 0x7F):
+            ws = torch.full((need + 4096,), fill, dtype=torch.uint8, device=DEV)
+            call = lambda n: L.mbx_qk_norm_rope_backward(
+                *map(mbx._heads, out[:2]), *map(mbx._view, out[2:]), *map(mbx._heads, (dq, dk, q, k)), mbx._view(w), mbx._view(w),
+                mbx._view(pos), mbx._view(fr), ax, 3, 1, 1e-6, ws.data_ptr(), n, st)
+            assert call(need) == 0
+            assert all(torch.equal(a, b) for a, b in zip(out, want)) and (ws[need:] == fill).all()
+            assert call(need - 16) == -10
+
+
+def test_one_weight_gradient_alone(mbx):
+    """A weight for Q or for K only; no K; a given dwq of which the rest is left alone."""
+    g = gen(61)
+    axes, fr = (32,), mbx.rope_axis_freqs((32,))
+    q, k = case(g, 2, 21, 4, 2, 32, F32)
+    dq, dk, w = rnd(g, q.shape, F32, 0.1), rnd(g, k.shape, F32, 0.1), rnd(g, (32,), F32, 0.1, 1.0)
+    pos = torch.arange(21, dtype=torch.int32, device=DEV)[:, None]
+    for wq, wk in ((w, None), (None, w)):
+        got = mbx.qk_norm_rope_backward(dq, dk, q, k, wq, wk, pos, fr, axes)
+        for i, (do, x, ww) in enumerate(((dq, q, wq), (dk, k, wk))):
+            (dx, tx), (dw, tw) = hr.norm_rope_backward(do, x, ww, pos, axes, fr, True, EPS)
+            tr.assert_close(got[i], dx, tx)
+            if ww is None:
+                assert got[2 + i] is None
+            else:
+                tr.assert_close(got[2 + i], dw, tw)
+    buf = torch.full((40,), 7.0, device=DEV)
+    a = mbx.qk_norm_rope_backward(dq, None, q, None, w, None, pos, fr, axes, dwq=buf[4:36])
+    b = mbx.qk_norm_rope_backward(dq, None, q, None, w, None, pos, fr, axes)
+    assert torch.equal(a[2], b[2]) and (buf[:4] == 7.0).all() and (buf[36:] == 7.0).all()
