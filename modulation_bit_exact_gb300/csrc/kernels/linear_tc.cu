@@ -289,10 +289,13 @@ __device__ __noinline__ float odd_products(const TcParams& p, int row, int64_t n
     return sum;
 }
 
-__device__ __forceinline__ void store_output(const TcParams& p, int row, int64_t n, float sum, float gs) {
+__device__ __forceinline__ float bias_of(const TcParams& p, int64_t n) {
+    return !p.l.bias || n >= p.l.N ? 0.0f
+           : p.l.bias_f32 ? load_elem(static_cast<const float*>(p.l.bias) + n) : load_elem(static_cast<const uint16_t*>(p.l.bias) + n);
+}
+__device__ __forceinline__ void store_output(const TcParams& p, int row, int64_t n, float sum, float gs, float bias) {
     float v = sum / gs;
-    if (p.l.bias) v += p.l.bias_f32 ? load_elem(static_cast<const float*>(p.l.bias) + n)
-                                    : load_elem(static_cast<const uint16_t*>(p.l.bias) + n);
+    if (p.l.bias) v += bias;
     const int64_t at = (int64_t)row * p.l.out_stride + n;
     if (p.out_f32) store_elem(static_cast<float*>(p.l.out) + at, v);
     else store_elem(static_cast<uint16_t*>(p.l.out) + at, v);
@@ -504,9 +507,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
         const float gs = p.slices == 1 ? *p.l.gs : 1.0f;
         for (int t = 0; t < my_tiles; ++t) {
             const int a = t & 1;
+            const int64_t n = (int64_t)(group + t * p.groups) * kTile + threadIdx.x % 128;
+            const float bias = p.slices == 1 ? bias_of(p, n) : 0.0f;
             const bool ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.acc_full[a]), (t / 2) & 1, failed));
             tc_fence_after();
-            const int64_t n = (int64_t)(group + t * p.groups) * kTile + threadIdx.x % 128;
             const uint32_t acc = tmem + a * kAccCols + ((uint32_t)(warp % 4 * 32) << 16);
             for (int r = warp / 4 * 2; r < rows; r += 8) {
                 uint32_t d[16];
@@ -529,7 +533,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
                     if (sh.rows.odd[r + h]) s += odd_products(p, row, n, blk0, blk1);
                     if (!ok) s = __uint_as_float(0x7fffffffu);
                     if (p.slices > 1) p.l.ws[((int64_t)slice * p.l.rows + row) * p.l.N + n] = s;
-                    else store_output(p, row, n, s, gs);
+                    else store_output(p, row, n, s, gs, bias);
                 }
             }
             __syncwarp();
@@ -586,12 +590,14 @@ __global__ void __launch_bounds__(64 * kMaxPieces) linear_digits_kernel(const Tc
 
 // out = the slices' sums, in order, over gs, and the bias
 __global__ void __launch_bounds__(256) linear_join_kernel(const TcParams p) {
+    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    // the product's blocks let this one begin when all before them had finished, so what
+    // they do not write is here
+    const float gs = *p.l.gs, bias = bias_of(p, n);
     grid_dep_wait();
     grid_dep_launch();
-    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (n >= p.l.N) return;
     const int row = blockIdx.y;
-    const float gs = *p.l.gs;
     const float* w = p.l.ws + (int64_t)row * p.l.N + n;
     float s = 0.0f;
     for (int i0 = 0; i0 < p.slices; i0 += 8) {  // eight loads under way
@@ -601,7 +607,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const TcParams p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) s += v[i];
     }
-    store_output(p, row, n, s, gs);
+    store_output(p, row, n, s, gs, bias);
 }
 
 // ---------------------------------------------------------------- launch
