@@ -16,7 +16,7 @@ namespace mbx {
 // The cheapest division by a model in steps of a warp (a head of each of its groups):
 // a round of tokens costs its steps and 2.5 more, for the angles and the chain of
 // one token's work, and a quarter for each further token of a warp.
-QkShare qk_share(const RopeParams& r, int64_t most, int groups) {
+QkShare qk_share(const RopeParams& r, int64_t most, int groups, bool may_be_together) {
     const int64_t total = r.batch * r.tokens;
     QkShare best = {};
     double cost = 1e30;
@@ -50,6 +50,19 @@ QkShare qk_share(const RopeParams& r, int64_t most, int groups) {
             best.wpt = wpt;
         }
     }
+    if (may_be_together && r.k.heads && r.q.heads + r.k.heads <= groups) {
+        QkDeal d = {};
+        d.tpw = groups / (r.q.heads + r.k.heads);
+        const int64_t per = kQkWarps * d.tpw, need = (total + per - 1) / per;
+        d.blocks = (int)(need < most ? need : most);
+        const double c = (double)((need + d.blocks - 1) / d.blocks) * (3.5 + 0.25 * (d.tpw - 1));
+        if (c <= cost) {
+            best.q = d;
+            best.k = QkDeal{0, d.tpw};
+            best.wpt = 1;
+            best.together = true;
+        }
+    }
     best.by_tokens = make_fastdiv((unsigned)r.tokens);
     return best;
 }
@@ -65,7 +78,7 @@ __global__ void __launch_bounds__(32 * kQkWarps, kQkBlocks)
     extern __shared__ uint4 smem[];  // [warps][stages] slots, the pairs' frequencies, [tokens of the block][pairs]
     const RopeParams& r = p.rope;
     const int G = GT ? GT : g, groups = 32 / G, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const QkPlace at(sh, r.q.heads, r.k.heads, G, groups);
+    const QkPlace at(sh, r.q.heads, r.k.heads, G, groups, Bool<true>());
     const RopeTensor& t = at.k ? r.k : r.q;
     const unsigned tokens = (unsigned)r.tokens, total = (unsigned)r.batch * tokens;
     const Head head(lane % G, G, r.hd, r.pairs);
@@ -126,7 +139,7 @@ static cudaError_t forward(const QkNormParams& p, bool f32, int align, cudaStrea
     return for_head_shape<16, 8, INTERLEAVED>(shape, f32, [&](auto t, auto inter, auto w, auto u, auto vec, auto gt) {
         using Head = HeadUnits<decltype(t), decltype(inter)::value, decltype(w)::value, decltype(u)::value, decltype(vec)::value>;
         constexpr int kStages = forward_stages(Head::E * decltype(u)::value * (int)sizeof(t));
-        const QkShare sh = qk_share(r, kQkBlocks * (int64_t)sm_count(), 32 / shape.g);
+        const QkShare sh = qk_share(r, kQkBlocks * (int64_t)sm_count(), 32 / shape.g, true);
         auto* k = qk_norm_rope_kernel<decltype(t), decltype(inter)::value, decltype(w)::value, decltype(u)::value,
                                       decltype(vec)::value, decltype(gt)::value>;
         const int most = sh.q.tpw > sh.k.tpw ? sh.q.tpw : sh.k.tpw;

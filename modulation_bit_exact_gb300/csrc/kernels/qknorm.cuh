@@ -17,6 +17,11 @@
 
 namespace mbx {
 
+template <int V>
+using Int = std::integral_constant<int, V>;
+template <bool V>
+using Bool = std::integral_constant<bool, V>;
+
 // The angles.  Position * frequency / (2 pi) turns, modulo a turn, in 64-bit fixed
 // point: the product of the frequency's 53 bits with 64 bits of 1 / (2 pi) is formed
 // once in a block for each pair, that with the position for each token, in integers,
@@ -441,9 +446,13 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// How tokens and heads are dealt out.  Blocks of kQkWarps warps; Q and K have blocks of
-// their own.  Either `wpt` warps (a power of two) share a token, or, where a warp has
-// room for the heads of several tokens, it takes `tpw` of them at a time.
+// How tokens and heads are dealt out.  Blocks of kQkWarps warps.  Q and K have blocks of
+// their own; either `wpt` warps (a power of two) share a token, or, where a warp has room
+// for the heads of several tokens, it takes `tpw` of them at a time.  Where it has room
+// for those of Q and of K the forward call takes both (`together`: all blocks are q's),
+// with the angles made once (65536 tokens of 1 + 1 heads of 128: 53 us apart, 37
+// together; the gradients lose more by lanes of one warp that have different tensors:
+// 1 + 1 heads 67 -> 57 us, but 16 + 16 of 256 144 -> 154).
 constexpr int kQkWarps = 8, kQkBlocks = 2;  // two blocks an SM: with a third the 80 registers a thread spill
 struct QkDeal {
     int blocks, tpw;  // of a tensor
@@ -451,10 +460,11 @@ struct QkDeal {
 struct QkShare {
     QkDeal q, k;
     int wpt;
+    bool together;
     FastDiv by_tokens;
 };
 // For `most` blocks and `groups` heads side by side in a warp.
-QkShare qk_share(const RopeParams& r, int64_t most, int groups);
+QkShare qk_share(const RopeParams& r, int64_t most, int groups, bool may_be_together);
 
 __device__ __forceinline__ unsigned batch_of(unsigned tok, const FastDiv& d) { return (unsigned)((tok * d.m) >> d.shift); }
 
@@ -467,7 +477,9 @@ struct QkPlace {
     unsigned tok, stride;  // of this lane
     int h0, h_first, step;
     bool part;            // the lane's group takes part
-    __device__ __forceinline__ QkPlace(const QkShare& sh, int heads_q, int heads_k, int G, int groups) {
+    template <bool TOGETHER>
+    __device__ __forceinline__ QkPlace(const QkShare& sh, int heads_q, int heads_k, int G, int groups, Bool<TOGETHER>) {
+        const bool together = TOGETHER && sh.together;
         const int warp = threadIdx.x / 32, group = threadIdx.x % 32 / G;
         // the blocks of K are spread evenly among those of Q (gradients of 2 x 4352 x
         // (24 + 24) heads of 128: 66 us with K's after Q's, 60 so)
@@ -478,13 +490,23 @@ struct QkPlace {
         tpw = k ? sh.k.tpw : sh.q.tpw;
         slot = warp / sh.wpt;
         share = warp % sh.wpt;
-        const int heads = k ? heads_k : heads_q;
-        sub = tpw > 1 ? group / heads : 0;
-        part = tpw > 1 ? sub < tpw : group < groups;
-        if (!part) sub = 0;
-        h_first = share * groups;
-        h0 = tpw > 1 ? group - sub * heads : h_first + group;
         step = groups * sh.wpt;
+        h_first = share * groups;
+        if (together || tpw > 1) {  // group = (token, head)
+            const int heads = together ? heads_q + heads_k : k ? heads_k : heads_q;
+            sub = group / heads;
+            h0 = group - sub * heads;
+            part = sub < tpw;
+            if (together && h0 >= heads_q) {
+                k = true;
+                h0 -= heads_q;
+            }
+        } else {
+            sub = 0;
+            h0 = h_first + group;
+            part = group < groups;
+        }
+        if (!part) sub = 0;
         const int per_block = kQkWarps / sh.wpt * tpw;
         tok = block * per_block + slot * tpw + sub;
         stride = blocks * per_block;
@@ -669,11 +691,6 @@ inline HeadShape head_shape(int hd, int n, bool f32, bool interleaved, int align
 
 // Calls f with a head's shape as types: the element, and Int or Bool of INTERLEAVED, W,
 // U, VEC and the group (0: as given).
-template <int V>
-using Int = std::integral_constant<int, V>;
-template <bool V>
-using Bool = std::integral_constant<bool, V>;
-
 template <int kElems, int kWidest, bool INTERLEAVED, class F>
 cudaError_t for_head_shape(const HeadShape& s, bool f32, F&& f) {
     auto with_g = [&](auto t, auto inter, auto w, auto u, auto v) {

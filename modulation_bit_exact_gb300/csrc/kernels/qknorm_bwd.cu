@@ -22,7 +22,7 @@ __global__ void __launch_bounds__(32 * kQkWarps, kQkBlocks)
     extern __shared__ uint4 smem[];  // [warps][stages][2] slots, the pairs' frequencies, [tokens of the block][pairs]
     const RopeParams& r = p.rope;
     const int G = GT ? GT : g, groups = 32 / G, hd = r.hd, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const QkPlace at(sh, r.q.heads, r.k.heads, G, groups);
+    const QkPlace at(sh, r.q.heads, r.k.heads, G, groups, Bool<false>());
     const RopeTensor& t = at.k ? r.k : r.q;
     const GradIn& d = p.dout[at.k];
     const unsigned tokens = (unsigned)r.tokens, total = (unsigned)r.batch * tokens;
@@ -147,7 +147,7 @@ static cudaError_t backward(const QkNormParams& p, bool f32, int align, ColSumPa
     return for_head_shape<8, kWidest, INTERLEAVED>(shape, f32, [&](auto t, auto inter, auto w, auto u, auto vec, auto gt) {
         using Head = HeadUnits<decltype(t), decltype(inter)::value, decltype(w)::value, decltype(u)::value, decltype(vec)::value>;
         constexpr int kStages = grad_stages(Head::E * decltype(u)::value * (int)sizeof(t));
-        const QkShare sh = qk_share(r, kQkBlocks * (int64_t)sm_count(), 32 / shape.g);
+        const QkShare sh = qk_share(r, kQkBlocks * (int64_t)sm_count(), 32 / shape.g, false);
         sums.parts = sh.q.blocks > sh.k.blocks ? sh.q.blocks : sh.k.blocks;
         auto* k = qk_norm_rope_bwd_kernel<decltype(t), decltype(inter)::value, decltype(w)::value, decltype(u)::value,
                                           decltype(vec)::value, decltype(gt)::value>;
