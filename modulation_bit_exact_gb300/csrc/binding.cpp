@@ -377,8 +377,9 @@ PyObject* rope_axes(PyObject* const* a) {
     return wrap2(qo, ko);
 }
 
-// An uninitialised tensor of t's shape, dtype and order of dimensions.  at::empty costs a
-// call 3 us less than at::empty_like, and gives the same where the order is the usual one.
+// An uninitialised tensor of t's shape, dtype and order of dimensions, as at::empty_like
+// makes it; at::empty costs less (the norm and rotation of 24 tokens, two outputs: 9.2 us
+// a call with the one, 7.3 with the other).
 at::Tensor heads_like(const at::Tensor& t) {
     const auto z = t.sizes();
     const auto s = t.strides();

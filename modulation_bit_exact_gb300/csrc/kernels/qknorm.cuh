@@ -6,9 +6,9 @@
 // are the access at j and the one at j+n; elements past the pairs come two
 // accesses a unit.  With W = 1 a unit is one pair, or two elements that pass.
 // A group of G lanes has the head's units, unit lane + G*u in place u < U, so a row
-// sum is a chain within the lane and a tree over the group.  W, G and U follow the head's size, its pairs and the
-// type alone: where a head lies decides only whether an access is one load
-// or one for each element, so its bits are the same at any address.
+// sum is a chain within the lane and a tree over the group.  W, G and U follow the
+// head's size, its pairs and the type alone: where a head lies decides only whether an
+// access is one load or one for each element, so its bits are the same at any address.
 #pragma once
 
 #include <type_traits>
@@ -27,7 +27,7 @@ using Bool = std::integral_constant<bool, V>;
 // once in a block for each pair, that with the position for each token, in integers,
 // so no position loses anything and the little binary64 that this GPU has is not used
 // (65536 tokens of one head of 128 each for Q and K, whose angles are most of the
-// work: 121 us with binary64, 89 in integers, the frequency's part for each token).
+// work: 121 us with binary64, 89 in integers, 37 with what else is shared now).
 struct PairFreq {
     uint64_t hi, lo;  // whole positions: hi = the step of one position in 2^-64 turns; others: the 128-bit product
     int sh;           // its place: turns * 2^64 = hi:lo >> sh
