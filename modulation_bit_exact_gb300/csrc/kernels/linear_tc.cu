@@ -38,8 +38,13 @@
 namespace mbx {
 
 constexpr int kTile = 128, kPiece = 256, kMaxPieces = 8, kPassRows = 16, kMaxStages = 15;
-constexpr int kWorkers = 512, kTcThreads = kWorkers + 64;  // then the copying warp and the multiplying one
-constexpr int kCopyWarp = kWorkers / 32, kMmaWarp = kCopyWarp + 1;
+// Warps: the workers, the multiplying one, those that copy.  Weight rows at 16-byte
+// boundaries are copied by TMA, rows at 8-byte ones (K / 2 an odd multiple of 8) by four
+// warps, 8 bytes a lane.
+constexpr int kWorkers = 512, kMmaWarp = kWorkers / 32, kCopyWarp = kMmaWarp + 1;
+constexpr int copy_threads(bool tma) { return tma ? 32 : 128; }
+constexpr int tc_threads(bool tma) { return kWorkers + 32 + copy_threads(tma); }
+constexpr int kLag = 4;  // pieces that the copying warps leave under way before they pass one on
 constexpr int kFirstStages = 3;  // copied before the block meets; a copy takes 0.1 us to issue
 constexpr int kStageBytes = 16384, kStageScales = 2048;
 constexpr int kMaxSmem = 227 * 1024;
@@ -318,7 +323,8 @@ struct TcShared {
     SliceRows rows;
 };
 
-__global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_constant__ CUtensorMap map, const TcParams p) {
+template <bool TMA>
+__global__ void __launch_bounds__(tc_threads(TMA), 1) linear_tc_kernel(const __grid_constant__ CUtensorMap map, const TcParams p) {
     extern __shared__ uint8_t raw_smem[];
     uint8_t* smem = raw_smem + ((1024u - (smem_addr(raw_smem) & 1023u)) & 1023u);
     __shared__ TcShared sh;
@@ -337,19 +343,41 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
 
     volatile int* failed = &sh.failed;
     const int total = my_tiles * (piece1 - piece0);  // pieces of weight that this block takes
-    auto fetch = [&](int u) {                         // the u-th, into stage u % stages
+    const int copier = (int)threadIdx.x - kCopyWarp * 32;  // of the copying threads
+    auto fetch = [&](int u) {                              // the u-th, into stage u % stages
         const int t = u / (piece1 - piece0), piece = piece0 + u - t * (piece1 - piece0), tile = group + t * p.groups;
         const int s = u % p.stages;
         const uint32_t bar = smem_addr(&sh.full[s]), bytes = (uint32_t)min(4, p.l.sf_col_tiles - piece * 4) * 512;
-        bar_expect(bar, kStageBytes + bytes);
-        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-                         smem_addr(ring + s * kStageBytes)),
-                     "l"(&map), "r"(piece * 128), "r"(tile * kTile), "r"(bar)
-                     : "memory");
-        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                         smem_addr(scales + s * kStageScales)),
-                     "l"(p.l.sf + ((int64_t)tile * p.l.sf_col_tiles + piece * 4) * 512), "r"(bytes), "r"(bar)
-                     : "memory");
+        if (copier == 0) {
+            bar_expect(bar, (TMA ? kStageBytes : 0) + bytes);
+            if constexpr (TMA)
+                asm volatile(
+                    "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                        smem_addr(ring + s * kStageBytes)),
+                    "l"(&map), "r"(piece * 128), "r"(tile * kTile), "r"(bar)
+                    : "memory");
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             smem_addr(scales + s * kStageScales)),
+                         "l"(p.l.sf + ((int64_t)tile * p.l.sf_col_tiles + piece * 4) * 512), "r"(bytes), "r"(bar)
+                         : "memory");
+        }
+        if constexpr (!TMA) {
+            // sixteen lanes a row, 32 rows a warp; in the order of the 128-byte swizzle, 0
+            // past the weight
+            const int half = copier % 32 / 16, c = copier % 16, row = copier / 32 * 32 + half;
+            const int64_t n = (int64_t)tile * kTile + row;
+            const uint8_t* from = p.l.w4 + n * p.l.w_stride + piece * 128 + c * 8;
+            const bool in = piece * 128 + c * 8 < p.l.K / 2;
+            const uint32_t to = smem_addr(ring + s * kStageBytes) + row * 128 + c % 2 * 8;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int size = in && n + 2 * i < p.l.N ? 8 : 0;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + i * 256 + ((c / 2 ^ (row + 2 * i) % 8) * 16)),
+                             "l"(size ? from + i * 2 * p.l.w_stride : p.l.w4), "r"(size)
+                             : "memory");
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
     };
     // the worker's quarters of blocks of activations, 0 past K: the c-th is quarter
     // id % 4 of block id / 4, id = c * kWorkers + thread
@@ -361,10 +389,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
         for (int i = 0; i < 4; ++i) v[c][i] = 0.0f;
     const uint8_t* image = p.images ? p.images + ((int64_t)blockIdx.y * p.slices + slice) * p.image_bytes : nullptr;
 
-    if (warp == kCopyWarp) {
-        if (lane == 0) {
+    if (warp >= kCopyWarp) {
+        if (copier == 0) {
             for (int i = 0; i < p.stages; ++i) {
-                bar_init(smem_addr(&sh.full[i]), 1);
+                bar_init(smem_addr(&sh.full[i]), TMA ? 1 : 1 + copy_threads(false));
                 bar_init(smem_addr(&sh.empty[i]), 1);
             }
             for (int i = 0; i < 2; ++i) {
@@ -375,10 +403,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
             bar_init(smem_addr(&sh.digits), 1);
             sh.failed = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        if (!TMA || copier == 0) {
             // the kernel that made the digits began when all before it had finished
             if (!p.images) grid_dep_wait();
             for (int u = 0; u < kFirstStages && u < p.stages && u < total; ++u) fetch(u);
-            if (p.images) {
+            if (p.images && copier == 0) {
                 grid_dep_wait();
                 const uint32_t bytes = p.pieces_per_slice * (cols * 128 + 2048);
                 bar_expect(smem_addr(&sh.digits), bytes);
@@ -412,12 +442,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
     const uint32_t tmem = sh.tmem;
     grid_dep_launch();
 
-    if (warp == kCopyWarp) {
-        if (lane == 0) {
-            int u = min(kFirstStages, p.stages);
+    if (warp >= kCopyWarp) {
+        if (!TMA || copier == 0) {
+            int u = min(kFirstStages, min(p.stages, total)), passed = 0;
+            auto pass = [&](int until) {  // this thread's copies of the pieces before `until` have landed
+                fence_async();
+                for (; passed < until; ++passed) bar_arrive(smem_addr(&sh.full[passed % p.stages]));
+            };
             for (; u < total; ++u) {
                 if (u >= p.stages && !bar_wait(smem_addr(&sh.empty[u % p.stages]), (u / p.stages - 1) & 1, failed)) break;
                 fetch(u);
+                if constexpr (!TMA) {
+                    // a ring of no more stages than are left under way would wait for itself
+                    if (p.stages <= kLag) {
+                        asm volatile("cp.async.wait_group 0;" ::: "memory");
+                        pass(u + 1);
+                    } else if (u >= kLag) {
+                        asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
+                        pass(u + 1 - kLag);
+                    }
+                }
+            }
+            if constexpr (!TMA) {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                pass(u);
             }
             // after a failure: the copies that are under way have to land before the block ends
             if (*failed && p.images) bar_wait(smem_addr(&sh.digits), 0, failed);
@@ -427,7 +475,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
                     }
         }
         __syncwarp();
-    } else if (warp < kCopyWarp && !p.images) {
+    } else if (warp < kMmaWarp && !p.images) {
         uint32_t block[kQuarters];
 #pragma unroll
         for (int c = 0; c < kQuarters; ++c) {
@@ -511,7 +559,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
             bar_wait(smem_addr(&sh.drained), 0, failed);
         }
         __syncwarp();
-    } else if (warp < kCopyWarp) {
+    } else if (warp < kMmaWarp) {
         const float gs = p.slices == 1 ? *p.l.gs : 1.0f;
         for (int t = 0; t < my_tiles; ++t) {
             const int a = t & 1;
@@ -638,10 +686,13 @@ static EncodeTiled encode_tiled() {
     return fn;
 }
 
-// The tensor map wants the weight's rows at multiples of 16 bytes, the copies of scales too.
+// The tensor map wants the weight's rows at multiples of 16 bytes, the copying warps at
+// multiples of 8, the copies of scales 16.
+static bool rows_at(const LinearParams& p, int bytes) {
+    return reinterpret_cast<uintptr_t>(p.w4) % bytes == 0 && (p.N == 1 || p.w_stride % bytes == 0);
+}
 bool linear_tc_takes(const LinearParams& p) {
-    return tc_plan(p.N, p.K).slices > 0 && reinterpret_cast<uintptr_t>(p.w4) % 16 == 0 && (p.N == 1 || p.w_stride % 16 == 0) &&
-           reinterpret_cast<uintptr_t>(p.sf) % 16 == 0;
+    return tc_plan(p.N, p.K).slices > 0 && rows_at(p, 8) && reinterpret_cast<uintptr_t>(p.sf) % 16 == 0;
 }
 
 template <class... KArgs, class... Args>
@@ -669,7 +720,8 @@ cudaError_t launch_linear_tc(const LinearParams& l, bool x_f32, bool out_f32, cu
     constexpr int kFixed = (int)sizeof(TcShared) + 256;  // the static part, rounded up
     constexpr int kMost = kMaxSmem - kFixed;
     if (!allowed[dev].load(std::memory_order_acquire)) {
-        if (cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost)) return e;
+        if (cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost)) return e;
+        if (cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost)) return e;
         allowed[dev].store(true, std::memory_order_release);
     }
     const TcPlan plan = tc_plan(l.N, l.K);
@@ -690,16 +742,19 @@ cudaError_t launch_linear_tc(const LinearParams& l, bool x_f32, bool out_f32, cu
     if (p.stages > work) p.stages = work;
     const size_t smem = 1024 + dig + (size_t)p.stages * (kStageBytes + kStageScales);
 
-    EncodeTiled encode = encode_tiled();
-    if (!encode) return cudaErrorNotSupported;
-    CUtensorMap map;
-    const cuuint64_t dims[2] = {(cuuint64_t)l.K / 2, (cuuint64_t)l.N};
-    const cuuint64_t strides[1] = {(cuuint64_t)(l.N > 1 ? l.w_stride : (l.K / 2 + 15) / 16 * 16)};
-    const cuuint32_t box[2] = {128, kTile}, one[2] = {1, 1};
-    if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(l.w4), dims, strides, box, one,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
+    const bool tma = rows_at(l, 16);
+    CUtensorMap map = {};
+    if (tma) {
+        EncodeTiled encode = encode_tiled();
+        if (!encode) return cudaErrorNotSupported;
+        const cuuint64_t dims[2] = {(cuuint64_t)l.K / 2, (cuuint64_t)l.N};
+        const cuuint64_t strides[1] = {(cuuint64_t)(l.N > 1 ? l.w_stride : (l.K / 2 + 15) / 16 * 16)};
+        const cuuint32_t box[2] = {128, kTile}, one[2] = {1, 1};
+        if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(l.w4), dims, strides, box, one,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
     const unsigned passes = (unsigned)((l.rows + kPassRows - 1) / kPassRows);
     if (digits_before(plan, l.rows)) {
         p.images = reinterpret_cast<uint8_t*>(l.ws) + sums_bytes(plan, l.rows, l.N);
@@ -707,7 +762,8 @@ cudaError_t launch_linear_tc(const LinearParams& l, bool x_f32, bool out_f32, cu
         const unsigned threads = (unsigned)plan.pieces_per_slice * 64;
         if (cudaError_t e = launch2(linear_digits_kernel, dim3((unsigned)plan.slices, (unsigned)l.rows), threads, 0, s, p)) return e;
     }
-    const cudaError_t e = launch2(linear_tc_kernel, dim3((unsigned)(p.slices * p.groups), passes), kTcThreads, smem, s, map, p);
+    const cudaError_t e = launch2(tma ? linear_tc_kernel<true> : linear_tc_kernel<false>, dim3((unsigned)(p.slices * p.groups), passes),
+                                  tc_threads(tma), smem, s, map, p);
     if (e != cudaSuccess || p.slices == 1) return e;
     return launch2(linear_join_kernel, dim3((unsigned)((l.N + 255) / 256), (unsigned)l.rows), 256, 0, s, p);
 }
