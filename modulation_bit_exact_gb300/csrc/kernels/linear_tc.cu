@@ -16,9 +16,9 @@
 //
 // A block of threads keeps the digits of one slice of K (up to 8 pieces of 256) and
 // walks the tiles of 128 outputs of its group; the slices' sums are added in order
-// by a second kernel.  One warp copies and one multiplies; the sixteen others make the
-// digits, while the first weights are on their way, and then read the accumulators
-// and write, each four of them a quarter of the rows.
+// by a second kernel.  One warp copies (or eight do) and one multiplies; the sixteen
+// others make the digits, while the first weights are on their way, and then read the
+// accumulators and write, each four of them a quarter of the rows.
 //
 // Floor: the weight's bytes, 9/16 of one a value.  Steady state, [1, 5120] x [245760,
 // 5120]: 106.5 us, 6.6 TB/s, 0.99 of what a copy reaches.  [1, 5120] x [30720, 5120]:
@@ -39,12 +39,14 @@ namespace mbx {
 
 constexpr int kTile = 128, kPiece = 256, kMaxPieces = 8, kPassRows = 16, kMaxStages = 15;
 // Warps: the workers, the multiplying one, those that copy.  Weight rows at 16-byte
-// boundaries are copied by TMA, rows at 8-byte ones (K / 2 an odd multiple of 8) by four
-// warps, 8 bytes a lane.
+// boundaries are copied by TMA, rows at 8-byte ones (K / 2 an odd multiple of 8) by eight
+// warps, 8 bytes a lane ([1, 5136] x [30720, 5136]: four warps 35.5 us, eight 30.8, the
+// copies' instructions the bound; with 4 pieces under way in place of 2 31.1, for 16 rows
+// 54 against 41).
 constexpr int kWorkers = 512, kMmaWarp = kWorkers / 32, kCopyWarp = kMmaWarp + 1;
-constexpr int copy_threads(bool tma) { return tma ? 32 : 128; }
+constexpr int copy_threads(bool tma) { return tma ? 32 : 256; }
 constexpr int tc_threads(bool tma) { return kWorkers + 32 + copy_threads(tma); }
-constexpr int kLag = 4;  // pieces that the copying warps leave under way before they pass one on
+constexpr int kLag = 2;  // pieces that the copying warps leave under way before they pass one on
 constexpr int kFirstStages = 3;  // copied before the block meets; a copy takes 0.1 us to issue
 constexpr int kStageBytes = 16384, kStageScales = 2048;
 constexpr int kMaxSmem = 227 * 1024;
@@ -362,15 +364,16 @@ __global__ void __launch_bounds__(tc_threads(TMA), 1) linear_tc_kernel(const __g
                          : "memory");
         }
         if constexpr (!TMA) {
-            // sixteen lanes a row, 32 rows a warp; in the order of the 128-byte swizzle, 0
-            // past the weight
-            const int half = copier % 32 / 16, c = copier % 16, row = copier / 32 * 32 + half;
+            // sixteen lanes a row, a share of the rows a warp; in the order of the 128-byte
+            // swizzle, 0 past the weight
+            constexpr int kRows = kTile * 32 / copy_threads(false);  // of a warp
+            const int half = copier % 32 / 16, c = copier % 16, row = copier / 32 * kRows + half;
             const int64_t n = (int64_t)tile * kTile + row;
             const uint8_t* from = p.l.w4 + n * p.l.w_stride + piece * 128 + c * 8;
             const bool in = piece * 128 + c * 8 < p.l.K / 2;
             const uint32_t to = smem_addr(ring + s * kStageBytes) + row * 128 + c % 2 * 8;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < kRows / 2; ++i) {
                 const int size = in && n + 2 * i < p.l.N ? 8 : 0;
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + i * 256 + ((c / 2 ^ (row + 2 * i) % 8) * 16)),
                              "l"(size ? from + i * 2 * p.l.w_stride : p.l.w4), "r"(size)
