@@ -351,10 +351,13 @@ MBX_API int mbx_check_qk_norm_rope_qkv_epilogue(
  * producers' out_sf; not negative; padding bytes are not used), gs = *fp4_scale,
  * read on the stream.
  * x [rows, K] MBX_BF16 or MBX_F32; out [rows, N] of x's dtype or MBX_F32; bias
- * [1, N] of either type or NULL.  One variant: products and sums to binary32's
- * accuracy (x is cut into exact parts where the tensor cores multiply), one
- * rounding at the output.  An infinity or NaN of x reaches the outputs of its
- * own row alone.  K a multiple of 16, at most 8192; rows at most 256 (more are
+ * [1, N] of either type or NULL.  One variant: binary32 products and sums, one
+ * rounding at the output.  Where the tensor cores multiply (rows of w4 at 8-byte
+ * boundaries, w_sf at a 16-byte one), a(x) is taken in whole parts, to 2^-22 of
+ * the largest magnitude of its 16 and to 2^-39 of that of its slice of K (at most
+ * 2048): an output is as near as with binary32 products unless the weights are
+ * zero, or next to it, where x is largest.  An infinity or NaN of x reaches the
+ * outputs of its own row alone.  K a multiple of 16, at most 8192; rows at most 256 (more are
  * a matrix product's work); N at most 2^24.  out overlaps nothing.
  * The workspace (mbx_linear_nvfp4_workspace gives its bytes for the current
  * device; 0: pass NULL) is scratch of one call: 16-byte aligned, overlapping no

@@ -480,13 +480,16 @@ def nvfp4_weight(weight, fp4_scale=None):
     rule of the NVFP4 producers (see mbx_ln_modulate_nvfp4): (w4 [N, K/2] uint8,
     w_sf in the 128x4 tile layout, fp4_scale).  Done once, when a model is
     loaded, with torch operators on weight's device.  fp4_scale: a one-element
-    float32 tensor; by default 448 * 6 / max|weight|."""
+    float32 tensor; by default 448 * 6 / max|weight|, at most 2^118."""
+    if weight.dim() != 2 or weight.shape[1] % 16:
+        raise MbxError(-5, "MBX_E_SHAPE: the weight must have two dimensions, the last a multiple of 16")
+    if not weight.numel():
+        raise MbxError(-3, "MBX_E_EMPTY: the weight has no elements")
     N, K = weight.shape
-    if K % 16:
-        raise MbxError(-5, "MBX_E_SHAPE: the weight's last dimension must be a multiple of 16")
     if fp4_scale is None:
         amax = weight.detach().abs().amax().float()
-        fp4_scale = torch.where(amax > 0, 2688.0 / amax, torch.ones_like(amax)).reshape(1)
+        # over the least block scale, 2^-9, a larger one than 2^118 is no float32
+        fp4_scale = torch.where(amax > 0, (2688.0 / amax).clamp(max=2.0 ** 118), torch.ones_like(amax)).reshape(1)
     b = weight.detach().float().reshape(N, K // 16, 16)
     s = (b.abs().amax(-1) * fp4_scale / 6.0).clamp(max=448.0).to(torch.float8_e4m3fn)
     sf = s.float()

@@ -8,8 +8,12 @@
 // |I| <= 2^22, and I = sum over i < 8 of d_i * 8^i with digits d_i from -4 to 3, whose halves
 // are E2M1 values.  The block's 2^e, as far as 2^-17 of the row's largest, is the
 // block's E4M3 scale.  A row of x becomes eight columns of the product, one a
-// digit, whose sums the epilogue adds up by their powers of 8: the accuracy is that
-// of binary32 products, and one to sixteen rows cost the same, 8 to 128 columns.
+// digit, whose sums the epilogue adds up by their powers of 8, and one to sixteen rows
+// cost the same, 8 to 128 columns.  The one rounding that binary32 products do not
+// have: a value is taken to 2^-22 of the largest of its 16, or 2^-39 of its row's.  Beside
+// the product of that largest value it is as small as their roundings; an output whose
+// weight there is zero has it beside its other products.  Sixteen digits would take
+// 256 columns for sixteen rows, and the tensor memory holds no two such accumulators.
 //
 // An infinity or NaN has no digits: it counts as 0 there, and the epilogue adds its
 // products, from the weight in memory, to the outputs of its row.

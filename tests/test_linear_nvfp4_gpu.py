@@ -138,6 +138,26 @@ def test_values_far_apart(mbx, K, dt):
 
 
 @pytest.mark.parametrize("K", [1024, 1040])
+@pytest.mark.parametrize("far", [2.0 ** 10, 2.0 ** 20, 2.0 ** 40])
+def test_weights_that_are_zero_where_x_is_largest(mbx, K, far):
+    """Such an output has the parts' stated precision: of its 16 values, and of the row."""
+    g = gen(14)
+    w4, sf, gs = weight(mbx, g, 140, K)
+    x = torch.randn((3, K), generator=g)
+    x[1:, 40] = far
+    w4[:, 20] = 0  # elements 40 and 41
+    x = x.bfloat16().to(DEV)
+    got = check(mbx, x, (w4, sf, gs), None, False)
+    assert got.isfinite().all() and torch.equal(got[1:2], mbx.linear_nvfp4(x[1:2], w4, sf, gs))
+    # rows of the fallback have no parts: binary32 products at any distance
+    out = mbx.linear_nvfp4(x.float(), torch.nn.functional.pad(w4, (1, 3))[:, 1:-3], sf, gs)
+    wa = lr.weight(w4, sf)
+    a = x.double().cpu()
+    err = (out.double().cpu() - a @ wa.t() / float(gs)).abs()
+    assert (err <= (48 + 4) * tr.U * (a.abs() @ wa.abs().t()) / float(gs)).all()
+
+
+@pytest.mark.parametrize("K", [1024, 1040])
 @pytest.mark.parametrize("silu", [False, True])
 def test_infinities_and_nan_stay_in_their_row(mbx, K, silu):
     g = gen(4)

@@ -105,3 +105,25 @@ def test_weight_is_the_oracles_copy(mbx, orc, N, K):  # noqa: F811
 def test_zero_weight(mbx):  # noqa: F811
     w4, sf, s = mbx.nvfp4_weight(torch.zeros(3, 32))
     assert s.item() == 1.0 and not w4.any() and not sf.any()
+
+
+@pytest.mark.parametrize("largest", [1e-30, 1e-33, 1e-37, 1e-44])
+def test_weight_next_to_zero(mbx, largest):  # noqa: F811
+    """The global scale and its quotient by the least block scale stay finite; zero blocks stay zero."""
+    w = torch.randn((5, 48), generator=torch.Generator().manual_seed(1))
+    w = (w / w.abs().max() * largest).float()
+    w[2, 16:32] = 0.0
+    w4, sf, s = mbx.nvfp4_weight(w)
+    assert 0 < s.item() <= 2.0 ** 118
+    got = lr.weight(w4, sf) / float(s)
+    assert got.isfinite().all() and not got[2, 16:32].any()
+    # as above: half the widest step of a scale at most 1/16 off, or 2^-10 below e4m3's smallest normal
+    lim = w.double().abs().max() * (17 / 16) / 6 + 6 * 2.0 ** -10 / float(s)
+    assert ((got - w.double()).abs() <= lim).all()
+
+
+def test_weight_refusals(mbx):  # noqa: F811
+    for shape, status in (((32,), -5), ((2, 4, 32), -5), ((0, 32), -3), ((4, 0), -3)):
+        with pytest.raises(mbx.MbxError) as e:
+            mbx.nvfp4_weight(torch.zeros(shape))
+        assert e.value.status == status
