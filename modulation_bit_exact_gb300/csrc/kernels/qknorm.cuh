@@ -3,8 +3,9 @@
 //
 // A head is cut into units, one unit of a lane at a time: interleaved pairs lie
 // side by side, so a unit is one access of W elements; pairs in halves (j, j+n)
-// are the access at j and the one at j+n; elements past the pairs come two
-// accesses a unit.  With W = 1 a unit is one pair, or two elements that pass.
+// are the access at j and the one at j+n; of the elements past the pairs a unit has an
+// access of their first half and one of their second, so that lanes side by side have
+// accesses side by side.  With W = 1 a unit is one pair, or two elements that pass.
 // A group of G lanes has the head's units, unit lane + G*u in place u < U, so a row
 // sum is a chain within the lane and a tree over the group.  W, G and U follow the
 // head's size, its pairs and the type alone: where a head lies decides only whether an
@@ -185,11 +186,11 @@ struct HeadUnits {
                 pair0[u] = a * P;
                 turns[u] = min(max(n - pair0[u], 0), P);
             } else {
-                const int nt = n / W;  // units that turn
-                const bool t = a < nt;
-                const int pass = 2 * n + 2 * (a - nt) * W;
-                off0[u] = t ? (INTERLEAVED ? 2 * a : a * W) : (pass < hd ? pass : -1);
-                off1[u] = t ? (INTERLEAVED ? 2 * a + 1 : n + a * W) : (pass + W < hd ? pass + W : -1);
+                const int nt = n / W, np = ((hd - 2 * n) / W + 1) / 2;  // units that turn, that pass
+                const bool t = a < nt, own = a < nt + np;
+                const int pass = 2 * n + (a - nt) * W;
+                off0[u] = t ? (INTERLEAVED ? 2 * a : a * W) : own ? pass : -1;
+                off1[u] = t ? (INTERLEAVED ? 2 * a + 1 : n + a * W) : own && pass + np * W < hd ? pass + np * W : -1;
                 pair0[u] = a * W;
                 turns[u] = t ? W : 0;
             }
