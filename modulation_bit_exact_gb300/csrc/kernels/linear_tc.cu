@@ -232,13 +232,18 @@ __device__ __forceinline__ uint32_t of_four(uint32_t m) {
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
-// e with |v| < 2^e; magnitudes below 2^-85 (of a row) take that.
-__device__ __forceinline__ int above(uint32_t bits) { return (int)(bits >> 23) - 126; }
+// e with |v| < 2^e and, unless v is 0, |v| >= 2^(e-1); -149 of 0.
+__device__ __forceinline__ int above(uint32_t bits) {
+    return bits < 0x800000u ? -117 - __clz((int)bits) : (int)(bits >> 23) - 126;
+}
+// 2^n, n from -126 to 127
+__device__ __forceinline__ float power_of_2(int n) { return __uint_as_float((uint32_t)(127 + n) << 23); }
 
-// The digits of v * 2^(22-e), digit i in nibble i as an E2M1 code of d_i / 2.
-__device__ __forceinline__ uint32_t digits(float v, float to_int) {
+// The digits of the whole number nearest to v, |v| <= 2^22, digit i in nibble i as an
+// E2M1 code of d_i / 2.
+__device__ __forceinline__ uint32_t digits(float v) {
     // digits + 4 are the octal places of I + 044444444, spread from 3 to 4 bits each
-    uint32_t x = (uint32_t)(__float2int_rn(v * to_int) + 9586980);
+    uint32_t x = (uint32_t)(__float2int_rn(v) + 9586980);
     x = (x & 0x00000fffu) | (x & 0x00fff000u) << 4;
     x = (x & 0x003f003fu) | (x & 0x0fc00fc0u) << 2;
     x = (x & 0x07070707u) | (x & 0x38383838u) << 1;
@@ -252,12 +257,13 @@ __device__ __forceinline__ uint32_t digits(float v, float to_int) {
 // swizzled), `scale` its scale (columns 16 bytes apart); b is the block's place in the
 // slice, q the quarter.
 __device__ __forceinline__ void put_digits(const float (&v)[4], uint32_t block, uint32_t most, int b, int q, uint8_t* col, uint8_t* scale) {
-    const int top = max(above(most), -85);
-    const int e = max(min(above(block), top), top - 17);
-    const float to_int = __uint_as_float((uint32_t)(127 + 22 - e) << 23);
+    const int top = above(most), e = max(above(block), top - 17);
+    // 2^(22-e) in two exact steps: for blocks below 2^-104 it is no binary32 number
+    const int up0 = min(22 - e, 126);
+    const float to_int = power_of_2(up0), rest = power_of_2(22 - e - up0);
     uint32_t d[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = digits((__float_as_uint(v[i]) & 0x7f800000u) == 0x7f800000u ? 0.0f : v[i], to_int);
+    for (int i = 0; i < 4; ++i) d[i] = digits((__float_as_uint(v[i]) & 0x7f800000u) == 0x7f800000u ? 0.0f : v[i] * to_int * rest);
     // two values a byte, the first in the low half: bytes of digits 0, 2, 4, 6 and of 1, 3, 5, 7
     uint32_t even[2], odd[2];
 #pragma unroll
@@ -590,8 +596,9 @@ __global__ void __launch_bounds__(tc_threads(TMA), 1) linear_tc_kernel(const __g
                     float s = __uint_as_float(d[8 * h + 7]);
 #pragma unroll
                     for (int i = 6; i >= 0; --i) s = __fmaf_rn(s, 8.0f, __uint_as_float(d[8 * h + i]));
-                    const int top = max(above(sh.rows.most[r + h]), -85);
-                    s *= __uint_as_float((uint32_t)(127 + top - 29) << 23);
+                    // 2^(top-29), the first step exact
+                    const int top = above(sh.rows.most[r + h]), down = max(top - 29, -100);
+                    s = s * power_of_2(down) * power_of_2(top - 29 - down);
                     const int row = row0 + r + h;
                     if (sh.rows.odd[r + h]) s += odd_products(p, row, n, blk0, blk1);
                     if (!ok) s = __uint_as_float(0x7fffffffu);
