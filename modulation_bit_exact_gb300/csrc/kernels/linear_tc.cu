@@ -392,6 +392,17 @@ __global__ void __launch_bounds__(tc_threads(TMA), 1) linear_tc_kernel(const __g
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
     };
+    auto prefetch = [&](int u) {  // the same into L2, as a hint
+        const int t = u / (piece1 - piece0), piece = piece0 + u - t * (piece1 - piece0), tile = group + t * p.groups;
+        if constexpr (TMA) {
+            asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(&map), "r"(piece * 128), "r"(tile * kTile)
+                         : "memory");
+        } else {
+            const int64_t n = (int64_t)tile * kTile + copier;
+            if (copier < kTile && n < p.l.N) prefetch_l2(p.l.w4 + n * p.l.w_stride + piece * 128);
+        }
+        if (copier == 0) prefetch_l2_bulk(p.l.sf + ((int64_t)tile * p.l.sf_col_tiles + piece * 4) * 512, (uint32_t)min(4, p.l.sf_col_tiles - piece * 4) * 512);
+    };
     // the worker's quarters of blocks of activations, 0 past K: the c-th is quarter
     // id % 4 of block id / 4, id = c * kWorkers + thread
     const int per_row = steps * 4, items = rows * per_row;
@@ -418,11 +429,14 @@ __global__ void __launch_bounds__(tc_threads(TMA), 1) linear_tc_kernel(const __g
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         if (!TMA || copier == 0) {
-            // the kernel that made the digits began when all before it had finished
-            if (!p.images) grid_dep_wait();
+            // Nothing is read before the wait.  Where another kernel makes the digits the first
+            // weights are brought into L2 meanwhile, a hint that holds no values ([16, 5120] x
+            // [10007, 5120]: 13.9 us without, 13.6 so), once for all rows.
+            if (p.images && blockIdx.y == 0)
+                for (int u = 0; u < kFirstStages && u < p.stages && u < total; ++u) prefetch(u);
+            grid_dep_wait();
             for (int u = 0; u < kFirstStages && u < p.stages && u < total; ++u) fetch(u);
             if (p.images && copier == 0) {
-                grid_dep_wait();
                 const uint32_t bytes = p.pieces_per_slice * (cols * 128 + 2048);
                 bar_expect(smem_addr(&sh.digits), bytes);
                 asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -661,12 +675,10 @@ __global__ void __launch_bounds__(64 * kMaxPieces) linear_digits_kernel(const Tc
 // out = the slices' sums, in order, over gs, and the bias
 __global__ void __launch_bounds__(256) linear_join_kernel(const TcParams p) {
     const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    // the product's blocks let this one begin when all before them had finished, so what
-    // they do not write is here
-    const float gs = *p.l.gs, bias = bias_of(p, n);
     grid_dep_wait();
     grid_dep_launch();
     if (n >= p.l.N) return;
+    const float gs = *p.l.gs, bias = bias_of(p, n);
     const int row = blockIdx.y;
     const float* w = p.l.ws + (int64_t)row * p.l.N + n;
     float s = 0.0f;
