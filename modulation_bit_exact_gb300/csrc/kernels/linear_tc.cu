@@ -135,22 +135,30 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
                  : "memory");
     return ok;
 }
-// Waits for the phase, for a second and a million tries at most (a block that was off the
-// GPU for that second has the tries left); false, and *failed set, when it did not come or
-// another wait of the block had failed.  Nothing is known to make one fail; the outputs of
-// the tiles that it leaves out are NaN.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
+// Waits for the phase until `ns` have passed and `rounds` of 64 tries (a block that was off
+// the GPU for that time has the tries left); false when it did not come, or when *failed
+// was set meanwhile.
+__device__ __forceinline__ bool bar_wait_while(uint32_t bar, uint32_t parity, unsigned long long ns, int rounds, const volatile int* failed) {
     unsigned long long start = 0, now = 0;
-    for (int i = 0; now - start < 1000000000ull || i < 1 << 14; ++i) {
+    for (int i = 0; now - start < ns || i < rounds; ++i) {
         for (int k = 0; k < 64; ++k)
             if (bar_try(bar, parity)) return true;
-        if (*failed) return false;
+        if (failed && *failed) return false;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
         if (i == 0) start = now;
     }
+    return false;
+}
+// A wait of the block's work, for a second and a million tries: *failed is set when it did
+// not come, and ends the others.  Nothing is known to make one fail; the outputs of the
+// tiles that it leaves out are NaN.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
+    if (bar_wait_while(bar, parity, 1000000000ull, 1 << 14, failed)) return true;
     *failed = 1;
     return false;
 }
+// A wait for what the block has under way when it ends, whatever has failed: a sixteenth of that.
+__device__ __forceinline__ void bar_land(uint32_t bar, uint32_t parity) { bar_wait_while(bar, parity, 62500000ull, 1 << 10, nullptr); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -331,7 +339,7 @@ __device__ __forceinline__ void store_output(const TcParams& p, int row, int64_t
 struct TcShared {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained, digits;
     uint32_t tmem;
-    int failed;
+    int failed, fetched;  // fetched: pieces whose copies were begun, when the roles meet
     SliceRows rows;
 };
 
@@ -494,12 +502,7 @@ __global__ void __launch_bounds__(tc_threads(TMA), 1) linear_tc_kernel(const __g
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
                 pass(u);
             }
-            // after a failure: the copies that are under way have to land before the block ends
-            if (*failed && p.images) bar_wait(smem_addr(&sh.digits), 0, failed);
-            if (*failed)
-                for (int i = max(u - p.stages, 0); i < u && i < total; ++i)
-                    for (int k = 0; k < 100000 && !bar_try(smem_addr(&sh.full[i % p.stages]), (i / p.stages) & 1); ++k) {
-                    }
+            if (copier == 0) sh.fetched = u;
         }
         __syncwarp();
     } else if (warp < kMmaWarp && !p.images) {
@@ -583,7 +586,7 @@ __global__ void __launch_bounds__(tc_threads(TMA), 1) linear_tc_kernel(const __g
         // nothing of the block may be under way when it gives the tensor memory back
         if (leader) {
             mma_commit(smem_addr(&sh.drained));
-            bar_wait(smem_addr(&sh.drained), 0, failed);
+            bar_land(smem_addr(&sh.drained), 0);
         }
         __syncwarp();
     } else if (warp < kMmaWarp) {
@@ -631,6 +634,13 @@ __global__ void __launch_bounds__(tc_threads(TMA), 1) linear_tc_kernel(const __g
     if (warp == kMmaWarp) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+    // A block that gave up, in whichever role, ends when its bulk copies have landed in its
+    // shared memory; otherwise all of them have been waited for.  The copying threads' own
+    // copies were, before they met the others.
+    if (*failed && copier == 0) {
+        if (p.images) bar_land(smem_addr(&sh.digits), 0);
+        for (int i = max(sh.fetched - p.stages, 0); i < sh.fetched; ++i) bar_land(smem_addr(&sh.full[i % p.stages]), (i / p.stages) & 1);
     }
 }
 
