@@ -488,14 +488,8 @@ __global__ void __launch_bounds__(tc_threads(TMA), 1) linear_tc_kernel(const __g
                 if (u >= p.stages && !bar_wait(smem_addr(&sh.empty[u % p.stages]), (u / p.stages - 1) & 1, failed)) break;
                 fetch(u);
                 if constexpr (!TMA) {
-                    // a ring of no more stages than are left under way would wait for itself
-                    if (p.stages <= kLag) {
-                        asm volatile("cp.async.wait_group 0;" ::: "memory");
-                        pass(u + 1);
-                    } else if (u >= kLag) {
-                        asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
-                        pass(u + 1 - kLag);
-                    }
+                    asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
+                    pass(u + 1 - kLag);
                 }
             }
             if constexpr (!TMA) {
@@ -774,6 +768,10 @@ cudaError_t launch_linear_tc(const LinearParams& l, bool x_f32, bool out_f32, cu
     const int dig = plan.pieces_per_slice * (cols * 128 + 4 * 512);
     p.stages = (kMost - 1024 - dig) / (kStageBytes + kStageScales);
     if (p.stages > kMaxStages + 1 - plan.pieces_per_slice) p.stages = kMaxStages + 1 - plan.pieces_per_slice;  // 512 columns
+    // A ring that is filled again (one of `work` stages is not) has more stages than are copied
+    // before the copying warps pass the first piece on, and than they leave under way.
+    constexpr int kBySmem = (kMost - 1024 - kMaxPieces * (kPassRows * 8 * 128 + 4 * 512)) / (kStageBytes + kStageScales);
+    static_assert(kBySmem > kFirstStages && kMaxStages + 1 - kMaxPieces > kFirstStages && kFirstStages >= kLag);
     const int work = (plan.tiles + plan.groups - 1) / plan.groups * plan.pieces_per_slice;
     if (p.stages > work) p.stages = work;
     const size_t smem = 1024 + dig + (size_t)p.stages * (kStageBytes + kStageScales);
