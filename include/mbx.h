@@ -518,8 +518,12 @@ MBX_API int mbx_rope_axes(const mbx_heads_view* q_out, const mbx_heads_view* k_o
  *   out = the pairs of n turned by positions[token] * freqs; the rest passes.
  * wq, wk [1, head_dim] (contiguous) of the heads' dtype, or MBX_F32 with
  * MBX_BF16 heads, both of one dtype; either NULL (1).  Everything else, and
- * in-place use, as in mbx_rope_axes.  One variant: binary32, one rounding.  A
- * head's bits do not depend on its address, its strides or its neighbours.
+ * in-place use, as in mbx_rope_axes.  One variant: binary32, one rounding.  The
+ * angle is the exact product of position and frequency, its cosine and sine are
+ * within 1.73 * 2^-24 (positions below 2^90 in magnitude; past that the product
+ * loses 2^-128 of a turn for each unit of the position); a frequency of 2^54 or
+ * more, or one that is not finite, gives NaN in its pair.  A head's bits do not
+ * depend on its address, its strides or its neighbours.
  */
 MBX_API int mbx_qk_norm_rope(const mbx_heads_view* q_out, const mbx_heads_view* k_out,
                              const mbx_heads_cview* q, const mbx_heads_cview* k,

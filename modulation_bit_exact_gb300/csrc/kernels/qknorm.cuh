@@ -23,37 +23,45 @@ using Int = std::integral_constant<int, V>;
 template <bool V>
 using Bool = std::integral_constant<bool, V>;
 
-// The angles.  Position * frequency / (2 pi) turns, modulo a turn, in 64-bit fixed
-// point: the product of the frequency's 53 bits with 64 bits of 1 / (2 pi) is formed
-// once in a block for each pair, that with the position for each token, in integers,
-// so no position loses anything and the little binary64 that this GPU has is not used
-// (65536 tokens of one head of 128 each for Q and K, whose angles are most of the
-// work: 121 us with binary64, 89 in integers, 37 with what else is shared now).
-struct PairFreq {
-    uint64_t hi, lo;  // whole positions: hi = the step of one position in 2^-64 turns; others: the 128-bit product
-    int sh;           // its place: turns * 2^64 = hi:lo >> sh
-    int16_t axis;
-    bool minus, bad;
+// The angles.  Position * frequency / (2 pi) turns, modulo a turn, in fixed point.  Once
+// in a block for each pair the turns of one position are formed, the product of the
+// frequency's 53 bits with 192 bits of 1 / (2 pi), to 2^-128 of a turn; once for each token
+// they are multiplied by the position and cut to 2^-64 of a turn, in integers: an angle
+// loses 2^-128 of a turn for each unit of its position, and the little binary64 that this
+// GPU has is not used (65536 tokens of one head of 128 each for Q and K, whose angles are
+// most of the work: 121 us with binary64, 89 in integers, 37 with what else is shared now).
+struct PairFreq {  // 24 bytes: lanes that read structures side by side meet two at a bank (of 32 eight, gradients +1.8%)
+    uint64_t hi, lo;  // the turns of one position: whole() + hi * 2^-64 + lo * 2^-128
+    uint64_t tagged;
+    __device__ __forceinline__ uint64_t whole() const { return tagged >> 4; }  // below 2^52
+    __device__ __forceinline__ bool bad() const { return tagged & 8; }        // 2^54 or more, or not finite
+    __device__ __forceinline__ bool minus() const { return tagged & 4; }
+    __device__ __forceinline__ int axis() const { return (int)tagged & 3; }
 };
+// (hi:lo) >> n, its low word; n below 64
+__device__ __forceinline__ uint64_t shift_right(uint64_t hi, uint64_t lo, int n) { return hi << 1 << (63 - n) | lo >> n; }
 __device__ __forceinline__ PairFreq pair_freq(const RopeParams& p, int j) {
     PairFreq q;
     int a = 0;
     while (a < p.axes - 1 && j >= p.axis_end[a]) ++a;
-    q.axis = (int16_t)a;
     const uint64_t fb = __double_as_longlong(p.freqs[j]);
     const int fe = (int)(fb >> 52 & 2047) - 1023;  // the frequency is 1.m * 2^fe
-    q.minus = (int64_t)fb < 0;
-    q.bad = fe > 53;
-    // frequency / (2 pi) = m * C * 2^(fe - 52 - 66), C = 2^66 / (2 pi)
+    const bool bad = fe > 53;
     const uint64_t m = fe < -1022 ? 0 : (fb & 0xfffffffffffffull) | 1ull << 52;
-    constexpr uint64_t C = 0xa2f9836e4e44152aull;
-    q.lo = m * C;
-    q.hi = __umul64hi(m, C);
-    q.sh = 54 - fe;
-    if (!p.pos_f32) {
-        const int sh = q.sh;
-        q.hi = sh >= 128 ? 0 : sh >= 64 ? q.hi >> (sh - 64) : sh > 0 ? q.hi << 1 << (63 - sh) | q.lo >> sh : 0;
-    }
+    // m / (2 pi) in units of 2^-192, four words
+    typedef unsigned __int128 u128;
+    const u128 t0 = (u128)m * 0x36d8a5664f10e410ull;
+    const u128 t1 = (u128)m * 0x7f09d5f47d4d3770ull + (uint64_t)(t0 >> 64);
+    const u128 t2 = (u128)m * 0x28be60db9391054aull + (uint64_t)(t1 >> 64);
+    uint64_t w0 = (uint64_t)t0, w1 = (uint64_t)t1, w2 = (uint64_t)t2, w3 = (uint64_t)(t2 >> 64);
+    // times 2^(fe - 52), in units of 2^-128
+    const int sh = bad ? 63 : 64 + 52 - fe;
+    if (sh & 64) w0 = w1, w1 = w2, w2 = w3, w3 = 0;
+    if (sh & 128) w0 = w2, w1 = w3, w2 = w3 = 0;
+    if (sh >= 256) w0 = w1 = w2 = w3 = 0;
+    q.lo = shift_right(w1, w0, sh & 63);
+    q.hi = shift_right(w2, w1, sh & 63);
+    q.tagged = shift_right(w3, w2, sh & 63) << 4 | (bad ? 8 : 0) | ((int64_t)fb < 0 ? 4 : 0) | (unsigned)a;
     return q;
 }
 // A position's bits on an axis at a token (its index `tok` in the batch, `s` in its sequence).
@@ -63,23 +71,26 @@ __device__ __forceinline__ uint32_t position_bits(const RopeParams& p, unsigned 
     asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(at));
     return v;
 }
-// cos and sin of the angle.  The remainder, at most an eighth of a turn, goes through
-// the Taylor series, whose first terms left out, t^11 / 11! and t^12 / 12!, are below 2^-29.
+// cos and sin of the angle, to 1.73 * 2^-24.  The remainder, at most an eighth of a turn,
+// goes through the Taylor series, whose first terms left out, t^11 / 11! and t^12 / 12!, are
+// below 2^-29.
 __device__ __forceinline__ float2 pair_angle(const RopeParams& p, const PairFreq& q, uint32_t pos) {
-    uint64_t T;
-    bool minus = q.minus != ((int)pos < 0), bad = q.bad;
+    uint64_t T;  // turns in units of 2^-64
+    bool minus = q.minus() != ((int)pos < 0), bad = q.bad();
     if (!p.pos_f32) {
-        T = q.hi * ((int)pos < 0 ? 0u - pos : pos);
+        const uint32_t n = (int)pos < 0 ? 0u - pos : pos;
+        T = q.hi * n + __umulhi((uint32_t)(q.lo >> 32), n);
     } else {
         const int e = (int)(pos >> 23 & 255);  // the position is pm * 2^(e - 150)
         bad |= e == 255;
         const uint64_t pm = e ? (pos & 0x7fffffu) | 0x800000u : (pos & 0x7fffffu) << 1;
-        const int sh = q.sh - (e - 150);
-        // 192-bit product, of which 64 bits from bit sh are wanted
+        // pm times the turns of one position in units of 2^-128, of which 64 bits from bit sh are wanted
         const uint64_t w0 = q.lo * pm, c0 = __umul64hi(q.lo, pm), w1 = q.hi * pm + c0;
-        const uint64_t w2 = __umul64hi(q.hi, pm) + (w1 < c0);
-        T = sh >= 192 ? 0 : sh >= 128 ? w2 >> (sh - 128) : sh > 64 ? w2 << 1 << (127 - sh) | w1 >> (sh - 64)
-            : sh == 64 ? w1 : sh > 0 ? w1 << 1 << (63 - sh) | w0 >> sh : sh > -64 ? w0 << -sh : 0;
+        const uint64_t c1 = __umul64hi(q.hi, pm) + (w1 < c0), w2 = q.whole() * pm + c1;
+        const uint64_t w3 = __umul64hi(q.whole(), pm) + (w2 < c1);
+        const int sh = 214 - e;
+        T = sh >= 192 ? w3 >> (sh - 192) : sh >= 128 ? shift_right(w3, w2, sh - 128) : sh >= 64 ? shift_right(w2, w1, sh - 64)
+            : sh >= 0 ? shift_right(w1, w0, sh) : w0 << -sh;
     }
     if (minus != p.inverse) T = 0 - T;
     const uint32_t quadrant = (uint32_t)((T + (1ull << 61)) >> 62);
@@ -536,7 +547,7 @@ struct TokenAngles {
         else named_bar(1 + threadIdx.x / 32 / wpt, wpt * 32);
     }
     __device__ __forceinline__ uint32_t position(unsigned tok, int j) const {
-        return position_bits(r, tok, tok - batch_of(tok, by_tokens) * (unsigned)r.tokens, freqs[j].axis);
+        return position_bits(r, tok, tok - batch_of(tok, by_tokens) * (unsigned)r.tokens, freqs[j].axis());
     }
     __device__ __forceinline__ void fetch(unsigned tok) {
         if (tpw > 1 || tok >= total) return;
