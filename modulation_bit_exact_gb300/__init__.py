@@ -512,8 +512,8 @@ def linear_nvfp4(x, w4, w_sf, fp4_scale, bias=None, silu: bool = False, out=None
     block's modulation vectors are ``linear_nvfp4(temb, ..., silu=True)``.
 
     x [..., K] bfloat16 or float32, at most 256 rows; w4 [N, K/2] and w_sf
-    uint8 as ``nvfp4_weight`` or an NVFP4 producer makes them; fp4_scale a
-    one-element float32 CUDA tensor; bias [N] bfloat16, float32 or None.  Returns
+    uint8 (w_sf also float8_e4m3fn) as ``nvfp4_weight`` or an NVFP4 producer
+    makes them; fp4_scale a one-element float32 CUDA tensor; bias [N] bfloat16, float32 or None.  Returns
     out [..., N] of x's dtype; a given out may also be float32."""
     return _native().linear_nvfp4(x, w4, w_sf, fp4_scale, bias, silu, out)
 
@@ -528,8 +528,8 @@ def linear_nvfp4_workspace(rows: int, outputs: int, cols: int) -> int:
 
 def _weight_views(w4, w_sf):
     w, f = _view(w4), _view(w_sf)
-    byte = (torch.uint8, torch.float8_e4m3fn)
-    w.dtype, f.dtype = MBX_E2M1X2 if w4.dtype in byte else 0, MBX_E4M3 if w_sf.dtype in byte else 0
+    w.dtype = MBX_E2M1X2 if w4.dtype == torch.uint8 else 0
+    f.dtype = MBX_E4M3 if w_sf.dtype in (torch.uint8, torch.float8_e4m3fn) else 0
     return w, f
 
 

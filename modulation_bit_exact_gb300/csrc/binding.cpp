@@ -149,9 +149,10 @@ const int64_t* rng_state(const at::Tensor& rng) {
 }
 constexpr const char* kBadRng = "MBX_E_ARG: rng must be a contiguous int64 tensor (seed, counter)";
 
-// Packed values and block scales are bytes; the scales may be torch's E4M3 type.
-bool bytes_of(const at::Tensor& t) {
-    return t.scalar_type() == at::kByte || t.scalar_type() == at::kFloat8_e4m3fn;
+// Packed pairs of E2M1 codes are bytes; block scales are bytes or torch's E4M3 type.
+int32_t pairs_dtype(const at::Tensor& t) { return t.scalar_type() == at::kByte ? MBX_E2M1X2 : 0; }
+int32_t scales_dtype(const at::Tensor& t) {
+    return t.scalar_type() == at::kByte || t.scalar_type() == at::kFloat8_e4m3fn ? MBX_E4M3 : 0;
 }
 constexpr const char* kBadScale = "MBX_E_ARG: fp4_scale must be a one-element float32 tensor";
 
@@ -475,8 +476,8 @@ PyObject* linear_nvfp4(PyObject* const* a) {
     const at::Tensor &x = tensor(a[0]), &w4 = tensor(a[1]), &gs = tensor(a[3]);
     const In xv(x);
     In wv(w4), sf(tensor(a[2]));
-    wv.v.dtype = bytes_of(w4) ? MBX_E2M1X2 : 0;
-    sf.v.dtype = bytes_of(tensor(a[2])) ? MBX_E4M3 : 0;
+    wv.v.dtype = pairs_dtype(w4);
+    sf.v.dtype = scales_dtype(tensor(a[2]));
     if (gs.scalar_type() != at::kFloat || gs.numel() != 1) return raise_status(MBX_E_ARG, kBadScale);
     const In bias(tensor_or_none(a[4]));
     const int silu = PyObject_IsTrue(a[5]);

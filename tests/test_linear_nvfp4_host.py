@@ -127,3 +127,13 @@ def test_weight_refusals(mbx):  # noqa: F811
         with pytest.raises(mbx.MbxError) as e:
             mbx.nvfp4_weight(torch.zeros(shape))
         assert e.value.status == status
+
+
+def test_scales_are_no_weight(mbx):  # noqa: F811
+    """An E4M3 tensor is refused as packed E2M1 pairs; as block scales it is taken (-9: no device)."""
+    x, w4, sf, gs = torch.zeros(2, 64), torch.zeros(200, 32, dtype=torch.uint8), torch.zeros(256, 4, dtype=torch.uint8), torch.ones(1)
+    e4 = torch.float8_e4m3fn
+    for w, f, want in ((w4.view(e4), sf, -2), (w4.view(e4), sf.view(e4), -2), (w4, sf.view(e4), -9)):
+        with pytest.raises(mbx.MbxError) as e:
+            mbx.linear_nvfp4(x, w, f, gs)
+        assert e.value.status == want == mbx.check_linear_nvfp4(torch.zeros(2, 200), x, w, f, gs)
