@@ -9,36 +9,12 @@
 // the lanes.  For weights that linear_tc.cu does not take (rows that start at no 8-byte
 // boundary, scales at no 16-byte one: slices of larger buffers): bound by
 // decoding, [1, 5120] x [30720, 5120] 176 us against 17.8 there.
-#include "linear.h"
-#include "rowgroup.cuh"
+#include "linear.cuh"
 
 namespace mbx {
 
 constexpr int kLinWarps = 8, kLinCols = 4, kLinRows = 4;
 constexpr int kPieceBlocks = 64;  // blocks of 16 in a piece of K
-
-__device__ __forceinline__ float silu_of(float v) { return v / (1.0f + expf(-v)); }
-
-// Eight E2M1 codes of a word, the lowest first.
-__device__ __forceinline__ void e2m1x8(float (&f)[8], uint32_t w) {
-    uint32_t h[4];
-    asm("{\n.reg .b8 a, b, c, d;\nmov.b32 {a, b, c, d}, %4;\n"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\ncvt.rn.f16x2.e2m1x2 %1, b;\ncvt.rn.f16x2.e2m1x2 %2, c;\ncvt.rn.f16x2.e2m1x2 %3, d;\n}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(w));
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        asm("{\n.reg .f16 a, b;\nmov.b32 {a, b}, %2;\ncvt.f32.f16 %0, a;\ncvt.f32.f16 %1, b;\n}"
-            : "=f"(f[2 * i]), "=f"(f[2 * i + 1])
-            : "r"(h[i]));
-}
-__device__ __forceinline__ float e4m3_value(uint8_t v) {
-    uint32_t h;
-    float f;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)v));
-    asm("{\n.reg .f16 a, b;\nmov.b32 {a, b}, %1;\ncvt.f32.f16 %0, a;\n}" : "=f"(f) : "r"(h));
-    return f;
-}
 
 template <class T, class O>
 __global__ void __launch_bounds__(32 * kLinWarps) linear_nvfp4_kernel(LinearParams p, int wide) {
@@ -56,7 +32,7 @@ __global__ void __launch_bounds__(32 * kLinWarps) linear_nvfp4_kernel(LinearPara
             const int r = i / (nb * 16), k = i - r * nb * 16;
             float v = 0.0f;
             if (r < rows) v = load_elem(static_cast<const T*>(p.x) + (int64_t)(row0 + r) * p.x_stride + b0 * 16 + k);
-            act[r][k % 16][k / 16] = p.silu ? silu_of(v) : v;
+            act[r][k % 16][k / 16] = p.silu ? silu(v) : v;
         }
         __syncthreads();
         for (int b = lane; b < nb; b += 32) {
@@ -112,18 +88,8 @@ __global__ void __launch_bounds__(32 * kLinWarps) linear_nvfp4_kernel(LinearPara
 template <class T, class O>
 static cudaError_t linear_rows(const LinearParams& p, cudaStream_t s) {
     const int wide = reinterpret_cast<uintptr_t>(p.w4) % 8 == 0 && p.w_stride % 8 == 0;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.N + kLinWarps * kLinCols - 1) / (kLinWarps * kLinCols)), (p.rows + kLinRows - 1) / kLinRows);
-    cfg.blockDim = dim3(32 * kLinWarps);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_nvfp4_kernel<T, O>, p, wide);
-    const cudaError_t last = cudaGetLastError();
-    return e != cudaSuccess ? e : last;
+    const dim3 grid((unsigned)((p.N + kLinWarps * kLinCols - 1) / (kLinWarps * kLinCols)), (p.rows + kLinRows - 1) / kLinRows);
+    return launch_pdl(linear_nvfp4_kernel<T, O>, grid, 32 * kLinWarps, 0, s, p, wide);
 }
 
 cudaError_t launch_linear_nvfp4(const LinearParams& p, bool x_f32, bool out_f32, cudaStream_t s) {

@@ -36,8 +36,7 @@
 #include <atomic>
 #include <mutex>
 
-#include "linear.h"
-#include "rowgroup.cuh"
+#include "linear.cuh"
 
 namespace mbx {
 
@@ -193,8 +192,6 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 
 // ---------------------------------------------------------------- activations and their digits
 
-__device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
-
 // Four activations, a quarter of a block of 16: x[row][k ...].
 __device__ __forceinline__ void load_quarter(float (&v)[4], const TcParams& p, int row, int k) {
     const int64_t at = (int64_t)row * p.l.x_stride + k;
@@ -307,16 +304,11 @@ __device__ __noinline__ float odd_products(const TcParams& p, int row, int64_t n
         }
         if (!odd) continue;
         const uint8_t b = p.l.sf[(n / 128 * p.l.sf_col_tiles + blk / 4) * 512 + n % 32 * 16 + n % 128 / 32 * 4 + blk % 4];
-        uint32_t h;
-        float s;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)b));
-        asm("{\n.reg .f16 a, b;\nmov.b32 {a, b}, %1;\ncvt.f32.f16 %0, a;\n}" : "=f"(s) : "r"(h));
+        const float s = e4m3_value(b);
         for (int i = 0; i < 16; ++i) {
             if ((__float_as_uint(v[i]) & 0x7f800000u) != 0x7f800000u) continue;
             const uint32_t c = p.l.w4[n * p.l.w_stride + blk * 8 + i / 2] >> (i % 2 * 4) & 15u;
-            const uint32_t e = c >> 1 & 3u;
-            const float m = e ? __uint_as_float((e + 126u) << 23 | (c & 1u) << 22) : (float)(c & 1u) * 0.5f;
-            sum += v[i] * ((c & 8u ? -m : m) * s);
+            sum += v[i] * (e2m1_value(c) * s);
         }
     }
     return sum;
@@ -725,23 +717,6 @@ bool linear_tc_takes(const LinearParams& p) {
     return tc_plan(p.N, p.K).slices > 0 && rows_at(p, 8) && reinterpret_cast<uintptr_t>(p.sf) % 16 == 0;
 }
 
-template <class... KArgs, class... Args>
-static cudaError_t launch2(void (*k)(KArgs...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, const Args&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k, args...);
-    const cudaError_t last = cudaGetLastError();
-    return e != cudaSuccess ? e : last;
-}
-
 cudaError_t launch_linear_tc(const LinearParams& l, bool x_f32, bool out_f32, cudaStream_t s) {
     static std::atomic<bool> allowed[64] = {};
     int dev = 0;
@@ -794,12 +769,12 @@ cudaError_t launch_linear_tc(const LinearParams& l, bool x_f32, bool out_f32, cu
         p.images = reinterpret_cast<uint8_t*>(l.ws) + sums_bytes(plan, l.rows, l.N);
         p.image_bytes = image_bytes(plan, l.rows);
         const unsigned threads = (unsigned)plan.pieces_per_slice * 64;
-        if (cudaError_t e = launch2(linear_digits_kernel, dim3((unsigned)plan.slices, (unsigned)l.rows), threads, 0, s, p)) return e;
+        if (cudaError_t e = launch_pdl(linear_digits_kernel, dim3((unsigned)plan.slices, (unsigned)l.rows), threads, 0, s, p)) return e;
     }
-    const cudaError_t e = launch2(tma ? linear_tc_kernel<true> : linear_tc_kernel<false>, dim3((unsigned)(p.slices * p.groups), passes),
+    const cudaError_t e = launch_pdl(tma ? linear_tc_kernel<true> : linear_tc_kernel<false>, dim3((unsigned)(p.slices * p.groups), passes),
                                   tc_threads(tma), smem, s, map, p);
     if (e != cudaSuccess || p.slices == 1) return e;
-    return launch2(linear_join_kernel, dim3((unsigned)((l.N + 255) / 256), (unsigned)l.rows), 256, 0, s, p);
+    return launch_pdl(linear_join_kernel, dim3((unsigned)((l.N + 255) / 256), (unsigned)l.rows), 256, 0, s, p);
 }
 
 }  // namespace mbx
