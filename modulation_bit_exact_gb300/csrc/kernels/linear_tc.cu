@@ -10,7 +10,7 @@
 // block's E4M3 scale.  A row of x becomes eight columns of the product, one a
 // digit, whose sums the epilogue adds up by their powers of 8, and one to sixteen rows
 // cost the same, 8 to 128 columns.  The one rounding that binary32 products do not
-// have: a value is taken to 2^-22 of the largest of its 16, or 2^-39 of its row's.  Beside
+// have: a value is taken to 2^-22 of the largest of its 16, or 2^-39 of its slice's.  Beside
 // the product of that largest value it is as small as their roundings; an output whose
 // weight there is zero has it beside its other products.  Sixteen digits would take
 // 256 columns for sixteen rows, and the tensor memory holds no two such accumulators.
@@ -25,9 +25,9 @@
 // accumulators and write, each four of them a quarter of the rows.
 //
 // Floor: the weight's bytes, 9/16 of one a value.  Steady state, [1, 5120] x [245760,
-// 5120]: 106.5 us, 6.6 TB/s, 0.99 of what a copy reaches.  [1, 5120] x [30720, 5120]:
+// 5120]: 107 us, 6.6 TB/s, 0.985 of what a copy reaches.  [1, 5120] x [30720, 5120]:
 // 17.8 us, 5.0 TB/s: 4 us until the first product, of which the copies hide most, and 2.5
-// for the second kernel.  [16, 5120] x [10007, 5120]: 12.1 us; its 29 MB take 4.4, the
+// for the second kernel.  [16, 5120] x [10007, 5120]: 12.4 us; its 29 MB take 4.4, the
 // digits' kernel, the product's 128 columns (0.4 us a piece of weight against 0.3 for 16)
 // and the sums' way through memory the rest.  The elected lane matters: the same operations
 // from `lane == 0` took 0.7 us a piece.

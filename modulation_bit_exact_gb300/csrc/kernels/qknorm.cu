@@ -11,9 +11,9 @@
 // ring in shared memory that it fills ahead (qknorm.cuh).
 //
 // Floor: every element read and written once.  32760 tokens of 40 + 40 heads of 128,
-// bfloat16: 208 us, 6.4 TB/s of 6.7 that a copy reaches; 8704 of 24 + 24: 40 us, 5.4 TB/s,
+// bfloat16: 210 us, 6.4 TB/s of 6.7 that a copy reaches; 8704 of 24 + 24: 40 us, 5.4 TB/s,
 // where issue shows (57% of the slots: 24 M warp instructions, 230 for four heads of 128)
-// and the start of the blocks, 3 us, is not hidden; 24 single tokens: 3.5 us in a graph.
+// and the start of the blocks, 3 us, is not hidden; 24 single tokens: 3.2 us in a graph.
 #include "qknorm.cuh"
 
 namespace mbx {

@@ -9,8 +9,8 @@
 // memory, and column_sums (colsum.cu) the blocks' parts, in a fixed order.
 //
 // Floor: two arrays read, one written.  32760 tokens of 40 + 40 heads of 128, bfloat16:
-// 320 us, 6.3 TB/s of 6.7 that a copy reaches; 8704 of 24 + 24: 61 us, 5.2 TB/s, of which 4
-// join the parts (issue 61%: 43 M warp instructions, 206 for two heads of 128).
+// 324 us, 6.2 TB/s of 6.7 that a copy reaches; 8704 of 24 + 24: 62 us, 5.2 TB/s, of which 4
+// join the parts (issue 61%: 44 M warp instructions, 211 for two heads of 128).
 #include "qknorm.cuh"
 
 namespace mbx {
