@@ -181,11 +181,11 @@ inline cudaError_t launch_all_or_none(F&& f) {
 // the previous kernel in the stream drains, and calls grid_dep_wait() before
 // it touches global memory that kernel may use.
 template <class... KArgs, class... Args>
-inline cudaError_t launch_pdl(void (*k)(KArgs...), dim3 grid, unsigned block, size_t smem, cudaStream_t s,
-                              const Args&... args) {
+inline cudaError_t launch_pdl(void (*k)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                              Args... args) {
     if (t_dry_run) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
+    cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;

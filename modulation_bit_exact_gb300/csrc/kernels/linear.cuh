@@ -1,4 +1,4 @@
-// linear.cuh -- the activation and the decoding of NVFP4 shared by the products
+// linear.cuh -- the launch, the activation and the decoding of NVFP4 shared by the products
 // (linear_tc.cu, linear_nvfp4.cu).
 #pragma once
 
@@ -6,6 +6,25 @@
 #include "rowgroup.cuh"
 
 namespace mbx {
+
+// launch_pdl of a grid of two dimensions.
+template <class... KArgs, class... Args>
+inline cudaError_t launch_pdl_2d(void (*k)(KArgs...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, const Args&... args) {
+    if (t_dry_run) return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k, args...);
+    const cudaError_t last = cudaGetLastError();
+    return e != cudaSuccess ? e : last;
+}
 
 __device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
 

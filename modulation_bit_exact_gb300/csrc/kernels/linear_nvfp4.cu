@@ -89,7 +89,7 @@ template <class T, class O>
 static cudaError_t linear_rows(const LinearParams& p, cudaStream_t s) {
     const int wide = reinterpret_cast<uintptr_t>(p.w4) % 8 == 0 && p.w_stride % 8 == 0;
     const dim3 grid((unsigned)((p.N + kLinWarps * kLinCols - 1) / (kLinWarps * kLinCols)), (p.rows + kLinRows - 1) / kLinRows);
-    return launch_pdl(linear_nvfp4_kernel<T, O>, grid, 32 * kLinWarps, 0, s, p, wide);
+    return launch_pdl_2d(linear_nvfp4_kernel<T, O>, grid, 32 * kLinWarps, 0, s, p, wide);
 }
 
 cudaError_t launch_linear_nvfp4(const LinearParams& p, bool x_f32, bool out_f32, cudaStream_t s) {

@@ -769,12 +769,12 @@ cudaError_t launch_linear_tc(const LinearParams& l, bool x_f32, bool out_f32, cu
         p.images = reinterpret_cast<uint8_t*>(l.ws) + sums_bytes(plan, l.rows, l.N);
         p.image_bytes = image_bytes(plan, l.rows);
         const unsigned threads = (unsigned)plan.pieces_per_slice * 64;
-        if (cudaError_t e = launch_pdl(linear_digits_kernel, dim3((unsigned)plan.slices, (unsigned)l.rows), threads, 0, s, p)) return e;
+        if (cudaError_t e = launch_pdl_2d(linear_digits_kernel, dim3((unsigned)plan.slices, (unsigned)l.rows), threads, 0, s, p)) return e;
     }
-    const cudaError_t e = launch_pdl(tma ? linear_tc_kernel<true> : linear_tc_kernel<false>, dim3((unsigned)(p.slices * p.groups), passes),
+    const cudaError_t e = launch_pdl_2d(tma ? linear_tc_kernel<true> : linear_tc_kernel<false>, dim3((unsigned)(p.slices * p.groups), passes),
                                   tc_threads(tma), smem, s, map, p);
     if (e != cudaSuccess || p.slices == 1) return e;
-    return launch_pdl(linear_join_kernel, dim3((unsigned)((l.N + 255) / 256), (unsigned)l.rows), 256, 0, s, p);
+    return launch_pdl_2d(linear_join_kernel, dim3((unsigned)((l.N + 255) / 256), (unsigned)l.rows), 256, 0, s, p);
 }
 
 }  // namespace mbx
