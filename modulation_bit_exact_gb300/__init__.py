@@ -513,8 +513,9 @@ def linear_nvfp4(x, w4, w_sf, fp4_scale, bias=None, silu: bool = False, out=None
 
     x [..., K] bfloat16 or float32, at most 256 rows; w4 [N, K/2] and w_sf
     uint8 (w_sf also float8_e4m3fn) as ``nvfp4_weight`` or an NVFP4 producer
-    makes them; fp4_scale a one-element float32 CUDA tensor; bias [N] bfloat16, float32 or None.  Returns
-    out [..., N] of x's dtype; a given out may also be float32."""
+    makes them; fp4_scale a one-element float32 CUDA tensor; bias [N] bfloat16,
+    float32 or None.  Returns out [..., N] of x's dtype; a given out may also be
+    float32."""
     return _native().linear_nvfp4(x, w4, w_sf, fp4_scale, bias, silu, out)
 
 

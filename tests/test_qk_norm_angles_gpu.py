@@ -52,7 +52,7 @@ def _exact(positions, freqs):
 
 def test_the_inverse():
     assert abs(float(INVERSE) - 1 / (2 * math.pi)) < 1e-16
-    # the tangent's own remainder: pi to 53 bits is off by 1.2246467991473532e-16
+    # pi rounded to 53 bits is 1.2246467991473532e-16 short
     assert abs(float((Fraction(1) / INVERSE / 2 - Fraction(math.pi))) - 1.2246467991473532e-16) < 1e-30
 
 
